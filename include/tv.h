@@ -77,6 +77,9 @@ extern "C" {
 #define TV_E_CHAIN       -14   /* single-path sampling on a tree that is not a chain    */
 #define TV_E_PROPOSAL    -15   /* a proposal row not finite, negative, off unit mass, or
                                   zero at its draft                                     */
+#define TV_E_SEQ         -16   /* a sequence list: an index out of range or listed twice, a
+                                  length or a row range that does not fit                */
+#define TV_E_PAGE        -17   /* a page entry out of range or a page that is not held    */
 
 typedef uint16_t tv_bf16;
 
@@ -577,6 +580,133 @@ TV_API int tv_commit_stack(const tv_stack *model, const tv_kv *kv, float *const 
                            int n_req, const int32_t *path, const int32_t *accept_len, int32_t *committed_src,
                            int32_t *new_ctx, const void *workspace, size_t workspace_bytes, int32_t *dev_status,
                            void *stream);
+
+/*
+ * A paged key-value cache.  The pages name no layout for a cache that many
+ * sequences share; this one stands beside tv_kv for serving loops that keep
+ * more sequences than contiguous caches allow, fork them (several samples of a
+ * prompt) and release them.  A page holds page_size tokens of every layer:
+ * page p of layer l is one contiguous block of K and one of V, laid out
+ * [n_kv_heads][page_size][head_dim], so that a head's tokens lie as in tv_kv.
+ *
+ *   tv_pool   k, v    device bf16 [n_layers][n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned
+ *             refs    device int32 [n_pages], 16-byte aligned: how many sequences hold the page, 0 = free
+ *             page_size 16, 32, 64 or 128; head_dim 64 or 128; at most 2^31 - 1 rows of head_dim in all
+ *   tv_seqs   pages   device int32 [max_seqs][max_pages]: a sequence's pages in order; entries past
+ *                     ceil(len / page_size) are neither read nor written
+ *             lens    device int32 [max_seqs]: its tokens, 0 = the row is unused
+ *             max_seqs at most 65536, max_pages * page_size at most 2^31 - 1
+ *
+ * All of it is the caller's memory, zeroed once (refs and lens); the calls keep
+ * refs equal to the number of table entries that name the page.  Free pages are
+ * taken lowest index first, so the outcome is a function of the state alone.
+ * Every list (ids, src, dst, add, keep, pos, starts) is device int32 and of n
+ * entries, 1 <= n <= 4096, so a call can be captured into a graph and replayed
+ * on other lists.  A call looks its whole list over before it changes
+ * anything, except where noted; where several codes apply, one of them is
+ * reported.
+ */
+typedef struct tv_pool {
+  tv_bf16 *k, *v;
+  int32_t *refs;
+  int32_t n_layers, n_pages, n_kv_heads, page_size, head_dim;
+} tv_pool;
+
+typedef struct tv_seqs {
+  int32_t *pages, *lens;
+  int32_t max_seqs, max_pages;
+} tv_seqs;
+
+/*
+ * tv_pages_workspace_size: bytes of workspace tv_pages_extend and
+ * tv_pages_compact need.  Host-only.
+ *
+ * tv_pages_extend: sequence ids[i] grows by add[i] >= 0 tokens (0 -> a new
+ * sequence too).  In list order: a partly filled last page that others hold as
+ * well is copied to a new page, all layers and slots of it (copy-on-write; the
+ * last holder keeps the page); then new pages follow.  The new tokens' rows
+ * are for tv_pages_write or tv_attend_paged to fill.
+ * Device checks: TV_E_SEQ, TV_E_PAGE, TV_E_CAPACITY (a table row or the pool
+ * too small for the whole list; nothing is changed).
+ *
+ * tv_pages_fork: sequence dst[i] (unused: length 0, in the list once, not among
+ * src) becomes a copy of sequence src[i] that shares its pages; no row moves.
+ * Device checks: TV_E_SEQ, TV_E_PAGE.
+ *
+ * tv_pages_release: sequence ids[i] keeps its first keep[i] <= len tokens (0:
+ * it ends) and gives up the pages past them: rejected drafts, finished
+ * sequences.  Device checks: TV_E_SEQ, TV_E_PAGE.
+ *
+ * tv_pages_compact: with U pages held, the k-th held page at or past U moves
+ * to the k-th free page below U, in every layer and every table row, so that
+ * the pool's tail is free.  remap (device int32 [n_pages]) receives each
+ * page's new index, -1 for pages that were free; n_used (device int32 [1])
+ * receives U.  Device checks: TV_E_SEQ, TV_E_PAGE.
+ *
+ * tv_pages_write / tv_pages_read: rows starts[i] .. starts[i + 1] - 1 of k and
+ * v (starts: n + 1 entries, ascending within 0 .. rows) are tokens pos[i],
+ * pos[i] + 1, ... of sequence ids[i] in layer `layer`; write puts them into the
+ * sequence's pages, read gets them from there.  Element (row, head, d) of k and
+ * v is at row * row_stride + head * head_stride + d (elements, multiples of 8;
+ * k and v 16-byte aligned): the K heads of a QKV projection's rows, or with
+ * row_stride = head_dim and head_stride = capacity * head_dim the cache of a
+ * tv_kv (offset the pointers to its slot), so that a paged sequence can be
+ * verified and what the verify committed written back.  Tokens must lie below
+ * the sequence's length.  write: a sequence may be listed once, and its rows
+ * must lie in pages that it alone holds (tv_pages_extend sees to it).
+ * Device checks: TV_E_SEQ, TV_E_CAPACITY (a token past the length); TV_E_PAGE
+ * (that row alone is left out).
+ *
+ * Host checks of all: TV_E_ARG (null or misaligned pointers, n < 1, a bad
+ * layer), TV_E_UNSUPPORTED (n > 4096, shapes outside the above),
+ * TV_E_WORKSPACE.
+ */
+TV_API int tv_pages_workspace_size(const tv_pool *pool, const tv_seqs *seqs, size_t *bytes);
+TV_API int tv_pages_extend(const tv_pool *pool, const tv_seqs *seqs, const int32_t *ids, const int32_t *add, int n,
+                           void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+TV_API int tv_pages_fork(const tv_pool *pool, const tv_seqs *seqs, const int32_t *src, const int32_t *dst, int n,
+                         int32_t *dev_status, void *stream);
+TV_API int tv_pages_release(const tv_pool *pool, const tv_seqs *seqs, const int32_t *ids, const int32_t *keep, int n,
+                            int32_t *dev_status, void *stream);
+TV_API int tv_pages_compact(const tv_pool *pool, const tv_seqs *seqs, int32_t *remap, int32_t *n_used, void *workspace,
+                            size_t workspace_bytes, int32_t *dev_status, void *stream);
+TV_API int tv_pages_write(const tv_pool *pool, int layer, const tv_seqs *seqs, const int32_t *ids, const int32_t *pos,
+                          const int32_t *starts, int n, int rows, const tv_bf16 *k, const tv_bf16 *v,
+                          size_t row_stride, size_t head_stride, int32_t *dev_status, void *stream);
+TV_API int tv_pages_read(const tv_pool *pool, int layer, const tv_seqs *seqs, const int32_t *ids, const int32_t *pos,
+                         const int32_t *starts, int n, int rows, tv_bf16 *k, tv_bf16 *v, size_t row_stride,
+                         size_t head_stride, int32_t *dev_status, void *stream);
+
+/*
+ * Attention of one new token per sequence over its pages, the single-token
+ * form of the prompt's attention: query head h of listed sequence i attends to
+ * every token of sequence ids[i] in layer `layer`,
+ *     out[i][h] = sum_j softmax_j(q[i][h] . k[j][g] / sqrt(head_dim)) v[j][g],
+ *     g = h / (n_q_heads / n_kv_heads).
+ * The new token is the sequence's last: tv_pages_extend by one comes first.
+ * With k_new and v_new its K and V rows go into its slot (position len - 1)
+ * and are attended to; without them (NULL) the slot holds them already.
+ *
+ *   q         device bf16, head h of listed sequence i at i * q_stride + h * head_dim
+ *   k_new, v_new  device bf16, KV head g of listed sequence i at i * kv_stride + g * head_dim
+ *             (strides in elements, multiples of 8, at least a row; pointers 16-byte
+ *             aligned: the Q, K and V heads of a QKV projection's rows)
+ *   out       device bf16 [n][n_q_heads][head_dim]; a sequence of length 0 gets zeros
+ *             (and stores nothing)
+ *   workspace device, >= tv_attend_paged_workspace_size(pool, n_q_heads, n)
+ * P is rounded to bf16 for the product with V, everything else is fp32.  Slots
+ * past a sequence's length are never used, whatever they hold.  The same
+ * inputs give the same bits.
+ * Host checks: TV_E_ARG, TV_E_UNSUPPORTED (n_q_heads not a multiple of
+ * n_kv_heads, n > 4096), TV_E_WORKSPACE.  Device checks: TV_E_SEQ (also a
+ * sequence listed twice with k_new), nothing is written; TV_E_PAGE (a page
+ * entry out of range: out is unspecified).
+ */
+TV_API int tv_attend_paged_workspace_size(const tv_pool *pool, int n_q_heads, int n, size_t *bytes);
+TV_API int tv_attend_paged(const tv_pool *pool, int layer, const tv_seqs *seqs, const int32_t *ids, int n,
+                           int n_q_heads, const tv_bf16 *q, size_t q_stride, const tv_bf16 *k_new,
+                           const tv_bf16 *v_new, size_t kv_stride, tv_bf16 *out, void *workspace,
+                           size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
  * Verify prices and the StairCut cut [Drafters and tree verify, §StairCut: the

@@ -20,7 +20,7 @@ STATUS = {
     0: "TV_OK", -1: "TV_E_ARG", -2: "TV_E_ORDER", -3: "TV_E_DUP_SIBLING", -4: "TV_E_TOKEN",
     -5: "TV_E_CAPACITY", -6: "TV_E_ROWS", -7: "TV_E_UNIFORM", -8: "TV_E_TEMP", -9: "TV_E_WORKSPACE",
     -10: "TV_E_CUDA", -11: "TV_E_UNSUPPORTED", -12: "TV_E_TIMEOUT", -13: "TV_E_PATH", -14: "TV_E_CHAIN",
-    -15: "TV_E_PROPOSAL",
+    -15: "TV_E_PROPOSAL", -16: "TV_E_SEQ", -17: "TV_E_PAGE",
 }
 CODES = {v: k for k, v in STATUS.items()}
 
@@ -30,7 +30,9 @@ SYMBOLS = ("tv_workspace_size", "tv_verify_tree", "tv_accept_greedy", "tv_accept
            "tv_sample_workspace_size", "tv_sample_filter", "tv_accept_single_draw", "tv_accept_gumbel",
            "tv_accept_rejection", "tv_dn_verify_tree", "tv_dn_commit", "tv_price_init", "tv_price_lookup",
            "tv_price_observe", "tv_staircut", "tv_packed_weight_bytes", "tv_pack_weight",
-           "tv_accept_greedy_commit", "tv_stack_workspace_size", "tv_verify_stack", "tv_commit_stack")
+           "tv_accept_greedy_commit", "tv_stack_workspace_size", "tv_verify_stack", "tv_commit_stack",
+           "tv_pages_workspace_size", "tv_pages_extend", "tv_pages_fork", "tv_pages_release", "tv_pages_compact",
+           "tv_pages_write", "tv_pages_read", "tv_attend_paged_workspace_size", "tv_attend_paged")
 PROFILE_STAGES = ("prologue+embed", "qkv_gemm", "qkv_finalize", "attention", "o_gemm", "o_finalize", "lm_head")
 
 
@@ -86,6 +88,17 @@ class TvStack(ctypes.Structure):
                 ("lm_head", ctypes.c_void_p), ("packed", ctypes.c_int32)]
 
 
+class TvPool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("n_layers", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class TvSeqs(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("max_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -137,6 +150,16 @@ def load():
                                         ctypes.POINTER(TvTree), I, P, P, P, P, P, Z, P, P]
         lib.tv_commit_stack.argtypes = [ctypes.POINTER(TvStack), ctypes.POINTER(TvKv), ctypes.POINTER(P),
                                         ctypes.POINTER(TvTree), I, P, P, P, P, P, Z, P, P]
+        PO, SQ = ctypes.POINTER(TvPool), ctypes.POINTER(TvSeqs)
+        lib.tv_pages_workspace_size.argtypes = [PO, SQ, ctypes.POINTER(Z)]
+        lib.tv_pages_extend.argtypes = [PO, SQ, P, P, I, P, Z, P, P]
+        lib.tv_pages_fork.argtypes = [PO, SQ, P, P, I, P, P]
+        lib.tv_pages_release.argtypes = [PO, SQ, P, P, I, P, P]
+        lib.tv_pages_compact.argtypes = [PO, SQ, P, P, P, Z, P, P]
+        lib.tv_pages_write.argtypes = [PO, I, SQ, P, P, P, I, I, P, P, Z, Z, P, P]
+        lib.tv_pages_read.argtypes = [PO, I, SQ, P, P, P, I, I, P, P, Z, Z, P, P]
+        lib.tv_attend_paged_workspace_size.argtypes = [PO, I, I, ctypes.POINTER(Z)]
+        lib.tv_attend_paged.argtypes = [PO, I, SQ, P, I, I, P, Z, P, P, Z, P, P, Z, P, P]
         D = ctypes.c_double
         lib.tv_price_init.argtypes = [ctypes.POINTER(TvPriceTable)]
         lib.tv_price_lookup.argtypes = [ctypes.POINTER(TvPriceTable), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
@@ -313,6 +336,68 @@ def tv_commit_stack(stack: TvStack, kvs: Sequence[TvKv], dn_states, trees: Seque
     return load().tv_commit_stack(ctypes.byref(stack), _arr(TvKv, kvs) if kvs else None, _ptrs(dn_states) if dn_states else None,
                                   _arr(TvTree, trees), len(trees), _p(path), _p(accept_len), _p(committed_src),
                                   _p(new_ctx), _p(workspace), int(workspace_bytes), _p(dev_status), _stream(stream))
+
+
+def tv_pages_workspace_size(pool: TvPool, seqs: TvSeqs) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().tv_pages_workspace_size(ctypes.byref(pool), ctypes.byref(seqs), ctypes.byref(out))
+    if rc != TV_OK:
+        raise ValueError(f"tv_pages_workspace_size: {STATUS.get(rc, rc)}")
+    return int(out.value)
+
+
+def tv_pages_extend(pool: TvPool, seqs: TvSeqs, ids, add, n: int, workspace, workspace_bytes: int, dev_status,
+                    stream=None) -> int:
+    return load().tv_pages_extend(ctypes.byref(pool), ctypes.byref(seqs), _p(ids), _p(add), int(n), _p(workspace),
+                                  int(workspace_bytes), _p(dev_status), _stream(stream))
+
+
+def tv_pages_fork(pool: TvPool, seqs: TvSeqs, src, dst, n: int, dev_status, stream=None) -> int:
+    return load().tv_pages_fork(ctypes.byref(pool), ctypes.byref(seqs), _p(src), _p(dst), int(n), _p(dev_status),
+                                _stream(stream))
+
+
+def tv_pages_release(pool: TvPool, seqs: TvSeqs, ids, keep, n: int, dev_status, stream=None) -> int:
+    return load().tv_pages_release(ctypes.byref(pool), ctypes.byref(seqs), _p(ids), _p(keep), int(n), _p(dev_status),
+                                   _stream(stream))
+
+
+def tv_pages_compact(pool: TvPool, seqs: TvSeqs, remap, n_used, workspace, workspace_bytes: int, dev_status,
+                     stream=None) -> int:
+    return load().tv_pages_compact(ctypes.byref(pool), ctypes.byref(seqs), _p(remap), _p(n_used), _p(workspace),
+                                   int(workspace_bytes), _p(dev_status), _stream(stream))
+
+
+def tv_pages_write(pool: TvPool, layer: int, seqs: TvSeqs, ids, pos, starts, n: int, rows: int, k, v,
+                   row_stride: int, head_stride: int, dev_status, stream=None) -> int:
+    """Strides in elements: the K heads of projection rows, or a tv_kv cache (row_stride = head_dim)."""
+    return load().tv_pages_write(ctypes.byref(pool), int(layer), ctypes.byref(seqs), _p(ids), _p(pos), _p(starts),
+                                 int(n), int(rows), _p(k), _p(v), int(row_stride), int(head_stride), _p(dev_status),
+                                 _stream(stream))
+
+
+def tv_pages_read(pool: TvPool, layer: int, seqs: TvSeqs, ids, pos, starts, n: int, rows: int, k, v, row_stride: int,
+                  head_stride: int, dev_status, stream=None) -> int:
+    """As tv_pages_write, from the pages into k and v."""
+    return load().tv_pages_read(ctypes.byref(pool), int(layer), ctypes.byref(seqs), _p(ids), _p(pos), _p(starts),
+                                int(n), int(rows), _p(k), _p(v), int(row_stride), int(head_stride), _p(dev_status),
+                                _stream(stream))
+
+
+def tv_attend_paged_workspace_size(pool: TvPool, n_q_heads: int, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().tv_attend_paged_workspace_size(ctypes.byref(pool), int(n_q_heads), int(n), ctypes.byref(out))
+    if rc != TV_OK:
+        raise ValueError(f"tv_attend_paged_workspace_size: {STATUS.get(rc, rc)}")
+    return int(out.value)
+
+
+def tv_attend_paged(pool: TvPool, layer: int, seqs: TvSeqs, ids, n: int, n_q_heads: int, q, q_stride: int, k_new,
+                    v_new, kv_stride: int, out, workspace, workspace_bytes: int, dev_status, stream=None) -> int:
+    """Strides in elements; k_new and v_new may be None."""
+    return load().tv_attend_paged(ctypes.byref(pool), int(layer), ctypes.byref(seqs), _p(ids), int(n), int(n_q_heads),
+                                  _p(q), int(q_stride), _p(k_new), _p(v_new), int(kv_stride), _p(out), _p(workspace),
+                                  int(workspace_bytes), _p(dev_status), _stream(stream))
 
 
 def tv_price_init(table: TvPriceTable) -> int:

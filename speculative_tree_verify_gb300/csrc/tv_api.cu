@@ -9,6 +9,19 @@
 #include "tv_kernels.cuh"
 
 namespace tv {
+
+int num_sms() {
+  static std::atomic<int> cache[64];   // 0 = not read yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+  int v = cache[dev].load(std::memory_order_relaxed);
+  if (v == 0) {
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+    cache[dev].store(v, std::memory_order_relaxed);
+  }
+  return v;
+}
+
 namespace {
 
 constexpr int kMaxHeadGrid = 1024;   // top-2 partial rows reserved in the workspace
@@ -56,18 +69,6 @@ int check_dims(const tv_dims& d) {
   if (d.hidden % 64 != 0 || (d.n_q_heads * d.head_dim) % 64 != 0) return TV_E_UNSUPPORTED;
   if (d.n_q_heads % d.n_kv_heads != 0) return TV_E_UNSUPPORTED;
   return TV_OK;
-}
-
-int num_sms() {
-  static std::atomic<int> cache[64];   // 0 = not read yet
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
-  int v = cache[dev].load(std::memory_order_relaxed);
-  if (v == 0) {
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-    cache[dev].store(v, std::memory_order_relaxed);
-  }
-  return v;
 }
 
 // ---- optional stage timing (tv_profile_*) ----------------------------------
@@ -490,6 +491,8 @@ const char* tv_status_string(int code) {
     case TV_E_PATH: return "accept length or path entry out of range";
     case TV_E_CHAIN: return "single-path sampling needs a chain";
     case TV_E_PROPOSAL: return "proposal row not finite, negative, off unit mass or zero at its draft";
+    case TV_E_SEQ: return "sequence index out of range or listed twice, or a length that does not fit";
+    case TV_E_PAGE: return "page entry out of range or a page that is not held";
     default: return "unknown status";
   }
 }

@@ -7,6 +7,9 @@
 
 namespace tv {
 
+// SMs of the current device (read once per device), -1 if it cannot be read
+int num_sms();
+
 // ---- attention chunking ------------------------------------------------------
 // The cached keys of a request are cut into chunks of whole 128-key tiles.  The
 // number of chunks aims at `target` = SMs / KV heads (at most kMaxChunks), so

@@ -1,0 +1,557 @@
+// Attention of one new token per sequence over a paged cache:
+//   o[i, h] = sum_{j < len} softmax_j(q[i, h] . k[j, g] / sqrt(D)) v[j, g],  g = h / (Hq / Hkv),
+// after the new token's own K and V rows went into slot len - 1.
+//
+// What bounds it: every cached K and V byte is read once for at most 16 query
+// heads, far below the tensor cores' rate, so the kernel is built as a stream
+// over memory.  The work is the list of 64-token tiles of every (sequence, KV
+// head, block of 16 query heads) in that order; CTA c takes an equal,
+// contiguous range of it, whatever the lengths, so one long context among
+// short ones and one sequence alone both fill every SM.  A head cut by a range
+// border leaves unnormalised partials that paged_merge_kernel joins in tile
+// order: no atomics, the same bits every run.
+//
+// In a CTA one warp looks up pages and issues TMA loads (a page's tokens of
+// one head are contiguous: boxes of min(page, 64) rows x 64 values, 128-byte
+// swizzle) into a ring of stages; eight warps compute, tile t by warps
+// 4 (t mod 2) .. + 3, 16 tokens each, with mma.sync m16n8k16: the query heads
+// are the 16 rows (a KV head's 5 or so need no 128-row tile, and the tokens of
+// a warp need no other warp until the head ends).  S = Q K^T leaves each
+// thread with the P it needs as the A operand of O += P V.  P is rounded to
+// bf16 for that product (relative 2^-9 a key, independent from key to key);
+// the sums add the rounded values, so a key that dominates passes its V row
+// through unchanged.  Offsets move only when a score passes them by 2^8.
+#include <cmath>
+
+#include "tv_gemm.cuh"
+#include "tv_kernels.cuh"
+#include "tv_pages.cuh"
+
+namespace tv {
+namespace {
+
+constexpr int kTile = 64;                        // tokens of a tile
+constexpr int kStages = 5;                       // tiles in flight: 160 KB of the SM at D = 128
+constexpr int kCompWarps = 8;
+constexpr int kCompThreads = kCompWarps * 32;
+constexpr int kPaThreads = kCompThreads + 32;
+constexpr int kRows = 16;                        // query heads of a block
+constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 a CTA
+constexpr float kMoveLog2 = 8.f;
+
+struct PaWs {
+  long long* first;   // [n + 1]: first tile of each sequence in the list of tiles
+  float* ml;          // [2 CTAs][kRows][2]: offset and sum
+  float* o;           // [2 CTAs][kRows][D]
+};
+
+struct PaParams {
+  tv_pool pool;
+  tv_seqs seqs;
+  const int32_t* ids;
+  const __nv_bfloat16 *q, *k_new, *v_new;
+  size_t q_stride, kv_stride;
+  __nv_bfloat16* out;
+  int32_t* status;
+  PaWs ws;
+  int layer, n, Hq, G, HB;   // G query heads a KV head, in HB blocks of kRows
+  float scale_log2;
+};
+
+template <int D>
+struct PaSmem {
+  static constexpr int SLAB = kTile * 128;                   // 64 dimensions of a tile
+  static constexpr int HALF = (D / 64) * SLAB;               // a tile's K (or V)
+  static constexpr int STAGE = 2 * HALF;
+  static constexpr int OFF_RED = kStages * STAGE;            // [8 warps][8 rows][D] fp32; the marks of listed rows first
+  static constexpr int OFF_ML = OFF_RED + kCompWarps * 8 * D * 4;
+  static constexpr int OFF_BAR = OFF_ML + kCompWarps * kRows * 8;
+  static constexpr int OFF_FIRST = OFF_BAR + 256;            // [n + 1] long long
+  static size_t bytes(int n) { return 1024 + OFF_FIRST + (size_t)(n + 1) * 8; }
+};
+
+__device__ __forceinline__ float ex2f(float x) {   // 2^x by the SFU, about 2^-22 relative, 2^-inf = 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void comp_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kCompThreads) : "memory"); }
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+template <int D>
+__global__ void __launch_bounds__(kPaThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const PaParams p) {
+  using L = PaSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* empty = full + kStages;
+  long long* s_first = reinterpret_cast<long long*>(smem + L::OFF_FIRST);
+  float* s_red = reinterpret_cast<float*>(smem + L::OFF_RED);
+  float2* s_ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
+  uint32_t* s_mark = reinterpret_cast<uint32_t*>(smem + L::OFF_RED);
+  __shared__ long long s_part[kPaThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ps = p.pool.page_size, Hkv = p.pool.n_kv_heads;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 4);   // the four warps that compute its tile
+    }
+    fence_mbar_init();
+    prefetch_tmap(&map_k);
+    prefetch_tmap(&map_v);
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- the list of tiles: every CTA reads the same lengths and finds the same list
+  int bad = status_get(p.status) != 0;
+  if (p.k_new) {
+    for (int i = tid; i < (p.seqs.max_seqs + 31) / 32; i += kPaThreads) s_mark[i] = 0u;
+    __syncthreads();
+  }
+  const int per = (p.n + kPaThreads - 1) / kPaThreads;
+  long long sum = 0;
+  for (int i = tid * per; i < min(p.n, (tid + 1) * per); ++i) {
+    const int s = p.ids[i];
+    int len = -1;
+    if (s >= 0 && s < p.seqs.max_seqs) {
+      len = seq_len(p.seqs, ps, s);
+      if (p.k_new && (atomicOr(&s_mark[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u) len = -1;   // two new tokens, one slot
+    }
+    if (len < 0) bad = TV_E_SEQ;
+    s_first[i] = sum;
+    sum += (long long)tiles_of(max(len, 0)) * Hkv * p.HB;
+  }
+  if (bad < 0) status_set(p.status, bad);
+  long long x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_part[warp] = x;
+  if (__syncthreads_or(bad)) return;
+  long long before = x - sum, all = 0;
+  for (int w = 0; w < kPaThreads / 32; ++w) {
+    if (w < warp) before += s_part[w];
+    all += s_part[w];
+  }
+  for (int i = tid * per; i < min(p.n, (tid + 1) * per); ++i) s_first[i] += before;
+  if (tid == 0) s_first[p.n] = all;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int i = tid; i <= p.n; i += kPaThreads) p.ws.first[i] = s_first[i];
+  // sequences without a token: zeros
+  for (int i = blockIdx.x; i < p.n; i += gridDim.x)
+    if (s_first[i + 1] == s_first[i])
+      for (int e = tid; e < p.Hq * D / 8; e += kPaThreads)
+        reinterpret_cast<uint4*>(p.out + (size_t)i * p.Hq * D)[e] = make_uint4(0u, 0u, 0u, 0u);
+
+  const long long chunk = (all + gridDim.x - 1) / gridDim.x;
+  const long long lo = chunk * blockIdx.x, hi = min(all, lo + chunk);
+  if (lo >= hi) return;
+  int i0 = 0;   // the sequence of tile lo: the last whose first tile is at or before it
+  for (int b = p.n - 1; i0 < b;) {
+    const int mid = (i0 + b + 1) >> 1;
+    if (s_first[mid] <= lo) i0 = mid;
+    else b = mid - 1;
+  }
+
+  // a run of tiles of one sequence and head block
+  struct Seg {
+    int i, hh, s, len, t0, t1;   // listed index, head block, table row, length, tiles [t0, t1)
+  };
+  auto segment = [&](long long at, int i) {   // the segment that holds tile `at` of sequence i (or a later one)
+    while (s_first[i + 1] <= at) ++i;
+    Seg g;
+    g.i = i;
+    g.s = __ldg(p.ids + i);
+    g.len = __ldcg(p.seqs.lens + g.s);
+    const int T = tiles_of(g.len);
+    const long long off = at - s_first[i];
+    g.hh = (int)(off / T);
+    g.t0 = (int)(off % T);
+    const long long left = hi - at;
+    g.t1 = (long long)(T - g.t0) <= left ? T : g.t0 + (int)left;
+    return g;
+  };
+
+  if (warp == kCompWarps) {
+    // ---------------- pages and loads ----------------
+    const int R = ps < kTile ? ps : kTile;          // rows of a box
+    const int nb = kTile / R;                       // boxes of a tile's K slab
+    constexpr int kPer = 2 * (D / 64);              // K and V slabs of a box
+    const int box = lane / kPer, which = lane % kPer;
+    const bool is_v = which >= D / 64;
+    const int slab = which % (D / 64);
+    const uint64_t pol = policy_evict_first();
+    bool ok = true;
+    int issued = 0;
+    long long at = lo;
+    int i = i0;
+    while (at < hi && ok) {
+      const Seg g = segment(at, i);
+      i = g.i;
+      const int32_t* row = p.seqs.pages + (size_t)g.s * p.seqs.max_pages;
+      const int h = g.hh / p.HB;
+      auto entry = [&](int t) {   // this lane's page of tile t, -1 past the length
+        const int tok = t * kTile + box * R;
+        return box < nb && tok < g.len ? __ldcg(row + tok / ps) : -1;
+      };
+      int page = entry(g.t0);
+      for (int t = g.t0; t < g.t1 && ok; ++t) {
+        const int tok = t * kTile + box * R;
+        const bool in = box < nb && tok < g.len;
+        const bool good = in && page >= 0 && page < p.pool.n_pages;
+        if (in && !good) status_set(p.status, TV_E_PAGE);
+        const int y = good ? (int)((((size_t)p.layer * p.pool.n_pages + page) * Hkv + h) * ps) + tok % ps : 0;
+        if (t + 1 < g.t1) page = entry(t + 1);
+        const int st = issued % kStages;
+        if (issued >= kStages) ok = mbar_wait(&empty[st], (uint32_t)(issued / kStages - 1) & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const unsigned boxes = __ballot_sync(0xffffffffu, good);
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(boxes) * (uint32_t)(R * 128));
+        __syncwarp();
+        if (good)
+          tma_load_2d(smem + st * L::STAGE + (is_v ? L::HALF : 0) + slab * L::SLAB + box * R * 128, is_v ? &map_v : &map_k,
+                      &full[st], slab * 64, y, pol);
+        __syncwarp();
+        ++issued;
+      }
+      at += g.t1 - g.t0;
+    }
+    if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
+    // loads in flight land before the CTA leaves
+    for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u) mbar_wait(&full[u % kStages], (uint32_t)(u / kStages) & 1u);
+    return;
+  }
+
+  // ---------------- compute warps ----------------
+  constexpr int KS = D / 16;                        // k steps of S, and pairs of n blocks of O
+  const int quad = warp >> 2, sl = warp & 3;        // tiles with (count mod 2) == quad; tokens 16 sl .. + 15 of a tile
+  const int g8 = lane >> 2, t4 = lane & 3;
+  bool ok = true;
+  int cnt = 0;                                      // tiles of this CTA before the current one
+  long long at = lo;
+  int i = i0;
+  // lane addresses inside a slab: K as [token][d] fragments, V transposed
+  const int k_tok = 16 * sl + (lane & 7) + ((lane >> 4) << 3), k_ch = (lane >> 3) & 1;
+  const int v_tok = 16 * sl + (lane & 15), v_ch = lane >> 4;
+  while (at < hi) {
+    const Seg g = segment(at, i);
+    i = g.i;
+    const int h = g.hh / p.HB, r0 = (g.hh % p.HB) * kRows;   // KV head, first query head of the block in the group
+    const int nr = min(kRows, p.G - r0);
+    uint32_t qf[KS][4];
+    {
+      const __nv_bfloat16* q0 = p.q + (size_t)g.i * p.q_stride + (size_t)(h * p.G + r0) * D + 2 * t4;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const __nv_bfloat16 *a = q0 + (size_t)g8 * D + 16 * k, *b = a + 8 * D;
+        qf[k][0] = g8 < nr ? __ldcg(reinterpret_cast<const uint32_t*>(a)) : 0u;
+        qf[k][1] = g8 + 8 < nr ? __ldcg(reinterpret_cast<const uint32_t*>(b)) : 0u;
+        qf[k][2] = g8 < nr ? __ldcg(reinterpret_cast<const uint32_t*>(a + 8)) : 0u;
+        qf[k][3] = g8 + 8 < nr ? __ldcg(reinterpret_cast<const uint32_t*>(b + 8)) : 0u;
+      }
+    }
+    float o[2 * KS][4];
+#pragma unroll
+    for (int k = 0; k < 2 * KS; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // rows g8 and g8 + 8; sums of this thread's tokens
+
+    for (int t = g.t0; t < g.t1; ++t, ++cnt) {
+      if ((cnt & 1) != quad) continue;
+      const int st = cnt % kStages;
+      uint8_t* sk = smem + st * L::STAGE;
+      uint8_t* sv = sk + L::HALF;
+      if (ok && !mbar_wait(&full[st], (uint32_t)(cnt / kStages) & 1u)) ok = false;
+      const int valid = min(16, g.len - t * kTile - 16 * sl);   // this warp's tokens
+      if (valid > 0) {
+        bool wrote = false;
+        if (p.k_new && t * kTile + 16 * sl + valid == g.len) {
+          // the new token: its rows into the tile and into the page
+          const bool v = lane >= 16;
+          const int c = lane & 15;
+          if (c < D / 8) {
+            const uint4 x = __ldcg(reinterpret_cast<const uint4*>((v ? p.v_new : p.k_new) + (size_t)g.i * p.kv_stride + (size_t)h * D) + c);
+            *reinterpret_cast<uint4*>((v ? sv : sk) + (c >> 3) * L::SLAB + swz(16 * sl + valid - 1, c & 7)) = x;
+            if (r0 == 0) {
+              const int page = __ldcg(p.seqs.pages + (size_t)g.s * p.seqs.max_pages + (g.len - 1) / ps);
+              if (page >= 0 && page < p.pool.n_pages) {
+                const size_t e = ((((size_t)p.layer * p.pool.n_pages + page) * Hkv + h) * ps + (g.len - 1) % ps) * D;
+                reinterpret_cast<uint4*>((v ? p.pool.v : p.pool.k) + e)[c] = x;
+              }
+            }
+          }
+          wrote = true;
+        }
+        if (valid < 16) {   // slots past the length: whatever they hold, 0 * V stays 0
+          for (int e = lane; e < (16 - valid) * (D / 8); e += 32) {
+            const int tk = 16 * sl + valid + e / (D / 8), c = e % (D / 8);
+            *reinterpret_cast<uint4*>(sv + (c >> 3) * L::SLAB + swz(tk, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          wrote = true;
+        }
+        __syncwarp();
+        float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t ka = smem_u32(sk), va = smem_u32(sv);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t b[4];
+          ldsm4(ka + (k >> 2) * L::SLAB + swz(k_tok, ((2 * k) & 7) + k_ch), b);
+          mma16816(c0, qf[k], b[0], b[1]);
+          mma16816(c1, qf[k], b[2], b[3]);
+        }
+        // tokens 2 t4, 2 t4 + 1 (c0) and 8 more (c1) of rows g8 (elements 0, 1) and g8 + 8 (2, 3)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tk = 2 * t4 + (e & 1);
+          c0[e] = tk < valid ? c0[e] * p.scale_log2 : -INFINITY;
+          c1[e] = tk + 8 < valid ? c1[e] * p.scale_log2 : -INFINITY;
+        }
+        float x0 = fmaxf(fmaxf(c0[0], c0[1]), fmaxf(c1[0], c1[1])), x1 = fmaxf(fmaxf(c0[2], c0[3]), fmaxf(c1[2], c1[3]));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+        if (__any_sync(0xffffffffu, x0 > m0 + kMoveLog2 || x1 > m1 + kMoveLog2)) {
+          const float n0 = x0 > m0 + kMoveLog2 ? x0 : m0, n1 = x1 > m1 + kMoveLog2 ? x1 : m1;
+          const float a0 = n0 == m0 ? 1.f : ex2f(m0 - n0), a1 = n1 == m1 ? 1.f : ex2f(m1 - n1);
+          m0 = n0;
+          m1 = n1;
+          l0 *= a0;
+          l1 *= a1;
+#pragma unroll
+          for (int k = 0; k < 2 * KS; ++k) {
+            o[k][0] *= a0;
+            o[k][1] *= a0;
+            o[k][2] *= a1;
+            o[k][3] *= a1;
+          }
+        }
+        const float f0 = m0 == -INFINITY ? 0.f : m0, f1 = m1 == -INFINITY ? 0.f : m1;
+        uint32_t pf[4];
+        auto pack = [](float a, float b, float& l) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(&v);
+          l += __uint_as_float(u << 16) + __uint_as_float(u & 0xffff0000u);
+          return u;
+        };
+        pf[0] = pack(ex2f(c0[0] - f0), ex2f(c0[1] - f0), l0);
+        pf[1] = pack(ex2f(c0[2] - f1), ex2f(c0[3] - f1), l1);
+        pf[2] = pack(ex2f(c1[0] - f0), ex2f(c1[1] - f0), l0);
+        pf[3] = pack(ex2f(c1[2] - f1), ex2f(c1[3] - f1), l1);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t b[4];
+          ldsm4t(va + (k >> 2) * L::SLAB + swz(v_tok, ((2 * k) & 7) + v_ch), b);
+          mma16816(o[2 * k], pf, b[0], b[1]);
+          mma16816(o[2 * k + 1], pf, b[2], b[3]);
+        }
+        if (wrote) fence_async_smem();   // before the stage takes another TMA write
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+
+    // ---- the head block's eight partial results into one ----
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (t4 == 0) {
+      s_ml[warp * kRows + g8] = make_float2(m0, l0);
+      s_ml[warp * kRows + g8 + 8] = make_float2(m1, l1);
+    }
+    comp_sync();
+    const int T = tiles_of(g.len);
+    const bool whole = g.t0 == 0 && g.t1 == T;
+    const size_t slot = (size_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0);   // a CTA's first segment may begin inside a head, its last end inside one
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (8 * half < nr) {
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kCompWarps; ++w) M = fmaxf(M, s_ml[w * kRows + g8 + 8 * half].x);
+        const float mine = half ? m1 : m0;
+        const float f = mine == -INFINITY ? 0.f : ex2f(mine - M);
+        float* dst = s_red + (warp * 8 + g8) * D + 2 * t4;
+#pragma unroll
+        for (int k = 0; k < 2 * KS; ++k)
+          *reinterpret_cast<float2*>(dst + 8 * k) = make_float2(o[k][2 * half] * f, o[k][2 * half + 1] * f);
+        comp_sync();
+        for (int e = tid; e < 8 * (D / 2); e += kCompThreads) {
+          const int r = e / (D / 2), d = 2 * (e % (D / 2)), row = r + 8 * half;
+          if (row < nr) {
+            float M2 = -INFINITY, Ls = 0.f;
+            float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kCompWarps; ++w) M2 = fmaxf(M2, s_ml[w * kRows + row].x);
+#pragma unroll
+            for (int w = 0; w < kCompWarps; ++w) {
+              const float2 ml = s_ml[w * kRows + row];
+              Ls += ml.x == -INFINITY ? ml.y : ml.y * ex2f(ml.x - M2);
+              const float2 v = *reinterpret_cast<const float2*>(s_red + (w * 8 + r) * D + d);
+              acc.x += v.x;
+              acc.y += v.y;
+            }
+            if (whole) {
+              *reinterpret_cast<__nv_bfloat162*>(p.out + ((size_t)g.i * p.Hq + h * p.G + r0 + row) * D + d) =
+                  __floats2bfloat162_rn(acc.x / Ls, acc.y / Ls);
+            } else {
+              *reinterpret_cast<float2*>(p.ws.o + (slot * kRows + row) * D + d) = acc;
+              if (d == 0) *reinterpret_cast<float2*>(p.ws.ml + (slot * kRows + row) * 2) = make_float2(M2, Ls);
+            }
+          }
+        }
+        comp_sync();
+      }
+    }
+    at += g.t1 - g.t0;
+  }
+  if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
+}
+
+// One block per (listed sequence, query head) that a range border cut: its
+// partials in tile order.
+template <int D>
+__global__ void __launch_bounds__(D) paged_merge_kernel(const PaParams p, int ctas) {
+  pdl_wait();
+  pdl_trigger();
+  if (status_get(p.status) != 0) return;
+  const int i = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, d = threadIdx.x;
+  const long long f0 = __ldcg(p.ws.first + i), f1 = __ldcg(p.ws.first + i + 1), all = __ldcg(p.ws.first + p.n);
+  if (f0 == f1) return;
+  const long long T = (f1 - f0) / (p.pool.n_kv_heads * p.HB), chunk = (all + ctas - 1) / ctas;
+  const int row = (hq % p.G) % kRows, hh = (hq / p.G) * p.HB + (hq % p.G) / kRows;
+  const long long a = f0 + hh * T, b = a + T;
+  const int c0 = (int)(a / chunk), c1 = (int)((b - 1) / chunk);
+  if (c0 == c1) return;
+  float M = -INFINITY;
+  for (int c = c0; c <= c1; ++c) {
+    const size_t slot = (size_t)c * 2 + (a >= c * chunk ? 1 : 0);
+    M = fmaxf(M, __ldcg(p.ws.ml + (slot * kRows + row) * 2));
+  }
+  float Ls = 0.f, o = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const size_t slot = (size_t)c * 2 + (a >= c * chunk ? 1 : 0);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws.ml + (slot * kRows + row) * 2));
+    const float w = ml.x == -INFINITY ? 0.f : ex2f(ml.x - M);
+    Ls += ml.x == -INFINITY ? ml.y : ml.y * w;
+    o += __ldcg(p.ws.o + (slot * kRows + row) * D + d) * w;
+  }
+  p.out[((size_t)i * p.Hq + hq) * D + d] = f2bf(o / Ls);
+}
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+size_t pa_ws(int n, int D, PaWs* ws, uint8_t* base) {
+  const size_t first = align256((size_t)(n + 1) * 8), ml = align256((size_t)2 * kMaxCtas * kRows * 2 * 4);
+  const size_t o = align256((size_t)2 * kMaxCtas * kRows * D * 4);
+  if (ws) {
+    ws->first = reinterpret_cast<long long*>(base);
+    ws->ml = reinterpret_cast<float*>(base + first);
+    ws->o = reinterpret_cast<float*>(base + first + ml);
+  }
+  return first + ml + o;
+}
+
+int check_heads(int n_q_heads, int n_kv_heads) {
+  if (n_q_heads < 1) return TV_E_ARG;
+  return n_q_heads % n_kv_heads != 0 || n_q_heads > 65536 ? TV_E_UNSUPPORTED : TV_OK;
+}
+
+template <int D>
+int launch_paged(const PaParams& p, int sms, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  const int rows = p.pool.n_layers * p.pool.n_pages * p.pool.n_kv_heads * p.pool.page_size;   // checked to fit
+  const int R = p.pool.page_size < kTile ? p.pool.page_size : kTile;
+  int rc = make_tmap_bf16(&mk, p.pool.k, D, rows, 64, R);
+  if (rc || (rc = make_tmap_bf16(&mv, p.pool.v, D, rows, 64, R))) return rc;
+  static std::atomic<bool> attr[64];
+  if (ensure_smem_limit(paged_attn_kernel<D>, PaSmem<D>::bytes(kMaxListed), attr)) return TV_E_CUDA;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  rc = launch_pdl(paged_attn_kernel<D>, dim3(ctas), dim3(kPaThreads), PaSmem<D>::bytes(p.n), st, mk, mv, p);
+  if (rc) return rc;
+  return launch_pdl(paged_merge_kernel<D>, dim3(p.n * p.Hq), dim3(D), 0, st, p, ctas);
+}
+
+}  // namespace
+}  // namespace tv
+
+using namespace tv;
+
+extern "C" {
+
+int tv_attend_paged_workspace_size(const tv_pool* pool, int n_q_heads, int n, size_t* bytes) {
+  int rc = check_pool(pool);
+  if (rc || (rc = check_heads(n_q_heads, pool->n_kv_heads)) || (rc = check_listed(n))) return rc;
+  if (!bytes) return TV_E_ARG;
+  *bytes = pa_ws(n, pool->head_dim, nullptr, nullptr);
+  return TV_OK;
+}
+
+int tv_attend_paged(const tv_pool* pool, int layer, const tv_seqs* seqs, const int32_t* ids, int n, int n_q_heads,
+                    const tv_bf16* q, size_t q_stride, const tv_bf16* k_new, const tv_bf16* v_new, size_t kv_stride,
+                    tv_bf16* out, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  int rc = check_pool(pool);
+  if (rc || (rc = check_seqs(seqs, pool))) return rc;
+  if (!ids || !q || !out || !dev_status || !k_new != !v_new || layer < 0 || layer >= pool->n_layers) return TV_E_ARG;
+  if ((rc = check_heads(n_q_heads, pool->n_kv_heads)) || (rc = check_listed(n))) return rc;
+  const size_t D = pool->head_dim;
+  if (!aligned16(q) || !aligned16(out) || q_stride % 8 != 0 || q_stride < n_q_heads * D) return TV_E_ARG;
+  if (k_new && (!aligned16(k_new) || !aligned16(v_new) || kv_stride % 8 != 0 || kv_stride < pool->n_kv_heads * D))
+    return TV_E_ARG;
+  if ((long long)n * n_q_heads > 0x7fffffffll) return TV_E_UNSUPPORTED;
+  PaParams p;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < pa_ws(n, pool->head_dim, &p.ws, base)) return TV_E_WORKSPACE;
+  const int sms = num_sms();
+  if (sms <= 0) return TV_E_CUDA;
+  p.pool = *pool;
+  p.seqs = *seqs;
+  p.ids = ids;
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.k_new = reinterpret_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = reinterpret_cast<const __nv_bfloat16*>(v_new);
+  p.q_stride = q_stride;
+  p.kv_stride = kv_stride;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.status = dev_status;
+  p.layer = layer;
+  p.n = n;
+  p.Hq = n_q_heads;
+  p.G = n_q_heads / pool->n_kv_heads;
+  p.HB = (p.G + kRows - 1) / kRows;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)pool->head_dim));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return pool->head_dim == 128 ? launch_paged<128>(p, sms, st) : launch_paged<64>(p, sms, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,150 @@
+"""Host side of the paged cache: argument checks (nothing is launched when one
+fails) and the oracle's own rules by hand on a small pool."""
+import numpy as np
+import pytest
+
+from oracle.paged import Cache, Refused, attend, attend_prompt
+from speculative_tree_verify_gb300 import abi, build
+
+FAKE = 0x10000   # 16-byte aligned, never dereferenced on these paths
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return abi.load()
+
+
+def _pool(**over):
+    a = dict(k=FAKE, v=FAKE, refs=FAKE, n_layers=2, n_pages=64, n_kv_heads=2, page_size=16, head_dim=64)
+    a.update(over)
+    return abi.TvPool(*a.values())
+
+
+def _seqs(**over):
+    a = dict(pages=FAKE, lens=FAKE, max_seqs=8, max_pages=10)
+    a.update(over)
+    return abi.TvSeqs(*a.values())
+
+
+CALLS = {
+    "extend": lambda pool, seqs, n=3, ids=FAKE, ws=FAKE, wsb=1 << 30, st=FAKE: abi.tv_pages_extend(pool, seqs, ids, FAKE, n, ws, wsb, st),
+    "fork": lambda pool, seqs, n=3, ids=FAKE, ws=FAKE, wsb=1 << 30, st=FAKE: abi.tv_pages_fork(pool, seqs, ids, FAKE, n, st),
+    "release": lambda pool, seqs, n=3, ids=FAKE, ws=FAKE, wsb=1 << 30, st=FAKE: abi.tv_pages_release(pool, seqs, ids, FAKE, n, st),
+    "compact": lambda pool, seqs, n=3, ids=FAKE, ws=FAKE, wsb=1 << 30, st=FAKE: abi.tv_pages_compact(pool, seqs, ids, FAKE, ws, wsb, st),
+    "write": lambda pool, seqs, n=3, ids=FAKE, ws=FAKE, wsb=1 << 30, st=FAKE: abi.tv_pages_write(pool, 0, seqs, ids, FAKE, FAKE, n, 9, FAKE, FAKE, 128, 64, st),
+    "read": lambda pool, seqs, n=3, ids=FAKE, ws=FAKE, wsb=1 << 30, st=FAKE: abi.tv_pages_read(pool, 0, seqs, ids, FAKE, FAKE, n, 9, FAKE, FAKE, 128, 64, st),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_pages_host_checks(name):
+    call, E = CALLS[name], abi.CODES
+    for over in (dict(k=None), dict(v=None), dict(refs=None), dict(k=FAKE + 2), dict(refs=FAKE + 4), dict(n_layers=0),
+                 dict(n_pages=0), dict(n_kv_heads=0)):
+        assert call(_pool(**over), _seqs()) == E["TV_E_ARG"], over
+    for over in (dict(page_size=8), dict(page_size=24), dict(page_size=256), dict(head_dim=96), dict(head_dim=0),
+                 dict(n_pages=1 << 30, n_layers=4), dict(n_pages=1 << 26)):
+        assert call(_pool(**over), _seqs()) == E["TV_E_UNSUPPORTED"], over
+    for over in (dict(pages=None), dict(lens=None), dict(max_seqs=0), dict(max_pages=0)):
+        assert call(_pool(), _seqs(**over)) == E["TV_E_ARG"], over
+    for over in (dict(max_seqs=65537), dict(max_pages=1 << 28)):
+        assert call(_pool(), _seqs(**over)) == E["TV_E_UNSUPPORTED"], over
+    assert call(_pool(), _seqs(), ids=None) == E["TV_E_ARG"]
+    assert call(_pool(), _seqs(), st=None) == E["TV_E_ARG"]
+    if name != "compact":
+        assert call(_pool(), _seqs(), n=0) == E["TV_E_ARG"]
+        assert call(_pool(), _seqs(), n=4097) == E["TV_E_UNSUPPORTED"]
+    if name in ("extend", "compact"):
+        need = abi.tv_pages_workspace_size(_pool(), _seqs())
+        assert need > 0 and need % 256 == 0
+        assert call(_pool(), _seqs(), wsb=need - 1) == E["TV_E_WORKSPACE"]
+        assert call(_pool(), _seqs(), ws=None) == E["TV_E_WORKSPACE"]
+        assert call(_pool(), _seqs(), ws=FAKE + 8) == E["TV_E_WORKSPACE"]
+
+
+@pytest.mark.parametrize("fn", [abi.tv_pages_write, abi.tv_pages_read])
+def test_rows_host_checks(fn):
+    E = abi.CODES
+
+    def call(layer=1, rows=9, k=FAKE, v=FAKE, rs=128, hs=64):
+        return fn(_pool(), layer, _seqs(), FAKE, FAKE, FAKE, 3, rows, k, v, rs, hs, FAKE)
+
+    for over in (dict(layer=-1), dict(layer=2), dict(rows=-1), dict(k=None), dict(v=None), dict(k=FAKE + 2), dict(v=FAKE + 8),
+                 dict(rs=129), dict(hs=68)):
+        assert call(**over) == E["TV_E_ARG"], over
+
+
+def test_attend_paged_host_checks():
+    E = abi.CODES
+    need = abi.tv_attend_paged_workspace_size(_pool(), 8, 3)
+    assert need > 0 and need % 256 == 0
+    with pytest.raises(ValueError, match="UNSUPPORTED"):
+        abi.tv_attend_paged_workspace_size(_pool(), 7, 3)
+    with pytest.raises(ValueError, match="ARG"):
+        abi.tv_attend_paged_workspace_size(_pool(), 0, 3)
+
+    def call(pool=None, layer=0, seqs=None, ids=FAKE, n=3, hq=8, q=FAKE, qs=512, k=FAKE, v=FAKE, kvs=128, out=FAKE, ws=FAKE, wsb=need, st=FAKE):
+        return abi.tv_attend_paged(pool or _pool(), layer, seqs or _seqs(), ids, n, hq, q, qs, k, v, kvs, out, ws, wsb, st)
+
+    for over in (dict(ids=None), dict(q=None), dict(out=None), dict(st=None), dict(k=None), dict(v=None), dict(layer=2), dict(layer=-1),
+                 dict(n=0), dict(hq=0), dict(q=FAKE + 2), dict(out=FAKE + 8), dict(k=FAKE + 2), dict(v=FAKE + 2), dict(qs=516), dict(qs=504),
+                 dict(kvs=132), dict(kvs=120), dict(pool=_pool(k=None)), dict(seqs=_seqs(lens=None))):
+        assert call(**over) == E["TV_E_ARG"], over
+    for over in (dict(n=4097), dict(hq=9), dict(pool=_pool(head_dim=96)), dict(pool=_pool(page_size=20))):
+        assert call(**over) == E["TV_E_UNSUPPORTED"], over
+    for over in (dict(wsb=need - 1), dict(ws=None), dict(ws=FAKE + 8)):
+        assert call(**over) == E["TV_E_WORKSPACE"], over
+
+
+def test_workspace_refuses_bad_shapes():
+    with pytest.raises(ValueError, match="UNSUPPORTED"):
+        abi.tv_pages_workspace_size(_pool(page_size=17), _seqs())
+    with pytest.raises(ValueError, match="ARG"):
+        abi.tv_pages_workspace_size(_pool(), _seqs(max_pages=0))
+
+
+# ---- the oracle by hand -------------------------------------------------------
+def _cache(n_pages=6, max_seqs=4, max_pages=3):
+    k = np.arange(2 * n_pages * 16 * 4, dtype=np.uint16).reshape(2, n_pages, 1, 16, 4)
+    return Cache(k.copy(), k + 7, np.zeros(n_pages, np.int32), np.full((max_seqs, max_pages), -9, np.int32), np.zeros(max_seqs, np.int32))
+
+
+def test_oracle_extend_fork_release():
+    c = _cache()
+    c.extend([2, 0], [17, 16])
+    assert c.pages[2].tolist() == [0, 1, -9] and c.pages[0].tolist() == [2, -9, -9]
+    assert c.refs.tolist() == [1, 1, 1, 0, 0, 0] and c.lens.tolist() == [16, 0, 17, 0]
+    c.fork([2, 2], [1, 3])
+    assert c.refs.tolist() == [3, 3, 1, 0, 0, 0] and c.lens.tolist() == [16, 17, 17, 17]
+    old = c.k[:, 1].copy()
+    c.extend([1, 2, 3, 0], [1, 2, 3, 0])   # three holders of page 1: the last in the list keeps it
+    assert c.pages[1].tolist() == [0, 3, -9] and c.pages[2].tolist() == [0, 4, -9] and c.pages[3].tolist() == [0, 1, -9]
+    assert c.refs.tolist() == [3, 1, 1, 1, 1, 0] and (c.k[:, 3] == old).all() and (c.k[:, 4] == old).all()
+    with pytest.raises(Refused, match="CAPACITY"):
+        c.extend([0, 3], [16, 14])
+    assert c.lens.tolist() == [16, 18, 19, 20] and c.refs.tolist() == [3, 1, 1, 1, 1, 0]
+    c.release([1, 3], [0, 16])
+    assert c.refs.tolist() == [2, 0, 1, 0, 1, 0] and c.lens.tolist() == [16, 0, 19, 16]
+    last = c.k[:, 4].copy()
+    remap, used = c.compact()
+    assert used == 3 and remap.tolist() == [0, -1, 2, -1, 1, -1] and c.refs.tolist() == [2, 1, 1, 0, 0, 0]
+    assert c.pages[2].tolist() == [0, 1, -9] and (c.k[:, 1] == last).all()
+    for bad in (([0, 0], [1, 1]), ([4], [1]), ([0], [-1])):
+        with pytest.raises(Refused, match="SEQ"):
+            c.extend(*bad)
+
+
+def test_oracle_attention_closed_forms():
+    rng = np.random.default_rng(0)
+    v = rng.standard_normal((5, 2, 8))
+    q = np.zeros((4, 8))
+    out = attend(q, rng.standard_normal((5, 2, 8)), v)   # no preference: the mean
+    assert np.allclose(out, np.repeat(v.mean(0), 2, axis=0))
+    k = np.zeros((5, 2, 8))
+    k[3] = 1000.0
+    assert np.allclose(attend(np.ones((4, 8)), k, v), np.repeat(v[3], 2, axis=0))   # one key takes all
+    assert (attend(q, k[:0], v[:0]) == 0).all()
+    o = attend_prompt(np.zeros((7, 4, 8)), np.zeros((7, 2, 8)), np.concatenate([v, v[:2]]), [1, 4, 4, 6])
+    assert np.isnan(o[0]).all() and np.isnan(o[6]).all()
+    assert np.allclose(o[3], np.repeat(v[1:4].mean(0), 2, axis=0)) and np.allclose(o[4], np.repeat(v[4], 2, axis=0))
