@@ -31,16 +31,21 @@ namespace tv {
 namespace {
 
 constexpr int kTile = 64;                        // tokens of a tile
-constexpr int kStages = 5;                       // tiles in flight: 160 KB of the SM at D = 128
+// Tiles in flight: 192 KB of the SM at D = 128.  Even, so that a stage always
+// belongs to the same four warps: their waits then see every phase of its
+// barrier, and a parity can not name the phase before last.
+constexpr int kStages = 6;
+static_assert(kStages % 2 == 0, "tile t: stage t mod kStages, warps 4 (t mod 2) .. + 3");
 constexpr int kCompWarps = 8;
 constexpr int kCompThreads = kCompWarps * 32;
 constexpr int kPaThreads = kCompThreads + 32;
 constexpr int kRows = 16;                        // query heads of a block
+constexpr int kRedRows = 4;                      // rows joined at a time when a head block ends
 constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 a CTA
 constexpr float kMoveLog2 = 8.f;
 
 struct PaWs {
-  long long* first;   // [n + 1]: first tile of each sequence in the list of tiles
+  uint32_t* first;    // [n + 1]: first tile of each sequence in the list of tiles
   float* ml;          // [2 CTAs][kRows][2]: offset and sum
   float* o;           // [2 CTAs][kRows][D]
 };
@@ -63,11 +68,13 @@ struct PaSmem {
   static constexpr int SLAB = kTile * 128;                   // 64 dimensions of a tile
   static constexpr int HALF = (D / 64) * SLAB;               // a tile's K (or V)
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int OFF_RED = kStages * STAGE;            // [8 warps][8 rows][D] fp32; the marks of listed rows first
-  static constexpr int OFF_ML = OFF_RED + kCompWarps * 8 * D * 4;
+  static constexpr int OFF_RED = kStages * STAGE;            // [8 warps][kRedRows][D] fp32; the marks of listed rows first
+  static constexpr int OFF_ML = OFF_RED + kCompWarps * kRedRows * D * 4;
   static constexpr int OFF_BAR = OFF_ML + kCompWarps * kRows * 8;
-  static constexpr int OFF_FIRST = OFF_BAR + 256;            // [n + 1] long long
-  static size_t bytes(int n) { return 1024 + OFF_FIRST + (size_t)(n + 1) * 8; }
+  static constexpr int OFF_FIRST = OFF_BAR + 256;            // [n + 1]
+  static size_t bytes(int n) { return 1024 + OFF_FIRST + (size_t)(n + 1) * 4; }
+  static_assert(kCompWarps * kRedRows * D * 4 >= kMaxSeqs / 8, "a mark for every table row");
+  static_assert(1024 + OFF_FIRST + (kMaxListed + 1) * 4 <= 232448 - 256, "shared memory of one CTA");
 };
 
 __device__ __forceinline__ float ex2f(float x) {   // 2^x by the SFU, about 2^-22 relative, 2^-inf = 0
@@ -105,11 +112,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* empty = full + kStages;
-  long long* s_first = reinterpret_cast<long long*>(smem + L::OFF_FIRST);
+  uint32_t* s_first = reinterpret_cast<uint32_t*>(smem + L::OFF_FIRST);
   float* s_red = reinterpret_cast<float*>(smem + L::OFF_RED);
   float2* s_ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
   uint32_t* s_mark = reinterpret_cast<uint32_t*>(smem + L::OFF_RED);
-  __shared__ long long s_part[kPaThreads / 32];
+  __shared__ uint32_t s_part[kPaThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ps = p.pool.page_size, Hkv = p.pool.n_kv_heads;
 
@@ -132,7 +139,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     __syncthreads();
   }
   const int per = (p.n + kPaThreads - 1) / kPaThreads;
-  long long sum = 0;
+  uint32_t sum = 0;   // the host has seen to it that all of them fit 31 bits
   for (int i = tid * per; i < min(p.n, (tid + 1) * per); ++i) {
     const int s = p.ids[i];
     int len = -1;
@@ -142,18 +149,18 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     if (len < 0) bad = TV_E_SEQ;
     s_first[i] = sum;
-    sum += (long long)tiles_of(max(len, 0)) * Hkv * p.HB;
+    sum += (uint32_t)(tiles_of(max(len, 0)) * Hkv * p.HB);
   }
   if (bad < 0) status_set(p.status, bad);
-  long long x = sum;
+  uint32_t x = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) s_part[warp] = x;
   if (__syncthreads_or(bad)) return;
-  long long before = x - sum, all = 0;
+  uint32_t before = x - sum, all = 0;
   for (int w = 0; w < kPaThreads / 32; ++w) {
     if (w < warp) before += s_part[w];
     all += s_part[w];
@@ -169,8 +176,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       for (int e = tid; e < p.Hq * D / 8; e += kPaThreads)
         reinterpret_cast<uint4*>(p.out + (size_t)i * p.Hq * D)[e] = make_uint4(0u, 0u, 0u, 0u);
 
-  const long long chunk = (all + gridDim.x - 1) / gridDim.x;
-  const long long lo = chunk * blockIdx.x, hi = min(all, lo + chunk);
+  const uint32_t chunk = (all + gridDim.x - 1) / gridDim.x;
+  const uint32_t lo = chunk * blockIdx.x, hi = min(all, lo + chunk);
   if (lo >= hi) return;
   int i0 = 0;   // the sequence of tile lo: the last whose first tile is at or before it
   for (int b = p.n - 1; i0 < b;) {
@@ -183,18 +190,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   struct Seg {
     int i, hh, s, len, t0, t1;   // listed index, head block, table row, length, tiles [t0, t1)
   };
-  auto segment = [&](long long at, int i) {   // the segment that holds tile `at` of sequence i (or a later one)
+  auto segment = [&](uint32_t at, int i) {   // the segment that holds tile `at` of sequence i (or a later one)
     while (s_first[i + 1] <= at) ++i;
     Seg g;
     g.i = i;
     g.s = __ldg(p.ids + i);
     g.len = __ldcg(p.seqs.lens + g.s);
-    const int T = tiles_of(g.len);
-    const long long off = at - s_first[i];
+    const uint32_t T = tiles_of(g.len), off = at - s_first[i];
     g.hh = (int)(off / T);
     g.t0 = (int)(off % T);
-    const long long left = hi - at;
-    g.t1 = (long long)(T - g.t0) <= left ? T : g.t0 + (int)left;
+    g.t1 = (int)min(T, g.t0 + (hi - at));
     return g;
   };
 
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const uint64_t pol = policy_evict_first();
     bool ok = true;
     int issued = 0;
-    long long at = lo;
+    uint32_t at = lo;
     int i = i0;
     while (at < hi && ok) {
       const Seg g = segment(at, i);
@@ -255,7 +260,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   const int g8 = lane >> 2, t4 = lane & 3;
   bool ok = true;
   int cnt = 0;                                      // tiles of this CTA before the current one
-  long long at = lo;
+  uint32_t at = lo;
   int i = i0;
   // lane addresses inside a slab: K as [token][d] fragments, V transposed
   const int k_tok = 16 * sl + (lane & 7) + ((lane >> 4) << 3), k_ch = (lane >> 3) & 1;
@@ -393,20 +398,23 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const bool whole = g.t0 == 0 && g.t1 == T;
     const size_t slot = (size_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0);   // a CTA's first segment may begin inside a head, its last end inside one
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (8 * half < nr) {
-        float M = -INFINITY;
+    for (int part = 0; part < kRows / kRedRows; ++part) {   // rows 4 part .. + 3, held by the lanes with g8 / 4 = part mod 2
+      if (kRedRows * part < nr) {
+        const int half = part >> 1;
+        if ((g8 >> 2) == (part & 1)) {
+          float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kCompWarps; ++w) M = fmaxf(M, s_ml[w * kRows + g8 + 8 * half].x);
-        const float mine = half ? m1 : m0;
-        const float f = mine == -INFINITY ? 0.f : ex2f(mine - M);
-        float* dst = s_red + (warp * 8 + g8) * D + 2 * t4;
+          for (int w = 0; w < kCompWarps; ++w) M = fmaxf(M, s_ml[w * kRows + g8 + 8 * half].x);
+          const float mine = half ? m1 : m0;
+          const float f = mine == -INFINITY ? 0.f : ex2f(mine - M);
+          float* dst = s_red + (warp * kRedRows + (g8 & 3)) * D + 2 * t4;
 #pragma unroll
-        for (int k = 0; k < 2 * KS; ++k)
-          *reinterpret_cast<float2*>(dst + 8 * k) = make_float2(o[k][2 * half] * f, o[k][2 * half + 1] * f);
+          for (int k = 0; k < 2 * KS; ++k)
+            *reinterpret_cast<float2*>(dst + 8 * k) = make_float2(o[k][2 * half] * f, o[k][2 * half + 1] * f);
+        }
         comp_sync();
-        for (int e = tid; e < 8 * (D / 2); e += kCompThreads) {
-          const int r = e / (D / 2), d = 2 * (e % (D / 2)), row = r + 8 * half;
+        for (int e = tid; e < kRedRows * (D / 2); e += kCompThreads) {
+          const int r = e / (D / 2), d = 2 * (e % (D / 2)), row = r + kRedRows * part;
           if (row < nr) {
             float M2 = -INFINITY, Ls = 0.f;
             float2 acc = make_float2(0.f, 0.f);
@@ -416,7 +424,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             for (int w = 0; w < kCompWarps; ++w) {
               const float2 ml = s_ml[w * kRows + row];
               Ls += ml.x == -INFINITY ? ml.y : ml.y * ex2f(ml.x - M2);
-              const float2 v = *reinterpret_cast<const float2*>(s_red + (w * 8 + r) * D + d);
+              const float2 v = *reinterpret_cast<const float2*>(s_red + (w * kRedRows + r) * D + d);
               acc.x += v.x;
               acc.y += v.y;
             }
@@ -445,11 +453,11 @@ __global__ void __launch_bounds__(D) paged_merge_kernel(const PaParams p, int ct
   pdl_trigger();
   if (status_get(p.status) != 0) return;
   const int i = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, d = threadIdx.x;
-  const long long f0 = __ldcg(p.ws.first + i), f1 = __ldcg(p.ws.first + i + 1), all = __ldcg(p.ws.first + p.n);
+  const uint32_t f0 = __ldcg(p.ws.first + i), f1 = __ldcg(p.ws.first + i + 1), all = __ldcg(p.ws.first + p.n);
   if (f0 == f1) return;
-  const long long T = (f1 - f0) / (p.pool.n_kv_heads * p.HB), chunk = (all + ctas - 1) / ctas;
+  const uint32_t T = (f1 - f0) / (p.pool.n_kv_heads * p.HB), chunk = (all + ctas - 1) / ctas;
   const int row = (hq % p.G) % kRows, hh = (hq / p.G) * p.HB + (hq % p.G) / kRows;
-  const long long a = f0 + hh * T, b = a + T;
+  const uint32_t a = f0 + hh * T, b = a + T;
   const int c0 = (int)(a / chunk), c1 = (int)((b - 1) / chunk);
   if (c0 == c1) return;
   float M = -INFINITY;
@@ -472,10 +480,10 @@ __global__ void __launch_bounds__(D) paged_merge_kernel(const PaParams p, int ct
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t pa_ws(int n, int D, PaWs* ws, uint8_t* base) {
-  const size_t first = align256((size_t)(n + 1) * 8), ml = align256((size_t)2 * kMaxCtas * kRows * 2 * 4);
+  const size_t first = align256((size_t)(n + 1) * 4), ml = align256((size_t)2 * kMaxCtas * kRows * 2 * 4);
   const size_t o = align256((size_t)2 * kMaxCtas * kRows * D * 4);
   if (ws) {
-    ws->first = reinterpret_cast<long long*>(base);
+    ws->first = reinterpret_cast<uint32_t*>(base);
     ws->ml = reinterpret_cast<float*>(base + first);
     ws->o = reinterpret_cast<float*>(base + first + ml);
   }
@@ -528,8 +536,12 @@ int tv_attend_paged(const tv_pool* pool, int layer, const tv_seqs* seqs, const i
   if (!aligned16(q) || !aligned16(out) || q_stride % 8 != 0 || q_stride < n_q_heads * D) return TV_E_ARG;
   if (k_new && (!aligned16(k_new) || !aligned16(v_new) || kv_stride % 8 != 0 || kv_stride < pool->n_kv_heads * D))
     return TV_E_ARG;
-  if ((long long)n * n_q_heads > 0x7fffffffll) return TV_E_UNSUPPORTED;
   PaParams p;
+  p.G = n_q_heads / pool->n_kv_heads;
+  p.HB = (p.G + kRows - 1) / kRows;
+  // blocks of the joining kernel, and the tiles of n sequences of the longest kind
+  const unsigned long long most = ((unsigned long long)seqs->max_pages * pool->page_size + kTile - 1) / kTile * pool->n_kv_heads * p.HB;
+  if ((long long)n * n_q_heads > 0x7fffffffll || most > 0x7fffffffull / (unsigned)n) return TV_E_UNSUPPORTED;
   uint8_t* base = static_cast<uint8_t*>(workspace);
   if (!workspace || !aligned16(workspace) || workspace_bytes < pa_ws(n, pool->head_dim, &p.ws, base)) return TV_E_WORKSPACE;
   const int sms = num_sms();
@@ -547,8 +559,6 @@ int tv_attend_paged(const tv_pool* pool, int layer, const tv_seqs* seqs, const i
   p.layer = layer;
   p.n = n;
   p.Hq = n_q_heads;
-  p.G = n_q_heads / pool->n_kv_heads;
-  p.HB = (p.G + kRows - 1) / kRows;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)pool->head_dim));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return pool->head_dim == 128 ? launch_paged<128>(p, sms, st) : launch_paged<64>(p, sms, st);

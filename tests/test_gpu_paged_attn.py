@@ -131,6 +131,17 @@ def test_long_short_and_many(gpu, lens):
     Case(lens, 8, 2, 128, 32, seed=len(lens)).check()
 
 
+@pytest.mark.parametrize("dim,ps", [(128, 64), (64, 16)])
+def test_many_tiles_a_cta(gpu, dim, ps):
+    """Some thirty tiles a CTA: the ring of stages goes round often.  Every run gives the same bits."""
+    c = Case([40001, 5], 16, 8, dim, ps, new=False)
+    c.check()
+    first = host(c.out).copy()
+    for _ in range(200):
+        assert c.run() == 0
+    assert np.array_equal(host(c.out), first) and int(c.status.item()) == 0
+
+
 def test_large_scores_move_the_offsets(gpu):
     """Scores of some hundreds, rising along the sequence: every offset moves, small weights vanish."""
     c = Case([333, 1000], 8, 2, 64, 16, new=False, scale=30.0)
