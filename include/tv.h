@@ -678,6 +678,33 @@ TV_API int tv_pages_read(const tv_pool *pool, int layer, const tv_seqs *seqs, co
                          size_t head_stride, int32_t *dev_status, void *stream);
 
 /*
+ * Attention over whole prompts, causal, packed: what fills a cache before the
+ * first round.  Sequence i is rows starts[i] .. starts[i + 1] - 1 of q, k, v
+ * and out; its row t sees its rows 0 .. t,
+ *     out[t][h] = sum_{j <= t} softmax_j(q[t][h] . k[j][g] / sqrt(head_dim)) v[j][g],
+ *     g = h / (n_q_heads / n_kv_heads).
+ * Rows of no sequence (before starts[0], behind starts[n_seqs]) are left as
+ * they were in out.  Positions were applied before (RoPE), as in tv_kv.
+ *
+ *   q, k, v   device bf16, 16-byte aligned: head h of row t at t * q_stride + h * head_dim
+ *             (k and v: kv_stride), strides in elements, multiples of 8, at least a row's
+ *             heads: the Q, K and V heads of a QKV projection's rows
+ *   starts    device int32 [n_seqs + 1], ascending within 0 .. rows; a sequence may be empty
+ *   rows      host: rows of q, k, v and out, >= 1
+ *   out       device bf16 [rows][n_q_heads][head_dim], 16-byte aligned; may not overlap the inputs
+ * head_dim 64 or 128, n_q_heads a multiple of n_kv_heads with at most 128 query
+ * heads a KV head, at most 4096 sequences (else TV_E_UNSUPPORTED).  P is
+ * rounded to bf16 for the product with V, everything else is fp32.  What a row
+ * may not see does not reach it, whatever it holds.  The same inputs give the
+ * same bits.  No workspace.
+ * Host checks: TV_E_ARG, TV_E_UNSUPPORTED.  Device checks: TV_E_SEQ (starts;
+ * nothing is written).
+ */
+TV_API int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const tv_bf16 *q, const tv_bf16 *k,
+                            const tv_bf16 *v, size_t q_stride, size_t kv_stride, const int32_t *starts, int n_seqs,
+                            int rows, tv_bf16 *out, int32_t *dev_status, void *stream);
+
+/*
  * Attention of one new token per sequence over its pages, the single-token
  * form of the prompt's attention: query head h of listed sequence i attends to
  * every token of sequence ids[i] in layer `layer`,

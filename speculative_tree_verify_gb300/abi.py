@@ -32,7 +32,8 @@ SYMBOLS = ("tv_workspace_size", "tv_verify_tree", "tv_accept_greedy", "tv_accept
            "tv_price_observe", "tv_staircut", "tv_packed_weight_bytes", "tv_pack_weight",
            "tv_accept_greedy_commit", "tv_stack_workspace_size", "tv_verify_stack", "tv_commit_stack",
            "tv_pages_workspace_size", "tv_pages_extend", "tv_pages_fork", "tv_pages_release", "tv_pages_compact",
-           "tv_pages_write", "tv_pages_read", "tv_attend_paged_workspace_size", "tv_attend_paged")
+           "tv_pages_write", "tv_pages_read", "tv_attend_paged_workspace_size", "tv_attend_paged",
+           "tv_attend_prompt")
 PROFILE_STAGES = ("prologue+embed", "qkv_gemm", "qkv_finalize", "attention", "o_gemm", "o_finalize", "lm_head")
 
 
@@ -158,6 +159,7 @@ def load():
         lib.tv_pages_compact.argtypes = [PO, SQ, P, P, P, Z, P, P]
         lib.tv_pages_write.argtypes = [PO, I, SQ, P, P, P, I, I, P, P, Z, Z, P, P]
         lib.tv_pages_read.argtypes = [PO, I, SQ, P, P, P, I, I, P, P, Z, Z, P, P]
+        lib.tv_attend_prompt.argtypes = [I, I, I, P, P, P, Z, Z, P, I, I, P, P, P]
         lib.tv_attend_paged_workspace_size.argtypes = [PO, I, I, ctypes.POINTER(Z)]
         lib.tv_attend_paged.argtypes = [PO, I, SQ, P, I, I, P, Z, P, P, Z, P, P, Z, P, P]
         D = ctypes.c_double
@@ -382,6 +384,14 @@ def tv_pages_read(pool: TvPool, layer: int, seqs: TvSeqs, ids, pos, starts, n: i
     return load().tv_pages_read(ctypes.byref(pool), int(layer), ctypes.byref(seqs), _p(ids), _p(pos), _p(starts),
                                 int(n), int(rows), _p(k), _p(v), int(row_stride), int(head_stride), _p(dev_status),
                                 _stream(stream))
+
+
+def tv_attend_prompt(n_q_heads: int, n_kv_heads: int, head_dim: int, q, k, v, q_stride: int, kv_stride: int, starts,
+                     n_seqs: int, rows: int, out, dev_status, stream=None) -> int:
+    """Strides in elements."""
+    return load().tv_attend_prompt(int(n_q_heads), int(n_kv_heads), int(head_dim), _p(q), _p(k), _p(v), int(q_stride),
+                                   int(kv_stride), _p(starts), int(n_seqs), int(rows), _p(out), _p(dev_status),
+                                   _stream(stream))
 
 
 def tv_attend_paged_workspace_size(pool: TvPool, n_q_heads: int, n: int) -> int:

@@ -40,6 +40,9 @@ int make_tmap_bf16(CUtensorMap* map, const void* base, int inner, int rows, int 
 // b2 x b1 x b0 and the 128-byte swizzle: a box lands as b2 * b1 rows of b0
 // elements, row (z, y) at row index z * b1 + y.
 int make_tmap_bf16_3d(CUtensorMap* map, const void* base, int d0, int d1, int d2, int b0, int b1, int b2);
+// The same over rows of d1 * d0 values that lie row_stride values apart.
+int make_tmap_bf16_rows(CUtensorMap* map, const void* base, int d0, int d1, int d2, size_t row_stride, int b0, int b1,
+                        int b2);
 int launch_gemm(int mode, const void* W, int M, int K, const void* X, int n_rows, const GemmPlan& pl,
                 const GemmParams& base, int num_sms, cudaStream_t stream);
 // W [rows][cols] row-major -> the tile-packed layout (128 x 64 tiles, rows

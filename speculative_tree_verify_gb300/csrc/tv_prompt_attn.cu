@@ -1,0 +1,524 @@
+// Causal attention of packed prompts, grouped heads:
+//   o[t, h] = sum_{j <= t} softmax_j(q[t, h] . k[j, g] / sqrt(D)) v[j, g],  g = h / G,
+// t and j rows of the same sequence.
+//
+// What bounds it: 4 D flops a (row, key) pair on the tensor cores, with one
+// exponential a pair on the SFU beside them.  So both products run on tcgen05
+// and the exponentials of one tile hide behind the products of another.
+//
+// A CTA takes two tiles of 128 query vectors of one KV head.  The vectors are
+// (token, head of the group) pairs, T = 128 / G tokens a tile, so that K and V
+// are read once for the whole group and a short prompt fills a tile with its
+// heads.  Its keys come in windows of 128, the last first, so that what is
+// masked (the corner of the CTA's own tokens, and what lies behind them) is in
+// the first windows alone:
+//   S_s  = Q_s K_w^T       tcgen05.mma 128 x 128 x D, operands in shared memory
+//   P_s  = 2^(S_s c - m)   one thread a row: 128 scores from TMEM to registers,
+//                          their maximum, exponentials, bf16 back into the
+//                          first half of the scores' columns
+//   O_s += P_s V_w         tcgen05.mma 128 x D x 128, P from TMEM, V from its
+//                          TMA layout (MN-major)
+// The issue order PV_0(w) S_0(w + 1) PV_1(w) S_1(w + 1) keeps the tensor pipe
+// on one tile while the other's softmax runs.  A row's offset m moves only when a score
+// passes it by 2^8; then O_s is rescaled in TMEM by the row's own thread (S_s(w) is committed
+// after PV_s(w - 1), so O_s is at rest).  Sums add the rounded P, fp32 throughout.
+//
+// Masked places: a key that a row may not see has weight zero, and its V may
+// be anything.  0 * NaN would reach the row through the product, so the V rows
+// past the CTA's first token are looked over in shared memory before they are
+// used; what is not finite is taken out and noted (per dimension, the first
+// such key), and put into the rows that do see it at the end.
+#include <cmath>
+#include <type_traits>
+
+#include "tv_gemm.cuh"
+#include "tv_kernels.cuh"
+#include "tv_pages.cuh"
+
+namespace tv {
+namespace {
+
+constexpr int kPrSoftWarps = 8;
+constexpr int kPrSoftThreads = kPrSoftWarps * 32;
+constexpr int kWarpMma = 8, kWarpTma = 9;
+constexpr int kPrThreads = 320;
+constexpr int kAtomP = 128 * 128;                // bytes of a 128-row x 128-byte swizzled slab
+constexpr float kMove = 8.f;                     // log2: an offset moves when a score passes it by more
+
+template <int D>
+struct PrSmem {
+  static constexpr int TILE = (D / 64) * kAtomP;   // 128 rows
+  static constexpr int OFF_Q = 0;                  // two tiles; the listed sequences' CTA counts first
+  static constexpr int OFF_K = 2 * TILE;           // two stages
+  static constexpr int OFF_V = OFF_K + 2 * TILE;   // two stages
+  static constexpr int OFF_BAD = OFF_V + 2 * TILE; // [3][D] first key whose V is NaN, +inf, -inf
+  static constexpr int OFF_BAR = OFF_BAD + 3 * D * 4;
+  static constexpr size_t BYTES = 1024 + OFF_BAR + 256;
+  static_assert(2 * TILE >= kMaxListed * 4, "a count for every listed sequence");
+};
+
+struct PrParams {
+  const int32_t* starts;
+  __nv_bfloat16* out;
+  int32_t* status;
+  int n, rows, Hq, Hkv, G, T;
+  float scale_log2;
+};
+
+__device__ __forceinline__ float ex2p(float x) {   // 2^x by the SFU, about 2^-22 relative, 2^-inf = 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// n consecutive 32-bit TMEM columns of this thread's lane
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem desc]: A holds two bf16 of a row per 32-bit column
+__device__ __forceinline__ void umma_ts_bf16(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 1-D grid: KV heads fastest, then the CTAs' places ordered by the tile index
+// inside their sequence, highest first (the longest rows start first, so that
+// what is left at the end is short).
+template <int D>
+__global__ void __launch_bounds__(kPrThreads, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const PrParams p) {
+  using L = PrSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  int* s_bad = reinterpret_cast<int*>(smem + L::OFF_BAD);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);   // [2] a query tile landed
+  uint64_t* k_full = q_full + 2;                                         // [2]
+  uint64_t* k_free = k_full + 2;                                         // [2] the products with it are done
+  uint64_t* v_full = k_free + 2;                                         // [2]
+  uint64_t* v_free = v_full + 2;                                         // [2]
+  uint64_t* s_full = v_free + 2;                                         // [2] S_s done (and every product before it)
+  uint64_t* p_full = s_full + 2;                                         // [2] P_s stored, O_s rescaled (4 warps)
+  uint64_t* o_fin = p_full + 2;                                          // [2] the last product into O_s done
+  // a window's V looked over (8 warps): one barrier for even windows and one
+  // for odd, since the warps may be a window ahead of the products
+  uint64_t* v_ok = o_fin + 2;
+  uint64_t* drain = v_ok + 2;                                            // after a timeout: every product issued is done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  __shared__ int s_place[4];                                             // sequence, tile pair; -1: nothing to do
+  __shared__ int s_anybad;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_free[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_free[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&o_fin[s], 1);
+      mbar_init(&v_ok[s], kPrSoftWarps);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    prefetch_tmap(&map_q);
+    prefetch_tmap(&map_k);
+    prefetch_tmap(&map_v);
+    s_anybad = 0;
+  }
+  for (int e = tid; e < 3 * D; e += kPrThreads) s_bad[e] = 0x7fffffff;
+  if (warp == kWarpMma) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this CTA's place ------------------------------------------------------------
+  // c_i = ceil(len_i / 2T) tile pairs of sequence i; N(l) = sum_i max(0, c_i - l) of them have an index >= l
+  int* s_cnt = reinterpret_cast<int*>(smem + L::OFF_Q);
+  int bad = status_get(p.status) != 0, most = 0;
+  for (int i = tid; i < p.n; i += kPrThreads) {
+    const int a = __ldg(p.starts + i), b = __ldg(p.starts + i + 1);
+    if (a < 0 || b < a || b > p.rows) bad = TV_E_SEQ;
+    const int c = (b - a + 2 * p.T - 1) / (2 * p.T);
+    s_cnt[i] = c;
+    most = max(most, c);
+  }
+  if (bad < 0) status_set(p.status, bad);
+  fence_async_smem();   // the counts' shared memory is the query tiles'
+  const bool stop = __syncthreads_or(bad);
+  if (warp == 0) {
+    int top = 0;
+    if (!stop) {
+      for (int i = lane; i < p.n; i += 32) top = max(top, s_cnt[i]);
+      top = __reduce_max_sync(0xffffffffu, top);
+      auto at_least = [&](int l) {   // N(l)
+        int x = 0;
+        for (int i = lane; i < p.n; i += 32) x += max(0, s_cnt[i] - l);
+        return __reduce_add_sync(0xffffffffu, x);
+      };
+      const int place = blockIdx.x / p.Hkv;
+      int lo = 0, hi = top;   // the largest l with N(l) > place; N(top) = 0
+      if (at_least(0) > place) {
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (at_least(mid) > place) lo = mid;
+          else hi = mid;
+        }
+        int k = place - at_least(lo + 1);   // the k-th sequence with more than lo pairs
+        for (int i0 = 0; i0 < p.n; i0 += 32) {
+          const int i = i0 + lane;
+          const unsigned m = __ballot_sync(0xffffffffu, i < p.n && s_cnt[i] > lo);
+          const int c = __popc(m);
+          if (k < c) {
+            if ((m >> lane & 1u) && __popc(m & ((1u << lane) - 1u)) == k) {
+              s_place[0] = i;
+              s_place[1] = lo;
+            }
+            break;
+          }
+          k -= c;
+        }
+      } else {
+        top = 0;
+      }
+    }
+    if (top == 0 && lane == 0) s_place[0] = -1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int seq = s_place[0];
+  if (seq >= 0) {
+    const int row0 = __ldg(p.starts + seq), len = __ldg(p.starts + seq + 1) - row0;
+    const int h = blockIdx.x % p.Hkv;
+    const int t0 = s_place[1] * 2 * p.T;
+    const int hi = min(len, t0 + 2 * p.T);            // one past the last key
+    const int nst = t0 + p.T < len ? 2 : 1;            // query tiles
+    const int nwin = (hi + 127) / 128;
+    const int skip0 = nst == 2 ? nwin - (t0 + p.T + 127) / 128 : 0;   // tile 0 sees nothing of the first window (0 or 1)
+    auto w_start = [&](int w) { return 128 * (nwin - 1 - w); };   // first key of window w
+    auto scrub = [&](int w) { return w_start(w) + 127 > t0; };   // holds keys that a row may not see
+    const uint32_t tS = tmem, tO = tmem + 256;
+
+    if (warp == kWarpTma) {
+      if (lane == 0) {
+        const uint32_t qbytes = (uint32_t)((D / 64) * p.T * p.G * 128);
+        bool ok = true;
+        auto load_kv = [&](const CUtensorMap* map, uint64_t* full, int off, int w) {
+          mbar_arrive_expect_tx(&full[w & 1], L::TILE);
+#pragma unroll
+          for (int a = 0; a < D / 64; ++a)
+            tma_load_3d(smem + off + (w & 1) * L::TILE + a * kAtomP, map, &full[w & 1], h * D + a * 64, 0, row0 + w_start(w));
+        };
+        auto load_q = [&](int s) {
+          mbar_arrive_expect_tx(&q_full[s], qbytes);
+#pragma unroll
+          for (int a = 0; a < D / 64; ++a)
+            tma_load_3d(smem + L::OFF_Q + s * L::TILE + a * kAtomP, &map_q, &q_full[s], a * 64, h * p.G, row0 + t0 + s * p.T);
+        };
+        load_q(0);
+        load_kv(&map_k, k_full, L::OFF_K, 0);
+        if (nst == 2) load_q(1);
+        load_kv(&map_v, v_full, L::OFF_V, 0);
+        int nk = 1, nv = 1;
+        for (int w = 1; w < nwin && ok; ++w) {
+          if (w >= 2) ok = mbar_wait(&k_free[w & 1], (uint32_t)((w - 2) >> 1) & 1u);
+          if (!ok) break;
+          load_kv(&map_k, k_full, L::OFF_K, w);
+          ++nk;
+          if (w >= 2) ok = mbar_wait(&v_free[w & 1], (uint32_t)((w - 2) >> 1) & 1u);
+          if (!ok) break;
+          load_kv(&map_v, v_full, L::OFF_V, w);
+          ++nv;
+        }
+        if (!ok) status_set(p.status, TV_E_TIMEOUT);
+        // loads in flight land before the CTA leaves
+        for (int s = 0; s < nst; ++s) mbar_wait(&q_full[s], 0);
+        for (int w = nk > 2 ? nk - 2 : 0; w < nk; ++w) mbar_wait(&k_full[w & 1], (uint32_t)(w >> 1) & 1u);
+        for (int w = nv > 2 ? nv - 2 : 0; w < nv; ++w) mbar_wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u);
+      }
+    } else if (warp == kWarpMma) {
+      if (lane == 0) {
+        const uint32_t idesc_s = idesc_bf16_f32(128, 128);
+        const uint32_t idesc_o = idesc_bf16_f32(128, D) | (1u << 16);   // B = V: MN-major
+        const uint32_t qa = smem_u32(smem + L::OFF_Q), ka = smem_u32(smem + L::OFF_K), va = smem_u32(smem + L::OFF_V);
+        bool ok = true;
+        int n_s[2] = {0, 0};
+        auto product_s = [&](int s, int w) {   // S_s = Q_s K_w^T
+          if (n_s[s] == 0) ok = ok && mbar_wait(&q_full[s], 0);
+          ok = ok && mbar_wait(&k_full[w & 1], (uint32_t)(w >> 1) & 1u);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (uint32_t)((k >> 2) * kAtomP + (k & 3) * 32);
+            umma_bf16(tS + s * 128, sdesc_sw128(qa + s * L::TILE + off, 16, 1024), sdesc_sw128(ka + (w & 1) * L::TILE + off, 16, 1024),
+                      idesc_s, k > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[s]);
+          if (s == nst - 1) umma_commit(&k_free[w & 1]);
+          ++n_s[s];
+        };
+        for (int s = 0; s < nst; ++s)
+          if (s > 0 || !skip0) product_s(s, 0);
+        for (int w = 0; w < nwin && ok; ++w) {
+          for (int s = 0; s < nst && ok; ++s) {
+            const int f = s == 0 ? skip0 : 0;
+            if (w >= f) {   // O_s += P_s V_w
+              ok = ok && mbar_wait(&p_full[s], (uint32_t)(w - f) & 1u);
+              ok = ok && mbar_wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u);
+              if (scrub(w)) ok = ok && mbar_wait(&v_ok[w & 1], (uint32_t)(w >> 1) & 1u);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 8; ++k)   // 16 keys a step
+                umma_ts_bf16(tO + s * D, tS + s * 128 + k * 8, sdesc_sw128(va + (w & 1) * L::TILE + k * 2048, kAtomP, 1024), idesc_o,
+                             (w > f || k > 0) ? 1u : 0u);
+              if (w == nwin - 1) umma_commit(&o_fin[s]);
+              if (s == nst - 1) umma_commit(&v_free[w & 1]);
+            }
+            if (w + 1 < nwin && w + 1 >= f) product_s(s, w + 1);
+          }
+        }
+        if (!ok) {   // what was issued is done before TMEM is given back: a commit covers every product before it
+          status_set(p.status, TV_E_TIMEOUT);
+          umma_commit(drain);
+          mbar_wait(drain, 0);
+        }
+      }
+    } else {
+      // ---------------- softmax: warps 4 s .. 4 s + 3, one thread a row of tile s ----------------
+      const int s = warp >> 2, r = tid & 127;
+      const bool active = s < nst;
+      const int f = s == 0 ? skip0 : 0;
+      const int tmin = t0 + s * p.T;
+      const int t = tmin + r / p.G;
+      const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t sS = tS + s * 128 + lb, sO = tO + s * D + lb;
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+
+      auto look_over = [&](int w) {   // V rows of keys past t0
+        if (ok && !mbar_wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u)) ok = false;
+        uint8_t* sv = smem + L::OFF_V + (w & 1) * L::TILE;
+        const int key0 = w_start(w), first = max(0, t0 + 1 - key0);
+        bool wrote = false;
+        for (int e = tid; e < (128 - first) * (D / 8); e += kPrSoftThreads) {
+          const int row = first + e / (D / 8), c = e % (D / 8);
+          uint32_t* x = reinterpret_cast<uint32_t*>(sv + (c >> 3) * kAtomP + swz(row, c & 7));
+          const uint4 y = *reinterpret_cast<const uint4*>(x);
+          // an exponent of all ones carries into the sign's place
+          const uint32_t any = ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
+                               ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
+          if (any & 0x80008000u) {
+            for (int u = 0; u < 8; ++u) {
+              const uint32_t b = (x[u >> 1] >> (16 * (u & 1))) & 0xffffu;
+              if ((b & 0x7f80u) == 0x7f80u) {
+                const int kind = (b & 0x7fu) ? 0 : (b & 0x8000u ? 2 : 1);
+                atomicMin(&s_bad[kind * D + c * 8 + u], key0 + row);
+                x[u >> 1] &= u & 1 ? 0x0000ffffu : 0xffff0000u;
+              }
+            }
+            s_anybad = 1;
+            wrote = true;
+          }
+        }
+        if (wrote) fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_ok[w & 1]);
+      };
+
+      auto window = [&](auto masked_c, int w) {
+        constexpr bool MASKED = decltype(masked_c)::value;
+        if (ok && !mbar_wait(&s_full[s], (uint32_t)(w - f) & 1u)) ok = false;
+        tc_fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ld32(sS + 32 * c, x + 32 * c);
+        tmem_ld_wait();
+        if constexpr (MASKED) {
+          const int lim = t - w_start(w);   // the last visible key of the window
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > lim) x[c] = 0xff800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 128; c += 4)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(x[c + u]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        const bool move = top > m + kMove;
+        if (__any_sync(0xffffffffu, move)) {
+          const float a = move ? ex2p(m - top) : 1.f;
+          if (move) m = top;
+          l *= a;
+          if (w > f) {
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              ld16(sO + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * a);
+              st16(sO + c, o);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const float a = ex2p(fmaf(__uint_as_float(x[32 * c + 2 * u]), p.scale_log2, neg));
+            const float b = ex2p(fmaf(__uint_as_float(x[32 * c + 2 * u + 1]), p.scale_log2, neg));
+            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+            pk[u] = *reinterpret_cast<const uint32_t*>(&v);
+            l0 += __uint_as_float(pk[u] << 16);
+            l1 += __uint_as_float(pk[u] & 0xffff0000u);
+          }
+          st16(sS + 16 * c, pk);   // columns whose scores are in registers already
+        }
+        l += l0 + l1;
+        st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[s]);
+      };
+
+      for (int w = 0; w < nwin; ++w) {
+        if (scrub(w)) look_over(w);
+        if (!active || w < f) continue;
+        if (w_start(w) + 127 > tmin) window(std::integral_constant<bool, true>{}, w);
+        else window(std::integral_constant<bool, false>{}, w);
+      }
+      if (active) {
+        if (ok && !mbar_wait(&o_fin[s], 0)) ok = false;
+        tc_fence_after();
+        const bool mine = ok && r < p.T * p.G && t < len;
+        const float inv = 1.f / l;
+        __nv_bfloat16* dst = p.out + ((size_t)(row0 + t) * p.Hq + h * p.G + r % p.G) * D;
+        const bool anybad = *reinterpret_cast<volatile int*>(&s_anybad) != 0;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          ld32(sO + c, o);
+          tmem_ld_wait();
+          if (anybad) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              const bool n = s_bad[c + u] <= t, pi = s_bad[D + c + u] <= t, ni = s_bad[2 * D + c + u] <= t;
+              if (n || (pi && ni)) o[u] = 0x7fc00000u;
+              else if (pi) o[u] = 0x7f800000u;
+              else if (ni) o[u] = 0xff800000u;
+            }
+          }
+          if (mine) {
+#pragma unroll
+            for (int u = 0; u < 32; u += 8) {
+              uint32_t b[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 v =
+                    __floats2bfloat162_rn(__uint_as_float(o[u + 2 * e]) * inv, __uint_as_float(o[u + 2 * e + 1]) * inv);
+                b[e] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              *reinterpret_cast<uint4*>(dst + c + u) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+          }
+        }
+      }
+      if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+int launch_prompt(const PrParams& p, const void* q, const void* k, const void* v, size_t q_stride, size_t kv_stride, cudaStream_t st) {
+  CUtensorMap mq, mk, mv;
+  int rc = make_tmap_bf16_rows(&mq, q, D, p.Hq, p.rows, q_stride, 64, p.G, p.T);
+  if (rc || (rc = make_tmap_bf16_rows(&mk, k, p.Hkv * D, 1, p.rows, kv_stride, 64, 1, 128)) ||
+      (rc = make_tmap_bf16_rows(&mv, v, p.Hkv * D, 1, p.rows, kv_stride, 64, 1, 128)))
+    return rc;
+  static std::atomic<bool> attr[64];
+  if (ensure_smem_limit(prompt_attn_kernel<D>, PrSmem<D>::BYTES, attr)) return TV_E_CUDA;
+  // at most rows / 2T whole pairs and one ragged pair a sequence
+  const long long pairs = (long long)p.rows / (2 * p.T) + (p.n < p.rows ? p.n : p.rows);
+  return launch_pdl(prompt_attn_kernel<D>, dim3((unsigned)(pairs * p.Hkv)), dim3(kPrThreads), PrSmem<D>::BYTES, st, mq, mk, mv, p);
+}
+
+}  // namespace
+}  // namespace tv
+
+using namespace tv;
+
+extern "C" int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const tv_bf16* q, const tv_bf16* k, const tv_bf16* v,
+                                size_t q_stride, size_t kv_stride, const int32_t* starts, int n_seqs, int rows, tv_bf16* out,
+                                int32_t* dev_status, void* stream) {
+  if (n_q_heads < 1 || n_kv_heads < 1 || !q || !k || !v || !starts || !out || !dev_status || rows < 1) return TV_E_ARG;
+  int rc = check_listed(n_seqs);
+  if (rc) return rc;
+  if (head_dim != 64 && head_dim != 128) return TV_E_UNSUPPORTED;
+  if (n_q_heads % n_kv_heads != 0 || n_q_heads / n_kv_heads > 128 || n_q_heads > 65536) return TV_E_UNSUPPORTED;
+  const size_t D = head_dim;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || q_stride % 8 != 0 || kv_stride % 8 != 0) return TV_E_ARG;
+  if (q_stride < n_q_heads * D || kv_stride < n_kv_heads * D) return TV_E_ARG;
+  PrParams p;
+  p.starts = starts;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.status = dev_status;
+  p.n = n_seqs;
+  p.rows = rows;
+  p.Hq = n_q_heads;
+  p.Hkv = n_kv_heads;
+  p.G = n_q_heads / n_kv_heads;
+  p.T = 128 / p.G;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
+  if (((long long)rows / (2 * p.T) + n_seqs) * n_kv_heads > 0x7fffffffll) return TV_E_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return head_dim == 128 ? launch_prompt<128>(p, q, k, v, q_stride, kv_stride, st)
+                         : launch_prompt<64>(p, q, k, v, q_stride, kv_stride, st);
+}

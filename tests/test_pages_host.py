@@ -97,6 +97,20 @@ def test_attend_paged_host_checks():
         assert call(**over) == E["TV_E_WORKSPACE"], over
 
 
+def test_attend_prompt_host_checks():
+    E = abi.CODES
+
+    def call(hq=8, hkv=2, d=64, q=FAKE, k=FAKE, v=FAKE, qs=512, kvs=128, starts=FAKE, n=3, rows=9, out=FAKE, st=FAKE):
+        return abi.tv_attend_prompt(hq, hkv, d, q, k, v, qs, kvs, starts, n, rows, out, st)
+
+    for over in (dict(hq=0), dict(hkv=0), dict(q=None), dict(k=None), dict(v=None), dict(starts=None), dict(out=None), dict(st=None),
+                 dict(n=0), dict(rows=0), dict(q=FAKE + 2), dict(k=FAKE + 8), dict(v=FAKE + 2), dict(out=FAKE + 4), dict(qs=516), dict(qs=504),
+                 dict(kvs=132), dict(kvs=120)):
+        assert call(**over) == E["TV_E_ARG"], over
+    for over in (dict(n=4097), dict(d=96), dict(hq=9), dict(hq=258, hkv=2, qs=258 * 64), dict(rows=2 ** 31 - 1, hq=256, hkv=8, kvs=512, qs=256 * 64)):
+        assert call(**over) == E["TV_E_UNSUPPORTED"], over
+
+
 def test_workspace_refuses_bad_shapes():
     with pytest.raises(ValueError, match="UNSUPPORTED"):
         abi.tv_pages_workspace_size(_pool(page_size=17), _seqs())
