@@ -99,15 +99,82 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// two fp32 values in a 64-bit register: one instruction for both
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {   // NaN inputs are ignored
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem desc]: A holds two bf16 of a row per 32-bit column
-__device__ __forceinline__ void umma_ts_bf16(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// The issuing warp runs as one (no branch on the lane), so that descriptors and
+// loop counters stay in its uniform registers, where the MMA takes them from;
+// the instructions themselves carry the elected lane's predicate.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                                        uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem desc]: A holds two bf16 of a row per 32-bit column
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                                        uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit_by(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
       : "memory");
 }
 
@@ -137,7 +204,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ int s_place[4];                                             // sequence, tile pair; -1: nothing to do
   __shared__ int s_anybad;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -222,11 +290,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int seq = s_place[0];
+  const int seq = __shfl_sync(0xffffffffu, s_place[0], 0);   // uniform values, and known to be
   if (seq >= 0) {
-    const int row0 = __ldg(p.starts + seq), len = __ldg(p.starts + seq + 1) - row0;
+    const int row0 = __shfl_sync(0xffffffffu, __ldg(p.starts + seq), 0);
+    const int len = __shfl_sync(0xffffffffu, __ldg(p.starts + seq + 1), 0) - row0;
     const int h = blockIdx.x % p.Hkv;
-    const int t0 = s_place[1] * 2 * p.T;
+    const int t0 = __shfl_sync(0xffffffffu, s_place[1], 0) * 2 * p.T;
     const int hi = min(len, t0 + 2 * p.T);            // one past the last key
     const int nst = t0 + p.T < len ? 2 : 1;            // query tiles
     const int nwin = (hi + 127) / 128;
@@ -273,53 +342,55 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         for (int w = nv > 2 ? nv - 2 : 0; w < nv; ++w) mbar_wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u);
       }
     } else if (warp == kWarpMma) {
-      if (lane == 0) {
-        const uint32_t idesc_s = idesc_bf16_f32(128, 128);
-        const uint32_t idesc_o = idesc_bf16_f32(128, D) | (1u << 16);   // B = V: MN-major
-        const uint32_t qa = smem_u32(smem + L::OFF_Q), ka = smem_u32(smem + L::OFF_K), va = smem_u32(smem + L::OFF_V);
-        bool ok = true;
-        int n_s[2] = {0, 0};
-        auto product_s = [&](int s, int w) {   // S_s = Q_s K_w^T
-          if (n_s[s] == 0) ok = ok && mbar_wait(&q_full[s], 0);
-          ok = ok && mbar_wait(&k_full[w & 1], (uint32_t)(w >> 1) & 1u);
-          if (!ok) return;
-          tc_fence_after();
+      const uint32_t leader = elect_one();
+      const uint32_t idesc_s = idesc_bf16_f32(128, 128);
+      const uint32_t idesc_o = idesc_bf16_f32(128, D) | (1u << 16);   // B = V: MN-major
+      const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t dq = sdesc_sw128(base + L::OFF_Q, 16, 1024), dk = sdesc_sw128(base + L::OFF_K, 16, 1024);
+      const uint64_t dv = sdesc_sw128(base + L::OFF_V, kAtomP, 1024);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
+      auto product_s = [&](int s, int w, bool first) {   // S_s = Q_s K_w^T
+        if (first) wait(&q_full[s], 0);
+        wait(&k_full[w & 1], (uint32_t)(w >> 1) & 1u);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t a = dq + (uint64_t)(s * (L::TILE >> 4)), b = dk + (uint64_t)((w & 1) * (L::TILE >> 4));
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (uint32_t)((k >> 2) * kAtomP + (k & 3) * 32);
-            umma_bf16(tS + s * 128, sdesc_sw128(qa + s * L::TILE + off, 16, 1024), sdesc_sw128(ka + (w & 1) * L::TILE + off, 16, 1024),
-                      idesc_s, k > 0 ? 1u : 0u);
-          }
-          umma_commit(&s_full[s]);
-          if (s == nst - 1) umma_commit(&k_free[w & 1]);
-          ++n_s[s];
-        };
-        for (int s = 0; s < nst; ++s)
-          if (s > 0 || !skip0) product_s(s, 0);
-        for (int w = 0; w < nwin && ok; ++w) {
-          for (int s = 0; s < nst && ok; ++s) {
-            const int f = s == 0 ? skip0 : 0;
-            if (w >= f) {   // O_s += P_s V_w
-              ok = ok && mbar_wait(&p_full[s], (uint32_t)(w - f) & 1u);
-              ok = ok && mbar_wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u);
-              if (scrub(w)) ok = ok && mbar_wait(&v_ok[w & 1], (uint32_t)(w >> 1) & 1u);
-              if (!ok) break;
-              tc_fence_after();
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = (uint64_t)(((k >> 2) * kAtomP + (k & 3) * 32) >> 4);
+          umma_ss(tm + s * 128, a + off, b + off, idesc_s, k > 0 ? 1u : 0u, leader);
+        }
+        commit_by(&s_full[s], leader);
+        if (s == nst - 1) commit_by(&k_free[w & 1], leader);
+      };
+      if (!skip0) product_s(0, 0, true);
+      if (nst == 2) product_s(1, 0, true);
+      for (int w = 0; w < nwin && ok; ++w) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)   // 16 keys a step
-                umma_ts_bf16(tO + s * D, tS + s * 128 + k * 8, sdesc_sw128(va + (w & 1) * L::TILE + k * 2048, kAtomP, 1024), idesc_o,
-                             (w > f || k > 0) ? 1u : 0u);
-              if (w == nwin - 1) umma_commit(&o_fin[s]);
-              if (s == nst - 1) umma_commit(&v_free[w & 1]);
-            }
-            if (w + 1 < nwin && w + 1 >= f) product_s(s, w + 1);
+        for (int s = 0; s < 2; ++s) {
+          if (s >= nst || !ok) break;
+          const int f = s == 0 ? skip0 : 0;
+          if (w >= f) {   // O_s += P_s V_w
+            wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u);
+            if (scrub(w)) wait(&v_ok[w & 1], (uint32_t)(w >> 1) & 1u);
+            wait(&p_full[s], (uint32_t)(w - f) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b = dv + (uint64_t)((w & 1) * (L::TILE >> 4));
+#pragma unroll
+            for (int k = 0; k < 8; ++k)   // 16 keys a step
+              umma_ts(tm + 256 + s * D, tm + s * 128 + k * 8, b + (uint64_t)(k * (2048 >> 4)), idesc_o, (w > f || k > 0) ? 1u : 0u, leader);
+            if (w == nwin - 1) commit_by(&o_fin[s], leader);
+            if (s == nst - 1) commit_by(&v_free[w & 1], leader);
           }
+          if (w + 1 < nwin && w + 1 >= f) product_s(s, w + 1, w + 1 == f && f > 0);
         }
-        if (!ok) {   // what was issued is done before TMEM is given back: a commit covers every product before it
-          status_set(p.status, TV_E_TIMEOUT);
-          umma_commit(drain);
-          mbar_wait(drain, 0);
-        }
+      }
+      if (!ok) {   // what was issued is done before TMEM is given back: a commit covers every product before it
+        if (leader) status_set(p.status, TV_E_TIMEOUT);
+        commit_by(drain, leader);
+        mbar_wait(drain, 0);
       }
     } else {
       // ---------------- softmax: warps 4 s .. 4 s + 3, one thread a row of tile s ----------------
@@ -363,31 +434,77 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (lane == 0) mbar_arrive(&v_ok[w & 1]);
       };
 
+      // One window.  The exponentials are taken at the offset the row has, while
+      // its maximum is found beside them; only if that says that an offset must
+      // move (rare after the first windows) are they taken again.  P stays in
+      // registers until then, because it goes where the scores are.
       auto window = [&](auto masked_c, int w) {
         constexpr bool MASKED = decltype(masked_c)::value;
         if (ok && !mbar_wait(&s_full[s], (uint32_t)(w - f) & 1u)) ok = false;
         tc_fence_after();
-        uint32_t x[128];
+        const int lim = t - w_start(w);   // the last visible key of the window
+        // 32 scores, the next 32 on their way
+        auto chunks = [&](auto&& use) {
+          uint32_t x[2][32];
+          ld32(sS, x[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ld32(sS + 32 * c, x + 32 * c);
-        tmem_ld_wait();
-        if constexpr (MASKED) {
-          const int lim = t - w_start(w);   // the last visible key of the window
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait();
+            if (c < 3) ld32(sS + 32 * (c + 1), x[(c + 1) & 1]);
+            if constexpr (MASKED) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > lim) x[c] = 0xff800000u;
+              for (int u = 0; u < 32; ++u)
+                if (32 * c + u > lim) x[c & 1][u] = 0xff800000u;
+            }
+            use(c, x[c & 1]);
+          }
+        };
+        auto max32 = [](const uint32_t (&x)[32], float top) {
+          float a = top, b = __uint_as_float(x[31]);
+#pragma unroll
+          for (int u = 0; u < 28; u += 4) {
+            a = max3(a, __uint_as_float(x[u]), __uint_as_float(x[u + 1]));
+            b = max3(b, __uint_as_float(x[u + 2]), __uint_as_float(x[u + 3]));
+          }
+          a = max3(a, __uint_as_float(x[28]), __uint_as_float(x[29]));
+          return max3(a, b, __uint_as_float(x[30]));
+        };
+        if (w == f) {
+          float top = -INFINITY;
+          chunks([&](int, const uint32_t (&x)[32]) { top = max32(x, top); });
+          m = top * p.scale_log2;
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint32_t pk[64];
+        float sum;
+        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+        for (;;) {
+          const float neg = m == -INFINITY ? 0.f : -m;
+          const uint64_t neg2 = pack2(neg, neg);
+          uint64_t l2 = 0, l3 = 0;
+          float top = -INFINITY;
+          chunks([&](int c, const uint32_t (&x)[32]) {
+            top = max32(x, top);
 #pragma unroll
-        for (int c = 0; c < 128; c += 4)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(x[c + u]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-        const bool move = top > m + kMove;
-        if (__any_sync(0xffffffffu, move)) {
-          const float a = move ? ex2p(m - top) : 1.f;
+            for (int u = 0; u < 16; ++u) {
+              float a, b;
+              unpack2(fma2(pack2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), scale2, neg2), a, b);
+              const __nv_bfloat162 v = __floats2bfloat162_rn(ex2p(a), ex2p(b));
+              const uint32_t q = *reinterpret_cast<const uint32_t*>(&v);
+              pk[16 * c + u] = q;
+              const uint64_t q2 = pack2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
+              if (u & 1) l3 = add2(l3, q2);
+              else l2 = add2(l2, q2);
+            }
+          });
+          float a, b;
+          unpack2(add2(l2, l3), a, b);
+          sum = a + b;
+          top *= p.scale_log2;
+          const bool move = top > m + kMove;
+          if (!__any_sync(0xffffffffu, move)) break;
+          const float scale = move ? ex2p(m - top) : 1.f;
           if (move) m = top;
-          l *= a;
+          l *= scale;
           if (w > f) {
 #pragma unroll
             for (int c = 0; c < D; c += 16) {
@@ -395,28 +512,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               ld16(sO + c, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * a);
+              for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * scale);
               st16(sO + c, o);
             }
           }
         }
-        const float neg = m == -INFINITY ? 0.f : -m;
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            const float a = ex2p(fmaf(__uint_as_float(x[32 * c + 2 * u]), p.scale_log2, neg));
-            const float b = ex2p(fmaf(__uint_as_float(x[32 * c + 2 * u + 1]), p.scale_log2, neg));
-            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-            pk[u] = *reinterpret_cast<const uint32_t*>(&v);
-            l0 += __uint_as_float(pk[u] << 16);
-            l1 += __uint_as_float(pk[u] & 0xffff0000u);
-          }
-          st16(sS + 16 * c, pk);   // columns whose scores are in registers already
-        }
-        l += l0 + l1;
+        l += sum;
+        st32(sS, pk);
+        st32(sS + 32, pk + 32);
         st_wait();
         tc_fence_before();
         __syncwarp();
