@@ -13,15 +13,16 @@
 // masked (the corner of the CTA's own tokens, and what lies behind them) is in
 // the first windows alone:
 //   S_s  = Q_s K_w^T       tcgen05.mma 128 x 128 x D, operands in shared memory
-//   P_s  = 2^(S_s c - m)   one thread a row: 128 scores from TMEM to registers,
-//                          their maximum, exponentials, bf16 back into the
-//                          first half of the scores' columns
+//   P_s  = 2^(S_s c - m)   two threads a row, 64 keys each: scores from TMEM to
+//                          registers, exponentials, bf16 back into the first
+//                          half of the scores' columns
 //   O_s += P_s V_w         tcgen05.mma 128 x D x 128, P from TMEM, V from its
 //                          TMA layout (MN-major)
 // The issue order PV_0(w) S_0(w + 1) PV_1(w) S_1(w + 1) keeps the tensor pipe
 // on one tile while the other's softmax runs.  A row's offset m moves only when a score
-// passes it by 2^8; then O_s is rescaled in TMEM by the row's own thread (S_s(w) is committed
-// after PV_s(w - 1), so O_s is at rest).  Sums add the rounded P, fp32 throughout.
+// passes it by 2^8; then O_s is rescaled in TMEM by the row's own threads
+// (S_s(w) is committed after PV_s(w - 1), so O_s is at rest).  Sums add the
+// rounded P, fp32 throughout.
 //
 // Masked places: a key that a row may not see has weight zero, and its V may
 // be anything.  0 * NaN would reach the row through the product, so the V rows
@@ -38,10 +39,10 @@
 namespace tv {
 namespace {
 
-constexpr int kPrSoftWarps = 8;
+constexpr int kPrSoftWarps = 16;                 // 8 a query tile
 constexpr int kPrSoftThreads = kPrSoftWarps * 32;
-constexpr int kWarpMma = 8, kWarpTma = 9;
-constexpr int kPrThreads = 320;
+constexpr int kWarpMma = kPrSoftWarps, kWarpTma = kPrSoftWarps + 1;
+constexpr int kPrThreads = kPrSoftThreads + 64;
 constexpr int kAtomP = 128 * 128;                // bytes of a 128-row x 128-byte swizzled slab
 constexpr float kMove = 8.f;                     // log2: an offset moves when a score passes it by more
 
@@ -52,7 +53,8 @@ struct PrSmem {
   static constexpr int OFF_K = 2 * TILE;           // two stages
   static constexpr int OFF_V = OFF_K + 2 * TILE;   // two stages
   static constexpr int OFF_BAD = OFF_V + 2 * TILE; // [3][D] first key whose V is NaN, +inf, -inf
-  static constexpr int OFF_BAR = OFF_BAD + 3 * D * 4;
+  static constexpr int OFF_TOP = OFF_BAD + 3 * D * 4;   // [2 tiles][2 halves][128 rows] maxima; sums at the end
+  static constexpr int OFF_BAR = OFF_TOP + 2 * 2 * 128 * 4;
   static constexpr size_t BYTES = 1024 + OFF_BAR + 256;
   static_assert(2 * TILE >= kMaxListed * 4, "a count for every listed sequence");
 };
@@ -133,6 +135,20 @@ __device__ __forceinline__ float max3(float a, float b, float c) {   // NaN inpu
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// the two warps of a pair: all have come; true if v is true on any thread
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_any(bool v, int id) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, %2, 64, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(out)
+      : "r"((uint32_t)v), "r"(id)
+      : "memory");
+  return out != 0;
+}
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // The issuing warp runs as one (no branch on the lane), so that descriptors and
@@ -195,9 +211,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* v_full = k_free + 2;                                         // [2]
   uint64_t* v_free = v_full + 2;                                         // [2]
   uint64_t* s_full = v_free + 2;                                         // [2] S_s done (and every product before it)
-  uint64_t* p_full = s_full + 2;                                         // [2] P_s stored, O_s rescaled (4 warps)
+  uint64_t* p_full = s_full + 2;                                         // [2] P_s stored, O_s rescaled (8 warps)
   uint64_t* o_fin = p_full + 2;                                          // [2] the last product into O_s done
-  // a window's V looked over (8 warps): one barrier for even windows and one
+  // a window's V looked over (16 warps): one barrier for even windows and one
   // for odd, since the warps may be a window ahead of the products
   uint64_t* v_ok = o_fin + 2;
   uint64_t* drain = v_ok + 2;                                            // after a timeout: every product issued is done
@@ -215,7 +231,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       mbar_init(&v_full[s], 1);
       mbar_init(&v_free[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 4);
+      mbar_init(&p_full[s], kPrSoftWarps / 2);
       mbar_init(&o_fin[s], 1);
       mbar_init(&v_ok[s], kPrSoftWarps);
     }
@@ -237,54 +253,67 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   // ---- this CTA's place ------------------------------------------------------------
   // c_i = ceil(len_i / 2T) tile pairs of sequence i; N(l) = sum_i max(0, c_i - l) of them have an index >= l
   int* s_cnt = reinterpret_cast<int*>(smem + L::OFF_Q);
-  int bad = status_get(p.status) != 0, most = 0;
-  for (int i = tid; i < p.n; i += kPrThreads) {
-    const int a = __ldg(p.starts + i), b = __ldg(p.starts + i + 1);
-    if (a < 0 || b < a || b > p.rows) bad = TV_E_SEQ;
-    const int c = (b - a + 2 * p.T - 1) / (2 * p.T);
-    s_cnt[i] = c;
-    most = max(most, c);
+  if (p.n > 32) {   // more than a warp's lanes hold
+    for (int i = tid; i < p.n; i += kPrThreads) {
+      const int a = __ldg(p.starts + i), b = __ldg(p.starts + i + 1);
+      s_cnt[i] = a < 0 || b < a || b > p.rows ? -1 : (b - a + 2 * p.T - 1) / (2 * p.T);
+    }
+    fence_async_smem();   // the counts' shared memory is the query tiles'
+    __syncthreads();
   }
-  if (bad < 0) status_set(p.status, bad);
-  fence_async_smem();   // the counts' shared memory is the query tiles'
-  const bool stop = __syncthreads_or(bad);
   if (warp == 0) {
-    int top = 0;
-    if (!stop) {
-      for (int i = lane; i < p.n; i += 32) top = max(top, s_cnt[i]);
-      top = __reduce_max_sync(0xffffffffu, top);
-      auto at_least = [&](int l) {   // N(l)
-        int x = 0;
-        for (int i = lane; i < p.n; i += 32) x += max(0, s_cnt[i] - l);
-        return __reduce_add_sync(0xffffffffu, x);
-      };
-      const int place = blockIdx.x / p.Hkv;
-      int lo = 0, hi = top;   // the largest l with N(l) > place; N(top) = 0
-      if (at_least(0) > place) {
+    int a = 0, mine = 0;   // n <= 32: the lane's sequence
+    if (p.n <= 32 && lane < p.n) {
+      a = __ldg(p.starts + lane);
+      const int b = __ldg(p.starts + lane + 1);
+      mine = a < 0 || b < a || b > p.rows ? -1 : (b - a + 2 * p.T - 1) / (2 * p.T);
+    }
+    const bool stop = status_get(p.status) != 0;
+    auto each = [&](auto&& use) {   // this lane's counts
+      if (p.n <= 32) use(mine);
+      else
+        for (int i = lane; i < p.n; i += 32) use(s_cnt[i]);
+    };
+    int top = 0, low = 0;
+    each([&](int c) { top = max(top, c), low = min(low, c); });
+    top = __reduce_max_sync(0xffffffffu, top);
+    const bool bad = __any_sync(0xffffffffu, low < 0);
+    if (bad && !stop && lane == 0) status_set(p.status, TV_E_SEQ);
+    auto at_least = [&](int l) {   // N(l)
+      int x = 0;
+      each([&](int c) { x += max(0, c - l); });
+      return __reduce_add_sync(0xffffffffu, x);
+    };
+    const int place = blockIdx.x / p.Hkv;
+    int found = -1, lo = 0;
+    if (!stop && !bad && at_least(0) > place) {
+      int hi = top;   // the largest l with N(l) > place; N(top) = 0
+      if (p.n == 1) lo = top - 1 - place;
+      else
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
           if (at_least(mid) > place) lo = mid;
           else hi = mid;
         }
-        int k = place - at_least(lo + 1);   // the k-th sequence with more than lo pairs
-        for (int i0 = 0; i0 < p.n; i0 += 32) {
-          const int i = i0 + lane;
-          const unsigned m = __ballot_sync(0xffffffffu, i < p.n && s_cnt[i] > lo);
-          const int c = __popc(m);
-          if (k < c) {
-            if ((m >> lane & 1u) && __popc(m & ((1u << lane) - 1u)) == k) {
-              s_place[0] = i;
-              s_place[1] = lo;
-            }
-            break;
-          }
-          k -= c;
+      int k = place - at_least(lo + 1);   // the k-th sequence with more than lo pairs
+      for (int i0 = 0; i0 < p.n; i0 += 32) {
+        const int i = i0 + lane;
+        const unsigned m = __ballot_sync(0xffffffffu, i < p.n && (p.n <= 32 ? mine : s_cnt[i]) > lo);
+        if (k < __popc(m)) {
+          found = i0 + (int)__fns(m, 0, k + 1);
+          break;
         }
-      } else {
-        top = 0;
+        k -= __popc(m);
       }
     }
-    if (top == 0 && lane == 0) s_place[0] = -1;
+    if (lane == 0) {
+      s_place[0] = found;
+      s_place[1] = lo;
+      if (found >= 0) {
+        s_place[2] = __ldg(p.starts + found);
+        s_place[3] = __ldg(p.starts + found + 1);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -292,8 +321,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int seq = __shfl_sync(0xffffffffu, s_place[0], 0);   // uniform values, and known to be
   if (seq >= 0) {
-    const int row0 = __shfl_sync(0xffffffffu, __ldg(p.starts + seq), 0);
-    const int len = __shfl_sync(0xffffffffu, __ldg(p.starts + seq + 1), 0) - row0;
+    const int row0 = __shfl_sync(0xffffffffu, s_place[2], 0);
+    const int len = __shfl_sync(0xffffffffu, s_place[3], 0) - row0;
     const int h = blockIdx.x % p.Hkv;
     const int t0 = __shfl_sync(0xffffffffu, s_place[1], 0) * 2 * p.T;
     const int hi = min(len, t0 + 2 * p.T);            // one past the last key
@@ -352,7 +381,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
       auto product_s = [&](int s, int w, bool first) {   // S_s = Q_s K_w^T
         if (first) wait(&q_full[s], 0);
-        wait(&k_full[w & 1], (uint32_t)(w >> 1) & 1u);
+        if (s == 0 || skip0 > w) wait(&k_full[w & 1], (uint32_t)(w >> 1) & 1u);   // once a window
         if (!ok) return;
         tc_fence_after();
         const uint64_t a = dq + (uint64_t)(s * (L::TILE >> 4)), b = dk + (uint64_t)((w & 1) * (L::TILE >> 4));
@@ -372,8 +401,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           if (s >= nst || !ok) break;
           const int f = s == 0 ? skip0 : 0;
           if (w >= f) {   // O_s += P_s V_w
-            wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u);
-            if (scrub(w)) wait(&v_ok[w & 1], (uint32_t)(w >> 1) & 1u);
+            if (s == 0 || skip0 > w) {   // once a window
+              wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u);
+              if (scrub(w)) wait(&v_ok[w & 1], (uint32_t)(w >> 1) & 1u);
+            }
             wait(&p_full[s], (uint32_t)(w - f) & 1u);
             if (!ok) break;
             tc_fence_after();
@@ -393,15 +424,17 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         mbar_wait(drain, 0);
       }
     } else {
-      // ---------------- softmax: warps 4 s .. 4 s + 3, one thread a row of tile s ----------------
-      const int s = warp >> 2, r = tid & 127;
+      // ---------------- softmax: warps 8 s .. 8 s + 7 hold tile s, thread pairs a row ----------------
+      const int s = warp >> 3, hf = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;   // tile, half of the keys, row
       const bool active = s < nst;
       const int f = s == 0 ? skip0 : 0;
       const int tmin = t0 + s * p.T;
       const int t = tmin + r / p.G;
       const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t sS = tS + s * 128 + lb, sO = tO + s * D + lb;
-      float m = -INFINITY, l = 0.f;
+      const uint32_t sS = tS + s * 128 + lb, sO = tO + s * D + hf * (D / 2) + lb;
+      float* s_top = reinterpret_cast<float*>(smem + L::OFF_TOP) + s * 256;
+      const int pair = 1 + s * 4 + (warp & 3);   // named barrier of the two warps that share rows
+      float m = -INFINITY, l = 0.f;              // offset of the row; sum over this thread's keys
       bool ok = true;
 
       auto look_over = [&](int w) {   // V rows of keys past t0
@@ -434,29 +467,34 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (lane == 0) mbar_arrive(&v_ok[w & 1]);
       };
 
+      // the row's maximum over both halves of the keys
+      auto both = [&](float top) {
+        s_top[hf * 128 + r] = top;
+        pair_sync(pair);
+        return fmaxf(top, s_top[(hf ^ 1) * 128 + r]);
+      };
       // One window.  The exponentials are taken at the offset the row has, while
       // its maximum is found beside them; only if that says that an offset must
       // move (rare after the first windows) are they taken again.  P stays in
-      // registers until then, because it goes where the scores are.
+      // registers until both warps have read their scores, because it goes
+      // where the scores are.
       auto window = [&](auto masked_c, int w) {
         constexpr bool MASKED = decltype(masked_c)::value;
         if (ok && !mbar_wait(&s_full[s], (uint32_t)(w - f) & 1u)) ok = false;
         tc_fence_after();
-        const int lim = t - w_start(w);   // the last visible key of the window
-        // 32 scores, the next 32 on their way
-        auto chunks = [&](auto&& use) {
-          uint32_t x[2][32];
-          ld32(sS, x[0]);
+        const int lim = t - w_start(w) - 64 * hf;   // the last visible one of this thread's keys
+        auto chunks = [&](auto&& use) {             // its scores, 32 at a time
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+            ld32(sS + 64 * hf + 32 * c, x);
             tmem_ld_wait();
-            if (c < 3) ld32(sS + 32 * (c + 1), x[(c + 1) & 1]);
             if constexpr (MASKED) {
 #pragma unroll
               for (int u = 0; u < 32; ++u)
-                if (32 * c + u > lim) x[c & 1][u] = 0xff800000u;
+                if (32 * c + u > lim) x[u] = 0xff800000u;
             }
-            use(c, x[c & 1]);
+            use(c, x);
           }
         };
         auto max32 = [](const uint32_t (&x)[32], float top) {
@@ -472,9 +510,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (w == f) {
           float top = -INFINITY;
           chunks([&](int, const uint32_t (&x)[32]) { top = max32(x, top); });
-          m = top * p.scale_log2;
+          m = both(top) * p.scale_log2;
         }
-        uint32_t pk[64];
+        uint32_t pk[32];
         float sum;
         const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
         for (;;) {
@@ -499,15 +537,18 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           float a, b;
           unpack2(add2(l2, l3), a, b);
           sum = a + b;
-          top *= p.scale_log2;
-          const bool move = top > m + kMove;
-          if (!__any_sync(0xffffffffu, move)) break;
-          const float scale = move ? ex2p(m - top) : 1.f;
-          if (move) m = top;
+          tc_fence_before();
+          const bool any = pair_any(top * p.scale_log2 > m + kMove, pair);
+          tc_fence_after();
+          if (!any) break;
+          const float next = both(top) * p.scale_log2;
+          const bool move = next > m + kMove;
+          const float scale = move ? ex2p(m - next) : 1.f;
+          if (move) m = next;
           l *= scale;
           if (w > f) {
 #pragma unroll
-            for (int c = 0; c < D; c += 16) {
+            for (int c = 0; c < D / 2; c += 16) {
               uint32_t o[16];
               ld16(sO + c, o);
               tmem_ld_wait();
@@ -518,8 +559,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
         }
         l += sum;
-        st32(sS, pk);
-        st32(sS + 32, pk + 32);
+        st32(sS + 32 * hf, pk);
         st_wait();
         tc_fence_before();
         __syncwarp();
@@ -533,21 +573,24 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         else window(std::integral_constant<bool, false>{}, w);
       }
       if (active) {
+        s_top[hf * 128 + r] = l;   // after the last window's pair_any: the maxima were read
+        pair_sync(pair);
+        const float inv = 1.f / (s_top[r] + s_top[128 + r]);
         if (ok && !mbar_wait(&o_fin[s], 0)) ok = false;
         tc_fence_after();
         const bool mine = ok && r < p.T * p.G && t < len;
-        const float inv = 1.f / l;
-        __nv_bfloat16* dst = p.out + ((size_t)(row0 + t) * p.Hq + h * p.G + r % p.G) * D;
+        __nv_bfloat16* dst = p.out + ((size_t)(row0 + t) * p.Hq + h * p.G + r % p.G) * D + hf * (D / 2);
         const bool anybad = *reinterpret_cast<volatile int*>(&s_anybad) != 0;
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D / 2; c += 32) {
           uint32_t o[32];
           ld32(sO + c, o);
           tmem_ld_wait();
           if (anybad) {
+            const int* first = s_bad + hf * (D / 2) + c;
 #pragma unroll
             for (int u = 0; u < 32; ++u) {
-              const bool n = s_bad[c + u] <= t, pi = s_bad[D + c + u] <= t, ni = s_bad[2 * D + c + u] <= t;
+              const bool n = first[u] <= t, pi = first[D + u] <= t, ni = first[2 * D + u] <= t;
               if (n || (pi && ni)) o[u] = 0x7fc00000u;
               else if (pi) o[u] = 0x7f800000u;
               else if (ni) o[u] = 0xff800000u;
