@@ -19,8 +19,8 @@
 //   O_s += P_s V_w         tcgen05.mma 128 x D x 128, P from TMEM, V from its
 //                          TMA layout (MN-major)
 // The issue order PV_0(w) S_0(w + 1) PV_1(w) S_1(w + 1) keeps the tensor pipe
-// on one tile while the other's softmax runs.  A row's offset m moves only when a score
-// passes it by 2^8; then O_s is rescaled in TMEM by the row's own threads
+// on one tile while the other's softmax runs.  A row's offset m moves only when
+// exponentials add up to more than 2^8; then O_s is rescaled in TMEM by the row's own threads
 // (S_s(w) is committed after PV_s(w - 1), so O_s is at rest).  Sums add the
 // rounded P, fp32 throughout.
 //
@@ -44,7 +44,7 @@ constexpr int kPrSoftThreads = kPrSoftWarps * 32;
 constexpr int kWarpMma = kPrSoftWarps, kWarpTma = kPrSoftWarps + 1;
 constexpr int kPrThreads = kPrSoftThreads + 64;
 constexpr int kAtomP = 128 * 128;                // bytes of a 128-row x 128-byte swizzled slab
-constexpr float kMove = 8.f;                     // log2: an offset moves when a score passes it by more
+constexpr float kMoveSum = 256.f;                // an offset moves when 64 keys' exponentials add up to more
 
 template <int D>
 struct PrSmem {
@@ -379,9 +379,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const uint64_t dv = sdesc_sw128(base + L::OFF_V, kAtomP, 1024);
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
-      auto product_s = [&](int s, int w, bool first) {   // S_s = Q_s K_w^T
+      auto wait_k = [&](int w) { wait(&k_full[w & 1], (uint32_t)(w >> 1) & 1u); };
+      auto product_s = [&](int s, int w, bool first) {   // S_s = Q_s K_w^T; K_w has landed
         if (first) wait(&q_full[s], 0);
-        if (s == 0 || skip0 > w) wait(&k_full[w & 1], (uint32_t)(w >> 1) & 1u);   // once a window
         if (!ok) return;
         tc_fence_after();
         const uint64_t a = dq + (uint64_t)(s * (L::TILE >> 4)), b = dk + (uint64_t)((w & 1) * (L::TILE >> 4));
@@ -393,18 +393,19 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         commit_by(&s_full[s], leader);
         if (s == nst - 1) commit_by(&k_free[w & 1], leader);
       };
+      wait_k(0);
       if (!skip0) product_s(0, 0, true);
       if (nst == 2) product_s(1, 0, true);
       for (int w = 0; w < nwin && ok; ++w) {
+        // both loads before the first P: nothing between a P and its products then
+        wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u);
+        if (scrub(w)) wait(&v_ok[w & 1], (uint32_t)(w >> 1) & 1u);
+        if (w + 1 < nwin) wait_k(w + 1);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (s >= nst || !ok) break;
           const int f = s == 0 ? skip0 : 0;
           if (w >= f) {   // O_s += P_s V_w
-            if (s == 0 || skip0 > w) {   // once a window
-              wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u);
-              if (scrub(w)) wait(&v_ok[w & 1], (uint32_t)(w >> 1) & 1u);
-            }
             wait(&p_full[s], (uint32_t)(w - f) & 1u);
             if (!ok) break;
             tc_fence_after();
@@ -434,7 +435,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const uint32_t sS = tS + s * 128 + lb, sO = tO + s * D + hf * (D / 2) + lb;
       float* s_top = reinterpret_cast<float*>(smem + L::OFF_TOP) + s * 256;
       const int pair = 1 + s * 4 + (warp & 3);   // named barrier of the two warps that share rows
-      float m = -INFINITY, l = 0.f;              // offset of the row; sum over this thread's keys
+      // rows of the tile behind the last vector or token hold anything: an
+      // infinite offset keeps them out of every decision
+      const bool live = r < p.T * p.G && t < len;
+      float m = live ? -INFINITY : INFINITY, l = 0.f;   // offset of the row; sum over this thread's keys
       bool ok = true;
 
       auto look_over = [&](int w) {   // V rows of keys past t0
@@ -467,15 +471,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (lane == 0) mbar_arrive(&v_ok[w & 1]);
       };
 
-      // the row's maximum over both halves of the keys
-      auto both = [&](float top) {
-        s_top[hf * 128 + r] = top;
-        pair_sync(pair);
-        return fmaxf(top, s_top[(hf ^ 1) * 128 + r]);
-      };
-      // One window.  The exponentials are taken at the offset the row has, while
-      // its maximum is found beside them; only if that says that an offset must
-      // move (rare after the first windows) are they taken again.  P stays in
+      // One window.  The exponentials are taken at the offset that the row has.
+      // A sum over this thread's 64 keys above kMoveSum says that some score
+      // has passed the offset: then (rarely after the first windows) both
+      // threads of the row find its maximum, move the offset there and take
+      // the exponentials again, whose sum can not pass 64.  P stays in
       // registers until both warps have read their scores, because it goes
       // where the scores are.
       auto window = [&](auto masked_c, int w) {
@@ -483,34 +483,35 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (ok && !mbar_wait(&s_full[s], (uint32_t)(w - f) & 1u)) ok = false;
         tc_fence_after();
         const int lim = t - w_start(w) - 64 * hf;   // the last visible one of this thread's keys
-        auto chunks = [&](auto&& use) {             // its scores, 32 at a time
+        auto scores = [&](uint32_t (&x)[64]) {      // its scores
+          ld32(sS + 64 * hf, x);
+          ld32(sS + 64 * hf + 32, x + 32);
+          tmem_ld_wait();
+          if constexpr (MASKED) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t x[32];
-            ld32(sS + 64 * hf + 32 * c, x);
-            tmem_ld_wait();
-            if constexpr (MASKED) {
-#pragma unroll
-              for (int u = 0; u < 32; ++u)
-                if (32 * c + u > lim) x[u] = 0xff800000u;
-            }
-            use(c, x);
+            for (int u = 0; u < 64; ++u)
+              if (u > lim) x[u] = 0xff800000u;
           }
         };
-        auto max32 = [](const uint32_t (&x)[32], float top) {
-          float a = top, b = __uint_as_float(x[31]);
+        auto new_offset = [&]() {   // of a live row: its maximum in this window
+          uint32_t x[64];
+          scores(x);
+          float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-          for (int u = 0; u < 28; u += 4) {
+          for (int u = 0; u < 64; u += 4) {
             a = max3(a, __uint_as_float(x[u]), __uint_as_float(x[u + 1]));
             b = max3(b, __uint_as_float(x[u + 2]), __uint_as_float(x[u + 3]));
           }
-          a = max3(a, __uint_as_float(x[28]), __uint_as_float(x[29]));
-          return max3(a, b, __uint_as_float(x[30]));
+          a = fmaxf(a, b);
+          s_top[hf * 128 + r] = a;
+          pair_sync(pair);
+          return fmaxf(a, s_top[(hf ^ 1) * 128 + r]) * p.scale_log2;
         };
-        if (w == f) {
-          float top = -INFINITY;
-          chunks([&](int, const uint32_t (&x)[32]) { top = max32(x, top); });
-          m = both(top) * p.scale_log2;
+        // rows that have seen no key yet: all of them in the first window, and
+        // those that lie before a window that hid it all
+        if (w == f || w_start(w - 1) > tmin) {
+          const float top = new_offset();
+          if (m == -INFINITY) m = top;
         }
         uint32_t pk[32];
         float sum;
@@ -519,32 +520,30 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           const float neg = m == -INFINITY ? 0.f : -m;
           const uint64_t neg2 = pack2(neg, neg);
           uint64_t l2 = 0, l3 = 0;
-          float top = -INFINITY;
-          chunks([&](int c, const uint32_t (&x)[32]) {
-            top = max32(x, top);
+          uint32_t x[64];
+          scores(x);
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              float a, b;
-              unpack2(fma2(pack2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), scale2, neg2), a, b);
-              const __nv_bfloat162 v = __floats2bfloat162_rn(ex2p(a), ex2p(b));
-              const uint32_t q = *reinterpret_cast<const uint32_t*>(&v);
-              pk[16 * c + u] = q;
-              const uint64_t q2 = pack2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
-              if (u & 1) l3 = add2(l3, q2);
-              else l2 = add2(l2, q2);
-            }
-          });
+          for (int u = 0; u < 32; ++u) {
+            float a, b;
+            unpack2(fma2(pack2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), scale2, neg2), a, b);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(ex2p(a), ex2p(b));
+            const uint32_t q = *reinterpret_cast<const uint32_t*>(&v);
+            pk[u] = q;
+            const uint64_t q2 = pack2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
+            if (u & 1) l3 = add2(l3, q2);
+            else l2 = add2(l2, q2);
+          }
           float a, b;
           unpack2(add2(l2, l3), a, b);
           sum = a + b;
           tc_fence_before();
-          const bool any = pair_any(top * p.scale_log2 > m + kMove, pair);
+          const bool any = pair_any(sum > kMoveSum, pair);
           tc_fence_after();
           if (!any) break;
-          const float next = both(top) * p.scale_log2;
-          const bool move = next > m + kMove;
-          const float scale = move ? ex2p(m - next) : 1.f;
-          if (move) m = next;
+          const float top = new_offset();
+          const bool move = live && top > m;
+          const float scale = move ? ex2p(m - top) : 1.f;
+          if (move) m = top;
           l *= scale;
           if (w > f) {
 #pragma unroll
@@ -578,7 +577,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const float inv = 1.f / (s_top[r] + s_top[128 + r]);
         if (ok && !mbar_wait(&o_fin[s], 0)) ok = false;
         tc_fence_after();
-        const bool mine = ok && r < p.T * p.G && t < len;
+        const bool mine = ok && live;
         __nv_bfloat16* dst = p.out + ((size_t)(row0 + t) * p.Hq + h * p.G + r % p.G) * D + hf * (D / 2);
         const bool anybad = *reinterpret_cast<volatile int*>(&s_anybad) != 0;
 #pragma unroll

@@ -102,6 +102,15 @@ def test_rising_scores_rescale_every_window(gpu):
     Prompt([1100], 4, 2, 128, seed=4, edit=edit).check()
 
 
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(5, 1, 128), (3, 1, 64), (1, 1, 128)])
+def test_very_low_scores(gpu, q_heads, kv_heads, dim):
+    """Scores of minus some hundreds everywhere: an offset that is not the row's own would leave nothing of it."""
+    def edit(p):
+        p.q[:, :, 0], p.k[:] = bits(np.full(p.q.shape[:2], 64.0)), bits(np.zeros(p.k.shape))
+        p.k[:, :, 0] = bits(np.random.default_rng(9).uniform(-64, -60, p.k.shape[:2]))
+    Prompt([300, 131, 128, 9], q_heads, kv_heads, dim, seed=8, edit=edit).check()
+
+
 @pytest.mark.parametrize("value", [0x7FC0, 0x7F80, 0xFF80])
 @pytest.mark.parametrize("q_heads,kv_heads,dim,lens", [(4, 2, 64, [300, 90]), (2, 2, 128, [513, 3]), (40, 8, 128, [70, 200])])
 def test_what_a_row_may_not_see_does_not_reach_it(gpu, value, q_heads, kv_heads, dim, lens):
