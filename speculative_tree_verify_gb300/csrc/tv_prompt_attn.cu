@@ -262,10 +262,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     __syncthreads();
   }
   if (warp == 0) {
-    int a = 0, mine = 0;   // n <= 32: the lane's sequence
+    int a = 0, b = 0, mine = 0;   // n <= 32: the lane's sequence
     if (p.n <= 32 && lane < p.n) {
       a = __ldg(p.starts + lane);
-      const int b = __ldg(p.starts + lane + 1);
+      b = __ldg(p.starts + lane + 1);
       mine = a < 0 || b < a || b > p.rows ? -1 : (b - a + 2 * p.T - 1) / (2 * p.T);
     }
     const bool stop = status_get(p.status) != 0;
@@ -286,33 +286,40 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     };
     const int place = blockIdx.x / p.Hkv;
     int found = -1, lo = 0;
-    if (!stop && !bad && at_least(0) > place) {
+    if (p.n == 1) {   // one sequence: its pairs from the last to the first
+      lo = top - 1 - place;
+      found = !stop && !bad && lo >= 0 ? 0 : -1;
+    } else if (!stop && !bad && at_least(0) > place) {
       int hi = top;   // the largest l with N(l) > place; N(top) = 0
-      if (p.n == 1) lo = top - 1 - place;
-      else
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (at_least(mid) > place) lo = mid;
-          else hi = mid;
-        }
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (at_least(mid) > place) lo = mid;
+        else hi = mid;
+      }
       int k = place - at_least(lo + 1);   // the k-th sequence with more than lo pairs
       for (int i0 = 0; i0 < p.n; i0 += 32) {
         const int i = i0 + lane;
         const unsigned m = __ballot_sync(0xffffffffu, i < p.n && (p.n <= 32 ? mine : s_cnt[i]) > lo);
         if (k < __popc(m)) {
-          found = i0 + (int)__fns(m, 0, k + 1);
+          const unsigned at = __ballot_sync(0xffffffffu, (m >> lane & 1u) && __popc(m & ((1u << lane) - 1u)) == k);
+          found = i0 + __ffs(at) - 1;
           break;
         }
         k -= __popc(m);
       }
     }
+    if (p.n <= 32) {
+      a = __shfl_sync(0xffffffffu, a, found & 31);
+      b = __shfl_sync(0xffffffffu, b, found & 31);
+    } else if (found >= 0) {
+      a = __ldg(p.starts + found);
+      b = __ldg(p.starts + found + 1);
+    }
     if (lane == 0) {
       s_place[0] = found;
       s_place[1] = lo;
-      if (found >= 0) {
-        s_place[2] = __ldg(p.starts + found);
-        s_place[3] = __ldg(p.starts + found + 1);
-      }
+      s_place[2] = a;
+      s_place[3] = b;
     }
   }
   tc_fence_before();
@@ -349,8 +356,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           for (int a = 0; a < D / 64; ++a)
             tma_load_3d(smem + L::OFF_Q + s * L::TILE + a * kAtomP, &map_q, &q_full[s], a * 64, h * p.G, row0 + t0 + s * p.T);
         };
-        load_q(0);
         load_kv(&map_k, k_full, L::OFF_K, 0);
+        load_q(0);
         if (nst == 2) load_q(1);
         load_kv(&map_v, v_full, L::OFF_V, 0);
         int nk = 1, nv = 1;
@@ -493,9 +500,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               if (u > lim) x[u] = 0xff800000u;
           }
         };
-        auto new_offset = [&]() {   // of a live row: its maximum in this window
-          uint32_t x[64];
-          scores(x);
+        auto row_max = [&](const uint32_t (&x)[64]) {   // over both halves, in log2 units
           float a = -INFINITY, b = -INFINITY;
 #pragma unroll
           for (int u = 0; u < 64; u += 4) {
@@ -507,10 +512,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           pair_sync(pair);
           return fmaxf(a, s_top[(hf ^ 1) * 128 + r]) * p.scale_log2;
         };
+        uint32_t x[64];
+        scores(x);
         // rows that have seen no key yet: all of them in the first window, and
         // those that lie before a window that hid it all
         if (w == f || w_start(w - 1) > tmin) {
-          const float top = new_offset();
+          const float top = row_max(x);
           if (m == -INFINITY) m = top;
         }
         uint32_t pk[32];
@@ -520,8 +527,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           const float neg = m == -INFINITY ? 0.f : -m;
           const uint64_t neg2 = pack2(neg, neg);
           uint64_t l2 = 0, l3 = 0;
-          uint32_t x[64];
-          scores(x);
 #pragma unroll
           for (int u = 0; u < 32; ++u) {
             float a, b;
@@ -540,7 +545,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           const bool any = pair_any(sum > kMoveSum, pair);
           tc_fence_after();
           if (!any) break;
-          const float top = new_offset();
+          scores(x);
+          const float top = row_max(x);
           const bool move = live && top > m;
           const float scale = move ? ex2p(m - top) : 1.f;
           if (move) m = top;
@@ -566,10 +572,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       };
 
       for (int w = 0; w < nwin; ++w) {
-        if (scrub(w)) look_over(w);
-        if (!active || w < f) continue;
-        if (w_start(w) + 127 > tmin) window(std::integral_constant<bool, true>{}, w);
-        else window(std::integral_constant<bool, false>{}, w);
+        if (active && w >= f) {
+          if (w_start(w) + 127 > tmin) window(std::integral_constant<bool, true>{}, w);
+          else window(std::integral_constant<bool, false>{}, w);
+        }
+        if (scrub(w)) look_over(w);   // V lands while the first softmax runs
       }
       if (active) {
         s_top[hf * 128 + r] = l;   // after the last window's pair_any: the maxima were read
@@ -577,9 +584,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const float inv = 1.f / (s_top[r] + s_top[128 + r]);
         if (ok && !mbar_wait(&o_fin[s], 0)) ok = false;
         tc_fence_after();
-        const bool mine = ok && live;
-        __nv_bfloat16* dst = p.out + ((size_t)(row0 + t) * p.Hq + h * p.G + r % p.G) * D + hf * (D / 2);
+        // this warp's 32 rows of D / 2 values through the query tile's shared
+        // memory (its products are done), so that a row is stored in one piece
         const bool anybad = *reinterpret_cast<volatile int*>(&s_anybad) != 0;
+        constexpr int CH = D / 16;   // 16-byte pieces of half a row
+        uint4* stage = reinterpret_cast<uint4*>(smem + L::OFF_Q + s * L::TILE) + (warp & 7) * 32 * CH;
 #pragma unroll
         for (int c = 0; c < D / 2; c += 32) {
           uint32_t o[32];
@@ -595,19 +604,26 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               else if (ni) o[u] = 0xff800000u;
             }
           }
-          if (mine) {
 #pragma unroll
-            for (int u = 0; u < 32; u += 8) {
-              uint32_t b[4];
+          for (int u = 0; u < 32; u += 8) {
+            uint32_t b[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 v =
-                    __floats2bfloat162_rn(__uint_as_float(o[u + 2 * e]) * inv, __uint_as_float(o[u + 2 * e + 1]) * inv);
-                b[e] = *reinterpret_cast<const uint32_t*>(&v);
-              }
-              *reinterpret_cast<uint4*>(dst + c + u) = make_uint4(b[0], b[1], b[2], b[3]);
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 v =
+                  __floats2bfloat162_rn(__uint_as_float(o[u + 2 * e]) * inv, __uint_as_float(o[u + 2 * e + 1]) * inv);
+              b[e] = *reinterpret_cast<const uint32_t*>(&v);
             }
+            stage[lane * CH + (((c + u) >> 3) ^ (lane & (CH - 1)))] = make_uint4(b[0], b[1], b[2], b[3]);
           }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int row = i * (32 / CH) + lane / CH, c = lane % CH;   // of the warp's 32 rows
+          const int rr = (warp & 3) * 32 + row, tt = tmin + rr / p.G;
+          if (ok && rr < p.T * p.G && tt < len)
+            *reinterpret_cast<uint4*>(p.out + ((size_t)(row0 + tt) * p.Hq + h * p.G + rr % p.G) * D + hf * (D / 2) + c * 8) =
+                stage[row * CH + (c ^ (row & (CH - 1)))];
         }
       }
       if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
