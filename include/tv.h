@@ -725,7 +725,7 @@ TV_API int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const t
  * past a sequence's length are never used, whatever they hold.  The same
  * inputs give the same bits.
  * Host checks: TV_E_ARG, TV_E_UNSUPPORTED (n_q_heads not a multiple of
- * n_kv_heads, n > 4096), TV_E_WORKSPACE.  Device checks: TV_E_SEQ (also a
+ * n_kv_heads, n > 2048), TV_E_WORKSPACE.  Device checks: TV_E_SEQ (also a
  * sequence listed twice with k_new), nothing is written; TV_E_PAGE (a page
  * entry out of range: out is unspecified).
  */

@@ -5,9 +5,10 @@
 // What bounds it: every cached K and V byte is read once for at most 16 query
 // heads, far below the tensor cores' rate, so the kernel is built as a stream
 // over memory.  The work is the list of 64-token tiles of every (sequence, KV
-// head, block of 16 query heads) in that order; CTA c takes an equal,
-// contiguous range of it, whatever the lengths, so one long context among
-// short ones and one sequence alone both fill every SM.  A head cut by a range
+// head, block of 16 query heads) in that order, each such head block counted
+// SEG_COST tiles more for what it costs to begin and end; CTA c takes an
+// equal, contiguous range of it, whatever the lengths, so one long context
+// among short ones and one sequence alone both fill every SM.  A head block cut by a range
 // border leaves unnormalised partials that paged_merge_kernel joins in tile
 // order: no atomics, the same bits every run.
 //
@@ -40,12 +41,15 @@ constexpr int kCompWarps = 8;
 constexpr int kCompThreads = kCompWarps * 32;
 constexpr int kPaThreads = kCompThreads + 32;
 constexpr int kRows = 16;                        // query heads of a block
+constexpr int kMaxTokens = 2048;                 // sequences of one call: their places fit shared memory beside the stages
+constexpr int kInfo = 640;                       // up to here their table rows and lengths do, too
 constexpr int kRedRows = 4;                      // rows joined at a time when a head block ends
 constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 a CTA
 constexpr float kMoveLog2 = 8.f;
 
 struct PaWs {
-  uint32_t* first;    // [n + 1]: first tile of each sequence in the list of tiles
+  int4* cut;          // [CTAs]: the head block whose first tile but not the last is the CTA's:
+                      // listed index, head block, last CTA with a tile of it; -1: none
   float* ml;          // [2 CTAs][kRows][2]: offset and sum
   float* o;           // [2 CTAs][kRows][D]
 };
@@ -69,12 +73,15 @@ struct PaSmem {
   static constexpr int HALF = (D / 64) * SLAB;               // a tile's K (or V)
   static constexpr int STAGE = 2 * HALF;
   static constexpr int OFF_RED = kStages * STAGE;            // [8 warps][kRedRows][D] fp32; the marks of listed rows first
+  static constexpr int SEG_COST = 256 / D;                   // what a head block costs besides its tiles, in tiles
   static constexpr int OFF_ML = OFF_RED + kCompWarps * kRedRows * D * 4;
-  static constexpr int OFF_BAR = OFF_ML + kCompWarps * kRows * 8;
-  static constexpr int OFF_FIRST = OFF_BAR + 256;            // [n + 1]
-  static size_t bytes(int n) { return 1024 + OFF_FIRST + (size_t)(n + 1) * 4; }
+  static constexpr int Q_ROW = D * 2 + 16;                   // rows 16 bytes apart in the banks: ldmatrix without conflicts
+  static constexpr int OFF_Q = OFF_ML + kCompWarps * kRows * 8;   // [2][kRows] query rows: a segment's
+  static constexpr int OFF_BAR = OFF_Q + 2 * kRows * Q_ROW;
+  static constexpr int OFF_FIRST = OFF_BAR + 128;            // [n + 1]; up to kInfo sequences also their rows and lengths
+  static size_t bytes(int n) { return 1024 + OFF_FIRST + (size_t)(n + 1) * 4 + (n <= kInfo ? (size_t)n * 8 : 0); }
   static_assert(kCompWarps * kRedRows * D * 4 >= kMaxSeqs / 8, "a mark for every table row");
-  static_assert(1024 + OFF_FIRST + (kMaxListed + 1) * 4 <= 232448 - 256, "shared memory of one CTA");
+  static_assert(1024 + OFF_FIRST + (kMaxTokens + 1) * 4 <= 232448 - 256 && kInfo * 12 <= kMaxTokens * 4, "shared memory of one CTA");
 };
 
 __device__ __forceinline__ float ex2f(float x) {   // 2^x by the SFU, about 2^-22 relative, 2^-inf = 0
@@ -100,6 +107,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// untiled copy: 16-byte aligned addresses, a multiple of 16 bytes
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(smem_dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 __device__ __forceinline__ void comp_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kCompThreads) : "memory"); }
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
@@ -112,64 +125,115 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* empty = full + kStages;
+  uint64_t* q_full = empty + kStages;    // [2] a segment's queries landed
+  uint64_t* q_free = q_full + 2;         // [2] the eight warps have them
   uint32_t* s_first = reinterpret_cast<uint32_t*>(smem + L::OFF_FIRST);
   float* s_red = reinterpret_cast<float*>(smem + L::OFF_RED);
   float2* s_ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
   uint32_t* s_mark = reinterpret_cast<uint32_t*>(smem + L::OFF_RED);
+  int* s_row = reinterpret_cast<int*>(s_first + p.n + 1);   // n <= kInfo: table row and length
+  int* s_len = s_row + p.n;
   __shared__ uint32_t s_part[kPaThreads / 32];
+  __shared__ int s_bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ps = p.pool.page_size, Hkv = p.pool.n_kv_heads;
+  const bool info = p.n <= kInfo;
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 4);   // the four warps that compute its tile
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_free[s], kCompWarps);
+    }
     fence_mbar_init();
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
+    s_bad = 0;
   }
+  // query rows past the group's heads: products nobody reads, of finite values
+  for (int e = tid; e < 2 * kRows * L::Q_ROW / 16; e += kPaThreads)
+    reinterpret_cast<uint4*>(smem + L::OFF_Q)[e] = make_uint4(0u, 0u, 0u, 0u);
+  fence_async_smem();
+  if (p.n > 32 && p.k_new)
+    for (int i = tid; i < (p.seqs.max_seqs + 31) / 32; i += kPaThreads) s_mark[i] = 0u;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
 
   // ---- the list of tiles: every CTA reads the same lengths and finds the same list
-  int bad = status_get(p.status) != 0;
-  if (p.k_new) {
-    for (int i = tid; i < (p.seqs.max_seqs + 31) / 32; i += kPaThreads) s_mark[i] = 0u;
+  uint32_t all;
+  auto head_tiles = [&](int len) {   // of one head block, its fixed cost included; the host has seen to it that all fit 31 bits
+    return len > 0 ? (uint32_t)(tiles_of(len) + L::SEG_COST) : 0u;
+  };
+  auto look = [&](int i, int& s) {   // length of listed sequence i, -1: refused
+    s = __ldg(p.ids + i);
+    return s >= 0 && s < p.seqs.max_seqs ? seq_len(p.seqs, ps, s) : -1;
+  };
+  if (p.n <= 32) {   // one warp, one barrier
+    if (warp == 0) {
+      const bool stop = status_get(p.status) != 0;
+      int s = -1 - lane, len = 0;
+      if (lane < p.n) len = look(lane, s);
+      const bool twice = __popc(__match_any_sync(0xffffffffu, lane < p.n ? s : -1 - lane)) > 1;
+      const bool bad = __any_sync(0xffffffffu, len < 0 || (p.k_new && twice));   // two new tokens, one slot
+      uint32_t x = head_tiles(len) * Hkv * p.HB;
+      const uint32_t own = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane < p.n) {
+        s_first[lane] = x - own;
+        s_row[lane] = s;
+        s_len[lane] = len;
+      }
+      if (lane == 31) s_first[p.n] = x;
+      if (lane == 0) {
+        if (bad && !stop) status_set(p.status, TV_E_SEQ);
+        s_bad = bad || stop;
+      }
+    }
+    __syncthreads();
+    if (s_bad) return;
+    all = s_first[p.n];
+  } else {
+    int bad = status_get(p.status) != 0;
+    const int per = (p.n + kPaThreads - 1) / kPaThreads;
+    uint32_t sum = 0;
+    for (int i = tid * per; i < min(p.n, (tid + 1) * per); ++i) {
+      int s, len = look(i, s);
+      if (len >= 0 && p.k_new && (atomicOr(&s_mark[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u) len = -1;
+      if (len < 0) bad = TV_E_SEQ;
+      if (info) {
+        s_row[i] = s;
+        s_len[i] = len;
+      }
+      s_first[i] = sum;
+      sum += head_tiles(len) * Hkv * p.HB;
+    }
+    if (bad < 0) status_set(p.status, bad);
+    uint32_t x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_part[warp] = x;
+    if (__syncthreads_or(bad)) return;
+    uint32_t before = x - sum;
+    all = 0;
+    for (int w = 0; w < kPaThreads / 32; ++w) {
+      if (w < warp) before += s_part[w];
+      all += s_part[w];
+    }
+    for (int i = tid * per; i < min(p.n, (tid + 1) * per); ++i) s_first[i] += before;
+    if (tid == 0) s_first[p.n] = all;
     __syncthreads();
   }
-  const int per = (p.n + kPaThreads - 1) / kPaThreads;
-  uint32_t sum = 0;   // the host has seen to it that all of them fit 31 bits
-  for (int i = tid * per; i < min(p.n, (tid + 1) * per); ++i) {
-    const int s = p.ids[i];
-    int len = -1;
-    if (s >= 0 && s < p.seqs.max_seqs) {
-      len = seq_len(p.seqs, ps, s);
-      if (p.k_new && (atomicOr(&s_mark[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u) len = -1;   // two new tokens, one slot
-    }
-    if (len < 0) bad = TV_E_SEQ;
-    s_first[i] = sum;
-    sum += (uint32_t)(tiles_of(max(len, 0)) * Hkv * p.HB);
-  }
-  if (bad < 0) status_set(p.status, bad);
-  uint32_t x = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_part[warp] = x;
-  if (__syncthreads_or(bad)) return;
-  uint32_t before = x - sum, all = 0;
-  for (int w = 0; w < kPaThreads / 32; ++w) {
-    if (w < warp) before += s_part[w];
-    all += s_part[w];
-  }
-  for (int i = tid * per; i < min(p.n, (tid + 1) * per); ++i) s_first[i] += before;
-  if (tid == 0) s_first[p.n] = all;
-  __syncthreads();
-  if (blockIdx.x == 0)
-    for (int i = tid; i <= p.n; i += kPaThreads) p.ws.first[i] = s_first[i];
   // sequences without a token: zeros
   for (int i = blockIdx.x; i < p.n; i += gridDim.x)
     if (s_first[i + 1] == s_first[i])
@@ -177,29 +241,34 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         reinterpret_cast<uint4*>(p.out + (size_t)i * p.Hq * D)[e] = make_uint4(0u, 0u, 0u, 0u);
 
   const uint32_t chunk = (all + gridDim.x - 1) / gridDim.x;
-  const uint32_t lo = chunk * blockIdx.x, hi = min(all, lo + chunk);
+  const uint32_t lo = min(all, chunk * blockIdx.x), hi = min(all, lo + chunk);
+  if (tid == 0) p.ws.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (lo >= hi) return;
-  int i0 = 0;   // the sequence of tile lo: the last whose first tile is at or before it
+  int i0 = 0;   // the sequence of place lo: the last whose first place is at or before it
   for (int b = p.n - 1; i0 < b;) {
     const int mid = (i0 + b + 1) >> 1;
     if (s_first[mid] <= lo) i0 = mid;
     else b = mid - 1;
   }
 
-  // a run of tiles of one sequence and head block
+  // a run of tiles of one sequence and head block; a range may hold no more
+  // than (part of) its fixed cost, then t0 == t1
   struct Seg {
     int i, hh, s, len, t0, t1;   // listed index, head block, table row, length, tiles [t0, t1)
+    uint32_t base, next;         // place of its first tile; place behind the run
   };
-  auto segment = [&](uint32_t at, int i) {   // the segment that holds tile `at` of sequence i (or a later one)
+  auto segment = [&](uint32_t at, int i) {   // the run that holds place `at` of sequence i (or a later one)
     while (s_first[i + 1] <= at) ++i;
     Seg g;
     g.i = i;
-    g.s = __ldg(p.ids + i);
-    g.len = __ldcg(p.seqs.lens + g.s);
-    const uint32_t T = tiles_of(g.len), off = at - s_first[i];
-    g.hh = (int)(off / T);
-    g.t0 = (int)(off % T);
-    g.t1 = (int)min(T, g.t0 + (hi - at));
+    g.s = info ? s_row[i] : __ldg(p.ids + i);
+    g.len = info ? s_len[i] : __ldcg(p.seqs.lens + g.s);
+    const uint32_t T = tiles_of(g.len), unit = T + L::SEG_COST, off = at - s_first[i];
+    g.hh = (int)(off / unit);
+    g.base = s_first[i] + g.hh * unit + L::SEG_COST;
+    g.next = min(hi, g.base + T);
+    g.t0 = at > g.base ? (int)(at - g.base) : 0;
+    g.t1 = g.next > g.base ? (int)(g.next - g.base) : 0;
     return g;
   };
 
@@ -213,12 +282,24 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int slab = which % (D / 64);
     const uint64_t pol = policy_evict_first();
     bool ok = true;
-    int issued = 0;
+    int issued = 0, segs = 0;
     uint32_t at = lo;
     int i = i0;
     while (at < hi && ok) {
       const Seg g = segment(at, i);
       i = g.i;
+      at = g.next;
+      if (g.t0 == g.t1) continue;
+      // its queries
+      if (segs >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&q_free[segs & 1], (uint32_t)((segs - 2) >> 1) & 1u));
+      if (!ok) break;
+      const int r0 = (g.hh % p.HB) * kRows, nr = min(kRows, p.G - r0);
+      if (lane == 0) mbar_arrive_expect_tx(&q_full[segs & 1], (uint32_t)(nr * D * 2));
+      __syncwarp();
+      if (lane < nr)
+        bulk_load(smem + L::OFF_Q + ((segs & 1) * kRows + lane) * L::Q_ROW,
+                  p.q + (size_t)g.i * p.q_stride + (size_t)((g.hh / p.HB) * p.G + r0 + lane) * D, D * 2, &q_full[segs & 1]);
+      ++segs;
       const int32_t* row = p.seqs.pages + (size_t)g.s * p.seqs.max_pages;
       const int h = g.hh / p.HB;
       auto entry = [&](int t) {   // this lane's page of tile t, -1 past the length
@@ -246,9 +327,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         __syncwarp();
         ++issued;
       }
-      at += g.t1 - g.t0;
     }
     if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
+    for (int u = segs > 2 ? segs - 2 : 0; u < segs; ++u) mbar_wait(&q_full[u & 1], (uint32_t)(u >> 1) & 1u);
     // loads in flight land before the CTA leaves
     for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u) mbar_wait(&full[u % kStages], (uint32_t)(u / kStages) & 1u);
     return;
@@ -259,7 +340,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   const int quad = warp >> 2, sl = warp & 3;        // tiles with (count mod 2) == quad; tokens 16 sl .. + 15 of a tile
   const int g8 = lane >> 2, t4 = lane & 3;
   bool ok = true;
-  int cnt = 0;                                      // tiles of this CTA before the current one
+  int cnt = 0, segs = 0;                            // tiles and segments of this CTA before the current one
   uint32_t at = lo;
   int i = i0;
   // lane addresses inside a slab: K as [token][d] fragments, V transposed
@@ -268,19 +349,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   while (at < hi) {
     const Seg g = segment(at, i);
     i = g.i;
+    at = g.next;
+    if (g.t0 == g.t1) continue;
     const int h = g.hh / p.HB, r0 = (g.hh % p.HB) * kRows;   // KV head, first query head of the block in the group
     const int nr = min(kRows, p.G - r0);
     uint32_t qf[KS][4];
     {
-      const __nv_bfloat16* q0 = p.q + (size_t)g.i * p.q_stride + (size_t)(h * p.G + r0) * D + 2 * t4;
+      if (ok && !mbar_wait(&q_full[segs & 1], (uint32_t)(segs >> 1) & 1u)) ok = false;
+      const uint32_t qa = smem_u32(smem + L::OFF_Q) + ((segs & 1) * kRows + (lane & 15)) * L::Q_ROW + (lane >> 4) * 16;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const __nv_bfloat16 *a = q0 + (size_t)g8 * D + 16 * k, *b = a + 8 * D;
-        qf[k][0] = g8 < nr ? __ldcg(reinterpret_cast<const uint32_t*>(a)) : 0u;
-        qf[k][1] = g8 + 8 < nr ? __ldcg(reinterpret_cast<const uint32_t*>(b)) : 0u;
-        qf[k][2] = g8 < nr ? __ldcg(reinterpret_cast<const uint32_t*>(a + 8)) : 0u;
-        qf[k][3] = g8 + 8 < nr ? __ldcg(reinterpret_cast<const uint32_t*>(b + 8)) : 0u;
-      }
+      for (int k = 0; k < KS; ++k) ldsm4(qa + k * 32, qf[k]);
     }
     float o[2 * KS][4];
 #pragma unroll
@@ -394,6 +472,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       s_ml[warp * kRows + g8 + 8] = make_float2(m1, l1);
     }
     comp_sync();
+    // The queries' place is given up here, not behind the loads: an arrival
+    // does not wait for ldmatrix results that nothing has used yet.  (A warp
+    // without a tile in this run has not used them, and never will.)
+    if (lane == 0) mbar_arrive(&q_free[segs & 1]);
+    ++segs;
     const int T = tiles_of(g.len);
     const bool whole = g.t0 == 0 && g.t1 == T;
     const size_t slot = (size_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0);   // a CTA's first segment may begin inside a head, its last end inside one
@@ -440,55 +523,77 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         comp_sync();
       }
     }
-    at += g.t1 - g.t0;
+    if (tid == 0 && g.t0 == 0 && !whole)   // the CTA's last run
+      p.ws.cut[blockIdx.x] = make_int4(g.i, g.hh, (int)((g.base + T - 1) / chunk), 0);
   }
   if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
 }
 
-// One block per (listed sequence, query head) that a range border cut: its
-// partials in tile order.
+// Block c joins the head block whose first tile CTA c had and whose last it had
+// not: the partials of CTAs c (its slot 1) to the last one's (slot 0), in that
+// order.  A warp a row for the weights, then every thread a pair of values.
+constexpr int kMergeThreads = 512;
 template <int D>
-__global__ void __launch_bounds__(D) paged_merge_kernel(const PaParams p, int ctas) {
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PaParams p) {
+  __shared__ float s_w[kRows][kMaxCtas];   // 2^(m_c - M) / sum
   pdl_wait();
   pdl_trigger();
-  if (status_get(p.status) != 0) return;
-  const int i = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, d = threadIdx.x;
-  const uint32_t f0 = __ldcg(p.ws.first + i), f1 = __ldcg(p.ws.first + i + 1), all = __ldcg(p.ws.first + p.n);
-  if (f0 == f1) return;
-  const uint32_t T = (f1 - f0) / (p.pool.n_kv_heads * p.HB), chunk = (all + ctas - 1) / ctas;
-  const int row = (hq % p.G) % kRows, hh = (hq / p.G) * p.HB + (hq % p.G) / kRows;
-  const uint32_t a = f0 + hh * T, b = a + T;
-  const int c0 = (int)(a / chunk), c1 = (int)((b - 1) / chunk);
-  if (c0 == c1) return;
-  float M = -INFINITY;
-  for (int c = c0; c <= c1; ++c) {
-    const size_t slot = (size_t)c * 2 + (a >= c * chunk ? 1 : 0);
-    M = fmaxf(M, __ldcg(p.ws.ml + (slot * kRows + row) * 2));
+  const int4 cut = __ldcg(p.ws.cut + blockIdx.x);
+  if (cut.x < 0 || status_get(p.status) != 0) return;
+  const int c0 = blockIdx.x, np = cut.z - c0 + 1, r0 = (cut.y % p.HB) * kRows, nr = min(kRows, p.G - r0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto slot = [&](int c) { return (size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0); };
+  if (warp < nr) {
+    float2 ml[kMaxCtas / 32];
+    float M = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxCtas / 32; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (32 * k + lane < np) ml[k] = __ldcg(reinterpret_cast<const float2*>(p.ws.ml + (slot(32 * k + lane) * kRows + warp) * 2));
+      M = fmaxf(M, ml[k].x);
+    }
+    M = warp_max(M);
+#pragma unroll
+    for (int k = 0; k < kMaxCtas / 32; ++k) {
+      const float w = ml[k].x == -INFINITY ? 0.f : ex2f(ml[k].x - M);
+      sum += ml[k].x == -INFINITY ? ml[k].y : ml[k].y * w;
+      ml[k].x = w;
+    }
+    sum = warp_sum(sum);
+#pragma unroll
+    for (int k = 0; k < kMaxCtas / 32; ++k)
+      if (32 * k + lane < np) s_w[warp][32 * k + lane] = ml[k].x / sum;
   }
-  float Ls = 0.f, o = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const size_t slot = (size_t)c * 2 + (a >= c * chunk ? 1 : 0);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws.ml + (slot * kRows + row) * 2));
-    const float w = ml.x == -INFINITY ? 0.f : ex2f(ml.x - M);
-    Ls += ml.x == -INFINITY ? ml.y : ml.y * w;
-    o += __ldcg(p.ws.o + (slot * kRows + row) * D + d) * w;
+  __syncthreads();
+  for (int e = threadIdx.x; e < nr * (D / 2); e += kMergeThreads) {
+    const int row = e / (D / 2), d = 2 * (e % (D / 2));
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 8
+    for (int c = 0; c < np; ++c) {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ws.o + (slot(c) * kRows + row) * D + d));
+      const float w = s_w[row][c];
+      acc.x = fmaf(v.x, w, acc.x);
+      acc.y = fmaf(v.y, w, acc.y);
+    }
+    *reinterpret_cast<__nv_bfloat162*>(p.out + ((size_t)cut.x * p.Hq + (cut.y / p.HB) * p.G + r0 + row) * D + d) =
+        __floats2bfloat162_rn(acc.x, acc.y);
   }
-  p.out[((size_t)i * p.Hq + hq) * D + d] = f2bf(o / Ls);
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-size_t pa_ws(int n, int D, PaWs* ws, uint8_t* base) {
-  const size_t first = align256((size_t)(n + 1) * 4), ml = align256((size_t)2 * kMaxCtas * kRows * 2 * 4);
+size_t pa_ws(int D, PaWs* ws, uint8_t* base) {
+  const size_t cut = align256((size_t)kMaxCtas * sizeof(int4)), ml = align256((size_t)2 * kMaxCtas * kRows * 2 * 4);
   const size_t o = align256((size_t)2 * kMaxCtas * kRows * D * 4);
   if (ws) {
-    ws->first = reinterpret_cast<uint32_t*>(base);
-    ws->ml = reinterpret_cast<float*>(base + first);
-    ws->o = reinterpret_cast<float*>(base + first + ml);
+    ws->cut = reinterpret_cast<int4*>(base);
+    ws->ml = reinterpret_cast<float*>(base + cut);
+    ws->o = reinterpret_cast<float*>(base + cut + ml);
   }
-  return first + ml + o;
+  return cut + ml + o;
 }
+
+int check_tokens(int n) { return n < 1 ? TV_E_ARG : (n > kMaxTokens ? TV_E_UNSUPPORTED : TV_OK); }
 
 int check_heads(int n_q_heads, int n_kv_heads) {
   if (n_q_heads < 1) return TV_E_ARG;
@@ -503,11 +608,11 @@ int launch_paged(const PaParams& p, int sms, cudaStream_t st) {
   int rc = make_tmap_bf16(&mk, p.pool.k, D, rows, 64, R);
   if (rc || (rc = make_tmap_bf16(&mv, p.pool.v, D, rows, 64, R))) return rc;
   static std::atomic<bool> attr[64];
-  if (ensure_smem_limit(paged_attn_kernel<D>, PaSmem<D>::bytes(kMaxListed), attr)) return TV_E_CUDA;
+  if (ensure_smem_limit(paged_attn_kernel<D>, PaSmem<D>::bytes(kMaxTokens), attr)) return TV_E_CUDA;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   rc = launch_pdl(paged_attn_kernel<D>, dim3(ctas), dim3(kPaThreads), PaSmem<D>::bytes(p.n), st, mk, mv, p);
   if (rc) return rc;
-  return launch_pdl(paged_merge_kernel<D>, dim3(p.n * p.Hq), dim3(D), 0, st, p, ctas);
+  return launch_pdl(paged_merge_kernel<D>, dim3(ctas), dim3(kMergeThreads), 0, st, p);
 }
 
 }  // namespace
@@ -519,9 +624,9 @@ extern "C" {
 
 int tv_attend_paged_workspace_size(const tv_pool* pool, int n_q_heads, int n, size_t* bytes) {
   int rc = check_pool(pool);
-  if (rc || (rc = check_heads(n_q_heads, pool->n_kv_heads)) || (rc = check_listed(n))) return rc;
+  if (rc || (rc = check_heads(n_q_heads, pool->n_kv_heads)) || (rc = check_tokens(n))) return rc;
   if (!bytes) return TV_E_ARG;
-  *bytes = pa_ws(n, pool->head_dim, nullptr, nullptr);
+  *bytes = pa_ws(pool->head_dim, nullptr, nullptr);
   return TV_OK;
 }
 
@@ -531,7 +636,7 @@ int tv_attend_paged(const tv_pool* pool, int layer, const tv_seqs* seqs, const i
   int rc = check_pool(pool);
   if (rc || (rc = check_seqs(seqs, pool))) return rc;
   if (!ids || !q || !out || !dev_status || !k_new != !v_new || layer < 0 || layer >= pool->n_layers) return TV_E_ARG;
-  if ((rc = check_heads(n_q_heads, pool->n_kv_heads)) || (rc = check_listed(n))) return rc;
+  if ((rc = check_heads(n_q_heads, pool->n_kv_heads)) || (rc = check_tokens(n))) return rc;
   const size_t D = pool->head_dim;
   if (!aligned16(q) || !aligned16(out) || q_stride % 8 != 0 || q_stride < n_q_heads * D) return TV_E_ARG;
   if (k_new && (!aligned16(k_new) || !aligned16(v_new) || kv_stride % 8 != 0 || kv_stride < pool->n_kv_heads * D))
@@ -539,11 +644,12 @@ int tv_attend_paged(const tv_pool* pool, int layer, const tv_seqs* seqs, const i
   PaParams p;
   p.G = n_q_heads / pool->n_kv_heads;
   p.HB = (p.G + kRows - 1) / kRows;
-  // blocks of the joining kernel, and the tiles of n sequences of the longest kind
-  const unsigned long long most = ((unsigned long long)seqs->max_pages * pool->page_size + kTile - 1) / kTile * pool->n_kv_heads * p.HB;
-  if ((long long)n * n_q_heads > 0x7fffffffll || most > 0x7fffffffull / (unsigned)n) return TV_E_UNSUPPORTED;
+  // the places of n sequences of the longest kind
+  const unsigned long long most =
+      (((unsigned long long)seqs->max_pages * pool->page_size + kTile - 1) / kTile + 4) * pool->n_kv_heads * p.HB;
+  if (most > 0x7fffffffull / (unsigned)n) return TV_E_UNSUPPORTED;
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  if (!workspace || !aligned16(workspace) || workspace_bytes < pa_ws(n, pool->head_dim, &p.ws, base)) return TV_E_WORKSPACE;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < pa_ws(pool->head_dim, &p.ws, base)) return TV_E_WORKSPACE;
   const int sms = num_sms();
   if (sms <= 0) return TV_E_CUDA;
   p.pool = *pool;

@@ -126,7 +126,8 @@ def test_page_sizes(gpu, ps, dim):
     Case(EDGES + [3 * ps - 1, 3 * ps, 3 * ps + 1], 8, 2, dim, ps, seed=ps).check()
 
 
-@pytest.mark.parametrize("lens", [[1], [7], [64 * 9], [20011], [1, 9001, 3, 1], [700] * 40])
+@pytest.mark.parametrize("lens", [[1], [7], [64 * 9], [20011], [1, 9001, 3, 1], [700] * 40, [5] * 33 + [900], [3, 0, 70] * 230, [1, 2] * 1024],
+                         ids=lambda x: f"{len(x)} of {x[0]}")
 def test_long_short_and_many(gpu, lens):
     Case(lens, 8, 2, 128, 32, seed=len(lens)).check()
 
@@ -198,8 +199,11 @@ def test_rows_past_two_to_the_31(gpu):
 
 def test_refusals(gpu):
     E = abi.CODES
-    for ids in ([0, 99, 1], [0, -1, 1], [1, 0, 1]):
-        c = Case([20, 30, 40], 4, 2, 64, 16)
+    for ids in ([0, 99, 1], [0, -1, 1], [1, 0, 1], list(range(38)) + [40], list(range(38)) + [99999], [3] + list(range(38))):
+        c = Case([20, 30, 40] if len(ids) == 3 else [20] * 39, 4, 2, 64, 16, unlisted=1)
+        if ids[-1] == 40:
+            c.glens[40 - 1] = 1000                           # (longer than its table row)
+            ids = ids[:-1] + [39]
         assert c.run(ids=i32(ids)) == 0
         assert int(c.status.item()) == E["TV_E_SEQ"]
         assert (host(c.out) == 77).all() and np.array_equal(host(c.gk), c.k) and np.array_equal(host(c.gv), c.v)

@@ -91,7 +91,7 @@ def test_attend_paged_host_checks():
                  dict(n=0), dict(hq=0), dict(q=FAKE + 2), dict(out=FAKE + 8), dict(k=FAKE + 2), dict(v=FAKE + 2), dict(qs=516), dict(qs=504),
                  dict(kvs=132), dict(kvs=120), dict(pool=_pool(k=None)), dict(seqs=_seqs(lens=None))):
         assert call(**over) == E["TV_E_ARG"], over
-    for over in (dict(n=4097), dict(hq=9), dict(pool=_pool(head_dim=96)), dict(pool=_pool(page_size=20))):
+    for over in (dict(n=4097), dict(n=2049), dict(hq=9), dict(pool=_pool(head_dim=96)), dict(pool=_pool(page_size=20))):
         assert call(**over) == E["TV_E_UNSUPPORTED"], over
     for over in (dict(wsb=need - 1), dict(ws=None), dict(ws=FAKE + 8)):
         assert call(**over) == E["TV_E_WORKSPACE"], over
