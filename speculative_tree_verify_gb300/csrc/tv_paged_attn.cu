@@ -490,10 +490,14 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           for (int w = 0; w < kCompWarps; ++w) M = fmaxf(M, s_ml[w * kRows + g8 + 8 * half].x);
           const float mine = half ? m1 : m0;
           const float f = mine == -INFINITY ? 0.f : ex2f(mine - M);
+          // row r: groups of 8 values XOR r, no bank twice
           float* dst = s_red + (warp * kRedRows + (g8 & 3)) * D + 2 * t4;
+          float* at[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) at[k] = dst + ((8 * k) ^ ((g8 & 3) * 8));
 #pragma unroll
           for (int k = 0; k < 2 * KS; ++k)
-            *reinterpret_cast<float2*>(dst + 8 * k) = make_float2(o[k][2 * half] * f, o[k][2 * half + 1] * f);
+            *reinterpret_cast<float2*>(at[k & 3] + 32 * (k >> 2)) = make_float2(o[k][2 * half] * f, o[k][2 * half + 1] * f);
         }
         comp_sync();
         for (int e = tid; e < kRedRows * (D / 2); e += kCompThreads) {
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             for (int w = 0; w < kCompWarps; ++w) {
               const float2 ml = s_ml[w * kRows + row];
               Ls += ml.x == -INFINITY ? ml.y : ml.y * ex2f(ml.x - M2);
-              const float2 v = *reinterpret_cast<const float2*>(s_red + (w * kRedRows + r) * D + d);
+              const float2 v = *reinterpret_cast<const float2*>(s_red + (w * kRedRows + r) * D + (d ^ (r * 8)));
               acc.x += v.x;
               acc.y += v.y;
             }
@@ -543,6 +547,14 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PaPara
   const int c0 = blockIdx.x, np = cut.z - c0 + 1, r0 = (cut.y % p.HB) * kRows, nr = min(kRows, p.G - r0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto slot = [&](int c) { return (size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0); };
+  auto partial = [&](int e, int c) {
+    return __ldcg(reinterpret_cast<const float2*>(p.ws.o + (slot(c) * kRows + e / (D / 2)) * D + 2 * (e % (D / 2))));
+  };
+  constexpr int kEarly = 16;   // partials asked for before the weights are known
+  float2 v[kEarly];
+#pragma unroll
+  for (int c = 0; c < kEarly; ++c)
+    v[c] = threadIdx.x < nr * (D / 2) && c < np ? partial(threadIdx.x, c) : make_float2(0.f, 0.f);
   if (warp < nr) {
     float2 ml[kMaxCtas / 32];
     float M = -INFINITY, sum = 0.f;
@@ -568,13 +580,19 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PaPara
   for (int e = threadIdx.x; e < nr * (D / 2); e += kMergeThreads) {
     const int row = e / (D / 2), d = 2 * (e % (D / 2));
     float2 acc = make_float2(0.f, 0.f);
-#pragma unroll 8
-    for (int c = 0; c < np; ++c) {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ws.o + (slot(c) * kRows + row) * D + d));
-      const float w = s_w[row][c];
-      acc.x = fmaf(v.x, w, acc.x);
-      acc.y = fmaf(v.y, w, acc.y);
+    auto add = [&](float2 x, float w) {
+      acc.x = fmaf(x.x, w, acc.x);
+      acc.y = fmaf(x.y, w, acc.y);
+    };
+    int c = 0;
+    if (e < kMergeThreads) {
+#pragma unroll
+      for (int u = 0; u < kEarly; ++u)
+        if (u < np) add(v[u], s_w[row][u]);
+      c = kEarly;
     }
+#pragma unroll 8
+    for (; c < np; ++c) add(partial(e, c), s_w[row][c]);
     *reinterpret_cast<__nv_bfloat162*>(p.out + ((size_t)cut.x * p.Hq + (cut.y / p.HB) * p.G + r0 + row) * D + d) =
         __floats2bfloat162_rn(acc.x, acc.y);
   }

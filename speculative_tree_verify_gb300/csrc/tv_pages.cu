@@ -7,9 +7,9 @@
 // lowest index first, which is found by scanning the counts (4 bytes a page,
 // from L2), so the outcome is a function of the state alone.
 //
-// Every bookkeeping call checks its whole list before it changes anything: a
-// first kernel looks (one block per listed sequence, or one block for all),
-// the next ones act only while the status word is zero.
+// Every bookkeeping call checks its whole list before it changes anything: for
+// short lists one block looks, meets and acts; for long ones a first kernel
+// looks and the next act only while the status word is zero.
 #include "tv_kernels.cuh"
 #include "tv_pages.cuh"
 
@@ -113,6 +113,76 @@ __global__ void __launch_bounds__(kListThreads) fork_kernel(tv_pool pool, tv_seq
   if (threadIdx.x == 0) t.lens[d] = len;
 }
 
+// Releasing (FORK = false: a = ids, b = keep) or forking (a = src, b = dst) by
+// one block: a warp for kSlice table entries of one listed sequence, which it
+// holds in registers between the look and the act.  Such a call is a chain of
+// dependent loads (list, length and entries, counts) and its launches.
+constexpr int kBlockThreads = 1024;
+constexpr int kSlice = 512;
+inline int n_slices(const tv_seqs& t) { return (t.max_pages + kSlice - 1) / kSlice; }
+
+template <bool FORK>
+__global__ void __launch_bounds__(kBlockThreads) list_block_kernel(tv_pool pool, tv_seqs t, const int32_t* a,
+                                                                   const int32_t* b, int n, int slices, int32_t* status) {
+  const int lane = threadIdx.x & 31, item = threadIdx.x >> 5, ps = pool.page_size;
+  const int i = item / slices, j0 = (item % slices) * kSlice + lane;
+  pdl_wait();
+  pdl_trigger();
+  const bool skip = status_get(status) != 0;
+  int bad = 0, s = 0, d = 0, len = 0, first = 0, last = 0;
+  int e[kSlice / 32];
+  if (i < n) {
+    s = __ldg(a + i);
+    d = __ldg(b + i);   // forking: the target row; releasing: the tokens kept
+    if (s < 0 || s >= t.max_seqs || (FORK && (d < 0 || d >= t.max_seqs))) {
+      bad = TV_E_SEQ;
+    } else {
+      const int32_t* row = t.pages + (size_t)s * t.max_pages;
+#pragma unroll
+      for (int k = 0; k < kSlice / 32; ++k)   // with the length on its way
+        if (j0 + 32 * k < t.max_pages) e[k] = __ldcg(row + j0 + 32 * k);
+      len = seq_len(t, ps, s);
+      if (len < 0 || (FORK ? __ldcg(t.lens + d) != 0 : d < 0 || d > len)) bad = TV_E_SEQ;
+    }
+    if (!bad) {
+      first = FORK ? 0 : pages_of(d, ps);
+      last = pages_of(len, ps);
+#pragma unroll
+      for (int k = 0; k < kSlice / 32; ++k) {
+        const int j = j0 + 32 * k;
+        if (j >= first && j < last && (e[k] < 0 || e[k] >= pool.n_pages || __ldcg(pool.refs + e[k]) < 1)) bad = TV_E_PAGE;
+      }
+    }
+  }
+  // no row listed twice; forking: no target among the sources (n <= 32: a lane a sequence)
+  if (item == 0) {
+    const int sa = lane < n ? __ldg(a + lane) : -1 - lane, sb = lane < n ? __ldg(b + lane) : -1 - lane;
+    const bool twice = __popc(__match_any_sync(0xffffffffu, FORK ? sb : sa)) > 1;
+    bool among = false;
+    for (int k = 0; k < n; ++k) among = among | (sb == __shfl_sync(0xffffffffu, sa, k));
+    if (lane < n && (twice || (FORK && among))) bad = TV_E_SEQ;
+  }
+  if (bad && !skip) status_set(status, bad);
+  if (__syncthreads_or(bad) || skip || i >= n) return;
+  int32_t* to = t.pages + (size_t)d * t.max_pages;
+#pragma unroll
+  for (int k = 0; k < kSlice / 32; ++k) {
+    const int j = j0 + 32 * k;
+    if (j >= first && j < last) {
+      if (FORK) {
+        to[j] = e[k];
+        atomicAdd(pool.refs + e[k], 1);
+      } else {
+        atomicSub(pool.refs + e[k], 1);
+      }
+    }
+  }
+  if (item % slices == 0 && lane == 0) t.lens[FORK ? d : s] = FORK ? len : d;
+}
+
+// one block when its 32 warps hold every entry the list can name
+inline bool one_block(const tv_seqs& t, int n) { return (long long)n * n_slices(t) <= kBlockThreads / 32; }
+
 // ---- extending -----------------------------------------------------------------
 // exclusive sum over the block's threads; *total = the sum of all
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
@@ -147,89 +217,40 @@ struct ExtendWs {
 // page is copied, so that the new tokens' rows go into a page of its own.  In
 // list order the last holder of a page keeps it, which with m listed holders of
 // a page with r references means: all m copy, except that the last in the list
-// keeps it when m = r.
+// keeps it when m = r.  The holders of a page are counted by comparing along
+// the list in shared memory (n comparisons for each listed holder of a shared
+// page, 4 at a time).
+//
+// The call is a chain of dependent loads (list, length, last entry, its count)
+// beside which the first counts are already on their way for the search of
+// free pages; nothing is written before the last check.
+struct ExtendSmem {   // of n listed sequences, and a mark for every table row
+  int *last, *off, *row, *len;
+  uint32_t* mark;
+  static size_t bytes(int n, int max_seqs) { return (size_t)((n + 3) & ~3) * 16 + (size_t)((max_seqs + 127) / 128) * 16; }
+};
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(tv_pool pool, tv_seqs t, const int32_t* ids,
                                                                    const int32_t* add, int n, ExtendWs ws,
                                                                    int32_t* status) {
-  __shared__ int s_last[kMaxListed];        // shared partly filled page of listed sequence i, or -1
-  __shared__ int s_off[kMaxListed];         // its need, then the offset of its new pages; bit 30: it copies
-  __shared__ uint32_t s_mark[kMaxSeqs / 32];
+  extern __shared__ __align__(16) int s_dyn[];
   __shared__ int s_warp[32];
   __shared__ uint32_t s_bad;
   __shared__ unsigned long long s_need;     // pages needed in all
   constexpr int kCow = 1 << 30;
-  const int tid = threadIdx.x, ps = pool.page_size;
+  const int tid = threadIdx.x, ps = pool.page_size, n4 = (n + 3) & ~3;
+  ExtendSmem sm;
+  sm.last = s_dyn;              // shared partly filled page of listed sequence i, or -1
+  sm.off = s_dyn + n4;          // its need, then the offset of its new pages; bit 30: it copies
+  sm.row = s_dyn + 2 * n4;      // its table row
+  sm.len = s_dyn + 3 * n4;      // its length
+  sm.mark = reinterpret_cast<uint32_t*>(s_dyn + 4 * n4);
+  for (int i = tid; i < (t.max_seqs + 31) / 32; i += kPlanThreads) sm.mark[i] = 0u;
+  if (tid == 0) s_bad = 0u, s_need = 0;
+  if (tid < n4 - n) sm.last[n + tid] = -1;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  if (block_skip(status)) return;
-  for (int i = tid; i < (t.max_seqs + 31) / 32; i += kPlanThreads) s_mark[i] = 0u;
-  if (tid == 0) s_bad = 0, s_need = 0;
-  __syncthreads();
-  for (int i = tid; i < n; i += kPlanThreads) {
-    const int s = ids[i], a = add[i];
-    uint32_t bad = 0u;
-    int last = -1;
-    if (s < 0 || s >= t.max_seqs || (atomicOr(&s_mark[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u) {
-      bad = kBadSeq;
-    } else {
-      const int len = seq_len(t, ps, s);
-      if (len < 0 || a < 0) bad = kBadSeq;
-      else if (a > t.max_pages * ps - len) bad = kBadCapacity;
-      else if (a > 0 && len % ps != 0) {
-        const int p = __ldcg(t.pages + (size_t)s * t.max_pages + len / ps);
-        const int r = p >= 0 && p < pool.n_pages ? __ldcg(pool.refs + p) : 0;
-        if (r < 1) bad = kBadPage;
-        else if (r > 1) last = p;
-      }
-    }
-    s_last[i] = last;
-    if (bad) atomicOr(&s_bad, bad);
-  }
-  __syncthreads();
-  if (s_bad) {
-    if (tid == 0) status_set(status, bad_code(s_bad));
-    return;
-  }
-  // the listed holders of a shared page give it up ...
-  for (int i = tid; i < n; i += kPlanThreads)
-    if (s_last[i] >= 0) atomicSub(pool.refs + s_last[i], 1);
-  __threadfence();
-  __syncthreads();
-  // ... and where none is left, the last of them in the list takes it back
-  for (int i = tid; i < n; i += kPlanThreads) {
-    const int len = __ldcg(t.lens + ids[i]);
-    int need = pages_of(len + add[i], ps) - pages_of(len, ps);   // below 2^28: a table row holds 2^31 - 1 tokens
-    const int p = s_last[i];
-    bool cow = false;
-    if (p >= 0) {
-      const int left = __ldcg(pool.refs + p);
-      if (left < 0) atomicOr(&s_bad, kBadPage);   // more holders than references
-      cow = left > 0;
-      for (int j = i + 1; j < n && !cow; ++j) cow = s_last[j] == p;
-      need += cow;
-    }
-    atomicAdd(&s_need, (unsigned long long)need);
-    s_off[i] = need | (cow ? kCow : 0);
-  }
-  __syncthreads();
-  for (int i = tid; i < n; i += kPlanThreads)
-    if (s_last[i] >= 0 && !(s_off[i] & kCow)) atomicAdd(pool.refs + s_last[i], 1);
-  __threadfence();
-  __syncthreads();
-  const bool fits = !s_bad && s_need <= (unsigned long long)pool.n_pages;
-  const int total = fits ? (int)s_need : 0;
-  int carry = 0;
-  for (int i0 = 0; i0 < n && fits; i0 += kPlanThreads) {   // needs -> offsets
-    const int i = i0 + tid;
-    const int v = i < n ? s_off[i] : 0;
-    int sum;
-    const int off = carry + block_scan(v & ~kCow, s_warp, &sum);
-    if (i < n) s_off[i] = off | (v & kCow);
-    carry += sum;
-  }
-  // the lowest free pages, in order
-  int found = 0;
-  for (int p0 = 0; p0 < pool.n_pages && found < total; p0 += 4 * kPlanThreads) {
+  auto counts = [&](int p0) {   // of pages p0 + 4 tid .. + 3; past the pool: held
     const int p = p0 + 4 * tid;
     int4 r = make_int4(1, 1, 1, 1);
     if (p + 3 < pool.n_pages) {
@@ -239,6 +260,73 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(tv_pool pool,
       if (p + 1 < pool.n_pages) r.y = __ldcg(pool.refs + p + 1);
       if (p + 2 < pool.n_pages) r.z = __ldcg(pool.refs + p + 2);
     }
+    return r;
+  };
+  const int skip = status_get(status);
+  int4 r = counts(0);
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const int s = __ldg(ids + i), a = __ldg(add + i);
+    uint32_t bad = 0u;
+    int last = -1, len = 0;
+    if (s < 0 || s >= t.max_seqs || (atomicOr(&sm.mark[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u) {
+      bad = kBadSeq;
+    } else {
+      len = seq_len(t, ps, s);
+      if (len < 0 || a < 0) bad = kBadSeq;
+      else if (a > t.max_pages * ps - len) bad = kBadCapacity;
+      else if (a > 0 && len % ps != 0) {
+        const int p = __ldcg(t.pages + (size_t)s * t.max_pages + len / ps);
+        const int held = p >= 0 && p < pool.n_pages ? __ldcg(pool.refs + p) : 0;
+        if (held < 1) bad = kBadPage;
+        else if (held > 1) last = p;
+      }
+    }
+    sm.last[i] = last;
+    sm.row[i] = s;
+    sm.len[i] = len;
+    if (bad) atomicOr(&s_bad, bad);
+  }
+  __syncthreads();
+  for (int i = tid; i < n && !s_bad; i += kPlanThreads) {
+    const int len = sm.len[i], p = sm.last[i];
+    int need = pages_of(len + __ldg(add + i), ps) - pages_of(len, ps);   // below 2^28: a table row holds 2^31 - 1 tokens
+    bool cow = false;
+    if (p >= 0) {
+      int holders = 0, after = 0;
+      for (int k = 0; k < n4; k += 4) {
+        const int4 q = *reinterpret_cast<const int4*>(sm.last + k);
+        holders += (q.x == p) + (q.y == p) + (q.z == p) + (q.w == p);
+        after += (q.x == p && k > i) + (q.y == p && k + 1 > i) + (q.z == p && k + 2 > i) + (q.w == p && k + 3 > i);
+      }
+      const int held = __ldcg(pool.refs + p);
+      if (holders > held) atomicOr(&s_bad, kBadPage);   // more holders than references
+      cow = holders < held || after > 0;
+      need += cow;
+    }
+    atomicAdd(&s_need, (unsigned long long)need);
+    sm.off[i] = need | (cow ? kCow : 0);
+  }
+  __syncthreads();
+  if (s_bad || skip) {
+    if (tid == 0 && !skip) status_set(status, bad_code(s_bad));
+    return;
+  }
+  const bool fits = s_need <= (unsigned long long)pool.n_pages;
+  const int total = fits ? (int)s_need : 0;
+  int carry = 0;
+  for (int i0 = 0; i0 < n && total > 0; i0 += kPlanThreads) {   // needs -> offsets
+    const int i = i0 + tid;
+    const int v = i < n ? sm.off[i] : 0;
+    int sum;
+    const int off = carry + block_scan(v & ~kCow, s_warp, &sum);
+    if (i < n) sm.off[i] = off | (v & kCow);
+    carry += sum;
+  }
+  // the lowest free pages, in order
+  int found = 0;
+  for (int p0 = 0; p0 < pool.n_pages && found < total; p0 += 4 * kPlanThreads) {
+    if (p0 > 0) r = counts(p0);
+    const int p = p0 + 4 * tid;
     int got;
     int at = found + block_scan((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), s_warp, &got);
     if (r.x == 0 && at < total) ws.free_list[at] = p;
@@ -250,11 +338,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(tv_pool pool,
     if (r.w == 0 && at < total) ws.free_list[at] = p + 3;
     found += got;
   }
-  if (!fits || total > found) {   // give back what was given up; nothing else has changed
-    __syncthreads();
-    for (int i = tid; i < n; i += kPlanThreads)
-      if (s_last[i] >= 0 && (s_off[i] & kCow)) atomicAdd(pool.refs + s_last[i], 1);
-    if (tid == 0) status_set(status, s_bad ? TV_E_PAGE : TV_E_CAPACITY);
+  if (!fits || total > found) {
+    if (tid == 0) status_set(status, TV_E_CAPACITY);
     return;
   }
   __syncthreads();
@@ -262,22 +347,21 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(tv_pool pool,
     int lo = 0, hi = n - 1;   // the last sequence whose first new page is at or before f
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((s_off[mid] & ~kCow) <= f) lo = mid;
+      if ((sm.off[mid] & ~kCow) <= f) lo = mid;
       else hi = mid - 1;
     }
-    const int s = ids[lo], k = f - (s_off[lo] & ~kCow), cow = (s_off[lo] & kCow) ? 1 : 0;
+    const int k = f - (sm.off[lo] & ~kCow), cow = (sm.off[lo] & kCow) ? 1 : 0;
     const int page = ws.free_list[f];
-    const int have = pages_of(__ldcg(t.lens + s), ps);
-    t.pages[(size_t)s * t.max_pages + have + k - cow] = page;
+    t.pages[(size_t)sm.row[lo] * t.max_pages + pages_of(sm.len[lo], ps) + k - cow] = page;
     pool.refs[page] = 1;
   }
   for (int i = tid; i < n; i += kPlanThreads) {
-    const bool cow = s_off[i] & kCow;
-    ws.pair[2 * i] = cow ? s_last[i] : -1;
-    ws.pair[2 * i + 1] = cow ? ws.free_list[s_off[i] & ~kCow] : -1;
+    const bool cow = total > 0 && (sm.off[i] & kCow);
+    ws.pair[2 * i] = cow ? sm.last[i] : -1;
+    ws.pair[2 * i + 1] = cow ? ws.free_list[sm.off[i] & ~kCow] : -1;
+    if (cow) atomicSub(pool.refs + sm.last[i], 1);
+    t.lens[sm.row[i]] = sm.len[i] + __ldg(add + i);
   }
-  __syncthreads();
-  for (int i = tid; i < n; i += kPlanThreads) t.lens[ids[i]] = __ldcg(t.lens + ids[i]) + add[i];
 }
 
 // One page of one layer's K or V is one contiguous block of memory.  bytes: a
@@ -562,6 +646,8 @@ int tv_pages_release(const tv_pool* pool, const tv_seqs* seqs, const int32_t* id
   if (!ids || !keep || !dev_status) return TV_E_ARG;
   if ((rc = check_listed(n))) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (one_block(*seqs, n))
+    return launch_pdl(list_block_kernel<false>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, ids, keep, n, n_slices(*seqs), dev_status);
   rc = launch_pdl(release_check_kernel, dim3(n), dim3(kListThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
   if (rc) return rc;
   return launch_pdl(release_kernel, dim3(n), dim3(kListThreads), 0, st, *pool, *seqs, ids, keep, dev_status);
@@ -574,6 +660,8 @@ int tv_pages_fork(const tv_pool* pool, const tv_seqs* seqs, const int32_t* src, 
   if (!src || !dst || !dev_status) return TV_E_ARG;
   if ((rc = check_listed(n))) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (one_block(*seqs, n))
+    return launch_pdl(list_block_kernel<true>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, src, dst, n, n_slices(*seqs), dev_status);
   rc = launch_pdl(fork_check_kernel, dim3(n), dim3(kListThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
   if (rc) return rc;
   return launch_pdl(fork_kernel, dim3(n), dim3(kListThreads), 0, st, *pool, *seqs, src, dst, dev_status);
@@ -591,7 +679,10 @@ int tv_pages_extend(const tv_pool* pool, const tv_seqs* seqs, const int32_t* ids
   ExtendWs ws;
   ws.free_list = reinterpret_cast<int32_t*>(w);
   ws.pair = reinterpret_cast<int32_t*>(w + 2 * align256((size_t)pool->n_pages * 4));
-  rc = launch_pdl(extend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, *pool, *seqs, ids, add, n, ws, dev_status);
+  static std::atomic<bool> attr[64];
+  if (ensure_smem_limit(extend_plan_kernel, ExtendSmem::bytes(kMaxListed, kMaxSeqs), attr)) return TV_E_CUDA;
+  rc = launch_pdl(extend_plan_kernel, dim3(1), dim3(kPlanThreads), ExtendSmem::bytes(n, seqs->max_seqs), st, *pool, *seqs, ids, add, n,
+                  ws, dev_status);
   if (rc) return rc;
   const int y = 2 * pool->n_layers < 65535 ? 2 * pool->n_layers : 65535;
   return launch_pdl(extend_copy_kernel, dim3(n, y), dim3(kListThreads), 0, st, *pool, ws, dev_status);
