@@ -6,6 +6,7 @@ arithmetic.
   DeviceRequest -- one request's KV cache and draft tree on the GPU
   RoundBuffers  -- every output and the workspace of one verify round
   run_round     -- verify -> accept -> commit through the C ABI on one stream
+  PagedCache    -- a paged KV cache: its pool, sequence table and workspaces
 """
 from __future__ import annotations
 
@@ -223,6 +224,89 @@ def run_round(model: DeviceModel, reqs: Sequence[DeviceRequest], b: RoundBuffers
     else:
         check(accept_residual(reqs, b, sampled, stream=stream), "tv_accept_residual")
         check(commit(reqs, b, stream), "tv_commit_kv")
+
+
+# ---------------------------------------------------------------------------
+# prompts and the paged cache (tv_attend_prompt, tv_pages_*, tv_attend_paged)
+# ---------------------------------------------------------------------------
+@dataclass
+class PagedCache:
+    """A pool of pages that many sequences share, their table, and the
+    workspaces and status word of the calls.  Lists (ids, add, ...) are int32
+    device tensors, one entry a sequence; rows of ``qkv`` hold the Q heads, the
+    K heads and the V heads of a token (a QKV projection's output)."""
+    dims: Dims
+    k: torch.Tensor        # [n_layers][n_pages][n_kv_heads][page_size][head_dim]
+    v: torch.Tensor
+    refs: torch.Tensor     # [n_pages]
+    pages: torch.Tensor    # [max_seqs][max_pages]
+    lens: torch.Tensor     # [max_seqs]
+    status: torch.Tensor
+    ws: torch.Tensor
+    attend_ws: torch.Tensor
+    pool: abi.TvPool
+    seqs: abi.TvSeqs
+
+    @classmethod
+    def alloc(cls, dims: Dims, n_layers: int, n_pages: int, page_size: int, max_seqs: int, max_pages: int,
+              device="cuda") -> "PagedCache":
+        shape = (n_layers, n_pages, dims.n_kv_heads, page_size, dims.head_dim)
+        k, v = (torch.empty(shape, device=device, dtype=torch.bfloat16) for _ in range(2))
+        i32 = dict(device=device, dtype=torch.int32)
+        refs, lens = torch.zeros(n_pages, **i32), torch.zeros(max_seqs, **i32)
+        pages = torch.full((max_seqs, max_pages), -1, **i32)
+        pool = abi.TvPool(k.data_ptr(), v.data_ptr(), refs.data_ptr(), n_layers, n_pages, dims.n_kv_heads, page_size,
+                          dims.head_dim)
+        seqs = abi.TvSeqs(pages.data_ptr(), lens.data_ptr(), max_seqs, max_pages)
+        bytes_ = (abi.tv_pages_workspace_size(pool, seqs),
+                  abi.tv_attend_paged_workspace_size(pool, dims.n_q_heads, min(max_seqs, 2048)))
+        ws, attend_ws = (torch.empty(b, device=device, dtype=torch.uint8) for b in bytes_)
+        return cls(dims, k, v, refs, pages, lens, torch.zeros(1, **i32), ws, attend_ws, pool, seqs)
+
+    def _heads(self, qkv: torch.Tensor):
+        q = self.dims.n_q_heads * self.dims.head_dim
+        return qkv, qkv[:, q:], qkv[:, q + self.dims.n_kv_heads * self.dims.head_dim:]
+
+    def extend(self, ids, add, stream=None) -> int:
+        return abi.tv_pages_extend(self.pool, self.seqs, ids, add, ids.numel(), self.ws, self.ws.numel(), self.status,
+                                   stream)
+
+    def fork(self, src, dst, stream=None) -> int:
+        return abi.tv_pages_fork(self.pool, self.seqs, src, dst, src.numel(), self.status, stream)
+
+    def release(self, ids, keep, stream=None) -> int:
+        return abi.tv_pages_release(self.pool, self.seqs, ids, keep, ids.numel(), self.status, stream)
+
+    def compact(self, remap, n_used, stream=None) -> int:
+        return abi.tv_pages_compact(self.pool, self.seqs, remap, n_used, self.ws, self.ws.numel(), self.status, stream)
+
+    def write(self, layer: int, ids, pos, starts, qkv: torch.Tensor, stream=None) -> int:
+        """Rows of a projection into the pages of the sequences they belong to."""
+        _, k, v = self._heads(qkv)
+        return abi.tv_pages_write(self.pool, layer, self.seqs, ids, pos, starts, ids.numel(), qkv.shape[0], k, v,
+                                  qkv.stride(0), self.dims.head_dim, self.status, stream)
+
+    def read_into(self, layer: int, ids, pos, starts, rows: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> int:
+        """Tokens of one or more sequences into contiguous caches [n_kv_heads][capacity][head_dim]."""
+        return abi.tv_pages_read(self.pool, layer, self.seqs, ids, pos, starts, ids.numel(), rows, k, v, k.stride(1),
+                                 k.stride(0), self.status, stream)
+
+    def write_from(self, layer: int, ids, pos, starts, rows: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> int:
+        """The other way: rows of contiguous caches (a committed path) into pages."""
+        return abi.tv_pages_write(self.pool, layer, self.seqs, ids, pos, starts, ids.numel(), rows, k, v, k.stride(1),
+                                  k.stride(0), self.status, stream)
+
+    def attend_prompt(self, qkv: torch.Tensor, starts, out: torch.Tensor, stream=None) -> int:
+        q, k, v = self._heads(qkv)
+        return abi.tv_attend_prompt(self.dims.n_q_heads, self.dims.n_kv_heads, self.dims.head_dim, q, k, v,
+                                    qkv.stride(0), qkv.stride(0), starts, starts.numel() - 1, qkv.shape[0], out,
+                                    self.status, stream)
+
+    def attend(self, layer: int, ids, qkv: torch.Tensor, out: torch.Tensor, stream=None) -> int:
+        """One new token a sequence: its K and V into the page, its queries over the whole sequence."""
+        q, k, v = self._heads(qkv)
+        return abi.tv_attend_paged(self.pool, layer, self.seqs, ids, ids.numel(), self.dims.n_q_heads, q, qkv.stride(0),
+                                   k, v, qkv.stride(0), out, self.attend_ws, self.attend_ws.numel(), self.status, stream)
 
 
 # ---------------------------------------------------------------------------

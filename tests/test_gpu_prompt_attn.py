@@ -172,3 +172,97 @@ def test_the_same_bits_every_time(gpu):
     for _ in range(100):
         assert p.run() == 0
         assert torch.equal(p.out, first)
+
+
+def test_a_serving_run(gpu):
+    """Two prompts through attention into pages, tokens decoded, a sequence forked, drafts given back, the pool
+    compacted, and the paged sequence verified as a contiguous cache and its committed rows written back; every result
+    against the oracle on the rows that were put in."""
+    import oracle
+    from speculative_tree_verify_gb300 import device as dv
+    from speculative_tree_verify_gb300 import synth
+    d, ps, layers = synth.TINY, 16, 2
+    Hq, Hkv, D = d.n_q_heads, d.n_kv_heads, d.head_dim
+    rng = np.random.default_rng(11)
+    c = dv.PagedCache.alloc(d, layers, 24, ps, 5, 6)
+    c.k.fill_(float("nan"))
+    c.v.fill_(float("nan"))
+    rows_of = {0: [], 2: [], 3: []}              # what the oracle keeps: (k, v) of every token
+
+    def ok(rc, what):
+        dv.check(rc, what)
+        assert int(c.status.item()) == 0, (what, abi.STATUS.get(int(c.status.item())))
+
+    def rows(n):
+        x = bits(rng.standard_normal((n, (Hq + 2 * Hkv) * D)))
+        parts = x[:, :Hq * D].reshape(n, Hq, D), x[:, Hq * D:(Hq + Hkv) * D].reshape(n, Hkv, D), x[:, (Hq + Hkv) * D:].reshape(n, Hkv, D)
+        return dev(x).view(torch.bfloat16), parts
+
+    def kv(s):
+        return (bf16_to_f64(np.array([r[i] for r in rows_of[s]])) for i in (0, 1))
+
+    # prompts of 37 and 16 tokens in one pass
+    lens = [37, 16]
+    starts, ids = i32([0, 37, 53]), i32([2, 0])
+    x, (q, k, v) = rows(53)
+    out = torch.zeros(53, Hq, D, device="cuda", dtype=torch.bfloat16)
+    ok(c.attend_prompt(x, starts, out), "attend_prompt")
+    o, off = attend_prompt(bf16_to_f64(q), bf16_to_f64(k), bf16_to_f64(v), [0, 37, 53], True)
+    close(bf16_to_f64(host(out.view(torch.int16))), o, off, "prompts")
+    ok(c.extend(ids, i32(lens)), "extend")
+    for layer in range(layers):
+        ok(c.write(layer, ids, i32([0, 0]), starts, x), "write")
+    rows_of[2] = [(k[t], v[t]) for t in range(37)]
+    rows_of[0] = [(k[t], v[t]) for t in range(37, 53)]
+
+    def decode(seqs):
+        x, (q, k, v) = rows(len(seqs))
+        ids, out = i32(seqs), torch.zeros(len(seqs), Hq, D, device="cuda", dtype=torch.bfloat16)
+        ok(c.extend(ids, i32([1] * len(seqs))), "extend")
+        for layer in range(layers):
+            ok(c.attend(layer, ids, x, out), "attend")
+        for i, s in enumerate(seqs):
+            rows_of[s] = rows_of[s] + [(k[i], v[i])]
+            o, off = attend(bf16_to_f64(q[i]), *kv(s), True)
+            close(bf16_to_f64(host(out.view(torch.int16))[i]), o, off, f"token of sequence {s}")
+
+    for _ in range(3):
+        decode([0, 2])
+    ok(c.fork(i32([2]), i32([3])), "fork")
+    rows_of[3] = list(rows_of[2])
+    for _ in range(9):                            # the two part ways: over a page's end
+        decode([3, 0, 2])
+    ok(c.release(i32([3, 0]), i32([41, 0])), "release")
+    rows_of[3], rows_of[0] = rows_of[3][:41], []
+    remap, used = i32([0] * 24), i32([0])
+    ok(c.compact(remap, used), "compact")
+    held = c.refs.cpu().numpy()
+    assert (held[:int(used.item())] > 0).all() and not held[int(used.item()):].any()
+    decode([2, 3])
+    # sequence 3 as a contiguous cache under a tree verify, and its committed path back into pages
+    n, tree = len(rows_of[3]), synth.tree_spine_random(8, 4, d.vocab, 3)
+    model = synth.gen_model(d, 1, random_gains=True)
+    cache = synth.gen_cache(d, n, n + 16, 5)
+    gk, gv = (dev(getattr(cache, w)).view(torch.bfloat16) for w in "kv")
+    gk[:, :n] = 0
+    gv[:, :n] = 0
+    ok(c.read_into(1, i32([3]), i32([0]), i32([0, n]), n, gk, gv), "read")
+    for t, (a, b) in enumerate(rows_of[3]):
+        cache.k[:, t], cache.v[:, t] = a, b
+    assert np.array_equal(host(gk.view(torch.int16)), cache.k) and np.array_equal(host(gv.view(torch.int16)), cache.v)
+    req = dv.DeviceRequest(gk, gv, n, torch.from_numpy(tree.parent.copy()).cuda(), torch.from_numpy(tree.token.copy()).cuda())
+    b = dv.RoundBuffers.alloc(d, tree.n, 1, n)
+    dv.run_round(dv.DeviceModel.from_host(model), [req], b)
+    torch.cuda.synchronize()
+    assert int(b.status.item()) == 0
+    orc = oracle.verify_tree(model, cache, tree)
+    lg, ol = b.logits.cpu().numpy().astype(np.float64), orc["logits"].astype(np.float64)
+    assert (np.abs(lg - ol).max(1) <= 2e-2 * np.sqrt((ol * ol).mean(1))).all()
+    more = int(b.new_ctx.item()) - n
+    assert more == int(b.accept_len.item()) + 1
+    ok(c.extend(i32([3]), i32([more])), "extend")
+    ok(c.write_from(1, i32([3]), i32([n]), i32([0, more]), more, gk[:, n:], gv[:, n:]), "write_from")
+    back = torch.zeros_like(gk), torch.zeros_like(gv)
+    ok(c.read_into(1, i32([3]), i32([0]), i32([0, n + more]), n + more, *back), "read")
+    for a, w in zip(back, (gk, gv)):
+        assert torch.equal(a[:, :n + more].view(torch.int16), w[:, :n + more].view(torch.int16))
