@@ -691,7 +691,7 @@ TV_API int tv_pages_read(const tv_pool *pool, int layer, const tv_seqs *seqs, co
  *             heads: the Q, K and V heads of a QKV projection's rows
  *   starts    device int32 [n_seqs + 1], ascending within 0 .. rows; a sequence may be empty
  *   rows      host: rows of q, k, v and out, >= 1
- *   out       device bf16 [rows][n_q_heads][head_dim], 16-byte aligned; may not overlap the inputs
+ *   out       device bf16 [rows][n_q_heads][head_dim], 32-byte aligned; may not overlap the inputs
  * head_dim 64 or 128, n_q_heads a multiple of n_kv_heads with at most 128 query
  * heads a KV head, at most 4096 sequences (else TV_E_UNSUPPORTED).  P is
  * rounded to bf16 for the product with V, everything else is fp32.  What a row

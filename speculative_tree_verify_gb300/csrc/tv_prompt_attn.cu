@@ -41,22 +41,27 @@ namespace {
 
 constexpr int kPrSoftWarps = 16;                 // 8 a query tile
 constexpr int kPrSoftThreads = kPrSoftWarps * 32;
-constexpr int kWarpMma = kPrSoftWarps, kWarpTma = kPrSoftWarps + 1;
-constexpr int kPrThreads = kPrSoftThreads + 64;
+constexpr int kWarpMma = kPrSoftWarps, kWarpTma = kPrSoftWarps + 1, kWarpPlan = kPrSoftWarps + 2;
+constexpr int kPrThreads = kPrSoftThreads + 128;  // a whole warpgroup for the four roles' registers
+// 640 threads of 96 registers at launch; 512 x 104 + 128 x 64 is the same sum
+constexpr int kSoftRegs = 104, kRoleRegs = 64;
+static_assert(kPrSoftThreads * kSoftRegs + 128 * kRoleRegs <= kPrThreads * 96, "registers of the launch");
 constexpr int kAtomP = 128 * 128;                // bytes of a 128-row x 128-byte swizzled slab
 constexpr float kMoveSum = 256.f;                // an offset moves when 64 keys' exponentials add up to more
 
 template <int D>
 struct PrSmem {
   static constexpr int TILE = (D / 64) * kAtomP;   // 128 rows
-  static constexpr int OFF_Q = 0;                  // two tiles; the listed sequences' CTA counts first
+  static constexpr int OFF_Q = 0;                  // two tiles
   static constexpr int OFF_K = 2 * TILE;           // two stages
   static constexpr int OFF_V = OFF_K + 2 * TILE;   // two stages
-  static constexpr int OFF_BAD = OFF_V + 2 * TILE; // [3][D] first key whose V is NaN, +inf, -inf
-  static constexpr int OFF_TOP = OFF_BAD + 3 * D * 4;   // [2 tiles][2 halves][128 rows] maxima; sums at the end
-  static constexpr int OFF_BAR = OFF_TOP + 2 * 2 * 128 * 4;
+  static constexpr int OFF_CNT = OFF_V + 2 * TILE; // tile pairs of every sequence, where there are more than 32
+  static constexpr int OFF_BAD = OFF_CNT + kMaxListed * 4;   // [2 places][3][D] first key whose V is NaN, +inf, -inf
+  static constexpr int OFF_TOP = OFF_BAD + 2 * 3 * D * 8;    // [2 tiles][2 halves][128 rows] maxima
+  static constexpr int OFF_SUM = OFF_TOP + 2 * 2 * 128 * 4;  // and sums
+  static constexpr int OFF_BAR = OFF_SUM + 2 * 2 * 128 * 4;
   static constexpr size_t BYTES = 1024 + OFF_BAR + 256;
-  static_assert(2 * TILE >= kMaxListed * 4, "a count for every listed sequence");
+  static_assert(BYTES <= 232448 - 256, "shared memory of one CTA");
 };
 
 struct PrParams {
@@ -194,9 +199,43 @@ __device__ __forceinline__ void commit_by(uint64_t* bar, uint32_t leader) {
       : "memory");
 }
 
-// 1-D grid: KV heads fastest, then the CTAs' places ordered by the tile index
-// inside their sequence, highest first (the longest rows start first, so that
-// what is left at the end is short).
+// ---- cluster launch control: the index of a CTA that has not started, whose
+// work this CTA takes over (16 bytes written to shared memory, counted on the
+// barrier)
+__device__ __forceinline__ void clc_ask(void* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// -1: every CTA has started
+__device__ __forceinline__ int clc_answer(const void* answer) {
+  uint32_t x, got;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "mov.b32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, h;\n\t}"
+      : "=r"(x), "=r"(got)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return got ? (int)x : -1;
+}
+
+// 32 bytes of one thread, one sector
+__device__ __forceinline__ void store32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// 1-D grid: KV heads fastest, then the places ordered by the tile index inside
+// their sequence, highest first (the longest rows start first, so that what is
+// left at the end is short).  A CTA that has issued its work's last loads asks for
+// the place of one that has not started, so that the next queries, keys and
+// first products are under way while it writes its output; set-up is paid once
+// an SM.
 template <int D>
 __global__ void __launch_bounds__(kPrThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -204,28 +243,35 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   using L = PrSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  int* s_bad = reinterpret_cast<int*>(smem + L::OFF_BAD);
+  unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(smem + L::OFF_BAD);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);   // [2] a query tile landed
-  uint64_t* k_full = q_full + 2;                                         // [2]
+  uint64_t* q_free = q_full + 2;                                         // [2] its products are done
+  uint64_t* k_full = q_free + 2;                                         // [2]
   uint64_t* k_free = k_full + 2;                                         // [2] the products with it are done
   uint64_t* v_full = k_free + 2;                                         // [2]
   uint64_t* v_free = v_full + 2;                                         // [2]
   uint64_t* s_full = v_free + 2;                                         // [2] S_s done (and every product before it)
   uint64_t* p_full = s_full + 2;                                         // [2] P_s stored, O_s rescaled (8 warps)
   uint64_t* o_fin = p_full + 2;                                          // [2] the last product into O_s done
-  // a window's V looked over (16 warps): one barrier for even windows and one
-  // for odd, since the warps may be a window ahead of the products
+  // a window's V looked over (16 warps): two barriers in turn, since the warps
+  // may be a window ahead of the products
   uint64_t* v_ok = o_fin + 2;
-  uint64_t* drain = v_ok + 2;                                            // after a timeout: every product issued is done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  __shared__ int s_place[4];                                             // sequence, tile pair; -1: nothing to do
-  __shared__ int s_anybad;
+  uint64_t* w_full = v_ok + 2;                                           // [2] a place written down
+  uint64_t* w_free = w_full + 2;                                         // [2] every role has read it
+  uint64_t* drain = w_free + 2;                                          // after a timeout: every product issued is done
+  uint64_t* clc_bar = drain + 1;
+  uint64_t* want = clc_bar + 1;                                          // a place's last loads are issued
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(want + 1);
+  __shared__ __align__(16) uint4 s_clc;
+  __shared__ int4 s_work[2];        // row0, length, first token, KV head; length 0: no more
+  __shared__ unsigned s_anybad[2];  // the place (counted from 1) whose V held something not finite
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
+      mbar_init(&q_free[s], 1);
       mbar_init(&k_full[s], 1);
       mbar_init(&k_free[s], 1);
       mbar_init(&v_full[s], 1);
@@ -234,224 +280,311 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       mbar_init(&p_full[s], kPrSoftWarps / 2);
       mbar_init(&o_fin[s], 1);
       mbar_init(&v_ok[s], kPrSoftWarps);
+      mbar_init(&w_full[s], 1);
+      mbar_init(&w_free[s], kPrSoftWarps + 2);
+      s_anybad[s] = 0;
     }
     mbar_init(drain, 1);
+    mbar_init(clc_bar, 1);
+    mbar_init(want, 1);
     fence_mbar_init();
     prefetch_tmap(&map_q);
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
-    s_anybad = 0;
   }
-  for (int e = tid; e < 3 * D; e += kPrThreads) s_bad[e] = 0x7fffffff;
+  for (int e = tid; e < 2 * 3 * D; e += kPrThreads) s_bad[e] = ~0ull;
   if (warp == kWarpMma) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   pdl_wait();
   pdl_trigger();
+  const uint32_t tmem = *tmem_slot;
 
-  // ---- this CTA's place ------------------------------------------------------------
-  // c_i = ceil(len_i / 2T) tile pairs of sequence i; N(l) = sum_i max(0, c_i - l) of them have an index >= l
-  int* s_cnt = reinterpret_cast<int*>(smem + L::OFF_Q);
-  if (p.n > 32) {   // more than a warp's lanes hold
-    for (int i = tid; i < p.n; i += kPrThreads) {
-      const int a = __ldg(p.starts + i), b = __ldg(p.starts + i + 1);
-      s_cnt[i] = a < 0 || b < a || b > p.rows ? -1 : (b - a + 2 * p.T - 1) / (2 * p.T);
-    }
-    fence_async_smem();   // the counts' shared memory is the query tiles'
-    __syncthreads();
-  }
-  if (warp == 0) {
+  // a place as every role sees it
+  struct Work {
+    int row0, len, t0, h;   // first row and length of the sequence, first token, KV head
+    int hi, nst, nwin, skip0;
+  };
+  auto read_work = [&](int it, bool ok) {   // again and again until free_work
+    Work w;
+    const int4 x = ok ? s_work[it & 1] : make_int4(0, 0, 0, 0);
+    w.row0 = __shfl_sync(0xffffffffu, x.x, 0);   // uniform values, and known to be
+    w.len = __shfl_sync(0xffffffffu, x.y, 0);
+    w.t0 = __shfl_sync(0xffffffffu, x.z, 0);
+    w.h = __shfl_sync(0xffffffffu, x.w, 0);
+    w.hi = min(w.len, w.t0 + 2 * p.T);                // one past the last key
+    w.nst = w.t0 + p.T < w.len ? 2 : 1;               // query tiles
+    w.nwin = (w.hi + 127) / 128;
+    w.skip0 = w.nst == 2 ? w.nwin - (w.t0 + p.T + 127) / 128 : 0;   // tile 0 sees nothing of the first window (0 or 1)
+    return w;
+  };
+  auto wait_work = [&](int it, bool& ok) {
+    if (ok && !mbar_wait(&w_full[it & 1], (uint32_t)(it >> 1) & 1u)) ok = false;
+  };
+  auto free_work = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&w_free[it & 1]);
+  };
+  auto w_start = [](const Work& k, int w) { return 128 * (k.nwin - 1 - w); };   // first key of window w, the last keys first
+  // window w holds keys that a row may not see (so does the first, if only as a rule)
+  auto scrub = [&](const Work& k, int w) { return w == 0 || w_start(k, w) + 127 > k.t0; };
+
+  if (warp >= kPrSoftWarps) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
+  if (warp == kWarpPlan) {
+    // ---------------- places ----------------
+    // c_i = ceil(len_i / 2T) tile pairs of sequence i; N(l) = sum_i max(0, c_i - l) of them have an index >= l
+    int* s_cnt = reinterpret_cast<int*>(smem + L::OFF_CNT);
     int a = 0, b = 0, mine = 0;   // n <= 32: the lane's sequence
-    if (p.n <= 32 && lane < p.n) {
-      a = __ldg(p.starts + lane);
-      b = __ldg(p.starts + lane + 1);
-      mine = a < 0 || b < a || b > p.rows ? -1 : (b - a + 2 * p.T - 1) / (2 * p.T);
-    }
+    auto count = [&](int x, int y) { return x < 0 || y < x || y > p.rows ? -1 : (y - x + 2 * p.T - 1) / (2 * p.T); };
     const bool stop = status_get(p.status) != 0;
-    auto each = [&](auto&& use) {   // this lane's counts
-      if (p.n <= 32) use(mine);
-      else
-        for (int i = lane; i < p.n; i += 32) use(s_cnt[i]);
-    };
     int top = 0, low = 0;
-    each([&](int c) { top = max(top, c), low = min(low, c); });
+    for (int i = lane; i < p.n; i += 32) {
+      a = __ldg(p.starts + i);
+      b = __ldg(p.starts + i + 1);
+      mine = count(a, b);
+      if (p.n > 32) s_cnt[i] = mine;
+      top = max(top, mine);
+      low = min(low, mine);
+    }
+    __syncwarp();
     top = __reduce_max_sync(0xffffffffu, top);
     const bool bad = __any_sync(0xffffffffu, low < 0);
     if (bad && !stop && lane == 0) status_set(p.status, TV_E_SEQ);
     auto at_least = [&](int l) {   // N(l)
       int x = 0;
-      each([&](int c) { x += max(0, c - l); });
+      if (p.n <= 32) x = max(0, mine - l);
+      else
+        for (int i = lane; i < p.n; i += 32) x += max(0, s_cnt[i] - l);
       return __reduce_add_sync(0xffffffffu, x);
     };
-    const int place = blockIdx.x / p.Hkv;
-    int found = -1, lo = 0;
-    if (p.n == 1) {   // one sequence: its pairs from the last to the first
-      lo = top - 1 - place;
-      found = !stop && !bad && lo >= 0 ? 0 : -1;
-    } else if (!stop && !bad && at_least(0) > place) {
-      int hi = top;   // the largest l with N(l) > place; N(top) = 0
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (at_least(mid) > place) lo = mid;
-        else hi = mid;
-      }
-      int k = place - at_least(lo + 1);   // the k-th sequence with more than lo pairs
-      for (int i0 = 0; i0 < p.n; i0 += 32) {
-        const int i = i0 + lane;
-        const unsigned m = __ballot_sync(0xffffffffu, i < p.n && (p.n <= 32 ? mine : s_cnt[i]) > lo);
-        if (k < __popc(m)) {
-          const unsigned at = __ballot_sync(0xffffffffu, (m >> lane & 1u) && __popc(m & ((1u << lane) - 1u)) == k);
-          found = i0 + __ffs(at) - 1;
-          break;
+    const int all = stop || bad ? 0 : at_least(0);
+    auto find = [&](int block) {   // {row0, length, first token, KV head} of a block's place, length 0: none
+      const int place = block / p.Hkv;
+      int found = -1, lo = 0, fa = a, fb = b;
+      if (p.n == 1) {   // one sequence: its pairs from the last to the first
+        lo = top - 1 - place;
+        if (place < all) found = 0;
+      } else if (place < all) {
+        int hi = top;   // the largest l with N(l) > place; N(top) = 0
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (at_least(mid) > place) lo = mid;
+          else hi = mid;
         }
-        k -= __popc(m);
+        int k = place - at_least(lo + 1);   // the k-th sequence with more than lo pairs
+        for (int i0 = 0; i0 < p.n; i0 += 32) {
+          const int i = i0 + lane;
+          const unsigned m = __ballot_sync(0xffffffffu, i < p.n && (p.n <= 32 ? mine : s_cnt[i]) > lo);
+          if (k < __popc(m)) {
+            const unsigned at = __ballot_sync(0xffffffffu, (m >> lane & 1u) && __popc(m & ((1u << lane) - 1u)) == k);
+            found = i0 + __ffs(at) - 1;
+            break;
+          }
+          k -= __popc(m);
+        }
       }
-    }
-    if (p.n <= 32) {
-      a = __shfl_sync(0xffffffffu, a, found & 31);
-      b = __shfl_sync(0xffffffffu, b, found & 31);
-    } else if (found >= 0) {
-      a = __ldg(p.starts + found);
-      b = __ldg(p.starts + found + 1);
-    }
-    if (lane == 0) {
-      s_place[0] = found;
-      s_place[1] = lo;
-      s_place[2] = a;
-      s_place[3] = b;
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int seq = __shfl_sync(0xffffffffu, s_place[0], 0);   // uniform values, and known to be
-  if (seq >= 0) {
-    const int row0 = __shfl_sync(0xffffffffu, s_place[2], 0);
-    const int len = __shfl_sync(0xffffffffu, s_place[3], 0) - row0;
-    const int h = blockIdx.x % p.Hkv;
-    const int t0 = __shfl_sync(0xffffffffu, s_place[1], 0) * 2 * p.T;
-    const int hi = min(len, t0 + 2 * p.T);            // one past the last key
-    const int nst = t0 + p.T < len ? 2 : 1;            // query tiles
-    const int nwin = (hi + 127) / 128;
-    const int skip0 = nst == 2 ? nwin - (t0 + p.T + 127) / 128 : 0;   // tile 0 sees nothing of the first window (0 or 1)
-    auto w_start = [&](int w) { return 128 * (nwin - 1 - w); };   // first key of window w
-    auto scrub = [&](int w) { return w_start(w) + 127 > t0; };   // holds keys that a row may not see
-    const uint32_t tS = tmem, tO = tmem + 256;
-
-    if (warp == kWarpTma) {
+      if (p.n <= 32) {
+        fa = __shfl_sync(0xffffffffu, a, found & 31);
+        fb = __shfl_sync(0xffffffffu, b, found & 31);
+      } else if (found >= 0) {
+        fa = __ldg(p.starts + found);
+        fb = __ldg(p.starts + found + 1);
+      }
+      return found >= 0 ? make_int4(fa, fb - fa, lo * 2 * p.T, block % p.Hkv) : make_int4(0, 0, 0, 0);
+    };
+    bool ok = true;
+    int block = blockIdx.x;
+    for (int it = 0, asked = 0;; ) {
+      const int4 x = block >= 0 ? find(block) : make_int4(0, 0, 0, 0);
+      if (x.y > 0 || block < 0 || all == 0) {
+        if (it >= 2 && ok && !mbar_wait(&w_free[it & 1], (uint32_t)((it - 2) >> 1) & 1u)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          s_work[it & 1] = x;
+          mbar_arrive(&w_full[it & 1]);
+        }
+        __syncwarp();
+        ++it;
+        if (x.y == 0) break;
+        // not before this place's end is near: who is done first takes the next
+        ok = __all_sync(0xffffffffu, mbar_wait(want, (uint32_t)(it - 1) & 1u));
+        if (!ok) break;
+      }
       if (lane == 0) {
-        const uint32_t qbytes = (uint32_t)((D / 64) * p.T * p.G * 128);
-        bool ok = true;
-        auto load_kv = [&](const CUtensorMap* map, uint64_t* full, int off, int w) {
-          mbar_arrive_expect_tx(&full[w & 1], L::TILE);
+        fence_async_smem();   // the last answer was read through the generic proxy
+        mbar_arrive_expect_tx(clc_bar, 16);
+        clc_ask(&s_clc, clc_bar);
+      }
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, mbar_wait(clc_bar, (uint32_t)asked & 1u));
+      if (!ok) break;
+      block = __shfl_sync(0xffffffffu, clc_answer(&s_clc), 0);
+      ++asked;
+    }
+    if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
+  } else if (warp == kWarpTma) {
+    // ---------------- loads ----------------
+    const uint32_t qbytes = (uint32_t)((D / 64) * p.T * p.G * 128);
+    bool ok = true;
+    int kv = 0, nk = 0, nv = 0, nq[2] = {0, 0};   // windows before this place; loads issued
+    for (int it = 0;; ++it) {
+      wait_work(it, ok);
+      const Work k = read_work(it, ok);
+      free_work(it);
+      if (k.len == 0) break;
+      auto load_kv = [&](const CUtensorMap* map, uint64_t* full, uint64_t* free, int off, int w, int& issued) {
+        const int i = kv + w;
+        if (i >= 2) ok = ok && mbar_wait(&free[i & 1], (uint32_t)((i - 2) >> 1) & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[i & 1], L::TILE);
 #pragma unroll
           for (int a = 0; a < D / 64; ++a)
-            tma_load_3d(smem + off + (w & 1) * L::TILE + a * kAtomP, map, &full[w & 1], h * D + a * 64, 0, row0 + w_start(w));
-        };
-        auto load_q = [&](int s) {
+            tma_load_3d(smem + off + (i & 1) * L::TILE + a * kAtomP, map, &full[i & 1], k.h * D + a * 64, 0, k.row0 + w_start(k, w));
+        }
+        ++issued;
+      };
+      auto load_q = [&](int s) {
+        if (nq[s] > 0) ok = ok && mbar_wait(&q_free[s], (uint32_t)(nq[s] - 1) & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        if (lane == 0) {
           mbar_arrive_expect_tx(&q_full[s], qbytes);
 #pragma unroll
           for (int a = 0; a < D / 64; ++a)
-            tma_load_3d(smem + L::OFF_Q + s * L::TILE + a * kAtomP, &map_q, &q_full[s], a * 64, h * p.G, row0 + t0 + s * p.T);
-        };
-        load_kv(&map_k, k_full, L::OFF_K, 0);
-        load_q(0);
-        if (nst == 2) load_q(1);
-        load_kv(&map_v, v_full, L::OFF_V, 0);
-        int nk = 1, nv = 1;
-        for (int w = 1; w < nwin && ok; ++w) {
-          if (w >= 2) ok = mbar_wait(&k_free[w & 1], (uint32_t)((w - 2) >> 1) & 1u);
-          if (!ok) break;
-          load_kv(&map_k, k_full, L::OFF_K, w);
-          ++nk;
-          if (w >= 2) ok = mbar_wait(&v_free[w & 1], (uint32_t)((w - 2) >> 1) & 1u);
-          if (!ok) break;
-          load_kv(&map_v, v_full, L::OFF_V, w);
-          ++nv;
+            tma_load_3d(smem + L::OFF_Q + s * L::TILE + a * kAtomP, &map_q, &q_full[s], a * 64, k.h * p.G, k.row0 + k.t0 + s * p.T);
         }
-        if (!ok) status_set(p.status, TV_E_TIMEOUT);
-        // loads in flight land before the CTA leaves
-        for (int s = 0; s < nst; ++s) mbar_wait(&q_full[s], 0);
-        for (int w = nk > 2 ? nk - 2 : 0; w < nk; ++w) mbar_wait(&k_full[w & 1], (uint32_t)(w >> 1) & 1u);
-        for (int w = nv > 2 ? nv - 2 : 0; w < nv; ++w) mbar_wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u);
+        ++nq[s];
+      };
+      for (int w = 0; w < k.nwin && ok; ++w) {
+        load_kv(&map_k, k_full, k_free, L::OFF_K, w, nk);
+        if (w == 0 && ok) load_q(0);
+        if (w == 0 && ok && k.nst == 2) load_q(1);
+        if (ok) load_kv(&map_v, v_full, v_free, L::OFF_V, w, nv);
       }
-    } else if (warp == kWarpMma) {
-      const uint32_t leader = elect_one();
-      const uint32_t idesc_s = idesc_bf16_f32(128, 128);
-      const uint32_t idesc_o = idesc_bf16_f32(128, D) | (1u << 16);   // B = V: MN-major
-      const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint64_t dq = sdesc_sw128(base + L::OFF_Q, 16, 1024), dk = sdesc_sw128(base + L::OFF_K, 16, 1024);
-      const uint64_t dv = sdesc_sw128(base + L::OFF_V, kAtomP, 1024);
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
-      auto wait_k = [&](int w) { wait(&k_full[w & 1], (uint32_t)(w >> 1) & 1u); };
-      auto product_s = [&](int s, int w, bool first) {   // S_s = Q_s K_w^T; K_w has landed
-        if (first) wait(&q_full[s], 0);
+      if (!ok) break;
+      kv += k.nwin;
+      if (lane == 0) mbar_arrive(want);
+    }
+    if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
+    // loads in flight land before the CTA leaves
+    for (int s = 0; s < 2; ++s)
+      if (nq[s] > 0) mbar_wait(&q_full[s], (uint32_t)(nq[s] - 1) & 1u);
+    for (int i = nk > 2 ? nk - 2 : 0; i < nk; ++i) mbar_wait(&k_full[i & 1], (uint32_t)(i >> 1) & 1u);
+    for (int i = nv > 2 ? nv - 2 : 0; i < nv; ++i) mbar_wait(&v_full[i & 1], (uint32_t)(i >> 1) & 1u);
+  } else if (warp == kWarpMma) {
+    // ---------------- products ----------------
+    const uint32_t leader = elect_one();
+    const uint32_t idesc_s = idesc_bf16_f32(128, 128);
+    const uint32_t idesc_o = idesc_bf16_f32(128, D) | (1u << 16);   // B = V: MN-major
+    const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t dq = sdesc_sw128(base + L::OFF_Q, 16, 1024), dk = sdesc_sw128(base + L::OFF_K, 16, 1024);
+    const uint64_t dv = sdesc_sw128(base + L::OFF_V, kAtomP, 1024);
+    bool ok = true;
+    int kv = 0, looked = 0, np[2] = {0, 0}, nq[2] = {0, 0};   // windows, windows looked over, P and query tiles before this place
+    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u)); };
+    for (int it = 0;; ++it) {
+      wait_work(it, ok);
+      const Work k = read_work(it, ok);
+      free_work(it);
+      if (k.len == 0) break;
+      auto product_s = [&](int s, int w, int i, bool first) {   // S_s = Q_s K_w^T; K_w (the CTA's i-th window) has landed
+        if (first) wait(&q_full[s], (uint32_t)nq[s]++);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t a = dq + (uint64_t)(s * (L::TILE >> 4)), b = dk + (uint64_t)((w & 1) * (L::TILE >> 4));
+        const uint64_t a = dq + (uint64_t)(s * (L::TILE >> 4)), b = dk + (uint64_t)((i & 1) * (L::TILE >> 4));
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = (uint64_t)(((k >> 2) * kAtomP + (k & 3) * 32) >> 4);
-          umma_ss(tm + s * 128, a + off, b + off, idesc_s, k > 0 ? 1u : 0u, leader);
+        for (int c = 0; c < D / 16; ++c) {
+          const uint64_t off = (uint64_t)(((c >> 2) * kAtomP + (c & 3) * 32) >> 4);
+          umma_ss(tm + s * 128, a + off, b + off, idesc_s, c > 0 ? 1u : 0u, leader);
         }
         commit_by(&s_full[s], leader);
-        if (s == nst - 1) commit_by(&k_free[w & 1], leader);
+        if (s == k.nst - 1) commit_by(&k_free[i & 1], leader);
+        if (w == k.nwin - 1) commit_by(&q_free[s], leader);
       };
-      wait_k(0);
-      if (!skip0) product_s(0, 0, true);
-      if (nst == 2) product_s(1, 0, true);
-      for (int w = 0; w < nwin && ok; ++w) {
+      const int i0 = __shfl_sync(0xffffffffu, kv, 0);
+      wait(&k_full[i0 & 1], (uint32_t)(i0 >> 1));
+      if (!k.skip0) product_s(0, 0, i0, true);
+      if (k.nst == 2) product_s(1, 0, i0, true);
+      for (int w = 0; w < k.nwin && ok; ++w) {
+        const int i = __shfl_sync(0xffffffffu, kv + w, 0);   // uniform, and known to be
         // both loads before the first P: nothing between a P and its products then
-        wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u);
-        if (scrub(w)) wait(&v_ok[w & 1], (uint32_t)(w >> 1) & 1u);
-        if (w + 1 < nwin) wait_k(w + 1);
+        wait(&v_full[i & 1], (uint32_t)(i >> 1));
+        if (scrub(k, w)) {
+          wait(&v_ok[looked & 1], (uint32_t)(looked >> 1));
+          ++looked;
+        }
+        if (w + 1 < k.nwin) wait(&k_full[(i + 1) & 1], (uint32_t)((i + 1) >> 1));
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (s >= nst || !ok) break;
-          const int f = s == 0 ? skip0 : 0;
+          if (s >= k.nst || !ok) break;
+          const int f = s == 0 ? k.skip0 : 0;
           if (w >= f) {   // O_s += P_s V_w
-            wait(&p_full[s], (uint32_t)(w - f) & 1u);
+            wait(&p_full[s], (uint32_t)np[s]++);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t b = dv + (uint64_t)((w & 1) * (L::TILE >> 4));
+            const uint64_t b = dv + (uint64_t)((i & 1) * (L::TILE >> 4));
 #pragma unroll
-            for (int k = 0; k < 8; ++k)   // 16 keys a step
-              umma_ts(tm + 256 + s * D, tm + s * 128 + k * 8, b + (uint64_t)(k * (2048 >> 4)), idesc_o, (w > f || k > 0) ? 1u : 0u, leader);
-            if (w == nwin - 1) commit_by(&o_fin[s], leader);
-            if (s == nst - 1) commit_by(&v_free[w & 1], leader);
+            for (int c = 0; c < 8; ++c)   // 16 keys a step
+              umma_ts(tm + 256 + s * D, tm + s * 128 + c * 8, b + (uint64_t)(c * (2048 >> 4)), idesc_o, (w > f || c > 0) ? 1u : 0u, leader);
+            if (w == k.nwin - 1) commit_by(&o_fin[s], leader);
+            if (s == k.nst - 1) commit_by(&v_free[i & 1], leader);
           }
-          if (w + 1 < nwin && w + 1 >= f) product_s(s, w + 1, w + 1 == f && f > 0);
+          if (w + 1 < k.nwin && w + 1 >= f) product_s(s, w + 1, i + 1, w + 1 == f && f > 0);
         }
       }
-      if (!ok) {   // what was issued is done before TMEM is given back: a commit covers every product before it
-        if (leader) status_set(p.status, TV_E_TIMEOUT);
-        commit_by(drain, leader);
-        mbar_wait(drain, 0);
-      }
-    } else {
-      // ---------------- softmax: warps 8 s .. 8 s + 7 hold tile s, thread pairs a row ----------------
-      const int s = warp >> 3, hf = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;   // tile, half of the keys, row
-      const bool active = s < nst;
-      const int f = s == 0 ? skip0 : 0;
-      const int tmin = t0 + s * p.T;
-      const int t = tmin + r / p.G;
-      const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t sS = tS + s * 128 + lb, sO = tO + s * D + hf * (D / 2) + lb;
-      float* s_top = reinterpret_cast<float*>(smem + L::OFF_TOP) + s * 256;
-      const int pair = 1 + s * 4 + (warp & 3);   // named barrier of the two warps that share rows
+      if (!ok) break;
+      kv += k.nwin;
+    }
+    if (!ok) {   // what was issued is done before TMEM is given back: a commit covers every product before it
+      if (leader) status_set(p.status, TV_E_TIMEOUT);
+      commit_by(drain, leader);
+      mbar_wait(drain, 0);
+    }
+  }
+  } else {
+    // ---------------- softmax: warps 8 s .. 8 s + 7 hold tile s, thread pairs a row ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    const int s = warp >> 3, hf = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;   // tile, half of the keys, row
+    const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t sS = tmem + s * 128 + lb, sO = tmem + 256 + s * D + hf * (D / 2) + lb;
+    float* s_top = reinterpret_cast<float*>(smem + L::OFF_TOP) + s * 256;
+    float* s_sum = reinterpret_cast<float*>(smem + L::OFF_SUM) + s * 256;
+    const int pair = 1 + s * 4 + (warp & 3);   // named barrier of the two warps that share rows
+    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+    const int rt = r / p.G;                    // token of the row in its tile
+    bool ok = true;
+    int kv = 0, looked = 0, ns = 0, nf = 0;    // windows, windows looked over, score tiles, finished outputs before this place
+
+    for (int it = 0;; ++it) {
+      wait_work(it, ok);
+      const Work k = read_work(it, ok);
+      if (pair_any(k.len == 0, pair)) break;   // the two warps of a pair leave together, whatever happened
+      const bool active = s < k.nst;
+      const int f = s == 0 ? k.skip0 : 0;
+      const int tmin = k.t0 + s * p.T, t = tmin + rt;
       // rows of the tile behind the last vector or token hold anything: an
       // infinite offset keeps them out of every decision
-      const bool live = r < p.T * p.G && t < len;
+      const bool live = r < p.T * p.G && t < k.len;
       float m = live ? -INFINITY : INFINITY, l = 0.f;   // offset of the row; sum over this thread's keys
-      bool ok = true;
+      unsigned long long* bad = s_bad + (it & 1) * 3 * D;
+      const unsigned tag = (unsigned)it + 1u;
 
-      auto look_over = [&](int w) {   // V rows of keys past t0
-        if (ok && !mbar_wait(&v_full[w & 1], (uint32_t)(w >> 1) & 1u)) ok = false;
-        uint8_t* sv = smem + L::OFF_V + (w & 1) * L::TILE;
-        const int key0 = w_start(w), first = max(0, t0 + 1 - key0);
+      // V rows of keys past the first token.  An entry of `bad` is the place's
+      // complement and the key, so that the smallest is the latest place's first
+      // key; what two places before left behind is larger.
+      auto look_over = [&](int w) {
+        const int i = kv + w;
+        if (ok && !mbar_wait(&v_full[i & 1], (uint32_t)(i >> 1) & 1u)) ok = false;
+        uint8_t* sv = smem + L::OFF_V + (i & 1) * L::TILE;
+        const int key0 = w_start(k, w), first = max(0, k.t0 + 1 - key0);
         bool wrote = false;
         for (int e = tid; e < (128 - first) * (D / 8); e += kPrSoftThreads) {
           const int row = first + e / (D / 8), c = e % (D / 8);
@@ -464,18 +597,19 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             for (int u = 0; u < 8; ++u) {
               const uint32_t b = (x[u >> 1] >> (16 * (u & 1))) & 0xffffu;
               if ((b & 0x7f80u) == 0x7f80u) {
-                const int kind = (b & 0x7fu) ? 0 : (b & 0x8000u ? 2 : 1);
-                atomicMin(&s_bad[kind * D + c * 8 + u], key0 + row);
+                const int kind = (b & 0x7fu) ? 0 : (b & 0x8000u ? 2 : 1);   // NaN, +inf, -inf
+                atomicMin(&bad[kind * D + c * 8 + u], (unsigned long long)~tag << 32 | (unsigned)(key0 + row));
                 x[u >> 1] &= u & 1 ? 0x0000ffffu : 0xffff0000u;
               }
             }
-            s_anybad = 1;
+            *reinterpret_cast<volatile unsigned*>(&s_anybad[it & 1]) = tag;
             wrote = true;
           }
         }
         if (wrote) fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&v_ok[w & 1]);
+        if (lane == 0) mbar_arrive(&v_ok[looked & 1]);
+        ++looked;
       };
 
       // One window.  The exponentials are taken at the offset that the row has.
@@ -485,58 +619,64 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       // the exponentials again, whose sum can not pass 64.  P stays in
       // registers until both warps have read their scores, because it goes
       // where the scores are.
-      auto window = [&](auto masked_c, int w) {
+      // lim: the last visible one of this thread's keys; unset: rows may not
+      // have seen a key yet; again: O_s holds earlier windows.
+      auto window = [&](auto masked_c, int lim, bool unset, bool again) {
         constexpr bool MASKED = decltype(masked_c)::value;
-        if (ok && !mbar_wait(&s_full[s], (uint32_t)(w - f) & 1u)) ok = false;
+        if (ok && !mbar_wait(&s_full[s], (uint32_t)ns & 1u)) ok = false;
+        ++ns;
         tc_fence_after();
-        const int lim = t - w_start(w) - 64 * hf;   // the last visible one of this thread's keys
-        auto scores = [&](uint32_t (&x)[64]) {      // its scores
-          ld32(sS + 64 * hf, x);
-          ld32(sS + 64 * hf + 32, x + 32);
+        auto scores = [&](int c, uint32_t (&x)[32]) {   // half of its scores
+          ld32(sS + 64 * hf + 32 * c, x);
           tmem_ld_wait();
           if constexpr (MASKED) {
 #pragma unroll
-            for (int u = 0; u < 64; ++u)
-              if (u > lim) x[u] = 0xff800000u;
+            for (int u = 0; u < 32; ++u)
+              if (32 * c + u > lim) x[u] = 0xff800000u;
           }
         };
-        auto row_max = [&](const uint32_t (&x)[64]) {   // over both halves, in log2 units
+        auto row_max = [&]() {   // over both threads' keys, in log2 units
           float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-          for (int u = 0; u < 64; u += 4) {
-            a = max3(a, __uint_as_float(x[u]), __uint_as_float(x[u + 1]));
-            b = max3(b, __uint_as_float(x[u + 2]), __uint_as_float(x[u + 3]));
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+            scores(c, x);
+#pragma unroll
+            for (int u = 0; u < 32; u += 4) {
+              a = max3(a, __uint_as_float(x[u]), __uint_as_float(x[u + 1]));
+              b = max3(b, __uint_as_float(x[u + 2]), __uint_as_float(x[u + 3]));
+            }
           }
           a = fmaxf(a, b);
           s_top[hf * 128 + r] = a;
           pair_sync(pair);
           return fmaxf(a, s_top[(hf ^ 1) * 128 + r]) * p.scale_log2;
         };
-        uint32_t x[64];
-        scores(x);
-        // rows that have seen no key yet: all of them in the first window, and
-        // those that lie before a window that hid it all
-        if (w == f || w_start(w - 1) > tmin) {
-          const float top = row_max(x);
+        if (unset) {
+          const float top = row_max();
           if (m == -INFINITY) m = top;
         }
         uint32_t pk[32];
         float sum;
-        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
         for (;;) {
           const float neg = m == -INFINITY ? 0.f : -m;
           const uint64_t neg2 = pack2(neg, neg);
           uint64_t l2 = 0, l3 = 0;
 #pragma unroll
-          for (int u = 0; u < 32; ++u) {
-            float a, b;
-            unpack2(fma2(pack2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), scale2, neg2), a, b);
-            const __nv_bfloat162 v = __floats2bfloat162_rn(ex2p(a), ex2p(b));
-            const uint32_t q = *reinterpret_cast<const uint32_t*>(&v);
-            pk[u] = q;
-            const uint64_t q2 = pack2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
-            if (u & 1) l3 = add2(l3, q2);
-            else l2 = add2(l2, q2);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+            scores(c, x);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+              float a, b;
+              unpack2(fma2(pack2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), scale2, neg2), a, b);
+              const __nv_bfloat162 v = __floats2bfloat162_rn(ex2p(a), ex2p(b));
+              const uint32_t q = *reinterpret_cast<const uint32_t*>(&v);
+              pk[16 * c + u] = q;
+              const uint64_t q2 = pack2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
+              if (u & 1) l3 = add2(l3, q2);
+              else l2 = add2(l2, q2);
+            }
           }
           float a, b;
           unpack2(add2(l2, l3), a, b);
@@ -545,13 +685,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           const bool any = pair_any(sum > kMoveSum, pair);
           tc_fence_after();
           if (!any) break;
-          scores(x);
-          const float top = row_max(x);
-          const bool move = live && top > m;
+          const float top = row_max();
+          const bool move = top > m;   // never of a row whose offset is infinite
           const float scale = move ? ex2p(m - top) : 1.f;
           if (move) m = top;
           l *= scale;
-          if (w > f) {
+          if (again) {
 #pragma unroll
             for (int c = 0; c < D / 2; c += 16) {
               uint32_t o[16];
@@ -571,63 +710,71 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[s]);
       };
 
-      for (int w = 0; w < nwin; ++w) {
+      // the windows that hide something, or are the first
+      int w = 0;
+      for (; w < k.nwin; ++w) {
+        const int start = w_start(k, w);
+        const bool masked = start + 127 > tmin, look = scrub(k, w);
+        // rows without a key: all in the first window, and those before a window that hid it all
+        const bool unset = w == f || start + 128 > tmin;
+        if (!look && (!active || (w > f && !masked && !unset))) break;
         if (active && w >= f) {
-          if (w_start(w) + 127 > tmin) window(std::integral_constant<bool, true>{}, w);
-          else window(std::integral_constant<bool, false>{}, w);
+          if (masked) window(std::integral_constant<bool, true>{}, t - start - 64 * hf, unset, w > f);
+          else window(std::integral_constant<bool, false>{}, 0, unset, w > f);
         }
-        if (scrub(w)) look_over(w);   // V lands while the first softmax runs
+        if (look) look_over(w);   // V lands while the first softmax runs
       }
+      // and all the others
+      if (active)
+        for (; w < k.nwin; ++w) window(std::integral_constant<bool, false>{}, 0, false, true);
+      kv += k.nwin;
+      // the place's end, for the warps of a tile that it does not have too:
+      // nobody runs ahead of the loads by more than a phase
+      if (ok && !mbar_wait(&o_fin[active ? s : 0], (uint32_t)(active && s == 1 ? nf : it) & 1u)) ok = false;
       if (active) {
-        s_top[hf * 128 + r] = l;   // after the last window's pair_any: the maxima were read
+        ++nf;
+        s_sum[hf * 128 + r] = l;
         pair_sync(pair);
-        const float inv = 1.f / (s_top[r] + s_top[128 + r]);
-        if (ok && !mbar_wait(&o_fin[s], 0)) ok = false;
+        const float inv = 1.f / (s_sum[r] + s_sum[128 + r]);
         tc_fence_after();
-        // this warp's 32 rows of D / 2 values through the query tile's shared
-        // memory (its products are done), so that a row is stored in one piece
-        const bool anybad = *reinterpret_cast<volatile int*>(&s_anybad) != 0;
-        constexpr int CH = D / 16;   // 16-byte pieces of half a row
-        uint4* stage = reinterpret_cast<uint4*>(smem + L::OFF_Q + s * L::TILE) + (warp & 7) * 32 * CH;
+        const Work k = read_work(it, true);   // read once more: not held through the windows
+        const int t = k.t0 + s * p.T + rt;
+        const bool live = r < p.T * p.G && t < k.len;
+        const bool anybad = *reinterpret_cast<volatile unsigned*>(&s_anybad[it & 1]) == tag;
+        __nv_bfloat16* dst = p.out + ((size_t)(k.row0 + t) * p.Hq + k.h * p.G + r % p.G) * D + hf * (D / 2);
 #pragma unroll
         for (int c = 0; c < D / 2; c += 32) {
           uint32_t o[32];
           ld32(sO + c, o);
           tmem_ld_wait();
           if (anybad) {
-            const int* first = s_bad + hf * (D / 2) + c;
+            const unsigned long long* first = bad + hf * (D / 2) + c;
+            auto sees = [&](unsigned long long x) { return (unsigned)(x >> 32) == ~tag && (int)(unsigned)x <= t; };
 #pragma unroll
             for (int u = 0; u < 32; ++u) {
-              const bool n = first[u] <= t, pi = first[D + u] <= t, ni = first[2 * D + u] <= t;
+              const bool n = sees(first[u]), pi = sees(first[D + u]), ni = sees(first[2 * D + u]);
               if (n || (pi && ni)) o[u] = 0x7fc00000u;
               else if (pi) o[u] = 0x7f800000u;
               else if (ni) o[u] = 0xff800000u;
             }
           }
 #pragma unroll
-          for (int u = 0; u < 32; u += 8) {
-            uint32_t b[4];
+          for (int u = 0; u < 32; u += 16) {
+            uint32_t b[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 8; ++e) {
               const __nv_bfloat162 v =
                   __floats2bfloat162_rn(__uint_as_float(o[u + 2 * e]) * inv, __uint_as_float(o[u + 2 * e + 1]) * inv);
               b[e] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            stage[lane * CH + (((c + u) >> 3) ^ (lane & (CH - 1)))] = make_uint4(b[0], b[1], b[2], b[3]);
+            if (ok && live) store32(dst + c + u, b);
           }
         }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int row = i * (32 / CH) + lane / CH, c = lane % CH;   // of the warp's 32 rows
-          const int rr = (warp & 3) * 32 + row, tt = tmin + rr / p.G;
-          if (ok && rr < p.T * p.G && tt < len)
-            *reinterpret_cast<uint4*>(p.out + ((size_t)(row0 + tt) * p.Hq + h * p.G + rr % p.G) * D + hf * (D / 2) + c * 8) =
-                stage[row * CH + (c ^ (row & (CH - 1)))];
-        }
+        tc_fence_before();   // the next place's products into O_s follow this warp's next arrival
       }
-      if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
+      free_work(it);
     }
+    if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
   }
   tc_fence_before();
   __syncthreads();
@@ -665,7 +812,7 @@ extern "C" int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, con
   if (head_dim != 64 && head_dim != 128) return TV_E_UNSUPPORTED;
   if (n_q_heads % n_kv_heads != 0 || n_q_heads / n_kv_heads > 128 || n_q_heads > 65536) return TV_E_UNSUPPORTED;
   const size_t D = head_dim;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || q_stride % 8 != 0 || kv_stride % 8 != 0) return TV_E_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(out) & 31u) != 0 || q_stride % 8 != 0 || kv_stride % 8 != 0) return TV_E_ARG;
   if (q_stride < n_q_heads * D || kv_stride < n_kv_heads * D) return TV_E_ARG;
   PrParams p;
   p.starts = starts;

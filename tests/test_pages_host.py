@@ -104,7 +104,7 @@ def test_attend_prompt_host_checks():
         return abi.tv_attend_prompt(hq, hkv, d, q, k, v, qs, kvs, starts, n, rows, out, st)
 
     for over in (dict(hq=0), dict(hkv=0), dict(q=None), dict(k=None), dict(v=None), dict(starts=None), dict(out=None), dict(st=None),
-                 dict(n=0), dict(rows=0), dict(q=FAKE + 2), dict(k=FAKE + 8), dict(v=FAKE + 2), dict(out=FAKE + 4), dict(qs=516), dict(qs=504),
+                 dict(n=0), dict(rows=0), dict(q=FAKE + 2), dict(k=FAKE + 8), dict(v=FAKE + 2), dict(out=FAKE + 4), dict(out=FAKE + 16), dict(qs=516), dict(qs=504),
                  dict(kvs=132), dict(kvs=120)):
         assert call(**over) == E["TV_E_ARG"], over
     for over in (dict(n=4097), dict(d=96), dict(hq=9), dict(hq=258, hkv=2, qs=258 * 64), dict(rows=2 ** 31 - 1, hq=256, hkv=8, kvs=512, qs=256 * 64)):
