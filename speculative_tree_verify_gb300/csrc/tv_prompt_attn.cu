@@ -19,8 +19,8 @@
 //   O_s += P_s V_w         tcgen05.mma 128 x D x 128, P from TMEM, V from its
 //                          TMA layout (MN-major)
 // The issue order PV_0(w) S_0(w + 1) PV_1(w) S_1(w + 1) keeps the tensor pipe
-// on one tile while the other's softmax runs.  A row's offset m moves only when
-// exponentials add up to more than 2^8; then O_s is rescaled in TMEM by the row's own threads
+// on one tile while the other's softmax runs.  A row's offset m need not be its
+// maximum, only near it; where it is not, O_s is rescaled in TMEM by the row's own threads
 // (S_s(w) is committed after PV_s(w - 1), so O_s is at rest).  Sums add the
 // rounded P, fp32 throughout.
 //
@@ -47,7 +47,9 @@ constexpr int kPrThreads = kPrSoftThreads + 128;  // a whole warpgroup for the f
 constexpr int kSoftRegs = 104, kRoleRegs = 64;
 static_assert(kPrSoftThreads * kSoftRegs + 128 * kRoleRegs <= kPrThreads * 96, "registers of the launch");
 constexpr int kAtomP = 128 * 128;                // bytes of a 128-row x 128-byte swizzled slab
-constexpr float kMoveSum = 256.f;                // an offset moves when 64 keys' exponentials add up to more
+// offsets, in powers of two (see the softmax): the first one, how far beyond a
+// maximum the next ones go, and the sums of 64 exponentials that an offset may have
+constexpr float kFirst = 20.f, kAbove = 20.f, kHigh = 256.f, kLow = 8.27180613e-25f;   // 2^-80
 
 template <int D>
 struct PrSmem {
@@ -69,6 +71,7 @@ struct PrParams {
   __nv_bfloat16* out;
   int32_t* status;
   int n, rows, Hq, Hkv, G, T;
+  int queued;   // the grid is larger than the GPU: CTAs may be waiting whose places can be taken over
   float scale_log2;
 };
 
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     int block = blockIdx.x;
     for (int it = 0, asked = 0;; ) {
       const int4 x = block >= 0 ? find(block) : make_int4(0, 0, 0, 0);
-      if (x.y > 0 || block < 0 || all == 0) {
+      if (x.y > 0 || block < 0 || all == 0 || !p.queued) {
         if (it >= 2 && ok && !mbar_wait(&w_free[it & 1], (uint32_t)((it - 2) >> 1) & 1u)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -412,6 +415,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         __syncwarp();
         ++it;
         if (x.y == 0) break;
+        if (!p.queued) {
+          block = -1;
+          continue;
+        }
         // not before this place's end is near: who is done first takes the next
         ok = __all_sync(0xffffffffu, mbar_wait(want, (uint32_t)(it - 1) & 1u));
         if (!ok) break;
@@ -573,7 +580,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       // rows of the tile behind the last vector or token hold anything: an
       // infinite offset keeps them out of every decision
       const bool live = r < p.T * p.G && t < k.len;
-      float m = live ? -INFINITY : INFINITY, l = 0.f;   // offset of the row; sum over this thread's keys
+      float m = live ? kFirst : INFINITY, l = 0.f;   // offset of the row; sum over this thread's keys
       unsigned long long* bad = s_bad + (it & 1) * 3 * D;
       const unsigned tag = (unsigned)it + 1u;
 
@@ -612,17 +619,21 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         ++looked;
       };
 
-      // One window.  The exponentials are taken at the offset that the row has.
-      // A sum over this thread's 64 keys above kMoveSum says that some score
-      // has passed the offset: then (rarely after the first windows) both
-      // threads of the row find its maximum, move the offset there and take
-      // the exponentials again, whose sum can not pass 64.  P stays in
-      // registers until both warps have read their scores, because it goes
-      // where the scores are.
-      // lim: the last visible one of this thread's keys; unset: rows may not
-      // have seen a key yet; again: O_s holds earlier windows.
-      auto window = [&](auto masked_c, int lim, bool unset, bool again) {
-        constexpr bool MASKED = decltype(masked_c)::value;
+      // One window.  The exponentials are taken at the offset that the row has,
+      // kFirst to begin with: what matters is that the offset lies within some
+      // 80 powers of two of the scores, since P and the sums are floating-point
+      // numbers.  A sum over this thread's 64 keys says whether it does: above
+      // kHigh some score lies too far above it, and below kLow, where the row
+      // sees its first keys, all of them lie too far below.  Then (hardly ever)
+      // both threads of the row find its maximum, the offset goes kAbove beyond
+      // it, and the exponentials are taken again, whose sum can not be above
+      // kHigh.  P stays in registers until both warps have read their scores,
+      // because it goes where the scores are.
+      // lim: the last visible one of this thread's keys; before: the first key
+      // of the window before (rows before it have seen none); again: O_s holds
+      // earlier windows.
+      auto window = [&](auto masked_c, auto fresh_c, int lim, int before, bool again) {
+        constexpr bool MASKED = decltype(masked_c)::value, FRESH = decltype(fresh_c)::value;
         if (ok && !mbar_wait(&s_full[s], (uint32_t)ns & 1u)) ok = false;
         ++ns;
         tc_fence_after();
@@ -635,32 +646,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               if (32 * c + u > lim) x[u] = 0xff800000u;
           }
         };
-        auto row_max = [&]() {   // over both threads' keys, in log2 units
-          float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t x[32];
-            scores(c, x);
-#pragma unroll
-            for (int u = 0; u < 32; u += 4) {
-              a = max3(a, __uint_as_float(x[u]), __uint_as_float(x[u + 1]));
-              b = max3(b, __uint_as_float(x[u + 2]), __uint_as_float(x[u + 3]));
-            }
-          }
-          a = fmaxf(a, b);
-          s_top[hf * 128 + r] = a;
-          pair_sync(pair);
-          return fmaxf(a, s_top[(hf ^ 1) * 128 + r]) * p.scale_log2;
-        };
-        if (unset) {
-          const float top = row_max();
-          if (m == -INFINITY) m = top;
-        }
         uint32_t pk[32];
         float sum;
-        for (;;) {
-          const float neg = m == -INFINITY ? 0.f : -m;
-          const uint64_t neg2 = pack2(neg, neg);
+        for (bool first = true;; first = false) {
+          const uint64_t neg2 = pack2(-m, -m);
           uint64_t l2 = 0, l3 = 0;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -681,14 +670,33 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           float a, b;
           unpack2(add2(l2, l3), a, b);
           sum = a + b;
+          const bool fresh = FRESH && before > t;   // the row's first keys, if it sees any
+          bool off = sum > kHigh;
+          if (FRESH) off = off || (first && fresh && live && (!MASKED || lim >= 0) && sum < kLow);
           tc_fence_before();
-          const bool any = pair_any(sum > kMoveSum, pair);
+          const bool any = pair_any(off, pair);
           tc_fence_after();
           if (!any) break;
-          const float top = row_max();
-          const bool move = top > m;   // never of a row whose offset is infinite
-          const float scale = move ? ex2p(m - top) : 1.f;
-          if (move) m = top;
+          float y = -INFINITY, z = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+            scores(c, x);
+#pragma unroll
+            for (int u = 0; u < 32; u += 4) {
+              y = max3(y, __uint_as_float(x[u]), __uint_as_float(x[u + 1]));
+              z = max3(z, __uint_as_float(x[u + 2]), __uint_as_float(x[u + 3]));
+            }
+          }
+          y = fmaxf(y, z);
+          s_top[hf * 128 + r] = y;
+          pair_sync(pair);
+          y = fmaxf(y, s_top[(hf ^ 1) * 128 + r]) * p.scale_log2;   // the row's maximum
+          // above: 64 keys below m + 2 do not add up to more than kHigh
+          const bool move = live && (y > m + 2.f || (fresh && y < m - kAbove && y > -INFINITY));
+          const float next = y + kAbove;
+          const float scale = move && !fresh ? ex2p(m - next) : 1.f;   // a row without keys has nothing to rescale
+          if (move) m = next;
           l *= scale;
           if (again) {
 #pragma unroll
@@ -716,17 +724,17 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const int start = w_start(k, w);
         const bool masked = start + 127 > tmin, look = scrub(k, w);
         // rows without a key: all in the first window, and those before a window that hid it all
-        const bool unset = w == f || start + 128 > tmin;
-        if (!look && (!active || (w > f && !masked && !unset))) break;
+        const int before = w == f ? 0x7fffffff : start + 128;
+        if (!look && (!active || (w > f && !masked && before <= tmin))) break;
         if (active && w >= f) {
-          if (masked) window(std::integral_constant<bool, true>{}, t - start - 64 * hf, unset, w > f);
-          else window(std::integral_constant<bool, false>{}, 0, unset, w > f);
+          if (masked) window(std::true_type{}, std::true_type{}, t - start - 64 * hf, before, w > f);
+          else window(std::false_type{}, std::true_type{}, 0, before, w > f);
         }
         if (look) look_over(w);   // V lands while the first softmax runs
       }
       // and all the others
       if (active)
-        for (; w < k.nwin; ++w) window(std::integral_constant<bool, false>{}, 0, false, true);
+        for (; w < k.nwin; ++w) window(std::false_type{}, std::false_type{}, 0, 0, true);
       kv += k.nwin;
       // the place's end, for the warps of a tile that it does not have too:
       // nobody runs ahead of the loads by more than a phase
@@ -785,7 +793,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 }
 
 template <int D>
-int launch_prompt(const PrParams& p, const void* q, const void* k, const void* v, size_t q_stride, size_t kv_stride, cudaStream_t st) {
+int launch_prompt(PrParams& p, const void* q, const void* k, const void* v, size_t q_stride, size_t kv_stride, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
   int rc = make_tmap_bf16_rows(&mq, q, D, p.Hq, p.rows, q_stride, 64, p.G, p.T);
   if (rc || (rc = make_tmap_bf16_rows(&mk, k, p.Hkv * D, 1, p.rows, kv_stride, 64, 1, 128)) ||
@@ -795,6 +803,9 @@ int launch_prompt(const PrParams& p, const void* q, const void* k, const void* v
   if (ensure_smem_limit(prompt_attn_kernel<D>, PrSmem<D>::BYTES, attr)) return TV_E_CUDA;
   // at most rows / 2T whole pairs and one ragged pair a sequence
   const long long pairs = (long long)p.rows / (2 * p.T) + (p.n < p.rows ? p.n : p.rows);
+  const int sms = num_sms();
+  if (sms <= 0) return TV_E_CUDA;
+  p.queued = pairs * p.Hkv > sms;
   return launch_pdl(prompt_attn_kernel<D>, dim3((unsigned)(pairs * p.Hkv)), dim3(kPrThreads), PrSmem<D>::BYTES, st, mq, mk, mv, p);
 }
 
