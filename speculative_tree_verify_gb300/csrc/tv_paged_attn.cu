@@ -23,6 +23,7 @@
 // the sums add the rounded values, so a key that dominates passes its V row
 // through unchanged.  Offsets move only when a score passes them by 2^8.
 #include <cmath>
+#include <type_traits>
 
 #include "tv_gemm.cuh"
 #include "tv_kernels.cuh"
@@ -41,6 +42,7 @@ constexpr int kCompWarps = 8;
 constexpr int kCompThreads = kCompWarps * 32;
 constexpr int kPaThreads = kCompThreads + 32;
 constexpr int kRows = 16;                        // query heads of a block
+constexpr int kQueries = 8;                      // segments whose queries are loaded ahead, at most
 constexpr int kMaxTokens = 2048;                 // sequences of one call: their places fit shared memory beside the stages
 constexpr int kInfo = 640;                       // up to here their table rows and lengths do, too
 constexpr int kRedRows = 4;                      // rows joined at a time when a head block ends
@@ -76,12 +78,12 @@ struct PaSmem {
   static constexpr int SEG_COST = 256 / D;                   // what a head block costs besides its tiles, in tiles
   static constexpr int OFF_ML = OFF_RED + kCompWarps * kRedRows * D * 4;
   static constexpr int Q_ROW = D * 2 + 16;                   // rows 16 bytes apart in the banks: ldmatrix without conflicts
-  static constexpr int OFF_Q = OFF_ML + kCompWarps * kRows * 8;   // [2][kRows] query rows: a segment's
+  static constexpr int OFF_Q = OFF_ML + kCompWarps * kRows * 8;   // 2 kRows query rows: those of the next 2 to kQueries segments
   static constexpr int OFF_BAR = OFF_Q + 2 * kRows * Q_ROW;
-  static constexpr int OFF_FIRST = OFF_BAR + 128;            // [n + 1]; up to kInfo sequences also their rows and lengths
+  static constexpr int OFF_FIRST = OFF_BAR + 256;            // [n + 1]; up to kInfo sequences also their rows and lengths
   static size_t bytes(int n) { return 1024 + OFF_FIRST + (size_t)(n + 1) * 4 + (n <= kInfo ? (size_t)n * 8 : 0); }
   static_assert(kCompWarps * kRedRows * D * 4 >= kMaxSeqs / 8, "a mark for every table row");
-  static_assert(1024 + OFF_FIRST + (kMaxTokens + 1) * 4 <= 232448 - 256 && kInfo * 12 <= kMaxTokens * 4, "shared memory of one CTA");
+  static_assert(1024 + OFF_FIRST + (kMaxTokens + 1) * 4 <= 232448 - 64 && kInfo * 12 <= kMaxTokens * 4, "shared memory of one CTA");
 };
 
 __device__ __forceinline__ float ex2f(float x) {   // 2^x by the SFU, about 2^-22 relative, 2^-inf = 0
@@ -115,6 +117,11 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint3
 }
 __device__ __forceinline__ void comp_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kCompThreads) : "memory"); }
 
+__device__ __forceinline__ void quad_sync(int quad) { asm volatile("bar.sync %0, %1;" ::"r"(2 + quad), "n"(kCompThreads / 2) : "memory"); }
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
 template <int D>
@@ -125,8 +132,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* empty = full + kStages;
-  uint64_t* q_full = empty + kStages;    // [2] a segment's queries landed
-  uint64_t* q_free = q_full + 2;         // [2] the eight warps have them
+  uint64_t* q_full = empty + kStages;    // [kQueries] a segment's queries landed
+  uint64_t* q_free = q_full + kQueries;  // [kQueries] the warps that compute it are done with them
   uint32_t* s_first = reinterpret_cast<uint32_t*>(smem + L::OFF_FIRST);
   float* s_red = reinterpret_cast<float*>(smem + L::OFF_RED);
   float2* s_ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
@@ -138,13 +145,14 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ps = p.pool.page_size, Hkv = p.pool.n_kv_heads;
   const bool info = p.n <= kInfo;
+  const int qrows = min(kRows, p.G), qslots = min(kQueries, 2 * kRows / qrows);   // short sequences need many segments ahead
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 4);   // the four warps that compute its tile
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kQueries; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_free[s], kCompWarps);
     }
@@ -153,10 +161,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     prefetch_tmap(&map_v);
     s_bad = 0;
   }
-  // query rows past the group's heads: products nobody reads, of finite values
-  for (int e = tid; e < 2 * kRows * L::Q_ROW / 16; e += kPaThreads)
-    reinterpret_cast<uint4*>(smem + L::OFF_Q)[e] = make_uint4(0u, 0u, 0u, 0u);
-  fence_async_smem();
   if (p.n > 32 && p.k_new)
     for (int i = tid; i < (p.seqs.max_seqs + 31) / 32; i += kPaThreads) s_mark[i] = 0u;
   __syncthreads();
@@ -244,32 +248,52 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   const uint32_t lo = min(all, chunk * blockIdx.x), hi = min(all, lo + chunk);
   if (tid == 0) p.ws.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (lo >= hi) return;
-  int i0 = 0;   // the sequence of place lo: the last whose first place is at or before it
-  for (int b = p.n - 1; i0 < b;) {
-    const int mid = (i0 + b + 1) >> 1;
-    if (s_first[mid] <= lo) i0 = mid;
-    else b = mid - 1;
-  }
-
-  // a run of tiles of one sequence and head block; a range may hold no more
-  // than (part of) its fixed cost, then t0 == t1
-  struct Seg {
-    int i, hh, s, len, t0, t1;   // listed index, head block, table row, length, tiles [t0, t1)
-    uint32_t base, next;         // place of its first tile; place behind the run
+  // A run: tiles [t0, t1) of one sequence and head block.  The CTA's runs in
+  // order; a range may begin or end within a head block's fixed cost.
+  struct Run {
+    int i, s, len, T;     // listed index, table row, length, tiles of the head block
+    int h, hb, t0, t1;    // KV head, block of its query heads
+    uint32_t base;        // place of tile 0
   };
-  auto segment = [&](uint32_t at, int i) {   // the run that holds place `at` of sequence i (or a later one)
-    while (s_first[i + 1] <= at) ++i;
-    Seg g;
+  auto sequence = [&](Run& g, int i) {
     g.i = i;
     g.s = info ? s_row[i] : __ldg(p.ids + i);
     g.len = info ? s_len[i] : __ldcg(p.seqs.lens + g.s);
-    const uint32_t T = tiles_of(g.len), unit = T + L::SEG_COST, off = at - s_first[i];
-    g.hh = (int)(off / unit);
-    g.base = s_first[i] + g.hh * unit + L::SEG_COST;
-    g.next = min(hi, g.base + T);
-    g.t0 = at > g.base ? (int)(at - g.base) : 0;
-    g.t1 = g.next > g.base ? (int)(g.next - g.base) : 0;
-    return g;
+    g.T = tiles_of(g.len);
+  };
+  auto bound = [&](Run& g) { g.t1 = hi > g.base ? (int)min((uint32_t)g.T, hi - g.base) : 0; };
+  auto next_run = [&](Run& g) {   // false: there is none
+    if (g.base + g.T >= hi) return false;
+    g.base += g.T + L::SEG_COST;
+    if (++g.hb == p.HB) {
+      g.hb = 0;
+      if (++g.h == Hkv) {
+        g.h = 0;
+        int i = g.i + 1;
+        while (s_first[i + 1] == s_first[i]) ++i;
+        sequence(g, i);
+        g.base = s_first[i] + L::SEG_COST;
+      }
+    }
+    g.t0 = 0;
+    bound(g);
+    return g.t1 > 0;
+  };
+  auto first_run = [&](Run& g) {
+    int i = 0;   // the sequence of place lo: the last whose first place is at or before it
+    for (int b = p.n - 1; i < b;) {
+      const int mid = (i + b + 1) >> 1;
+      if (s_first[mid] <= lo) i = mid;
+      else b = mid - 1;
+    }
+    sequence(g, i);
+    const uint32_t unit = g.T + L::SEG_COST, hh = (lo - s_first[i]) / unit;
+    g.h = (int)(hh / p.HB);
+    g.hb = (int)(hh % p.HB);
+    g.base = s_first[i] + hh * unit + L::SEG_COST;
+    g.t0 = lo > g.base ? (int)(lo - g.base) : 0;
+    bound(g);
+    return g.t0 < g.t1 || next_run(g);
   };
 
   if (warp == kCompWarps) {
@@ -282,41 +306,40 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int slab = which % (D / 64);
     const uint64_t pol = policy_evict_first();
     bool ok = true;
-    int issued = 0, segs = 0;
-    uint32_t at = lo;
-    int i = i0;
-    while (at < hi && ok) {
-      const Seg g = segment(at, i);
-      i = g.i;
-      at = g.next;
-      if (g.t0 == g.t1) continue;
+    int issued = 0, segs = 0, st = 0, qs = 0;   // tiles and queries loaded so far, their places in the rings
+    uint32_t st_par = 1u, qs_par = 1u;          // of the wait before a place is used again; the first round waits for nothing
+    const int psh = 31 - __clz(ps);
+    auto entry = [&](const Run& g, int t) {   // this lane's page of tile t, -1 past the length
+      const int tok = t * kTile + box * R;
+      return box < nb && tok < g.len ? __ldcg(p.seqs.pages + (size_t)g.s * p.seqs.max_pages + (tok >> psh)) : -1;
+    };
+    Run g;
+    bool have = first_run(g);
+    int page = have ? entry(g, g.t0) : -1;
+    while (have && ok) {
+      Run next = g;   // the next run's first pages are on their way before this one's tiles
+      const bool more = next_run(next);
+      const int next_page = more ? entry(next, next.t0) : -1;
       // its queries
-      if (segs >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&q_free[segs & 1], (uint32_t)((segs - 2) >> 1) & 1u));
+      if (segs >= qslots) ok = __all_sync(0xffffffffu, mbar_wait(&q_free[qs], qs_par));
       if (!ok) break;
-      const int r0 = (g.hh % p.HB) * kRows, nr = min(kRows, p.G - r0);
-      if (lane == 0) mbar_arrive_expect_tx(&q_full[segs & 1], (uint32_t)(nr * D * 2));
+      const int r0 = g.hb * kRows, nr = min(kRows, p.G - r0);
+      if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], (uint32_t)(nr * D * 2));
       __syncwarp();
       if (lane < nr)
-        bulk_load(smem + L::OFF_Q + ((segs & 1) * kRows + lane) * L::Q_ROW,
-                  p.q + (size_t)g.i * p.q_stride + (size_t)((g.hh / p.HB) * p.G + r0 + lane) * D, D * 2, &q_full[segs & 1]);
+        bulk_load(smem + L::OFF_Q + (qs * qrows + lane) * L::Q_ROW,
+                  p.q + (size_t)g.i * p.q_stride + (size_t)(g.h * p.G + r0 + lane) * D, D * 2, &q_full[qs]);
       ++segs;
-      const int32_t* row = p.seqs.pages + (size_t)g.s * p.seqs.max_pages;
-      const int h = g.hh / p.HB;
-      auto entry = [&](int t) {   // this lane's page of tile t, -1 past the length
-        const int tok = t * kTile + box * R;
-        return box < nb && tok < g.len ? __ldcg(row + tok / ps) : -1;
-      };
-      int page = entry(g.t0);
-      for (int t = g.t0; t < g.t1 && ok; ++t) {
+      if (++qs == qslots) qs = 0, qs_par ^= 1u;
+      const int y0 = p.layer * p.pool.n_pages;   // the host has seen to it that a row of the pool is an int
+      for (int t = g.t0; t < g.t1; ++t) {
         const int tok = t * kTile + box * R;
         const bool in = box < nb && tok < g.len;
         const bool good = in && page >= 0 && page < p.pool.n_pages;
         if (in && !good) status_set(p.status, TV_E_PAGE);
-        const int y = good ? (int)((((size_t)p.layer * p.pool.n_pages + page) * Hkv + h) * ps) + tok % ps : 0;
-        if (t + 1 < g.t1) page = entry(t + 1);
-        const int st = issued % kStages;
-        if (issued >= kStages) ok = mbar_wait(&empty[st], (uint32_t)(issued / kStages - 1) & 1u);
-        ok = __all_sync(0xffffffffu, ok);
+        const int y = good ? (((y0 + page) * Hkv + g.h) << psh) + (tok & (ps - 1)) : 0;
+        if (t + 1 < g.t1) page = entry(g, t + 1);
+        if (issued >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], st_par));
         if (!ok) break;
         const unsigned boxes = __ballot_sync(0xffffffffu, good);
         if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(boxes) * (uint32_t)(R * 128));
@@ -326,10 +349,14 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                       &full[st], slab * 64, y, pol);
         __syncwarp();
         ++issued;
+        if (++st == kStages) st = 0, st_par ^= 1u;
       }
+      g = next;
+      have = more;
+      page = next_page;
     }
     if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
-    for (int u = segs > 2 ? segs - 2 : 0; u < segs; ++u) mbar_wait(&q_full[u & 1], (uint32_t)(u >> 1) & 1u);
+    for (int u = segs > qslots ? segs - qslots : 0; u < segs; ++u) mbar_wait(&q_full[u % qslots], (uint32_t)(u / qslots) & 1u);
     // loads in flight land before the CTA leaves
     for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u) mbar_wait(&full[u % kStages], (uint32_t)(u / kStages) & 1u);
     return;
@@ -340,23 +367,21 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   const int quad = warp >> 2, sl = warp & 3;        // tiles with (count mod 2) == quad; tokens 16 sl .. + 15 of a tile
   const int g8 = lane >> 2, t4 = lane & 3;
   bool ok = true;
-  int cnt = 0, segs = 0;                            // tiles and segments of this CTA before the current one
-  uint32_t at = lo;
-  int i = i0;
+  // the next tile and queries of this CTA: places in the rings, parities
+  int st = 0, qs = 0;
+  uint32_t st_par = 0u, qs_par = 0u;
   // lane addresses inside a slab: K as [token][d] fragments, V transposed
   const int k_tok = 16 * sl + (lane & 7) + ((lane >> 4) << 3), k_ch = (lane >> 3) & 1;
   const int v_tok = 16 * sl + (lane & 15), v_ch = lane >> 4;
-  while (at < hi) {
-    const Seg g = segment(at, i);
-    i = g.i;
-    at = g.next;
-    if (g.t0 == g.t1) continue;
-    const int h = g.hh / p.HB, r0 = (g.hh % p.HB) * kRows;   // KV head, first query head of the block in the group
+  Run g;
+  for (bool have = first_run(g); have; have = next_run(g)) {
+    const int h = g.h, r0 = g.hb * kRows;   // KV head, first query head of the block in the group
     const int nr = min(kRows, p.G - r0);
     uint32_t qf[KS][4];
     {
-      if (ok && !mbar_wait(&q_full[segs & 1], (uint32_t)(segs >> 1) & 1u)) ok = false;
-      const uint32_t qa = smem_u32(smem + L::OFF_Q) + ((segs & 1) * kRows + (lane & 15)) * L::Q_ROW + (lane >> 4) * 16;
+      if (ok && !mbar_wait(&q_full[qs], qs_par)) ok = false;
+      // rows past the group's heads: the last one again, products nobody reads
+      const uint32_t qa = smem_u32(smem + L::OFF_Q) + (qs * qrows + min(lane & 15, nr - 1)) * L::Q_ROW + (lane >> 4) * 16;
 #pragma unroll
       for (int k = 0; k < KS; ++k) ldsm4(qa + k * 32, qf[k]);
     }
@@ -367,12 +392,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // rows g8 and g8 + 8; sums of this thread's tokens
 
-    for (int t = g.t0; t < g.t1; ++t, ++cnt) {
-      if ((cnt & 1) != quad) continue;
-      const int st = cnt % kStages;
-      uint8_t* sk = smem + st * L::STAGE;
+    int mine = 0;   // tiles of this run that were these four warps'
+    for (int t = g.t0; t < g.t1; ++t) {
+      const int at = st;
+      const uint32_t par = st_par;
+      if (++st == kStages) st = 0, st_par ^= 1u;
+      if ((at & 1) != quad) continue;   // an even number of stages: the place's parity is the tile's
+      ++mine;
+      uint8_t* sk = smem + at * L::STAGE;
       uint8_t* sv = sk + L::HALF;
-      if (ok && !mbar_wait(&full[st], (uint32_t)(cnt / kStages) & 1u)) ok = false;
+      if (ok && !mbar_wait(&full[at], par)) ok = false;
       const int valid = min(16, g.len - t * kTile - 16 * sl);   // this warp's tokens
       if (valid > 0) {
         bool wrote = false;
@@ -459,76 +488,88 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (wrote) fence_async_smem();   // before the stage takes another TMA write
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      if (lane == 0) mbar_arrive(&empty[at]);
     }
 
-    // ---- the head block's eight partial results into one ----
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if (t4 == 0) {
-      s_ml[warp * kRows + g8] = make_float2(m0, l0);
-      s_ml[warp * kRows + g8 + 8] = make_float2(m1, l1);
-    }
-    comp_sync();
-    // The queries' place is given up here, not behind the loads: an arrival
-    // does not wait for ldmatrix results that nothing has used yet.  (A warp
-    // without a tile in this run has not used them, and never will.)
-    if (lane == 0) mbar_arrive(&q_free[segs & 1]);
-    ++segs;
-    const int T = tiles_of(g.len);
-    const bool whole = g.t0 == 0 && g.t1 == T;
+    // ---- the head block's partial results into one ----
+    // of all eight warps, or, where the head block is one tile, of the four
+    // that had it: the other four go on to the next head block meanwhile (not
+    // far: its queries are not loaded before these have given up theirs)
+    const bool whole = g.t0 == 0 && g.t1 == g.T;
     const size_t slot = (size_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0);   // a CTA's first segment may begin inside a head, its last end inside one
+    auto join = [&](auto nw_c) {
+      constexpr int NW = decltype(nw_c)::value;        // warps that take part, from w0 on
+      const int w0 = NW == kCompWarps ? 0 : 4 * quad, me = tid - 32 * w0;
+      auto meet = [&]() {
+        if constexpr (NW == kCompWarps) comp_sync();
+        else quad_sync(quad);
+      };
+      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+      if (t4 == 0) {
+        s_ml[warp * kRows + g8] = make_float2(m0, l0);
+        s_ml[warp * kRows + g8 + 8] = make_float2(m1, l1);
+      }
+      meet();
+      // The queries' place is given up here, not behind the loads: an arrival
+      // does not wait for ldmatrix results that nothing has used yet.  (A warp
+      // without a tile in this run has not used them, and never will.)
+      if (lane == 0) mbar_arrive_n(&q_free[qs], kCompWarps / NW);
 #pragma unroll
-    for (int part = 0; part < kRows / kRedRows; ++part) {   // rows 4 part .. + 3, held by the lanes with g8 / 4 = part mod 2
-      if (kRedRows * part < nr) {
-        const int half = part >> 1;
-        if ((g8 >> 2) == (part & 1)) {
-          float M = -INFINITY;
+      for (int part = 0; part < kRows / kRedRows; ++part) {   // rows 4 part .. + 3, held by the lanes with g8 / 4 = part mod 2
+        if (kRedRows * part < nr) {
+          const int half = part >> 1;
+          if ((g8 >> 2) == (part & 1)) {
+            float M = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < kCompWarps; ++w) M = fmaxf(M, s_ml[w * kRows + g8 + 8 * half].x);
-          const float mine = half ? m1 : m0;
-          const float f = mine == -INFINITY ? 0.f : ex2f(mine - M);
-          // row r: groups of 8 values XOR r, no bank twice
-          float* dst = s_red + (warp * kRedRows + (g8 & 3)) * D + 2 * t4;
-          float* at[4];
+            for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[(w0 + w) * kRows + g8 + 8 * half].x);
+            const float mine = half ? m1 : m0;
+            const float f = mine == -INFINITY ? 0.f : ex2f(mine - M);
+            // row r: groups of 8 values XOR r, no bank twice
+            float* dst = s_red + (warp * kRedRows + (g8 & 3)) * D + 2 * t4;
+            float* at[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) at[k] = dst + ((8 * k) ^ ((g8 & 3) * 8));
+            for (int k = 0; k < 4; ++k) at[k] = dst + ((8 * k) ^ ((g8 & 3) * 8));
 #pragma unroll
-          for (int k = 0; k < 2 * KS; ++k)
-            *reinterpret_cast<float2*>(at[k & 3] + 32 * (k >> 2)) = make_float2(o[k][2 * half] * f, o[k][2 * half + 1] * f);
-        }
-        comp_sync();
-        for (int e = tid; e < kRedRows * (D / 2); e += kCompThreads) {
-          const int r = e / (D / 2), d = 2 * (e % (D / 2)), row = r + kRedRows * part;
-          if (row < nr) {
-            float M2 = -INFINITY, Ls = 0.f;
-            float2 acc = make_float2(0.f, 0.f);
+            for (int k = 0; k < 2 * KS; ++k)
+              *reinterpret_cast<float2*>(at[k & 3] + 32 * (k >> 2)) = make_float2(o[k][2 * half] * f, o[k][2 * half + 1] * f);
+          }
+          meet();
+          for (int e = me; e < kRedRows * (D / 2); e += 32 * NW) {
+            const int r = e / (D / 2), d = 2 * (e % (D / 2)), row = r + kRedRows * part;
+            if (row < nr) {
+              float M2 = -INFINITY, Ls = 0.f;
+              float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kCompWarps; ++w) M2 = fmaxf(M2, s_ml[w * kRows + row].x);
+              for (int w = 0; w < NW; ++w) M2 = fmaxf(M2, s_ml[(w0 + w) * kRows + row].x);
 #pragma unroll
-            for (int w = 0; w < kCompWarps; ++w) {
-              const float2 ml = s_ml[w * kRows + row];
-              Ls += ml.x == -INFINITY ? ml.y : ml.y * ex2f(ml.x - M2);
-              const float2 v = *reinterpret_cast<const float2*>(s_red + (w * kRedRows + r) * D + (d ^ (r * 8)));
-              acc.x += v.x;
-              acc.y += v.y;
-            }
-            if (whole) {
-              *reinterpret_cast<__nv_bfloat162*>(p.out + ((size_t)g.i * p.Hq + h * p.G + r0 + row) * D + d) =
-                  __floats2bfloat162_rn(acc.x / Ls, acc.y / Ls);
-            } else {
-              *reinterpret_cast<float2*>(p.ws.o + (slot * kRows + row) * D + d) = acc;
-              if (d == 0) *reinterpret_cast<float2*>(p.ws.ml + (slot * kRows + row) * 2) = make_float2(M2, Ls);
+              for (int w = 0; w < NW; ++w) {
+                const float2 ml = s_ml[(w0 + w) * kRows + row];
+                Ls += ml.x == -INFINITY ? ml.y : ml.y * ex2f(ml.x - M2);
+                const float2 v = *reinterpret_cast<const float2*>(s_red + ((w0 + w) * kRedRows + r) * D + (d ^ (r * 8)));
+                acc.x += v.x;
+                acc.y += v.y;
+              }
+              if (whole) {
+                *reinterpret_cast<__nv_bfloat162*>(p.out + ((size_t)g.i * p.Hq + h * p.G + r0 + row) * D + d) =
+                    __floats2bfloat162_rn(acc.x / Ls, acc.y / Ls);
+              } else {
+                *reinterpret_cast<float2*>(p.ws.o + (slot * kRows + row) * D + d) = acc;
+                if (d == 0) *reinterpret_cast<float2*>(p.ws.ml + (slot * kRows + row) * 2) = make_float2(M2, Ls);
+              }
             }
           }
+          meet();
         }
-        comp_sync();
       }
-    }
+    };
+    if (g.T > 1) join(std::integral_constant<int, kCompWarps>{});
+    else if (mine) join(std::integral_constant<int, kCompWarps / 2>{});
+    if (++qs == qslots) qs = 0, qs_par ^= 1u;
     if (tid == 0 && g.t0 == 0 && !whole)   // the CTA's last run
-      p.ws.cut[blockIdx.x] = make_int4(g.i, g.hh, (int)((g.base + T - 1) / chunk), 0);
+      p.ws.cut[blockIdx.x] = make_int4(g.i, g.h * p.HB + g.hb, (int)((g.base + g.T - 1) / chunk), 0);
   }
   if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
 }
