@@ -377,6 +377,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   for (bool have = first_run(g); have; have = next_run(g)) {
     const int h = g.h, r0 = g.hb * kRows;   // KV head, first query head of the block in the group
     const int nr = min(kRows, p.G - r0);
+    if (g.T == 1 && (st & 1) != quad) {   // one tile, and the other four warps'
+      if (ok && !mbar_wait(&q_full[qs], qs_par)) ok = false;   // no further ahead than the queries
+      if (++st == kStages) st = 0, st_par ^= 1u;
+      if (++qs == qslots) qs = 0, qs_par ^= 1u;
+      continue;
+    }
     uint32_t qf[KS][4];
     {
       if (ok && !mbar_wait(&q_full[qs], qs_par)) ok = false;
@@ -392,13 +398,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // rows g8 and g8 + 8; sums of this thread's tokens
 
-    int mine = 0;   // tiles of this run that were these four warps'
     for (int t = g.t0; t < g.t1; ++t) {
       const int at = st;
       const uint32_t par = st_par;
       if (++st == kStages) st = 0, st_par ^= 1u;
       if ((at & 1) != quad) continue;   // an even number of stages: the place's parity is the tile's
-      ++mine;
       uint8_t* sk = smem + at * L::STAGE;
       uint8_t* sv = sk + L::HALF;
       if (ok && !mbar_wait(&full[at], par)) ok = false;
@@ -515,58 +519,59 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       meet();
       // The queries' place is given up here, not behind the loads: an arrival
       // does not wait for ldmatrix results that nothing has used yet.  (A warp
-      // without a tile in this run has not used them, and never will.)
+      // without a token in this run has not used them, and never will.)
       if (lane == 0) mbar_arrive_n(&q_free[qs], kCompWarps / NW);
+#pragma unroll 1   // one copy of the code: most groups need one or two parts, and short sequences run it once a tile
+      for (int part = 0; part * kRedRows < nr; ++part) {   // rows 4 part .. + 3, held by the lanes with g8 / 4 = part mod 2
+        const bool upper = part >> 1;
+        if ((g8 >> 2) == (part & 1)) {
+          const int row = g8 + (upper ? 8 : 0);
+          float2 ml[NW];
+          float M = -INFINITY, L = 0.f;
 #pragma unroll
-      for (int part = 0; part < kRows / kRedRows; ++part) {   // rows 4 part .. + 3, held by the lanes with g8 / 4 = part mod 2
-        if (kRedRows * part < nr) {
-          const int half = part >> 1;
-          if ((g8 >> 2) == (part & 1)) {
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[(w0 + w) * kRows + g8 + 8 * half].x);
-            const float mine = half ? m1 : m0;
-            const float f = mine == -INFINITY ? 0.f : ex2f(mine - M);
-            // row r: groups of 8 values XOR r, no bank twice
-            float* dst = s_red + (warp * kRedRows + (g8 & 3)) * D + 2 * t4;
-            float* at[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) at[k] = dst + ((8 * k) ^ ((g8 & 3) * 8));
-#pragma unroll
-            for (int k = 0; k < 2 * KS; ++k)
-              *reinterpret_cast<float2*>(at[k & 3] + 32 * (k >> 2)) = make_float2(o[k][2 * half] * f, o[k][2 * half + 1] * f);
+          for (int w = 0; w < NW; ++w) {
+            ml[w] = s_ml[(w0 + w) * kRows + row];
+            M = fmaxf(M, ml[w].x);
           }
-          meet();
-          for (int e = me; e < kRedRows * (D / 2); e += 32 * NW) {
-            const int r = e / (D / 2), d = 2 * (e % (D / 2)), row = r + kRedRows * part;
-            if (row < nr) {
-              float M2 = -INFINITY, Ls = 0.f;
-              float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int w = 0; w < NW; ++w) M2 = fmaxf(M2, s_ml[(w0 + w) * kRows + row].x);
+          for (int w = 0; w < NW; ++w) L += ml[w].x == -INFINITY ? ml[w].y : ml[w].y * ex2f(ml[w].x - M);
+          const float own = upper ? m1 : m0;
+          float f = own == -INFINITY ? 0.f : ex2f(own - M);
+          if (whole) f /= L;
+          else if (warp == w0 && t4 == 0 && row < nr) *reinterpret_cast<float2*>(p.ws.ml + (slot * kRows + row) * 2) = make_float2(M, L);
+          // row r: groups of 8 values XOR r, no bank twice
+          float* dst = s_red + (warp * kRedRows + (g8 & 3)) * D + 2 * t4;
+          float* at[4];
 #pragma unroll
-              for (int w = 0; w < NW; ++w) {
-                const float2 ml = s_ml[(w0 + w) * kRows + row];
-                Ls += ml.x == -INFINITY ? ml.y : ml.y * ex2f(ml.x - M2);
-                const float2 v = *reinterpret_cast<const float2*>(s_red + ((w0 + w) * kRedRows + r) * D + (d ^ (r * 8)));
-                acc.x += v.x;
-                acc.y += v.y;
-              }
-              if (whole) {
-                *reinterpret_cast<__nv_bfloat162*>(p.out + ((size_t)g.i * p.Hq + h * p.G + r0 + row) * D + d) =
-                    __floats2bfloat162_rn(acc.x / Ls, acc.y / Ls);
-              } else {
-                *reinterpret_cast<float2*>(p.ws.o + (slot * kRows + row) * D + d) = acc;
-                if (d == 0) *reinterpret_cast<float2*>(p.ws.ml + (slot * kRows + row) * 2) = make_float2(M2, Ls);
-              }
-            }
-          }
-          meet();
+          for (int k = 0; k < 4; ++k) at[k] = dst + ((8 * k) ^ ((g8 & 3) * 8));
+#pragma unroll
+          for (int k = 0; k < 2 * KS; ++k)
+            *reinterpret_cast<float2*>(at[k & 3] + 32 * (k >> 2)) =
+                make_float2((upper ? o[k][2] : o[k][0]) * f, (upper ? o[k][3] : o[k][1]) * f);
         }
+        meet();
+        for (int e = me; e < kRedRows * (D / 2); e += 32 * NW) {
+          const int r = e / (D / 2), d = 2 * (e % (D / 2)), row = r + kRedRows * part;
+          if (row < nr) {
+            float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+              const float2 v = *reinterpret_cast<const float2*>(s_red + ((w0 + w) * kRedRows + r) * D + (d ^ (r * 8)));
+              acc.x += v.x;
+              acc.y += v.y;
+            }
+            if (whole)
+              *reinterpret_cast<__nv_bfloat162*>(p.out + ((size_t)g.i * p.Hq + h * p.G + r0 + row) * D + d) =
+                  __floats2bfloat162_rn(acc.x, acc.y);
+            else
+              *reinterpret_cast<float2*>(p.ws.o + (slot * kRows + row) * D + d) = acc;
+          }
+        }
+        meet();
       }
     };
     if (g.T > 1) join(std::integral_constant<int, kCompWarps>{});
-    else if (mine) join(std::integral_constant<int, kCompWarps / 2>{});
+    else join(std::integral_constant<int, kCompWarps / 2>{});
     if (++qs == qslots) qs = 0, qs_par ^= 1u;
     if (tid == 0 && g.t0 == 0 && !whole)   // the CTA's last run
       p.ws.cut[blockIdx.x] = make_int4(g.i, g.h * p.HB + g.hb, (int)((g.base + g.T - 1) / chunk), 0);
