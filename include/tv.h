@@ -721,8 +721,9 @@ TV_API int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const t
  *   out       device bf16 [n][n_q_heads][head_dim]; a sequence of length 0 gets zeros
  *             (and stores nothing)
  *   workspace device, >= tv_attend_paged_workspace_size(pool, n_q_heads, n)
- * P is rounded to bf16 for the product with V, everything else is fp32.  Slots
- * past a sequence's length are never used, whatever they hold.  The same
+ * fp32 throughout: P enters the product with V as two bf16 parts, and out is
+ * rounded once.  Slots past a sequence's length are never used, whatever they
+ * hold.  The same
  * inputs give the same bits.
  * Host checks: TV_E_ARG, TV_E_UNSUPPORTED (n_q_heads not a multiple of
  * n_kv_heads, n > 2048), TV_E_WORKSPACE.  Device checks: TV_E_SEQ (also a

@@ -177,11 +177,10 @@ def load():
 
 def _p(x) -> Optional[int]:
     """Device/host address of a tensor, an int, or None."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    try:
+        return x.data_ptr()
+    except AttributeError:   # an address already, or None
         return x
-    return int(x.data_ptr())
 
 
 def _arr(ctype, items: Sequence):
