@@ -595,7 +595,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PaPara
   pdl_wait();
   pdl_trigger();
   const int4 cut = __ldcg(p.ws.cut + blockIdx.x);
-  if (cut.x < 0 || status_get(p.status) != 0) return;
+  const int stop = status_get(p.status);
+  if (cut.x < 0 || stop != 0) return;
   const int c0 = blockIdx.x, np = cut.z - c0 + 1, r0 = (cut.y % p.HB) * kRows, nr = min(kRows, p.G - r0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto slot = [&](int c) { return (size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0); };

@@ -16,7 +16,8 @@
 namespace tv {
 namespace {
 
-constexpr int kListThreads = 256;    // block of the per-sequence kernels
+constexpr int kListThreads = 256;    // block of the kernels that move rows and pages
+constexpr int kSeqThreads = 1024;    // block of the kernels that follow a sequence's pages: few rounds of dependent loads
 constexpr int kPlanThreads = 1024;   // the one block that allocates
 
 // what a block found wrong with its list; the lowest bit is reported, so that
@@ -29,7 +30,7 @@ __device__ __forceinline__ int bad_code(uint32_t bad) {
 // ---- releasing and forking ---------------------------------------------------
 // one block per listed sequence: index, length and page entries in range, no
 // index listed twice
-__global__ void __launch_bounds__(kListThreads) release_check_kernel(tv_pool pool, tv_seqs t, const int32_t* ids,
+__global__ void __launch_bounds__(kSeqThreads) release_check_kernel(tv_pool pool, tv_seqs t, const int32_t* ids,
                                                                      const int32_t* keep, int n, int32_t* status) {
   pdl_wait();
   pdl_trigger();
@@ -39,7 +40,7 @@ __global__ void __launch_bounds__(kListThreads) release_check_kernel(tv_pool poo
   if (s < 0 || s >= t.max_seqs) {
     bad = TV_E_SEQ;
   } else {
-    for (int j = threadIdx.x; j < n; j += kListThreads)
+    for (int j = threadIdx.x; j < n; j += kSeqThreads)
       if (j != i && ids[j] == s) bad = TV_E_SEQ;
     const int len = seq_len(t, pool.page_size, s);
     const int kept = keep[i];
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(kListThreads) release_check_kernel(tv_pool poo
       bad = TV_E_SEQ;
     } else {
       const int32_t* row = t.pages + (size_t)s * t.max_pages;
-      for (int j = pages_of(kept, pool.page_size) + threadIdx.x; j < pages_of(len, pool.page_size); j += kListThreads) {
+      for (int j = pages_of(kept, pool.page_size) + threadIdx.x; j < pages_of(len, pool.page_size); j += kSeqThreads) {
         const int p = __ldcg(row + j);
         if (p < 0 || p >= pool.n_pages || __ldcg(pool.refs + p) < 1) bad = TV_E_PAGE;
       }
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(kListThreads) release_check_kernel(tv_pool poo
   if (bad) status_set(status, bad);
 }
 
-__global__ void __launch_bounds__(kListThreads) release_kernel(tv_pool pool, tv_seqs t, const int32_t* ids,
+__global__ void __launch_bounds__(kSeqThreads) release_kernel(tv_pool pool, tv_seqs t, const int32_t* ids,
                                                                const int32_t* keep, int32_t* status) {
   pdl_wait();
   pdl_trigger();
@@ -64,13 +65,13 @@ __global__ void __launch_bounds__(kListThreads) release_kernel(tv_pool pool, tv_
   const int s = ids[blockIdx.x], kept = keep[blockIdx.x];
   const int len = __ldcg(t.lens + s);
   const int32_t* row = t.pages + (size_t)s * t.max_pages;
-  for (int j = pages_of(kept, pool.page_size) + threadIdx.x; j < pages_of(len, pool.page_size); j += kListThreads)
+  for (int j = pages_of(kept, pool.page_size) + threadIdx.x; j < pages_of(len, pool.page_size); j += kSeqThreads)
     atomicSub(pool.refs + __ldcg(row + j), 1);
   __syncthreads();   // every thread has the old length
   if (threadIdx.x == 0) t.lens[s] = kept;
 }
 
-__global__ void __launch_bounds__(kListThreads) fork_check_kernel(tv_pool pool, tv_seqs t, const int32_t* src,
+__global__ void __launch_bounds__(kSeqThreads) fork_check_kernel(tv_pool pool, tv_seqs t, const int32_t* src,
                                                                   const int32_t* dst, int n, int32_t* status) {
   pdl_wait();
   pdl_trigger();
@@ -80,14 +81,14 @@ __global__ void __launch_bounds__(kListThreads) fork_check_kernel(tv_pool pool, 
   if (s < 0 || s >= t.max_seqs || d < 0 || d >= t.max_seqs) {
     bad = TV_E_SEQ;
   } else {
-    for (int j = threadIdx.x; j < n; j += kListThreads)
+    for (int j = threadIdx.x; j < n; j += kSeqThreads)
       if ((j != i && dst[j] == d) || src[j] == d) bad = TV_E_SEQ;
     const int len = seq_len(t, pool.page_size, s);
     if (len < 0 || __ldcg(t.lens + d) != 0) {
       bad = TV_E_SEQ;
     } else {
       const int32_t* row = t.pages + (size_t)s * t.max_pages;
-      for (int j = threadIdx.x; j < pages_of(len, pool.page_size); j += kListThreads) {
+      for (int j = threadIdx.x; j < pages_of(len, pool.page_size); j += kSeqThreads) {
         const int p = __ldcg(row + j);
         if (p < 0 || p >= pool.n_pages || __ldcg(pool.refs + p) < 1) bad = TV_E_PAGE;
       }
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kListThreads) fork_check_kernel(tv_pool pool, 
   if (bad) status_set(status, bad);
 }
 
-__global__ void __launch_bounds__(kListThreads) fork_kernel(tv_pool pool, tv_seqs t, const int32_t* src,
+__global__ void __launch_bounds__(kSeqThreads) fork_kernel(tv_pool pool, tv_seqs t, const int32_t* src,
                                                             const int32_t* dst, int32_t* status) {
   pdl_wait();
   pdl_trigger();
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kListThreads) fork_kernel(tv_pool pool, tv_seq
   const int len = __ldcg(t.lens + s);
   const int32_t* from = t.pages + (size_t)s * t.max_pages;
   int32_t* to = t.pages + (size_t)d * t.max_pages;
-  for (int j = threadIdx.x; j < pages_of(len, pool.page_size); j += kListThreads) {
+  for (int j = threadIdx.x; j < pages_of(len, pool.page_size); j += kSeqThreads) {
     const int p = __ldcg(from + j);
     to[j] = p;
     atomicAdd(pool.refs + p, 1);
@@ -648,9 +649,9 @@ int tv_pages_release(const tv_pool* pool, const tv_seqs* seqs, const int32_t* id
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (one_block(*seqs, n))
     return launch_pdl(list_block_kernel<false>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, ids, keep, n, n_slices(*seqs), dev_status);
-  rc = launch_pdl(release_check_kernel, dim3(n), dim3(kListThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
+  rc = launch_pdl(release_check_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
   if (rc) return rc;
-  return launch_pdl(release_kernel, dim3(n), dim3(kListThreads), 0, st, *pool, *seqs, ids, keep, dev_status);
+  return launch_pdl(release_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, dev_status);
 }
 
 int tv_pages_fork(const tv_pool* pool, const tv_seqs* seqs, const int32_t* src, const int32_t* dst, int n,
@@ -662,9 +663,9 @@ int tv_pages_fork(const tv_pool* pool, const tv_seqs* seqs, const int32_t* src, 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (one_block(*seqs, n))
     return launch_pdl(list_block_kernel<true>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, src, dst, n, n_slices(*seqs), dev_status);
-  rc = launch_pdl(fork_check_kernel, dim3(n), dim3(kListThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
+  rc = launch_pdl(fork_check_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
   if (rc) return rc;
-  return launch_pdl(fork_kernel, dim3(n), dim3(kListThreads), 0, st, *pool, *seqs, src, dst, dev_status);
+  return launch_pdl(fork_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, dev_status);
 }
 
 int tv_pages_extend(const tv_pool* pool, const tv_seqs* seqs, const int32_t* ids, const int32_t* add, int n,
