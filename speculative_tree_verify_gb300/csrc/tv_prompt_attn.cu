@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kPrSoftWarps = 16;                 // 8 a query tile
 constexpr int kPrSoftThreads = kPrSoftWarps * 32;
-constexpr int kWarpMma = kPrSoftWarps, kWarpTma = kPrSoftWarps + 1, kWarpPlan = kPrSoftWarps + 2;
+constexpr int kWarpMma = kPrSoftWarps, kWarpTma = kPrSoftWarps + 1, kWarpPlan = kPrSoftWarps + 2, kWarpLook = kPrSoftWarps + 3;
 constexpr int kPrThreads = kPrSoftThreads + 128;  // a whole warpgroup for the four roles' registers
 // 640 threads of 96 registers at launch; 512 x 104 + 128 x 64 is the same sum
 constexpr int kSoftRegs = 104, kRoleRegs = 64;
@@ -256,8 +256,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* s_full = v_free + 2;                                         // [2] S_s done (and every product before it)
   uint64_t* p_full = s_full + 2;                                         // [2] P_s stored, O_s rescaled (8 warps)
   uint64_t* o_fin = p_full + 2;                                          // [2] the last product into O_s done
-  // a window's V looked over (16 warps): two barriers in turn, since the warps
-  // may be a window ahead of the products
+  // a window's V looked over: two barriers in turn, since the look may be a
+  // window ahead of the products
   uint64_t* v_ok = o_fin + 2;
   uint64_t* w_full = v_ok + 2;                                           // [2] a place written down
   uint64_t* w_free = w_full + 2;                                         // [2] every role has read it
@@ -282,9 +282,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], kPrSoftWarps / 2);
       mbar_init(&o_fin[s], 1);
-      mbar_init(&v_ok[s], kPrSoftWarps);
+      mbar_init(&v_ok[s], 1);
       mbar_init(&w_full[s], 1);
-      mbar_init(&w_free[s], kPrSoftWarps + 2);
+      mbar_init(&w_free[s], kPrSoftWarps + 3);
       s_anybad[s] = 0;
     }
     mbar_init(drain, 1);
@@ -555,6 +555,75 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       commit_by(drain, leader);
       mbar_wait(drain, 0);
     }
+  } else if (warp == kWarpLook) {
+    // ---------------- V rows that a row may not see ----------------
+    bool ok = true;
+    int kv = 0, looked = 0, nf = 0;   // windows, windows looked over, places with two tiles before this place
+    for (int it = 0;; ++it) {
+      wait_work(it, ok);
+      const Work k = read_work(it, ok);
+      free_work(it);
+      if (k.len == 0) break;
+      // An entry of `bad` is the place's complement and the key, so that the
+      // smallest is the latest place's first key; what two places before left
+      // behind is larger.
+      unsigned long long* bad = s_bad + (it & 1) * 3 * D;
+      const unsigned tag = (unsigned)it + 1u;
+      for (int w = 0; w < k.nwin && scrub(k, w); ++w, ++looked) {
+        const int i = kv + w;
+        if (ok && !mbar_wait(&v_full[i & 1], (uint32_t)(i >> 1) & 1u)) ok = false;
+        uint8_t* sv = smem + L::OFF_V + (i & 1) * L::TILE;
+        // rows of this pair's tokens but the first are looked at, those behind its last token emptied
+        const int key0 = w_start(k, w), first = max(0, k.t0 + 1 - key0), last = min(128, k.hi - key0);
+        constexpr int CH = D / 8;   // 16-byte pieces of a row, 32 / CH rows a step
+        bool wrote = last < 128;
+        const int c = lane % CH;
+        uint8_t* piece = sv + (c >> 3) * kAtomP;
+        for (int row = last + lane / CH; row < 128; row += 32 / CH)
+          *reinterpret_cast<uint4*>(piece + swz(row, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
+        constexpr int BATCH = 8;
+        for (int r0 = first + lane / CH; r0 < last; r0 += BATCH * (32 / CH)) {
+          uint4 y[BATCH];
+          uint32_t any = 0u;
+#pragma unroll
+          for (int u = 0; u < BATCH; ++u) {
+            const int row = r0 + u * (32 / CH);
+            y[u] = row < last ? *reinterpret_cast<const uint4*>(piece + swz(row, c & 7)) : make_uint4(0u, 0u, 0u, 0u);
+          }
+          // an exponent of all ones carries into the sign's place
+#pragma unroll
+          for (int u = 0; u < BATCH; ++u)
+            any |= ((y[u].x & 0x7f807f80u) + 0x00800080u) | ((y[u].y & 0x7f807f80u) + 0x00800080u) |
+                   ((y[u].z & 0x7f807f80u) + 0x00800080u) | ((y[u].w & 0x7f807f80u) + 0x00800080u);
+          if (any & 0x80008000u) {
+#pragma unroll 1
+            for (int row = r0; row < last && row < r0 + BATCH * (32 / CH); row += 32 / CH) {
+              uint16_t* x = reinterpret_cast<uint16_t*>(piece + swz(row, c & 7));
+#pragma unroll 1
+              for (int u = 0; u < 8; ++u) {
+                const uint32_t b = x[u];
+                if ((b & 0x7f80u) == 0x7f80u) {
+                  const int kind = (b & 0x7fu) ? 0 : (b & 0x8000u ? 2 : 1);   // NaN, +inf, -inf
+                  atomicMin(&bad[kind * D + c * 8 + u], (unsigned long long)~tag << 32 | (unsigned)(key0 + row));
+                  x[u] = 0;
+                }
+              }
+            }
+            *reinterpret_cast<volatile unsigned*>(&s_anybad[it & 1]) = tag;
+            wrote = true;
+          }
+        }
+        if (wrote) fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_ok[looked & 1]);
+      }
+      kv += k.nwin;
+      // to the place's end: every window before the next place's first has
+      // landed then, so that the wait for that one is for its own phase
+      if (ok && !mbar_wait(&o_fin[k.nst - 1], (uint32_t)(k.nst == 2 ? nf : it) & 1u)) ok = false;
+      nf += k.nst - 1;
+    }
+    if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
   }
   } else {
     // ---------------- softmax: warps 8 s .. 8 s + 7 hold tile s, thread pairs a row ----------------
@@ -567,8 +636,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const int pair = 1 + s * 4 + (warp & 3);   // named barrier of the two warps that share rows
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     const int rt = r / p.G;                    // token of the row in its tile
+    const int ot = (s * p.T + rt) * p.Hq + r % p.G;   // the row's place in the output, from the tile pair's and group's first
     bool ok = true;
-    int kv = 0, looked = 0, ns = 0, nf = 0;    // windows, windows looked over, score tiles, finished outputs before this place
+    int ns = 0, nf = 0;                        // score tiles, finished outputs before this place
 
     for (int it = 0;; ++it) {
       wait_work(it, ok);
@@ -581,43 +651,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       // infinite offset keeps them out of every decision
       const bool live = r < p.T * p.G && t < k.len;
       float m = live ? kFirst : INFINITY, l = 0.f;   // offset of the row; sum over this thread's keys
-      unsigned long long* bad = s_bad + (it & 1) * 3 * D;
-      const unsigned tag = (unsigned)it + 1u;
-
-      // V rows of keys past the first token.  An entry of `bad` is the place's
-      // complement and the key, so that the smallest is the latest place's first
-      // key; what two places before left behind is larger.
-      auto look_over = [&](int w) {
-        const int i = kv + w;
-        if (ok && !mbar_wait(&v_full[i & 1], (uint32_t)(i >> 1) & 1u)) ok = false;
-        uint8_t* sv = smem + L::OFF_V + (i & 1) * L::TILE;
-        const int key0 = w_start(k, w), first = max(0, k.t0 + 1 - key0);
-        bool wrote = false;
-        for (int e = tid; e < (128 - first) * (D / 8); e += kPrSoftThreads) {
-          const int row = first + e / (D / 8), c = e % (D / 8);
-          uint32_t* x = reinterpret_cast<uint32_t*>(sv + (c >> 3) * kAtomP + swz(row, c & 7));
-          const uint4 y = *reinterpret_cast<const uint4*>(x);
-          // an exponent of all ones carries into the sign's place
-          const uint32_t any = ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
-                               ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
-          if (any & 0x80008000u) {
-            for (int u = 0; u < 8; ++u) {
-              const uint32_t b = (x[u >> 1] >> (16 * (u & 1))) & 0xffffu;
-              if ((b & 0x7f80u) == 0x7f80u) {
-                const int kind = (b & 0x7fu) ? 0 : (b & 0x8000u ? 2 : 1);   // NaN, +inf, -inf
-                atomicMin(&bad[kind * D + c * 8 + u], (unsigned long long)~tag << 32 | (unsigned)(key0 + row));
-                x[u >> 1] &= u & 1 ? 0x0000ffffu : 0xffff0000u;
-              }
-            }
-            *reinterpret_cast<volatile unsigned*>(&s_anybad[it & 1]) = tag;
-            wrote = true;
-          }
-        }
-        if (wrote) fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_ok[looked & 1]);
-        ++looked;
-      };
 
       // One window.  The exponentials are taken at the offset that the row has,
       // kFirst to begin with: what matters is that the offset lies within some
@@ -718,28 +751,21 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[s]);
       };
 
-      // the windows that hide something, or are the first
-      int w = 0;
-      for (; w < k.nwin; ++w) {
-        const int start = w_start(k, w);
-        const bool masked = start + 127 > tmin, look = scrub(k, w);
-        // rows without a key: all in the first window, and those before a window that hid it all
-        const int before = w == f ? 0x7fffffff : start + 128;
-        if (!look && (!active || (w > f && !masked && before <= tmin))) break;
-        if (active && w >= f) {
+      if (active) {
+        // the windows that hide something, or are the first
+        int w = f;
+        for (; w < k.nwin; ++w) {
+          const int start = w_start(k, w);
+          const bool masked = start + 127 > tmin;
+          // rows without a key: all in the first window, and those before a window that hid it all
+          const int before = w == f ? 0x7fffffff : start + 128;
+          if (w > f && !masked && before <= tmin) break;
           if (masked) window(std::true_type{}, std::true_type{}, t - start - 64 * hf, before, w > f);
           else window(std::false_type{}, std::true_type{}, 0, before, w > f);
         }
-        if (look) look_over(w);   // V lands while the first softmax runs
-      }
-      // and all the others
-      if (active)
+        // and all the others
         for (; w < k.nwin; ++w) window(std::false_type{}, std::false_type{}, 0, 0, true);
-      kv += k.nwin;
-      // the place's end, for the warps of a tile that it does not have too:
-      // nobody runs ahead of the loads by more than a phase
-      if (ok && !mbar_wait(&o_fin[active ? s : 0], (uint32_t)(active && s == 1 ? nf : it) & 1u)) ok = false;
-      if (active) {
+        if (ok && !mbar_wait(&o_fin[s], (uint32_t)nf & 1u)) ok = false;
         ++nf;
         s_sum[hf * 128 + r] = l;
         pair_sync(pair);
@@ -748,8 +774,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const Work k = read_work(it, true);   // read once more: not held through the windows
         const int t = k.t0 + s * p.T + rt;
         const bool live = r < p.T * p.G && t < k.len;
+        const unsigned tag = (unsigned)it + 1u;
+        const unsigned long long* bad = s_bad + (it & 1) * 3 * D;
         const bool anybad = *reinterpret_cast<volatile unsigned*>(&s_anybad[it & 1]) == tag;
-        __nv_bfloat16* dst = p.out + ((size_t)(k.row0 + t) * p.Hq + k.h * p.G + r % p.G) * D + hf * (D / 2);
+        __nv_bfloat16* dst = p.out + ((size_t)(k.row0 + k.t0) * p.Hq + k.h * p.G + ot) * D + hf * (D / 2);
 #pragma unroll
         for (int c = 0; c < D / 2; c += 32) {
           uint32_t o[32];
