@@ -657,7 +657,8 @@ typedef struct tv_seqs {
  * Device checks: TV_E_SEQ, TV_E_CAPACITY (a token past the length); TV_E_PAGE
  * (that row alone is left out).
  *
- * Host checks of all: TV_E_ARG (null or misaligned pointers, n < 1, a bad
+ * The workspace and the pool's tables belong to one call at a time: order
+ * calls that share them on one stream.  Host checks of all: TV_E_ARG (null or misaligned pointers, n < 1, a bad
  * layer), TV_E_UNSUPPORTED (n > 4096, shapes outside the above),
  * TV_E_WORKSPACE.
  */
@@ -720,7 +721,10 @@ TV_API int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const t
  *             aligned: the Q, K and V heads of a QKV projection's rows)
  *   out       device bf16 [n][n_q_heads][head_dim]; a sequence of length 0 gets zeros
  *             (and stores nothing)
- *   workspace device, >= tv_attend_paged_workspace_size(pool, n_q_heads, n)
+ *   workspace device, >= tv_attend_paged_workspace_size(pool, n_q_heads, n); used by one
+ *             call at a time (calls on one stream may share it, captured or not)
+ * With k_new a sequence's last page must be its own (tv_pages_extend sees to
+ * it).
  * fp32 throughout: P enters the product with V as two bf16 parts, and out is
  * rounded once.  Slots past a sequence's length are never used, whatever they
  * hold.  The same

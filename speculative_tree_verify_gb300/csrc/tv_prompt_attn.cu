@@ -829,6 +829,14 @@ int launch_prompt(PrParams& p, const void* q, const void* k, const void* v, size
     return rc;
   static std::atomic<bool> attr[64];
   if (ensure_smem_limit(prompt_attn_kernel<D>, PrSmem<D>::BYTES, attr)) return TV_E_CUDA;
+  // the roles' register split must not ask for more than the launch brings
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, prompt_attn_kernel<D>) != cudaSuccess) return TV_E_CUDA;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) * kPrThreads < kPrSoftThreads * kSoftRegs + 128 * kRoleRegs) return TV_E_UNSUPPORTED;
   // at most rows / 2T whole pairs and one ragged pair a sequence
   const long long pairs = (long long)p.rows / (2 * p.T) + (p.n < p.rows ? p.n : p.rows);
   const int sms = num_sms();

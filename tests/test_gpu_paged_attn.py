@@ -226,6 +226,21 @@ def test_listed_twice_without_new_rows(gpu):
     assert np.array_equal(host(c.out)[0], host(c.out)[1])
 
 
+def test_two_calls_at_once(gpu):
+    """On two streams, each with its own pool, workspace and status."""
+    cs = [Case([3000 + 500 * i, 70, 1], 8, 2, 128, 16, seed=30 + i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s in zip(cs, streams):
+            assert c.run(s) == 0
+    torch.cuda.synchronize()
+    got = [c.out.clone() for c in cs]
+    for c, g in zip(cs, got):
+        c.check()
+        assert torch.equal(c.out, g)
+
+
 def test_graphs_share_a_workspace_and_lengths_grow(gpu):
     """Two captured calls on one workspace; replayed as the lengths change, each gives what a plain call gives, twice."""
     a, b = Case([900, 77, 5], 8, 2, 128, 16, seed=1, new=False), Case([64, 2000, 1], 8, 2, 128, 16, seed=2, new=False)

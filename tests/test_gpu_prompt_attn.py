@@ -134,6 +134,32 @@ def test_what_a_row_may_not_see_does_not_reach_it(gpu, value, q_heads, kv_heads,
     assert np.isfinite(k[:20]).all() and np.isnan(k[20:lens[0], :q_heads // kv_heads]).all() and np.isfinite(k[lens[0]:]).all()
 
 
+def test_separate_tensors_with_strides_of_their_own(gpu):
+    p = Prompt([150, 70], 6, 2, 64, seed=12)
+    o, off = attend_prompt(bf16_to_f64(p.q), bf16_to_f64(p.k), bf16_to_f64(p.v), p.starts, True)
+    q, k, v = dev(p.q), dev(np.pad(p.k.reshape(220, -1), ((0, 0), (0, 24)), constant_values=NAN)), None
+    v = dev(np.pad(p.v.reshape(220, -1), ((0, 0), (0, 24)), constant_values=NAN))
+    assert abi.tv_attend_prompt(6, 2, 64, q, k, v, 384, 152, p.gstarts, 2, 220, p.out, p.status) == 0
+    assert int(p.status.item()) == 0
+    close(bf16_to_f64(host(p.out)), o, off)
+
+
+def test_two_calls_at_once(gpu):
+    """On two streams, each on its own tensors and status."""
+    ps = [Prompt([900 + 300 * i, 5], 8, 2, 128, seed=20 + i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for p, s in zip(ps, streams):
+            assert p.run(s) == 0
+    torch.cuda.synchronize()
+    got = [p.out.clone() for p in ps]
+    for p, g in zip(ps, got):
+        assert int(p.status.item()) == 0
+        p.check()
+        assert torch.equal(p.out, g)
+
+
 def test_refusals(gpu):
     for starts in ([5, 4, 6], [-1, 4, 6], [0, 4, 101], [0, 101, 100]):
         p = Prompt([40, 60], 4, 2, 64)
