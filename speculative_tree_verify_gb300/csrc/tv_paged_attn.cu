@@ -6,7 +6,7 @@
 // heads, far below the tensor cores' rate, so the kernel is built as a stream
 // over memory.  The work is the list of 64-token tiles of every (sequence, KV
 // head, block of 16 query heads) in that order, each such head block counted
-// SEG_COST tiles more for what it costs to begin and end; CTA c takes an
+// kSegCost tiles more for what it costs to begin and end; CTA c takes an
 // equal, contiguous range of it, whatever the lengths, so one long context
 // among short ones and one sequence alone both fill every SM.  A head block cut by a range
 // border leaves unnormalised partials that paged_merge_kernel joins in tile
@@ -47,6 +47,10 @@ constexpr int kQueries = 8;                      // segments whose queries are l
 constexpr int kMaxTokens = 2048;                 // sequences of one call: their places fit shared memory beside the stages
 constexpr int kInfo = 640;                       // up to here their table rows and lengths do, too
 constexpr int kRedRows = 4;                      // rows joined at a time when a head block ends
+// What a head block costs besides its tiles, in tiles (its queries, its join).
+// 48 sequences of 1 to 8191 tokens, 8/2 heads, with 0, 1, 2, 4 tiles: 19.4,
+// 16.4, 15.0, 16.3 us (D = 128; 1 and 2 of 64 values: 13.9, 12.6 us).
+constexpr int kSegCost = 2;
 constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 a CTA
 constexpr float kMoveLog2 = 8.f;
 
@@ -76,7 +80,6 @@ struct PaSmem {
   static constexpr int HALF = (D / 64) * SLAB;               // a tile's K (or V)
   static constexpr int STAGE = 2 * HALF;
   static constexpr int OFF_RED = kStages * STAGE;            // [8 warps][kRedRows][D] fp32; the marks of listed rows first
-  static constexpr int SEG_COST = 256 / D;                   // what a head block costs besides its tiles, in tiles
   static constexpr int OFF_ML = OFF_RED + kCompWarps * kRedRows * D * 4;
   static constexpr int Q_ROW = D * 2 + 16;                   // rows 16 bytes apart in the banks: ldmatrix without conflicts
   static constexpr int OFF_Q = OFF_ML + kCompWarps * kRows * 8;   // 2 kRows query rows: those of the next 2 to kQueries segments
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   // ---- the list of tiles: every CTA reads the same lengths and finds the same list
   uint32_t all;
   auto head_tiles = [&](int len) {   // of one head block, its fixed cost included; the host has seen to it that all fit 31 bits
-    return len > 0 ? (uint32_t)(tiles_of(len) + L::SEG_COST) : 0u;
+    return len > 0 ? (uint32_t)(tiles_of(len) + kSegCost) : 0u;
   };
   auto look = [&](int i, int& s) {   // length of listed sequence i, -1: refused
     s = __ldg(p.ids + i);
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   auto bound = [&](Run& g) { g.t1 = hi > g.base ? (int)min((uint32_t)g.T, hi - g.base) : 0; };
   auto next_run = [&](Run& g) {   // false: there is none
     if (g.base + g.T >= hi) return false;
-    g.base += g.T + L::SEG_COST;
+    g.base += g.T + kSegCost;
     if (++g.hb == p.HB) {
       g.hb = 0;
       if (++g.h == Hkv) {
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         int i = g.i + 1;
         while (s_first[i + 1] == s_first[i]) ++i;
         sequence(g, i);
-        g.base = s_first[i] + L::SEG_COST;
+        g.base = s_first[i] + kSegCost;
       }
     }
     g.t0 = 0;
@@ -288,10 +291,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       else b = mid - 1;
     }
     sequence(g, i);
-    const uint32_t unit = g.T + L::SEG_COST, hh = (lo - s_first[i]) / unit;
+    const uint32_t unit = g.T + kSegCost, hh = (lo - s_first[i]) / unit;
     g.h = (int)(hh / p.HB);
     g.hb = (int)(hh % p.HB);
-    g.base = s_first[i] + hh * unit + L::SEG_COST;
+    g.base = s_first[i] + hh * unit + kSegCost;
     g.t0 = lo > g.base ? (int)(lo - g.base) : 0;
     bound(g);
     return g.t0 < g.t1 || next_run(g);

@@ -115,23 +115,29 @@ __global__ void __launch_bounds__(kSeqThreads) fork_kernel(tv_pool pool, tv_seqs
 }
 
 // Releasing (FORK = false: a = ids, b = keep) or forking (a = src, b = dst) by
-// one block: a warp for kSlice table entries of one listed sequence, which it
-// holds in registers between the look and the act.  Such a call is a chain of
-// dependent loads (list, length and entries, counts) and its launches.
+// one block, a warp a listed sequence, which holds its table entries in
+// registers between the look and the act.  Such a call is a chain of dependent
+// loads (list, length and entries, counts), about 0.6 us each, and its
+// launches, 2 to 3 us each; one SM's atomics are what it can run out of.  A
+// pass of release, fork, extend, release took, by one block against two
+// launches a call: 14.7 against 18.1 us for 8 sequences of 65 pages, but 24.0
+// against 18.9 us for 8 of 494 and 40.3 against 25.4 us for 32 of 494.
 constexpr int kBlockThreads = 1024;
-constexpr int kSlice = 512;
-inline int n_slices(const tv_seqs& t) { return (t.max_pages + kSlice - 1) / kSlice; }
+constexpr int kWarpEntries = 512;     // table entries a warp's registers hold
+constexpr int kBlockEntries = 1024;   // and those a block takes on
+inline bool one_block(const tv_seqs& t, int n) {
+  return n <= kBlockThreads / 32 && t.max_pages <= kWarpEntries && n * t.max_pages <= kBlockEntries;
+}
 
 template <bool FORK>
 __global__ void __launch_bounds__(kBlockThreads) list_block_kernel(tv_pool pool, tv_seqs t, const int32_t* a,
-                                                                   const int32_t* b, int n, int slices, int32_t* status) {
-  const int lane = threadIdx.x & 31, item = threadIdx.x >> 5, ps = pool.page_size;
-  const int i = item / slices, j0 = (item % slices) * kSlice + lane;
+                                                                   const int32_t* b, int n, int32_t* status) {
+  const int lane = threadIdx.x & 31, i = threadIdx.x >> 5, ps = pool.page_size;
   pdl_wait();
   pdl_trigger();
   const bool skip = status_get(status) != 0;
   int bad = 0, s = 0, d = 0, len = 0, first = 0, last = 0;
-  int e[kSlice / 32];
+  int e[kWarpEntries / 32];
   if (i < n) {
     s = __ldg(a + i);
     d = __ldg(b + i);   // forking: the target row; releasing: the tokens kept
@@ -140,8 +146,8 @@ __global__ void __launch_bounds__(kBlockThreads) list_block_kernel(tv_pool pool,
     } else {
       const int32_t* row = t.pages + (size_t)s * t.max_pages;
 #pragma unroll
-      for (int k = 0; k < kSlice / 32; ++k)   // with the length on its way
-        if (j0 + 32 * k < t.max_pages) e[k] = __ldcg(row + j0 + 32 * k);
+      for (int k = 0; k < kWarpEntries / 32; ++k)   // with the length on its way
+        if (lane + 32 * k < t.max_pages) e[k] = __ldcg(row + lane + 32 * k);
       len = seq_len(t, ps, s);
       if (len < 0 || (FORK ? __ldcg(t.lens + d) != 0 : d < 0 || d > len)) bad = TV_E_SEQ;
     }
@@ -149,14 +155,14 @@ __global__ void __launch_bounds__(kBlockThreads) list_block_kernel(tv_pool pool,
       first = FORK ? 0 : pages_of(d, ps);
       last = pages_of(len, ps);
 #pragma unroll
-      for (int k = 0; k < kSlice / 32; ++k) {
-        const int j = j0 + 32 * k;
+      for (int k = 0; k < kWarpEntries / 32; ++k) {
+        const int j = lane + 32 * k;
         if (j >= first && j < last && (e[k] < 0 || e[k] >= pool.n_pages || __ldcg(pool.refs + e[k]) < 1)) bad = TV_E_PAGE;
       }
     }
   }
   // no row listed twice; forking: no target among the sources (n <= 32: a lane a sequence)
-  if (item == 0) {
+  if (i == 0) {
     const int sa = lane < n ? __ldg(a + lane) : -1 - lane, sb = lane < n ? __ldg(b + lane) : -1 - lane;
     const bool twice = __popc(__match_any_sync(0xffffffffu, FORK ? sb : sa)) > 1;
     bool among = false;
@@ -167,8 +173,8 @@ __global__ void __launch_bounds__(kBlockThreads) list_block_kernel(tv_pool pool,
   if (__syncthreads_or(bad) || skip || i >= n) return;
   int32_t* to = t.pages + (size_t)d * t.max_pages;
 #pragma unroll
-  for (int k = 0; k < kSlice / 32; ++k) {
-    const int j = j0 + 32 * k;
+  for (int k = 0; k < kWarpEntries / 32; ++k) {
+    const int j = lane + 32 * k;
     if (j >= first && j < last) {
       if (FORK) {
         to[j] = e[k];
@@ -178,11 +184,8 @@ __global__ void __launch_bounds__(kBlockThreads) list_block_kernel(tv_pool pool,
       }
     }
   }
-  if (item % slices == 0 && lane == 0) t.lens[FORK ? d : s] = FORK ? len : d;
+  if (lane == 0) t.lens[FORK ? d : s] = FORK ? len : d;
 }
-
-// one block when its 32 warps hold every entry the list can name
-inline bool one_block(const tv_seqs& t, int n) { return (long long)n * n_slices(t) <= kBlockThreads / 32; }
 
 // ---- extending -----------------------------------------------------------------
 // exclusive sum over the block's threads; *total = the sum of all
@@ -648,7 +651,7 @@ int tv_pages_release(const tv_pool* pool, const tv_seqs* seqs, const int32_t* id
   if ((rc = check_listed(n))) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (one_block(*seqs, n))
-    return launch_pdl(list_block_kernel<false>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, ids, keep, n, n_slices(*seqs), dev_status);
+    return launch_pdl(list_block_kernel<false>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
   rc = launch_pdl(release_check_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
   if (rc) return rc;
   return launch_pdl(release_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, dev_status);
@@ -662,7 +665,7 @@ int tv_pages_fork(const tv_pool* pool, const tv_seqs* seqs, const int32_t* src, 
   if ((rc = check_listed(n))) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (one_block(*seqs, n))
-    return launch_pdl(list_block_kernel<true>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, src, dst, n, n_slices(*seqs), dev_status);
+    return launch_pdl(list_block_kernel<true>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
   rc = launch_pdl(fork_check_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
   if (rc) return rc;
   return launch_pdl(fork_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, dev_status);
