@@ -3,7 +3,6 @@ fails) and the oracle's own rules by hand on a small pool."""
 import numpy as np
 import pytest
 
-from oracle.paged import Cache, Refused, attend, attend_prompt
 from speculative_tree_verify_gb300 import abi, build
 
 FAKE = 0x10000   # 16-byte aligned, never dereferenced on these paths
@@ -118,24 +117,26 @@ def test_workspace_refuses_bad_shapes():
         abi.tv_pages_workspace_size(_pool(), _seqs(max_pages=0))
 
 
-# ---- the oracle by hand -------------------------------------------------------
-def _cache(n_pages=6, max_seqs=4, max_pages=3):
+# ---- the oracle by hand, and with planted mistakes ------------------------------
+def _cache(P, n_pages=6, max_seqs=4, max_pages=3):
     k = np.arange(2 * n_pages * 16 * 4, dtype=np.uint16).reshape(2, n_pages, 1, 16, 4)
-    return Cache(k.copy(), k + 7, np.zeros(n_pages, np.int32), np.full((max_seqs, max_pages), -9, np.int32), np.zeros(max_seqs, np.int32))
+    return P.Cache(k.copy(), k + 7, np.zeros(n_pages, np.int32), np.full((max_seqs, max_pages), -9, np.int32), np.zeros(max_seqs, np.int32))
 
 
-def test_oracle_extend_fork_release():
-    c = _cache()
+def _pin_pages(P):
+    c = _cache(P)
     c.extend([2, 0], [17, 16])
     assert c.pages[2].tolist() == [0, 1, -9] and c.pages[0].tolist() == [2, -9, -9]
     assert c.refs.tolist() == [1, 1, 1, 0, 0, 0] and c.lens.tolist() == [16, 0, 17, 0]
     c.fork([2, 2], [1, 3])
     assert c.refs.tolist() == [3, 3, 1, 0, 0, 0] and c.lens.tolist() == [16, 17, 17, 17]
-    old = c.k[:, 1].copy()
+    old = c.k[:, 1].copy(), c.v[:, 1].copy()
     c.extend([1, 2, 3, 0], [1, 2, 3, 0])   # three holders of page 1: the last in the list keeps it
     assert c.pages[1].tolist() == [0, 3, -9] and c.pages[2].tolist() == [0, 4, -9] and c.pages[3].tolist() == [0, 1, -9]
-    assert c.refs.tolist() == [3, 1, 1, 1, 1, 0] and (c.k[:, 3] == old).all() and (c.k[:, 4] == old).all()
-    with pytest.raises(Refused, match="CAPACITY"):
+    assert c.refs.tolist() == [3, 1, 1, 1, 1, 0]
+    for p in (3, 4):
+        assert (c.k[:, p] == old[0]).all() and (c.v[:, p] == old[1]).all()
+    with pytest.raises(P.Refused, match="CAPACITY"):
         c.extend([0, 3], [16, 14])
     assert c.lens.tolist() == [16, 18, 19, 20] and c.refs.tolist() == [3, 1, 1, 1, 1, 0]
     c.release([1, 3], [0, 16])
@@ -144,21 +145,70 @@ def test_oracle_extend_fork_release():
     remap, used = c.compact()
     assert used == 3 and remap.tolist() == [0, -1, 2, -1, 1, -1] and c.refs.tolist() == [2, 1, 1, 0, 0, 0]
     assert c.pages[2].tolist() == [0, 1, -9] and (c.k[:, 1] == last).all()
+    c.write(1, 2, 14, np.full((4, 1, 4), 500, np.uint16), np.full((4, 1, 4), 600, np.uint16))
+    assert (c.k[1, 0, 0, 14:] == 500).all() and (c.v[1, 1, 0, :2] == 600).all() and not (c.k[0] == 500).any()
+    k, v = c.rows(1, 2, 13, 3)
+    assert (k[1:] == 500).all() and (v[1:] == 600).all() and (k[0] != 500).all()
     for bad in (([0, 0], [1, 1]), ([4], [1]), ([0], [-1])):
-        with pytest.raises(Refused, match="SEQ"):
+        with pytest.raises(P.Refused, match="SEQ"):
             c.extend(*bad)
+    for bad in (([0], [0]), ([0], [2]), ([0, 0], [1, 1])):
+        with pytest.raises(P.Refused, match="SEQ"):
+            c.fork(*bad)
+    with pytest.raises(P.Refused, match="SEQ"):
+        c.release([0], [17])
+    c.pages[0, 0] = 5
+    with pytest.raises(P.Refused, match="PAGE"):
+        c.release([0], [0])
 
 
-def test_oracle_attention_closed_forms():
+def _pin_attention(P):
     rng = np.random.default_rng(0)
     v = rng.standard_normal((5, 2, 8))
     q = np.zeros((4, 8))
-    out = attend(q, rng.standard_normal((5, 2, 8)), v)   # no preference: the mean
+    out = P.attend(q, rng.standard_normal((5, 2, 8)), v)   # no preference: the mean
     assert np.allclose(out, np.repeat(v.mean(0), 2, axis=0))
     k = np.zeros((5, 2, 8))
     k[3] = 1000.0
-    assert np.allclose(attend(np.ones((4, 8)), k, v), np.repeat(v[3], 2, axis=0))   # one key takes all
-    assert (attend(q, k[:0], v[:0]) == 0).all()
-    o = attend_prompt(np.zeros((7, 4, 8)), np.zeros((7, 2, 8)), np.concatenate([v, v[:2]]), [1, 4, 4, 6])
+    assert np.allclose(P.attend(np.ones((4, 8)), k, v), np.repeat(v[3], 2, axis=0))   # one key takes all
+    k[3], k[1] = 0.0, np.sqrt(8.0) * np.log(3.0) / 8.0                                   # one key three times as heavy
+    assert np.allclose(P.attend(np.ones((4, 8)), k, v), np.repeat((v.sum(0) + 2 * v[1]) / 7, 2, axis=0))
+    k[1, 1], k[4, 1] = 0.0, 1000.0                                                       # each KV head its own keys
+    assert np.allclose(P.attend(np.ones((4, 8)), k, v), [(v[:, 0].sum(0) + 2 * v[1, 0]) / 7] * 2 + [v[4, 1]] * 2)
+    assert (P.attend(q, k[:0], v[:0]) == 0).all()
+    o = P.attend_prompt(np.zeros((7, 4, 8)), np.zeros((7, 2, 8)), np.concatenate([v, v[:2]]), [1, 4, 4, 6])
     assert np.isnan(o[0]).all() and np.isnan(o[6]).all()
-    assert np.allclose(o[3], np.repeat(v[1:4].mean(0), 2, axis=0)) and np.allclose(o[4], np.repeat(v[4], 2, axis=0))
+    assert np.allclose(o[1], np.repeat(v[1], 2, axis=0)) and np.allclose(o[3], np.repeat(v[1:4].mean(0), 2, axis=0))
+    assert np.allclose(o[4], np.repeat(v[4], 2, axis=0))
+    # the spread around the result: of two equally heavy values half their distance
+    assert np.allclose(P.attend(q, k[:2] * 0, v[:2], True)[1], np.repeat(np.abs(v[0] - v[1]) / 2, 2, axis=0))
+
+
+def test_oracle_pins():
+    import oracle.paged
+    _pin_pages(oracle.paged)
+    _pin_attention(oracle.paged)
+
+
+MISTAKES = [("refs[self.pages[s, have - 1]] > 1", "refs[self.pages[s, have - 1]] > 0"), ("n % self.ps and refs", "refs"),
+            ("            refs[self.pages[s, have - 1]] -= 1\n", ""), ("if refs[p] == 0]", "if refs[p] == 0][::-1]"),
+            ("self.k[:, p], self.v[:, p] = self.k[:, old], self.v[:, old]", "self.k[:, p] = self.k[:, old]"),
+            ("self.refs[self.pages[s, j]] += 1", "pass"), ("or self.lens[d] != 0 ", ""), ("range(self._held(m), self._held(int", "range(self._held(m) + 1, self._held(int"),
+            ("if not 0 <= m <= n", "if not 0 <= m"), ("self.refs[b], self.refs[a] = self.refs[a], 0", "self.refs[b] = self.refs[a]"),
+            ("self.pages[s, j] = remap[self.pages[s, j]]", "pass"), ("p, o = self.slot(s, pos + r)", "p, o = self.slot(s, pos)"),
+            ("/ np.sqrt(dim)", ""), ("k[:, h // group] @", "k[:, h % k.shape[1]] @"), ("k[a:t + 1], v[a:t + 1], True", "k[a:t], v[a:t], True"),
+            ("k[a:t + 1], v[a:t + 1], True", "k[:t + 1], v[:t + 1], True"), ("np.abs(v[:, h // group] - out[h])", "np.abs(v[:, h // group])")]
+
+
+@pytest.mark.parametrize("old,new", MISTAKES, ids=range(len(MISTAKES)))
+def test_planted_mistakes_fail_a_pin(old, new):
+    import types
+
+    import oracle.paged
+    text = open(oracle.paged.__file__).read()
+    assert old in text
+    m = types.ModuleType("planted")
+    exec(compile(text.replace(old, new), "planted", "exec"), m.__dict__)
+    with pytest.raises((AssertionError, IndexError, ValueError, m.Refused, pytest.fail.Exception)):
+        _pin_pages(m)
+        _pin_attention(m)
