@@ -226,6 +226,13 @@ __device__ __forceinline__ int clc_answer(const void* answer) {
   return got ? (int)x : -1;
 }
 
+// a * 0 + c of two bf16 each
+__device__ __forceinline__ uint32_t times_zero(uint32_t a, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0u), "r"(c));
+  return r;
+}
+
 // 32 bytes of one thread, one sector
 __device__ __forceinline__ void store32(void* p, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
@@ -263,7 +270,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* w_free = w_full + 2;                                         // [2] every role has read it
   uint64_t* drain = w_free + 2;                                          // after a timeout: every product issued is done
   uint64_t* clc_bar = drain + 1;
-  uint64_t* want = clc_bar + 1;                                          // a place's last loads are issued
+  uint64_t* want = clc_bar + 1;                                          // a place's end is near
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(want + 1);
   __shared__ __align__(16) uint4 s_clc;
   __shared__ int4 s_work[2];        // row0, length, first token, KV head; length 0: no more
@@ -471,14 +478,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         ++nq[s];
       };
       for (int w = 0; w < k.nwin && ok; ++w) {
+        // some three windows (5 us) before its end, time to find the next place
+        if (w == max(0, k.nwin - 3) && lane == 0) mbar_arrive(want);
         load_kv(&map_k, k_full, k_free, L::OFF_K, w, nk);
         if (w == 0 && ok) load_q(0);
-        if (w == 0 && ok && k.nst == 2) load_q(1);
         if (ok) load_kv(&map_v, v_full, v_free, L::OFF_V, w, nv);
+        if (w == 0 && ok && k.nst == 2) load_q(1);
       }
       if (!ok) break;
       kv += k.nwin;
-      if (lane == 0) mbar_arrive(want);
     }
     if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
     // loads in flight land before the CTA leaves
@@ -584,18 +592,21 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         constexpr int BATCH = 8;
         for (int r0 = first + lane / CH; r0 < last; r0 += BATCH * (32 / CH)) {
           uint4 y[BATCH];
-          uint32_t any = 0u;
 #pragma unroll
           for (int u = 0; u < BATCH; ++u) {
             const int row = r0 + u * (32 / CH);
             y[u] = row < last ? *reinterpret_cast<const uint4*>(piece + swz(row, c & 7)) : make_uint4(0u, 0u, 0u, 0u);
           }
-          // an exponent of all ones carries into the sign's place
+          // 0 x, summed: NaN where an x is not finite
+          uint32_t any[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int u = 0; u < BATCH; ++u)
-            any |= ((y[u].x & 0x7f807f80u) + 0x00800080u) | ((y[u].y & 0x7f807f80u) + 0x00800080u) |
-                   ((y[u].z & 0x7f807f80u) + 0x00800080u) | ((y[u].w & 0x7f807f80u) + 0x00800080u);
-          if (any & 0x80008000u) {
+          for (int u = 0; u < BATCH; ++u) {
+            any[0] = times_zero(y[u].x, any[0]);
+            any[1] = times_zero(y[u].y, any[1]);
+            any[2] = times_zero(y[u].z, any[2]);
+            any[3] = times_zero(y[u].w, any[3]);
+          }
+          if (((any[0] | any[1]) | (any[2] | any[3])) & 0x7fff7fffu) {
 #pragma unroll 1
             for (int row = r0; row < last && row < r0 + BATCH * (32 / CH); row += 32 / CH) {
               uint16_t* x = reinterpret_cast<uint16_t*>(piece + swz(row, c & 7));
@@ -670,13 +681,24 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (ok && !mbar_wait(&s_full[s], (uint32_t)ns & 1u)) ok = false;
         ++ns;
         tc_fence_after();
+        // Of a masked window's pieces of 16 keys, those that every row of the
+        // warp sees need no mask, and those that none sees are not read.
+        int all_see = 63, any_see = 63;
+        if constexpr (MASKED) {
+          all_see = __reduce_min_sync(0xffffffffu, live ? lim : 63);
+          any_see = __reduce_max_sync(0xffffffffu, live ? lim : -1);
+        }
         auto scores = [&](int c, uint32_t (&x)[32]) {   // half of its scores
           ld32(sS + 64 * hf + 32 * c, x);
           tmem_ld_wait();
           if constexpr (MASKED) {
 #pragma unroll
-            for (int u = 0; u < 32; ++u)
-              if (32 * c + u > lim) x[u] = 0xff800000u;
+            for (int h = 0; h < 32; h += 16)
+              if (32 * c + h + 15 > all_see) {
+#pragma unroll
+                for (int u = h; u < h + 16; ++u)
+                  if (32 * c + u > lim) x[u] = 0xff800000u;
+              }
           }
         };
         uint32_t pk[32];
@@ -686,18 +708,34 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           uint64_t l2 = 0, l3 = 0;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
+            auto none = [&](int h) {
+#pragma unroll
+              for (int u = h / 2; u < h / 2 + 8; ++u) pk[16 * c + u] = 0u;
+            };
+            if (MASKED && 32 * c > any_see) {
+              none(0);
+              none(16);
+              continue;
+            }
             uint32_t x[32];
             scores(c, x);
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              float a, b;
-              unpack2(fma2(pack2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), scale2, neg2), a, b);
-              const __nv_bfloat162 v = __floats2bfloat162_rn(ex2p(a), ex2p(b));
-              const uint32_t q = *reinterpret_cast<const uint32_t*>(&v);
-              pk[16 * c + u] = q;
-              const uint64_t q2 = pack2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
-              if (u & 1) l3 = add2(l3, q2);
-              else l2 = add2(l2, q2);
+            for (int h = 0; h < 32; h += 16) {
+              if (MASKED && 32 * c + h > any_see) {
+                none(h);
+                continue;
+              }
+#pragma unroll
+              for (int u = h / 2; u < h / 2 + 8; ++u) {
+                float a, b;
+                unpack2(fma2(pack2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), scale2, neg2), a, b);
+                const __nv_bfloat162 v = __floats2bfloat162_rn(ex2p(a), ex2p(b));
+                const uint32_t q = *reinterpret_cast<const uint32_t*>(&v);
+                pk[16 * c + u] = q;
+                const uint64_t q2 = pack2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
+                if (u & 1) l3 = add2(l3, q2);
+                else l2 = add2(l2, q2);
+              }
             }
           }
           float a, b;
