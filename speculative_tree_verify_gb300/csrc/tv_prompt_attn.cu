@@ -340,6 +340,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     if (lane == 0) mbar_arrive(&w_free[it & 1]);
   };
   auto w_start = [](const Work& k, int w) { return 128 * (k.nwin - 1 - w); };   // first key of window w, the last keys first
+  // 16-key steps of window w that tile s sees anything of: what lies behind
+  // its last token is neither multiplied nor looked at
+  auto steps = [&](const Work& k, int s, int w) { return min(8, (min(k.len, k.t0 + (s + 1) * p.T) - w_start(k, w) + 15) >> 4); };
   // window w holds keys that a row may not see (so does the first, if only as a rule)
   auto scrub = [&](const Work& k, int w) { return w == 0 || w_start(k, w) + 127 > k.t0; };
 
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   } else if (warp == kWarpMma) {
     // ---------------- products ----------------
     const uint32_t leader = elect_one();
-    const uint32_t idesc_s = idesc_bf16_f32(128, 128);
+    const uint32_t idesc_s = idesc_bf16_f32(128, 0);                // N, the keys, comes with the window
     const uint32_t idesc_o = idesc_bf16_f32(128, D) | (1u << 16);   // B = V: MN-major
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dq = sdesc_sw128(base + L::OFF_Q, 16, 1024), dk = sdesc_sw128(base + L::OFF_K, 16, 1024);
@@ -515,10 +518,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (!ok) return;
         tc_fence_after();
         const uint64_t a = dq + (uint64_t)(s * (L::TILE >> 4)), b = dk + (uint64_t)((i & 1) * (L::TILE >> 4));
+        const uint32_t idesc = idesc_s | (uint32_t)steps(k, s, w) << 18;   // N >> 3, at bit 17
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           const uint64_t off = (uint64_t)(((c >> 2) * kAtomP + (c & 3) * 32) >> 4);
-          umma_ss(tm + s * 128, a + off, b + off, idesc_s, c > 0 ? 1u : 0u, leader);
+          umma_ss(tm + s * 128, a + off, b + off, idesc, c > 0 ? 1u : 0u, leader);
         }
         commit_by(&s_full[s], leader);
         if (s == k.nst - 1) commit_by(&k_free[i & 1], leader);
@@ -532,11 +536,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const int i = __shfl_sync(0xffffffffu, kv + w, 0);   // uniform, and known to be
         // both loads before the first P: nothing between a P and its products then
         wait(&v_full[i & 1], (uint32_t)(i >> 1));
-        if (scrub(k, w)) {
-          wait(&v_ok[looked & 1], (uint32_t)(looked >> 1));
-          ++looked;
-        }
         if (w + 1 < k.nwin) wait(&k_full[(i + 1) & 1], (uint32_t)((i + 1) >> 1));
+        bool look = scrub(k, w);
+        const int seen = min(8, max(0, k.t0 + 1 - w_start(k, w)) >> 4);   // steps whose keys every row sees
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (s >= k.nst || !ok) break;
@@ -546,9 +548,27 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const uint64_t b = dv + (uint64_t)((i & 1) * (L::TILE >> 4));
-#pragma unroll
-            for (int c = 0; c < 8; ++c)   // 16 keys a step
+            auto step = [&](int c) {   // 16 keys
               umma_ts(tm + 256 + s * D, tm + s * 128 + c * 8, b + (uint64_t)(c * (2048 >> 4)), idesc_o, (w > f || c > 0) ? 1u : 0u, leader);
+            };
+            if (!look) {
+              const int n = steps(k, s, w);
+              if (n == 8) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) step(c);
+              } else {
+                for (int c = 0; c < n; ++c) step(c);
+              }
+            } else {   // what every row sees does not wait for the look at the rest
+              const int n = steps(k, s, w), m = min(n, seen);
+              for (int c = 0; c < m; ++c) step(c);
+              wait(&v_ok[looked & 1], (uint32_t)(looked >> 1));
+              ++looked;
+              look = false;
+              if (!ok) break;
+              tc_fence_after();
+              for (int c = m; c < n; ++c) step(c);
+            }
             if (w == k.nwin - 1) commit_by(&o_fin[s], leader);
             if (s == k.nst - 1) commit_by(&v_free[i & 1], leader);
           }
@@ -581,22 +601,28 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const int i = kv + w;
         if (ok && !mbar_wait(&v_full[i & 1], (uint32_t)(i >> 1) & 1u)) ok = false;
         uint8_t* sv = smem + L::OFF_V + (i & 1) * L::TILE;
-        // rows of this pair's tokens but the first are looked at, those behind its last token emptied
-        const int key0 = w_start(k, w), first = max(0, k.t0 + 1 - key0), last = min(128, k.hi - key0);
+        // rows of this pair's tokens but the first are looked at, those behind its last token in the same step emptied
+        const int key0 = w_start(k, w), first = max(0, k.t0 + 1 - key0), last = min(128, k.hi - key0), end = (last + 15) & ~15;
         constexpr int CH = D / 8;   // 16-byte pieces of a row, 32 / CH rows a step
-        bool wrote = last < 128;
+        bool wrote = last < end;
         const int c = lane % CH;
         uint8_t* piece = sv + (c >> 3) * kAtomP;
-        for (int row = last + lane / CH; row < 128; row += 32 / CH)
+        for (int row = last + lane / CH; row < end; row += 32 / CH)
           *reinterpret_cast<uint4*>(piece + swz(row, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
-        constexpr int BATCH = 8;
-        for (int r0 = first + lane / CH; r0 < last; r0 += BATCH * (32 / CH)) {
+        // eight rows a round: their swizzles repeat, so that a round's addresses are the last's and 1024
+        constexpr int PER = CH / 4, BATCH = 2 * PER;
+        const uint8_t* at[PER];
+#pragma unroll
+        for (int u = 0; u < PER; ++u) at[u] = piece + swz(first + lane / CH + u * (32 / CH), c & 7);
+        for (int r0 = first + lane / CH; r0 < last; r0 += 16) {
           uint4 y[BATCH];
 #pragma unroll
           for (int u = 0; u < BATCH; ++u) {
             const int row = r0 + u * (32 / CH);
-            y[u] = row < last ? *reinterpret_cast<const uint4*>(piece + swz(row, c & 7)) : make_uint4(0u, 0u, 0u, 0u);
+            y[u] = row < last ? *reinterpret_cast<const uint4*>(at[u % PER] + (u / PER) * 1024) : make_uint4(0u, 0u, 0u, 0u);
           }
+#pragma unroll
+          for (int u = 0; u < PER; ++u) at[u] += 2048;
           // 0 x, summed: NaN where an x is not finite
           uint32_t any[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -608,7 +634,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           if (((any[0] | any[1]) | (any[2] | any[3])) & 0x7fff7fffu) {
 #pragma unroll 1
-            for (int row = r0; row < last && row < r0 + BATCH * (32 / CH); row += 32 / CH) {
+            for (int row = r0; row < last && row < r0 + 16; row += 32 / CH) {
               uint16_t* x = reinterpret_cast<uint16_t*>(piece + swz(row, c & 7));
 #pragma unroll 1
               for (int u = 0; u < 8; ++u) {
