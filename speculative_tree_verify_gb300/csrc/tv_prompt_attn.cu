@@ -24,6 +24,20 @@
 // (S_s(w) is committed after PV_s(w - 1), so O_s is at rest).  Sums add the
 // rounded P, fp32 throughout.
 //
+// Six kinds of warps keep their own pace, each one place (a pair of tiles)
+// after the other, and meet only on barriers in shared memory: softmax (16),
+// products, loads, the next places, and the look at what is masked.  A CTA
+// takes over the places of CTAs that have not started, three windows before
+// it is done with its own.
+//
+// Measured (40/8 heads of 128, us; each step with the ones before it): 16k
+// tokens 2866 as first built; 1984 with the issuing warp in step (its
+// descriptors stay in uniform registers); 1838 with two threads a row; 1749
+// with sums instead of maxima; 1690 taking over places; 1654 with headroom in
+// the offsets; 1623 to 1655 now, 1660 to 1690 TFLOP/s: 88 % of what cuBLAS
+// reaches in a burst, 98 % of its sustained rate.  4k: 112 (1.5 PFLOP/s);
+// 24 prompts of 1 to 1531: 64; one of 1024: 17.5.
+//
 // Masked places: a key that a row may not see has weight zero, and its V may
 // be anything.  0 * NaN would reach the row through the product, so the V rows
 // past the CTA's first token are looked over in shared memory before they are
@@ -702,29 +716,29 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       // lim: the last visible one of this thread's keys; before: the first key
       // of the window before (rows before it have seen none); again: O_s holds
       // earlier windows.
-      auto window = [&](auto masked_c, auto fresh_c, int lim, int before, bool again) {
-        constexpr bool MASKED = decltype(masked_c)::value, FRESH = decltype(fresh_c)::value;
+      // Two copies of the code: PLAIN for windows that hide nothing of rows that
+      // have keys already, one for all the others (a place of one or two
+      // windows spends as long fetching instructions as on them: with a third
+      // for masked windows the packed prompts took 66 us instead of 64).
+      auto window = [&](auto plain_c, bool masked, int lim, int before, bool again) {
+        constexpr bool PLAIN = decltype(plain_c)::value;
         if (ok && !mbar_wait(&s_full[s], (uint32_t)ns & 1u)) ok = false;
         ++ns;
         tc_fence_after();
-        // Of a masked window's pieces of 16 keys, those that every row of the
+        // Of a masked window's pieces of 32 keys, those that every row of the
         // warp sees need no mask, and those that none sees are not read.
         int all_see = 63, any_see = 63;
-        if constexpr (MASKED) {
+        if (!PLAIN && masked) {
           all_see = __reduce_min_sync(0xffffffffu, live ? lim : 63);
           any_see = __reduce_max_sync(0xffffffffu, live ? lim : -1);
         }
         auto scores = [&](int c, uint32_t (&x)[32]) {   // half of its scores
           ld32(sS + 64 * hf + 32 * c, x);
           tmem_ld_wait();
-          if constexpr (MASKED) {
+          if (!PLAIN && 32 * c + 31 > all_see) {
 #pragma unroll
-            for (int h = 0; h < 32; h += 16)
-              if (32 * c + h + 15 > all_see) {
-#pragma unroll
-                for (int u = h; u < h + 16; ++u)
-                  if (32 * c + u > lim) x[u] = 0xff800000u;
-              }
+            for (int u = 0; u < 32; ++u)
+              if (32 * c + u > lim) x[u] = 0xff800000u;
           }
         };
         uint32_t pk[32];
@@ -734,42 +748,30 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           uint64_t l2 = 0, l3 = 0;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            auto none = [&](int h) {
+            if (!PLAIN && 32 * c > any_see) {
 #pragma unroll
-              for (int u = h / 2; u < h / 2 + 8; ++u) pk[16 * c + u] = 0u;
-            };
-            if (MASKED && 32 * c > any_see) {
-              none(0);
-              none(16);
+              for (int u = 0; u < 16; ++u) pk[16 * c + u] = 0u;
               continue;
             }
             uint32_t x[32];
             scores(c, x);
 #pragma unroll
-            for (int h = 0; h < 32; h += 16) {
-              if (MASKED && 32 * c + h > any_see) {
-                none(h);
-                continue;
-              }
-#pragma unroll
-              for (int u = h / 2; u < h / 2 + 8; ++u) {
-                float a, b;
-                unpack2(fma2(pack2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), scale2, neg2), a, b);
-                const __nv_bfloat162 v = __floats2bfloat162_rn(ex2p(a), ex2p(b));
-                const uint32_t q = *reinterpret_cast<const uint32_t*>(&v);
-                pk[16 * c + u] = q;
-                const uint64_t q2 = pack2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
-                if (u & 1) l3 = add2(l3, q2);
-                else l2 = add2(l2, q2);
-              }
+            for (int u = 0; u < 16; ++u) {
+              float a, b;
+              unpack2(fma2(pack2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), scale2, neg2), a, b);
+              const __nv_bfloat162 v = __floats2bfloat162_rn(ex2p(a), ex2p(b));
+              const uint32_t q = *reinterpret_cast<const uint32_t*>(&v);
+              pk[16 * c + u] = q;
+              const uint64_t q2 = pack2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
+              if (u & 1) l3 = add2(l3, q2);
+              else l2 = add2(l2, q2);
             }
           }
           float a, b;
           unpack2(add2(l2, l3), a, b);
           sum = a + b;
-          const bool fresh = FRESH && before > t;   // the row's first keys, if it sees any
-          bool off = sum > kHigh;
-          if (FRESH) off = off || (first && fresh && live && (!MASKED || lim >= 0) && sum < kLow);
+          const bool fresh = !PLAIN && before > t;   // the row's first keys, if it sees any
+          const bool off = sum > kHigh || (first && fresh && live && lim >= 0 && sum < kLow);
           tc_fence_before();
           const bool any = pair_any(off, pair);
           tc_fence_after();
@@ -824,11 +826,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           // rows without a key: all in the first window, and those before a window that hid it all
           const int before = w == f ? 0x7fffffff : start + 128;
           if (w > f && !masked && before <= tmin) break;
-          if (masked) window(std::true_type{}, std::true_type{}, t - start - 64 * hf, before, w > f);
-          else window(std::false_type{}, std::true_type{}, 0, before, w > f);
+          window(std::false_type{}, masked, masked ? t - start - 64 * hf : 63, before, w > f);
         }
         // and all the others
-        for (; w < k.nwin; ++w) window(std::false_type{}, std::false_type{}, 0, 0, true);
+        for (; w < k.nwin; ++w) window(std::true_type{}, false, 63, 0, true);
         if (ok && !mbar_wait(&o_fin[s], (uint32_t)nf & 1u)) ok = false;
         ++nf;
         s_sum[hf * 128 + r] = l;
