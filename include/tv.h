@@ -658,7 +658,8 @@ typedef struct tv_seqs {
  * (that row alone is left out).
  *
  * The workspace and the pool's tables belong to one call at a time: order
- * calls that share them on one stream.  Host checks of all: TV_E_ARG (null or misaligned pointers, n < 1, a bad
+ * calls that share them on one stream.
+ * Host checks of all: TV_E_ARG (null or misaligned pointers, n < 1, a bad
  * layer), TV_E_UNSUPPORTED (n > 4096, shapes outside the above),
  * TV_E_WORKSPACE.
  */

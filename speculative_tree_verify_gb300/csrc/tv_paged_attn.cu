@@ -8,9 +8,9 @@
 // head, block of 16 query heads) in that order, each such head block counted
 // kSegCost tiles more for what it costs to begin and end; CTA c takes an
 // equal, contiguous range of it, whatever the lengths, so one long context
-// among short ones and one sequence alone both fill every SM.  A head block cut by a range
-// border leaves unnormalised partials that paged_merge_kernel joins in tile
-// order: no atomics, the same bits every run.
+// among short ones and one sequence alone both fill every SM.  A head block cut
+// by a range border leaves unnormalised partials that paged_merge_kernel joins
+// in tile order: no atomics, the same bits every run.
 //
 // In a CTA one warp looks up pages and issues TMA loads (a page's tokens of
 // one head are contiguous: boxes of min(page, 64) rows x 64 values, 128-byte
@@ -44,7 +44,7 @@ constexpr int kCompThreads = kCompWarps * 32;
 constexpr int kPaThreads = kCompThreads + 32;
 constexpr int kRows = 16;                        // query heads of a block
 constexpr int kQueries = 8;                      // segments whose queries are loaded ahead, at most
-constexpr int kMaxTokens = 2048;                 // sequences of one call: their places fit shared memory beside the stages
+constexpr int kMaxTokens = 2048;                 // sequences of one call: their places fit beside the stages
 constexpr int kInfo = 640;                       // up to here their table rows and lengths do, too
 constexpr int kRedRows = 4;                      // rows joined at a time when a head block ends
 // What a head block costs besides its tiles, in tiles (its queries, its join).
@@ -79,15 +79,17 @@ struct PaSmem {
   static constexpr int SLAB = kTile * 128;                   // 64 dimensions of a tile
   static constexpr int HALF = (D / 64) * SLAB;               // a tile's K (or V)
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int OFF_RED = kStages * STAGE;            // [8 warps][kRedRows][D] fp32; the marks of listed rows first
+  static constexpr int OFF_RED = kStages * STAGE;   // [8 warps][kRedRows][D] fp32; the marks of listed rows first
   static constexpr int OFF_ML = OFF_RED + kCompWarps * kRedRows * D * 4;
-  static constexpr int Q_ROW = D * 2 + 16;                   // rows 16 bytes apart in the banks: ldmatrix without conflicts
-  static constexpr int OFF_Q = OFF_ML + kCompWarps * kRows * 8;   // 2 kRows query rows: those of the next 2 to kQueries segments
+  static constexpr int Q_ROW = D * 2 + 16;          // rows 16 bytes apart in the banks: ldmatrix without conflicts
+  // 2 kRows query rows: those of the next 2 to kQueries runs
+  static constexpr int OFF_Q = OFF_ML + kCompWarps * kRows * 8;
   static constexpr int OFF_BAR = OFF_Q + 2 * kRows * Q_ROW;
-  static constexpr int OFF_FIRST = OFF_BAR + 256;            // [n + 1]; up to kInfo sequences also their rows and lengths
+  static constexpr int OFF_FIRST = OFF_BAR + 256;   // [n + 1]; up to kInfo sequences also their rows and lengths
   static size_t bytes(int n) { return 1024 + OFF_FIRST + (size_t)(n + 1) * 4 + (n <= kInfo ? (size_t)n * 8 : 0); }
   static_assert(kCompWarps * kRedRows * D * 4 >= kMaxSeqs / 8, "a mark for every table row");
-  static_assert(1024 + OFF_FIRST + (kMaxTokens + 1) * 4 <= 232448 - 64 && kInfo * 12 <= kMaxTokens * 4, "shared memory of one CTA");
+  static_assert(1024 + OFF_FIRST + (kMaxTokens + 1) * 4 <= 232448 - 64, "shared memory of one CTA");
+  static_assert(kInfo * 12 <= kMaxTokens * 4, "rows and lengths in the places of more sequences");
 };
 
 __device__ __forceinline__ float ex2f(float x) {   // 2^x by the SFU, about 2^-22 relative, 2^-inf = 0
@@ -115,22 +117,26 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 // untiled copy: 16-byte aligned addresses, a multiple of 16 bytes
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(smem_dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :
+               : "r"(smem_u32(smem_dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
 __device__ __forceinline__ void comp_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kCompThreads) : "memory"); }
 
-__device__ __forceinline__ void quad_sync(int quad) { asm volatile("bar.sync %0, %1;" ::"r"(2 + quad), "n"(kCompThreads / 2) : "memory"); }
+__device__ __forceinline__ void quad_sync(int quad) {
+  asm volatile("bar.sync %0, %1;" ::"r"(2 + quad), "n"(kCompThreads / 2) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+__device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % kTile != 0); }
 
 template <int D>
 __global__ void __launch_bounds__(kPaThreads, 1)
-    paged_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const PaParams p) {
+    paged_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                      const PaParams p) {
   using L = PaSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -149,7 +155,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ps = p.pool.page_size, Hkv = p.pool.n_kv_heads;
   const bool info = p.n <= kInfo;
-  const int qrows = min(kRows, p.G), qslots = min(kQueries, 2 * kRows / qrows);   // short sequences need many segments ahead
+  // places of the query ring: short sequences need many runs ahead
+  const int qrows = min(kRows, p.G), qslots = min(kQueries, 2 * kRows / qrows);
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -173,7 +180,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 
   // ---- the list of tiles: every CTA reads the same lengths and finds the same list
   uint32_t all;
-  auto head_tiles = [&](int len) {   // of one head block, its fixed cost included; the host has seen to it that all fit 31 bits
+  // of one head block, its fixed cost included; the host has seen to it that all fit 31 bits
+  auto head_tiles = [&](int len) {
     return len > 0 ? (uint32_t)(tiles_of(len) + kSegCost) : 0u;
   };
   auto look = [&](int i, int& s) {   // length of listed sequence i, -1: refused
@@ -311,7 +319,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const uint64_t pol = policy_evict_first();
     bool ok = true;
     int issued = 0, segs = 0, st = 0, qs = 0;   // tiles and queries loaded so far, their places in the rings
-    uint32_t st_par = 1u, qs_par = 1u;          // of the wait before a place is used again; the first round waits for nothing
+    uint32_t st_par = 1u, qs_par = 1u;          // of the wait before a place is used again (not in the first round)
     const int psh = 31 - __clz(ps);
     auto entry = [&](const Run& g, int t) {   // this lane's page of tile t, -1 past the length
       const int tok = t * kTile + box * R;
@@ -360,9 +368,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       page = next_page;
     }
     if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
-    for (int u = segs > qslots ? segs - qslots : 0; u < segs; ++u) mbar_wait(&q_full[u % qslots], (uint32_t)(u / qslots) & 1u);
+    for (int u = segs > qslots ? segs - qslots : 0; u < segs; ++u)
+      mbar_wait(&q_full[u % qslots], (uint32_t)(u / qslots) & 1u);
     // loads in flight land before the CTA leaves
-    for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u) mbar_wait(&full[u % kStages], (uint32_t)(u / kStages) & 1u);
+    for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u)
+      mbar_wait(&full[u % kStages], (uint32_t)(u / kStages) & 1u);
     return;
   }
 
@@ -418,7 +428,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           const bool v = lane >= 16;
           const int c = lane & 15;
           if (c < D / 8) {
-            const uint4 x = __ldcg(reinterpret_cast<const uint4*>((v ? p.v_new : p.k_new) + (size_t)g.i * p.kv_stride + (size_t)h * D) + c);
+            const __nv_bfloat16* row = (v ? p.v_new : p.k_new) + (size_t)g.i * p.kv_stride + (size_t)h * D;
+            const uint4 x = __ldcg(reinterpret_cast<const uint4*>(row) + c);
             *reinterpret_cast<uint4*>((v ? sv : sk) + (c >> 3) * L::SLAB + swz(16 * sl + valid - 1, c & 7)) = x;
             if (r0 == 0) {
               const int page = __ldcg(p.seqs.pages + (size_t)g.s * p.seqs.max_pages + (g.len - 1) / ps);
@@ -509,7 +520,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     // that had it: the other four go on to the next head block meanwhile (not
     // far: its queries are not loaded before these have given up theirs)
     const bool whole = g.t0 == 0 && g.t1 == g.T;
-    const size_t slot = (size_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0);   // a CTA's first segment may begin inside a head, its last end inside one
+    // a CTA's first run may begin inside a head block, its last end inside one
+    const size_t slot = (size_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0);
     auto join = [&](auto nw_c) {
       constexpr int NW = decltype(nw_c)::value;        // warps that take part, from w0 on
       const int w0 = NW == kCompWarps ? 0 : 4 * quad, me = tid - 32 * w0;
@@ -531,7 +543,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       // without a token in this run has not used them, and never will.)
       if (lane == 0) mbar_arrive_n(&q_free[qs], kCompWarps / NW);
 #pragma unroll 1   // one copy of the code: most groups need one or two parts, and short sequences run it once a tile
-      for (int part = 0; part * kRedRows < nr; ++part) {   // rows 4 part .. + 3, held by the lanes with g8 / 4 = part mod 2
+      for (int part = 0; part * kRedRows < nr; ++part) {   // rows 4 part .. + 3, of the lanes with g8 / 4 = part mod 2
         const bool upper = part >> 1;
         if ((g8 >> 2) == (part & 1)) {
           const int row = g8 + (upper ? 8 : 0);
@@ -547,7 +559,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           const float own = upper ? m1 : m0;
           float f = own == -INFINITY ? 0.f : ex2f(own - M);
           if (whole) f /= L;
-          else if (warp == w0 && t4 == 0 && row < nr) *reinterpret_cast<float2*>(p.ws.ml + (slot * kRows + row) * 2) = make_float2(M, L);
+          else if (warp == w0 && t4 == 0 && row < nr)
+            *reinterpret_cast<float2*>(p.ws.ml + (slot * kRows + row) * 2) = make_float2(M, L);
           // row r: groups of 8 values XOR r, no bank twice
           float* dst = s_red + (warp * kRedRows + (g8 & 3)) * D + 2 * t4;
           float* at[4];
@@ -617,7 +630,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PaPara
 #pragma unroll
     for (int k = 0; k < kMaxCtas / 32; ++k) {
       ml[k] = make_float2(-INFINITY, 0.f);
-      if (32 * k + lane < np) ml[k] = __ldcg(reinterpret_cast<const float2*>(p.ws.ml + (slot(32 * k + lane) * kRows + warp) * 2));
+      if (32 * k + lane < np)
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(p.ws.ml + (slot(32 * k + lane) * kRows + warp) * 2));
       M = fmaxf(M, ml[k].x);
     }
     M = warp_max(M);

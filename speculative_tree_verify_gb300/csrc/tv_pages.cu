@@ -17,7 +17,7 @@ namespace tv {
 namespace {
 
 constexpr int kListThreads = 256;    // block of the kernels that move rows and pages
-constexpr int kSeqThreads = 1024;    // block of the kernels that follow a sequence's pages: few rounds of dependent loads
+constexpr int kSeqThreads = 1024;    // of those that follow a sequence's pages: few rounds of dependent loads
 constexpr int kPlanThreads = 1024;   // the one block that allocates
 
 // what a block found wrong with its list; the lowest bit is reported, so that
@@ -231,7 +231,9 @@ struct ExtendWs {
 struct ExtendSmem {   // of n listed sequences, and a mark for every table row
   int *last, *off, *row, *len;
   uint32_t* mark;
-  static size_t bytes(int n, int max_seqs) { return (size_t)((n + 3) & ~3) * 16 + (size_t)((max_seqs + 127) / 128) * 16; }
+  static size_t bytes(int n, int max_seqs) {
+    return (size_t)((n + 3) & ~3) * 16 + (size_t)((max_seqs + 127) / 128) * 16;
+  }
 };
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(tv_pool pool, tv_seqs t, const int32_t* ids,
                                                                    const int32_t* add, int n, ExtendWs ws,
@@ -558,14 +560,17 @@ __global__ void __launch_bounds__(kListThreads) rows_kernel(tv_pool pool, int la
   const int pieces = pool.n_kv_heads * (pool.head_dim / 8);   // 16-byte pieces of a row's K
   const int dsh = pool.head_dim == 128 ? 4 : 3;
   const size_t page_elems = (size_t)pool.n_kv_heads * ps * pool.head_dim;
-  for (int r = first + blockIdx.x * (kListThreads / 32) + (tid >> 5); r < total; r += gridDim.x * (kListThreads / 32)) {
+  __nv_bfloat16 *pk = reinterpret_cast<__nv_bfloat16*>(pool.k), *pv = reinterpret_cast<__nv_bfloat16*>(pool.v);
+  // (unsigned: a count near 2^31 and a stride do not wrap)
+  for (uint32_t r = first + blockIdx.x * (kListThreads / 32) + (tid >> 5); r < (uint32_t)total;
+       r += gridDim.x * (kListThreads / 32)) {
     int lo = 0, hi = n - 1;   // the sequence of row r
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (s_start[mid] <= r) lo = mid;
+      if ((uint32_t)s_start[mid] <= r) lo = mid;
       else hi = mid - 1;
     }
-    const int at = __ldg(pos + lo) + r - s_start[lo];
+    const int at = __ldg(pos + lo) + (int)r - s_start[lo];
     const int p = __ldcg(t.pages + (size_t)__ldg(ids + lo) * t.max_pages + at / ps);
     if (p < 0 || p >= pool.n_pages) {
       if (lane == 0) status_set(status, TV_E_PAGE);
@@ -581,8 +586,8 @@ __global__ void __launch_bounds__(kListThreads) rows_kernel(tv_pool pool, int la
           const int h = c >> dsh, e = (c & ((1 << dsh) - 1)) * 8;
           const size_t in_page = base + (size_t)h * ps * pool.head_dim + e;
           const size_t in_rows = (size_t)r * row_stride + (size_t)h * head_stride + e;
-          x[2 * u] = __ldcg(reinterpret_cast<const uint4*>(WRITE ? k + in_rows : reinterpret_cast<const __nv_bfloat16*>(pool.k) + in_page));
-          x[2 * u + 1] = __ldcg(reinterpret_cast<const uint4*>(WRITE ? v + in_rows : reinterpret_cast<const __nv_bfloat16*>(pool.v) + in_page));
+          x[2 * u] = __ldcg(reinterpret_cast<const uint4*>(WRITE ? k + in_rows : pk + in_page));
+          x[2 * u + 1] = __ldcg(reinterpret_cast<const uint4*>(WRITE ? v + in_rows : pv + in_page));
         }
       }
 #pragma unroll
@@ -592,8 +597,8 @@ __global__ void __launch_bounds__(kListThreads) rows_kernel(tv_pool pool, int la
           const int h = c >> dsh, e = (c & ((1 << dsh) - 1)) * 8;
           const size_t in_page = base + (size_t)h * ps * pool.head_dim + e;
           const size_t in_rows = (size_t)r * row_stride + (size_t)h * head_stride + e;
-          *reinterpret_cast<uint4*>(WRITE ? reinterpret_cast<__nv_bfloat16*>(pool.k) + in_page : k + in_rows) = x[2 * u];
-          *reinterpret_cast<uint4*>(WRITE ? reinterpret_cast<__nv_bfloat16*>(pool.v) + in_page : v + in_rows) = x[2 * u + 1];
+          *reinterpret_cast<uint4*>(WRITE ? pk + in_page : k + in_rows) = x[2 * u];
+          *reinterpret_cast<uint4*>(WRITE ? pv + in_page : v + in_rows) = x[2 * u + 1];
         }
       }
     }
@@ -685,8 +690,8 @@ int tv_pages_extend(const tv_pool* pool, const tv_seqs* seqs, const int32_t* ids
   ws.pair = reinterpret_cast<int32_t*>(w + 2 * align256((size_t)pool->n_pages * 4));
   static std::atomic<bool> attr[64];
   if (ensure_smem_limit(extend_plan_kernel, ExtendSmem::bytes(kMaxListed, kMaxSeqs), attr)) return TV_E_CUDA;
-  rc = launch_pdl(extend_plan_kernel, dim3(1), dim3(kPlanThreads), ExtendSmem::bytes(n, seqs->max_seqs), st, *pool, *seqs, ids, add, n,
-                  ws, dev_status);
+  rc = launch_pdl(extend_plan_kernel, dim3(1), dim3(kPlanThreads), ExtendSmem::bytes(n, seqs->max_seqs), st, *pool, *seqs,
+                  ids, add, n, ws, dev_status);
   if (rc) return rc;
   const int y = 2 * pool->n_layers < 65535 ? 2 * pool->n_layers : 65535;
   return launch_pdl(extend_copy_kernel, dim3(n, y), dim3(kListThreads), 0, st, *pool, ws, dev_status);

@@ -33,7 +33,8 @@ inline int check_seqs(const tv_seqs* s, const tv_pool* p) {
 
 inline int check_listed(int n) { return n < 1 ? TV_E_ARG : (n > kMaxListed ? TV_E_UNSUPPORTED : TV_OK); }
 
-__device__ __forceinline__ int pages_of(int len, int page_size) { return (len + page_size - 1) / page_size; }
+// (a length may be near 2^31: nothing is added to it)
+__device__ __forceinline__ int pages_of(int len, int page_size) { return len / page_size + (len % page_size != 0); }
 
 // a sequence's length if its table row allows it, -1 otherwise
 __device__ __forceinline__ int seq_len(const tv_seqs& t, int page_size, int s) {

@@ -20,11 +20,11 @@
 //                          TMA layout (MN-major)
 // The issue order PV_0(w) S_0(w + 1) PV_1(w) S_1(w + 1) keeps the tensor pipe
 // on one tile while the other's softmax runs.  A row's offset m need not be its
-// maximum, only near it; where it is not, O_s is rescaled in TMEM by the row's own threads
-// (S_s(w) is committed after PV_s(w - 1), so O_s is at rest).  Sums add the
+// maximum, only near it; where it is not, O_s is rescaled in TMEM by the row's
+// own threads (S_s(w) is committed after PV_s(w - 1), so O_s is at rest).  Sums add the
 // rounded P, fp32 throughout.
 //
-// Six kinds of warps keep their own pace, each one place (a pair of tiles)
+// Five kinds of warps keep their own pace, each one place (a pair of tiles)
 // after the other, and meet only on barriers in shared memory: softmax (16),
 // products, loads, the next places, and the look at what is masked.  A CTA
 // takes over the places of CTAs that have not started, three windows before
@@ -55,7 +55,8 @@ namespace {
 
 constexpr int kPrSoftWarps = 16;                 // 8 a query tile
 constexpr int kPrSoftThreads = kPrSoftWarps * 32;
-constexpr int kWarpMma = kPrSoftWarps, kWarpTma = kPrSoftWarps + 1, kWarpPlan = kPrSoftWarps + 2, kWarpLook = kPrSoftWarps + 3;
+constexpr int kWarpMma = kPrSoftWarps, kWarpTma = kPrSoftWarps + 1;
+constexpr int kWarpPlan = kPrSoftWarps + 2, kWarpLook = kPrSoftWarps + 3;
 constexpr int kPrThreads = kPrSoftThreads + 128;  // a whole warpgroup for the four roles' registers
 // 640 threads of 96 registers at launch; 512 x 104 + 128 x 64 is the same sum
 constexpr int kSoftRegs = 104, kRoleRegs = 64;
@@ -98,7 +99,8 @@ __device__ __forceinline__ float ex2p(float x) {   // 2^x by the SFU, about 2^-2
 __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
@@ -126,7 +128,8 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
         "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
@@ -186,8 +189,8 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T
-__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
-                                        uint32_t leader) {
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate, uint32_t leader) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -197,8 +200,8 @@ __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64
       : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem desc]: A holds two bf16 of a row per 32-bit column
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
-                                        uint32_t leader) {
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate, uint32_t leader) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -220,8 +223,9 @@ __device__ __forceinline__ void commit_by(uint64_t* bar, uint32_t leader) {
 // work this CTA takes over (16 bytes written to shared memory, counted on the
 // barrier)
 __device__ __forceinline__ void clc_ask(void* answer, uint64_t* bar) {
-  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(answer)),
-               "r"(smem_u32(bar))
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+               :
+               : "r"(smem_u32(answer)), "r"(smem_u32(bar))
                : "memory");
 }
 // -1: every CTA has started
@@ -249,8 +253,9 @@ __device__ __forceinline__ uint32_t times_zero(uint32_t a, uint32_t c) {
 
 // 32 bytes of one thread, one sector
 __device__ __forceinline__ void store32(void* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :
+               : "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
 
@@ -353,10 +358,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&w_free[it & 1]);
   };
-  auto w_start = [](const Work& k, int w) { return 128 * (k.nwin - 1 - w); };   // first key of window w, the last keys first
+  // first key of window w, the last keys first
+  auto w_start = [](const Work& k, int w) { return 128 * (k.nwin - 1 - w); };
   // 16-key steps of window w that tile s sees anything of: what lies behind
   // its last token is neither multiplied nor looked at
-  auto steps = [&](const Work& k, int s, int w) { return min(8, (min(k.len, k.t0 + (s + 1) * p.T) - w_start(k, w) + 15) >> 4); };
+  auto steps = [&](const Work& k, int s, int w) {
+    return min(8, (min(k.len, k.t0 + (s + 1) * p.T) - w_start(k, w) + 15) >> 4);
+  };
   // window w holds keys that a row may not see (so does the first, if only as a rule)
   auto scrub = [&](const Work& k, int w) { return w == 0 || w_start(k, w) + 127 > k.t0; };
 
@@ -478,7 +486,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           mbar_arrive_expect_tx(&full[i & 1], L::TILE);
 #pragma unroll
           for (int a = 0; a < D / 64; ++a)
-            tma_load_3d(smem + off + (i & 1) * L::TILE + a * kAtomP, map, &full[i & 1], k.h * D + a * 64, 0, k.row0 + w_start(k, w));
+            tma_load_3d(smem + off + (i & 1) * L::TILE + a * kAtomP, map, &full[i & 1], k.h * D + a * 64, 0,
+                        k.row0 + w_start(k, w));
         }
         ++issued;
       };
@@ -490,7 +499,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           mbar_arrive_expect_tx(&q_full[s], qbytes);
 #pragma unroll
           for (int a = 0; a < D / 64; ++a)
-            tma_load_3d(smem + L::OFF_Q + s * L::TILE + a * kAtomP, &map_q, &q_full[s], a * 64, k.h * p.G, k.row0 + k.t0 + s * p.T);
+            tma_load_3d(smem + L::OFF_Q + s * L::TILE + a * kAtomP, &map_q, &q_full[s], a * 64, k.h * p.G,
+                        k.row0 + k.t0 + s * p.T);
         }
         ++nq[s];
       };
@@ -520,14 +530,16 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const uint64_t dq = sdesc_sw128(base + L::OFF_Q, 16, 1024), dk = sdesc_sw128(base + L::OFF_K, 16, 1024);
     const uint64_t dv = sdesc_sw128(base + L::OFF_V, kAtomP, 1024);
     bool ok = true;
-    int kv = 0, looked = 0, np[2] = {0, 0}, nq[2] = {0, 0};   // windows, windows looked over, P and query tiles before this place
+    // before this place: windows, windows looked over, P and query tiles
+    int kv = 0, looked = 0, np[2] = {0, 0}, nq[2] = {0, 0};
     auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u)); };
     for (int it = 0;; ++it) {
       wait_work(it, ok);
       const Work k = read_work(it, ok);
       free_work(it);
       if (k.len == 0) break;
-      auto product_s = [&](int s, int w, int i, bool first) {   // S_s = Q_s K_w^T; K_w (the CTA's i-th window) has landed
+      // S_s = Q_s K_w^T; K_w (the CTA's i-th window) has landed
+      auto product_s = [&](int s, int w, int i, bool first) {
         if (first) wait(&q_full[s], (uint32_t)nq[s]++);
         if (!ok) return;
         tc_fence_after();
@@ -563,7 +575,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             tc_fence_after();
             const uint64_t b = dv + (uint64_t)((i & 1) * (L::TILE >> 4));
             auto step = [&](int c) {   // 16 keys
-              umma_ts(tm + 256 + s * D, tm + s * 128 + c * 8, b + (uint64_t)(c * (2048 >> 4)), idesc_o, (w > f || c > 0) ? 1u : 0u, leader);
+              umma_ts(tm + 256 + s * D, tm + s * 128 + c * 8, b + (uint64_t)(c * (2048 >> 4)), idesc_o,
+                      (w > f || c > 0) ? 1u : 0u, leader);
             };
             if (!look) {
               const int n = steps(k, s, w);
@@ -615,8 +628,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const int i = kv + w;
         if (ok && !mbar_wait(&v_full[i & 1], (uint32_t)(i >> 1) & 1u)) ok = false;
         uint8_t* sv = smem + L::OFF_V + (i & 1) * L::TILE;
-        // rows of this pair's tokens but the first are looked at, those behind its last token in the same step emptied
-        const int key0 = w_start(k, w), first = max(0, k.t0 + 1 - key0), last = min(128, k.hi - key0), end = (last + 15) & ~15;
+        // rows of this pair's tokens but the first are looked at, those behind
+        // its last token in the same step emptied
+        const int key0 = w_start(k, w), first = max(0, k.t0 + 1 - key0), last = min(128, k.hi - key0);
+        const int end = (last + 15) & ~15;
         constexpr int CH = D / 8;   // 16-byte pieces of a row, 32 / CH rows a step
         bool wrote = last < end;
         const int c = lane % CH;
@@ -687,7 +702,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const int pair = 1 + s * 4 + (warp & 3);   // named barrier of the two warps that share rows
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     const int rt = r / p.G;                    // token of the row in its tile
-    const int ot = (s * p.T + rt) * p.Hq + r % p.G;   // the row's place in the output, from the tile pair's and group's first
+    // the row's place in the output, from the tile pair's and group's first
+    const int ot = (s * p.T + rt) * p.Hq + r % p.G;
     bool ok = true;
     int ns = 0, nf = 0;                        // score tiles, finished outputs before this place
 
@@ -886,7 +902,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 }
 
 template <int D>
-int launch_prompt(PrParams& p, const void* q, const void* k, const void* v, size_t q_stride, size_t kv_stride, cudaStream_t st) {
+int launch_prompt(PrParams& p, const void* q, const void* k, const void* v, size_t q_stride, size_t kv_stride,
+                  cudaStream_t st) {
   CUtensorMap mq, mk, mv;
   int rc = make_tmap_bf16_rows(&mq, q, D, p.Hq, p.rows, q_stride, 64, p.G, p.T);
   if (rc || (rc = make_tmap_bf16_rows(&mk, k, p.Hkv * D, 1, p.rows, kv_stride, 64, 1, 128)) ||
@@ -901,13 +918,15 @@ int launch_prompt(PrParams& p, const void* q, const void* k, const void* v, size
     if (cudaFuncGetAttributes(&fa, prompt_attn_kernel<D>) != cudaSuccess) return TV_E_CUDA;
     regs.store(fa.numRegs, std::memory_order_relaxed);
   }
-  if (regs.load(std::memory_order_relaxed) * kPrThreads < kPrSoftThreads * kSoftRegs + 128 * kRoleRegs) return TV_E_UNSUPPORTED;
+  if (regs.load(std::memory_order_relaxed) * kPrThreads < kPrSoftThreads * kSoftRegs + 128 * kRoleRegs)
+    return TV_E_UNSUPPORTED;
   // at most rows / 2T whole pairs and one ragged pair a sequence
   const long long pairs = (long long)p.rows / (2 * p.T) + (p.n < p.rows ? p.n : p.rows);
   const int sms = num_sms();
   if (sms <= 0) return TV_E_CUDA;
   p.queued = pairs * p.Hkv > sms;
-  return launch_pdl(prompt_attn_kernel<D>, dim3((unsigned)(pairs * p.Hkv)), dim3(kPrThreads), PrSmem<D>::BYTES, st, mq, mk, mv, p);
+  return launch_pdl(prompt_attn_kernel<D>, dim3((unsigned)(pairs * p.Hkv)), dim3(kPrThreads), PrSmem<D>::BYTES, st, mq,
+                    mk, mv, p);
 }
 
 }  // namespace
@@ -915,16 +934,17 @@ int launch_prompt(PrParams& p, const void* q, const void* k, const void* v, size
 
 using namespace tv;
 
-extern "C" int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const tv_bf16* q, const tv_bf16* k, const tv_bf16* v,
-                                size_t q_stride, size_t kv_stride, const int32_t* starts, int n_seqs, int rows, tv_bf16* out,
-                                int32_t* dev_status, void* stream) {
+extern "C" int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const tv_bf16* q, const tv_bf16* k,
+                                const tv_bf16* v, size_t q_stride, size_t kv_stride, const int32_t* starts, int n_seqs,
+                                int rows, tv_bf16* out, int32_t* dev_status, void* stream) {
   if (n_q_heads < 1 || n_kv_heads < 1 || !q || !k || !v || !starts || !out || !dev_status || rows < 1) return TV_E_ARG;
   int rc = check_listed(n_seqs);
   if (rc) return rc;
   if (head_dim != 64 && head_dim != 128) return TV_E_UNSUPPORTED;
   if (n_q_heads % n_kv_heads != 0 || n_q_heads / n_kv_heads > 128 || n_q_heads > 65536) return TV_E_UNSUPPORTED;
   const size_t D = head_dim;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(out) & 31u) != 0 || q_stride % 8 != 0 || kv_stride % 8 != 0) return TV_E_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(out) & 31u) != 0) return TV_E_ARG;
+  if (q_stride % 8 != 0 || kv_stride % 8 != 0) return TV_E_ARG;
   if (q_stride < n_q_heads * D || kv_stride < n_kv_heads * D) return TV_E_ARG;
   PrParams p;
   p.starts = starts;

@@ -197,6 +197,32 @@ def test_rows_past_two_to_the_31(gpu):
     assert np.array_equal(host(k[3, 7]), kk[39, 0]) and np.array_equal(host(v[3, 7]), vv[39, 0])
 
 
+def test_the_longest_length(gpu):
+    """2^31 - 16 tokens: a table row that names one page over and over, but for its last place.
+
+    A CTA adds up 2^24 / 148 tiles or fewer, two products each, and a sum that drops what lies below its
+    last place loses at most 2^-23 of itself a product: 2^18 2^-23 = 2^-5 of sum w |v|, and half of that
+    of the denominator.  The other page's 16 tokens weigh less than 2^-20 (scores differ by less than 4)."""
+    ps, D, n_pages = 16, 64, 2 ** 27 - 1
+    rng = np.random.default_rng(2)
+    k, v = (bits(rng.standard_normal((2, ps, D)) / 8) for _ in range(2))
+    q = bits(rng.standard_normal((1, 4, D)) / 2)
+    table = torch.zeros(1, n_pages, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    gk, gv, refs, lens = dev(k), dev(v), i32([1, 1]), i32([n_pages * ps])
+    pool, seqs = abi.TvPool(gk.data_ptr(), gv.data_ptr(), refs.data_ptr(), 1, 2, 1, ps, D), abi.TvSeqs(table.data_ptr(), lens.data_ptr(), 1, n_pages)
+    out, st, gq = torch.zeros(1, 4, D, dtype=torch.int16, device="cuda"), i32([0]), dev(q)
+    wsb = abi.tv_attend_paged_workspace_size(pool, 4, 1)
+    ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+    assert abi.tv_attend_paged(pool, 0, seqs, i32([0]), 1, 4, gq, 4 * D, None, None, 0, out, ws, wsb, st) == 0
+    assert int(st.item()) == 0
+    qf, kf, vf = bf16_to_f64(q[0]), bf16_to_f64(k[0]), bf16_to_f64(v[0])
+    w = np.exp(qf @ kf.T / np.sqrt(D))
+    w /= w.sum(1, keepdims=True)
+    o, size = w @ vf, w @ np.abs(vf)
+    assert (np.abs(bf16_to_f64(host(out))[0] - o) <= (2.0 ** -5 + 2.0 ** -6 + 3 * 2.0 ** -8 + 2.0 ** -19) * size).all()
+
+
 def test_refusals(gpu):
     E = abi.CODES
     for ids in ([0, 99, 1], [0, -1, 1], [1, 0, 1], list(range(38)) + [40], list(range(38)) + [99999], [3] + list(range(38))):
