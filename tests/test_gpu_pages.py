@@ -259,3 +259,37 @@ def test_captured_and_replayed_on_other_lists(gpu):
         b.o.extend(k, a)
         b.o.compact()
         b.same()
+
+
+@pytest.mark.parametrize("n,max_pages", [(1, 33), (17, 32), (16, 1025), (35, 700), (20, 4000), (2, 8192), (33, 3000), (1, 8200)])
+def test_lists_of_every_width(gpu, n, max_pages):
+    """From one block's work to many blocks'; the first, a middle and the last sequence can refuse."""
+    rows, long = 2 * n + 3, max_pages * 16 - 3
+    b = Both(1, 2 * max_pages + 3 * n + 8, 1, 16, 64, rows, max_pages, n)
+    rng = np.random.default_rng(n)
+    order = rng.permutation(rows).tolist()
+    parents, kids, more = order[:2], order[2:2 + n], order[2 + n:2 + 2 * n]
+    b.extend(parents, [long, long // 2])
+    b.fork([parents[i * i % 3 % 2] for i in range(n)], kids)           # runs of one source, and changes
+    b.extend(kids, [i % 3 for i in range(n)])                          # some last pages are their own now
+    b.fork(kids, more)
+    j = (long + 15) // 16 - 1
+    for row in {kids[0], kids[n // 2], kids[-1]}:                      # one bad entry: nothing changes
+        at = min(j, -(-int(b.o.lens[row]) // 16) - 1)
+        for wrong in (-1, b.o.refs.shape[0], int(np.flatnonzero(b.o.refs == 0)[0])):
+            keep, b.o.pages[row, at] = int(b.o.pages[row, at]), wrong
+            b.pages.copy_(i32(b.o.pages))
+            b.release(kids, [0] * n)
+            b.fork([row], [order[-1]])
+            b.o.pages[row, at] = keep
+            b.pages.copy_(i32(b.o.pages))
+    if n > 1:
+        b.release(kids[:-1] + [kids[0]], [0] * n)
+        b.fork([parents[0]] * n, [order[-1]] * n)
+        b.release(kids, [0] * (n - 1) + [int(b.o.lens[kids[-1]]) + 1])
+        b.release(kids[:-1] + [rows], [0] * n)
+    b.release(kids, [int(rng.integers(0, int(b.o.lens[s]) + 1)) if i % 4 else 0 for i, s in enumerate(kids)])
+    b.release(more + parents, [i % 2 for i in range(n)] + [0, 0])
+    b.release(kids, [0] * n)
+    b.release(more, [0] * n)
+    assert not b.o.refs.any() and not b.refs.any()
