@@ -28,100 +28,101 @@ __device__ __forceinline__ int bad_code(uint32_t bad) {
 }
 
 // ---- releasing and forking ---------------------------------------------------
-// one block per listed sequence: index, length and page entries in range, no
-// index listed twice
-__global__ void __launch_bounds__(kSeqThreads) release_check_kernel(tv_pool pool, tv_seqs t, const int32_t* ids,
-                                                                     const int32_t* keep, int n, int32_t* status) {
+// Releasing (FORK = false: a = ids, b = keep) or forking (a = src, b = dst): one
+// block per listed sequence.  A block is a chain of dependent loads (list,
+// length, entries, counts), so the first entries, kPer a thread, are asked for
+// with the length, and kPer counts are on their way at once.
+constexpr int kPer = 4;
+struct Entries {   // of places j0 + thread + kSeqThreads u of a table row
+  int e[kPer];
+  __device__ __forceinline__ void load(const int32_t* row, int j0, int end) {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int j = j0 + (int)threadIdx.x + u * kSeqThreads;
+      e[u] = j < end ? __ldcg(row + j) : -1;
+    }
+  }
+  template <class F>
+  __device__ __forceinline__ void each(int j0, int first, int last, F f) const {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int j = j0 + (int)threadIdx.x + u * kSeqThreads;
+      if (j >= first && j < last) f(u, j, e[u]);
+    }
+  }
+};
+
+// indexes, lengths and page entries in range, no index listed twice; forking:
+// no target among the sources, every target empty
+template <bool FORK>
+__global__ void __launch_bounds__(kSeqThreads) list_check_kernel(tv_pool pool, tv_seqs t, const int32_t* a,
+                                                                 const int32_t* b, int n, int32_t* status) {
   pdl_wait();
   pdl_trigger();
-  const int i = blockIdx.x;
-  const int s = ids[i];
+  const int i = blockIdx.x, ps = pool.page_size;
+  const int s = a[i], d = b[i];   // d: the target row, or the tokens kept
   int bad = 0;
-  if (s < 0 || s >= t.max_seqs) {
+  if (s < 0 || s >= t.max_seqs || (FORK && (d < 0 || d >= t.max_seqs))) {
     bad = TV_E_SEQ;
   } else {
+    const int32_t* row = t.pages + (size_t)s * t.max_pages;
+    Entries x;
+    x.load(row, 0, t.max_pages);
+    const int len = seq_len(t, ps, s), there = FORK ? __ldcg(t.lens + d) : 0;
     for (int j = threadIdx.x; j < n; j += kSeqThreads)
-      if (j != i && ids[j] == s) bad = TV_E_SEQ;
-    const int len = seq_len(t, pool.page_size, s);
-    const int kept = keep[i];
-    if (len < 0 || kept < 0 || kept > len) {
+      if (FORK ? (j != i && b[j] == d) || a[j] == d : j != i && a[j] == s) bad = TV_E_SEQ;
+    if (len < 0 || there != 0 || (!FORK && (d < 0 || d > len))) {
       bad = TV_E_SEQ;
     } else {
-      const int32_t* row = t.pages + (size_t)s * t.max_pages;
-      for (int j = pages_of(kept, pool.page_size) + threadIdx.x; j < pages_of(len, pool.page_size); j += kSeqThreads) {
-        const int p = __ldcg(row + j);
-        if (p < 0 || p >= pool.n_pages || __ldcg(pool.refs + p) < 1) bad = TV_E_PAGE;
+      const int first = FORK ? 0 : pages_of(d, ps), last = pages_of(len, ps);
+      for (long long j0 = 0; j0 < last; j0 += kPer * kSeqThreads) {
+        if (j0 > 0) x.load(row, (int)j0, last);
+        int held[kPer];
+        x.each((int)j0, 0, last, [&](int u, int, int p) {
+          held[u] = p >= 0 && p < pool.n_pages ? __ldcg(pool.refs + p) : 0;
+        });
+        x.each((int)j0, first, last, [&](int u, int, int) {
+          if (held[u] < 1) bad = TV_E_PAGE;
+        });
       }
     }
   }
   if (bad) status_set(status, bad);
 }
 
-__global__ void __launch_bounds__(kSeqThreads) release_kernel(tv_pool pool, tv_seqs t, const int32_t* ids,
-                                                               const int32_t* keep, int32_t* status) {
+template <bool FORK>
+__global__ void __launch_bounds__(kSeqThreads) list_apply_kernel(tv_pool pool, tv_seqs t, const int32_t* a,
+                                                                 const int32_t* b, int32_t* status) {
   pdl_wait();
   pdl_trigger();
-  if (block_skip(status)) return;
-  const int s = ids[blockIdx.x], kept = keep[blockIdx.x];
-  const int len = __ldcg(t.lens + s);
-  const int32_t* row = t.pages + (size_t)s * t.max_pages;
-  for (int j = pages_of(kept, pool.page_size) + threadIdx.x; j < pages_of(len, pool.page_size); j += kSeqThreads)
-    atomicSub(pool.refs + __ldcg(row + j), 1);
-  __syncthreads();   // every thread has the old length
-  if (threadIdx.x == 0) t.lens[s] = kept;
-}
-
-__global__ void __launch_bounds__(kSeqThreads) fork_check_kernel(tv_pool pool, tv_seqs t, const int32_t* src,
-                                                                  const int32_t* dst, int n, int32_t* status) {
-  pdl_wait();
-  pdl_trigger();
-  const int i = blockIdx.x;
-  const int s = src[i], d = dst[i];
-  int bad = 0;
-  if (s < 0 || s >= t.max_seqs || d < 0 || d >= t.max_seqs) {
-    bad = TV_E_SEQ;
-  } else {
-    for (int j = threadIdx.x; j < n; j += kSeqThreads)
-      if ((j != i && dst[j] == d) || src[j] == d) bad = TV_E_SEQ;
-    const int len = seq_len(t, pool.page_size, s);
-    if (len < 0 || __ldcg(t.lens + d) != 0) {
-      bad = TV_E_SEQ;
-    } else {
-      const int32_t* row = t.pages + (size_t)s * t.max_pages;
-      for (int j = threadIdx.x; j < pages_of(len, pool.page_size); j += kSeqThreads) {
-        const int p = __ldcg(row + j);
-        if (p < 0 || p >= pool.n_pages || __ldcg(pool.refs + p) < 1) bad = TV_E_PAGE;
-      }
-    }
+  const int stop = status_get(status), ps = pool.page_size;
+  const int s = a[blockIdx.x], d = b[blockIdx.x];
+  const bool in = s >= 0 && s < t.max_seqs && (!FORK || (d >= 0 && d < t.max_seqs));   // false only where it stops
+  Entries x;
+  int len = 0;
+  if (in) {
+    x.load(t.pages + (size_t)s * t.max_pages, 0, t.max_pages);
+    len = __ldcg(t.lens + s);
   }
-  if (bad) status_set(status, bad);
-}
-
-__global__ void __launch_bounds__(kSeqThreads) fork_kernel(tv_pool pool, tv_seqs t, const int32_t* src,
-                                                            const int32_t* dst, int32_t* status) {
-  pdl_wait();
-  pdl_trigger();
-  if (block_skip(status)) return;
-  const int s = src[blockIdx.x], d = dst[blockIdx.x];
-  const int len = __ldcg(t.lens + s);
-  const int32_t* from = t.pages + (size_t)s * t.max_pages;
-  int32_t* to = t.pages + (size_t)d * t.max_pages;
-  for (int j = threadIdx.x; j < pages_of(len, pool.page_size); j += kSeqThreads) {
-    const int p = __ldcg(from + j);
-    to[j] = p;
-    atomicAdd(pool.refs + p, 1);
+  if (__syncthreads_or(stop != 0 || !in)) return;   // from here on every thread has the old length
+  const int first = FORK ? 0 : pages_of(d, ps), last = pages_of(len, ps);
+  for (long long j0 = 0; j0 < last; j0 += kPer * kSeqThreads) {
+    if (j0 > 0) x.load(t.pages + (size_t)s * t.max_pages, (int)j0, last);
+    x.each((int)j0, first, last, [&](int, int j, int p) {
+      if (FORK) t.pages[(size_t)d * t.max_pages + j] = p;
+      atomicAdd(pool.refs + p, FORK ? 1 : -1);
+    });
   }
-  if (threadIdx.x == 0) t.lens[d] = len;
+  if (threadIdx.x == 0) t.lens[FORK ? d : s] = FORK ? len : d;
 }
 
-// Releasing (FORK = false: a = ids, b = keep) or forking (a = src, b = dst) by
-// one block, a warp a listed sequence, which holds its table entries in
-// registers between the look and the act.  Such a call is a chain of dependent
+// The same by one block, a warp a listed sequence, which holds its table
+// entries in registers between the look and the act.  Such a call is a chain of dependent
 // loads (list, length and entries, counts), about 0.6 us each, and its
 // launches, 2 to 3 us each; one SM's atomics are what it can run out of.  A
 // pass of release, fork, extend, release took, by one block against two
-// launches a call: 14.7 against 18.1 us for 8 sequences of 65 pages, but 24.0
-// against 18.9 us for 8 of 494 and 40.3 against 25.4 us for 32 of 494.
+// launches a call: 14.5 against 18.1 us for 8 sequences of 65 pages, but 24.0
+// against 18.6 us for 8 of 494 and 40.3 against 25.3 us for 32 of 494.
 constexpr int kBlockThreads = 1024;
 constexpr int kWarpEntries = 512;     // table entries a warp's registers hold
 constexpr int kBlockEntries = 1024;   // and those a block takes on
@@ -657,9 +658,9 @@ int tv_pages_release(const tv_pool* pool, const tv_seqs* seqs, const int32_t* id
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (one_block(*seqs, n))
     return launch_pdl(list_block_kernel<false>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
-  rc = launch_pdl(release_check_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
+  rc = launch_pdl(list_check_kernel<false>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
   if (rc) return rc;
-  return launch_pdl(release_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, dev_status);
+  return launch_pdl(list_apply_kernel<false>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, dev_status);
 }
 
 int tv_pages_fork(const tv_pool* pool, const tv_seqs* seqs, const int32_t* src, const int32_t* dst, int n,
@@ -671,9 +672,9 @@ int tv_pages_fork(const tv_pool* pool, const tv_seqs* seqs, const int32_t* src, 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (one_block(*seqs, n))
     return launch_pdl(list_block_kernel<true>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
-  rc = launch_pdl(fork_check_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
+  rc = launch_pdl(list_check_kernel<true>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
   if (rc) return rc;
-  return launch_pdl(fork_kernel, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, dev_status);
+  return launch_pdl(list_apply_kernel<true>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, dev_status);
 }
 
 int tv_pages_extend(const tv_pool* pool, const tv_seqs* seqs, const int32_t* ids, const int32_t* add, int n,
