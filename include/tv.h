@@ -696,7 +696,8 @@ TV_API int tv_pages_read(const tv_pool *pool, int layer, const tv_seqs *seqs, co
  *   out       device bf16 [rows][n_q_heads][head_dim], 32-byte aligned; may not overlap the inputs
  * head_dim 64 or 128, n_q_heads a multiple of n_kv_heads with at most 128 query
  * heads a KV head, at most 4096 sequences (else TV_E_UNSUPPORTED).  P is
- * rounded to bf16 for the product with V, everything else is fp32.  What a row
+ * rounded to bf16 for the product with V, everything else is fp32; scores
+ * (q . k / sqrt(head_dim)) up to 2^27 in magnitude.  What a row
  * may not see does not reach it, whatever it holds.  The same inputs give the
  * same bits.  No workspace.
  * Host checks: TV_E_ARG, TV_E_UNSUPPORTED.  Device checks: TV_E_SEQ (starts;

@@ -726,8 +726,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       // kHigh some score lies too far above it, and below kLow, where the row
       // sees its first keys, all of them lie too far below.  Then (hardly ever)
       // both threads of the row find its maximum, the offset goes kAbove beyond
-      // it, and the exponentials are taken again, whose sum can not be above
-      // kHigh.  P stays in registers until both warps have read their scores,
+      // it, and the exponentials are taken again, once: their sum is below kHigh
+      // then, but for scores beyond some 2^16, whose maximum (as the offset) is
+      // known only to half its last place: 2^3 at the end of what the call
+      // allows, so that a sum stays below 2^26.  P stays in registers until both warps have read their scores,
       // because it goes where the scores are.
       // lim: the last visible one of this thread's keys; before: the first key
       // of the window before (rows before it have seen none); again: O_s holds
@@ -791,7 +793,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           tc_fence_before();
           const bool any = pair_any(off, pair);
           tc_fence_after();
-          if (!any) break;
+          if (!any || !first) break;
           float y = -INFINITY, z = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {

@@ -102,6 +102,36 @@ def test_rising_scores_rescale_every_window(gpu):
     Prompt([1100], 4, 2, 128, seed=4, edit=edit).check()
 
 
+@pytest.mark.parametrize("up", [1.0, 2.0 ** 7, -2.0 ** 7])
+def test_scores_at_the_end_of_their_precision(gpu, up):
+    """Scores of 2^20 and 2^27 (powers of two), known to half of 2^-4 and of 2^3.
+
+    The products are integers below 2^24 times `up`, so the scores are exact.  The second window's are chosen so
+    that an offset taken from the first one's, 20 beyond it, seems to be right for them (they round to at most 2
+    above it) while 64 exponentials add up to more than the 256 that an offset may have."""
+    f = np.float32
+    scale = f(1.4426950408889634 / 8)
+    for first in range(4_000_000, 4_002_000):
+        x = (first + np.arange(-300, 400)) * up
+        m = f(f(f(first * up) * scale) + f(20))
+        over = x * float(scale) - float(m)
+        found = np.flatnonzero((x.astype(f) * scale <= f(m + f(2))) & (over > 2.012) & (over < 60))
+        if found.size:
+            break
+    assert found.size
+    second = int(found[0]) - 300 + first
+
+    def rows(dot):
+        whole, rest = divmod(dot, 256)
+        return np.array([whole // 63 + (i < whole % 63) for i in range(63)] + [rest], np.float64)
+
+    def edit(p):
+        p.q[:], p.k[:] = bits(np.full(p.q.shape, 256.0 * up)), bits(np.broadcast_to(rows(first), p.k.shape))
+        p.q[:, :, 63] = bits(np.array([up]))[0]
+        p.k[256:384] = bits(rows(second))
+    Prompt([700], 1, 1, 64, seed=11, edit=edit).check()
+
+
 @pytest.mark.parametrize("q_heads,kv_heads,dim", [(5, 1, 128), (3, 1, 64), (1, 1, 128)])
 def test_very_low_scores(gpu, q_heads, kv_heads, dim):
     """Scores of minus some hundreds everywhere: an offset that is not the row's own would leave nothing of it."""
