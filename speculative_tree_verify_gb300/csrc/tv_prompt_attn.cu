@@ -860,7 +860,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const unsigned tag = (unsigned)it + 1u;
         const unsigned long long* bad = s_bad + (it & 1) * 3 * D;
         const bool anybad = *reinterpret_cast<volatile unsigned*>(&s_anybad[it & 1]) == tag;
-        __nv_bfloat16* dst = p.out + ((size_t)(k.row0 + k.t0) * p.Hq + k.h * p.G + ot) * D + hf * (D / 2);
+        // Two lanes store 64 bytes of one row, then of the other's: a store
+        // instruction takes the memory pipe a cycle for every 128-byte line that
+        // it touches.
+        const bool odd = lane & 1;
+        const int mate = __shfl_xor_sync(0xffffffffu, ot, 1);
+        const unsigned keep = __ballot_sync(0xffffffffu, ok && live);
+        __nv_bfloat16* dst = p.out + ((size_t)(k.row0 + k.t0) * p.Hq + k.h * p.G) * D + hf * (D / 2) + (odd ? 16 : 0);
+        __nv_bfloat16 *dst0 = dst + (size_t)(odd ? mate : ot) * D, *dst1 = dst + (size_t)(odd ? ot : mate) * D;
+        const bool keep0 = keep >> (lane & 30) & 1u, keep1 = keep >> (lane | 1) & 1u;
 #pragma unroll
         for (int c = 0; c < D / 2; c += 32) {
           uint32_t o[32];
@@ -877,17 +885,20 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               else if (ni) o[u] = 0xff800000u;
             }
           }
+          uint32_t b0[8], b1[8];
 #pragma unroll
-          for (int u = 0; u < 32; u += 16) {
-            uint32_t b[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const __nv_bfloat162 v =
-                  __floats2bfloat162_rn(__uint_as_float(o[u + 2 * e]) * inv, __uint_as_float(o[u + 2 * e + 1]) * inv);
-              b[e] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            if (ok && live) store32(dst + c + u, b);
+          for (int e = 0; e < 8; ++e) {
+            const __nv_bfloat162 v =
+                __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+            const __nv_bfloat162 w =
+                __floats2bfloat162_rn(__uint_as_float(o[16 + 2 * e]) * inv, __uint_as_float(o[17 + 2 * e]) * inv);
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(&v), y = *reinterpret_cast<const uint32_t*>(&w);
+            const uint32_t z = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
+            b0[e] = odd ? z : x;
+            b1[e] = odd ? y : z;
           }
+          if (keep0) store32(dst0 + c, b0);
+          if (keep1) store32(dst1 + c, b1);
         }
         tc_fence_before();   // the next place's products into O_s follow this warp's next arrival
       }
