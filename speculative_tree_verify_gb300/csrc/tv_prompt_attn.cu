@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           tc_fence_after();
           if (!any || !first) break;
           float y = -INFINITY, z = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             uint32_t x[32];
             scores(c, x);
@@ -816,7 +816,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           if (move) m = next;
           l *= scale;
           if (again) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 2; c += 16) {
               uint32_t o[16];
               ld16(sO + c, o);
@@ -858,8 +858,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const int t = k.t0 + s * p.T + rt;
         const bool live = r < p.T * p.G && t < k.len;
         const unsigned tag = (unsigned)it + 1u;
-        const unsigned long long* bad = s_bad + (it & 1) * 3 * D;
-        const bool anybad = *reinterpret_cast<volatile unsigned*>(&s_anybad[it & 1]) == tag;
         // Two lanes store 64 bytes of one row, then of the other's: a store
         // instruction takes the memory pipe a cycle for every 128-byte line that
         // it touches.
@@ -869,22 +867,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         __nv_bfloat16* dst = p.out + ((size_t)(k.row0 + k.t0) * p.Hq + k.h * p.G) * D + hf * (D / 2) + (odd ? 16 : 0);
         __nv_bfloat16 *dst0 = dst + (size_t)(odd ? mate : ot) * D, *dst1 = dst + (size_t)(odd ? ot : mate) * D;
         const bool keep0 = keep >> (lane & 30) & 1u, keep1 = keep >> (lane | 1) & 1u;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 2; c += 32) {
           uint32_t o[32];
           ld32(sO + c, o);
           tmem_ld_wait();
-          if (anybad) {
-            const unsigned long long* first = bad + hf * (D / 2) + c;
-            auto sees = [&](unsigned long long x) { return (unsigned)(x >> 32) == ~tag && (int)(unsigned)x <= t; };
-#pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              const bool n = sees(first[u]), pi = sees(first[D + u]), ni = sees(first[2 * D + u]);
-              if (n || (pi && ni)) o[u] = 0x7fc00000u;
-              else if (pi) o[u] = 0x7f800000u;
-              else if (ni) o[u] = 0xff800000u;
-            }
-          }
           uint32_t b0[8], b1[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -899,6 +886,17 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           if (keep0) store32(dst0 + c, b0);
           if (keep1) store32(dst1 + c, b1);
+        }
+        if (*reinterpret_cast<volatile unsigned*>(&s_anybad[it & 1]) == tag) {   // what of V is not finite
+          const unsigned long long* first = s_bad + (it & 1) * 3 * D + hf * (D / 2);
+          uint16_t* row = reinterpret_cast<uint16_t*>(dst - (odd ? 16 : 0)) + (size_t)ot * D;
+          auto sees = [&](unsigned long long x) { return (unsigned)(x >> 32) == ~tag && (int)(unsigned)x <= t; };
+          __syncwarp();   // over what the other lane has stored
+#pragma unroll 1
+          for (int c = 0; c < D / 2; ++c) {
+            const bool n = sees(first[c]), pi = sees(first[D + c]), ni = sees(first[2 * D + c]);
+            if ((n || pi || ni) && ok && live) row[c] = n || (pi && ni) ? 0x7fc0 : (pi ? 0x7f80 : 0xff80);
+          }
         }
         tc_fence_before();   // the next place's products into O_s follow this warp's next arrival
       }
