@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* p_full = s_full + 2;                                         // [2] P_s stored, O_s rescaled (8 warps)
   uint64_t* o_fin = p_full + 2;                                          // [2] the last product into O_s done
   // a window's V looked over: two barriers in turn, since the look may be a
-  // window ahead of the products
+  // window ahead of the products (not two: V has two stages)
   uint64_t* v_ok = o_fin + 2;
   uint64_t* w_full = v_ok + 2;                                           // [2] a place written down
   uint64_t* w_free = w_full + 2;                                         // [2] every role has read it
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       mbar_init(&k_full[s], 1);
       mbar_init(&k_free[s], 1);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_free[s], 1);
+      mbar_init(&v_free[s], 2);   // the products and the look
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], kPrSoftWarps / 2);
       mbar_init(&o_fin[s], 1);
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   } else if (warp == kWarpLook) {
     // ---------------- V rows that a row may not see ----------------
     bool ok = true;
-    int kv = 0, looked = 0, nf = 0;   // windows, windows looked over, places with two tiles before this place
+    int kv = 0, looked = 0;   // windows, windows looked over before this place
     for (int it = 0;; ++it) {
       wait_work(it, ok);
       const Work k = read_work(it, ok);
@@ -624,9 +624,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       // behind is larger.
       unsigned long long* bad = s_bad + (it & 1) * 3 * D;
       const unsigned tag = (unsigned)it + 1u;
-      for (int w = 0; w < k.nwin && scrub(k, w); ++w, ++looked) {
+      for (int w = 0; w < k.nwin; ++w) {
         const int i = kv + w;
-        if (ok && !mbar_wait(&v_full[i & 1], (uint32_t)(i >> 1) & 1u)) ok = false;
+        ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i & 1], (uint32_t)(i >> 1) & 1u));
+        if (!ok) break;
+        if (!scrub(k, w)) {   // nothing to look at; the stage is not filled again before this, so that no phase is missed
+          if (lane == 0) mbar_arrive(&v_free[i & 1]);
+          continue;
+        }
         uint8_t* sv = smem + L::OFF_V + (i & 1) * L::TILE;
         // rows of this pair's tokens but the first are looked at, those behind
         // its last token in the same step emptied
@@ -681,13 +686,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         if (wrote) fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&v_ok[looked & 1]);
+        if (lane == 0) {
+          mbar_arrive(&v_ok[looked & 1]);
+          mbar_arrive(&v_free[i & 1]);
+        }
+        ++looked;
       }
+      if (!ok) break;
       kv += k.nwin;
-      // to the place's end: every window before the next place's first has
-      // landed then, so that the wait for that one is for its own phase
-      if (ok && !mbar_wait(&o_fin[k.nst - 1], (uint32_t)(k.nst == 2 ? nf : it) & 1u)) ok = false;
-      nf += k.nst - 1;
     }
     if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
   }
