@@ -34,9 +34,9 @@
 // tokens 2866 as first built; 1984 with the issuing warp in step (its
 // descriptors stay in uniform registers); 1838 with two threads a row; 1749
 // with sums instead of maxima; 1690 taking over places; 1654 with headroom in
-// the offsets; 1623 to 1655 now, 1660 to 1690 TFLOP/s: 88 % of what cuBLAS
-// reaches in a burst, 98 % of its sustained rate.  4k: 112 (1.5 PFLOP/s);
-// 24 prompts of 1 to 1531: 64; one of 1024: 17.5.
+// the offsets; 1623 to 1677 now, 1640 to 1690 TFLOP/s: 86 to 88 % of what
+// cuBLAS reaches in a burst, 96 to 98 % of its sustained rate.  4k: 111 (1.55
+// PFLOP/s); 24 prompts of 1 to 1531: 60; one of 1024: 16.8.
 //
 // Masked places: a key that a row may not see has weight zero, and its V may
 // be anything.  0 * NaN would reach the row through the product, so the V rows
