@@ -80,6 +80,14 @@ def test_long(gpu, q_heads, kv_heads, dim, length):
     Prompt([length, 257], q_heads, kv_heads, dim, seed=length).check()
 
 
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(10, 2, 64), (10, 2, 128), (4, 4, 64), (48, 2, 64)])
+def test_more_places_than_blocks(gpu, q_heads, kv_heads, dim):
+    """Blocks that take over several places each, of one window to many, of one tile of queries and of two."""
+    tokens = 128 // (q_heads // kv_heads)
+    lens = [1500, tokens, 900, 3 * tokens, 1, 700, 2 * tokens + 1, 1111, 130, 5 * tokens - 1, 600, 257, 1, 800]
+    Prompt(lens if dim == 128 or q_heads > 4 else lens * 3, q_heads, kv_heads, dim, seed=dim + q_heads).check()
+
+
 def test_many_short(gpu):
     rng = np.random.default_rng(1)
     Prompt(rng.integers(0, 9, 700).tolist(), 4, 2, 64, seed=2).check()
