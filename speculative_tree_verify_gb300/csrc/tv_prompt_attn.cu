@@ -150,10 +150,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+// a += x, x the bits of a bf16
+__device__ __forceinline__ void add_bf16(float& a, uint16_t x) {
+  asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(a) : "h"(x));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {   // NaN inputs are ignored
   float r;
@@ -769,7 +768,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         float sum;
         for (bool first = true;; first = false) {
           const uint64_t neg2 = pack2(-m, -m);
-          uint64_t l2 = 0, l3 = 0;
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             if (!PLAIN && 32 * c > any_see) {
@@ -786,14 +785,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               const __nv_bfloat162 v = __floats2bfloat162_rn(ex2p(a), ex2p(b));
               const uint32_t q = *reinterpret_cast<const uint32_t*>(&v);
               pk[16 * c + u] = q;
-              const uint64_t q2 = pack2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
-              if (u & 1) l3 = add2(l3, q2);
-              else l2 = add2(l2, q2);
+              add_bf16(part[2 * (u & 1)], (uint16_t)q);
+              add_bf16(part[2 * (u & 1) + 1], (uint16_t)(q >> 16));
             }
           }
-          float a, b;
-          unpack2(add2(l2, l3), a, b);
-          sum = a + b;
+          sum = (part[0] + part[1]) + (part[2] + part[3]);
           const bool fresh = !PLAIN && before > t;   // the row's first keys, if it sees any
           const bool off = sum > kHigh || (first && fresh && live && lim >= 0 && sum < kLow);
           tc_fence_before();
