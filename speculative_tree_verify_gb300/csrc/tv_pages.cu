@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kSeqThreads) list_check_kernel(tv_pool pool, t
 
 template <bool FORK>
 __global__ void __launch_bounds__(kSeqThreads) list_apply_kernel(tv_pool pool, tv_seqs t, const int32_t* a,
-                                                                 const int32_t* b, int32_t* status) {
+                                                                 const int32_t* b, int n, int32_t* status) {
   pdl_wait();
   pdl_trigger();
   const int stop = status_get(status), ps = pool.page_size;
@@ -104,13 +104,25 @@ __global__ void __launch_bounds__(kSeqThreads) list_apply_kernel(tv_pool pool, t
     x.load(t.pages + (size_t)s * t.max_pages, 0, t.max_pages);
     len = __ldcg(t.lens + s);
   }
+  // Samples of one source stand next to each other: the first of a run counts
+  // its pages for all of them.
+  int count = 1;
+  if (FORK) {
+    const int i = blockIdx.x, lane = threadIdx.x & 31;
+    if (i > 0 && a[i - 1] == s) count = 0;
+    for (int j = i + 1; count > 0; j += 32) {
+      const unsigned other = __ballot_sync(0xffffffffu, j + lane >= n || a[j + lane] != s);
+      count += other ? __ffs(other) - 1 : 32;
+      if (other) break;
+    }
+  }
   if (__syncthreads_or(stop != 0 || !in)) return;   // from here on every thread has the old length
   const int first = FORK ? 0 : pages_of(d, ps), last = pages_of(len, ps);
   for (long long j0 = 0; j0 < last; j0 += kPer * kSeqThreads) {
     if (j0 > 0) x.load(t.pages + (size_t)s * t.max_pages, (int)j0, last);
     x.each((int)j0, first, last, [&](int, int j, int p) {
       if (FORK) t.pages[(size_t)d * t.max_pages + j] = p;
-      atomicAdd(pool.refs + p, FORK ? 1 : -1);
+      if (count > 0) atomicAdd(pool.refs + p, FORK ? count : -1);
     });
   }
   if (threadIdx.x == 0) t.lens[FORK ? d : s] = FORK ? len : d;
@@ -122,7 +134,7 @@ __global__ void __launch_bounds__(kSeqThreads) list_apply_kernel(tv_pool pool, t
 // launches, 2 to 3 us each; one SM's atomics are what it can run out of.  A
 // pass of release, fork, extend, release took, by one block against two
 // launches a call: 14.5 against 18.1 us for 8 sequences of 65 pages, but 24.0
-// against 18.6 us for 8 of 494 and 40.3 against 25.3 us for 32 of 494.
+// against 18.2 us for 8 of 494 and 40.3 against 23.6 us for 32 of 494.
 constexpr int kBlockThreads = 1024;
 constexpr int kWarpEntries = 512;     // table entries a warp's registers hold
 constexpr int kBlockEntries = 1024;   // and those a block takes on
@@ -660,7 +672,7 @@ int tv_pages_release(const tv_pool* pool, const tv_seqs* seqs, const int32_t* id
     return launch_pdl(list_block_kernel<false>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
   rc = launch_pdl(list_check_kernel<false>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
   if (rc) return rc;
-  return launch_pdl(list_apply_kernel<false>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, dev_status);
+  return launch_pdl(list_apply_kernel<false>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
 }
 
 int tv_pages_fork(const tv_pool* pool, const tv_seqs* seqs, const int32_t* src, const int32_t* dst, int n,
@@ -674,7 +686,7 @@ int tv_pages_fork(const tv_pool* pool, const tv_seqs* seqs, const int32_t* src, 
     return launch_pdl(list_block_kernel<true>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
   rc = launch_pdl(list_check_kernel<true>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
   if (rc) return rc;
-  return launch_pdl(list_apply_kernel<true>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, dev_status);
+  return launch_pdl(list_apply_kernel<true>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
 }
 
 int tv_pages_extend(const tv_pool* pool, const tv_seqs* seqs, const int32_t* ids, const int32_t* add, int n,
