@@ -179,8 +179,10 @@ def _p(x) -> Optional[int]:
     """Device/host address of a tensor, an int, or None."""
     try:
         return x.data_ptr()
-    except AttributeError:   # an address already, or None
-        return x
+    except AttributeError:
+        if x is None or isinstance(x, int):
+            return x
+        raise
 
 
 def _arr(ctype, items: Sequence):

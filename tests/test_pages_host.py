@@ -110,6 +110,12 @@ def test_attend_prompt_host_checks():
         assert call(**over) == E["TV_E_UNSUPPORTED"], over
 
 
+@pytest.mark.parametrize("what", [b"x" * 64, "x", 1.5, np.zeros(4, np.int32), [1]])
+def test_what_is_no_address(what):
+    with pytest.raises(AttributeError):
+        CALLS["fork"](_pool(), _seqs(), ids=what)
+
+
 def test_workspace_refuses_bad_shapes():
     with pytest.raises(ValueError, match="UNSUPPORTED"):
         abi.tv_pages_workspace_size(_pool(page_size=17), _seqs())
