@@ -127,9 +127,6 @@ __device__ __forceinline__ void comp_sync() { asm volatile("bar.sync 1, %0;" ::"
 __device__ __forceinline__ void quad_sync(int quad) {
   asm volatile("bar.sync %0, %1;" ::"r"(2 + quad), "n"(kCompThreads / 2) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
-}
 
 __device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % kTile != 0); }
 
@@ -143,7 +140,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* empty = full + kStages;
   uint64_t* q_full = empty + kStages;    // [kQueries] a segment's queries landed
-  uint64_t* q_free = q_full + kQueries;  // [kQueries] the warps that compute it are done with them
+  uint64_t* q_free = q_full + kQueries;  // [kQueries] all eight warps have seen them, those that compute it are done with them
   uint32_t* s_first = reinterpret_cast<uint32_t*>(smem + L::OFF_FIRST);
   float* s_red = reinterpret_cast<float*>(smem + L::OFF_RED);
   float2* s_ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
@@ -392,7 +389,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int h = g.h, r0 = g.hb * kRows;   // KV head, first query head of the block in the group
     const int nr = min(kRows, p.G - r0);
     if (g.T == 1 && (st & 1) != quad) {   // one tile, and the other four warps'
-      if (ok && !mbar_wait(&q_full[qs], qs_par)) ok = false;   // no further ahead than the queries
+      // no further ahead than the queries, nor further behind than their place:
+      // it is not loaded again before these warps, too, have seen this phase (a
+      // wait that comes a round late names the phase before last, which a parity can not)
+      if (ok && !mbar_wait(&q_full[qs], qs_par)) ok = false;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_free[qs]);
       if (++st == kStages) st = 0, st_par ^= 1u;
       if (++qs == qslots) qs = 0, qs_par ^= 1u;
       continue;
@@ -517,8 +519,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 
     // ---- the head block's partial results into one ----
     // of all eight warps, or, where the head block is one tile, of the four
-    // that had it: the other four go on to the next head block meanwhile (not
-    // far: its queries are not loaded before these have given up theirs)
+    // that had it: the other four go on to the next head block meanwhile
     const bool whole = g.t0 == 0 && g.t1 == g.T;
     // a CTA's first run may begin inside a head block, its last end inside one
     const size_t slot = (size_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0);
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       // The queries' place is given up here, not behind the loads: an arrival
       // does not wait for ldmatrix results that nothing has used yet.  (A warp
       // without a token in this run has not used them, and never will.)
-      if (lane == 0) mbar_arrive_n(&q_free[qs], kCompWarps / NW);
+      if (lane == 0) mbar_arrive(&q_free[qs]);
 #pragma unroll 1   // one copy of the code: most groups need one or two parts, and short sequences run it once a tile
       for (int part = 0; part * kRedRows < nr; ++part) {   // rows 4 part .. + 3, of the lanes with g8 / 4 = part mod 2
         const bool upper = part >> 1;

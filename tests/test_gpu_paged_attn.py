@@ -298,3 +298,19 @@ def test_graphs_share_a_workspace_and_lengths_grow(gpu):
                 c.out.fill_(77)
                 assert c.run() == 0
                 assert np.array_equal(host(c.out), x)     # the same bits
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(10, 2, 128), (16, 2, 64), (12, 1, 64), (16, 1, 128), (24, 1, 64)])
+@pytest.mark.parametrize("n", [600, 2048])
+def test_many_sequences_of_one_tile(gpu, q_heads, kv_heads, dim, n):
+    """Groups of 5 to 24 heads, whose queries have 6 to 2 places, and runs that the two halves of a block take in turn;
+    lists whose rows and lengths lie in shared memory and longer ones.  The same bits every time."""
+    lens = np.random.default_rng(n + q_heads).integers(1, 65, n).tolist()
+    c = Case(lens, q_heads, kv_heads, dim, 16, seed=n)
+    c.check()
+    first = host(c.out).copy()
+    for _ in range(100):
+        assert c.run() == 0
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0, abi.STATUS.get(int(c.status.item()))
+    assert np.array_equal(host(c.out), first)
