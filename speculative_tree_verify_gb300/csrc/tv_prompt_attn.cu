@@ -895,10 +895,17 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           uint16_t* row = reinterpret_cast<uint16_t*>(dst - (odd ? 16 : 0)) + (size_t)ot * D;
           auto sees = [&](unsigned long long x) { return (unsigned)(x >> 32) == ~tag && (int)(unsigned)x <= t; };
           __syncwarp();   // over what the other lane has stored
+          // Added to what the products left, which may be NaN or infinite
+          // itself: by a key before the pair's own, by the row's scores.
 #pragma unroll 1
           for (int c = 0; c < D / 2; ++c) {
             const bool n = sees(first[c]), pi = sees(first[D + c]), ni = sees(first[2 * D + c]);
-            if ((n || pi || ni) && ok && live) row[c] = n || (pi && ni) ? 0x7fc0 : (pi ? 0x7f80 : 0xff80);
+            if ((n || pi || ni) && ok && live) {
+              float x = __uint_as_float((uint32_t)*reinterpret_cast<volatile uint16_t*>(row + c) << 16);
+              if (pi) x += INFINITY;
+              if (ni) x -= INFINITY;
+              row[c] = n || x != x ? 0x7fc0 : (uint16_t)(__float_as_uint(x) >> 16);
+            }
           }
         }
         tc_fence_before();   // the next place's products into O_s follow this warp's next arrival

@@ -172,6 +172,51 @@ def test_what_a_row_may_not_see_does_not_reach_it(gpu, value, q_heads, kv_heads,
     assert np.isfinite(k[:20]).all() and np.isnan(k[20:lens[0], :q_heads // kv_heads]).all() and np.isfinite(k[lens[0]:]).all()
 
 
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(4, 2, 64), (5, 1, 128), (1, 1, 128)])
+@pytest.mark.parametrize("early,late", [(0x7FC0, 0x7F80), (0x7FC0, 0xFF80), (0xFF80, 0x7F80), (0x7F80, 0xFF80), (0x7F80, 0x7F80), (0xFF80, 0xFF80)])
+def test_values_that_are_not_finite_add_up(gpu, early, late, q_heads, kv_heads, dim):
+    """An early token's value comes through the products, that of a row's own tile pair beside them: both together are
+    what their sum is, wherever the tile pairs begin."""
+    n = 700
+    plain = Prompt([n], q_heads, kv_heads, dim, seed=13).result()
+    a, b = bf16_to_f64(np.array([early, late], np.uint16))
+    with np.errstate(invalid="ignore"):
+        both = a + b
+    for first, second in ((10, 200), (3, 520), (130, 699), (255, 257), (0, 1)):
+        def edit(p):
+            p.v[first, 0, 3], p.v[second, 0, 3] = early, late
+        got = Prompt([n], q_heads, kv_heads, dim, seed=13, edit=edit).result()
+        want = plain.copy()
+        G = q_heads // kv_heads
+        want[first:, :G, 3], want[second:, :G, 3] = a, both
+        assert np.array_equal(got, want, equal_nan=True), (first, second)
+
+
+@pytest.mark.parametrize("value", [0x7FC0, 0x7F80, 0xFF80])
+@pytest.mark.parametrize("what", ["q", "k"])
+def test_a_row_that_is_nan_stays_nan_beside_them(gpu, what, value):
+    """NaN in a row's query, or in a key that rows see, next to a V that is not finite in a token of the same tile pair."""
+    def edit(p):
+        p.v[200, 0, 3] = value
+        if what == "q":
+            p.q[210, 1, 5] = NAN
+        else:
+            p.k[190, 0, 5] = NAN
+    got = Prompt([300], 4, 2, 64, seed=14, edit=edit).result()
+    want = bf16_to_f64(np.array([value], np.uint16))[0]
+    nan = np.zeros(got.shape, bool)
+    if what == "q":
+        nan[210, 1] = True
+        hit = nan.copy()
+        hit[200:, :2, 3] = True
+        assert np.array_equal(got[hit & ~nan], np.full((hit & ~nan).sum(), want), equal_nan=True)
+        assert np.isfinite(got[~hit]).all()
+    else:
+        nan[190:, :2] = True
+        assert np.isfinite(got[~nan]).all()
+    assert np.isnan(got[nan]).all()
+
+
 def test_separate_tensors_with_strides_of_their_own(gpu):
     p = Prompt([150, 70], 6, 2, 64, seed=12)
     o, off = attend_prompt(bf16_to_f64(p.q), bf16_to_f64(p.k), bf16_to_f64(p.v), p.starts, True)
