@@ -655,7 +655,7 @@ typedef struct tv_seqs {
  * the sequence's length.  write: a sequence may be listed once, and its rows
  * must lie in pages that it alone holds (tv_pages_extend sees to it).
  * Device checks: TV_E_SEQ, TV_E_CAPACITY (a token past the length); TV_E_PAGE
- * (that row alone is left out).
+ * (a page entry out of range: its rows alone are left out).
  *
  * The workspace and the pool's tables belong to one call at a time: order
  * calls that share them on one stream.

@@ -529,6 +529,11 @@ __global__ void __launch_bounds__(kListThreads) compact_move_kernel(tv_pool pool
 // Row r of listed sequence i (starts[i] <= r < starts[i + 1]) is token
 // pos[i] + r - starts[i].  One warp per row; a row's K and V are each n_kv_heads
 // pieces of head_dim values, contiguous per head on both sides.
+//
+// A bad page entry leaves out its rows alone.  Blocks that have yet to start
+// would take the status it is reported by for an earlier call's and leave out
+// theirs as well, so a call of more than one block reports by a kernel of its
+// own behind the moves (rows_report_kernel).
 template <bool WRITE>
 __global__ void __launch_bounds__(kListThreads) rows_kernel(tv_pool pool, int layer, tv_seqs t, const int32_t* ids,
                                                             const int32_t* pos, const int32_t* starts, int n, int rows,
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(kListThreads) rows_kernel(tv_pool pool, int la
     const int at = __ldg(pos + lo) + (int)r - s_start[lo];
     const int p = __ldcg(t.pages + (size_t)__ldg(ids + lo) * t.max_pages + at / ps);
     if (p < 0 || p >= pool.n_pages) {
-      if (lane == 0) status_set(status, TV_E_PAGE);
+      if (gridDim.x == 1 && lane == 0) status_set(status, TV_E_PAGE);
       continue;
     }
     const size_t base = ((size_t)layer * pool.n_pages + p) * page_elems + (size_t)(at % ps) * pool.head_dim;
@@ -618,6 +623,30 @@ __global__ void __launch_bounds__(kListThreads) rows_kernel(tv_pool pool, int la
   }
 }
 
+// The entries of the rows of rows_kernel, looked at while it moves them: it
+// triggers behind its own wait, so what it reads is there when this kernel
+// starts.  Lists that it refuses reach no entry here that they name wrongly,
+// and have set the status.
+__global__ void __launch_bounds__(kListThreads) rows_report_kernel(int n_pages, int ps, tv_seqs t, const int32_t* ids,
+                                                                   const int32_t* pos, const int32_t* starts, int n,
+                                                                   int rows, int32_t* status) {
+  bool bad = false;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int a = __ldcg(starts + i), b = __ldcg(starts + i + 1), s = __ldcg(ids + i), at = __ldcg(pos + i);
+    if (a < 0 || b <= a || b > rows || s < 0 || s >= t.max_seqs || at < 0) continue;
+    const int len = seq_len(t, ps, s);
+    if ((long long)at + (b - a) > len) continue;
+    const int last = (at + (b - a) - 1) / ps;
+    for (int j = at / ps + (int)threadIdx.x; j <= last; j += kListThreads) {
+      const int p = __ldcg(t.pages + (size_t)s * t.max_pages + j);
+      bad = bad || p < 0 || p >= n_pages;
+    }
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (bad) status_set(status, TV_E_PAGE);   // (where the call was stopped, the word is set)
+}
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // extend: the free list and the pairs; compact: two page lists and two counts
@@ -642,8 +671,11 @@ int rows_call(bool write, const tv_pool* pool, int layer, const tv_seqs* seqs, c
   __nv_bfloat16 *kp = static_cast<__nv_bfloat16*>(k), *vp = static_cast<__nv_bfloat16*>(v);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t smem = write ? (size_t)((seqs->max_seqs + 31) / 32) * 4 : 0;
-  return launch_pdl(write ? rows_kernel<true> : rows_kernel<false>, grid, dim3(kListThreads), smem, st, *pool, layer, *seqs,
-                    ids, pos, starts, n, rows, kp, vp, row_stride, head_stride, status);
+  rc = launch_pdl(write ? rows_kernel<true> : rows_kernel<false>, grid, dim3(kListThreads), smem, st, *pool, layer, *seqs,
+                  ids, pos, starts, n, rows, kp, vp, row_stride, head_stride, status);
+  if (rc || grid.x == 1) return rc;
+  return launch_pdl(rows_report_kernel, dim3(n < sms ? n : sms), dim3(kListThreads), 0, st, pool->n_pages, pool->page_size,
+                    *seqs, ids, pos, starts, n, rows, status);
 }
 
 }  // namespace

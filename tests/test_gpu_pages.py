@@ -233,6 +233,44 @@ def test_rows_refusals(gpu):
     b.same()
 
 
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_many_rows_around_a_bad_page(gpu, which):
+    """Rows for several waves of blocks; a bad entry in the first page, a middle one or the last leaves out its own rows
+    and no other, every time, and the next call does nothing."""
+    ps, heads, dim, lens = 16, 1, 64, [9000, 12000, 20000]
+    b = Both(1, sum(-(-x // ps) for x in lens) + 3, heads, ps, dim, 4, 1300, 21)
+    b.extend([2, 0, 1], lens)
+    ids, rows = [2, 0, 1], sum(lens)
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    s, j = ((2, 0), (0, 400), (1, 1249))[which]
+    b.o.pages[s, j] = b.o.refs.shape[0] if which else -1
+    b.pages.copy_(i32(b.o.pages))
+    left = starts[ids.index(s)] + ps * j
+    E = abi.CODES
+    rng = np.random.default_rng(which)
+    for _ in range(10):
+        x = rng.integers(0, 1 << 16, (2, rows, heads, dim)).astype(np.uint16)
+        k, v = (torch.from_numpy(y.view(np.int16)).cuda() for y in x)
+        assert abi.tv_pages_write(b.pool, 0, b.seqs, i32(ids), i32([0] * 3), i32(starts), 3, rows, k, v, dim, dim, b.status) == 0
+        assert int(b.status.item()) == E["TV_E_PAGE"]
+        for i, q in enumerate(ids):
+            for m in range(-(-lens[i] // ps)):
+                p, a, e = b.o.pages[q, m], starts[i] + ps * m, min(starts[i] + ps * (m + 1), starts[i + 1])
+                if (q, m) != (s, j):
+                    b.o.k[0, p, :, :e - a], b.o.v[0, p, :, :e - a] = x[0, a:e].transpose(1, 0, 2), x[1, a:e].transpose(1, 0, 2)
+        b.same()
+        got = [torch.full((rows, heads, dim), 77, dtype=torch.int16, device="cuda") for _ in range(2)]
+        read = lambda: abi.tv_pages_read(b.pool, 0, b.seqs, i32(ids), i32([0] * 3), i32(starts), 3, rows, *got, dim, dim, b.status)
+        assert read() == 0 and all((g == 77).all() for g in got)          # stopped by the status
+        b.status.zero_()
+        assert read() == 0 and int(b.status.item()) == E["TV_E_PAGE"]
+        b.status.zero_()
+        for g, y in zip(got, x):
+            want = y.copy()
+            want[left:left + min(ps, starts[ids.index(s) + 1] - left)] = 77
+            assert np.array_equal(g.cpu().numpy().view(np.uint16), want)
+
+
 def test_captured_and_replayed_on_other_lists(gpu):
     """One graph of release, fork, extend and compact, replayed with other lists in the same tensors, on a side stream."""
     b = Both(2, 80, 2, 16, 64, 9, 12, 8)
