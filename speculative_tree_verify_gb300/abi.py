@@ -177,12 +177,9 @@ def load():
 
 def _p(x) -> Optional[int]:
     """Device/host address of a tensor, an int, or None."""
-    try:
-        return x.data_ptr()
-    except AttributeError:
-        if x is None or isinstance(x, int):
-            return x
-        raise
+    if x is None or isinstance(x, int):
+        return x
+    return x.data_ptr()
 
 
 def _arr(ctype, items: Sequence):

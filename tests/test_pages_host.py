@@ -110,6 +110,25 @@ def test_attend_prompt_host_checks():
         assert call(**over) == E["TV_E_UNSUPPORTED"], over
 
 
+def test_what_is_an_address():
+    """None and ints go as they are, without an exception on the way; tensors by their address."""
+    import sys
+
+    import torch
+    x, raised = torch.zeros(4), []
+
+    def trace(frame, event, arg):
+        if event == "exception":
+            raised.append(arg)
+        return trace
+    sys.settrace(trace)
+    try:
+        got = [abi._p(a) for a in (None, 0, FAKE, x, x[1:])]
+    finally:
+        sys.settrace(None)
+    assert got == [None, 0, FAKE, x.data_ptr(), x.data_ptr() + 4] and not raised
+
+
 @pytest.mark.parametrize("what", [b"x" * 64, "x", 1.5, np.zeros(4, np.int32), [1]])
 def test_what_is_no_address(what):
     with pytest.raises(AttributeError):
