@@ -405,9 +405,12 @@ __device__ __forceinline__ void copy_block(const uint8_t* from, uint8_t* to, uin
   }
 }
 __device__ __forceinline__ void copy_page(const tv_pool& pool, int layer, bool is_v, int src, int dst) {
+  constexpr size_t kPiece = size_t(1) << 31;   // a page of very many heads passes 2^32 bytes
   const size_t bytes = (size_t)pool.n_kv_heads * pool.page_size * pool.head_dim * 2;
   uint8_t* base = reinterpret_cast<uint8_t*>(is_v ? pool.v : pool.k) + (size_t)layer * pool.n_pages * bytes;
-  copy_block(base + (size_t)src * bytes, base + (size_t)dst * bytes, (uint32_t)bytes);
+  for (size_t at = 0; at < bytes; at += kPiece)
+    copy_block(base + (size_t)src * bytes + at, base + (size_t)dst * bytes + at,
+               (uint32_t)(bytes - at < kPiece ? bytes - at : kPiece));
 }
 
 // grid (listed sequences, 2 layers): the copies of extend_plan_kernel

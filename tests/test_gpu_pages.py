@@ -271,6 +271,28 @@ def test_many_rows_around_a_bad_page(gpu, which):
             assert np.array_equal(g.cpu().numpy().view(np.uint16), want)
 
 
+def test_a_page_of_2_to_the_32_bytes(gpu):
+    """131,073 heads of 128 tokens: what a copy-on-write and a compaction move has more bytes than 32 bits hold."""
+    heads, ps, dim = 2 ** 17 + 1, 128, 128
+    k, v = (torch.zeros(1, 3, heads, ps, dim, dtype=torch.int16, device="cuda") for _ in range(2))
+    for x in (k, v):
+        x[0, 0].view(-1, 1 << 14)[:, 0] = torch.arange(heads * ps * dim >> 14, device="cuda").to(torch.int16)
+        x[0, 0, -1] = 7
+    refs, table, lens, status = i32([1, 0, 0]), i32([[0], [-1]]), i32([5, 0]), i32([0])
+    pool, seqs = abi.TvPool(k.data_ptr(), v.data_ptr(), refs.data_ptr(), 1, 3, heads, ps, dim), abi.TvSeqs(table.data_ptr(), lens.data_ptr(), 2, 1)
+    wsb = abi.tv_pages_workspace_size(pool, seqs)
+    ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+    assert abi.tv_pages_fork(pool, seqs, i32([0]), i32([1]), 1, status) == 0
+    assert abi.tv_pages_extend(pool, seqs, i32([1]), i32([1]), 1, ws, wsb, status) == 0
+    assert int(status.item()) == 0 and table.tolist() == [[0], [1]]
+    assert torch.equal(k[0, 1], k[0, 0]) and torch.equal(v[0, 1], v[0, 0])
+    assert abi.tv_pages_release(pool, seqs, i32([0]), i32([0]), 1, status) == 0
+    k[0, 0], v[0, 0] = 0, 0
+    assert abi.tv_pages_compact(pool, seqs, i32([0] * 3), i32([0]), ws, wsb, status) == 0
+    assert int(status.item()) == 0 and table.tolist() == [[0], [0]]
+    assert torch.equal(k[0, 1], k[0, 0]) and torch.equal(v[0, 1], v[0, 0])
+
+
 def test_captured_and_replayed_on_other_lists(gpu):
     """One graph of release, fork, extend and compact, replayed with other lists in the same tensors, on a side stream."""
     b = Both(2, 80, 2, 16, 64, 9, 12, 8)
