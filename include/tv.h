@@ -698,8 +698,10 @@ TV_API int tv_pages_read(const tv_pool *pool, int layer, const tv_seqs *seqs, co
  * heads a KV head, at most 4096 sequences (else TV_E_UNSUPPORTED).  P is
  * rounded to bf16 for the product with V, everything else is fp32; scores
  * (q . k / sqrt(head_dim)) up to 2^27 in magnitude.  What a row
- * may not see does not reach it, whatever it holds.  The same inputs give the
- * same bits.  No workspace.
+ * may not see does not reach it, whatever it holds; an infinity in v that it
+ * sees is the result in its dimension (beside the other one, or a NaN: NaN;
+ * also NaN where its weight rounds to zero).  The same inputs give the same
+ * bits.  No workspace.
  * Host checks: TV_E_ARG, TV_E_UNSUPPORTED.  Device checks: TV_E_SEQ (starts;
  * nothing is written).
  */
@@ -729,8 +731,8 @@ TV_API int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const t
  * it).
  * fp32 throughout: P enters the product with V as two bf16 parts, and out is
  * rounded once.  Slots past a sequence's length are never used, whatever they
- * hold.  The same
- * inputs give the same bits.
+ * hold; an infinity in v is the result in its dimension, whatever it weighs
+ * (beside the other one, or a NaN: NaN).  The same inputs give the same bits.
  * Host checks: TV_E_ARG, TV_E_UNSUPPORTED (n_q_heads not a multiple of
  * n_kv_heads, n > 2048), TV_E_WORKSPACE.  Device checks: TV_E_SEQ (also a
  * sequence listed twice with k_new), nothing is written; TV_E_PAGE (a page

@@ -23,6 +23,12 @@
 // (128 x 8k tokens: 648 -> 652 us; one of 32k: 29.0 -> 30.1 us) and leaves the
 // output's own rounding as the only one.  Offsets move only when a score
 // passes them by 2^8.
+//
+// An infinity in a token's V is the result in its dimension, but the products
+// have it times the second part of P, which may be zero or below it, and sums
+// that are joined have it times a weight that may be zero: NaN.  So where an
+// element is NaN and its row's sum is not, the run's V is looked over again,
+// and the element is what the infinities and NaN there make of it.
 #include <cmath>
 #include <type_traits>
 
@@ -128,12 +134,75 @@ __device__ __forceinline__ void quad_sync(int quad) {
   asm volatile("bar.sync %0, %1;" ::"r"(2 + quad), "n"(kCompThreads / 2) : "memory");
 }
 
+// a barrier of n threads: true if v is true on any of them
+__device__ __forceinline__ bool bar_any(bool v, int id, int n) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, %2, %3, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(out)
+      : "r"((uint32_t)v), "r"(id), "r"(n)
+      : "memory");
+  return out != 0;
+}
+
 __device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % kTile != 0); }
+
+// Rows r0 .. r0 + nr - 1 of a run's output (out) or partial result (part_o), an
+// element of which is NaN: what is not finite among the run's V, by dimension,
+// and where that is infinities of one sign, the infinity.  By 32 nw threads
+// that meet on barrier bar; kinds: D words, ml: offsets and sums of the nw
+// warps.  Out of line, since a call that has no use for it pays for its place
+// in the join (us without it, out of line, inside: 256 short sequences x 16
+// heads 49.4, 50.4, 52.2; one of 1k 9.33, 9.50, 9.65).
+template <int D>
+__device__ __noinline__ void put_infinities(const PaParams& p, int i, int s, int len, uint32_t tok, uint32_t end, int h,
+                                            int nr, uint32_t* kinds, const float2* ml, int nw, int me, int bar,
+                                            __nv_bfloat16* out, float* part_o) {
+  const int ps = p.pool.page_size, c = 8 * (me % (D / 8));
+  auto meet = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * nw) : "memory"); };
+  for (int d = me; d < D; d += 32 * nw) kinds[d] = 0u;   // 1: NaN, 2: +inf, 4: -inf
+  meet();
+  for (tok += me / (D / 8); tok < end; tok += 32 * nw / (D / 8)) {   // (unsigned: lengths near 2^31)
+    const __nv_bfloat16* v = p.v_new + (size_t)i * p.kv_stride + (size_t)h * D;   // the new row may not be in its page yet
+    if (!p.v_new || tok != (uint32_t)len - 1) {
+      const int page = __ldcg(p.seqs.pages + (size_t)s * p.seqs.max_pages + tok / ps);
+      if (page < 0 || page >= p.pool.n_pages) continue;
+      v = reinterpret_cast<const __nv_bfloat16*>(p.pool.v) +
+          ((((size_t)p.layer * p.pool.n_pages + page) * p.pool.n_kv_heads + h) * ps + tok % ps) * D;
+    }
+    const uint4 x = __ldcg(reinterpret_cast<const uint4*>(v + c));
+    const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t b = q[u >> 1] >> (16 * (u & 1)) & 0xffffu;
+      if ((b & 0x7f80u) == 0x7f80u) atomicOr(kinds + c + u, b & 0x7fu ? 1u : (b & 0x8000u ? 4u : 2u));
+    }
+  }
+  meet();
+  for (int e = me; e < nr * D; e += 32 * nw) {
+    const int row = e / D;
+    float M = -INFINITY, L = 0.f;
+    for (int w = 0; w < nw; ++w) M = fmaxf(M, ml[w * kRows + row].x);
+    for (int w = 0; w < nw; ++w) {
+      const float2 x = ml[w * kRows + row];
+      L += x.x == -INFINITY ? x.y : x.y * ex2f(x.x - M);
+    }
+    const uint32_t kind = kinds[e % D];
+    if (!(L > 0.f && L < INFINITY) || (kind != 2u && kind != 4u)) continue;   // the row's own NaN, and both infinities, stay NaN
+    const float x = kind == 2u ? INFINITY : -INFINITY;
+    if (out) out[e] = __float2bfloat16_rn(x);
+    else part_o[e] = x;
+  }
+  meet();
+}
 
 template <int D>
 __global__ void __launch_bounds__(kPaThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                      const PaParams p) {
+                      const __grid_constant__ PaParams p) {
   using L = PaSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -543,6 +612,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       // does not wait for ldmatrix results that nothing has used yet.  (A warp
       // without a token in this run has not used them, and never will.)
       if (lane == 0) mbar_arrive(&q_free[qs]);
+      bool lost = false;   // an element is NaN
 #pragma unroll 1   // one copy of the code: most groups need one or two parts, and short sequences run it once a tile
       for (int part = 0; part * kRedRows < nr; ++part) {   // rows 4 part .. + 3, of the lanes with g8 / 4 = part mod 2
         const bool upper = part >> 1;
@@ -583,6 +653,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               acc.x += v.x;
               acc.y += v.y;
             }
+            lost = lost || acc.x != acc.x || acc.y != acc.y;
             if (whole)
               *reinterpret_cast<__nv_bfloat162*>(p.out + ((size_t)g.i * p.Hq + h * p.G + r0 + row) * D + d) =
                   __floats2bfloat162_rn(acc.x, acc.y);
@@ -590,8 +661,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               *reinterpret_cast<float2*>(p.ws.o + (slot * kRows + row) * D + d) = acc;
           }
         }
-        meet();
+        if ((part + 1) * kRedRows < nr) meet();
       }
+      const int bar = NW == kCompWarps ? 1 : 2 + quad;
+      if (bar_any(lost, bar, 32 * NW))
+        put_infinities<D>(p, g.i, g.s, g.len, (uint32_t)g.t0 * kTile, g.t1 == g.T ? g.len : (uint32_t)g.t1 * kTile, h, nr,
+                          reinterpret_cast<uint32_t*>(s_red + w0 * kRedRows * D), s_ml + w0 * kRows, NW, me, bar,
+                          whole ? p.out + ((size_t)g.i * p.Hq + h * p.G + r0) * D : nullptr, p.ws.o + slot * kRows * D);
     };
     if (g.T > 1) join(std::integral_constant<int, kCompWarps>{});
     else join(std::integral_constant<int, kCompWarps / 2>{});
@@ -664,6 +740,16 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PaPara
     }
 #pragma unroll 8
     for (; c < np; ++c) add(partial(e, c), s_w[row][c]);
+    if (acc.x != acc.x || acc.y != acc.y) {   // again, with an infinity that weighs nothing as it is
+      acc = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (c = 0; c < np; ++c) {
+        const float2 x = partial(e, c);
+        const float w = s_w[row][c];
+        acc.x += w == 0.f && isinf(x.x) ? x.x : x.x * w;
+        acc.y += w == 0.f && isinf(x.y) ? x.y : x.y * w;
+      }
+    }
     *reinterpret_cast<__nv_bfloat162*>(p.out + ((size_t)cut.x * p.Hq + (cut.y / p.HB) * p.G + r0 + row) * D + d) =
         __floats2bfloat162_rn(acc.x, acc.y);
   }

@@ -314,3 +314,45 @@ def test_many_sequences_of_one_tile(gpu, q_heads, kv_heads, dim, n):
     torch.cuda.synchronize()
     assert int(c.status.item()) == 0, abi.STATUS.get(int(c.status.item()))
     assert np.array_equal(host(c.out), first)
+
+
+def _set_value(c, i, t, g, d, value):
+    """V of token t of listed sequence i; the last one comes with the new rows where there are any."""
+    Hq, Hkv, D = c.dims
+    word = int(np.array(value, np.uint16).view(np.int16))
+    if c.new and t == c.lens[i] - 1:
+        c.gq[i, (Hq + Hkv + g) * D + d] = word
+    else:
+        c.gv[c.layer, c.pages[c.ids[i], t // c.pool.page_size], g, t % c.pool.page_size, d] = word
+
+
+@pytest.mark.parametrize("new", [True, False])
+@pytest.mark.parametrize("scale", [1.0, 30.0])
+@pytest.mark.parametrize("q_heads,kv_heads,dim,ps,lens", [(4, 2, 64, 16, [1, 40, 64, 65, 700]), (10, 2, 128, 32, [9001, 3]), (24, 1, 128, 64, [30, 5000]),
+                                                          (16, 8, 128, 16, [50] * 300 + [1000]), (33, 1, 64, 16, [60] * 200)])
+def test_infinities_that_are_seen(gpu, q_heads, kv_heads, dim, ps, lens, scale, new):
+    """An infinity in a token's V is the result in its dimension, whatever the token weighs; with the other infinity or
+    a NaN beside it, NaN.  Every other element keeps its bits, and a query that is NaN stays so."""
+    case = lambda: Case(lens, q_heads, kv_heads, dim, ps, layers=2, layer=1, seed=17, new=new, scale=scale)
+    c, G = case(), q_heads // kv_heads
+    assert c.run() == 0
+    want = bf16_to_f64(host(c.out))[:len(lens)]
+    assert np.isfinite(want).all()
+    c = case()
+    inf, ninf, nan = 0x7F80, 0xFF80, NAN
+    for i in range(0, len(lens), max(1, len(lens) // 7)):
+        n, g = lens[i], i % kv_heads
+        heads = slice(g * G, (g + 1) * G)
+        for d, marks, value in ((3, [(n - 1, inf)], np.inf), (9, [(0, ninf)], -np.inf), (16, [(n // 2, inf), (n - 1, inf)], np.inf),
+                                (31, [(n // 3, nan)], np.nan), (dim - 1, [(0, inf), (n - 1, ninf)], np.nan), (40, [(0, nan), (n - 1, inf)], np.nan)):
+            if n == 1 and len({m for _, m in marks}) > 1:
+                continue
+            for t, m in marks:
+                _set_value(c, i, t, g, d, m)
+            want[i, heads, d] = value
+    c.gq[0, (q_heads - 1) * dim] = int(np.array(NAN, np.uint16).view(np.int16))
+    want[0, q_heads - 1] = np.nan
+    assert c.run() == 0
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    assert np.array_equal(bf16_to_f64(host(c.out))[:len(lens)], want, equal_nan=True)
