@@ -592,8 +592,9 @@ TV_API int tv_commit_stack(const tv_stack *model, const tv_kv *kv, float *const 
  *   tv_pool   k, v    device bf16 [n_layers][n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned
  *             refs    device int32 [n_pages], 16-byte aligned: how many sequences hold the page, 0 = free
  *             page_size 16, 32, 64 or 128; head_dim 64 or 128; at most 2^31 - 1 rows of head_dim in all
- *   tv_seqs   pages   device int32 [max_seqs][max_pages]: a sequence's pages in order; entries past
- *                     ceil(len / page_size) are neither read nor written
+ *   tv_seqs   pages   device int32 [max_seqs][max_pages], all of it readable: a sequence's pages in
+ *                     order; entries past ceil(len / page_size) are never used or written (they may
+ *                     be read)
  *             lens    device int32 [max_seqs]: its tokens, 0 = the row is unused
  *             max_seqs at most 65536, max_pages * page_size at most 2^31 - 1
  *
@@ -651,8 +652,8 @@ typedef struct tv_seqs {
  * k and v 16-byte aligned): the K heads of a QKV projection's rows, or with
  * row_stride = head_dim and head_stride = capacity * head_dim the cache of a
  * tv_kv (offset the pointers to its slot), so that a paged sequence can be
- * verified and what the verify committed written back.  Tokens must lie below
- * the sequence's length.  write: a sequence may be listed once, and its rows
+ * verified and what the verify committed written back.  read: no two of these
+ * places may be the same.  Tokens must lie below the sequence's length.  write: a sequence may be listed once, and its rows
  * must lie in pages that it alone holds (tv_pages_extend sees to it).
  * Device checks: TV_E_SEQ, TV_E_CAPACITY (a token past the length); TV_E_PAGE
  * (a page entry out of range: its rows alone are left out).
@@ -697,7 +698,8 @@ TV_API int tv_pages_read(const tv_pool *pool, int layer, const tv_seqs *seqs, co
  * head_dim 64 or 128, n_q_heads a multiple of n_kv_heads with at most 128 query
  * heads a KV head, at most 4096 sequences (else TV_E_UNSUPPORTED).  P is
  * rounded to bf16 for the product with V, everything else is fp32; scores
- * (q . k / sqrt(head_dim)) up to 2^27 in magnitude.  What a row
+ * (q . k / sqrt(head_dim)) up to 2^27 and finite v up to 2^76 in magnitude
+ * (sums of weights, relative to a row's offset, stay below 2^51).  What a row
  * may not see does not reach it, whatever it holds; an infinity in v that it
  * sees is the result in its dimension (beside the other one, or a NaN: NaN;
  * also NaN where its weight rounds to zero).  The same inputs give the same
@@ -730,13 +732,15 @@ TV_API int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const t
  * With k_new a sequence's last page must be its own (tv_pages_extend sees to
  * it).
  * fp32 throughout: P enters the product with V as two bf16 parts, and out is
- * rounded once.  Slots past a sequence's length are never used, whatever they
- * hold; an infinity in v is the result in its dimension, whatever it weighs
- * (beside the other one, or a NaN: NaN).  The same inputs give the same bits.
+ * rounded once; finite v up to 2^76 in magnitude (weights, relative to a row's
+ * offset, stay below 2^17).  Slots past a sequence's length are never used,
+ * whatever they hold; an infinity in v is the result in its dimension, whatever
+ * it weighs (beside the other one, or a NaN: NaN).  The same inputs give the
+ * same bits.
  * Host checks: TV_E_ARG, TV_E_UNSUPPORTED (n_q_heads not a multiple of
  * n_kv_heads, n > 2048), TV_E_WORKSPACE.  Device checks: TV_E_SEQ (also a
  * sequence listed twice with k_new), nothing is written; TV_E_PAGE (a page
- * entry out of range: out is unspecified).
+ * entry out of range: out, and which new rows are stored, is unspecified).
  */
 TV_API int tv_attend_paged_workspace_size(const tv_pool *pool, int n_q_heads, int n, size_t *bytes);
 TV_API int tv_attend_paged(const tv_pool *pool, int layer, const tv_seqs *seqs, const int32_t *ids, int n,
