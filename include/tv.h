@@ -725,8 +725,8 @@ TV_API int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const t
  *   k_new, v_new  device bf16, KV head g of listed sequence i at i * kv_stride + g * head_dim
  *             (strides in elements, multiples of 8, at least a row; pointers 16-byte
  *             aligned: the Q, K and V heads of a QKV projection's rows)
- *   out       device bf16 [n][n_q_heads][head_dim]; a sequence of length 0 gets zeros
- *             (and stores nothing)
+ *   out       device bf16 [n][n_q_heads][head_dim], 16-byte aligned; may not overlap the
+ *             inputs; a sequence of length 0 gets zeros (and stores nothing)
  *   workspace device, >= tv_attend_paged_workspace_size(pool, n_q_heads, n); used by one
  *             call at a time (calls on one stream may share it, captured or not)
  * With k_new a sequence's last page must be its own (tv_pages_extend sees to

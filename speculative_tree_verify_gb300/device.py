@@ -263,49 +263,97 @@ class PagedCache:
         ws, attend_ws = (torch.empty(b, device=device, dtype=torch.uint8) for b in bytes_)
         return cls(dims, k, v, refs, pages, lens, torch.zeros(1, **i32), ws, attend_ws, pool, seqs)
 
+    # What a kernel would take for something else, or read and write out of
+    # range by, is refused here: ValueError, nothing launched.
+    def _tensor(self, name: str, x: torch.Tensor):
+        if x.device != self.refs.device or x.dtype not in (torch.bfloat16, torch.int16, torch.uint16):   # bf16 or its bits
+            raise ValueError(f"{name}: bf16 on {self.refs.device} expected, got {x.dtype} on {x.device}")
+
+    def _list(self, n: int, **lists) -> int:
+        for name, x in lists.items():
+            if x.dtype != torch.int32 or x.device != self.refs.device or not x.is_contiguous() or x.numel() != n:
+                raise ValueError(f"{name}: {n} int32 on {self.refs.device} expected, got {tuple(x.shape)} {x.dtype} on {x.device}")
+        return n
+
     def _heads(self, qkv: torch.Tensor):
         q = self.dims.n_q_heads * self.dims.head_dim
-        return qkv, qkv[:, q:], qkv[:, q + self.dims.n_kv_heads * self.dims.head_dim:]
+        kv = self.dims.n_kv_heads * self.dims.head_dim
+        self._tensor("qkv", qkv)
+        if qkv.dim() != 2 or qkv.shape[1] < q + 2 * kv or qkv.stride(1) != 1:
+            raise ValueError(f"qkv: rows of {q + 2 * kv} values expected, got {tuple(qkv.shape)} with strides {qkv.stride()}")
+        return qkv, qkv[:, q:], qkv[:, q + kv:]
+
+    def _out(self, out: torch.Tensor, rows: int):
+        self._tensor("out", out)
+        if not out.is_contiguous() or out.numel() < rows * self.dims.n_q_heads * self.dims.head_dim:
+            raise ValueError(f"out: {rows} contiguous rows of {self.dims.n_q_heads} heads expected, got {tuple(out.shape)}")
+
+    def _caches(self, k: torch.Tensor, v: torch.Tensor, rows: int):
+        self._tensor("k", k)
+        self._tensor("v", v)
+        d = self.dims
+        if (k.shape != v.shape or k.stride() != v.stride() or k.dim() != 3 or k.shape[0] != d.n_kv_heads
+                or k.shape[2] != d.head_dim or k.stride(2) != 1 or not 0 <= rows <= k.shape[1]):
+            raise ValueError(f"caches [{d.n_kv_heads}][at least {rows}][{d.head_dim}] of one layout expected, got "
+                             f"{tuple(k.shape)} {k.stride()} and {tuple(v.shape)} {v.stride()}")
 
     def extend(self, ids, add, stream=None) -> int:
-        return abi.tv_pages_extend(self.pool, self.seqs, ids, add, ids.numel(), self.ws, self.ws.numel(), self.status,
-                                   stream)
+        n = self._list(ids.numel(), ids=ids, add=add)
+        return abi.tv_pages_extend(self.pool, self.seqs, ids, add, n, self.ws, self.ws.numel(), self.status, stream)
 
     def fork(self, src, dst, stream=None) -> int:
-        return abi.tv_pages_fork(self.pool, self.seqs, src, dst, src.numel(), self.status, stream)
+        n = self._list(src.numel(), src=src, dst=dst)
+        return abi.tv_pages_fork(self.pool, self.seqs, src, dst, n, self.status, stream)
 
     def release(self, ids, keep, stream=None) -> int:
-        return abi.tv_pages_release(self.pool, self.seqs, ids, keep, ids.numel(), self.status, stream)
+        n = self._list(ids.numel(), ids=ids, keep=keep)
+        return abi.tv_pages_release(self.pool, self.seqs, ids, keep, n, self.status, stream)
 
     def compact(self, remap, n_used, stream=None) -> int:
+        self._list(self.refs.numel(), remap=remap)
+        self._list(1, n_used=n_used)
         return abi.tv_pages_compact(self.pool, self.seqs, remap, n_used, self.ws, self.ws.numel(), self.status, stream)
 
     def write(self, layer: int, ids, pos, starts, qkv: torch.Tensor, stream=None) -> int:
         """Rows of a projection into the pages of the sequences they belong to."""
+        n = self._list(ids.numel(), ids=ids, pos=pos)
+        self._list(n + 1, starts=starts)
         _, k, v = self._heads(qkv)
-        return abi.tv_pages_write(self.pool, layer, self.seqs, ids, pos, starts, ids.numel(), qkv.shape[0], k, v,
+        return abi.tv_pages_write(self.pool, layer, self.seqs, ids, pos, starts, n, qkv.shape[0], k, v,
                                   qkv.stride(0), self.dims.head_dim, self.status, stream)
 
     def read_into(self, layer: int, ids, pos, starts, rows: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> int:
         """Tokens of one or more sequences into contiguous caches [n_kv_heads][capacity][head_dim]."""
-        return abi.tv_pages_read(self.pool, layer, self.seqs, ids, pos, starts, ids.numel(), rows, k, v, k.stride(1),
+        n = self._list(ids.numel(), ids=ids, pos=pos)
+        self._list(n + 1, starts=starts)
+        self._caches(k, v, rows)
+        return abi.tv_pages_read(self.pool, layer, self.seqs, ids, pos, starts, n, rows, k, v, k.stride(1),
                                  k.stride(0), self.status, stream)
 
     def write_from(self, layer: int, ids, pos, starts, rows: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> int:
         """The other way: rows of contiguous caches (a committed path) into pages."""
-        return abi.tv_pages_write(self.pool, layer, self.seqs, ids, pos, starts, ids.numel(), rows, k, v, k.stride(1),
+        n = self._list(ids.numel(), ids=ids, pos=pos)
+        self._list(n + 1, starts=starts)
+        self._caches(k, v, rows)
+        return abi.tv_pages_write(self.pool, layer, self.seqs, ids, pos, starts, n, rows, k, v, k.stride(1),
                                   k.stride(0), self.status, stream)
 
     def attend_prompt(self, qkv: torch.Tensor, starts, out: torch.Tensor, stream=None) -> int:
+        self._list(starts.numel(), starts=starts)
         q, k, v = self._heads(qkv)
+        self._out(out, qkv.shape[0])
         return abi.tv_attend_prompt(self.dims.n_q_heads, self.dims.n_kv_heads, self.dims.head_dim, q, k, v,
                                     qkv.stride(0), qkv.stride(0), starts, starts.numel() - 1, qkv.shape[0], out,
                                     self.status, stream)
 
     def attend(self, layer: int, ids, qkv: torch.Tensor, out: torch.Tensor, stream=None) -> int:
         """One new token a sequence: its K and V into the page, its queries over the whole sequence."""
+        n = self._list(ids.numel(), ids=ids)
         q, k, v = self._heads(qkv)
-        return abi.tv_attend_paged(self.pool, layer, self.seqs, ids, ids.numel(), self.dims.n_q_heads, q, qkv.stride(0),
+        if qkv.shape[0] < n:
+            raise ValueError(f"qkv: {n} rows expected, got {qkv.shape[0]}")
+        self._out(out, n)
+        return abi.tv_attend_paged(self.pool, layer, self.seqs, ids, n, self.dims.n_q_heads, q, qkv.stride(0),
                                    k, v, qkv.stride(0), out, self.attend_ws, self.attend_ws.numel(), self.status, stream)
 
 

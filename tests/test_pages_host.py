@@ -135,6 +135,81 @@ def test_what_is_no_address(what):
         CALLS["fork"](_pool(), _seqs(), ids=what)
 
 
+def _paged_cache():
+    import torch
+
+    from speculative_tree_verify_gb300 import device, synth
+    c = device.PagedCache.alloc(synth.TINY, 2, 24, 16, 5, 6, device="cpu")
+    d = c.dims
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)
+    width = (d.n_q_heads + 2 * d.n_kv_heads) * d.head_dim
+    bf16 = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16)
+    return c, i32, bf16, width, (d.n_q_heads, d.n_kv_heads, d.head_dim)
+
+
+def _reached(monkeypatch):
+    """The C calls replaced by a note that they were reached: what is accepted is not launched here."""
+    calls = []
+    for name in abi.SYMBOLS:
+        if name.startswith(("tv_pages", "tv_attend")) and not name.endswith("size"):
+            monkeypatch.setattr(abi, name, lambda *a, _n=name, **k: calls.append(_n) or 0)
+    return calls
+
+
+def test_paged_cache_takes_what_fits(monkeypatch):
+    c, i32, bf16, width, (Hq, Hkv, D) = _paged_cache()
+    calls, ids = _reached(monkeypatch), i32(0, 1)
+    qkv, k = bf16(9, width + 8)[:, :width], bf16(Hkv, 32, D)
+    c.extend(ids, i32(3, 4))
+    c.fork(ids, i32(2, 3))
+    c.release(ids, i32(0, 0))
+    c.compact(i32(*[0] * 24), i32(0))
+    c.write(0, ids, i32(0, 0), i32(0, 4, 9), qkv)
+    c.read_into(0, ids, i32(0, 0), i32(0, 4, 9), 9, k, k.clone())
+    c.write_from(0, ids, i32(0, 0), i32(0, 4, 9), 9, k[:, 5:], k.clone()[:, 5:])
+    c.attend_prompt(qkv, i32(0, 4, 9), bf16(9, Hq, D))
+    c.attend(0, ids, qkv, bf16(2, Hq, D))
+    assert len(calls) == 9
+
+
+def test_paged_cache_refuses(monkeypatch):
+    """Lists of other lengths, types or strides, tensors of another device or layout, too few rows: nothing is called."""
+    import torch
+    c, i32, bf16, width, (Hq, Hkv, D) = _paged_cache()
+    calls, ids, one = _reached(monkeypatch), i32(0, 1), i32(0)
+    qkv, out, k = bf16(9, width), bf16(9, Hq, D), bf16(Hkv, 32, D)
+    long, strided, far = torch.tensor([0, 1]), i32(0, 7, 1, 7)[::2], ids.to("meta")
+    starts = i32(0, 4, 9)
+    for bad in (one, long, strided, far, ids.float()):
+        for call in (c.extend, c.fork, c.release):
+            with pytest.raises(ValueError):
+                call(ids, bad)
+        for call in (lambda: c.write(0, ids, bad, starts, qkv), lambda: c.read_into(0, ids, bad, starts, 9, k, k),
+                     lambda: c.write_from(0, ids, bad, starts, 9, k, k), lambda: c.write(0, ids, ids, bad, qkv),
+                     lambda: c.read_into(0, ids, ids, bad, 9, k, k), lambda: c.write_from(0, ids, ids, bad, 9, k, k),
+                     lambda: c.compact(bad, one)):
+            with pytest.raises(ValueError):
+                call()
+    for bad in (long, strided, far):
+        for call in (lambda: c.extend(bad, ids), lambda: c.attend(0, bad, qkv, out), lambda: c.attend_prompt(qkv, bad, out)):
+            with pytest.raises(ValueError):
+                call()
+    for bad in (bf16(9, width - 1), bf16(9, width).float(), bf16(9, width).to("meta"), bf16(width, 9).T, bf16(9 * width)):
+        for call in (lambda: c.write(0, ids, ids, starts, bad), lambda: c.attend(0, ids, bad, out), lambda: c.attend_prompt(bad, starts, out)):
+            with pytest.raises(ValueError):
+                call()
+    for call in (lambda: c.attend(0, ids, qkv[:1], out), lambda: c.attend(0, ids, qkv, out[:1]), lambda: c.attend_prompt(qkv, starts, out[:8]),
+                 lambda: c.attend_prompt(qkv, starts, bf16(Hq, 9, D).transpose(0, 1)), lambda: c.compact(i32(*[0] * 24), ids)):
+        with pytest.raises(ValueError):
+            call()
+    for a, b, rows in ((k, bf16(Hkv, 33, D), 9), (k, bf16(Hkv, 33, D)[:, :32], 9), (k, k, 33), (k, k, -1), (bf16(32, Hkv, D), bf16(32, Hkv, D), 2),
+                       (k.float(), k, 9), (k, k.to("meta"), 9), (k[..., :1], k[..., :1], 9), (bf16(Hkv, D, 32).transpose(1, 2),) * 2 + (9,)):
+        for call in (c.read_into, c.write_from):
+            with pytest.raises(ValueError):
+                call(0, ids, ids, starts, rows, a, b)
+    assert not calls
+
+
 def test_workspace_refuses_bad_shapes():
     with pytest.raises(ValueError, match="UNSUPPORTED"):
         abi.tv_pages_workspace_size(_pool(page_size=17), _seqs())
