@@ -34,10 +34,11 @@
 // tokens 2866 as first built; 1984 with the issuing warp in step (its
 // descriptors stay in uniform registers); 1838 with two threads a row; 1749
 // with sums instead of maxima; 1690 taking over places; 1654 with headroom in
-// the offsets; 1610 to 1660 now, 1660 to 1710 TFLOP/s: 87 to 90 % of what
-// cuBLAS reaches in a burst, 97 to 100 % of its sustained rate.  4k: 109 (1.58
-// PFLOP/s); 24 prompts of 1 to 1531: 60; one of 1024: 16.7.  With heads of 64
-// the softmax is what bounds it: 16k 1280 (1070 TFLOP/s).
+// the offsets; 1597 to 1684 now (box to box), 1630 to 1720 TFLOP/s: 86 to 91 %
+// of what cuBLAS reaches in a burst, 95 to 100 % of its sustained rate.  4k:
+// 109 (1.58 PFLOP/s); 24 prompts of 1 to 1531: 59 to 60; one of 1024: 16.5.
+// With heads of 64: 16k 1280 (1070 TFLOP/s; the softmax, which does not halve
+// with the products).
 //
 // Masked places: a key that a row may not see has weight zero, and its V may
 // be anything.  0 * NaN would reach the row through the product, so the V rows
