@@ -749,6 +749,145 @@ TV_API int tv_attend_paged(const tv_pool *pool, int layer, const tv_seqs *seqs, 
                            size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
+ * Attention through a sliding window: row t of a sequence sees its last
+ * `window` rows, t itself among them, and the sequence's first `sinks` rows,
+ *     j <= t  and  (j > t - window  or  j < sinks).
+ * window >= 1, sinks >= 0 (TV_E_ARG otherwise); a window of 2^31 - 1 hides
+ * nothing.  What a row may not see does not reach it, whatever it holds.  Keys
+ * outside every row's window are not read (but for the rest of a tile of 128
+ * or 64).
+ *
+ * tv_attend_prompt_window: otherwise as tv_attend_prompt.
+ * tv_attend_paged_window: otherwise as tv_attend_paged, of the new token: it
+ * is row len - 1 of its sequence.  Pages that only hold rows between the sinks
+ * and the window are not looked at; their table entries may name anything.
+ */
+TV_API int tv_attend_prompt_window(int n_q_heads, int n_kv_heads, int head_dim, int window, int sinks,
+                                   const tv_bf16 *q, const tv_bf16 *k, const tv_bf16 *v, size_t q_stride,
+                                   size_t kv_stride, const int32_t *starts, int n_seqs, int rows, tv_bf16 *out,
+                                   int32_t *dev_status, void *stream);
+TV_API int tv_attend_paged_window(const tv_pool *pool, int layer, const tv_seqs *seqs, const int32_t *ids, int n,
+                                  int n_q_heads, int window, int sinks, const tv_bf16 *q, size_t q_stride,
+                                  const tv_bf16 *k_new, const tv_bf16 *v_new, size_t kv_stride, tv_bf16 *out,
+                                  void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * The paged cache in 4 bits: 9/32 of tv_pool's bytes.  32 values x of one
+ * token's head (dimensions 32 g .. 32 g + 31) share a scale
+ *     s = bf16(max |x| / 7), 0 where that is below 2^-126,
+ * and each is the code 8 + n, n = x / s rounded to the nearest integer, halves
+ * away from zero (8 where s = 0), which stands for n s.  A group that holds
+ * something not finite has s = NaN and stands for NaN throughout.
+ *
+ *   tv_pool4  k, v    device, 16-byte aligned: [n_layers][n_pages][n_kv_heads][page_size / 16] blocks of
+ *                     9 head_dim bytes, each the rows of 16 tokens t = 0 .. 15 (G = head_dim / 32):
+ *             k       dimensions 32 g + 8 c .. + 7 of token t: 4 bytes at t head_dim / 2 + (c G + g) 4,
+ *                     the lowest dimension in the lowest 4 bits
+ *             v       dimensions 32 g + 4 c .. + 3 of token t: 2 bytes at
+ *                     ((t / 8 * 32 + c * 4 + t % 8 / 2) G + g) 4 + t % 2 * 2, lowest first
+ *             both    the scale of token t's group g: bf16 at
+ *                     8 head_dim + ((t / 8 * 4 + t % 8 / 2) G + g) 4 + t % 2 * 2
+ *             (the order in which a lane of the attention holds them as tensor-core operands)
+ *             refs and the sizes as tv_pool
+ *
+ * The calls are those of tv_pool with the same arguments, checks and errors,
+ * over the same tv_seqs; a sequence table belongs to one pool.  tv_pages4_write
+ * takes bf16 rows and rounds them as above; tv_pages4_read gives bf16(n s).
+ * What a forked or moved page stands for does not change.
+ */
+typedef struct tv_pool4 {
+  uint8_t *k, *v;
+  int32_t *refs;
+  int32_t n_layers, n_pages, n_kv_heads, page_size, head_dim;
+} tv_pool4;
+
+TV_API int tv_pages4_workspace_size(const tv_pool4 *pool, const tv_seqs *seqs, size_t *bytes);
+TV_API int tv_pages4_extend(const tv_pool4 *pool, const tv_seqs *seqs, const int32_t *ids, const int32_t *add, int n,
+                            void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+TV_API int tv_pages4_fork(const tv_pool4 *pool, const tv_seqs *seqs, const int32_t *src, const int32_t *dst, int n,
+                          int32_t *dev_status, void *stream);
+TV_API int tv_pages4_release(const tv_pool4 *pool, const tv_seqs *seqs, const int32_t *ids, const int32_t *keep, int n,
+                             int32_t *dev_status, void *stream);
+TV_API int tv_pages4_compact(const tv_pool4 *pool, const tv_seqs *seqs, int32_t *remap, int32_t *n_used,
+                             void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+TV_API int tv_pages4_write(const tv_pool4 *pool, int layer, const tv_seqs *seqs, const int32_t *ids,
+                           const int32_t *pos, const int32_t *starts, int n, int rows, const tv_bf16 *k,
+                           const tv_bf16 *v, size_t row_stride, size_t head_stride, int32_t *dev_status,
+                           void *stream);
+TV_API int tv_pages4_read(const tv_pool4 *pool, int layer, const tv_seqs *seqs, const int32_t *ids,
+                          const int32_t *pos, const int32_t *starts, int n, int rows, tv_bf16 *k, tv_bf16 *v,
+                          size_t row_stride, size_t head_stride, int32_t *dev_status, void *stream);
+
+/*
+ * Attention of one new token per sequence over the pages in 4 bits: as
+ * tv_attend_paged_window, of the values that the cache stands for.  k_new and
+ * v_new are bf16 rows; they are stored in 4 bits, and the new token sees what
+ * was stored.
+ * Scores are fp32 (q . k of one group of 32 dimensions exactly as the tensor
+ * core adds it, then scaled; q enters with 11 bits relative to its own
+ * exponent down to 2^-28 of the row's largest value); weights relative to a row's
+ * offset enter the product with V, scaled by its group's scale, as fp16
+ * (11 bits, and 2^-39 of the largest scaled weight or so); sums are fp32; out is rounded
+ * once.  |q| up to 2^100.
+ */
+TV_API int tv_attend_paged4_workspace_size(const tv_pool4 *pool, int n_q_heads, int n, size_t *bytes);
+TV_API int tv_attend_paged4(const tv_pool4 *pool, int layer, const tv_seqs *seqs, const int32_t *ids, int n,
+                            int n_q_heads, int window, int sinks, const tv_bf16 *q, size_t q_stride,
+                            const tv_bf16 *k_new, const tv_bf16 *v_new, size_t kv_stride, tv_bf16 *out,
+                            void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * Rotary positions.  Of every head's first rot_dim values, pair i (i <
+ * rot_dim / 2) is turned by the angle a = position * freq[i]:
+ *     (u, w) -> gain (u cos a - w sin a, u sin a + w cos a),
+ * the pair being values (i, i + rot_dim / 2), or (2 i, 2 i + 1) where
+ * interleaved; the head's other values stay as they are.
+ *
+ * tv_rope_init (host only) fills the table: freq[i] = theta^(-2 i / rot_dim),
+ * stretched for contexts beyond original_ctx by `factor`:
+ *   TV_ROPE_PLAIN   as it is (factor, original_ctx and the turns are not used)
+ *   TV_ROPE_LINEAR  every freq divided by factor (the positions interpolated)
+ *   TV_ROPE_BASE    theta times factor^(rot_dim / (rot_dim - 2)): the slowest
+ *                   pair as under LINEAR, the fastest as it was
+ *   TV_ROPE_BLEND   by how often a pair turns in original_ctx positions:
+ *                   low_turns or fewer as LINEAR, high_turns or more as PLAIN,
+ *                   linear in between
+ * rot_dim: a multiple of 16 up to 128; theta and factor finite and positive;
+ * 0 <= low_turns < high_turns and original_ctx >= 1 (BLEND); gain finite (1,
+ * or what a stretched model multiplies its rotated values by).  A caller may
+ * set freq itself, to any finite values.  TV_E_ARG otherwise.
+ *
+ * tv_rope_rows: head h of row t of x, at t * x_stride + h * head_dim, to the
+ * same place of out (strides in elements): the Q heads and the K heads of a
+ * QKV projection's rows are n_q_heads + n_kv_heads heads of one call.
+ *   rope       host, read during the call
+ *   x, out     device bf16, 16-byte aligned, strides multiples of 8, at least a
+ *              row's heads; out may be x (with the same stride) and may not
+ *              overlap it otherwise
+ *   positions  device int32 [rows], any value
+ * Angles are exact to 2^-31 of a turn at every position (fixed point), one
+ * fp32 sine and cosine each; the result is rounded once.
+ * Host checks: TV_E_ARG, TV_E_UNSUPPORTED (head_dim not 64 or 128, rot_dim
+ * above it, n_heads > 65536).
+ */
+#define TV_ROPE_PLAIN 0
+#define TV_ROPE_LINEAR 1
+#define TV_ROPE_BASE 2
+#define TV_ROPE_BLEND 3
+#define TV_ROPE_MAX_PAIRS 64
+typedef struct tv_rope {
+  int32_t rot_dim, interleaved;
+  double gain;
+  double freq[TV_ROPE_MAX_PAIRS];   /* radians a position */
+} tv_rope;
+
+TV_API int tv_rope_init(tv_rope *rope, int rot_dim, int interleaved, double theta, int scaling, double factor,
+                        int32_t original_ctx, double low_turns, double high_turns, double gain);
+TV_API int tv_rope_rows(const tv_rope *rope, const tv_bf16 *x, size_t x_stride, tv_bf16 *out, size_t out_stride,
+                        int n_heads, int head_dim, const int32_t *positions, int rows, int32_t *dev_status,
+                        void *stream);
+
+/*
  * Verify prices and the StairCut cut [Drafters and tree verify, §StairCut: the
  * node count, calculated each round; §StairCut on Flash-Next, and the shared
  * price files].  Host-only: no device memory, nothing launched.

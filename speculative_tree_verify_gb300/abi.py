@@ -33,7 +33,9 @@ SYMBOLS = ("tv_workspace_size", "tv_verify_tree", "tv_accept_greedy", "tv_accept
            "tv_accept_greedy_commit", "tv_stack_workspace_size", "tv_verify_stack", "tv_commit_stack",
            "tv_pages_workspace_size", "tv_pages_extend", "tv_pages_fork", "tv_pages_release", "tv_pages_compact",
            "tv_pages_write", "tv_pages_read", "tv_attend_paged_workspace_size", "tv_attend_paged",
-           "tv_attend_prompt")
+           "tv_attend_prompt", "tv_attend_prompt_window", "tv_attend_paged_window", "tv_pages4_workspace_size",
+           "tv_pages4_extend", "tv_pages4_fork", "tv_pages4_release", "tv_pages4_compact", "tv_pages4_write",
+           "tv_pages4_read", "tv_attend_paged4_workspace_size", "tv_attend_paged4", "tv_rope_init", "tv_rope_rows")
 PROFILE_STAGES = ("prologue+embed", "qkv_gemm", "qkv_finalize", "attention", "o_gemm", "o_finalize", "lm_head")
 
 
@@ -93,6 +95,19 @@ class TvPool(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("n_layers", ctypes.c_int32),
                 ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32)]
+
+
+class TvPool4(ctypes.Structure):
+    _fields_ = TvPool._fields_
+
+
+TV_ROPE_PLAIN, TV_ROPE_LINEAR, TV_ROPE_BASE, TV_ROPE_BLEND = 0, 1, 2, 3
+ROPE_MAX_PAIRS = 64
+
+
+class TvRope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("gain", ctypes.c_double),
+                ("freq", ctypes.c_double * ROPE_MAX_PAIRS)]
 
 
 class TvSeqs(ctypes.Structure):
@@ -162,7 +177,16 @@ def load():
         lib.tv_attend_prompt.argtypes = [I, I, I, P, P, P, Z, Z, P, I, I, P, P, P]
         lib.tv_attend_paged_workspace_size.argtypes = [PO, I, I, ctypes.POINTER(Z)]
         lib.tv_attend_paged.argtypes = [PO, I, SQ, P, I, I, P, Z, P, P, Z, P, P, Z, P, P]
+        lib.tv_attend_prompt_window.argtypes = [I, I, I, I, I, P, P, P, Z, Z, P, I, I, P, P, P]
+        lib.tv_attend_paged_window.argtypes = [PO, I, SQ, P, I, I, I, I, P, Z, P, P, Z, P, P, Z, P, P]
+        P4 = ctypes.POINTER(TvPool4)
+        for name in ("workspace_size", "extend", "fork", "release", "compact", "write", "read"):   # as those of tv_pool
+            getattr(lib, "tv_pages4_" + name).argtypes = [P4] + getattr(lib, "tv_pages_" + name).argtypes[1:]
+        lib.tv_attend_paged4_workspace_size.argtypes = [P4, I, I, ctypes.POINTER(Z)]
+        lib.tv_attend_paged4.argtypes = [P4] + lib.tv_attend_paged_window.argtypes[1:]
         D = ctypes.c_double
+        lib.tv_rope_init.argtypes = [ctypes.POINTER(TvRope), I, I, D, I, D, ctypes.c_int32, D, D, D]
+        lib.tv_rope_rows.argtypes = [ctypes.POINTER(TvRope), P, Z, P, Z, I, I, P, I, P, P]
         lib.tv_price_init.argtypes = [ctypes.POINTER(TvPriceTable)]
         lib.tv_price_lookup.argtypes = [ctypes.POINTER(TvPriceTable), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                         ctypes.POINTER(D)]
@@ -406,6 +430,107 @@ def tv_attend_paged(pool: TvPool, layer: int, seqs: TvSeqs, ids, n: int, n_q_hea
     return load().tv_attend_paged(ctypes.byref(pool), int(layer), ctypes.byref(seqs), _p(ids), int(n), int(n_q_heads),
                                   _p(q), int(q_stride), _p(k_new), _p(v_new), int(kv_stride), _p(out), _p(workspace),
                                   int(workspace_bytes), _p(dev_status), _stream(stream))
+
+
+def tv_attend_prompt_window(n_q_heads: int, n_kv_heads: int, head_dim: int, window: int, sinks: int, q, k, v,
+                            q_stride: int, kv_stride: int, starts, n_seqs: int, rows: int, out, dev_status,
+                            stream=None) -> int:
+    """Strides in elements."""
+    return load().tv_attend_prompt_window(int(n_q_heads), int(n_kv_heads), int(head_dim), int(window), int(sinks),
+                                          _p(q), _p(k), _p(v), int(q_stride), int(kv_stride), _p(starts), int(n_seqs),
+                                          int(rows), _p(out), _p(dev_status), _stream(stream))
+
+
+def tv_attend_paged_window(pool: TvPool, layer: int, seqs: TvSeqs, ids, n: int, n_q_heads: int, window: int,
+                           sinks: int, q, q_stride: int, k_new, v_new, kv_stride: int, out, workspace,
+                           workspace_bytes: int, dev_status, stream=None) -> int:
+    """Strides in elements; k_new and v_new may be None."""
+    return load().tv_attend_paged_window(ctypes.byref(pool), int(layer), ctypes.byref(seqs), _p(ids), int(n),
+                                         int(n_q_heads), int(window), int(sinks), _p(q), int(q_stride), _p(k_new),
+                                         _p(v_new), int(kv_stride), _p(out), _p(workspace), int(workspace_bytes),
+                                         _p(dev_status), _stream(stream))
+
+
+def tv_pages4_workspace_size(pool: TvPool4, seqs: TvSeqs) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().tv_pages4_workspace_size(ctypes.byref(pool), ctypes.byref(seqs), ctypes.byref(out))
+    if rc != TV_OK:
+        raise ValueError(f"tv_pages4_workspace_size: {STATUS.get(rc, rc)}")
+    return int(out.value)
+
+
+def tv_pages4_extend(pool: TvPool4, seqs: TvSeqs, ids, add, n: int, workspace, workspace_bytes: int, dev_status,
+                     stream=None) -> int:
+    return load().tv_pages4_extend(ctypes.byref(pool), ctypes.byref(seqs), _p(ids), _p(add), int(n), _p(workspace),
+                                   int(workspace_bytes), _p(dev_status), _stream(stream))
+
+
+def tv_pages4_fork(pool: TvPool4, seqs: TvSeqs, src, dst, n: int, dev_status, stream=None) -> int:
+    return load().tv_pages4_fork(ctypes.byref(pool), ctypes.byref(seqs), _p(src), _p(dst), int(n), _p(dev_status),
+                                 _stream(stream))
+
+
+def tv_pages4_release(pool: TvPool4, seqs: TvSeqs, ids, keep, n: int, dev_status, stream=None) -> int:
+    return load().tv_pages4_release(ctypes.byref(pool), ctypes.byref(seqs), _p(ids), _p(keep), int(n), _p(dev_status),
+                                    _stream(stream))
+
+
+def tv_pages4_compact(pool: TvPool4, seqs: TvSeqs, remap, n_used, workspace, workspace_bytes: int, dev_status,
+                      stream=None) -> int:
+    return load().tv_pages4_compact(ctypes.byref(pool), ctypes.byref(seqs), _p(remap), _p(n_used), _p(workspace),
+                                    int(workspace_bytes), _p(dev_status), _stream(stream))
+
+
+def tv_pages4_write(pool: TvPool4, layer: int, seqs: TvSeqs, ids, pos, starts, n: int, rows: int, k, v,
+                    row_stride: int, head_stride: int, dev_status, stream=None) -> int:
+    """As tv_pages_write, from bf16 rows into 4 bits."""
+    return load().tv_pages4_write(ctypes.byref(pool), int(layer), ctypes.byref(seqs), _p(ids), _p(pos), _p(starts),
+                                  int(n), int(rows), _p(k), _p(v), int(row_stride), int(head_stride), _p(dev_status),
+                                  _stream(stream))
+
+
+def tv_pages4_read(pool: TvPool4, layer: int, seqs: TvSeqs, ids, pos, starts, n: int, rows: int, k, v,
+                   row_stride: int, head_stride: int, dev_status, stream=None) -> int:
+    """As tv_pages_read, from 4 bits into bf16 rows."""
+    return load().tv_pages4_read(ctypes.byref(pool), int(layer), ctypes.byref(seqs), _p(ids), _p(pos), _p(starts),
+                                 int(n), int(rows), _p(k), _p(v), int(row_stride), int(head_stride), _p(dev_status),
+                                 _stream(stream))
+
+
+def tv_attend_paged4_workspace_size(pool: TvPool4, n_q_heads: int, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().tv_attend_paged4_workspace_size(ctypes.byref(pool), int(n_q_heads), int(n), ctypes.byref(out))
+    if rc != TV_OK:
+        raise ValueError(f"tv_attend_paged4_workspace_size: {STATUS.get(rc, rc)}")
+    return int(out.value)
+
+
+def tv_attend_paged4(pool: TvPool4, layer: int, seqs: TvSeqs, ids, n: int, n_q_heads: int, window: int, sinks: int, q,
+                     q_stride: int, k_new, v_new, kv_stride: int, out, workspace, workspace_bytes: int, dev_status,
+                     stream=None) -> int:
+    """Strides in elements; k_new and v_new may be None."""
+    return load().tv_attend_paged4(ctypes.byref(pool), int(layer), ctypes.byref(seqs), _p(ids), int(n),
+                                   int(n_q_heads), int(window), int(sinks), _p(q), int(q_stride), _p(k_new), _p(v_new),
+                                   int(kv_stride), _p(out), _p(workspace), int(workspace_bytes), _p(dev_status),
+                                   _stream(stream))
+
+
+def tv_rope_init(rot_dim: int, interleaved: bool = False, theta: float = 10000.0, scaling: int = TV_ROPE_PLAIN,
+                 factor: float = 1.0, original_ctx: int = 1, low_turns: float = 1.0, high_turns: float = 32.0,
+                 gain: float = 1.0) -> TvRope:
+    rope = TvRope()
+    rc = load().tv_rope_init(ctypes.byref(rope), int(rot_dim), 1 if interleaved else 0, float(theta), int(scaling),
+                             float(factor), int(original_ctx), float(low_turns), float(high_turns), float(gain))
+    if rc != TV_OK:
+        raise ValueError(f"tv_rope_init: {STATUS.get(rc, rc)}")
+    return rope
+
+
+def tv_rope_rows(rope: TvRope, x, x_stride: int, out, out_stride: int, n_heads: int, head_dim: int, positions,
+                 rows: int, dev_status, stream=None) -> int:
+    """Strides in elements; out may be x."""
+    return load().tv_rope_rows(ctypes.byref(rope), _p(x), int(x_stride), _p(out), int(out_stride), int(n_heads),
+                               int(head_dim), _p(positions), int(rows), _p(dev_status), _stream(stream))
 
 
 def tv_price_init(table: TvPriceTable) -> int:

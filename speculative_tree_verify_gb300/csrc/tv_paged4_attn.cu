@@ -1,0 +1,593 @@
+// Attention of one new token per sequence over a paged cache in 4 bits (tv_pool4),
+// through a window or not:
+//   o[i, h] = sum_j softmax_j(q[i, h] . k[j, g] / sqrt(D)) v[j, g],  k, v = n s,
+// n the codes less 8, s a scale of each token's 32 dimensions.
+//
+// What bounds it: 9/8 bytes a value of K and V together, so that instructions
+// come near to memory: a block of 16 tokens of one head (2.3 KB of K and V at D = 128) is
+// about 90 cycles of an SM's share of the bandwidth, and as many issue slots
+// on each of its four schedulers as there are.  Hence:
+// - The cache lies as the tensor cores' operands do (tv_pool4): a lane loads its
+//   codes with 16-byte loads, no ldmatrix, no shuffle.
+// - Codes become fp16 without arithmetic: masked out of a word, 4 bits are the
+//   subnormal n' 2^-24, or 16 times that, n' = n + 8.  q is scaled to its row's
+//   exponent, and the 16 taken into it where it meets the higher bits.
+// - Q K^T (m16n8k16: rows are heads, columns tokens) begins at -8 sum q instead of
+//   zero, a group of 32 dimensions at a time, and each group's sum takes the
+//   token's scale.  Its 8 heads by 16 tokens are, in the same lanes, the B operand
+//   of O^T += V^T P^T (rows are dimensions, columns 8 heads): up to 8 heads a KV
+//   head cost half of what 16 do.  V's codes less 8 are one packed subtraction.
+// - A token's V scale goes into its weight, four weights of fp16 a token (one a
+//   group), so that V needs no product.  The weights are relative to the largest
+//   scale so far, as they are to the offset: 2^15 at most, 2^-24 at least.
+//
+// How the work is cut over CTAs is in tv_paged_runs.cuh.  In a CTA one warp looks
+// up pages (32 boxes' entries at a time, the next 32 on their way) and copies whole blocks into
+// a ring of stages; the others compute, tile t by warps 4 (t mod quads) .. + 3, 16 tokens
+// each.
+#include <cmath>
+#include <type_traits>
+
+#include <cuda_fp16.h>
+
+#include "tv_paged_runs.cuh"
+#include "tv_pages4.cuh"
+
+namespace tv {
+namespace {
+
+constexpr int kStages = 12;                      // tiles in flight: 108 KB at D = 128
+constexpr int kQueries = 8;                      // runs whose queries are loaded ahead, at most
+constexpr int kSegCost = 3;                      // what a head block costs besides its tiles, in tiles
+constexpr float kMoveLog2 = 8.f;                 // offsets move when a score passes them by this
+constexpr uint32_t kLiftBits = (127u + 127u + 7u) << 23;   // weights times scales up to 2^15; less a power of two's bits
+
+// HN: blocks of 8 heads
+template <int D, int HN>
+struct P4 {
+  using B = Block4<D>;
+  static constexpr int WARPS = HN == 1 ? 12 : 8;   // that compute; the accumulators of 16 heads need the other half's registers
+  static constexpr int QUADS = WARPS / 4;
+  static constexpr int THREADS = 32 * WARPS + 32;
+  static constexpr int HEADS = 8 * HN;
+  static constexpr int HALF = kTile / 16 * B::BYTES;   // a tile's K (or V)
+  static constexpr int STAGE = 2 * HALF;
+  static constexpr int OFF_RED = kStages * STAGE;      // [WARPS][HEADS][D] fp32; the marks of listed rows first
+  static constexpr int OFF_ML = OFF_RED + WARPS * HEADS * D * 4;
+  static constexpr int Q_ROW = D * 2 + 16;
+  static constexpr int OFF_Q = OFF_ML + WARPS * kRows * 8;
+  static constexpr int OFF_BAR = OFF_Q + 2 * kRows * Q_ROW;
+  static constexpr int OFF_FIRST = OFF_BAR + 512;
+  static size_t bytes(int n) { return 128 + OFF_FIRST + (size_t)(n + 1) * 4 + (n <= kInfo ? (size_t)n * 8 : 0); }
+  static_assert(kStages % QUADS == 0, "a stage always belongs to the same four warps");
+  static_assert((2 * kStages + 2 * kQueries) * 8 <= 512, "barriers");
+  static_assert(WARPS * HEADS * D * 4 >= kMaxSeqs / 8, "a mark for every table row");
+  static_assert(128 + OFF_FIRST + (kMaxTokens + 1) * 4 <= 232448 - 512, "shared memory of one CTA");
+  static_assert(HALF % 16 == 0 && B::BYTES % 16 == 0, "bulk copies");
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// G words of shared memory, 4 G bytes aligned
+template <int G>
+__device__ __forceinline__ void lds_words(const uint8_t* a, uint32_t (&w)[G]) {
+  if constexpr (G == 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(a);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2*>(a);
+    w[0] = x.x, w[1] = x.y;
+  }
+}
+
+template <int D, int HN>
+__global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(const __grid_constant__ PaParams p) {
+  using L = P4<D, HN>;
+  using B = Block4<D>;
+  constexpr int G = B::G, NW = L::WARPS, NQ = L::QUADS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* empty = full + kStages;
+  uint64_t* q_full = empty + kStages;    // [kQueries] a run's queries landed
+  uint64_t* q_free = q_full + kQueries;  // [kQueries] all warps have seen them, those that compute it are done with them
+  uint32_t* s_first = reinterpret_cast<uint32_t*>(smem + L::OFF_FIRST);
+  float* s_red = reinterpret_cast<float*>(smem + L::OFF_RED);
+  float2* s_ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
+  uint32_t* s_mark = reinterpret_cast<uint32_t*>(smem + L::OFF_RED);
+  __shared__ uint32_t s_part[L::THREADS / 32];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ps = p.pool.page_size, Hkv = p.pool.n_kv_heads;
+  const int qrows = min(kRows, p.G), qslots = min(kQueries, 2 * kRows / qrows);
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 4);   // the four warps that compute its tile
+    }
+    for (int s = 0; s < kQueries; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_free[s], NW);
+    }
+    fence_mbar_init();
+    s_bad = 0;
+  }
+  if (p.n > 32 && p.k_new)
+    for (int i = tid; i < (p.seqs.max_seqs + 31) / 32; i += L::THREADS) s_mark[i] = 0u;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+
+  RunList<L::THREADS, kSegCost, true> runs(p, s_first);
+  if (!runs.build(s_mark, s_part, &s_bad)) return;
+  // sequences without a token: zeros
+  for (int i = blockIdx.x; i < p.n; i += gridDim.x)
+    if (s_first[i + 1] == s_first[i])
+      for (int e = tid; e < p.Hq * D / 8; e += L::THREADS)
+        reinterpret_cast<uint4*>(p.out + (size_t)i * p.Hq * D)[e] = make_uint4(0u, 0u, 0u, 0u);
+  runs.range();
+  if (tid == 0) p.ws.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (runs.lo >= runs.hi) return;
+
+  if (warp == NW) {
+    // ---------------- pages and loads ----------------
+    const int R = ps < kTile ? ps : kTile;                 // tokens of a box
+    const int nsh = 6 - (31 - __clz(R)), nb = 1 << nsh;    // boxes of a tile
+    const int psh = 31 - __clz(ps), per = 32 >> nsh;       // tiles of 32 boxes
+    const size_t head_bytes = (size_t)(ps / 16) * B::BYTES;
+    bool ok = true;
+    int issued = 0, segs = 0, st = 0, qs = 0;   // tiles and queries loaded so far, their places in the rings
+    uint32_t st_par = 1u, qs_par = 1u;          // of the wait before a place is used again (not in the first round)
+    // blocks [a, b) of the box at tok hold tokens that are seen
+    auto blocks = [&](const Run& g, int tok, int& a, int& b) {
+      a = 0;
+      b = (min(R, g.len - tok) + 15) >> 4;
+      if (tok >= p.sinks) a = max(0, g.lo - tok) >> 4;
+      else if (tok <= g.lo - R) b = min(b, (p.sinks - tok + 15) >> 4);   // (sinks and window in one box: all of it)
+    };
+    auto entry = [&](const Run& g, int tb) {   // the page of this lane's box of tiles tb ..., -1: not seen
+      const int t = tb + (lane >> nsh);
+      if (t >= g.t1) return -1;
+      const int tok = g.tile<true>(t) * kTile + (lane & (nb - 1)) * R;
+      if (tok >= g.len) return -1;
+      int a, b;
+      blocks(g, tok, a, b);
+      return a < b ? __ldcg(p.seqs.pages + (size_t)g.s * p.seqs.max_pages + (tok >> psh)) : -1;
+    };
+    Run g;
+    bool have = runs.first_run(g);
+    int pages = have ? entry(g, g.t0) : -1;
+    while (have && ok) {
+      Run next = g;   // the next entries are on their way before this run's tiles
+      const bool more = runs.next_run(next);
+      // its queries
+      if (segs >= qslots) ok = __all_sync(0xffffffffu, mbar_wait(&q_free[qs], qs_par));
+      if (!ok) break;
+      const int r0 = g.hb * kRows, nr = min(kRows, p.G - r0);
+      if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], (uint32_t)(nr * D * 2));
+      __syncwarp();
+      if (lane < nr)
+        bulk_load(smem + L::OFF_Q + (qs * qrows + lane) * L::Q_ROW,
+                  p.q + (size_t)g.i * p.q_stride + (size_t)(g.h * p.G + r0 + lane) * D, D * 2, &q_full[qs]);
+      ++segs;
+      if (++qs == qslots) qs = 0, qs_par ^= 1u;
+      for (int tb = g.t0; tb < g.t1 && ok; tb += per) {
+        const int next_pages = tb + per < g.t1 ? entry(g, tb + per) : (more ? entry(next, next.t0) : -1);
+        for (int t = tb; t < min(tb + per, g.t1); ++t) {
+          // lane 2 b: K of box b, lane 2 b + 1: V
+          const int box = lane >> 1;
+          const int page = __shfl_sync(0xffffffffu, pages, ((t - tb) << nsh) + (box & (nb - 1)));
+          const int tok = g.tile<true>(t) * kTile + box * R;
+          int a = 0, b = 0;
+          if (box < nb && tok < g.len) blocks(g, tok, a, b);
+          const bool in = a < b, good = in && page >= 0 && page < p.pool.n_pages;
+          if (in && !good) status_set(p.status, TV_E_PAGE);
+          const uint32_t bytes = good ? (uint32_t)((b - a) * B::BYTES) : 0u;
+          const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+          if (issued >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], st_par));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], total);
+          __syncwarp();
+          if (good) {
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(lane & 1 ? p.pool.v : p.pool.k) +
+                                 (((size_t)p.layer * p.pool.n_pages + page) * Hkv + g.h) * head_bytes +
+                                 (size_t)(((tok & (ps - 1)) >> 4) + a) * B::BYTES;
+            bulk_load(smem + st * L::STAGE + (lane & 1) * L::HALF + (box * (R / 16) + a) * B::BYTES, src, bytes, &full[st]);
+          }
+          __syncwarp();
+          ++issued;
+          if (++st == kStages) st = 0, st_par ^= 1u;
+        }
+        pages = next_pages;
+      }
+      g = next;
+      have = more;
+    }
+    if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
+    for (int u = segs > qslots ? segs - qslots : 0; u < segs; ++u)
+      mbar_wait(&q_full[u % qslots], (uint32_t)(u / qslots) & 1u);
+    // loads in flight land before the CTA leaves
+    for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u)
+      mbar_wait(&full[u % kStages], (uint32_t)(u / kStages) & 1u);
+    return;
+  }
+
+  // ---------------- compute warps ----------------
+  const int quad = warp >> 2, sl = warp & 3;        // tiles with (count mod NQ) == quad; tokens 16 sl .. + 15 of a tile
+  const int g8 = lane >> 2, t4 = lane & 3;
+  auto meet = [&](int nw) {
+    asm volatile("bar.sync %0, %1;" ::"r"(nw == NW ? 1 : 2 + quad), "r"(32 * nw) : "memory");
+  };
+  bool ok = true;
+  // the next tile and queries of this CTA: places in the rings, parities
+  int st = 0, qs = 0;
+  uint32_t st_par = 0u, qs_par = 0u;
+  Run g;
+  for (bool have = runs.first_run(g); have; have = runs.next_run(g)) {
+    const int h = g.h, r0 = g.hb * kRows;   // KV head, first query head of the block in the group
+    const int nr = min(kRows, p.G - r0);
+    if (ok && !mbar_wait(&q_full[qs], qs_par)) ok = false;
+    if (g.T == 1 && st % NQ != quad) {   // one tile, and another four warps'
+      // (no further ahead than the queries, nor further behind than their place:
+      // it is not loaded again before these warps, too, have seen this phase)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_free[qs]);
+      if (++st == kStages) st = 0, st_par ^= 1u;
+      if (++qs == qslots) qs = 0, qs_par ^= 1u;
+      continue;
+    }
+    // Queries: rows g8 (and g8 + 8), dimensions 32 j + 8 t4 .. + 7 of group j, as
+    // fp16 relative to the row's exponent.  qf[row block][j][u]: dimensions u and
+    // u + 4, where u is odd over 16, since their codes come times 16.
+    uint32_t qf[HN][G][4];
+    float bias[HN][G], sc[HN];   // -8 sum q of a group; what a product of q and codes is worth, in powers of two
+#pragma unroll
+    for (int b = 0; b < HN; ++b) {
+      // rows past the group's heads: the last one again, products nobody reads
+      const uint8_t* row = smem + L::OFF_Q + (qs * qrows + min(g8 + 8 * b, nr - 1)) * L::Q_ROW + t4 * 16;
+      uint4 x[G];
+      uint32_t top = 0u;
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        x[j] = *reinterpret_cast<const uint4*>(row + j * 64);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu),
+                                     __vmaxu2(x[j].z & 0x7fff7fffu, x[j].w & 0x7fff7fffu)));
+      }
+      top = max(top & 0xffffu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the largest to 2^13 .. 2^14; below 2^-114 it stays smaller
+      const int e = max((int)(top >> 7), 13);   // 127 + exponent
+      const float f = __uint_as_float((uint32_t)(267 - e) << 23);
+      sc[b] = p.scale_log2 * 0x1p24f * __uint_as_float((uint32_t)max(e - 13, 1) << 23);
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {   // dimensions u and u + 4: halves u % 2 of words u / 2 and u / 2 + 2
+          const float k = u & 1 ? f * 0.0625f : f;
+          const float a = (u & 1 ? __uint_as_float(w[u >> 1] & 0xffff0000u) : __uint_as_float(w[u >> 1] << 16)) * k;
+          const float c = (u & 1 ? __uint_as_float(w[(u >> 1) + 2] & 0xffff0000u) : __uint_as_float(w[(u >> 1) + 2] << 16)) * k;
+          const __half2 v = __floats2half2_rn(a, c);
+          qf[b][j][u] = *reinterpret_cast<const uint32_t*>(&v);
+          const float2 r = __half22float2(v);
+          sum += (r.x + r.y) * (u & 1 ? 16.f : 1.f);
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        bias[b][j] = sum * -0x1p-21f;   // -8 * 2^-24
+      }
+    }
+    // O^T: o[row block][j][0 .. 3] rows 32 j + 4 g8 + {0, 0, 1, 1}, heads 2 t4 + {0, 1, 0, 1}; [4 .. 7]: 2 more
+    float o[HN][G][8];
+    float m[HN], l[HN];          // offsets and sums of rows g8 (+ 8), of this thread's tokens
+    float vtop = 0x1p-100f;      // power of two above the scales of V so far
+#pragma unroll
+    for (int b = 0; b < HN; ++b) {
+      m[b] = -INFINITY, l[b] = 0.f;
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[b][j][e] = 0.f;
+    }
+
+    for (int t = g.t0; t < g.t1; ++t) {
+      const int at = st;
+      const uint32_t par = st_par;
+      if (++st == kStages) st = 0, st_par ^= 1u;
+      if (at % NQ != quad) continue;   // the number of stages is a multiple of the quads': the place's parity is the tile's
+      uint8_t* sk = smem + at * L::STAGE + sl * B::BYTES;
+      uint8_t* sv = sk + L::HALF;
+      if (ok && !mbar_wait(&full[at], par)) ok = false;
+      const int tok0 = g.tile<true>(t) * kTile + 16 * sl;
+      int valid = min(16, g.len - tok0);   // this warp's tokens
+      const int hide0 = max(0, p.sinks - tok0), hide1 = min(16, g.lo - tok0);   // those from hide0 up to hide1 are hidden
+      if (hide0 == 0 && hide1 >= valid) valid = 0;
+      if (valid > 0) {
+        bool wrote = false;
+        if (p.k_new && tok0 + valid == g.len) {
+          // the new token: its codes into the tile and into the page
+          const bool is_v = lane >= 16;
+          const int c = lane & 15, tk = valid - 1, half = tk % 2 * 2;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (c < D / 8)
+            x = __ldcg(reinterpret_cast<const uint4*>((is_v ? p.v_new : p.k_new) + (size_t)g.i * p.kv_stride + (size_t)h * D) + c);
+          uint32_t scale;
+          const uint32_t w = round4(x, scale);
+          const int page = __ldcg(p.seqs.pages + (size_t)g.s * p.seqs.max_pages + (g.len - 1) / ps);
+          const bool store = r0 == 0 && page >= 0 && page < p.pool.n_pages;
+          if (c < D / 8) {
+            auto put = [&](uint8_t* block) {
+              if (is_v) {
+                *reinterpret_cast<uint16_t*>(block + B::v_word(tk, 2 * c) + half) = (uint16_t)w;
+                *reinterpret_cast<uint16_t*>(block + B::v_word(tk, 2 * c + 1) + half) = (uint16_t)(w >> 16);
+              } else {
+                *reinterpret_cast<uint32_t*>(block + B::k_word(tk, c)) = w;
+              }
+              if (c % 4 == 0) *reinterpret_cast<uint16_t*>(block + B::scale(tk, c / 4) + half) = (uint16_t)scale;
+            };
+            put(is_v ? sv : sk);
+            if (store)
+              put(reinterpret_cast<uint8_t*>(is_v ? p.pool.v : p.pool.k) +
+                  ((((size_t)p.layer * p.pool.n_pages + page) * Hkv + h) * ps + (g.len - 1) % ps / 16 * 16) / 16 * B::BYTES);
+          }
+          wrote = true;
+          __syncwarp();
+        }
+        // tokens of this thread, as columns of S and rows of P: 2 t4, 2 t4 + 1 (half 0) and 8 more (half 1)
+        float x[HN][2][2];
+        {
+          uint32_t ka[2][G], sa[2][G];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            lds_words<G>(sk + (8 * n + g8) * (D / 2) + t4 * (D / 8), ka[n]);
+            lds_words<G>(sk + B::OFF_SCALE + (n * 4 + t4) * G * 4, sa[n]);
+          }
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              const uint32_t w = ka[n][j], w8 = w >> 8;
+              float c[4], d[4];
+              mma_f16(c, qf[0][j][0], HN > 1 ? qf[HN - 1][j][0] : 0u, qf[0][j][1], HN > 1 ? qf[HN - 1][j][1] : 0u,
+                      w & 0x000f000fu, w & 0x00f000f0u, bias[0][j], bias[0][j], bias[HN - 1][j], bias[HN - 1][j]);
+              mma_f16(d, qf[0][j][2], HN > 1 ? qf[HN - 1][j][2] : 0u, qf[0][j][3], HN > 1 ? qf[HN - 1][j][3] : 0u,
+                      w8 & 0x000f000fu, w8 & 0x00f000f0u, c[0], c[1], c[2], c[3]);
+              const float s0 = __uint_as_float(sa[n][j] << 16), s1 = __uint_as_float(sa[n][j] & 0xffff0000u);
+#pragma unroll
+              for (int b = 0; b < HN; ++b) {
+                x[b][n][0] = j == 0 ? d[2 * b] * s0 : fmaf(d[2 * b], s0, x[b][n][0]);
+                x[b][n][1] = j == 0 ? d[2 * b + 1] * s1 : fmaf(d[2 * b + 1], s1, x[b][n][1]);
+              }
+            }
+          }
+        }
+        uint32_t sb[2][G];   // scales of V
+#pragma unroll
+        for (int n = 0; n < 2; ++n) lds_words<G>(sv + B::OFF_SCALE + (n * 4 + t4) * G * 4, sb[n]);
+#pragma unroll
+        for (int b = 0; b < HN; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[b][e >> 1][e & 1] *= sc[b];
+        if (valid < 16 || hide0 < hide1) {   // what is past the length or hidden: no score, and a scale of zero, whatever it holds
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tk = 8 * (e >> 1) + 2 * t4 + (e & 1);
+            if (tk >= valid || (tk >= hide0 && tk < hide1)) {
+#pragma unroll
+              for (int b = 0; b < HN; ++b) x[b][e >> 1][e & 1] = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < G; ++j) sb[e >> 1][j] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+            }
+          }
+        }
+        // offsets and the largest scale: moved when passed, hardly ever
+        bool pass = false;
+#pragma unroll
+        for (int b = 0; b < HN; ++b)
+          pass = pass || fmaxf(fmaxf(x[b][0][0], x[b][0][1]), fmaxf(x[b][1][0], x[b][1][1])) > m[b] + kMoveLog2;
+        uint32_t top = 0u;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int j = 0; j < G; ++j) top = __vmaxu2(top, sb[n][j]);
+        top = max(top & 0xffffu, top >> 16);
+        if (__any_sync(0xffffffffu, pass || __uint_as_float(top << 16) > vtop || top >= 0x7f80u)) {
+          // scales that are NaN say nothing of the others
+          top = 0u;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              const uint32_t a = sb[n][j] & 0xffffu, b = sb[n][j] >> 16;
+              top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+            }
+          top = __reduce_max_sync(0xffffffffu, top);
+          float all = 1.f;
+          if (__uint_as_float(top << 16) > vtop) {   // to the next power of two
+            const float v = __uint_as_float(((top >> 7) + 1u) << 23);
+            all = vtop / v;
+            vtop = v;
+          }
+#pragma unroll
+          for (int b = 0; b < HN; ++b) {
+            float y = fmaxf(fmaxf(x[b][0][0], x[b][0][1]), fmaxf(x[b][1][0], x[b][1][1]));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+            const float n = y > m[b] + kMoveLog2 ? y : m[b];
+            const float a = n == m[b] ? 1.f : ex2f(m[b] - n);
+            m[b] = n;
+            l[b] *= a;
+            // of heads 2 t4 and 2 t4 + 1: rows of the lanes 8 t4 and 8 t4 + 4
+            const float a0 = __shfl_sync(0xffffffffu, a, 8 * t4) * all, a1 = __shfl_sync(0xffffffffu, a, 8 * t4 + 4) * all;
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[b][j][e] *= e & 1 ? a1 : a0;
+          }
+        }
+        const float lift = __uint_as_float(kLiftBits - __float_as_uint(vtop));   // 2^7 / vtop
+#pragma unroll
+        for (int b = 0; b < HN; ++b) {
+          const float f = m[b] == -INFINITY ? 0.f : m[b];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = ex2f(x[b][e >> 1][e & 1] - f);
+            l[b] += y;
+            x[b][e >> 1][e & 1] = y * lift;
+          }
+        }
+        uint32_t va[2][G];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) lds_words<G>(sv + (n * 32 + lane) * G * 4, va[n]);
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          // rows u of V^T: dimensions 4 g8 + u of the group, the odd ones times 16; columns: tokens 2 t4, 2 t4 + 1 and 8 more
+          uint32_t a[4][2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t w = va[n][j], w8 = w >> 8;
+            a[0][n] = sub_f16(w & 0x000f000fu, 0x00080008u);
+            a[1][n] = sub_f16(w & 0x00f000f0u, 0x00800080u);
+            a[2][n] = sub_f16(w8 & 0x000f000fu, 0x00080008u);
+            a[3][n] = sub_f16(w8 & 0x00f000f0u, 0x00800080u);
+          }
+#pragma unroll
+          for (int b = 0; b < HN; ++b) {
+            uint32_t pw[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              pw[n] = pack_f16(x[b][n][0] * __uint_as_float(sb[n][j] << 16), x[b][n][1] * __uint_as_float(sb[n][j] & 0xffff0000u));
+            float(&lo)[4] = *reinterpret_cast<float(*)[4]>(&o[b][j][0]);
+            float(&hi)[4] = *reinterpret_cast<float(*)[4]>(&o[b][j][4]);
+            mma_f16(lo, a[0][0], a[1][0], a[0][1], a[1][1], pw[0], pw[1], lo[0], lo[1], lo[2], lo[3]);
+            mma_f16(hi, a[2][0], a[3][0], a[2][1], a[3][1], pw[0], pw[1], hi[0], hi[1], hi[2], hi[3]);
+          }
+        }
+        if (wrote) fence_async_smem();   // before the stage takes another copy
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[at]);
+    }
+
+    // ---- the head block's partial results into one ----
+    // of all warps, or, where the head block is one tile, of the four that had
+    // it: the others go on to the next head block meanwhile
+    const bool whole = g.t0 == 0 && g.t1 == g.T;
+    const int nw = g.T > 1 ? NW : 4, w0 = g.T > 1 ? 0 : 4 * quad, me = tid - 32 * w0;
+    // a CTA's first run may begin inside a head block, its last end inside one
+    const size_t slot = (size_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0);
+#pragma unroll
+    for (int b = 0; b < HN; ++b) {
+      l[b] += __shfl_xor_sync(0xffffffffu, l[b], 1);
+      l[b] += __shfl_xor_sync(0xffffffffu, l[b], 2);
+      if (t4 == 0) s_ml[warp * kRows + 8 * b + g8] = make_float2(m[b], l[b]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {   // head 8 b + 2 t4 + e, dimensions 32 j + 4 g8 .. + 3: chunks turned by the head, no bank twice
+        float* dst = s_red + ((size_t)warp * L::HEADS + 8 * b + 2 * t4 + e) * D + ((g8 + 2 * t4) & 7) * 4;
+        if (8 * b + 2 * t4 + e < nr)
+#pragma unroll
+          for (int j = 0; j < G; ++j) {   // what the codes' and the weights' factors leave: 2^17 and 2^13 of vtop
+            const float(&r)[8] = o[b][j];
+            *reinterpret_cast<float4*>(dst + 32 * j) = make_float4(r[e] * 0x1p17f * vtop, r[2 + e] * 0x1p13f * vtop,
+                                                                   r[4 + e] * 0x1p17f * vtop, r[6 + e] * 0x1p13f * vtop);
+          }
+      }
+    }
+    meet(nw);
+    if (lane == 0) mbar_arrive(&q_free[qs]);
+    for (int e = me; e < nr * (D / 4); e += 32 * nw) {
+      const int row = e / (D / 4), d = e % (D / 4);   // head, four dimensions
+      float M = -INFINITY, sum = 0.f;
+      for (int w = 0; w < nw; ++w) M = fmaxf(M, s_ml[(w0 + w) * kRows + row].x);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float* src = s_red + ((size_t)w0 * L::HEADS + row) * D + d / 8 * 32 + ((d + (row & 6)) & 7) * 4;
+#pragma unroll 4
+      for (int w = 0; w < nw; ++w) {
+        const float2 x = s_ml[(w0 + w) * kRows + row];
+        const float4 v = *reinterpret_cast<const float4*>(src + (size_t)w * L::HEADS * D);
+        const float f = x.x == -INFINITY ? 1.f : ex2f(x.x - M);   // (no token: zeros; or scores that are no numbers)
+        sum = fmaf(x.y, f, sum);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+      if (whole) {
+        const float f = 1.f / sum;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f), hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+        *reinterpret_cast<uint2*>(p.out + ((size_t)g.i * p.Hq + h * p.G + r0 + row) * D + 4 * d) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      } else {
+        *reinterpret_cast<float4*>(p.ws.o + (slot * kRows + row) * D + 4 * d) = acc;
+        if (d == 0) *reinterpret_cast<float2*>(p.ws.ml + (slot * kRows + row) * 2) = make_float2(M, sum);
+      }
+    }
+    meet(nw);   // before the places of the sums are written again
+    if (++qs == qslots) qs = 0, qs_par ^= 1u;
+    if (tid == 0 && g.t0 == 0 && !whole)   // the CTA's last run
+      p.ws.cut[blockIdx.x] = make_int4(g.i, g.h * p.HB + g.hb, (int)((g.base + g.T - 1) / runs.chunk), 0);
+  }
+  if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
+}
+
+template <int D, int HN>
+int launch_paged4(const PaParams& p, int ctas, cudaStream_t st) {
+  static std::atomic<bool> attr[64];
+  if (ensure_smem_limit(paged4_attn_kernel<D, HN>, P4<D, HN>::bytes(kMaxTokens), attr)) return TV_E_CUDA;
+  const int rc = launch_pdl(paged4_attn_kernel<D, HN>, dim3(ctas), dim3(P4<D, HN>::THREADS), P4<D, HN>::bytes(p.n), st, p);
+  return rc ? rc : launch_paged_merge(p, ctas, st);
+}
+
+}  // namespace
+}  // namespace tv
+
+using namespace tv;
+
+extern "C" {
+
+int tv_attend_paged4_workspace_size(const tv_pool4* pool, int n_q_heads, int n, size_t* bytes) {
+  PagePool q;
+  int rc = check_pool(pool, &q);
+  if (rc || (rc = check_paged_heads(n_q_heads, q.n_kv_heads, n))) return rc;
+  if (!bytes) return TV_E_ARG;
+  *bytes = paged_workspace(q.head_dim, nullptr, nullptr);
+  return TV_OK;
+}
+
+int tv_attend_paged4(const tv_pool4* pool, int layer, const tv_seqs* seqs, const int32_t* ids, int n, int n_q_heads,
+                     int window, int sinks, const tv_bf16* q, size_t q_stride, const tv_bf16* k_new, const tv_bf16* v_new,
+                     size_t kv_stride, tv_bf16* out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                     void* stream) {
+  PagePool pages;
+  PaParams p;
+  int sms;
+  int rc = check_pool(pool, &pages);
+  if (rc || (rc = fill_paged(p, pages, layer, seqs, ids, n, n_q_heads, window, sinks, q, q_stride, k_new, v_new, kv_stride,
+                             out, workspace, workspace_bytes, dev_status, &sms)))
+    return rc;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // up to 8 query heads a KV head take half of the products and registers of 16
+  if (p.G <= 8) return pages.head_dim == 128 ? launch_paged4<128, 1>(p, ctas, st) : launch_paged4<64, 1>(p, ctas, st);
+  return pages.head_dim == 128 ? launch_paged4<128, 2>(p, ctas, st) : launch_paged4<64, 2>(p, ctas, st);
+}
+
+}  // extern "C"

@@ -4,13 +4,7 @@
 //
 // What bounds it: every cached K and V byte is read once for at most 16 query
 // heads, far below the tensor cores' rate, so the kernel is built as a stream
-// over memory.  The work is the list of 64-token tiles of every (sequence, KV
-// head, block of 16 query heads) in that order, each such head block counted
-// kSegCost tiles more for what it costs to begin and end; CTA c takes an
-// equal, contiguous range of it, whatever the lengths, so one long context
-// among short ones and one sequence alone both fill every SM.  A head block cut
-// by a range border leaves unnormalised partials that paged_merge_kernel joins
-// in tile order: no atomics, the same bits every run.
+// over memory; how it is cut over the CTAs is in tv_paged_runs.cuh.
 //
 // In a CTA one warp looks up pages and issues TMA loads (a page's tokens of
 // one head are contiguous: boxes of min(page, 64) rows x 64 values, 128-byte
@@ -29,17 +23,20 @@
 // that are joined have it times a weight that may be zero: NaN.  So where an
 // element is NaN and its row's sum is not, the run's V is looked over again,
 // and the element is what the infinities and NaN there make of it.
+//
+// Through a window (WIN: tv_attend_paged_window) the tiles between the sinks
+// and the window are no work at all, and boxes that hold nothing visible are
+// not loaded; of the others the hidden tokens' scores are -inf and their V is
+// emptied in shared memory, as that of the slots past the length.
 #include <cmath>
 #include <type_traits>
 
 #include "tv_gemm.cuh"
-#include "tv_kernels.cuh"
-#include "tv_pages.cuh"
+#include "tv_paged_runs.cuh"
 
 namespace tv {
 namespace {
 
-constexpr int kTile = 64;                        // tokens of a tile
 // Tiles in flight: 192 KB of the SM at D = 128.  Even, so that a stage always
 // belongs to the same four warps: their waits then see every phase of its
 // barrier, and a parity can not name the phase before last.
@@ -48,37 +45,13 @@ static_assert(kStages % 2 == 0, "tile t: stage t mod kStages, warps 4 (t mod 2) 
 constexpr int kCompWarps = 8;
 constexpr int kCompThreads = kCompWarps * 32;
 constexpr int kPaThreads = kCompThreads + 32;
-constexpr int kRows = 16;                        // query heads of a block
 constexpr int kQueries = 8;                      // segments whose queries are loaded ahead, at most
-constexpr int kMaxTokens = 2048;                 // sequences of one call: their places fit beside the stages
-constexpr int kInfo = 640;                       // up to here their table rows and lengths do, too
 constexpr int kRedRows = 4;                      // rows joined at a time when a head block ends
 // What a head block costs besides its tiles, in tiles (its queries, its join).
 // 48 sequences of 1 to 8191 tokens, 8/2 heads, with 0, 1, 2, 4 tiles: 19.4,
 // 16.4, 15.0, 16.3 us (D = 128; 1 and 2 of 64 values: 13.9, 12.6 us).
 constexpr int kSegCost = 2;
-constexpr int kMaxCtas = 256;                    // partial slots reserved: 2 a CTA
 constexpr float kMoveLog2 = 8.f;
-
-struct PaWs {
-  int4* cut;          // [CTAs]: the head block whose first tile but not the last is the CTA's:
-                      // listed index, head block, last CTA with a tile of it; -1: none
-  float* ml;          // [2 CTAs][kRows][2]: offset and sum
-  float* o;           // [2 CTAs][kRows][D]
-};
-
-struct PaParams {
-  tv_pool pool;
-  tv_seqs seqs;
-  const int32_t* ids;
-  const __nv_bfloat16 *q, *k_new, *v_new;
-  size_t q_stride, kv_stride;
-  __nv_bfloat16* out;
-  int32_t* status;
-  PaWs ws;
-  int layer, n, Hq, G, HB;   // G query heads a KV head, in HB blocks of kRows
-  float scale_log2;
-};
 
 template <int D>
 struct PaSmem {
@@ -95,14 +68,8 @@ struct PaSmem {
   static size_t bytes(int n) { return 1024 + OFF_FIRST + (size_t)(n + 1) * 4 + (n <= kInfo ? (size_t)n * 8 : 0); }
   static_assert(kCompWarps * kRedRows * D * 4 >= kMaxSeqs / 8, "a mark for every table row");
   static_assert(1024 + OFF_FIRST + (kMaxTokens + 1) * 4 <= 232448 - 64, "shared memory of one CTA");
-  static_assert(kInfo * 12 <= kMaxTokens * 4, "rows and lengths in the places of more sequences");
 };
 
-__device__ __forceinline__ float ex2f(float x) {   // 2^x by the SFU, about 2^-22 relative, 2^-inf = 0
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -120,13 +87,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// untiled copy: 16-byte aligned addresses, a multiple of 16 bytes
-__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               :
-               : "r"(smem_u32(smem_dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
 }
 __device__ __forceinline__ void comp_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kCompThreads) : "memory"); }
 
@@ -148,24 +108,28 @@ __device__ __forceinline__ bool bar_any(bool v, int id, int n) {
   return out != 0;
 }
 
-__device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % kTile != 0); }
-
 // Rows r0 .. r0 + nr - 1 of a run's output (out) or partial result (part_o), an
 // element of which is NaN: what is not finite among the run's V, by dimension,
 // and where that is infinities of one sign, the infinity.  By 32 nw threads
 // that meet on barrier bar; kinds: D words, ml: offsets and sums of the nw
 // warps.  Out of line, since a call that has no use for it pays for its place
 // in the join (us without it, out of line, inside: 256 short sequences x 16
-// heads 49.4, 50.4, 52.2; one of 1k 9.33, 9.50, 9.65).
-template <int D>
-__device__ __noinline__ void put_infinities(const PaParams& p, int i, int s, int len, uint32_t tok, uint32_t end, int h,
+// heads 49.4, 50.4, 52.2; one of 1k 9.33, 9.50, 9.65).  WIN: at and end count the
+// tokens of the list's tiles.
+template <int D, bool WIN>
+__device__ __noinline__ void put_infinities(const PaParams& p, int i, int s, int len, Run g, uint32_t at, uint32_t end, int h,
                                             int nr, uint32_t* kinds, const float2* ml, int nw, int me, int bar,
                                             __nv_bfloat16* out, float* part_o) {
   const int ps = p.pool.page_size, c = 8 * (me % (D / 8));
   auto meet = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * nw) : "memory"); };
   for (int d = me; d < D; d += 32 * nw) kinds[d] = 0u;   // 1: NaN, 2: +inf, 4: -inf
   meet();
-  for (tok += me / (D / 8); tok < end; tok += 32 * nw / (D / 8)) {   // (unsigned: lengths near 2^31)
+  for (at += me / (D / 8); at < end; at += 32 * nw / (D / 8)) {   // (unsigned: lengths near 2^31)
+    uint32_t tok = at;
+    if constexpr (WIN) {
+      if (at >= (uint32_t)g.sink_tiles * kTile) tok += (uint32_t)g.skip * kTile;
+      if (tok >= (uint32_t)len || (tok < (uint32_t)g.lo && tok >= (uint32_t)p.sinks)) continue;
+    }
     const __nv_bfloat16* v = p.v_new + (size_t)i * p.kv_stride + (size_t)h * D;   // the new row may not be in its page yet
     if (!p.v_new || tok != (uint32_t)len - 1) {
       const int page = __ldcg(p.seqs.pages + (size_t)s * p.seqs.max_pages + tok / ps);
@@ -199,7 +163,7 @@ __device__ __noinline__ void put_infinities(const PaParams& p, int i, int s, int
   meet();
 }
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kPaThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                       const __grid_constant__ PaParams p) {
@@ -214,13 +178,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   float* s_red = reinterpret_cast<float*>(smem + L::OFF_RED);
   float2* s_ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
   uint32_t* s_mark = reinterpret_cast<uint32_t*>(smem + L::OFF_RED);
-  int* s_row = reinterpret_cast<int*>(s_first + p.n + 1);   // n <= kInfo: table row and length
-  int* s_len = s_row + p.n;
   __shared__ uint32_t s_part[kPaThreads / 32];
   __shared__ int s_bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ps = p.pool.page_size, Hkv = p.pool.n_kv_heads;
-  const bool info = p.n <= kInfo;
   // places of the query ring: short sequences need many runs ahead
   const int qrows = min(kRows, p.G), qslots = min(kQueries, 2 * kRows / qrows);
 
@@ -244,135 +205,17 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  // ---- the list of tiles: every CTA reads the same lengths and finds the same list
-  uint32_t all;
-  // of one head block, its fixed cost included; the host has seen to it that all fit 31 bits
-  auto head_tiles = [&](int len) {
-    return len > 0 ? (uint32_t)(tiles_of(len) + kSegCost) : 0u;
-  };
-  auto look = [&](int i, int& s) {   // length of listed sequence i, -1: refused
-    s = __ldg(p.ids + i);
-    return s >= 0 && s < p.seqs.max_seqs ? seq_len(p.seqs, ps, s) : -1;
-  };
-  if (p.n <= 32) {   // one warp, one barrier
-    if (warp == 0) {
-      const bool stop = status_get(p.status) != 0;
-      int s = -1 - lane, len = 0;
-      if (lane < p.n) len = look(lane, s);
-      const bool twice = __popc(__match_any_sync(0xffffffffu, lane < p.n ? s : -1 - lane)) > 1;
-      const bool bad = __any_sync(0xffffffffu, len < 0 || (p.k_new && twice));   // two new tokens, one slot
-      uint32_t x = head_tiles(len) * Hkv * p.HB;
-      const uint32_t own = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (lane < p.n) {
-        s_first[lane] = x - own;
-        s_row[lane] = s;
-        s_len[lane] = len;
-      }
-      if (lane == 31) s_first[p.n] = x;
-      if (lane == 0) {
-        if (bad && !stop) status_set(p.status, TV_E_SEQ);
-        s_bad = bad || stop;
-      }
-    }
-    __syncthreads();
-    if (s_bad) return;
-    all = s_first[p.n];
-  } else {
-    int bad = status_get(p.status) != 0;
-    const int per = (p.n + kPaThreads - 1) / kPaThreads;
-    uint32_t sum = 0;
-    for (int i = tid * per; i < min(p.n, (tid + 1) * per); ++i) {
-      int s, len = look(i, s);
-      if (len >= 0 && p.k_new && (atomicOr(&s_mark[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u) len = -1;
-      if (len < 0) bad = TV_E_SEQ;
-      if (info) {
-        s_row[i] = s;
-        s_len[i] = len;
-      }
-      s_first[i] = sum;
-      sum += head_tiles(len) * Hkv * p.HB;
-    }
-    if (bad < 0) status_set(p.status, bad);
-    uint32_t x = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s_part[warp] = x;
-    if (__syncthreads_or(bad)) return;
-    uint32_t before = x - sum;
-    all = 0;
-    for (int w = 0; w < kPaThreads / 32; ++w) {
-      if (w < warp) before += s_part[w];
-      all += s_part[w];
-    }
-    for (int i = tid * per; i < min(p.n, (tid + 1) * per); ++i) s_first[i] += before;
-    if (tid == 0) s_first[p.n] = all;
-    __syncthreads();
-  }
+  RunList<kPaThreads, kSegCost, WIN> runs(p, s_first);
+  if (!runs.build(s_mark, s_part, &s_bad)) return;
   // sequences without a token: zeros
   for (int i = blockIdx.x; i < p.n; i += gridDim.x)
     if (s_first[i + 1] == s_first[i])
       for (int e = tid; e < p.Hq * D / 8; e += kPaThreads)
         reinterpret_cast<uint4*>(p.out + (size_t)i * p.Hq * D)[e] = make_uint4(0u, 0u, 0u, 0u);
 
-  const uint32_t chunk = (all + gridDim.x - 1) / gridDim.x;
-  const uint32_t lo = min(all, chunk * blockIdx.x), hi = min(all, lo + chunk);
+  runs.range();
   if (tid == 0) p.ws.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  if (lo >= hi) return;
-  // A run: tiles [t0, t1) of one sequence and head block.  The CTA's runs in
-  // order; a range may begin or end within a head block's fixed cost.
-  struct Run {
-    int i, s, len, T;     // listed index, table row, length, tiles of the head block
-    int h, hb, t0, t1;    // KV head, block of its query heads
-    uint32_t base;        // place of tile 0
-  };
-  auto sequence = [&](Run& g, int i) {
-    g.i = i;
-    g.s = info ? s_row[i] : __ldg(p.ids + i);
-    g.len = info ? s_len[i] : __ldcg(p.seqs.lens + g.s);
-    g.T = tiles_of(g.len);
-  };
-  auto bound = [&](Run& g) { g.t1 = hi > g.base ? (int)min((uint32_t)g.T, hi - g.base) : 0; };
-  auto next_run = [&](Run& g) {   // false: there is none
-    if (g.base + g.T >= hi) return false;
-    g.base += g.T + kSegCost;
-    if (++g.hb == p.HB) {
-      g.hb = 0;
-      if (++g.h == Hkv) {
-        g.h = 0;
-        int i = g.i + 1;
-        while (s_first[i + 1] == s_first[i]) ++i;
-        sequence(g, i);
-        g.base = s_first[i] + kSegCost;
-      }
-    }
-    g.t0 = 0;
-    bound(g);
-    return g.t1 > 0;
-  };
-  auto first_run = [&](Run& g) {
-    int i = 0;   // the sequence of place lo: the last whose first place is at or before it
-    for (int b = p.n - 1; i < b;) {
-      const int mid = (i + b + 1) >> 1;
-      if (s_first[mid] <= lo) i = mid;
-      else b = mid - 1;
-    }
-    sequence(g, i);
-    const uint32_t unit = g.T + kSegCost, hh = (lo - s_first[i]) / unit;
-    g.h = (int)(hh / p.HB);
-    g.hb = (int)(hh % p.HB);
-    g.base = s_first[i] + hh * unit + kSegCost;
-    g.t0 = lo > g.base ? (int)(lo - g.base) : 0;
-    bound(g);
-    return g.t0 < g.t1 || next_run(g);
-  };
+  if (runs.lo >= runs.hi) return;
 
   if (warp == kCompWarps) {
     // ---------------- pages and loads ----------------
@@ -387,16 +230,20 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     int issued = 0, segs = 0, st = 0, qs = 0;   // tiles and queries loaded so far, their places in the rings
     uint32_t st_par = 1u, qs_par = 1u;          // of the wait before a place is used again (not in the first round)
     const int psh = 31 - __clz(ps);
+    // a box of tokens tok .. tok + R - 1 holds something that is seen
+    auto seen = [&](const Run& g, int tok) {
+      return box < nb && tok < g.len && (!WIN || tok >= g.lo - (R - 1) || tok < p.sinks);
+    };
     auto entry = [&](const Run& g, int t) {   // this lane's page of tile t, -1 past the length
-      const int tok = t * kTile + box * R;
-      return box < nb && tok < g.len ? __ldcg(p.seqs.pages + (size_t)g.s * p.seqs.max_pages + (tok >> psh)) : -1;
+      const int tok = g.tile<WIN>(t) * kTile + box * R;
+      return seen(g, tok) ? __ldcg(p.seqs.pages + (size_t)g.s * p.seqs.max_pages + (tok >> psh)) : -1;
     };
     Run g;
-    bool have = first_run(g);
+    bool have = runs.first_run(g);
     int page = have ? entry(g, g.t0) : -1;
     while (have && ok) {
       Run next = g;   // the next run's first pages are on their way before this one's tiles
-      const bool more = next_run(next);
+      const bool more = runs.next_run(next);
       const int next_page = more ? entry(next, next.t0) : -1;
       // its queries
       if (segs >= qslots) ok = __all_sync(0xffffffffu, mbar_wait(&q_free[qs], qs_par));
@@ -411,8 +258,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       if (++qs == qslots) qs = 0, qs_par ^= 1u;
       const int y0 = p.layer * p.pool.n_pages;   // the host has seen to it that a row of the pool is an int
       for (int t = g.t0; t < g.t1; ++t) {
-        const int tok = t * kTile + box * R;
-        const bool in = box < nb && tok < g.len;
+        const int tok = g.tile<WIN>(t) * kTile + box * R;
+        const bool in = seen(g, tok);
         const bool good = in && page >= 0 && page < p.pool.n_pages;
         if (in && !good) status_set(p.status, TV_E_PAGE);
         const int y = good ? (((y0 + page) * Hkv + g.h) << psh) + (tok & (ps - 1)) : 0;
@@ -454,7 +301,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   const int k_tok = 16 * sl + (lane & 7) + ((lane >> 4) << 3), k_ch = (lane >> 3) & 1;
   const int v_tok = 16 * sl + (lane & 15), v_ch = lane >> 4;
   Run g;
-  for (bool have = first_run(g); have; have = next_run(g)) {
+  for (bool have = runs.first_run(g); have; have = runs.next_run(g)) {
     const int h = g.h, r0 = g.hb * kRows;   // KV head, first query head of the block in the group
     const int nr = min(kRows, p.G - r0);
     if (g.T == 1 && (st & 1) != quad) {   // one tile, and the other four warps'
@@ -491,10 +338,17 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       uint8_t* sk = smem + at * L::STAGE;
       uint8_t* sv = sk + L::HALF;
       if (ok && !mbar_wait(&full[at], par)) ok = false;
-      const int valid = min(16, g.len - t * kTile - 16 * sl);   // this warp's tokens
+      const int tok0 = g.tile<WIN>(t) * kTile + 16 * sl;
+      int valid = min(16, g.len - tok0);   // this warp's tokens
+      int hide0 = 0, hide1 = 0;            // those from hide0 up to hide1 are hidden
+      if constexpr (WIN) {
+        hide0 = max(0, p.sinks - tok0);
+        hide1 = min(16, g.lo - tok0);
+        if (hide0 == 0 && hide1 >= valid) valid = 0;
+      }
       if (valid > 0) {
         bool wrote = false;
-        if (p.k_new && t * kTile + 16 * sl + valid == g.len) {
+        if (p.k_new && tok0 + valid == g.len) {
           // the new token: its rows into the tile and into the page
           const bool v = lane >= 16;
           const int c = lane & 15;
@@ -519,6 +373,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           }
           wrote = true;
         }
+        if (WIN && hide0 < hide1) {   // nor do hidden ones
+          for (int e = lane; e < (hide1 - hide0) * (D / 8); e += 32) {
+            const int tk = 16 * sl + hide0 + e / (D / 8), c = e % (D / 8);
+            *reinterpret_cast<uint4*>(sv + (c >> 3) * L::SLAB + swz(tk, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          wrote = true;
+        }
         __syncwarp();
         float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
         const uint32_t ka = smem_u32(sk), va = smem_u32(sv);
@@ -533,8 +394,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tk = 2 * t4 + (e & 1);
-          c0[e] = tk < valid ? c0[e] * p.scale_log2 : -INFINITY;
-          c1[e] = tk + 8 < valid ? c1[e] * p.scale_log2 : -INFINITY;
+          const bool in0 = tk < valid && (!WIN || tk < hide0 || tk >= hide1);
+          const bool in1 = tk + 8 < valid && (!WIN || tk + 8 < hide0 || tk + 8 >= hide1);
+          c0[e] = in0 ? c0[e] * p.scale_log2 : -INFINITY;
+          c1[e] = in1 ? c1[e] * p.scale_log2 : -INFINITY;
         }
         float x0 = fmaxf(fmaxf(c0[0], c0[1]), fmaxf(c1[0], c1[1])), x1 = fmaxf(fmaxf(c0[2], c0[3]), fmaxf(c1[2], c1[3]));
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
@@ -665,7 +528,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
       const int bar = NW == kCompWarps ? 1 : 2 + quad;
       if (bar_any(lost, bar, 32 * NW))
-        put_infinities<D>(p, g.i, g.s, g.len, (uint32_t)g.t0 * kTile, g.t1 == g.T ? g.len : (uint32_t)g.t1 * kTile, h, nr,
+        put_infinities<D, WIN>(p, g.i, g.s, g.len, g, (uint32_t)g.t0 * kTile,
+                          !WIN && g.t1 == g.T ? g.len : (uint32_t)g.t1 * kTile, h, nr,
                           reinterpret_cast<uint32_t*>(s_red + w0 * kRedRows * D), s_ml + w0 * kRows, NW, me, bar,
                           whole ? p.out + ((size_t)g.i * p.Hq + h * p.G + r0) * D : nullptr, p.ws.o + slot * kRows * D);
     };
@@ -673,7 +537,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     else join(std::integral_constant<int, kCompWarps / 2>{});
     if (++qs == qslots) qs = 0, qs_par ^= 1u;
     if (tid == 0 && g.t0 == 0 && !whole)   // the CTA's last run
-      p.ws.cut[blockIdx.x] = make_int4(g.i, g.h * p.HB + g.hb, (int)((g.base + g.T - 1) / chunk), 0);
+      p.ws.cut[blockIdx.x] = make_int4(g.i, g.h * p.HB + g.hb, (int)((g.base + g.T - 1) / runs.chunk), 0);
   }
   if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
 }
@@ -757,7 +621,38 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PaPara
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-size_t pa_ws(int D, PaWs* ws, uint8_t* base) {
+template <int D, bool WIN>
+int launch_paged(const PaParams& p, int ctas, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  const int rows = p.pool.n_layers * p.pool.n_pages * p.pool.n_kv_heads * p.pool.page_size;   // checked to fit
+  const int R = p.pool.page_size < kTile ? p.pool.page_size : kTile;
+  int rc = make_tmap_bf16(&mk, p.pool.k, D, rows, 64, R);
+  if (rc || (rc = make_tmap_bf16(&mv, p.pool.v, D, rows, 64, R))) return rc;
+  static std::atomic<bool> attr[64];
+  if (ensure_smem_limit(paged_attn_kernel<D, WIN>, PaSmem<D>::bytes(kMaxTokens), attr)) return TV_E_CUDA;
+  rc = launch_pdl(paged_attn_kernel<D, WIN>, dim3(ctas), dim3(kPaThreads), PaSmem<D>::bytes(p.n), st, mk, mv, p);
+  return rc ? rc : launch_paged_merge(p, ctas, st);
+}
+
+int attend_paged(bool win, const tv_pool* pool, int layer, const tv_seqs* seqs, const int32_t* ids, int n, int n_q_heads,
+                 int window, int sinks, const tv_bf16* q, size_t q_stride, const tv_bf16* k_new, const tv_bf16* v_new,
+                 size_t kv_stride, tv_bf16* out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                 void* stream) {
+  PaParams p;
+  int sms;
+  int rc = check_pool(pool);
+  if (rc || (rc = fill_paged(p, *pool, layer, seqs, ids, n, n_q_heads, window, sinks, q, q_stride, k_new, v_new, kv_stride,
+                             out, workspace, workspace_bytes, dev_status, &sms)))
+    return rc;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (win) return pool->head_dim == 128 ? launch_paged<128, true>(p, ctas, st) : launch_paged<64, true>(p, ctas, st);
+  return pool->head_dim == 128 ? launch_paged<128, false>(p, ctas, st) : launch_paged<64, false>(p, ctas, st);
+}
+
+}  // namespace
+
+size_t paged_workspace(int D, PaWs* ws, uint8_t* base) {
   const size_t cut = align256((size_t)kMaxCtas * sizeof(int4)), ml = align256((size_t)2 * kMaxCtas * kRows * 2 * 4);
   const size_t o = align256((size_t)2 * kMaxCtas * kRows * D * 4);
   if (ws) {
@@ -768,66 +663,35 @@ size_t pa_ws(int D, PaWs* ws, uint8_t* base) {
   return cut + ml + o;
 }
 
-int check_tokens(int n) { return n < 1 ? TV_E_ARG : (n > kMaxTokens ? TV_E_UNSUPPORTED : TV_OK); }
-
-int check_heads(int n_q_heads, int n_kv_heads) {
+int check_paged_heads(int n_q_heads, int n_kv_heads, int n) {
   if (n_q_heads < 1) return TV_E_ARG;
-  return n_q_heads % n_kv_heads != 0 || n_q_heads > 65536 ? TV_E_UNSUPPORTED : TV_OK;
+  if (n_q_heads % n_kv_heads != 0 || n_q_heads > 65536) return TV_E_UNSUPPORTED;
+  return n < 1 ? TV_E_ARG : (n > kMaxTokens ? TV_E_UNSUPPORTED : TV_OK);
 }
 
-template <int D>
-int launch_paged(const PaParams& p, int sms, cudaStream_t st) {
-  CUtensorMap mk, mv;
-  const int rows = p.pool.n_layers * p.pool.n_pages * p.pool.n_kv_heads * p.pool.page_size;   // checked to fit
-  const int R = p.pool.page_size < kTile ? p.pool.page_size : kTile;
-  int rc = make_tmap_bf16(&mk, p.pool.k, D, rows, 64, R);
-  if (rc || (rc = make_tmap_bf16(&mv, p.pool.v, D, rows, 64, R))) return rc;
-  static std::atomic<bool> attr[64];
-  if (ensure_smem_limit(paged_attn_kernel<D>, PaSmem<D>::bytes(kMaxTokens), attr)) return TV_E_CUDA;
-  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  rc = launch_pdl(paged_attn_kernel<D>, dim3(ctas), dim3(kPaThreads), PaSmem<D>::bytes(p.n), st, mk, mv, p);
+int fill_paged(PaParams& p, const tv_pool& pool, int layer, const tv_seqs* seqs, const int32_t* ids, int n, int n_q_heads,
+               int window, int sinks, const tv_bf16* q, size_t q_stride, const tv_bf16* k_new, const tv_bf16* v_new,
+               size_t kv_stride, tv_bf16* out, void* workspace, size_t workspace_bytes, int32_t* dev_status, int* sms) {
+  int rc = check_seqs(seqs, &pool);
   if (rc) return rc;
-  return launch_pdl(paged_merge_kernel<D>, dim3(ctas), dim3(kMergeThreads), 0, st, p);
-}
-
-}  // namespace
-}  // namespace tv
-
-using namespace tv;
-
-extern "C" {
-
-int tv_attend_paged_workspace_size(const tv_pool* pool, int n_q_heads, int n, size_t* bytes) {
-  int rc = check_pool(pool);
-  if (rc || (rc = check_heads(n_q_heads, pool->n_kv_heads)) || (rc = check_tokens(n))) return rc;
-  if (!bytes) return TV_E_ARG;
-  *bytes = pa_ws(pool->head_dim, nullptr, nullptr);
-  return TV_OK;
-}
-
-int tv_attend_paged(const tv_pool* pool, int layer, const tv_seqs* seqs, const int32_t* ids, int n, int n_q_heads,
-                    const tv_bf16* q, size_t q_stride, const tv_bf16* k_new, const tv_bf16* v_new, size_t kv_stride,
-                    tv_bf16* out, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
-  int rc = check_pool(pool);
-  if (rc || (rc = check_seqs(seqs, pool))) return rc;
-  if (!ids || !q || !out || !dev_status || !k_new != !v_new || layer < 0 || layer >= pool->n_layers) return TV_E_ARG;
-  if ((rc = check_heads(n_q_heads, pool->n_kv_heads)) || (rc = check_tokens(n))) return rc;
-  const size_t D = pool->head_dim;
+  if (!ids || !q || !out || !dev_status || !k_new != !v_new || layer < 0 || layer >= pool.n_layers) return TV_E_ARG;
+  if (window < 1 || sinks < 0) return TV_E_ARG;
+  if ((rc = check_paged_heads(n_q_heads, pool.n_kv_heads, n))) return rc;
+  const size_t D = pool.head_dim;
   if (!aligned16(q) || !aligned16(out) || q_stride % 8 != 0 || q_stride < n_q_heads * D) return TV_E_ARG;
-  if (k_new && (!aligned16(k_new) || !aligned16(v_new) || kv_stride % 8 != 0 || kv_stride < pool->n_kv_heads * D))
+  if (k_new && (!aligned16(k_new) || !aligned16(v_new) || kv_stride % 8 != 0 || kv_stride < pool.n_kv_heads * D))
     return TV_E_ARG;
-  PaParams p;
-  p.G = n_q_heads / pool->n_kv_heads;
+  p.G = n_q_heads / pool.n_kv_heads;
   p.HB = (p.G + kRows - 1) / kRows;
   // the places of n sequences of the longest kind
   const unsigned long long most =
-      (((unsigned long long)seqs->max_pages * pool->page_size + kTile - 1) / kTile + 4) * pool->n_kv_heads * p.HB;
+      (((unsigned long long)seqs->max_pages * pool.page_size + kTile - 1) / kTile + 4) * pool.n_kv_heads * p.HB;
   if (most > 0x7fffffffull / (unsigned)n) return TV_E_UNSUPPORTED;
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  if (!workspace || !aligned16(workspace) || workspace_bytes < pa_ws(pool->head_dim, &p.ws, base)) return TV_E_WORKSPACE;
-  const int sms = num_sms();
-  if (sms <= 0) return TV_E_CUDA;
-  p.pool = *pool;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < paged_workspace(pool.head_dim, &p.ws, base)) return TV_E_WORKSPACE;
+  *sms = num_sms();
+  if (*sms <= 0) return TV_E_CUDA;
+  p.pool = pool;
   p.seqs = *seqs;
   p.ids = ids;
   p.q = reinterpret_cast<const __nv_bfloat16*>(q);
@@ -840,9 +704,44 @@ int tv_attend_paged(const tv_pool* pool, int layer, const tv_seqs* seqs, const i
   p.layer = layer;
   p.n = n;
   p.Hq = n_q_heads;
-  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)pool->head_dim));
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return pool->head_dim == 128 ? launch_paged<128>(p, sms, st) : launch_paged<64>(p, sms, st);
+  p.window = window;
+  p.sinks = sinks;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)pool.head_dim));
+  return TV_OK;
+}
+
+int launch_paged_merge(const PaParams& p, int ctas, cudaStream_t st) {
+  return p.pool.head_dim == 128 ? launch_pdl(paged_merge_kernel<128>, dim3(ctas), dim3(kMergeThreads), 0, st, p)
+                                : launch_pdl(paged_merge_kernel<64>, dim3(ctas), dim3(kMergeThreads), 0, st, p);
+}
+
+}  // namespace tv
+
+using namespace tv;
+
+extern "C" {
+
+int tv_attend_paged_workspace_size(const tv_pool* pool, int n_q_heads, int n, size_t* bytes) {
+  int rc = check_pool(pool);
+  if (rc || (rc = check_paged_heads(n_q_heads, pool->n_kv_heads, n))) return rc;
+  if (!bytes) return TV_E_ARG;
+  *bytes = paged_workspace(pool->head_dim, nullptr, nullptr);
+  return TV_OK;
+}
+
+int tv_attend_paged(const tv_pool* pool, int layer, const tv_seqs* seqs, const int32_t* ids, int n, int n_q_heads,
+                    const tv_bf16* q, size_t q_stride, const tv_bf16* k_new, const tv_bf16* v_new, size_t kv_stride,
+                    tv_bf16* out, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  return attend_paged(false, pool, layer, seqs, ids, n, n_q_heads, 0x7fffffff, 0, q, q_stride, k_new, v_new, kv_stride,
+                      out, workspace, workspace_bytes, dev_status, stream);
+}
+
+int tv_attend_paged_window(const tv_pool* pool, int layer, const tv_seqs* seqs, const int32_t* ids, int n, int n_q_heads,
+                           int window, int sinks, const tv_bf16* q, size_t q_stride, const tv_bf16* k_new,
+                           const tv_bf16* v_new, size_t kv_stride, tv_bf16* out, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_status, void* stream) {
+  return attend_paged(true, pool, layer, seqs, ids, n, n_q_heads, window, sinks, q, q_stride, k_new, v_new, kv_stride, out,
+                      workspace, workspace_bytes, dev_status, stream);
 }
 
 }  // extern "C"

@@ -16,16 +16,8 @@
 namespace tv {
 namespace {
 
-constexpr int kListThreads = 256;    // block of the kernels that move rows and pages
 constexpr int kSeqThreads = 1024;    // of those that follow a sequence's pages: few rounds of dependent loads
 constexpr int kPlanThreads = 1024;   // the one block that allocates
-
-// what a block found wrong with its list; the lowest bit is reported, so that
-// the code does not depend on the order of the threads
-constexpr uint32_t kBadSeq = 1u, kBadCapacity = 2u, kBadPage = 4u;
-__device__ __forceinline__ int bad_code(uint32_t bad) {
-  return bad & kBadSeq ? TV_E_SEQ : (bad & kBadCapacity ? TV_E_CAPACITY : TV_E_PAGE);
-}
 
 // ---- releasing and forking ---------------------------------------------------
 // Releasing (FORK = false: a = ids, b = keep) or forking (a = src, b = dst): one
@@ -384,8 +376,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(tv_pool pool,
 }
 
 // One page of one layer's K or V is one contiguous block of memory.  bytes: a
-// multiple of 2048 (16 tokens of 64 bf16 values); eight 16-byte loads a thread
-// are in flight before the first store.
+// multiple of 16 (16 tokens are 2048 bytes or more in bf16, 576 or more in 4
+// bits); eight 16-byte loads a thread are in flight before the first store.
 __device__ __forceinline__ void copy_block(const uint8_t* from, uint8_t* to, uint32_t bytes) {
   const uint4* a = reinterpret_cast<const uint4*>(from);
   uint4* b = reinterpret_cast<uint4*>(to);
@@ -404,9 +396,9 @@ __device__ __forceinline__ void copy_block(const uint8_t* from, uint8_t* to, uin
     }
   }
 }
-__device__ __forceinline__ void copy_page(const tv_pool& pool, int layer, bool is_v, int src, int dst) {
+__device__ __forceinline__ void copy_page(const PagePool& pool, int layer, bool is_v, int src, int dst) {
   constexpr size_t kPiece = size_t(1) << 31;   // a page of very many heads passes 2^32 bytes
-  const size_t bytes = (size_t)pool.n_kv_heads * pool.page_size * pool.head_dim * 2;
+  const size_t bytes = (size_t)pool.n_kv_heads * pool.page_size * pool.row_bytes;
   uint8_t* base = reinterpret_cast<uint8_t*>(is_v ? pool.v : pool.k) + (size_t)layer * pool.n_pages * bytes;
   for (size_t at = 0; at < bytes; at += kPiece)
     copy_block(base + (size_t)src * bytes + at, base + (size_t)dst * bytes + at,
@@ -414,7 +406,7 @@ __device__ __forceinline__ void copy_page(const tv_pool& pool, int layer, bool i
 }
 
 // grid (listed sequences, 2 layers): the copies of extend_plan_kernel
-__global__ void __launch_bounds__(kListThreads) extend_copy_kernel(tv_pool pool, ExtendWs ws, int32_t* status) {
+__global__ void __launch_bounds__(kListThreads) extend_copy_kernel(PagePool pool, ExtendWs ws, int32_t* status) {
   pdl_wait();
   pdl_trigger();
   if (block_skip(status)) return;
@@ -505,7 +497,7 @@ __global__ void __launch_bounds__(kListThreads) compact_remap_kernel(tv_pool poo
 
 // The moves (no target is a source: targets lie below `used`, sources past it),
 // the tables, then the counts of the moved pages.
-__global__ void __launch_bounds__(kListThreads) compact_move_kernel(tv_pool pool, tv_seqs t, CompactWs ws,
+__global__ void __launch_bounds__(kListThreads) compact_move_kernel(PagePool pool, tv_seqs t, CompactWs ws,
                                                                     const int32_t* remap, int32_t* status) {
   pdl_wait();
   pdl_trigger();
@@ -529,17 +521,15 @@ __global__ void __launch_bounds__(kListThreads) compact_move_kernel(tv_pool pool
 }
 
 // ---- rows into pages and out of them ---------------------------------------------
-// Row r of listed sequence i (starts[i] <= r < starts[i + 1]) is token
-// pos[i] + r - starts[i].  One warp per row; a row's K and V are each n_kv_heads
-// pieces of head_dim values, contiguous per head on both sides.
+// One warp per row; a row's K and V are each n_kv_heads pieces of head_dim
+// values, contiguous per head on both sides.
 //
 // A bad page entry leaves out its rows alone.  Blocks that have yet to start
 // would take the status it is reported by for an earlier call's and leave out
 // theirs as well, so a call of more than one block reports by a kernel of its
 // own behind the moves (rows_report_kernel).
 template <bool WRITE>
-__global__ void __launch_bounds__(kListThreads) rows_kernel(tv_pool pool, int layer, tv_seqs t, const int32_t* ids,
-                                                            const int32_t* pos, const int32_t* starts, int n, int rows,
+__global__ void __launch_bounds__(kListThreads) rows_kernel(tv_pool pool, int layer, tv_seqs t, RowList list,
                                                             __nv_bfloat16* k, __nv_bfloat16* v, size_t row_stride,
                                                             size_t head_stride, int32_t* status) {
   __shared__ int s_start[kMaxListed + 1];
@@ -549,34 +539,8 @@ __global__ void __launch_bounds__(kListThreads) rows_kernel(tv_pool pool, int la
   pdl_trigger();
   const int tid = threadIdx.x, ps = pool.page_size;
   if (block_skip(status)) return;
-  // every block checks the whole list before it moves a row
-  if (tid == 0) s_bad = 0u;
-  if (WRITE)
-    for (int i = tid; i < (t.max_seqs + 31) / 32; i += kListThreads) s_mark[i] = 0u;
-  __syncthreads();
-  for (int i = tid; i <= n; i += kListThreads) {
-    const int a = starts[i];
-    s_start[i] = a;
-    uint32_t bad = a < 0 || a > rows ? kBadSeq : 0u;
-    if (i < n) {
-      const int b = starts[i + 1], s = ids[i], at = pos[i];
-      if (b < a || s < 0 || s >= t.max_seqs || at < 0) {
-        bad = kBadSeq;
-      } else {
-        if (WRITE && (atomicOr(&s_mark[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u) bad = kBadSeq;
-        const int len = seq_len(t, ps, s);
-        if (len < 0) bad = kBadSeq;
-        else if ((long long)at + (b - a) > len) bad |= kBadCapacity;
-      }
-    }
-    if (bad) atomicOr(&s_bad, bad);
-  }
-  __syncthreads();
-  if (s_bad) {
-    if (tid == 0) status_set(status, bad_code(s_bad));
-    return;
-  }
-  const int first = s_start[0], total = s_start[n];
+  if (!look_over<WRITE>(t, ps, list, s_start, s_mark, &s_bad, status)) return;
+  const int first = s_start[0], total = s_start[list.n];
   const int lane = tid & 31;
   const int pieces = pool.n_kv_heads * (pool.head_dim / 8);   // 16-byte pieces of a row's K
   const int dsh = pool.head_dim == 128 ? 4 : 3;
@@ -585,14 +549,9 @@ __global__ void __launch_bounds__(kListThreads) rows_kernel(tv_pool pool, int la
   // (unsigned: a count near 2^31 and a stride do not wrap)
   for (uint32_t r = first + blockIdx.x * (kListThreads / 32) + (tid >> 5); r < (uint32_t)total;
        r += gridDim.x * (kListThreads / 32)) {
-    int lo = 0, hi = n - 1;   // the sequence of row r
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((uint32_t)s_start[mid] <= r) lo = mid;
-      else hi = mid - 1;
-    }
-    const int at = __ldg(pos + lo) + (int)r - s_start[lo];
-    const int p = __ldcg(t.pages + (size_t)__ldg(ids + lo) * t.max_pages + at / ps);
+    const int i = sequence_of(s_start, list.n, r);
+    const int at = __ldg(list.pos + i) + (int)r - s_start[i];
+    const int p = __ldcg(t.pages + (size_t)__ldg(list.ids + i) * t.max_pages + at / ps);
     if (p < 0 || p >= pool.n_pages) {
       if (gridDim.x == 1 && lane == 0) status_set(status, TV_E_PAGE);
       continue;
@@ -630,13 +589,12 @@ __global__ void __launch_bounds__(kListThreads) rows_kernel(tv_pool pool, int la
 // triggers behind its own wait, so what it reads is there when this kernel
 // starts.  Lists that it refuses reach no entry here that they name wrongly,
 // and have set the status.
-__global__ void __launch_bounds__(kListThreads) rows_report_kernel(int n_pages, int ps, tv_seqs t, const int32_t* ids,
-                                                                   const int32_t* pos, const int32_t* starts, int n,
-                                                                   int rows, int32_t* status) {
+__global__ void __launch_bounds__(kListThreads) rows_report_kernel(int n_pages, int ps, tv_seqs t, RowList l,
+                                                                   int32_t* status) {
   bool bad = false;
-  for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    const int a = __ldcg(starts + i), b = __ldcg(starts + i + 1), s = __ldcg(ids + i), at = __ldcg(pos + i);
-    if (a < 0 || b <= a || b > rows || s < 0 || s >= t.max_seqs || at < 0) continue;
+  for (int i = blockIdx.x; i < l.n; i += gridDim.x) {
+    const int a = __ldcg(l.starts + i), b = __ldcg(l.starts + i + 1), s = __ldcg(l.ids + i), at = __ldcg(l.pos + i);
+    if (a < 0 || b <= a || b > l.rows || s < 0 || s >= t.max_seqs || at < 0) continue;
     const int len = seq_len(t, ps, s);
     if ((long long)at + (b - a) > len) continue;
     const int last = (at + (b - a) - 1) / ps;
@@ -652,36 +610,124 @@ __global__ void __launch_bounds__(kListThreads) rows_report_kernel(int n_pages, 
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// extend: the free list and the pairs; compact: two page lists and two counts
-size_t pages_ws_bytes(const tv_pool& p) {
-  return align256((size_t)p.n_pages * 4) * 2 + align256(2 * kMaxListed * 4);
-}
-
-int rows_call(bool write, const tv_pool* pool, int layer, const tv_seqs* seqs, const int32_t* ids, const int32_t* pos,
-              const int32_t* starts, int n, int rows, void* k, void* v, size_t row_stride, size_t head_stride,
-              int32_t* status, void* stream) {
+int rows_call(bool write, const tv_pool* pool, int layer, const tv_seqs* seqs, const RowList& l, void* k, void* v,
+              size_t row_stride, size_t head_stride, int32_t* status, void* stream) {
   int rc = check_pool(pool);
-  if (rc || (rc = check_seqs(seqs, pool))) return rc;
-  if (!ids || !pos || !starts || !k || !v || !status || layer < 0 || layer >= pool->n_layers || rows < 0) return TV_E_ARG;
-  if ((rc = check_listed(n))) return rc;
-  // 16-byte pieces on both sides
-  if (!aligned16(k) || !aligned16(v) || row_stride % 8 != 0 || head_stride % 8 != 0) return TV_E_ARG;
+  if (rc || (rc = check_rows(*pool, layer, seqs, l, k, v, row_stride, head_stride, status))) return rc;
   const int sms = num_sms();
   if (sms <= 0) return TV_E_CUDA;
   const int per = kListThreads / 32;
-  const int want = (rows + per - 1) / per, most = sms * 8;
+  const int want = (l.rows + per - 1) / per, most = sms * 8;
   const dim3 grid(want < 1 ? 1 : (want < most ? want : most));
   __nv_bfloat16 *kp = static_cast<__nv_bfloat16*>(k), *vp = static_cast<__nv_bfloat16*>(v);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t smem = write ? (size_t)((seqs->max_seqs + 31) / 32) * 4 : 0;
   rc = launch_pdl(write ? rows_kernel<true> : rows_kernel<false>, grid, dim3(kListThreads), smem, st, *pool, layer, *seqs,
-                  ids, pos, starts, n, rows, kp, vp, row_stride, head_stride, status);
+                  l, kp, vp, row_stride, head_stride, status);
   if (rc || grid.x == 1) return rc;
-  return launch_pdl(rows_report_kernel, dim3(n < sms ? n : sms), dim3(kListThreads), 0, st, pool->n_pages, pool->page_size,
-                    *seqs, ids, pos, starts, n, rows, status);
+  return launch_rows_report(*pool, *seqs, l, sms, status, st);
 }
 
 }  // namespace
+
+int check_rows(const tv_pool& pool, int layer, const tv_seqs* seqs, const RowList& l, const void* k, const void* v,
+               size_t row_stride, size_t head_stride, const int32_t* status) {
+  int rc = check_seqs(seqs, &pool);
+  if (rc) return rc;
+  if (!l.ids || !l.pos || !l.starts || !k || !v || !status || layer < 0 || layer >= pool.n_layers || l.rows < 0) return TV_E_ARG;
+  if ((rc = check_listed(l.n))) return rc;
+  // 16-byte pieces on both sides
+  return !aligned16(k) || !aligned16(v) || row_stride % 8 != 0 || head_stride % 8 != 0 ? TV_E_ARG : TV_OK;
+}
+
+int launch_rows_report(const tv_pool& pool, const tv_seqs& seqs, const RowList& l, int sms, int32_t* status,
+                       cudaStream_t st) {
+  return launch_pdl(rows_report_kernel, dim3(l.n < sms ? l.n : sms), dim3(kListThreads), 0, st, pool.n_pages,
+                    pool.page_size, seqs, l, status);
+}
+
+// extend: the free list and the pairs; compact: two page lists and two counts
+size_t pages_ws_bytes(const tv_pool& p) {
+  return align256((size_t)p.n_pages * 4) * 2 + align256(2 * kMaxListed * 4);
+}
+
+int pages_release(const PagePool& pool, const tv_seqs* seqs, const int32_t* ids, const int32_t* keep, int n,
+                  int32_t* dev_status, void* stream) {
+  int rc = check_seqs(seqs, &pool);
+  if (rc) return rc;
+  if (!ids || !keep || !dev_status) return TV_E_ARG;
+  if ((rc = check_listed(n))) return rc;
+  const tv_pool p = pool;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (one_block(*seqs, n))
+    return launch_pdl(list_block_kernel<false>, dim3(1), dim3(kBlockThreads), 0, st, p, *seqs, ids, keep, n, dev_status);
+  rc = launch_pdl(list_check_kernel<false>, dim3(n), dim3(kSeqThreads), 0, st, p, *seqs, ids, keep, n, dev_status);
+  if (rc) return rc;
+  return launch_pdl(list_apply_kernel<false>, dim3(n), dim3(kSeqThreads), 0, st, p, *seqs, ids, keep, n, dev_status);
+}
+
+int pages_fork(const PagePool& pool, const tv_seqs* seqs, const int32_t* src, const int32_t* dst, int n,
+               int32_t* dev_status, void* stream) {
+  int rc = check_seqs(seqs, &pool);
+  if (rc) return rc;
+  if (!src || !dst || !dev_status) return TV_E_ARG;
+  if ((rc = check_listed(n))) return rc;
+  const tv_pool p = pool;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (one_block(*seqs, n))
+    return launch_pdl(list_block_kernel<true>, dim3(1), dim3(kBlockThreads), 0, st, p, *seqs, src, dst, n, dev_status);
+  rc = launch_pdl(list_check_kernel<true>, dim3(n), dim3(kSeqThreads), 0, st, p, *seqs, src, dst, n, dev_status);
+  if (rc) return rc;
+  return launch_pdl(list_apply_kernel<true>, dim3(n), dim3(kSeqThreads), 0, st, p, *seqs, src, dst, n, dev_status);
+}
+
+int pages_extend(const PagePool& pool, const tv_seqs* seqs, const int32_t* ids, const int32_t* add, int n,
+                 void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  int rc = check_seqs(seqs, &pool);
+  if (rc) return rc;
+  if (!ids || !add || !dev_status) return TV_E_ARG;
+  if ((rc = check_listed(n))) return rc;
+  if (!workspace || workspace_bytes < pages_ws_bytes(pool) || !aligned16(workspace)) return TV_E_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  ExtendWs ws;
+  ws.free_list = reinterpret_cast<int32_t*>(w);
+  ws.pair = reinterpret_cast<int32_t*>(w + 2 * align256((size_t)pool.n_pages * 4));
+  static std::atomic<bool> attr[64];
+  if (ensure_smem_limit(extend_plan_kernel, ExtendSmem::bytes(kMaxListed, kMaxSeqs), attr)) return TV_E_CUDA;
+  rc = launch_pdl(extend_plan_kernel, dim3(1), dim3(kPlanThreads), ExtendSmem::bytes(n, seqs->max_seqs), st,
+                  static_cast<const tv_pool&>(pool), *seqs, ids, add, n, ws, dev_status);
+  if (rc) return rc;
+  const int y = 2 * pool.n_layers < 65535 ? 2 * pool.n_layers : 65535;
+  return launch_pdl(extend_copy_kernel, dim3(n, y), dim3(kListThreads), 0, st, pool, ws, dev_status);
+}
+
+int pages_compact(const PagePool& pool, const tv_seqs* seqs, int32_t* remap, int32_t* n_used, void* workspace,
+                  size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  int rc = check_seqs(seqs, &pool);
+  if (rc) return rc;
+  if (!remap || !n_used || !dev_status) return TV_E_ARG;
+  if (!workspace || workspace_bytes < pages_ws_bytes(pool) || !aligned16(workspace)) return TV_E_WORKSPACE;
+  const int sms = num_sms();
+  if (sms <= 0) return TV_E_CUDA;
+  const tv_pool p = pool;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  CompactWs ws;
+  ws.src = reinterpret_cast<int32_t*>(w);
+  ws.dst = reinterpret_cast<int32_t*>(w + align256((size_t)pool.n_pages * 4));
+  ws.moves = reinterpret_cast<int32_t*>(w + 2 * align256((size_t)pool.n_pages * 4));
+  const int checks = seqs->max_seqs < sms - 1 ? seqs->max_seqs : sms - 1;
+  rc = launch_pdl(compact_plan_kernel, dim3(1 + checks), dim3(kPlanThreads), 0, st, p, *seqs, ws, dev_status);
+  if (rc) return rc;
+  const int rb = (pool.n_pages + kListThreads - 1) / kListThreads;
+  rc = launch_pdl(compact_remap_kernel, dim3(rb < sms ? rb : sms), dim3(kListThreads), 0, st, p, ws, remap, n_used,
+                  dev_status);
+  if (rc) return rc;
+  return launch_pdl(compact_move_kernel, dim3(sms * 8), dim3(kListThreads), 0, st, pool, *seqs, ws,
+                    (const int32_t*)remap, dev_status);
+}
+
 }  // namespace tv
 
 using namespace tv;
@@ -698,89 +744,40 @@ int tv_pages_workspace_size(const tv_pool* pool, const tv_seqs* seqs, size_t* by
 
 int tv_pages_release(const tv_pool* pool, const tv_seqs* seqs, const int32_t* ids, const int32_t* keep, int n,
                      int32_t* dev_status, void* stream) {
-  int rc = check_pool(pool);
-  if (rc || (rc = check_seqs(seqs, pool))) return rc;
-  if (!ids || !keep || !dev_status) return TV_E_ARG;
-  if ((rc = check_listed(n))) return rc;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (one_block(*seqs, n))
-    return launch_pdl(list_block_kernel<false>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
-  rc = launch_pdl(list_check_kernel<false>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
-  if (rc) return rc;
-  return launch_pdl(list_apply_kernel<false>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, ids, keep, n, dev_status);
+  const int rc = check_pool(pool);
+  return rc ? rc : pages_release(page_pool(*pool), seqs, ids, keep, n, dev_status, stream);
 }
 
 int tv_pages_fork(const tv_pool* pool, const tv_seqs* seqs, const int32_t* src, const int32_t* dst, int n,
                   int32_t* dev_status, void* stream) {
-  int rc = check_pool(pool);
-  if (rc || (rc = check_seqs(seqs, pool))) return rc;
-  if (!src || !dst || !dev_status) return TV_E_ARG;
-  if ((rc = check_listed(n))) return rc;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (one_block(*seqs, n))
-    return launch_pdl(list_block_kernel<true>, dim3(1), dim3(kBlockThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
-  rc = launch_pdl(list_check_kernel<true>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
-  if (rc) return rc;
-  return launch_pdl(list_apply_kernel<true>, dim3(n), dim3(kSeqThreads), 0, st, *pool, *seqs, src, dst, n, dev_status);
+  const int rc = check_pool(pool);
+  return rc ? rc : pages_fork(page_pool(*pool), seqs, src, dst, n, dev_status, stream);
 }
 
 int tv_pages_extend(const tv_pool* pool, const tv_seqs* seqs, const int32_t* ids, const int32_t* add, int n,
                     void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
-  int rc = check_pool(pool);
-  if (rc || (rc = check_seqs(seqs, pool))) return rc;
-  if (!ids || !add || !dev_status) return TV_E_ARG;
-  if ((rc = check_listed(n))) return rc;
-  if (!workspace || workspace_bytes < pages_ws_bytes(*pool) || !aligned16(workspace)) return TV_E_WORKSPACE;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  uint8_t* w = static_cast<uint8_t*>(workspace);
-  ExtendWs ws;
-  ws.free_list = reinterpret_cast<int32_t*>(w);
-  ws.pair = reinterpret_cast<int32_t*>(w + 2 * align256((size_t)pool->n_pages * 4));
-  static std::atomic<bool> attr[64];
-  if (ensure_smem_limit(extend_plan_kernel, ExtendSmem::bytes(kMaxListed, kMaxSeqs), attr)) return TV_E_CUDA;
-  rc = launch_pdl(extend_plan_kernel, dim3(1), dim3(kPlanThreads), ExtendSmem::bytes(n, seqs->max_seqs), st, *pool, *seqs,
-                  ids, add, n, ws, dev_status);
-  if (rc) return rc;
-  const int y = 2 * pool->n_layers < 65535 ? 2 * pool->n_layers : 65535;
-  return launch_pdl(extend_copy_kernel, dim3(n, y), dim3(kListThreads), 0, st, *pool, ws, dev_status);
+  const int rc = check_pool(pool);
+  return rc ? rc : pages_extend(page_pool(*pool), seqs, ids, add, n, workspace, workspace_bytes, dev_status, stream);
 }
 
 int tv_pages_compact(const tv_pool* pool, const tv_seqs* seqs, int32_t* remap, int32_t* n_used, void* workspace,
                      size_t workspace_bytes, int32_t* dev_status, void* stream) {
-  int rc = check_pool(pool);
-  if (rc || (rc = check_seqs(seqs, pool))) return rc;
-  if (!remap || !n_used || !dev_status) return TV_E_ARG;
-  if (!workspace || workspace_bytes < pages_ws_bytes(*pool) || !aligned16(workspace)) return TV_E_WORKSPACE;
-  const int sms = num_sms();
-  if (sms <= 0) return TV_E_CUDA;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  uint8_t* w = static_cast<uint8_t*>(workspace);
-  CompactWs ws;
-  ws.src = reinterpret_cast<int32_t*>(w);
-  ws.dst = reinterpret_cast<int32_t*>(w + align256((size_t)pool->n_pages * 4));
-  ws.moves = reinterpret_cast<int32_t*>(w + 2 * align256((size_t)pool->n_pages * 4));
-  const int checks = seqs->max_seqs < sms - 1 ? seqs->max_seqs : sms - 1;
-  rc = launch_pdl(compact_plan_kernel, dim3(1 + checks), dim3(kPlanThreads), 0, st, *pool, *seqs, ws, dev_status);
-  if (rc) return rc;
-  const int rb = (pool->n_pages + kListThreads - 1) / kListThreads;
-  rc = launch_pdl(compact_remap_kernel, dim3(rb < sms ? rb : sms), dim3(kListThreads), 0, st, *pool, ws, remap, n_used,
-                  dev_status);
-  if (rc) return rc;
-  return launch_pdl(compact_move_kernel, dim3(sms * 8), dim3(kListThreads), 0, st, *pool, *seqs, ws,
-                    (const int32_t*)remap, dev_status);
+  const int rc = check_pool(pool);
+  return rc ? rc : pages_compact(page_pool(*pool), seqs, remap, n_used, workspace, workspace_bytes, dev_status, stream);
 }
 
 int tv_pages_write(const tv_pool* pool, int layer, const tv_seqs* seqs, const int32_t* ids, const int32_t* pos,
                    const int32_t* starts, int n, int rows, const tv_bf16* k, const tv_bf16* v, size_t row_stride,
                    size_t head_stride, int32_t* dev_status, void* stream) {
-  return rows_call(true, pool, layer, seqs, ids, pos, starts, n, rows, const_cast<tv_bf16*>(k), const_cast<tv_bf16*>(v),
-                   row_stride, head_stride, dev_status, stream);
+  return rows_call(true, pool, layer, seqs, RowList{ids, pos, starts, n, rows}, const_cast<tv_bf16*>(k),
+                   const_cast<tv_bf16*>(v), row_stride, head_stride, dev_status, stream);
 }
 
 int tv_pages_read(const tv_pool* pool, int layer, const tv_seqs* seqs, const int32_t* ids, const int32_t* pos,
                   const int32_t* starts, int n, int rows, tv_bf16* k, tv_bf16* v, size_t row_stride,
                   size_t head_stride, int32_t* dev_status, void* stream) {
-  return rows_call(false, pool, layer, seqs, ids, pos, starts, n, rows, k, v, row_stride, head_stride, dev_status, stream);
+  return rows_call(false, pool, layer, seqs, RowList{ids, pos, starts, n, rows}, k, v, row_stride, head_stride,
+                   dev_status, stream);
 }
 
 }  // extern "C"

@@ -45,6 +45,16 @@
 // past the CTA's first token are looked over in shared memory before they are
 // used; what is not finite is taken out and noted (per dimension, the first
 // such key), and put into the rows that do see it at the end.
+//
+// Through a window (WIN: tv_attend_prompt_window) row t sees keys (t - W, t]
+// and the first K, the sinks:  of the pair's keys, those from lo, its first
+// token's lowest, come in windows of 128 counted from lo, then the sinks in
+// windows counted from 0, of 16-key steps that hold any.  So a pair costs
+// (W + 2T + 127) / 128 windows and the sinks' steps, whatever the length.  What
+// is masked is now at both ends; the lower end's V (keys up to W before the
+// pair's last token) is looked over as well, and a pair whose V held something
+// not finite reads its keys again from memory at the end, each row those that
+// it sees (put_back): which rows see a key is no longer told by one number.
 #include <cmath>
 #include <type_traits>
 
@@ -88,6 +98,9 @@ struct PrParams {
   __nv_bfloat16* out;
   int32_t* status;
   int n, rows, Hq, Hkv, G, T;
+  int window, sinks;              // WIN
+  const __nv_bfloat16* v;         // WIN: V once more, for put_back
+  size_t kv_stride;
   int queued;   // the grid is larger than the GPU: CTAs may be waiting whose places can be taken over
   float scale_log2;
 };
@@ -260,13 +273,35 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* r) {
                : "memory");
 }
 
+// WIN: what is not finite in V, of keys j0 .. j1 - 1 that row t sees, into its
+// result in dimensions d0 .. + n - 1 (row), added to what the products left.
+// Keys that the products had are added twice, which changes nothing.
+__device__ __noinline__ void put_back(const PrParams& p, const __nv_bfloat16* v, int j0, int j1, int t, uint16_t* row,
+                                      int n) {
+  for (int j = j0; j < j1 && j <= t; ++j) {
+    if (j <= t - p.window && j >= p.sinks) continue;
+    const uint4* x = reinterpret_cast<const uint4*>(v + (size_t)j * p.kv_stride);
+    for (int c = 0; c < n; c += 8) {
+      const uint4 y = __ldg(x + c / 8);
+      const uint32_t q[4] = {y.x, y.y, y.z, y.w};
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t b = q[u >> 1] >> (16 * (u & 1)) & 0xffffu;
+        if ((b & 0x7f80u) != 0x7f80u) continue;
+        const float was = __uint_as_float((uint32_t)*reinterpret_cast<volatile uint16_t*>(row + c + u) << 16);
+        const float sum = was + __uint_as_float(b << 16);
+        row[c + u] = sum != sum ? 0x7fc0 : (uint16_t)(__float_as_uint(sum) >> 16);
+      }
+    }
+  }
+}
+
 // 1-D grid: KV heads fastest, then the places ordered by the tile index inside
 // their sequence, highest first (the longest rows start first, so that what is
 // left at the end is short).  A CTA that has issued its work's last loads asks for
 // the place of one that has not started, so that the next queries, keys and
 // first products are under way while it writes its output; set-up is paid once
 // an SM.
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kPrThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const PrParams p) {
@@ -338,6 +373,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   struct Work {
     int row0, len, t0, h;   // first row and length of the sequence, first token, KV head
     int hi, nst, nwin, skip0;
+    int lo, nlow;   // WIN: the pair's first key but for the sinks; windows from it on, the others hold sinks
   };
   auto read_work = [&](int it, bool ok) {   // again and again until free_work
     Work w;
@@ -348,8 +384,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     w.h = __shfl_sync(0xffffffffu, x.w, 0);
     w.hi = min(w.len, w.t0 + 2 * p.T);                // one past the last key
     w.nst = w.t0 + p.T < w.len ? 2 : 1;               // query tiles
-    w.nwin = (w.hi + 127) / 128;
-    w.skip0 = w.nst == 2 ? w.nwin - (w.t0 + p.T + 127) / 128 : 0;   // tile 0 sees nothing of the first window (0 or 1)
+    w.lo = 0;
+    if constexpr (WIN) {
+      const int lo = w.t0 - p.window + 1;
+      if (lo > p.sinks) w.lo = lo;
+    }
+    w.nlow = (w.hi - w.lo + 127) / 128;
+    w.nwin = w.nlow;
+    if (WIN && w.lo > 0) w.nwin += (p.sinks + 127) / 128;   // (sinks < lo)
+    w.skip0 = w.nst == 2 ? w.nlow - (w.t0 + p.T - w.lo + 127) / 128 : 0;   // tile 0 sees nothing of the first window (0 or 1)
     return w;
   };
   auto wait_work = [&](int it, bool& ok) {
@@ -360,14 +403,32 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     if (lane == 0) mbar_arrive(&w_free[it & 1]);
   };
   // first key of window w, the last keys first
-  auto w_start = [](const Work& k, int w) { return 128 * (k.nwin - 1 - w); };
+  auto w_start = [](const Work& k, int w) {
+    if constexpr (WIN) return w < k.nlow ? k.lo + 128 * (k.nlow - 1 - w) : 128 * (k.nwin - 1 - w);
+    else return 128 * (k.nwin - 1 - w);
+  };
   // 16-key steps of window w that tile s sees anything of: what lies behind
   // its last token is neither multiplied nor looked at
   auto steps = [&](const Work& k, int s, int w) {
-    return min(8, (min(k.len, k.t0 + (s + 1) * p.T) - w_start(k, w) + 15) >> 4);
+    const int end = WIN && w >= k.nlow ? p.sinks : min(k.len, k.t0 + (s + 1) * p.T);
+    return min(8, (end - w_start(k, w) + 15) >> 4);
+  };
+  // WIN: rows [x, y) of window w that are hidden from some row of the pair by
+  // the window's lower end; in a window of sinks, those behind them in a step
+  auto below = [&](const Work& k, int w) {
+    const int start = w_start(k, w);
+    if (w >= k.nlow) return make_int2(min(128, p.sinks - start), 16 * steps(k, 0, w));
+    return make_int2(max(0, p.sinks - start), min(128, k.hi - p.window - start));
   };
   // window w holds keys that a row may not see (so does the first, if only as a rule)
-  auto scrub = [&](const Work& k, int w) { return w == 0 || w_start(k, w) + 127 > k.t0; };
+  auto scrub = [&](const Work& k, int w) {
+    if constexpr (WIN) {
+      const int2 b = below(k, w);
+      if (b.x < b.y) return true;
+      if (w >= k.nlow) return false;
+    }
+    return w == 0 || w_start(k, w) + 127 > k.t0;
+  };
 
   if (warp >= kPrSoftWarps) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
@@ -565,7 +626,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         wait(&v_full[i & 1], (uint32_t)(i >> 1));
         if (w + 1 < k.nwin) wait(&k_full[(i + 1) & 1], (uint32_t)((i + 1) >> 1));
         bool look = scrub(k, w);
-        const int seen = min(8, max(0, k.t0 + 1 - w_start(k, w)) >> 4);   // steps whose keys every row sees
+        int seen = min(8, max(0, k.t0 + 1 - w_start(k, w)) >> 4);   // steps whose keys every row sees
+        int low = 0;   // WIN: the first of them
+        if constexpr (WIN) {
+          const int2 b = below(k, w);
+          if (look && b.x < b.y) low = (b.y + 15) >> 4;
+          if (w >= k.nlow) seen = 8;
+        }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (s >= k.nst || !ok) break;
@@ -589,12 +656,16 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               }
             } else {   // what every row sees does not wait for the look at the rest
               const int n = steps(k, s, w), m = min(n, seen);
-              for (int c = 0; c < m; ++c) step(c);
+              // (the first window's first step is the one that overwrites O_s)
+              const int l = WIN && w == f && low > 0 ? m : min(m, low);
+              for (int c = l; c < m; ++c) step(c);
               wait(&v_ok[looked & 1], (uint32_t)(looked >> 1));
               ++looked;
               look = false;
               if (!ok) break;
               tc_fence_after();
+              if constexpr (WIN)
+                for (int c = 0; c < l; ++c) step(c);
               for (int c = m; c < n; ++c) step(c);
             }
             if (w == k.nwin - 1) commit_by(&o_fin[s], leader);
@@ -636,13 +707,24 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         uint8_t* sv = smem + L::OFF_V + (i & 1) * L::TILE;
         // rows of this pair's tokens but the first are looked at, those behind
         // its last token in the same step emptied
-        const int key0 = w_start(k, w), first = max(0, k.t0 + 1 - key0), last = min(128, k.hi - key0);
-        const int end = (last + 15) & ~15;
+        const int key0 = w_start(k, w);
+        int first = max(0, k.t0 + 1 - key0), last = min(128, k.hi - key0);
+        int empty = last, end = (last + 15) & ~15;
+        if constexpr (WIN) {   // and the rows that the lower end hides
+          const int2 b = below(k, w);
+          if (w >= k.nlow) {   // the sinks are seen, what is behind them in their last step is not
+            first = last = empty = b.x;
+            end = b.y;
+          } else if (b.x < b.y) {
+            if (first >= last) last = b.y;
+            first = b.x;
+          }
+        }
         constexpr int CH = D / 8;   // 16-byte pieces of a row, 32 / CH rows a step
-        bool wrote = last < end;
+        bool wrote = empty < end;
         const int c = lane % CH;
         uint8_t* piece = sv + (c >> 3) * kAtomP;
-        for (int row = last + lane / CH; row < end; row += 32 / CH)
+        for (int row = empty + lane / CH; row < end; row += 32 / CH)
           *reinterpret_cast<uint4*>(piece + swz(row, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
         // eight rows a round: their swizzles repeat, so that a round's addresses are the last's and 1024
         constexpr int PER = CH / 4, BATCH = 2 * PER;
@@ -676,7 +758,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 const uint32_t b = x[u];
                 if ((b & 0x7f80u) == 0x7f80u) {
                   const int kind = (b & 0x7fu) ? 0 : (b & 0x8000u ? 2 : 1);   // NaN, +inf, -inf
-                  atomicMin(&bad[kind * D + c * 8 + u], (unsigned long long)~tag << 32 | (unsigned)(key0 + row));
+                  if (!WIN) atomicMin(&bad[kind * D + c * 8 + u], (unsigned long long)~tag << 32 | (unsigned)(key0 + row));
                   x[u] = 0;
                 }
               }
@@ -740,12 +822,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       // because it goes where the scores are.
       // lim: the last visible one of this thread's keys; before: the first key
       // of the window before (rows before it have seen none); again: O_s holds
-      // earlier windows.
+      // earlier windows.  WIN: of them, those above low or below sink are visible.
       // Two copies of the code: PLAIN for windows that hide nothing of rows that
       // have keys already, one for all the others (a place of one or two
       // windows spends as long fetching instructions as on them: with a third
       // for masked windows the packed prompts took 66 us instead of 64).
-      auto window = [&](auto plain_c, bool masked, int lim, int before, bool again) {
+      auto window = [&](auto plain_c, bool masked, int lim, int before, bool again, int low, int sink) {
         constexpr bool PLAIN = decltype(plain_c)::value;
         if (ok && !mbar_wait(&s_full[s], (uint32_t)ns & 1u)) ok = false;
         ++ns;
@@ -757,6 +839,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           all_see = __reduce_min_sync(0xffffffffu, live ? lim : 63);
           any_see = __reduce_max_sync(0xffffffffu, live ? lim : -1);
         }
+        int all_low = -1, any_low = -1;   // above all_low every row sees them again; up to any_low no row does
+        if (WIN && !PLAIN && masked) {
+          all_low = __reduce_max_sync(0xffffffffu, live ? low : -1);
+          any_low = __reduce_min_sync(0xffffffffu, live ? low : 63);
+        }
+        auto unseen = [&](int c) {   // by every row of the warp
+          return 32 * c > any_see || (WIN && 32 * c + 31 <= any_low && 32 * c >= sink);
+        };
         auto scores = [&](int c, uint32_t (&x)[32]) {   // half of its scores
           ld32(sS + 64 * hf + 32 * c, x);
           tmem_ld_wait();
@@ -764,6 +854,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 #pragma unroll
             for (int u = 0; u < 32; ++u)
               if (32 * c + u > lim) x[u] = 0xff800000u;
+          }
+          if (WIN && !PLAIN && 32 * c <= all_low) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u)
+              if (32 * c + u <= low && 32 * c + u >= sink) x[u] = 0xff800000u;
           }
         };
         uint32_t pk[32];
@@ -773,7 +868,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            if (!PLAIN && 32 * c > any_see) {
+            if (!PLAIN && unseen(c)) {
 #pragma unroll
               for (int u = 0; u < 16; ++u) pk[16 * c + u] = 0u;
               continue;
@@ -793,7 +888,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           sum = (part[0] + part[1]) + (part[2] + part[3]);
           const bool fresh = !PLAIN && before > t;   // the row's first keys, if it sees any
-          const bool off = sum > kHigh || (first && fresh && live && lim >= 0 && sum < kLow);
+          const bool has = lim >= 0 && (!WIN || low < min(lim, 63) || sink > 0);   // it sees some of them
+          const bool off = sum > kHigh || (first && fresh && live && has && sum < kLow);
           tc_fence_before();
           const bool any = pair_any(off, pair);
           tc_fence_after();
@@ -842,16 +938,32 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       if (active) {
         // the windows that hide something, or are the first
         int w = f;
-        for (; w < k.nwin; ++w) {
-          const int start = w_start(k, w);
-          const bool masked = start + 127 > tmin;
-          // rows without a key: all in the first window, and those before a window that hid it all
-          const int before = w == f ? 0x7fffffff : start + 128;
-          if (w > f && !masked && before <= tmin) break;
-          window(std::false_type{}, masked, masked ? t - start - 64 * hf : 63, before, w > f);
+        if constexpr (WIN) {
+          const int last = min(k.len, tmin + p.T) - 1;   // the tile's last token
+#pragma unroll 1
+          for (; w < k.nwin; ++w) {
+            const int start = w_start(k, w);
+            const bool sinks = w >= k.nlow;
+            const int before = w == f ? 0x7fffffff : (sinks ? 0 : start + 128);
+            const bool masked = sinks ? p.sinks - start < 128
+                                      : start + 127 > tmin || (start <= last - p.window && start + 127 >= p.sinks);
+            const int at = start + 64 * hf;
+            if (!masked && before <= tmin) window(std::true_type{}, false, 63, 0, true, -1, 0);
+            else if (sinks) window(std::false_type{}, masked, p.sinks - 1 - at, before, w > f, -1, 0);
+            else window(std::false_type{}, masked, masked ? t - at : 63, before, w > f, masked ? t - p.window - at : -1, p.sinks - at);
+          }
+        } else {
+          for (; w < k.nwin; ++w) {
+            const int start = w_start(k, w);
+            const bool masked = start + 127 > tmin;
+            // rows without a key: all in the first window, and those before a window that hid it all
+            const int before = w == f ? 0x7fffffff : start + 128;
+            if (w > f && !masked && before <= tmin) break;
+            window(std::false_type{}, masked, masked ? t - start - 64 * hf : 63, before, w > f, -1, 0);
+          }
+          // and all the others
+          for (; w < k.nwin; ++w) window(std::true_type{}, false, 63, 0, true, -1, 0);
         }
-        // and all the others
-        for (; w < k.nwin; ++w) window(std::true_type{}, false, 63, 0, true);
         if (ok && !mbar_wait(&o_fin[s], (uint32_t)nf & 1u)) ok = false;
         ++nf;
         s_sum[hf * 128 + r] = l;
@@ -894,6 +1006,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (*reinterpret_cast<volatile unsigned*>(&s_anybad[it & 1]) == tag) {   // what of V is not finite
           const unsigned long long* first = s_bad + (it & 1) * 3 * D + hf * (D / 2);
           uint16_t* row = reinterpret_cast<uint16_t*>(dst - (odd ? 16 : 0)) + (size_t)ot * D;
+          if constexpr (WIN) {
+            __syncwarp();   // over what the other lane has stored
+            const __nv_bfloat16* v = p.v + (size_t)k.row0 * p.kv_stride + (size_t)k.h * D + hf * (D / 2);
+            if (ok && live)
+              for (int w = 0; w < k.nlow; ++w)
+                if (scrub(k, w)) put_back(p, v, w_start(k, w), w_start(k, w) + 128, t, row, D / 2);
+          } else {
           auto sees = [&](unsigned long long x) { return (unsigned)(x >> 32) == ~tag && (int)(unsigned)x <= t; };
           __syncwarp();   // over what the other lane has stored
           // Added to what the products left, which may be NaN or infinite
@@ -907,6 +1026,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               if (ni) x -= INFINITY;
               row[c] = n || x != x ? 0x7fc0 : (uint16_t)(__float_as_uint(x) >> 16);
             }
+          }
           }
         }
         tc_fence_before();   // the next place's products into O_s follow this warp's next arrival
@@ -923,7 +1043,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool WIN>
 int launch_prompt(PrParams& p, const void* q, const void* k, const void* v, size_t q_stride, size_t kv_stride,
                   cudaStream_t st) {
   CUtensorMap mq, mk, mv;
@@ -932,12 +1052,12 @@ int launch_prompt(PrParams& p, const void* q, const void* k, const void* v, size
       (rc = make_tmap_bf16_rows(&mv, v, p.Hkv * D, 1, p.rows, kv_stride, 64, 1, 128)))
     return rc;
   static std::atomic<bool> attr[64];
-  if (ensure_smem_limit(prompt_attn_kernel<D>, PrSmem<D>::BYTES, attr)) return TV_E_CUDA;
+  if (ensure_smem_limit(prompt_attn_kernel<D, WIN>, PrSmem<D>::BYTES, attr)) return TV_E_CUDA;
   // the roles' register split must not ask for more than the launch brings
   static std::atomic<int> regs{0};
   if (regs.load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, prompt_attn_kernel<D>) != cudaSuccess) return TV_E_CUDA;
+    if (cudaFuncGetAttributes(&fa, prompt_attn_kernel<D, WIN>) != cudaSuccess) return TV_E_CUDA;
     regs.store(fa.numRegs, std::memory_order_relaxed);
   }
   if (regs.load(std::memory_order_relaxed) * kPrThreads < kPrSoftThreads * kSoftRegs + 128 * kRoleRegs)
@@ -947,19 +1067,15 @@ int launch_prompt(PrParams& p, const void* q, const void* k, const void* v, size
   const int sms = num_sms();
   if (sms <= 0) return TV_E_CUDA;
   p.queued = pairs * p.Hkv > sms;
-  return launch_pdl(prompt_attn_kernel<D>, dim3((unsigned)(pairs * p.Hkv)), dim3(kPrThreads), PrSmem<D>::BYTES, st, mq,
+  return launch_pdl(prompt_attn_kernel<D, WIN>, dim3((unsigned)(pairs * p.Hkv)), dim3(kPrThreads), PrSmem<D>::BYTES, st, mq,
                     mk, mv, p);
 }
 
-}  // namespace
-}  // namespace tv
-
-using namespace tv;
-
-extern "C" int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const tv_bf16* q, const tv_bf16* k,
-                                const tv_bf16* v, size_t q_stride, size_t kv_stride, const int32_t* starts, int n_seqs,
-                                int rows, tv_bf16* out, int32_t* dev_status, void* stream) {
+int attend_prompt(bool win, int n_q_heads, int n_kv_heads, int head_dim, int window, int sinks, const tv_bf16* q,
+                  const tv_bf16* k, const tv_bf16* v, size_t q_stride, size_t kv_stride, const int32_t* starts,
+                  int n_seqs, int rows, tv_bf16* out, int32_t* dev_status, void* stream) {
   if (n_q_heads < 1 || n_kv_heads < 1 || !q || !k || !v || !starts || !out || !dev_status || rows < 1) return TV_E_ARG;
+  if (window < 1 || sinks < 0) return TV_E_ARG;
   int rc = check_listed(n_seqs);
   if (rc) return rc;
   if (head_dim != 64 && head_dim != 128) return TV_E_UNSUPPORTED;
@@ -978,9 +1094,40 @@ extern "C" int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, con
   p.Hkv = n_kv_heads;
   p.G = n_q_heads / n_kv_heads;
   p.T = 128 / p.G;
+  p.window = window < rows ? window : rows;   // no length is above rows, and differences of the two stay in range
+  p.sinks = sinks < rows ? sinks : rows;
+  p.v = reinterpret_cast<const __nv_bfloat16*>(v);
+  p.kv_stride = kv_stride;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
   if (((long long)rows / (2 * p.T) + n_seqs) * n_kv_heads > 0x7fffffffll) return TV_E_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return head_dim == 128 ? launch_prompt<128>(p, q, k, v, q_stride, kv_stride, st)
-                         : launch_prompt<64>(p, q, k, v, q_stride, kv_stride, st);
+  if (win)
+    return head_dim == 128 ? launch_prompt<128, true>(p, q, k, v, q_stride, kv_stride, st)
+                           : launch_prompt<64, true>(p, q, k, v, q_stride, kv_stride, st);
+  return head_dim == 128 ? launch_prompt<128, false>(p, q, k, v, q_stride, kv_stride, st)
+                         : launch_prompt<64, false>(p, q, k, v, q_stride, kv_stride, st);
 }
+
+}  // namespace
+}  // namespace tv
+
+using namespace tv;
+
+extern "C" {
+
+int tv_attend_prompt(int n_q_heads, int n_kv_heads, int head_dim, const tv_bf16* q, const tv_bf16* k, const tv_bf16* v,
+                     size_t q_stride, size_t kv_stride, const int32_t* starts, int n_seqs, int rows, tv_bf16* out,
+                     int32_t* dev_status, void* stream) {
+  return attend_prompt(false, n_q_heads, n_kv_heads, head_dim, 0x7fffffff, 0, q, k, v, q_stride, kv_stride, starts, n_seqs,
+                       rows, out, dev_status, stream);
+}
+
+int tv_attend_prompt_window(int n_q_heads, int n_kv_heads, int head_dim, int window, int sinks, const tv_bf16* q,
+                            const tv_bf16* k, const tv_bf16* v, size_t q_stride, size_t kv_stride,
+                            const int32_t* starts, int n_seqs, int rows, tv_bf16* out, int32_t* dev_status,
+                            void* stream) {
+  return attend_prompt(true, n_q_heads, n_kv_heads, head_dim, window, sinks, q, k, v, q_stride, kv_stride, starts, n_seqs,
+                       rows, out, dev_status, stream);
+}
+
+}  // extern "C"
