@@ -9,22 +9,25 @@
 // on each of its four schedulers as there are.  Hence:
 // - The cache lies as the tensor cores' operands do (tv_pool4): a lane loads its
 //   codes with 16-byte loads, no ldmatrix, no shuffle.
-// - Codes become fp16 without arithmetic: masked out of a word, 4 bits are the
-//   subnormal n' 2^-24, or 16 times that, n' = n + 8.  q is scaled to its row's
-//   exponent, and the 16 taken into it where it meets the higher bits.
-// - Q K^T (m16n8k16: rows are heads, columns tokens) begins at -8 sum q instead of
-//   zero, a group of 32 dimensions at a time, and each group's sum takes the
-//   token's scale.  Its 8 heads by 16 tokens are, in the same lanes, the B operand
-//   of O^T += V^T P^T (rows are dimensions, columns 8 heads): up to 8 heads a KV
-//   head cost half of what 16 do.  V's codes less 8 are one packed subtraction.
+// - Codes become fp16 operands without arithmetic: 4 or 8 bits masked out of 16 are
+//   the subnormals n' 2^-24 and (n' + 16 n") 2^-24, n' and n" = n + 8 of neighbours,
+//   two of each from a word of eight by four instructions.  Where dimensions are
+//   rows (V), neighbours come apart at the end; where they are summed (K), q' n' +
+//   q" n" = (q' - q" / 16) n' + q" / 16 (n' + 16 n"), the first factor as two fp16
+//   parts in the two halves of the 16 rows, which 8 heads leave free.
+// - Q K^T begins at -8 sum q instead of zero, a group of 32 dimensions at a time,
+//   and each group's sum takes the token's scale.  Its 8 heads by 16 tokens are, in the
+//   same lanes, the B operand of O^T += V^T P^T (rows are dimensions, columns 8 heads).
+//   V's codes less 8 are one packed subtraction.
 // - A token's V scale goes into its weight, four weights of fp16 a token (one a
 //   group), so that V needs no product.  The weights are relative to the largest
 //   scale so far, as they are to the offset: 2^15 at most, 2^-24 at least.
 //
-// How the work is cut over CTAs is in tv_paged_runs.cuh.  In a CTA one warp looks
-// up pages (32 boxes' entries at a time, the next 32 on their way) and copies whole blocks into
-// a ring of stages; the others compute, tile t by warps 4 (t mod quads) .. + 3, 16 tokens
-// each.
+// How the work is cut over CTAs is in tv_paged_runs.cuh.  In a CTA four warps look
+// up pages (32 boxes' entries at a time, the next 32 on their way) and copy whole
+// blocks into a ring of stages, each every fourth tile (one warp alone takes 1200
+// cycles a tile); the others compute, tile t by warps 4 (t mod quads) .. + 3, 16
+// tokens each.
 #include <cmath>
 #include <type_traits>
 
@@ -37,6 +40,7 @@ namespace tv {
 namespace {
 
 constexpr int kStages = 12;                      // tiles in flight: 108 KB at D = 128
+constexpr int kLoadWarps = 4;
 constexpr int kQueries = 8;                      // runs whose queries are loaded ahead, at most
 constexpr int kSegCost = 3;                      // what a head block costs besides its tiles, in tiles
 constexpr float kMoveLog2 = 8.f;                 // offsets move when a score passes them by this
@@ -48,7 +52,7 @@ struct P4 {
   using B = Block4<D>;
   static constexpr int WARPS = HN == 1 ? 12 : 8;   // that compute; the accumulators of 16 heads need the other half's registers
   static constexpr int QUADS = WARPS / 4;
-  static constexpr int THREADS = 32 * WARPS + 32;
+  static constexpr int THREADS = 32 * (WARPS + kLoadWarps);
   static constexpr int HEADS = 8 * HN;
   static constexpr int HALF = kTile / 16 * B::BYTES;   // a tile's K (or V)
   static constexpr int STAGE = 2 * HALF;
@@ -83,16 +87,34 @@ __device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// two fp32 values, one instruction for both
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// the scales of an even token and the odd one behind it
+__device__ __forceinline__ float2 scales(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
 // G words of shared memory, 4 G bytes aligned
 template <int G>
-__device__ __forceinline__ void lds_words(const uint8_t* a, uint32_t (&w)[G]) {
-  if constexpr (G == 4) {
-    const uint4 x = *reinterpret_cast<const uint4*>(a);
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-  } else {
-    const uint2 x = *reinterpret_cast<const uint2*>(a);
-    w[0] = x.x, w[1] = x.y;
-  }
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[G]) {
+  if constexpr (G == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
+  else
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
 }
 
 template <int D, int HN>
@@ -145,15 +167,16 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
   if (tid == 0) p.ws.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (runs.lo >= runs.hi) return;
 
-  if (warp == NW) {
+  if (warp >= NW) {
     // ---------------- pages and loads ----------------
+    const int mine = warp - NW;                            // every fourth tile, every fourth run's queries
     const int R = ps < kTile ? ps : kTile;                 // tokens of a box
     const int nsh = 6 - (31 - __clz(R)), nb = 1 << nsh;    // boxes of a tile
     const int psh = 31 - __clz(ps), per = 32 >> nsh;       // tiles of 32 boxes
     const size_t head_bytes = (size_t)(ps / 16) * B::BYTES;
     bool ok = true;
-    int issued = 0, segs = 0, st = 0, qs = 0;   // tiles and queries loaded so far, their places in the rings
-    uint32_t st_par = 1u, qs_par = 1u;          // of the wait before a place is used again (not in the first round)
+    int count = 0, segs = 0;     // tiles and runs so far, anyone's
+    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u)); };
     // blocks [a, b) of the box at tok hold tokens that are seen
     auto blocks = [&](const Run& g, int tok, int& a, int& b) {
       a = 0;
@@ -176,20 +199,24 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
     while (have && ok) {
       Run next = g;   // the next entries are on their way before this run's tiles
       const bool more = runs.next_run(next);
-      // its queries
-      if (segs >= qslots) ok = __all_sync(0xffffffffu, mbar_wait(&q_free[qs], qs_par));
-      if (!ok) break;
-      const int r0 = g.hb * kRows, nr = min(kRows, p.G - r0);
-      if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], (uint32_t)(nr * D * 2));
-      __syncwarp();
-      if (lane < nr)
-        bulk_load(smem + L::OFF_Q + (qs * qrows + lane) * L::Q_ROW,
-                  p.q + (size_t)g.i * p.q_stride + (size_t)(g.h * p.G + r0 + lane) * D, D * 2, &q_full[qs]);
+      if (segs % kLoadWarps == mine) {   // its queries
+        const int qs = segs % qslots;
+        if (segs >= qslots) wait(&q_free[qs], (uint32_t)(segs / qslots - 1));
+        if (!ok) break;
+        const int r0 = g.hb * kRows, nr = min(kRows, p.G - r0);
+        if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], (uint32_t)(nr * D * 2));
+        __syncwarp();
+        if (lane < nr)
+          bulk_load(smem + L::OFF_Q + (qs * qrows + lane) * L::Q_ROW,
+                    p.q + (size_t)g.i * p.q_stride + (size_t)(g.h * p.G + r0 + lane) * D, D * 2, &q_full[qs]);
+        __syncwarp();
+      }
       ++segs;
-      if (++qs == qslots) qs = 0, qs_par ^= 1u;
       for (int tb = g.t0; tb < g.t1 && ok; tb += per) {
         const int next_pages = tb + per < g.t1 ? entry(g, tb + per) : (more ? entry(next, next.t0) : -1);
-        for (int t = tb; t < min(tb + per, g.t1); ++t) {
+        const int end = min(tb + per, g.t1);
+        for (int t = tb + ((mine - count) & (kLoadWarps - 1)); t < end; t += kLoadWarps) {
+          const int issued = count + (t - tb), st = issued % kStages;
           // lane 2 b: K of box b, lane 2 b + 1: V
           const int box = lane >> 1;
           const int page = __shfl_sync(0xffffffffu, pages, ((t - tb) << nsh) + (box & (nb - 1)));
@@ -200,7 +227,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
           if (in && !good) status_set(p.status, TV_E_PAGE);
           const uint32_t bytes = good ? (uint32_t)((b - a) * B::BYTES) : 0u;
           const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
-          if (issued >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], st_par));
+          if (issued >= kStages) wait(&empty[st], (uint32_t)(issued / kStages - 1));
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&full[st], total);
           __syncwarp();
@@ -211,20 +238,18 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
             bulk_load(smem + st * L::STAGE + (lane & 1) * L::HALF + (box * (R / 16) + a) * B::BYTES, src, bytes, &full[st]);
           }
           __syncwarp();
-          ++issued;
-          if (++st == kStages) st = 0, st_par ^= 1u;
         }
+        count += end - tb;
         pages = next_pages;
       }
       g = next;
       have = more;
     }
     if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
-    for (int u = segs > qslots ? segs - qslots : 0; u < segs; ++u)
-      mbar_wait(&q_full[u % qslots], (uint32_t)(u / qslots) & 1u);
-    // loads in flight land before the CTA leaves
-    for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u)
-      mbar_wait(&full[u % kStages], (uint32_t)(u / kStages) & 1u);
+    // loads in flight land before the CTA leaves: with all of its warps, whose
+    // tiles and queries these are; what a timeout left unissued is not waited for
+    for (int u = max(0, segs - qslots); ok && u < segs; ++u) wait(&q_full[u % qslots], (uint32_t)(u / qslots));
+    for (int u = max(0, count - kStages); ok && u < count; ++u) wait(&full[u % kStages], (uint32_t)(u / kStages));
     return;
   }
 
@@ -235,39 +260,41 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
     asm volatile("bar.sync %0, %1;" ::"r"(nw == NW ? 1 : 2 + quad), "r"(32 * nw) : "memory");
   };
   bool ok = true;
-  // the next tile and queries of this CTA: places in the rings, parities
-  int st = 0, qs = 0;
+  // this warp's next tile and the CTA's next queries: places in the rings, parities
+  int st = quad, qs = 0;
   uint32_t st_par = 0u, qs_par = 0u;
+  int turn = quad;   // tiles of the CTA until its next one
   Run g;
   for (bool have = runs.first_run(g); have; have = runs.next_run(g)) {
     const int h = g.h, r0 = g.hb * kRows;   // KV head, first query head of the block in the group
     const int nr = min(kRows, p.G - r0);
     if (ok && !mbar_wait(&q_full[qs], qs_par)) ok = false;
-    if (g.T == 1 && st % NQ != quad) {   // one tile, and another four warps'
+    if (g.T == 1 && turn > 0) {   // one tile, and another four warps'
       // (no further ahead than the queries, nor further behind than their place:
       // it is not loaded again before these warps, too, have seen this phase)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_free[qs]);
-      if (++st == kStages) st = 0, st_par ^= 1u;
+      --turn;
       if (++qs == qslots) qs = 0, qs_par ^= 1u;
       continue;
     }
-    // Queries: rows g8 (and g8 + 8), dimensions 32 j + 8 t4 .. + 7 of group j, as
-    // fp16 relative to the row's exponent.  qf[row block][j][u]: dimensions u and
-    // u + 4, where u is odd over 16, since their codes come times 16.
+    // Queries: heads g8 (and g8 + 8), dimensions 32 j + 8 t4 .. + 7 of group j, q0 ..
+    // q7, relative to the row's exponent.  qc: (q1, q5) / 16 and (q3, q7) / 16; qf:
+    // what q0, q4 are above the first, as two parts, and q2, q6 above the second.
+    uint32_t qc[HN][G][2];
     uint32_t qf[HN][G][4];
-    float bias[HN][G], sc[HN];   // -8 sum q of a group; what a product of q and codes is worth, in powers of two
+    float bias[HN][G], sc[HN];   // -8 sum q of a group; what a product of q and codes is worth
 #pragma unroll
     for (int b = 0; b < HN; ++b) {
       // rows past the group's heads: the last one again, products nobody reads
-      const uint8_t* row = smem + L::OFF_Q + (qs * qrows + min(g8 + 8 * b, nr - 1)) * L::Q_ROW + t4 * 16;
-      uint4 x[G];
+      const uint32_t row = smem_u32(smem) + L::OFF_Q + (qs * qrows + min(g8 + 8 * b, nr - 1)) * L::Q_ROW + t4 * 16;
+      uint32_t x[G][4];
       uint32_t top = 0u;
 #pragma unroll
       for (int j = 0; j < G; ++j) {
-        x[j] = *reinterpret_cast<const uint4*>(row + j * 64);
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu),
-                                     __vmaxu2(x[j].z & 0x7fff7fffu, x[j].w & 0x7fff7fffu)));
+        lds_words<4>(row + j * 64, x[j]);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[j][0] & 0x7fff7fffu, x[j][1] & 0x7fff7fffu),
+                                     __vmaxu2(x[j][2] & 0x7fff7fffu, x[j][3] & 0x7fff7fffu)));
       }
       top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -278,24 +305,28 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
       sc[b] = p.scale_log2 * 0x1p24f * __uint_as_float((uint32_t)max(e - 13, 1) << 23);
 #pragma unroll
       for (int j = 0; j < G; ++j) {
-        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
         float sum = 0.f;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {   // dimensions u and u + 4: halves u % 2 of words u / 2 and u / 2 + 2
-          const float k = u & 1 ? f * 0.0625f : f;
-          const float a = (u & 1 ? __uint_as_float(w[u >> 1] & 0xffff0000u) : __uint_as_float(w[u >> 1] << 16)) * k;
-          const float c = (u & 1 ? __uint_as_float(w[(u >> 1) + 2] & 0xffff0000u) : __uint_as_float(w[(u >> 1) + 2] << 16)) * k;
-          const __half2 v = __floats2half2_rn(a, c);
-          qf[b][j][u] = *reinterpret_cast<const uint32_t*>(&v);
-          const float2 r = __half22float2(v);
-          sum += (r.x + r.y) * (u & 1 ? 16.f : 1.f);
+        for (int u = 0; u < 2; ++u) {   // dimensions 2 u, 2 u + 1 (word u) and 4 more (word u + 2)
+          const float2 even = make_float2(__uint_as_float(x[j][u] << 16) * f, __uint_as_float(x[j][u + 2] << 16) * f);
+          const __half2 c = __floats2half2_rn(__uint_as_float(x[j][u] & 0xffff0000u) * (f * 0.0625f),
+                                              __uint_as_float(x[j][u + 2] & 0xffff0000u) * (f * 0.0625f));
+          const float2 cf = __half22float2(c), d = make_float2(even.x - cf.x, even.y - cf.y);
+          const __half2 hi = __floats2half2_rn(d.x, d.y);
+          const float2 hf = __half22float2(hi);
+          const __half2 lo = __floats2half2_rn(d.x - hf.x, d.y - hf.y);
+          const float2 lf = __half22float2(lo);
+          qc[b][j][u] = *reinterpret_cast<const uint32_t*>(&c);
+          qf[b][j][2 * u] = *reinterpret_cast<const uint32_t*>(&hi);
+          qf[b][j][2 * u + 1] = *reinterpret_cast<const uint32_t*>(&lo);
+          sum += 17.f * (cf.x + cf.y) + ((hf.x + lf.x) + (hf.y + lf.y));
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         bias[b][j] = sum * -0x1p-21f;   // -8 * 2^-24
       }
     }
-    // O^T: o[row block][j][0 .. 3] rows 32 j + 4 g8 + {0, 0, 1, 1}, heads 2 t4 + {0, 1, 0, 1}; [4 .. 7]: 2 more
+    // O^T: o[8 heads][j][0 .. 3] rows 32 j + 4 g8, that and 16 times the next, heads 2 t4, 2 t4 + 1; [4 .. 7]: two rows more
     float o[HN][G][8];
     float m[HN], l[HN];          // offsets and sums of rows g8 (+ 8), of this thread's tokens
     float vtop = 0x1p-100f;      // power of two above the scales of V so far
@@ -308,14 +339,11 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
         for (int e = 0; e < 8; ++e) o[b][j][e] = 0.f;
     }
 
-    for (int t = g.t0; t < g.t1; ++t) {
-      const int at = st;
-      const uint32_t par = st_par;
-      if (++st == kStages) st = 0, st_par ^= 1u;
-      if (at % NQ != quad) continue;   // the number of stages is a multiple of the quads': the place's parity is the tile's
-      uint8_t* sk = smem + at * L::STAGE + sl * B::BYTES;
+    int t = g.t0 + turn;
+    for (; t < g.t1; t += NQ) {
+      uint8_t* sk = smem + st * L::STAGE + sl * B::BYTES;
       uint8_t* sv = sk + L::HALF;
-      if (ok && !mbar_wait(&full[at], par)) ok = false;
+      if (ok && !mbar_wait(&full[st], st_par)) ok = false;
       const int tok0 = g.tile<true>(t) * kTile + 16 * sl;
       int valid = min(16, g.len - tok0);   // this warp's tokens
       const int hide0 = max(0, p.sinks - tok0), hide1 = min(16, g.lo - tok0);   // those from hide0 up to hide1 are hidden
@@ -352,64 +380,60 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
           __syncwarp();
         }
         // tokens of this thread, as columns of S and rows of P: 2 t4, 2 t4 + 1 (half 0) and 8 more (half 1)
-        float x[HN][2][2];
-        {
-          uint32_t ka[2][G], sa[2][G];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            lds_words<G>(sk + (8 * n + g8) * (D / 2) + t4 * (D / 8), ka[n]);
-            lds_words<G>(sk + B::OFF_SCALE + (n * 4 + t4) * G * 4, sa[n]);
-          }
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-              const uint32_t w = ka[n][j], w8 = w >> 8;
-              float c[4], d[4];
-              mma_f16(c, qf[0][j][0], HN > 1 ? qf[HN - 1][j][0] : 0u, qf[0][j][1], HN > 1 ? qf[HN - 1][j][1] : 0u,
-                      w & 0x000f000fu, w & 0x00f000f0u, bias[0][j], bias[0][j], bias[HN - 1][j], bias[HN - 1][j]);
-              mma_f16(d, qf[0][j][2], HN > 1 ? qf[HN - 1][j][2] : 0u, qf[0][j][3], HN > 1 ? qf[HN - 1][j][3] : 0u,
-                      w8 & 0x000f000fu, w8 & 0x00f000f0u, c[0], c[1], c[2], c[3]);
-              const float s0 = __uint_as_float(sa[n][j] << 16), s1 = __uint_as_float(sa[n][j] & 0xffff0000u);
-#pragma unroll
-              for (int b = 0; b < HN; ++b) {
-                x[b][n][0] = j == 0 ? d[2 * b] * s0 : fmaf(d[2 * b], s0, x[b][n][0]);
-                x[b][n][1] = j == 0 ? d[2 * b + 1] * s1 : fmaf(d[2 * b + 1], s1, x[b][n][1]);
-              }
-            }
-          }
-        }
+        const uint32_t ka = smem_u32(sk), va = ka + L::HALF;
+        float2 x[HN][2];
         uint32_t sb[2][G];   // scales of V
 #pragma unroll
-        for (int n = 0; n < 2; ++n) lds_words<G>(sv + B::OFF_SCALE + (n * 4 + t4) * G * 4, sb[n]);
+        for (int n = 0; n < 2; ++n) {
+          uint32_t w[G], sa[G];
+          lds_words<G>(ka + (8 * n + g8) * (D / 2) + t4 * (D / 8), w);
+          lds_words<G>(ka + B::OFF_SCALE + (n * 4 + t4) * G * 4, sa);
+          lds_words<G>(va + B::OFF_SCALE + (n * 4 + t4) * G * 4, sb[n]);
 #pragma unroll
-        for (int b = 0; b < HN; ++b)
+          for (int b = 0; b < HN; ++b) x[b][n] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[b][e >> 1][e & 1] *= sc[b];
+          for (int j = 0; j < G; ++j) {
+            // n' + 16 n" of neighbours, and n'
+            const uint32_t u0 = w[j] & 0x00ff00ffu, u1 = __byte_perm(w[j], 0u, 0x4341);
+            const uint32_t v0 = w[j] & 0x000f000fu, v1 = u1 & 0x000f000fu;
+            const float2 s2 = scales(sa[j]);
+#pragma unroll
+            for (int b = 0; b < HN; ++b) {
+              float c[4];
+              mma_f16(c, qc[b][j][0], 0u, qc[b][j][1], 0u, u0, u1, bias[b][j], bias[b][j], 0.f, 0.f);
+              mma_f16(c, qf[b][j][0], qf[b][j][1], qf[b][j][2], qf[b][j][3], v0, v1, c[0], c[1], c[2], c[3]);
+              x[b][n] = fma2(make_float2(c[0], c[1]), s2, fma2(make_float2(c[2], c[3]), s2, x[b][n]));
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < HN; ++b) x[b][n] = mul2(x[b][n], make_float2(sc[b], sc[b]));
+        }
         if (valid < 16 || hide0 < hide1) {   // what is past the length or hidden: no score, and a scale of zero, whatever it holds
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tk = 8 * (e >> 1) + 2 * t4 + (e & 1);
-            if (tk >= valid || (tk >= hide0 && tk < hide1)) {
+          for (int n = 0; n < 2; ++n) {
+            auto out = [&](int tk) { return tk >= valid || (tk >= hide0 && tk < hide1); };
+            const bool even = out(8 * n + 2 * t4), odd = out(8 * n + 2 * t4 + 1);
 #pragma unroll
-              for (int b = 0; b < HN; ++b) x[b][e >> 1][e & 1] = -INFINITY;
-#pragma unroll
-              for (int j = 0; j < G; ++j) sb[e >> 1][j] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+            for (int b = 0; b < HN; ++b) {
+              if (even) x[b][n].x = -INFINITY;
+              if (odd) x[b][n].y = -INFINITY;
             }
+            const uint32_t keep = (even ? 0u : 0x0000ffffu) | (odd ? 0u : 0xffff0000u);
+#pragma unroll
+            for (int j = 0; j < G; ++j) sb[n][j] &= keep;
           }
         }
         // offsets and the largest scale: moved when passed, hardly ever
         bool pass = false;
 #pragma unroll
-        for (int b = 0; b < HN; ++b)
-          pass = pass || fmaxf(fmaxf(x[b][0][0], x[b][0][1]), fmaxf(x[b][1][0], x[b][1][1])) > m[b] + kMoveLog2;
-        uint32_t top = 0u;
+        for (int b = 0; b < HN; ++b) pass = pass || fmaxf(fmaxf(x[b][0].x, x[b][0].y), fmaxf(x[b][1].x, x[b][1].y)) > m[b] + kMoveLog2;
+        const uint32_t vt = __byte_perm(__float_as_uint(vtop), 0u, 0x3232);   // its upper half twice
+        uint32_t top = vt;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int j = 0; j < G; ++j) top = __vmaxu2(top, sb[n][j]);
-        top = max(top & 0xffffu, top >> 16);
-        if (__any_sync(0xffffffffu, pass || __uint_as_float(top << 16) > vtop || top >= 0x7f80u)) {
+          for (int j = 0; j < G; j += 2) top = __vimax3_u16x2(top, sb[n][j], sb[n][j + 1]);
+        if (__any_sync(0xffffffffu, pass || top != vt)) {
           // scales that are NaN say nothing of the others
           top = 0u;
 #pragma unroll
@@ -428,7 +452,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
           }
 #pragma unroll
           for (int b = 0; b < HN; ++b) {
-            float y = fmaxf(fmaxf(x[b][0][0], x[b][0][1]), fmaxf(x[b][1][0], x[b][1][1]));
+            float y = fmaxf(fmaxf(x[b][0].x, x[b][0].y), fmaxf(x[b][1].x, x[b][1].y));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
             const float n = y > m[b] + kMoveLog2 ? y : m[b];
@@ -448,33 +472,35 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
         for (int b = 0; b < HN; ++b) {
           const float f = m[b] == -INFINITY ? 0.f : m[b];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y = ex2f(x[b][e >> 1][e & 1] - f);
-            l[b] += y;
-            x[b][e >> 1][e & 1] = y * lift;
+          for (int n = 0; n < 2; ++n) {
+            const float2 y = make_float2(ex2f(x[b][n].x - f), ex2f(x[b][n].y - f));
+            l[b] += y.x + y.y;
+            x[b][n] = mul2(y, make_float2(lift, lift));
           }
         }
-        uint32_t va[2][G];
+        uint32_t vw[2][G];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) lds_words<G>(sv + (n * 32 + lane) * G * 4, va[n]);
+        for (int n = 0; n < 2; ++n) lds_words<G>(va + (n * 32 + lane) * G * 4, vw[n]);
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-          // rows u of V^T: dimensions 4 g8 + u of the group, the odd ones times 16; columns: tokens 2 t4, 2 t4 + 1 and 8 more
+          // rows of V^T: dimensions 4 g8, that and 16 times the next, two more; columns: tokens 2 t4, 2 t4 + 1 and 8 more
           uint32_t a[4][2];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const uint32_t w = va[n][j], w8 = w >> 8;
+            const uint32_t w = vw[n][j], u1 = __byte_perm(w, 0u, 0x4341);
             a[0][n] = sub_f16(w & 0x000f000fu, 0x00080008u);
-            a[1][n] = sub_f16(w & 0x00f000f0u, 0x00800080u);
-            a[2][n] = sub_f16(w8 & 0x000f000fu, 0x00080008u);
-            a[3][n] = sub_f16(w8 & 0x00f000f0u, 0x00800080u);
+            a[1][n] = sub_f16(w & 0x00ff00ffu, 0x00880088u);
+            a[2][n] = sub_f16(u1 & 0x000f000fu, 0x00080008u);
+            a[3][n] = sub_f16(u1, 0x00880088u);
           }
 #pragma unroll
           for (int b = 0; b < HN; ++b) {
             uint32_t pw[2];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-              pw[n] = pack_f16(x[b][n][0] * __uint_as_float(sb[n][j] << 16), x[b][n][1] * __uint_as_float(sb[n][j] & 0xffff0000u));
+            for (int n = 0; n < 2; ++n) {
+              const float2 y = mul2(x[b][n], scales(sb[n][j]));
+              pw[n] = pack_f16(y.x, y.y);
+            }
             float(&lo)[4] = *reinterpret_cast<float(*)[4]>(&o[b][j][0]);
             float(&hi)[4] = *reinterpret_cast<float(*)[4]>(&o[b][j][4]);
             mma_f16(lo, a[0][0], a[1][0], a[0][1], a[1][1], pw[0], pw[1], lo[0], lo[1], lo[2], lo[3]);
@@ -484,8 +510,10 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
         if (wrote) fence_async_smem();   // before the stage takes another copy
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[at]);
+      if (lane == 0) mbar_arrive(&empty[st]);
+      if ((st += NQ) >= kStages) st = quad, st_par ^= 1u;
     }
+    turn = t - g.t1;
 
     // ---- the head block's partial results into one ----
     // of all warps, or, where the head block is one tile, of the four that had
@@ -504,10 +532,11 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
         float* dst = s_red + ((size_t)warp * L::HEADS + 8 * b + 2 * t4 + e) * D + ((g8 + 2 * t4) & 7) * 4;
         if (8 * b + 2 * t4 + e < nr)
 #pragma unroll
-          for (int j = 0; j < G; ++j) {   // what the codes' and the weights' factors leave: 2^17 and 2^13 of vtop
+          for (int j = 0; j < G; ++j) {   // what the codes' and the weights' factors leave: 2^17 vtop
             const float(&r)[8] = o[b][j];
-            *reinterpret_cast<float4*>(dst + 32 * j) = make_float4(r[e] * 0x1p17f * vtop, r[2 + e] * 0x1p13f * vtop,
-                                                                   r[4 + e] * 0x1p17f * vtop, r[6 + e] * 0x1p13f * vtop);
+            *reinterpret_cast<float4*>(dst + 32 * j) =
+                make_float4(r[e] * 0x1p17f * vtop, (r[2 + e] - r[e]) * 0x1p13f * vtop, r[4 + e] * 0x1p17f * vtop,
+                            (r[6 + e] - r[4 + e]) * 0x1p13f * vtop);
           }
       }
     }
