@@ -9,16 +9,15 @@
 // on each of its four schedulers as there are.  Hence:
 // - The cache lies as the tensor cores' operands do (tv_pool4): a lane loads its
 //   codes with 16-byte loads, no ldmatrix, no shuffle.
-// - Codes become fp16 operands without arithmetic: 4 or 8 bits masked out of 16 are
-//   the subnormals n' 2^-24 and (n' + 16 n") 2^-24, n' and n" = n + 8 of neighbours,
-//   two of each from a word of eight by four instructions.  Where dimensions are
-//   rows (V), neighbours come apart at the end; where they are summed (K), q' n' +
-//   q" n" = (q' - q" / 16) n' + q" / 16 (n' + 16 n"), the first factor as two fp16
-//   parts in the two halves of the 16 rows, which 8 heads leave free.
-// - Q K^T begins at -8 sum q instead of zero, a group of 32 dimensions at a time,
-//   and each group's sum takes the token's scale.  Its 8 heads by 16 tokens are, in the
-//   same lanes, the B operand of O^T += V^T P^T (rows are dimensions, columns 8 heads).
-//   V's codes less 8 are one packed subtraction.
+// - Codes become fp16 operands without arithmetic: 4 bits masked out of 16 are the
+//   subnormal n' 2^-24 or 16 times that, n' = n + 8, and 8 bits (n' + 16 n") 2^-24 of
+//   neighbours.  Where dimensions are summed (K), q carries the 16th part; where
+//   they are rows (V), neighbours come apart at the end, which saves a mask.
+// - Both products have the codes as the operand of 16 rows and 8 heads as columns
+//   (S^T = K Q^T, O^T += V^T P^T): up to 8 heads a KV head cost half of what 16 do.
+//   S^T begins at -8 sum q instead of zero, a group of 32 dimensions at a time, and
+//   each group's sum takes the token's scale; V's codes less 8 are one packed
+//   subtraction.
 // - A token's V scale goes into its weight, four weights of fp16 a token (one a
 //   group), so that V needs no product.  The weights are relative to the largest
 //   scale so far, as they are to the offset: 2^15 at most, 2^-24 at least.
@@ -87,27 +86,28 @@ __device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// two fp32 values, one instruction for both
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+// an 8 x 8 matrix of 16-bit values, a row to four lanes, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
+// mbar_wait of warps with nothing to do meanwhile: asleep up to 2 us at a time,
+// so that they do not take issue slots from those that compute
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
+  for (uint32_t n = 0; n < (uint32_t)(kWaitLimitNs / 2000); ++n) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
+        : "memory");
+    if (done) return true;
+  }
+  return mbar_wait(bar, parity);
 }
-// the scales of an even token and the odd one behind it
-__device__ __forceinline__ float2 scales(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
 // G words of shared memory, 4 G bytes aligned
 template <int G>
 __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[G]) {
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
     const size_t head_bytes = (size_t)(ps / 16) * B::BYTES;
     bool ok = true;
     int count = 0, segs = 0;     // tiles and runs so far, anyone's
-    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u)); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, mbar_sleep(bar, parity & 1u)); };
     // blocks [a, b) of the box at tok hold tokens that are seen
     auto blocks = [&](const Run& g, int tok, int& a, int& b) {
       a = 0;
@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
   // ---------------- compute warps ----------------
   const int quad = warp >> 2, sl = warp & 3;        // tiles with (count mod NQ) == quad; tokens 16 sl .. + 15 of a tile
   const int g8 = lane >> 2, t4 = lane & 3;
+  const uint32_t pick = g8 & 1 ? 0x3244u : 0x1044u;   // of a word of two bf16, token g8's as fp32
   auto meet = [&](int nw) {
     asm volatile("bar.sync %0, %1;" ::"r"(nw == NW ? 1 : 2 + quad), "r"(32 * nw) : "memory");
   };
@@ -278,12 +279,12 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
       if (++qs == qslots) qs = 0, qs_par ^= 1u;
       continue;
     }
-    // Queries: heads g8 (and g8 + 8), dimensions 32 j + 8 t4 .. + 7 of group j, q0 ..
-    // q7, relative to the row's exponent.  qc: (q1, q5) / 16 and (q3, q7) / 16; qf:
-    // what q0, q4 are above the first, as two parts, and q2, q6 above the second.
-    uint32_t qc[HN][G][2];
-    uint32_t qf[HN][G][4];
-    float bias[HN][G], sc[HN];   // -8 sum q of a group; what a product of q and codes is worth
+    // Queries, as columns: head g8 (and g8 + 8), dimensions 32 j + 8 t4 .. + 7 of
+    // group j, q0 .. q7, relative to the row's exponent: (q0, q4), (q1, q5) / 16,
+    // (q2, q6), (q3, q7) / 16, exact down to 2^-24 of the row's largest.
+    uint32_t q[HN][G][4];
+    // of heads 2 t4 and 2 t4 + 1: -8 sum q of a group; what a product of q and codes is worth
+    float bias[HN][G][2], sc[HN][2];
 #pragma unroll
     for (int b = 0; b < HN; ++b) {
       // rows past the group's heads: the last one again, products nobody reads
@@ -302,55 +303,59 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
       // the largest to 2^13 .. 2^14; below 2^-114 it stays smaller
       const int e = max((int)(top >> 7), 13);   // 127 + exponent
       const float f = __uint_as_float((uint32_t)(267 - e) << 23);
-      sc[b] = p.scale_log2 * 0x1p24f * __uint_as_float((uint32_t)max(e - 13, 1) << 23);
+      const float worth = p.scale_log2 * 0x1p24f * __uint_as_float((uint32_t)max(e - 13, 1) << 23);
+      sc[b][0] = __shfl_sync(0xffffffffu, worth, 8 * t4);
+      sc[b][1] = __shfl_sync(0xffffffffu, worth, 8 * t4 + 4);
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         float sum = 0.f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {   // dimensions 2 u, 2 u + 1 (word u) and 4 more (word u + 2)
-          const float2 even = make_float2(__uint_as_float(x[j][u] << 16) * f, __uint_as_float(x[j][u + 2] << 16) * f);
-          const __half2 c = __floats2half2_rn(__uint_as_float(x[j][u] & 0xffff0000u) * (f * 0.0625f),
-                                              __uint_as_float(x[j][u + 2] & 0xffff0000u) * (f * 0.0625f));
-          const float2 cf = __half22float2(c), d = make_float2(even.x - cf.x, even.y - cf.y);
-          const __half2 hi = __floats2half2_rn(d.x, d.y);
-          const float2 hf = __half22float2(hi);
-          const __half2 lo = __floats2half2_rn(d.x - hf.x, d.y - hf.y);
-          const float2 lf = __half22float2(lo);
-          qc[b][j][u] = *reinterpret_cast<const uint32_t*>(&c);
-          qf[b][j][2 * u] = *reinterpret_cast<const uint32_t*>(&hi);
-          qf[b][j][2 * u + 1] = *reinterpret_cast<const uint32_t*>(&lo);
-          sum += 17.f * (cf.x + cf.y) + ((hf.x + lf.x) + (hf.y + lf.y));
+        for (int u = 0; u < 4; ++u) {   // dimensions u and u + 4: halves u % 2 of words u / 2 and u / 2 + 2
+          const float k = u & 1 ? f * 0.0625f : f;
+          const uint32_t y = x[j][u >> 1], z = x[j][(u >> 1) + 2];
+          const __half2 v = __floats2half2_rn(__uint_as_float(u & 1 ? y & 0xffff0000u : y << 16) * k,
+                                              __uint_as_float(u & 1 ? z & 0xffff0000u : z << 16) * k);
+          const float2 r = __half22float2(v);
+          q[b][j][u] = *reinterpret_cast<const uint32_t*>(&v);
+          sum += (r.x + r.y) * (u & 1 ? 16.f : 1.f);
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        bias[b][j] = sum * -0x1p-21f;   // -8 * 2^-24
+        bias[b][j][0] = __shfl_sync(0xffffffffu, sum, 8 * t4) * -0x1p-21f;   // -8 * 2^-24
+        bias[b][j][1] = __shfl_sync(0xffffffffu, sum, 8 * t4 + 4) * -0x1p-21f;
       }
     }
     // O^T: o[8 heads][j][0 .. 3] rows 32 j + 4 g8, that and 16 times the next, heads 2 t4, 2 t4 + 1; [4 .. 7]: two rows more
     float o[HN][G][8];
-    float m[HN], l[HN];          // offsets and sums of rows g8 (+ 8), of this thread's tokens
+    float m[HN][2], l[HN][2];    // their offsets, and sums of this thread's tokens
     float vtop = 0x1p-100f;      // power of two above the scales of V so far
 #pragma unroll
     for (int b = 0; b < HN; ++b) {
-      m[b] = -INFINITY, l[b] = 0.f;
+      m[b][0] = m[b][1] = 0.f, l[b][0] = l[b][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < G; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[b][j][e] = 0.f;
     }
 
+    bool fresh = true;           // no token so far
     int t = g.t0 + turn;
     for (; t < g.t1; t += NQ) {
       uint8_t* sk = smem + st * L::STAGE + sl * B::BYTES;
       uint8_t* sv = sk + L::HALF;
       if (ok && !mbar_wait(&full[st], st_par)) ok = false;
-      const int tok0 = g.tile<true>(t) * kTile + 16 * sl;
-      int valid = min(16, g.len - tok0);   // this warp's tokens
-      const int hide0 = max(0, p.sinks - tok0), hide1 = min(16, g.lo - tok0);   // those from hide0 up to hide1 are hidden
-      if (hide0 == 0 && hide1 >= valid) valid = 0;
-      if (valid > 0) {
-        bool wrote = false;
-        if (p.k_new && tok0 + valid == g.len) {
+      const uint32_t ka = smem_u32(sk), va = ka + L::HALF;
+      // Which of the warp's tokens are seen: all of them but in a sequence's last
+      // tile, the window's first and the sinks' last.
+      int tok0 = 0, valid = 16, hide0 = 0, hide1 = 0;   // the first; those in the sequence; from hide0 up to hide1 hidden
+      const bool special = t == g.T - 1 || (g.lo > 0 && (t == g.sink_tiles || t == g.sink_tiles - 1));
+      bool wrote = false;
+      if (special) {
+        tok0 = g.tile<true>(t) * kTile + 16 * sl;
+        valid = min(16, g.len - tok0);
+        hide0 = max(0, p.sinks - tok0), hide1 = min(16, g.lo - tok0);
+        if (hide0 == 0 && hide1 >= valid) valid = 0;
+        if (valid > 0 && p.k_new && tok0 + valid == g.len) {
           // the new token: its codes into the tile and into the page
           const bool is_v = lane >= 16;
           const int c = lane & 15, tk = valid - 1, half = tk % 2 * 2;
@@ -379,61 +384,69 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
           wrote = true;
           __syncwarp();
         }
-        // tokens of this thread, as columns of S and rows of P: 2 t4, 2 t4 + 1 (half 0) and 8 more (half 1)
-        const uint32_t ka = smem_u32(sk), va = ka + L::HALF;
-        float2 x[HN][2];
-        uint32_t sb[2][G];   // scales of V
+      }
+      if (valid > 0) {
+        // Tokens of this thread, as rows of S^T: g8 (n = 0) and g8 + 8 (1).
+        float x[HN][2][2];   // [n][head]
+        uint32_t sb[2][G];   // scales of V: of g8 and its neighbour
+        {
+          uint32_t w[2][G], sa[2][G];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          uint32_t w[G], sa[G];
-          lds_words<G>(ka + (8 * n + g8) * (D / 2) + t4 * (D / 8), w);
-          lds_words<G>(ka + B::OFF_SCALE + (n * 4 + t4) * G * 4, sa);
-          lds_words<G>(va + B::OFF_SCALE + (n * 4 + t4) * G * 4, sb[n]);
-#pragma unroll
-          for (int b = 0; b < HN; ++b) x[b][n] = make_float2(0.f, 0.f);
+          for (int n = 0; n < 2; ++n) {
+            lds_words<G>(ka + (8 * n + g8) * (D / 2) + t4 * (D / 8), w[n]);
+            lds_words<G>(ka + B::OFF_SCALE + (n * 4 + (g8 >> 1)) * G * 4, sa[n]);
+            lds_words<G>(va + B::OFF_SCALE + (n * 4 + (g8 >> 1)) * G * 4, sb[n]);
+          }
 #pragma unroll
           for (int j = 0; j < G; ++j) {
-            // n' + 16 n" of neighbours, and n'
-            const uint32_t u0 = w[j] & 0x00ff00ffu, u1 = __byte_perm(w[j], 0u, 0x4341);
-            const uint32_t v0 = w[j] & 0x000f000fu, v1 = u1 & 0x000f000fu;
-            const float2 s2 = scales(sa[j]);
+            const uint32_t w0 = w[0][j], w1 = w[1][j];
+            const uint32_t u0 = __byte_perm(w0, 0u, 0x4341), u1 = __byte_perm(w1, 0u, 0x4341);   // its second and fourth bytes
+            const float s0 = __uint_as_float(__byte_perm(sa[0][j], 0u, pick)), s1 = __uint_as_float(__byte_perm(sa[1][j], 0u, pick));
 #pragma unroll
             for (int b = 0; b < HN; ++b) {
               float c[4];
-              mma_f16(c, qc[b][j][0], 0u, qc[b][j][1], 0u, u0, u1, bias[b][j], bias[b][j], 0.f, 0.f);
-              mma_f16(c, qf[b][j][0], qf[b][j][1], qf[b][j][2], qf[b][j][3], v0, v1, c[0], c[1], c[2], c[3]);
-              x[b][n] = fma2(make_float2(c[0], c[1]), s2, fma2(make_float2(c[2], c[3]), s2, x[b][n]));
+              mma_f16(c, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, q[b][j][0], q[b][j][1],
+                      0.f, 0.f, 0.f, 0.f);
+              mma_f16(c, u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u, q[b][j][2], q[b][j][3], c[0],
+                      c[1], c[2], c[3]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                x[b][0][e] = j == 0 ? (c[e] + bias[b][j][e]) * s0 : fmaf(c[e] + bias[b][j][e], s0, x[b][0][e]);
+                x[b][1][e] = j == 0 ? (c[2 + e] + bias[b][j][e]) * s1 : fmaf(c[2 + e] + bias[b][j][e], s1, x[b][1][e]);
+              }
             }
           }
-#pragma unroll
-          for (int b = 0; b < HN; ++b) x[b][n] = mul2(x[b][n], make_float2(sc[b], sc[b]));
         }
-        if (valid < 16 || hide0 < hide1) {   // what is past the length or hidden: no score, and a scale of zero, whatever it holds
+        if (special) {   // what is past the length or hidden: no score, and a scale of zero, whatever it holds
+          auto out = [&](int tk) { return tk >= valid || (tk >= hide0 && tk < hide1); };
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            auto out = [&](int tk) { return tk >= valid || (tk >= hide0 && tk < hide1); };
-            const bool even = out(8 * n + 2 * t4), odd = out(8 * n + 2 * t4 + 1);
+            const int tk = 8 * n + (g8 & ~1);
+            if (out(8 * n + g8))
 #pragma unroll
-            for (int b = 0; b < HN; ++b) {
-              if (even) x[b][n].x = -INFINITY;
-              if (odd) x[b][n].y = -INFINITY;
-            }
-            const uint32_t keep = (even ? 0u : 0x0000ffffu) | (odd ? 0u : 0xffff0000u);
+              for (int b = 0; b < HN; ++b) x[b][n][0] = x[b][n][1] = -INFINITY;
+            const uint32_t keep = (out(tk) ? 0u : 0x0000ffffu) | (out(tk + 1) ? 0u : 0xffff0000u);
 #pragma unroll
             for (int j = 0; j < G; ++j) sb[n][j] &= keep;
           }
         }
-        // offsets and the largest scale: moved when passed, hardly ever
-        bool pass = false;
+        // exponents relative to the offsets, which move when passed, as the largest scale does, hardly ever
+        float most = -INFINITY;
 #pragma unroll
-        for (int b = 0; b < HN; ++b) pass = pass || fmaxf(fmaxf(x[b][0].x, x[b][0].y), fmaxf(x[b][1].x, x[b][1].y)) > m[b] + kMoveLog2;
+        for (int b = 0; b < HN; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float& z = x[b][e >> 1][e & 1];
+            z = fmaf(z, sc[b][e & 1], -m[b][e & 1]);
+            most = fmaxf(most, z);
+          }
         const uint32_t vt = __byte_perm(__float_as_uint(vtop), 0u, 0x3232);   // its upper half twice
         uint32_t top = vt;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int j = 0; j < G; j += 2) top = __vimax3_u16x2(top, sb[n][j], sb[n][j + 1]);
-        if (__any_sync(0xffffffffu, pass || top != vt)) {
+        if (__any_sync(0xffffffffu, fresh || most > kMoveLog2 || top != vt)) {
           // scales that are NaN say nothing of the others
           top = 0u;
 #pragma unroll
@@ -451,33 +464,33 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
             vtop = v;
           }
 #pragma unroll
-          for (int b = 0; b < HN; ++b) {
-            float y = fmaxf(fmaxf(x[b][0].x, x[b][0].y), fmaxf(x[b][1].x, x[b][1].y));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-            const float n = y > m[b] + kMoveLog2 ? y : m[b];
-            const float a = n == m[b] ? 1.f : ex2f(m[b] - n);
-            m[b] = n;
-            l[b] *= a;
-            // of heads 2 t4 and 2 t4 + 1: rows of the lanes 8 t4 and 8 t4 + 4
-            const float a0 = __shfl_sync(0xffffffffu, a, 8 * t4) * all, a1 = __shfl_sync(0xffffffffu, a, 8 * t4 + 4) * all;
+          for (int b = 0; b < HN; ++b)
 #pragma unroll
-            for (int j = 0; j < G; ++j)
+            for (int e = 0; e < 2; ++e) {
+              float y = fmaxf(x[b][0][e], x[b][1][e]);   // above the offset, by the tokens of all lanes
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[b][j][e] *= e & 1 ? a1 : a0;
-          }
+              for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+              const bool move = fresh || y > kMoveLog2;
+              const float up = move ? y : 0.f, a = move ? ex2f(-y) : 1.f;
+              m[b][e] += up;
+              x[b][0][e] -= up, x[b][1][e] -= up;
+              l[b][e] *= a;
+#pragma unroll
+              for (int j = 0; j < G; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[b][j][2 * i + e] = fresh ? 0.f : o[b][j][2 * i + e] * (a * all);
+            }
+          fresh = false;
         }
         const float lift = __uint_as_float(kLiftBits - __float_as_uint(vtop));   // 2^7 / vtop
 #pragma unroll
-        for (int b = 0; b < HN; ++b) {
-          const float f = m[b] == -INFINITY ? 0.f : m[b];
+        for (int b = 0; b < HN; ++b)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float2 y = make_float2(ex2f(x[b][n].x - f), ex2f(x[b][n].y - f));
-            l[b] += y.x + y.y;
-            x[b][n] = mul2(y, make_float2(lift, lift));
+          for (int e = 0; e < 4; ++e) {
+            const float y = ex2f(x[b][e >> 1][e & 1]);
+            l[b][e & 1] += y;
+            x[b][e >> 1][e & 1] = y * lift;
           }
-        }
         uint32_t vw[2][G];
 #pragma unroll
         for (int n = 0; n < 2; ++n) lds_words<G>(va + (n * 32 + lane) * G * 4, vw[n]);
@@ -495,11 +508,11 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
           }
 #pragma unroll
           for (int b = 0; b < HN; ++b) {
-            uint32_t pw[2];
+            uint32_t pw[2];   // weights of this group, columns now: tokens 2 t4, 2 t4 + 1 (and 8 more) of head g8
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-              const float2 y = mul2(x[b][n], scales(sb[n][j]));
-              pw[n] = pack_f16(y.x, y.y);
+              const float y = __uint_as_float(__byte_perm(sb[n][j], 0u, pick));
+              pw[n] = transpose8(pack_f16(x[b][n][0] * y, x[b][n][1] * y));
             }
             float(&lo)[4] = *reinterpret_cast<float(*)[4]>(&o[b][j][0]);
             float(&hi)[4] = *reinterpret_cast<float(*)[4]>(&o[b][j][4]);
@@ -524,9 +537,12 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
     const size_t slot = (size_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0);
 #pragma unroll
     for (int b = 0; b < HN; ++b) {
-      l[b] += __shfl_xor_sync(0xffffffffu, l[b], 1);
-      l[b] += __shfl_xor_sync(0xffffffffu, l[b], 2);
-      if (t4 == 0) s_ml[warp * kRows + 8 * b + g8] = make_float2(m[b], l[b]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
+        if (g8 == 0) s_ml[warp * kRows + 8 * b + 2 * t4 + e] = make_float2(fresh ? -INFINITY : m[b][e], l[b][e]);
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {   // head 8 b + 2 t4 + e, dimensions 32 j + 4 g8 .. + 3: chunks turned by the head, no bank twice
         float* dst = s_red + ((size_t)warp * L::HEADS + 8 * b + 2 * t4 + e) * D + ((g8 + 2 * t4) & 7) * 4;
@@ -552,7 +568,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
       for (int w = 0; w < nw; ++w) {
         const float2 x = s_ml[(w0 + w) * kRows + row];
         const float4 v = *reinterpret_cast<const float4*>(src + (size_t)w * L::HEADS * D);
-        const float f = x.x == -INFINITY ? 1.f : ex2f(x.x - M);   // (no token: zeros; or scores that are no numbers)
+        const float f = ex2f(x.x - M);
         sum = fmaf(x.y, f, sum);
         acc.x = fmaf(v.x, f, acc.x);
         acc.y = fmaf(v.y, f, acc.y);
