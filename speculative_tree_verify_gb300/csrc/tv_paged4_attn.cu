@@ -16,8 +16,8 @@
 // - Both products have the codes as the operand of 16 rows and 8 heads as columns
 //   (S^T = K Q^T, O^T += V^T P^T): up to 8 heads a KV head cost half of what 16 do.
 //   S^T begins at -8 sum q instead of zero, a group of 32 dimensions at a time, and
-//   each group's sum takes the token's scale; V's codes less 8 are one packed
-//   subtraction.
+//   each group's sum takes the token's scale; V's 8 goes by a product of the weights
+//   with a constant, which costs less than 32 packed subtractions did.
 // - A token's V scale goes into its weight, four weights of fp16 a token (one a
 //   group), so that V needs no product.  The weights are relative to the largest
 //   scale so far, as they are to the offset: 2^15 at most, 2^-24 at least.
@@ -25,7 +25,7 @@
 // How the work is cut over CTAs is in tv_paged_runs.cuh.  In a CTA four warps look
 // up pages (32 boxes' entries at a time, the next 32 on their way) and copy whole
 // blocks into a ring of stages, each every fourth tile (one warp alone takes 1200
-// cycles a tile); the others compute, tile t by warps 4 (t mod quads) .. + 3, 16
+// cycles a tile); the others compute, tile t by warps 2 (t mod teams) and the next, 32
 // tokens each.
 #include <cmath>
 #include <type_traits>
@@ -43,16 +43,19 @@ constexpr int kLoadWarps = 4;
 constexpr int kQueries = 8;                      // runs whose queries are loaded ahead, at most
 constexpr int kSegCost = 3;                      // what a head block costs besides its tiles, in tiles
 constexpr float kMoveLog2 = 8.f;                 // offsets move when a score passes them by this
-constexpr uint32_t kLiftBits = (127u + 127u + 7u) << 23;   // weights times scales up to 2^15; less a power of two's bits
 
 // HN: blocks of 8 heads
 template <int D, int HN>
 struct P4 {
   using B = Block4<D>;
   static constexpr int WARPS = HN == 1 ? 12 : 8;   // that compute; the accumulators of 16 heads need the other half's registers
-  static constexpr int QUADS = WARPS / 4;
+  static constexpr int TEAMS = WARPS / 2;          // two warps a tile, two blocks of 16 tokens each
   static constexpr int THREADS = 32 * (WARPS + kLoadWarps);
   static constexpr int HEADS = 8 * HN;
+  // registers: the launch's, and how its warpgroups divide them
+  static constexpr int REGS = 65536 / THREADS / 8 * 8, LOAD_REGS = 72;
+  static constexpr int COMP_REGS = (REGS * THREADS - LOAD_REGS * 32 * kLoadWarps) / (32 * WARPS) / 8 * 8;
+  static_assert(COMP_REGS * 32 * WARPS + LOAD_REGS * 32 * kLoadWarps <= REGS * THREADS, "registers of the launch");
   static constexpr int HALF = kTile / 16 * B::BYTES;   // a tile's K (or V)
   static constexpr int STAGE = 2 * HALF;
   static constexpr int OFF_RED = kStages * STAGE;      // [WARPS][HEADS][D] fp32; the marks of listed rows first
@@ -62,7 +65,7 @@ struct P4 {
   static constexpr int OFF_BAR = OFF_Q + 2 * kRows * Q_ROW;
   static constexpr int OFF_FIRST = OFF_BAR + 512;
   static size_t bytes(int n) { return 128 + OFF_FIRST + (size_t)(n + 1) * 4 + (n <= kInfo ? (size_t)n * 8 : 0); }
-  static_assert(kStages % QUADS == 0, "a stage always belongs to the same four warps");
+  static_assert(kStages % TEAMS == 0, "a stage always belongs to the same two warps");
   static_assert((2 * kStages + 2 * kQueries) * 8 <= 512, "barriers");
   static_assert(WARPS * HEADS * D * 4 >= kMaxSeqs / 8, "a mark for every table row");
   static_assert(128 + OFF_FIRST + (kMaxTokens + 1) * 4 <= 232448 - 512, "shared memory of one CTA");
@@ -81,30 +84,18 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 // an 8 x 8 matrix of 16-bit values, a row to four lanes, transposed
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
-// mbar_wait of warps with nothing to do meanwhile: asleep up to 2 us at a time,
-// so that they do not take issue slots from those that compute
+// mbar_wait of warps with nothing to do meanwhile: asleep between looks, so that
+// they do not take issue slots from those that compute
 __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
-  for (uint32_t n = 0; n < (uint32_t)(kWaitLimitNs / 2000); ++n) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
-        : "memory");
-    if (done) return true;
+  for (uint32_t n = 0; n < (uint32_t)(kWaitLimitNs / 1000); ++n) {   // (a sleep is up to twice as long)
+    if (mbar_test(bar, parity)) return true;
+    __nanosleep(500);
   }
   return mbar_wait(bar, parity);
 }
@@ -121,7 +112,7 @@ template <int D, int HN>
 __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(const __grid_constant__ PaParams p) {
   using L = P4<D, HN>;
   using B = Block4<D>;
-  constexpr int G = B::G, NW = L::WARPS, NQ = L::QUADS;
+  constexpr int G = B::G, NW = L::WARPS, NT = L::TEAMS, NS = 2;   // NS: blocks of 16 tokens of a warp's tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
@@ -141,7 +132,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 4);   // the four warps that compute its tile
+      mbar_init(&empty[s], 2);   // the two warps that compute its tile
     }
     for (int s = 0; s < kQueries; ++s) {
       mbar_init(&q_full[s], 1);
@@ -169,6 +160,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
 
   if (warp >= NW) {
     // ---------------- pages and loads ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::LOAD_REGS));
     const int mine = warp - NW;                            // every fourth tile, every fourth run's queries
     const int R = ps < kTile ? ps : kTile;                 // tokens of a box
     const int nsh = 6 - (31 - __clz(R)), nb = 1 << nsh;    // boxes of a tile
@@ -254,23 +246,24 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
   }
 
   // ---------------- compute warps ----------------
-  const int quad = warp >> 2, sl = warp & 3;        // tiles with (count mod NQ) == quad; tokens 16 sl .. + 15 of a tile
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::COMP_REGS));
+  const int team = warp >> 1, first = 32 * (warp & 1);   // tiles with (count mod NT) == team; tokens first .. + 31 of a tile
   const int g8 = lane >> 2, t4 = lane & 3;
   const uint32_t pick = g8 & 1 ? 0x3244u : 0x1044u;   // of a word of two bf16, token g8's as fp32
   auto meet = [&](int nw) {
-    asm volatile("bar.sync %0, %1;" ::"r"(nw == NW ? 1 : 2 + quad), "r"(32 * nw) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(nw == NW ? 1 : 2 + team), "r"(32 * nw) : "memory");
   };
   bool ok = true;
   // this warp's next tile and the CTA's next queries: places in the rings, parities
-  int st = quad, qs = 0;
+  int st = team, qs = 0;
   uint32_t st_par = 0u, qs_par = 0u;
-  int turn = quad;   // tiles of the CTA until its next one
+  int turn = team;   // tiles of the CTA until its next one
   Run g;
   for (bool have = runs.first_run(g); have; have = runs.next_run(g)) {
     const int h = g.h, r0 = g.hb * kRows;   // KV head, first query head of the block in the group
     const int nr = min(kRows, p.G - r0);
     if (ok && !mbar_wait(&q_full[qs], qs_par)) ok = false;
-    if (g.T == 1 && turn > 0) {   // one tile, and another four warps'
+    if (g.T == 1 && turn > 0) {   // one tile, and another team's
       // (no further ahead than the queries, nor further behind than their place:
       // it is not loaded again before these warps, too, have seen this phase)
       __syncwarp();
@@ -327,11 +320,14 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
     }
     // O^T: o[8 heads][j][0 .. 3] rows 32 j + 4 g8, that and 16 times the next, heads 2 t4, 2 t4 + 1; [4 .. 7]: two rows more
     float o[HN][G][8];
-    float m[HN][2], l[HN][2];    // their offsets, and sums of this thread's tokens
+    // Weights are 2^(score - off) and go up to 2^limit: off is the head's offset less
+    // what lifts the weights to fp16's range beside the scales, limit = 15 - log2 vtop.
+    float off[HN][2], l[HN][2];  // l: sums of this thread's tokens
     float vtop = 0x1p-100f;      // power of two above the scales of V so far
+    float limit = 115.f;
 #pragma unroll
     for (int b = 0; b < HN; ++b) {
-      m[b][0] = m[b][1] = 0.f, l[b][0] = l[b][1] = 0.f;
+      off[b][0] = off[b][1] = 0.f, l[b][0] = l[b][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < G; ++j)
 #pragma unroll
@@ -340,62 +336,57 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
 
     bool fresh = true;           // no token so far
     int t = g.t0 + turn;
-    for (; t < g.t1; t += NQ) {
-      uint8_t* sk = smem + st * L::STAGE + sl * B::BYTES;
+    for (; t < g.t1; t += NT) {
+      uint8_t* sk = smem + st * L::STAGE + first / 16 * B::BYTES;
       uint8_t* sv = sk + L::HALF;
       if (ok && !mbar_wait(&full[st], st_par)) ok = false;
       const uint32_t ka = smem_u32(sk), va = ka + L::HALF;
-      // Which of the warp's tokens are seen: all of them but in a sequence's last
-      // tile, the window's first and the sinks' last.
-      int tok0 = 0, valid = 16, hide0 = 0, hide1 = 0;   // the first; those in the sequence; from hide0 up to hide1 hidden
+      // All of the warp's tokens are seen but in a sequence's last tile, the
+      // window's first and the sinks' last.
       const bool special = t == g.T - 1 || (g.lo > 0 && (t == g.sink_tiles || t == g.sink_tiles - 1));
+      const int tok0 = special ? g.tile<true>(t) * kTile + first : 0;
+      auto out = [&](int tok) { return tok >= g.len || (tok >= p.sinks && tok < g.lo); };
       bool wrote = false;
-      if (special) {
-        tok0 = g.tile<true>(t) * kTile + 16 * sl;
-        valid = min(16, g.len - tok0);
-        hide0 = max(0, p.sinks - tok0), hide1 = min(16, g.lo - tok0);
-        if (hide0 == 0 && hide1 >= valid) valid = 0;
-        if (valid > 0 && p.k_new && tok0 + valid == g.len) {
-          // the new token: its codes into the tile and into the page
-          const bool is_v = lane >= 16;
-          const int c = lane & 15, tk = valid - 1, half = tk % 2 * 2;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (c < D / 8)
-            x = __ldcg(reinterpret_cast<const uint4*>((is_v ? p.v_new : p.k_new) + (size_t)g.i * p.kv_stride + (size_t)h * D) + c);
-          uint32_t scale;
-          const uint32_t w = round4(x, scale);
-          const int page = __ldcg(p.seqs.pages + (size_t)g.s * p.seqs.max_pages + (g.len - 1) / ps);
-          const bool store = r0 == 0 && page >= 0 && page < p.pool.n_pages;
-          if (c < D / 8) {
-            auto put = [&](uint8_t* block) {
-              if (is_v) {
-                *reinterpret_cast<uint16_t*>(block + B::v_word(tk, 2 * c) + half) = (uint16_t)w;
-                *reinterpret_cast<uint16_t*>(block + B::v_word(tk, 2 * c + 1) + half) = (uint16_t)(w >> 16);
-              } else {
-                *reinterpret_cast<uint32_t*>(block + B::k_word(tk, c)) = w;
-              }
-              if (c % 4 == 0) *reinterpret_cast<uint16_t*>(block + B::scale(tk, c / 4) + half) = (uint16_t)scale;
-            };
-            put(is_v ? sv : sk);
-            if (store)
-              put(reinterpret_cast<uint8_t*>(is_v ? p.pool.v : p.pool.k) +
-                  ((((size_t)p.layer * p.pool.n_pages + page) * Hkv + h) * ps + (g.len - 1) % ps / 16 * 16) / 16 * B::BYTES);
-          }
-          wrote = true;
-          __syncwarp();
+      if (special && p.k_new && tok0 < g.len && tok0 + 32 >= g.len) {
+        // the new token: its codes into the tile and into the page
+        const bool is_v = lane >= 16;
+        const int c = lane & 15, at = g.len - 1, tk = at & 15, half = tk % 2 * 2;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (c < D / 8)
+          x = __ldcg(reinterpret_cast<const uint4*>((is_v ? p.v_new : p.k_new) + (size_t)g.i * p.kv_stride + (size_t)h * D) + c);
+        uint32_t scale;
+        const uint32_t w = round4(x, scale);
+        const int page = __ldcg(p.seqs.pages + (size_t)g.s * p.seqs.max_pages + at / ps);
+        if (c < D / 8) {
+          auto put = [&](uint8_t* block) {
+            if (is_v) {
+              *reinterpret_cast<uint16_t*>(block + B::v_word(tk, 2 * c) + half) = (uint16_t)w;
+              *reinterpret_cast<uint16_t*>(block + B::v_word(tk, 2 * c + 1) + half) = (uint16_t)(w >> 16);
+            } else {
+              *reinterpret_cast<uint32_t*>(block + B::k_word(tk, c)) = w;
+            }
+            if (c % 4 == 0) *reinterpret_cast<uint16_t*>(block + B::scale(tk, c / 4) + half) = (uint16_t)scale;
+          };
+          put((is_v ? sv : sk) + (at - tok0) / 16 * B::BYTES);
+          if (r0 == 0 && page >= 0 && page < p.pool.n_pages)
+            put(reinterpret_cast<uint8_t*>(is_v ? p.pool.v : p.pool.k) +
+                ((((size_t)p.layer * p.pool.n_pages + page) * Hkv + h) * ps + at % ps / 16 * 16) / 16 * B::BYTES);
         }
+        wrote = true;
+        __syncwarp();
       }
-      if (valid > 0) {
-        // Tokens of this thread, as rows of S^T: g8 (n = 0) and g8 + 8 (1).
-        float x[HN][2][2];   // [n][head]
-        uint32_t sb[2][G];   // scales of V: of g8 and its neighbour
-        {
+      if (!special || __any_sync(0xffffffffu, !out(tok0 + lane))) {
+        // Tokens of this thread, as rows of S^T: g8 (n = 0) and g8 + 8 (1) of each block.
+        float x[NS][HN][2][2];   // [n][head]
+        uint32_t sb[NS][2][G];   // scales of V: of g8 and its neighbour
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
           uint32_t w[2][G], sa[2][G];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            lds_words<G>(ka + (8 * n + g8) * (D / 2) + t4 * (D / 8), w[n]);
-            lds_words<G>(ka + B::OFF_SCALE + (n * 4 + (g8 >> 1)) * G * 4, sa[n]);
-            lds_words<G>(va + B::OFF_SCALE + (n * 4 + (g8 >> 1)) * G * 4, sb[n]);
+            lds_words<G>(ka + s * B::BYTES + (8 * n + g8) * (D / 2) + t4 * (D / 8), w[n]);
+            lds_words<G>(ka + s * B::BYTES + B::OFF_SCALE + (n * 4 + (g8 >> 1)) * G * 4, sa[n]);
+            lds_words<G>(va + s * B::BYTES + B::OFF_SCALE + (n * 4 + (g8 >> 1)) * G * 4, sb[s][n]);
           }
 #pragma unroll
           for (int j = 0; j < G; ++j) {
@@ -411,137 +402,156 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
                       c[1], c[2], c[3]);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                x[b][0][e] = j == 0 ? (c[e] + bias[b][j][e]) * s0 : fmaf(c[e] + bias[b][j][e], s0, x[b][0][e]);
-                x[b][1][e] = j == 0 ? (c[2 + e] + bias[b][j][e]) * s1 : fmaf(c[2 + e] + bias[b][j][e], s1, x[b][1][e]);
+                float(&y)[2][2] = x[s][b];
+                y[0][e] = j == 0 ? (c[e] + bias[b][j][e]) * s0 : fmaf(c[e] + bias[b][j][e], s0, y[0][e]);
+                y[1][e] = j == 0 ? (c[2 + e] + bias[b][j][e]) * s1 : fmaf(c[2 + e] + bias[b][j][e], s1, y[1][e]);
               }
             }
           }
         }
         if (special) {   // what is past the length or hidden: no score, and a scale of zero, whatever it holds
-          auto out = [&](int tk) { return tk >= valid || (tk >= hide0 && tk < hide1); };
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int tk = 8 * n + (g8 & ~1);
-            if (out(8 * n + g8))
+          for (int s = 0; s < NS; ++s)
 #pragma unroll
-              for (int b = 0; b < HN; ++b) x[b][n][0] = x[b][n][1] = -INFINITY;
-            const uint32_t keep = (out(tk) ? 0u : 0x0000ffffu) | (out(tk + 1) ? 0u : 0xffff0000u);
+            for (int n = 0; n < 2; ++n) {
+              const int tok = tok0 + 16 * s + 8 * n + (g8 & ~1);
+              const bool even = out(tok), odd = out(tok + 1);
+              if (g8 & 1 ? odd : even)
 #pragma unroll
-            for (int j = 0; j < G; ++j) sb[n][j] &= keep;
-          }
+                for (int b = 0; b < HN; ++b) x[s][b][n][0] = x[s][b][n][1] = -INFINITY;
+              const uint32_t keep = (even ? 0u : 0x0000ffffu) | (odd ? 0u : 0xffff0000u);
+#pragma unroll
+              for (int j = 0; j < G; ++j) sb[s][n][j] &= keep;
+            }
         }
-        // exponents relative to the offsets, which move when passed, as the largest scale does, hardly ever
+        // exponents; the offsets move when passed, as the largest scale does, hardly ever
         float most = -INFINITY;
-#pragma unroll
-        for (int b = 0; b < HN; ++b)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float& z = x[b][e >> 1][e & 1];
-            z = fmaf(z, sc[b][e & 1], -m[b][e & 1]);
-            most = fmaxf(most, z);
-          }
         const uint32_t vt = __byte_perm(__float_as_uint(vtop), 0u, 0x3232);   // its upper half twice
         uint32_t top = vt;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int s = 0; s < NS; ++s) {
 #pragma unroll
-          for (int j = 0; j < G; j += 2) top = __vimax3_u16x2(top, sb[n][j], sb[n][j + 1]);
-        if (__any_sync(0xffffffffu, fresh || most > kMoveLog2 || top != vt)) {
-          // scales that are NaN say nothing of the others
-          top = 0u;
+          for (int b = 0; b < HN; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float& z = x[s][b][e >> 1][e & 1];
+              z = fmaf(z, sc[b][e & 1], -off[b][e & 1]);
+              most = fmaxf(most, z);
+            }
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-              const uint32_t a = sb[n][j] & 0xffffu, b = sb[n][j] >> 16;
-              top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
-            }
+            for (int j = 0; j < G; j += 2) top = __vimax3_u16x2(top, sb[s][n][j], sb[s][n][j + 1]);
+        }
+        if (__any_sync(0xffffffffu, fresh || most > limit || top != vt)) {
+          // scales that are NaN say nothing of the others
+          top = 0u;
+#pragma unroll
+          for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int j = 0; j < G; ++j) {
+                const uint32_t a = sb[s][n][j] & 0xffffu, b = sb[s][n][j] >> 16;
+                top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+              }
           top = __reduce_max_sync(0xffffffffu, top);
-          float all = 1.f;
+          float down = 0.f;   // log2 of vtop's growth
           if (__uint_as_float(top << 16) > vtop) {   // to the next power of two
-            const float v = __uint_as_float(((top >> 7) + 1u) << 23);
-            all = vtop / v;
-            vtop = v;
+            down = (float)((int)(top >> 7) + 1 - (int)(__float_as_uint(vtop) >> 23));
+            vtop = __uint_as_float(((top >> 7) + 1u) << 23);
+            limit -= down;
           }
 #pragma unroll
           for (int b = 0; b < HN; ++b)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float y = fmaxf(x[b][0][e], x[b][1][e]);   // above the offset, by the tokens of all lanes
+              float y = -INFINITY;   // the largest, by the tokens of all lanes
+#pragma unroll
+              for (int s = 0; s < NS; ++s) y = fmaxf(y, fmaxf(x[s][b][0][e], x[s][b][1][e]));
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-              const bool move = fresh || y > kMoveLog2;
-              const float up = move ? y : 0.f, a = move ? ex2f(-y) : 1.f;
-              m[b][e] += up;
-              x[b][0][e] -= up, x[b][1][e] -= up;
-              l[b][e] *= a;
+              y -= down;
+              // the offset to 2^kMoveLog2 above the largest, or as it was
+              const float up = (fresh || y > limit ? y - (limit - kMoveLog2) : 0.f) + down, a = ex2f(-up);
+              off[b][e] += up;
+#pragma unroll
+              for (int s = 0; s < NS; ++s) x[s][b][0][e] -= up, x[s][b][1][e] -= up;
+              l[b][e] = fresh ? 0.f : l[b][e] * a;
 #pragma unroll
               for (int j = 0; j < G; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[b][j][2 * i + e] = fresh ? 0.f : o[b][j][2 * i + e] * (a * all);
+                for (int i = 0; i < 4; ++i) o[b][j][2 * i + e] = fresh ? 0.f : o[b][j][2 * i + e] * a;
             }
           fresh = false;
         }
-        const float lift = __uint_as_float(kLiftBits - __float_as_uint(vtop));   // 2^7 / vtop
 #pragma unroll
-        for (int b = 0; b < HN; ++b)
+        for (int s = 0; s < NS; ++s) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y = ex2f(x[b][e >> 1][e & 1]);
-            l[b][e & 1] += y;
-            x[b][e >> 1][e & 1] = y * lift;
-          }
-        uint32_t vw[2][G];
+          for (int b = 0; b < HN; ++b)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) lds_words<G>(va + (n * 32 + lane) * G * 4, vw[n]);
+            for (int e = 0; e < 4; ++e) {
+              float& y = x[s][b][e >> 1][e & 1];
+              y = ex2f(y);
+              l[b][e & 1] += y;
+            }
+          uint32_t vw[2][G];
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-          // rows of V^T: dimensions 4 g8, that and 16 times the next, two more; columns: tokens 2 t4, 2 t4 + 1 and 8 more
-          uint32_t a[4][2];
+          for (int n = 0; n < 2; ++n) lds_words<G>(va + s * B::BYTES + (n * 32 + lane) * G * 4, vw[n]);
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const uint32_t w = vw[n][j], u1 = __byte_perm(w, 0u, 0x4341);
-            a[0][n] = sub_f16(w & 0x000f000fu, 0x00080008u);
-            a[1][n] = sub_f16(w & 0x00ff00ffu, 0x00880088u);
-            a[2][n] = sub_f16(u1 & 0x000f000fu, 0x00080008u);
-            a[3][n] = sub_f16(u1, 0x00880088u);
-          }
-#pragma unroll
-          for (int b = 0; b < HN; ++b) {
-            uint32_t pw[2];   // weights of this group, columns now: tokens 2 t4, 2 t4 + 1 (and 8 more) of head g8
+          for (int j = 0; j < G; ++j) {
+            // rows of V^T: dimensions 4 g8, that and 16 times the next, two more; columns: tokens 2 t4, 2 t4 + 1 and 8 more
+            uint32_t a[4][2];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-              const float y = __uint_as_float(__byte_perm(sb[n][j], 0u, pick));
-              pw[n] = transpose8(pack_f16(x[b][n][0] * y, x[b][n][1] * y));
+              const uint32_t w = vw[n][j], u1 = __byte_perm(w, 0u, 0x4341);
+              a[0][n] = w & 0x000f000fu;
+              a[1][n] = w & 0x00ff00ffu;
+              a[2][n] = u1 & 0x000f000fu;
+              a[3][n] = u1;
             }
-            float(&lo)[4] = *reinterpret_cast<float(*)[4]>(&o[b][j][0]);
-            float(&hi)[4] = *reinterpret_cast<float(*)[4]>(&o[b][j][4]);
-            mma_f16(lo, a[0][0], a[1][0], a[0][1], a[1][1], pw[0], pw[1], lo[0], lo[1], lo[2], lo[3]);
-            mma_f16(hi, a[2][0], a[3][0], a[2][1], a[3][1], pw[0], pw[1], hi[0], hi[1], hi[2], hi[3]);
+#pragma unroll
+            for (int b = 0; b < HN; ++b) {
+              uint32_t pw[2];   // weights of this group, columns now: tokens 2 t4, 2 t4 + 1 (and 8 more) of head g8
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+                const float y = __uint_as_float(__byte_perm(sb[s][n][j], 0u, pick));
+                pw[n] = transpose8(pack_f16(x[s][b][n][0] * y, x[s][b][n][1] * y));
+              }
+              float(&lo)[4] = *reinterpret_cast<float(*)[4]>(&o[b][j][0]);
+              float(&hi)[4] = *reinterpret_cast<float(*)[4]>(&o[b][j][4]);
+              mma_f16(lo, a[0][0], a[1][0], a[0][1], a[1][1], pw[0], pw[1], lo[0], lo[1], lo[2], lo[3]);
+              mma_f16(hi, a[2][0], a[3][0], a[2][1], a[3][1], pw[0], pw[1], hi[0], hi[1], hi[2], hi[3]);
+              // less 8 (and 8 + 16 * 8) of every code
+              mma_f16(lo, 0x80088008u, 0x80888088u, 0x80088008u, 0x80888088u, pw[0], pw[1], lo[0], lo[1], lo[2], lo[3]);
+              mma_f16(hi, 0x80088008u, 0x80888088u, 0x80088008u, 0x80888088u, pw[0], pw[1], hi[0], hi[1], hi[2], hi[3]);
+            }
           }
         }
         if (wrote) fence_async_smem();   // before the stage takes another copy
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
-      if ((st += NQ) >= kStages) st = quad, st_par ^= 1u;
+      if ((st += NT) >= kStages) st = team, st_par ^= 1u;
     }
     turn = t - g.t1;
 
     // ---- the head block's partial results into one ----
-    // of all warps, or, where the head block is one tile, of the four that had
+    // of all warps, or, where the head block is one tile, of the two that had
     // it: the others go on to the next head block meanwhile
     const bool whole = g.t0 == 0 && g.t1 == g.T;
-    const int nw = g.T > 1 ? NW : 4, w0 = g.T > 1 ? 0 : 4 * quad, me = tid - 32 * w0;
+    const int nw = g.T > 1 ? NW : 2, w0 = g.T > 1 ? 0 : 2 * team, me = tid - 32 * w0;
     // a CTA's first run may begin inside a head block, its last end inside one
     const size_t slot = (size_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0);
+    // the weights' lift, 2^7 / vtop, is the offset's again
+    const float lift = limit - kMoveLog2, unlift = __uint_as_float(__float_as_uint(vtop) - (7u << 23));
 #pragma unroll
     for (int b = 0; b < HN; ++b) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
-        if (g8 == 0) s_ml[warp * kRows + 8 * b + 2 * t4 + e] = make_float2(fresh ? -INFINITY : m[b][e], l[b][e]);
+        if (g8 == 0) s_ml[warp * kRows + 8 * b + 2 * t4 + e] = make_float2(fresh ? -INFINITY : off[b][e] + lift, l[b][e] * unlift);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {   // head 8 b + 2 t4 + e, dimensions 32 j + 4 g8 .. + 3: chunks turned by the head, no bank twice
@@ -597,6 +607,14 @@ template <int D, int HN>
 int launch_paged4(const PaParams& p, int ctas, cudaStream_t st) {
   static std::atomic<bool> attr[64];
   if (ensure_smem_limit(paged4_attn_kernel<D, HN>, P4<D, HN>::bytes(kMaxTokens), attr)) return TV_E_CUDA;
+  // the split of the registers must not ask for more than the launch brings
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, paged4_attn_kernel<D, HN>) != cudaSuccess) return TV_E_CUDA;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) < P4<D, HN>::REGS) return TV_E_UNSUPPORTED;
   const int rc = launch_pdl(paged4_attn_kernel<D, HN>, dim3(ctas), dim3(P4<D, HN>::THREADS), P4<D, HN>::bytes(p.n), st, p);
   return rc ? rc : launch_paged_merge(p, ctas, st);
 }
