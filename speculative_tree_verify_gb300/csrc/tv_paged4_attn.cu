@@ -39,7 +39,11 @@ namespace tv {
 namespace {
 
 constexpr int kStages = 12;                      // tiles in flight: 108 KB at D = 128
+// Each has every fourth tile, so that a stage (and a place of the queries) always
+// belongs to the same warp: its waits then see every phase of the place's
+// barrier, and a parity can not name the phase before last.
 constexpr int kLoadWarps = 4;
+static_assert(kStages % kLoadWarps == 0, "a stage always belongs to the same loading warp");
 constexpr int kQueries = 8;                      // runs whose queries are loaded ahead, at most
 constexpr int kSegCost = 3;                      // what a head block costs besides its tiles, in tiles
 constexpr float kMoveLog2 = 8.f;                 // offsets move when a score passes them by this
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
   if (warp >= NW) {
     // ---------------- pages and loads ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::LOAD_REGS));
-    const int mine = warp - NW;                            // every fourth tile, every fourth run's queries
+    const int mine = warp - NW;                            // tiles with (count mod kLoadWarps) == mine, and places of queries
     const int R = ps < kTile ? ps : kTile;                 // tokens of a box
     const int nsh = 6 - (31 - __clz(R)), nb = 1 << nsh;    // boxes of a tile
     const int psh = 31 - __clz(ps), per = 32 >> nsh;       // tiles of 32 boxes
@@ -191,8 +195,8 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
     while (have && ok) {
       Run next = g;   // the next entries are on their way before this run's tiles
       const bool more = runs.next_run(next);
-      if (segs % kLoadWarps == mine) {   // its queries
-        const int qs = segs % qslots;
+      const int qs = segs % qslots;
+      if (qs % kLoadWarps == mine) {   // its queries
         if (segs >= qslots) wait(&q_free[qs], (uint32_t)(segs / qslots - 1));
         if (!ok) break;
         const int r0 = g.hb * kRows, nr = min(kRows, p.G - r0);
@@ -238,10 +242,12 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
       have = more;
     }
     if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
-    // loads in flight land before the CTA leaves: with all of its warps, whose
-    // tiles and queries these are; what a timeout left unissued is not waited for
-    for (int u = max(0, segs - qslots); ok && u < segs; ++u) wait(&q_full[u % qslots], (uint32_t)(u / qslots));
-    for (int u = max(0, count - kStages); ok && u < count; ++u) wait(&full[u % kStages], (uint32_t)(u / kStages));
+    // loads in flight land before the CTA leaves: each warp has armed the
+    // barriers of its own, and what a timeout left unissued is not waited for
+    for (int u = max(0, segs - qslots); ok && u < segs; ++u)
+      if (u % qslots % kLoadWarps == mine) wait(&q_full[u % qslots], (uint32_t)(u / qslots));
+    for (int u = max(0, count - kStages); ok && u < count; ++u)
+      if (u % kLoadWarps == mine) wait(&full[u % kStages], (uint32_t)(u / kStages));
     return;
   }
 

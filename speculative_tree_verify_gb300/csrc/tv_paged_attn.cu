@@ -6,9 +6,10 @@
 // heads, far below the tensor cores' rate, so the kernel is built as a stream
 // over memory; how it is cut over the CTAs is in tv_paged_runs.cuh.
 //
-// In a CTA one warp looks up pages and issues TMA loads (a page's tokens of
-// one head are contiguous: boxes of min(page, 64) rows x 64 values, 128-byte
-// swizzle) into a ring of stages; eight warps compute, tile t by warps
+// In a CTA three warps look up pages (32 boxes' entries at a time, the next 32 on
+// their way) and issue TMA loads (a page's tokens of one head are contiguous:
+// boxes of min(page, 64) rows x 64 values, 128-byte swizzle) into a ring of
+// stages, each every third tile; eight warps compute, tile t by warps
 // 4 (t mod 2) .. + 3, 16 tokens each, with mma.sync m16n8k16: the query heads
 // are the 16 rows (a KV head's 5 or so need no 128-row tile, and the tokens of
 // a warp need no other warp until the head ends).  S = Q K^T leaves each
@@ -44,7 +45,12 @@ constexpr int kStages = 6;
 static_assert(kStages % 2 == 0, "tile t: stage t mod kStages, warps 4 (t mod 2) .. + 3");
 constexpr int kCompWarps = 8;
 constexpr int kCompThreads = kCompWarps * 32;
-constexpr int kPaThreads = kCompThreads + 32;
+// Each has every third tile, so that a stage (and a place of the queries) always
+// belongs to the same warp: its waits then see every phase of the place's
+// barrier, and a parity can not name the phase before last.
+constexpr int kLoadWarps = 3;
+static_assert(kStages % kLoadWarps == 0, "a stage always belongs to the same loading warp");
+constexpr int kPaThreads = kCompThreads + 32 * kLoadWarps;
 constexpr int kQueries = 8;                      // segments whose queries are loaded ahead, at most
 constexpr int kRedRows = 4;                      // rows joined at a time when a head block ends
 // What a head block costs besides its tiles, in tiles (its queries, its join).
@@ -217,75 +223,84 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   if (tid == 0) p.ws.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (runs.lo >= runs.hi) return;
 
-  if (warp == kCompWarps) {
+  if (warp >= kCompWarps) {
     // ---------------- pages and loads ----------------
+    const int mine = warp - kCompWarps;             // tiles with (count mod kLoadWarps) == mine, and places of queries
     const int R = ps < kTile ? ps : kTile;          // rows of a box
-    const int nb = kTile / R;                       // boxes of a tile's K slab
+    const int nsh = 6 - (31 - __clz(R)), nb = 1 << nsh;   // boxes of a tile's K slab
+    const int psh = 31 - __clz(ps), per = 32 >> nsh;      // tiles of 32 boxes
     constexpr int kPer = 2 * (D / 64);              // K and V slabs of a box
     const int box = lane / kPer, which = lane % kPer;
     const bool is_v = which >= D / 64;
     const int slab = which % (D / 64);
     const uint64_t pol = policy_evict_first();
+    const int y0 = p.layer * p.pool.n_pages;   // the host has seen to it that a row of the pool is an int
     bool ok = true;
-    int issued = 0, segs = 0, st = 0, qs = 0;   // tiles and queries loaded so far, their places in the rings
-    uint32_t st_par = 1u, qs_par = 1u;          // of the wait before a place is used again (not in the first round)
-    const int psh = 31 - __clz(ps);
+    int count = 0, segs = 0;   // tiles and runs so far, anyone's
+    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u)); };
     // a box of tokens tok .. tok + R - 1 holds something that is seen
     auto seen = [&](const Run& g, int tok) {
-      return box < nb && tok < g.len && (!WIN || tok >= g.lo - (R - 1) || tok < p.sinks);
+      return tok < g.len && (!WIN || tok >= g.lo - (R - 1) || tok < p.sinks);
     };
-    auto entry = [&](const Run& g, int t) {   // this lane's page of tile t, -1 past the length
-      const int tok = g.tile<WIN>(t) * kTile + box * R;
+    auto entry = [&](const Run& g, int tb) {   // the page of this lane's box of tiles tb ..., -1: not seen
+      const int t = tb + (lane >> nsh);
+      if (t >= g.t1) return -1;
+      const int tok = g.tile<WIN>(t) * kTile + (lane & (nb - 1)) * R;
       return seen(g, tok) ? __ldcg(p.seqs.pages + (size_t)g.s * p.seqs.max_pages + (tok >> psh)) : -1;
     };
     Run g;
     bool have = runs.first_run(g);
-    int page = have ? entry(g, g.t0) : -1;
+    int pages = have ? entry(g, g.t0) : -1;
     while (have && ok) {
-      Run next = g;   // the next run's first pages are on their way before this one's tiles
+      Run next = g;   // the next entries are on their way before this run's tiles
       const bool more = runs.next_run(next);
-      const int next_page = more ? entry(next, next.t0) : -1;
-      // its queries
-      if (segs >= qslots) ok = __all_sync(0xffffffffu, mbar_wait(&q_free[qs], qs_par));
-      if (!ok) break;
-      const int r0 = g.hb * kRows, nr = min(kRows, p.G - r0);
-      if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], (uint32_t)(nr * D * 2));
-      __syncwarp();
-      if (lane < nr)
-        bulk_load(smem + L::OFF_Q + (qs * qrows + lane) * L::Q_ROW,
-                  p.q + (size_t)g.i * p.q_stride + (size_t)(g.h * p.G + r0 + lane) * D, D * 2, &q_full[qs]);
-      ++segs;
-      if (++qs == qslots) qs = 0, qs_par ^= 1u;
-      const int y0 = p.layer * p.pool.n_pages;   // the host has seen to it that a row of the pool is an int
-      for (int t = g.t0; t < g.t1; ++t) {
-        const int tok = g.tile<WIN>(t) * kTile + box * R;
-        const bool in = seen(g, tok);
-        const bool good = in && page >= 0 && page < p.pool.n_pages;
-        if (in && !good) status_set(p.status, TV_E_PAGE);
-        const int y = good ? (((y0 + page) * Hkv + g.h) << psh) + (tok & (ps - 1)) : 0;
-        if (t + 1 < g.t1) page = entry(g, t + 1);
-        if (issued >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], st_par));
+      const int qs = segs % qslots;
+      if (qs % kLoadWarps == mine) {   // its queries
+        if (segs >= qslots) wait(&q_free[qs], (uint32_t)(segs / qslots - 1));
         if (!ok) break;
-        const unsigned boxes = __ballot_sync(0xffffffffu, good);
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(boxes) * (uint32_t)(R * 128));
+        const int r0 = g.hb * kRows, nr = min(kRows, p.G - r0);
+        if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], (uint32_t)(nr * D * 2));
         __syncwarp();
-        if (good)
-          tma_load_2d(smem + st * L::STAGE + (is_v ? L::HALF : 0) + slab * L::SLAB + box * R * 128, is_v ? &map_v : &map_k,
-                      &full[st], slab * 64, y, pol);
+        if (lane < nr)
+          bulk_load(smem + L::OFF_Q + (qs * qrows + lane) * L::Q_ROW,
+                    p.q + (size_t)g.i * p.q_stride + (size_t)(g.h * p.G + r0 + lane) * D, D * 2, &q_full[qs]);
         __syncwarp();
-        ++issued;
-        if (++st == kStages) st = 0, st_par ^= 1u;
+      }
+      ++segs;
+      for (int tb = g.t0; tb < g.t1 && ok; tb += per) {
+        const int next_pages = tb + per < g.t1 ? entry(g, tb + per) : (more ? entry(next, next.t0) : -1);
+        const int end = min(tb + per, g.t1);
+        for (int t = tb + (mine + kLoadWarps - count % kLoadWarps) % kLoadWarps; t < end; t += kLoadWarps) {
+          const int issued = count + (t - tb), st = issued % kStages;
+          const int page = __shfl_sync(0xffffffffu, pages, ((t - tb) << nsh) + (box & (nb - 1)));
+          const int tok = g.tile<WIN>(t) * kTile + box * R;
+          const bool in = box < nb && seen(g, tok);
+          const bool good = in && page >= 0 && page < p.pool.n_pages;
+          if (in && !good) status_set(p.status, TV_E_PAGE);
+          const int y = good ? (((y0 + page) * Hkv + g.h) << psh) + (tok & (ps - 1)) : 0;
+          if (issued >= kStages) wait(&empty[st], (uint32_t)(issued / kStages - 1));
+          if (!ok) break;
+          const unsigned boxes = __ballot_sync(0xffffffffu, good);
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(boxes) * (uint32_t)(R * 128));
+          __syncwarp();
+          if (good)
+            tma_load_2d(smem + st * L::STAGE + (is_v ? L::HALF : 0) + slab * L::SLAB + box * R * 128, is_v ? &map_v : &map_k,
+                        &full[st], slab * 64, y, pol);
+          __syncwarp();
+        }
+        count += end - tb;
+        pages = next_pages;
       }
       g = next;
       have = more;
-      page = next_page;
     }
     if (!ok && lane == 0) status_set(p.status, TV_E_TIMEOUT);
-    for (int u = segs > qslots ? segs - qslots : 0; u < segs; ++u)
-      mbar_wait(&q_full[u % qslots], (uint32_t)(u / qslots) & 1u);
-    // loads in flight land before the CTA leaves
-    for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u)
-      mbar_wait(&full[u % kStages], (uint32_t)(u / kStages) & 1u);
+    // loads in flight land before the CTA leaves: each warp has armed the
+    // barriers of its own, and what a timeout left unissued is not waited for
+    for (int u = max(0, segs - qslots); ok && u < segs; ++u)
+      if (u % qslots % kLoadWarps == mine) wait(&q_full[u % qslots], (uint32_t)(u / qslots));
+    for (int u = max(0, count - kStages); ok && u < count; ++u)
+      if (u % kLoadWarps == mine) wait(&full[u % kStages], (uint32_t)(u / kStages));
     return;
   }
 
