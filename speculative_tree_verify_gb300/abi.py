@@ -101,6 +101,7 @@ class TvPool4(ctypes.Structure):
     _fields_ = TvPool._fields_
 
 
+NO_WINDOW = (1 << 31) - 1   # a window that hides nothing
 TV_ROPE_PLAIN, TV_ROPE_LINEAR, TV_ROPE_BASE, TV_ROPE_BLEND = 0, 1, 2, 3
 ROPE_MAX_PAIRS = 64
 

@@ -45,7 +45,10 @@ constexpr int kStages = 12;                      // tiles in flight: 108 KB at D
 constexpr int kLoadWarps = 4;
 static_assert(kStages % kLoadWarps == 0, "a stage always belongs to the same loading warp");
 constexpr int kQueries = 8;                      // runs whose queries are loaded ahead, at most
-constexpr int kSegCost = 3;                      // what a head block costs besides its tiles, in tiles
+// What a head block costs besides its tiles, in tiles: its queries, the wait of
+// all warps for the last one's, its join.  128 sequences of 1 to 8191 tokens, 40/8
+// heads, with 1, 3, 5, 8 tiles: 98, 85, 72, 64 us.
+constexpr int kSegCost = 8;
 constexpr float kMoveLog2 = 8.f;                 // offsets move when a score passes them by this
 
 // HN: blocks of 8 heads
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
       const int tok0 = special ? g.tile<true>(t) * kTile + first : 0;
       auto out = [&](int tok) { return tok >= g.len || (tok >= p.sinks && tok < g.lo); };
       bool wrote = false;
-      if (special && p.k_new && tok0 < g.len && tok0 + 32 >= g.len) {
+      if (special && p.k_new && tok0 < g.len && g.len - tok0 <= 32) {
         // the new token: its codes into the tile and into the page
         const bool is_v = lane >= 16;
         const int c = lane & 15, at = g.len - 1, tk = at & 15, half = tk % 2 * 2;
@@ -649,7 +652,7 @@ int tv_attend_paged4(const tv_pool4* pool, int layer, const tv_seqs* seqs, const
   PaParams p;
   int sms;
   int rc = check_pool(pool, &pages);
-  if (rc || (rc = fill_paged(p, pages, layer, seqs, ids, n, n_q_heads, window, sinks, q, q_stride, k_new, v_new, kv_stride,
+  if (rc || (rc = fill_paged(p, kSegCost, pages, layer, seqs, ids, n, n_q_heads, window, sinks, q, q_stride, k_new, v_new, kv_stride,
                              out, workspace, workspace_bytes, dev_status, &sms)))
     return rc;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;

@@ -55,8 +55,10 @@ constexpr int kQueries = 8;                      // segments whose queries are l
 constexpr int kRedRows = 4;                      // rows joined at a time when a head block ends
 // What a head block costs besides its tiles, in tiles (its queries, its join).
 // 48 sequences of 1 to 8191 tokens, 8/2 heads, with 0, 1, 2, 4 tiles: 19.4,
-// 16.4, 15.0, 16.3 us (D = 128; 1 and 2 of 64 values: 13.9, 12.6 us).
-constexpr int kSegCost = 2;
+// 16.4, 15.0, 16.3 us (D = 128; 1 and 2 of 64 values: 13.9, 12.6 us).  Through a
+// window few tiles are left to a head block (128 such sequences, 40/8 heads, a
+// window of 2047, with 1, 2, 3, 5, 8 tiles: 85, 72, 66, 64, 68 us).
+constexpr int kSegCost = 2, kSegCostWin = 5;
 constexpr float kMoveLog2 = 8.f;
 
 template <int D>
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  RunList<kPaThreads, kSegCost, WIN> runs(p, s_first);
+  RunList<kPaThreads, WIN ? kSegCostWin : kSegCost, WIN> runs(p, s_first);
   if (!runs.build(s_mark, s_part, &s_bad)) return;
   // sequences without a token: zeros
   for (int i = blockIdx.x; i < p.n; i += gridDim.x)
@@ -656,7 +658,7 @@ int attend_paged(bool win, const tv_pool* pool, int layer, const tv_seqs* seqs, 
   PaParams p;
   int sms;
   int rc = check_pool(pool);
-  if (rc || (rc = fill_paged(p, *pool, layer, seqs, ids, n, n_q_heads, window, sinks, q, q_stride, k_new, v_new, kv_stride,
+  if (rc || (rc = fill_paged(p, win ? kSegCostWin : kSegCost, *pool, layer, seqs, ids, n, n_q_heads, window, sinks, q, q_stride, k_new, v_new, kv_stride,
                              out, workspace, workspace_bytes, dev_status, &sms)))
     return rc;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
@@ -684,7 +686,7 @@ int check_paged_heads(int n_q_heads, int n_kv_heads, int n) {
   return n < 1 ? TV_E_ARG : (n > kMaxTokens ? TV_E_UNSUPPORTED : TV_OK);
 }
 
-int fill_paged(PaParams& p, const tv_pool& pool, int layer, const tv_seqs* seqs, const int32_t* ids, int n, int n_q_heads,
+int fill_paged(PaParams& p, int seg_cost, const tv_pool& pool, int layer, const tv_seqs* seqs, const int32_t* ids, int n, int n_q_heads,
                int window, int sinks, const tv_bf16* q, size_t q_stride, const tv_bf16* k_new, const tv_bf16* v_new,
                size_t kv_stride, tv_bf16* out, void* workspace, size_t workspace_bytes, int32_t* dev_status, int* sms) {
   int rc = check_seqs(seqs, &pool);
@@ -700,7 +702,7 @@ int fill_paged(PaParams& p, const tv_pool& pool, int layer, const tv_seqs* seqs,
   p.HB = (p.G + kRows - 1) / kRows;
   // the places of n sequences of the longest kind
   const unsigned long long most =
-      (((unsigned long long)seqs->max_pages * pool.page_size + kTile - 1) / kTile + 4) * pool.n_kv_heads * p.HB;
+      (((unsigned long long)seqs->max_pages * pool.page_size + kTile - 1) / kTile + seg_cost + 2) * pool.n_kv_heads * p.HB;
   if (most > 0x7fffffffull / (unsigned)n) return TV_E_UNSUPPORTED;
   uint8_t* base = static_cast<uint8_t*>(workspace);
   if (!workspace || !aligned16(workspace) || workspace_bytes < paged_workspace(pool.head_dim, &p.ws, base)) return TV_E_WORKSPACE;

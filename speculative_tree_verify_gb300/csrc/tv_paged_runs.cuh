@@ -234,8 +234,9 @@ struct RunList {
 // ---- host (tv_paged_attn.cu) ---------------------------------------------------
 size_t paged_workspace(int D, PaWs* ws, uint8_t* base);
 int check_paged_heads(int n_q_heads, int n_kv_heads, int n);
-// the arguments of a call over either pool, checked and put in p; *sms: the GPU's
-int fill_paged(PaParams& p, const tv_pool& pool, int layer, const tv_seqs* seqs, const int32_t* ids, int n, int n_q_heads,
+// the arguments of a call over either pool, checked and put in p; *sms: the GPU's.
+// seg_cost: the kernel's, which with the tiles has to fit the list's 31 bits
+int fill_paged(PaParams& p, int seg_cost, const tv_pool& pool, int layer, const tv_seqs* seqs, const int32_t* ids, int n, int n_q_heads,
                int window, int sinks, const tv_bf16* q, size_t q_stride, const tv_bf16* k_new, const tv_bf16* v_new,
                size_t kv_stride, tv_bf16* out, void* workspace, size_t workspace_bytes, int32_t* dev_status, int* sms);
 // joins what ctas CTAs left

@@ -124,6 +124,7 @@ int tv_rope_init(tv_rope* rope, int rot_dim, int interleaved, double theta, int 
       (original_ctx < 1 || !(low_turns >= 0.0) || !(high_turns > low_turns) || !std::isfinite(high_turns)))
     return TV_E_ARG;
   if (scaling == TV_ROPE_BASE) theta *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+  if (!std::isfinite(theta) || theta <= 0.0) return TV_E_ARG;   // beyond what a double holds
   tv_rope r = {};
   r.rot_dim = rot_dim;
   r.interleaved = interleaved;
@@ -138,7 +139,7 @@ int tv_rope_init(tv_rope* rope, int rot_dim, int interleaved, double theta, int 
     }
     r.freq[i] = f;
   }
-  if (!finite_all(r.freq, rot_dim / 2)) return TV_E_ARG;   // a theta or factor beyond what powers of it can hold
+  if (!finite_all(r.freq, rot_dim / 2)) return TV_E_ARG;   // (nor may the frequencies be)
   *rope = r;
   return TV_OK;
 }
@@ -171,9 +172,10 @@ int tv_rope_rows(const tv_rope* rope, const tv_bf16* x, size_t x_stride, tv_bf16
   p.per = 1;
   while (p.per < kMaxBlockRows && rows / (2 * p.per) >= 8 * sms) p.per *= 2;
   for (int i = 0; i < kPairs; ++i) {
-    const double t = i < p.rot / 2 ? std::fmod(rope->freq[i] / 6.283185307179586476925286766559, 1.0) : 0.0;
     // a fraction of a turn, negative ones modulo one (the highest double below 1 is below 2^64 here, too)
-    p.turn[i] = t < 0.0 ? 0ull - (uint64_t)std::ldexp(-t, 64) : (uint64_t)std::ldexp(t, 64);
+    double t = i < p.rot / 2 ? rope->freq[i] / 6.283185307179586476925286766559 : 0.0;
+    if (t >= 1.0 || t <= -1.0) t = std::fmod(t, 1.0);
+    p.turn[i] = t < 0.0 ? 0ull - (uint64_t)(-t * 0x1p64) : (uint64_t)(t * 0x1p64);
   }
   const unsigned grid = (unsigned)((rows - 1) / p.per + 1);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -227,14 +227,17 @@ def run_round(model: DeviceModel, reqs: Sequence[DeviceRequest], b: RoundBuffers
 
 
 # ---------------------------------------------------------------------------
-# prompts and the paged cache (tv_attend_prompt, tv_pages_*, tv_attend_paged)
+# prompts and the paged cache (tv_attend_prompt, tv_pages_*, tv_attend_paged,
+# their forms through a window, and the cache in 4 bits)
 # ---------------------------------------------------------------------------
 @dataclass
 class PagedCache:
     """A pool of pages that many sequences share, their table, and the
     workspaces and status word of the calls.  Lists (ids, add, ...) are int32
     device tensors, one entry a sequence; rows of ``qkv`` hold the Q heads, the
-    K heads and the V heads of a token (a QKV projection's output)."""
+    K heads and the V heads of a token (a QKV projection's output).  window and
+    sinks of the attentions: a row sees its last ``window`` rows and the first
+    ``sinks`` (None: all of them)."""
     dims: Dims
     k: torch.Tensor        # [n_layers][n_pages][n_kv_heads][page_size][head_dim]
     v: torch.Tensor
@@ -248,18 +251,27 @@ class PagedCache:
     seqs: abi.TvSeqs
 
     @classmethod
+    def _pages(cls, n_layers: int, n_pages: int, dims: Dims, page_size: int, device):
+        shape = (n_layers, n_pages, dims.n_kv_heads, page_size, dims.head_dim)
+        return [torch.empty(shape, device=device, dtype=torch.bfloat16) for _ in range(2)]
+
+    @staticmethod
+    def _abi(name: str):
+        """The library's call of that name for this kind of pool."""
+        return {"pool": abi.TvPool, "attend_workspace_size": abi.tv_attend_paged_workspace_size}.get(name) or getattr(abi, "tv_pages_" + name)
+
+    @classmethod
     def alloc(cls, dims: Dims, n_layers: int, n_pages: int, page_size: int, max_seqs: int, max_pages: int,
               device="cuda") -> "PagedCache":
-        shape = (n_layers, n_pages, dims.n_kv_heads, page_size, dims.head_dim)
-        k, v = (torch.empty(shape, device=device, dtype=torch.bfloat16) for _ in range(2))
+        k, v = cls._pages(n_layers, n_pages, dims, page_size, device)
         i32 = dict(device=device, dtype=torch.int32)
         refs, lens = torch.zeros(n_pages, **i32), torch.zeros(max_seqs, **i32)
         pages = torch.full((max_seqs, max_pages), -1, **i32)
-        pool = abi.TvPool(k.data_ptr(), v.data_ptr(), refs.data_ptr(), n_layers, n_pages, dims.n_kv_heads, page_size,
-                          dims.head_dim)
+        pool = cls._abi("pool")(k.data_ptr(), v.data_ptr(), refs.data_ptr(), n_layers, n_pages, dims.n_kv_heads, page_size,
+                                dims.head_dim)
         seqs = abi.TvSeqs(pages.data_ptr(), lens.data_ptr(), max_seqs, max_pages)
-        bytes_ = (abi.tv_pages_workspace_size(pool, seqs),
-                  abi.tv_attend_paged_workspace_size(pool, dims.n_q_heads, min(max_seqs, 2048)))
+        bytes_ = (cls._abi("workspace_size")(pool, seqs),
+                  cls._abi("attend_workspace_size")(pool, dims.n_q_heads, min(max_seqs, 2048)))
         ws, attend_ws = (torch.empty(b, device=device, dtype=torch.uint8) for b in bytes_)
         return cls(dims, k, v, refs, pages, lens, torch.zeros(1, **i32), ws, attend_ws, pool, seqs)
 
@@ -299,27 +311,27 @@ class PagedCache:
 
     def extend(self, ids, add, stream=None) -> int:
         n = self._list(ids.numel(), ids=ids, add=add)
-        return abi.tv_pages_extend(self.pool, self.seqs, ids, add, n, self.ws, self.ws.numel(), self.status, stream)
+        return self._abi("extend")(self.pool, self.seqs, ids, add, n, self.ws, self.ws.numel(), self.status, stream)
 
     def fork(self, src, dst, stream=None) -> int:
         n = self._list(src.numel(), src=src, dst=dst)
-        return abi.tv_pages_fork(self.pool, self.seqs, src, dst, n, self.status, stream)
+        return self._abi("fork")(self.pool, self.seqs, src, dst, n, self.status, stream)
 
     def release(self, ids, keep, stream=None) -> int:
         n = self._list(ids.numel(), ids=ids, keep=keep)
-        return abi.tv_pages_release(self.pool, self.seqs, ids, keep, n, self.status, stream)
+        return self._abi("release")(self.pool, self.seqs, ids, keep, n, self.status, stream)
 
     def compact(self, remap, n_used, stream=None) -> int:
         self._list(self.refs.numel(), remap=remap)
         self._list(1, n_used=n_used)
-        return abi.tv_pages_compact(self.pool, self.seqs, remap, n_used, self.ws, self.ws.numel(), self.status, stream)
+        return self._abi("compact")(self.pool, self.seqs, remap, n_used, self.ws, self.ws.numel(), self.status, stream)
 
     def write(self, layer: int, ids, pos, starts, qkv: torch.Tensor, stream=None) -> int:
         """Rows of a projection into the pages of the sequences they belong to."""
         n = self._list(ids.numel(), ids=ids, pos=pos)
         self._list(n + 1, starts=starts)
         _, k, v = self._heads(qkv)
-        return abi.tv_pages_write(self.pool, layer, self.seqs, ids, pos, starts, n, qkv.shape[0], k, v,
+        return self._abi("write")(self.pool, layer, self.seqs, ids, pos, starts, n, qkv.shape[0], k, v,
                                   qkv.stride(0), self.dims.head_dim, self.status, stream)
 
     def read_into(self, layer: int, ids, pos, starts, rows: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> int:
@@ -327,7 +339,7 @@ class PagedCache:
         n = self._list(ids.numel(), ids=ids, pos=pos)
         self._list(n + 1, starts=starts)
         self._caches(k, v, rows)
-        return abi.tv_pages_read(self.pool, layer, self.seqs, ids, pos, starts, n, rows, k, v, k.stride(1),
+        return self._abi("read")(self.pool, layer, self.seqs, ids, pos, starts, n, rows, k, v, k.stride(1),
                                  k.stride(0), self.status, stream)
 
     def write_from(self, layer: int, ids, pos, starts, rows: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> int:
@@ -335,26 +347,72 @@ class PagedCache:
         n = self._list(ids.numel(), ids=ids, pos=pos)
         self._list(n + 1, starts=starts)
         self._caches(k, v, rows)
-        return abi.tv_pages_write(self.pool, layer, self.seqs, ids, pos, starts, n, rows, k, v, k.stride(1),
+        return self._abi("write")(self.pool, layer, self.seqs, ids, pos, starts, n, rows, k, v, k.stride(1),
                                   k.stride(0), self.status, stream)
 
-    def attend_prompt(self, qkv: torch.Tensor, starts, out: torch.Tensor, stream=None) -> int:
+    def attend_prompt(self, qkv: torch.Tensor, starts, out: torch.Tensor, stream=None, window: Optional[int] = None,
+                      sinks: int = 0) -> int:
         self._list(starts.numel(), starts=starts)
         q, k, v = self._heads(qkv)
         self._out(out, qkv.shape[0])
-        return abi.tv_attend_prompt(self.dims.n_q_heads, self.dims.n_kv_heads, self.dims.head_dim, q, k, v,
-                                    qkv.stride(0), qkv.stride(0), starts, starts.numel() - 1, qkv.shape[0], out,
-                                    self.status, stream)
+        heads = self.dims.n_q_heads, self.dims.n_kv_heads, self.dims.head_dim
+        rest = (q, k, v, qkv.stride(0), qkv.stride(0), starts, starts.numel() - 1, qkv.shape[0], out, self.status, stream)
+        if window is None:
+            return abi.tv_attend_prompt(*heads, *rest)
+        return abi.tv_attend_prompt_window(*heads, window, sinks, *rest)
 
-    def attend(self, layer: int, ids, qkv: torch.Tensor, out: torch.Tensor, stream=None) -> int:
-        """One new token a sequence: its K and V into the page, its queries over the whole sequence."""
+    def _token(self, ids, qkv: torch.Tensor, out: torch.Tensor):
         n = self._list(ids.numel(), ids=ids)
         q, k, v = self._heads(qkv)
         if qkv.shape[0] < n:
             raise ValueError(f"qkv: {n} rows expected, got {qkv.shape[0]}")
         self._out(out, n)
-        return abi.tv_attend_paged(self.pool, layer, self.seqs, ids, n, self.dims.n_q_heads, q, qkv.stride(0),
-                                   k, v, qkv.stride(0), out, self.attend_ws, self.attend_ws.numel(), self.status, stream)
+        return n, (q, qkv.stride(0), k, v, qkv.stride(0), out, self.attend_ws, self.attend_ws.numel(), self.status)
+
+    def attend(self, layer: int, ids, qkv: torch.Tensor, out: torch.Tensor, stream=None, window: Optional[int] = None,
+               sinks: int = 0) -> int:
+        """One new token a sequence: its K and V into the page, its queries over the sequence."""
+        n, rest = self._token(ids, qkv, out)
+        if window is None:
+            return abi.tv_attend_paged(self.pool, layer, self.seqs, ids, n, self.dims.n_q_heads, *rest, stream)
+        return abi.tv_attend_paged_window(self.pool, layer, self.seqs, ids, n, self.dims.n_q_heads, window, sinks, *rest, stream)
+
+
+@dataclass
+class PagedCache4(PagedCache):
+    """The same over a pool in 4 bits (k, v: uint8 [n_layers][n_pages][n_kv_heads][page_size / 16][9 head_dim],
+    tv_pool4 in tv.h): rows are rounded as they are written, and read back as what they stand for."""
+
+    @classmethod
+    def _pages(cls, n_layers: int, n_pages: int, dims: Dims, page_size: int, device):
+        shape = (n_layers, n_pages, dims.n_kv_heads, page_size // 16, 9 * dims.head_dim)
+        return [torch.empty(shape, device=device, dtype=torch.uint8) for _ in range(2)]
+
+    @staticmethod
+    def _abi(name: str):
+        return {"pool": abi.TvPool4, "attend_workspace_size": abi.tv_attend_paged4_workspace_size}.get(name) or getattr(abi, "tv_pages4_" + name)
+
+    def attend(self, layer: int, ids, qkv: torch.Tensor, out: torch.Tensor, stream=None, window: Optional[int] = None,
+               sinks: int = 0) -> int:
+        n, rest = self._token(ids, qkv, out)
+        return abi.tv_attend_paged4(self.pool, layer, self.seqs, ids, n, self.dims.n_q_heads,
+                                    abi.NO_WINDOW if window is None else window, sinks, *rest, stream)
+
+
+def rotate(rope: abi.TvRope, x: torch.Tensor, positions: torch.Tensor, n_heads: int, head_dim: int, status: torch.Tensor,
+           out: Optional[torch.Tensor] = None, stream=None) -> int:
+    """Rotary positions of the first ``n_heads`` heads of every row of ``x`` (of a projection's rows: the Q and K
+    heads), in place or into ``out``."""
+    out = x if out is None else out
+    for name, y in (("x", x), ("out", out)):
+        if y.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or y.device != status.device:
+            raise ValueError(f"{name}: bf16 on {status.device} expected, got {y.dtype} on {y.device}")
+        if y.dim() != 2 or y.shape[0] != x.shape[0] or y.shape[1] < n_heads * head_dim or y.stride(1) != 1:
+            raise ValueError(f"{name}: {x.shape[0]} rows of {n_heads * head_dim} values expected, got {tuple(y.shape)} with strides {y.stride()}")
+    if (positions.dtype != torch.int32 or positions.device != status.device or not positions.is_contiguous()
+            or positions.numel() != x.shape[0]):
+        raise ValueError(f"positions: {x.shape[0]} int32 on {status.device} expected, got {tuple(positions.shape)} {positions.dtype} on {positions.device}")
+    return abi.tv_rope_rows(rope, x, x.stride(0), out, out.stride(0), n_heads, head_dim, positions, x.shape[0], status, stream)
 
 
 # ---------------------------------------------------------------------------
