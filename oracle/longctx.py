@@ -75,7 +75,7 @@ def attend_prompt(q, k, v, starts, window, sinks):
 # ---- 4 bits ----------------------------------------------------------------------
 def quantise(x):
     """bits [..., D] -> (codes [..., D], scales' bits [..., D / 32])."""
-    g = bf16_to_f64(x).reshape(*x.shape[:-1], -1, 32)
+    g = bf16_to_f64(x).reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
     fine = np.isfinite(g).all(-1)
     g = np.where(fine[..., None], g, 0.0)
     scales = bf16(np.abs(g).max(-1) / 7)

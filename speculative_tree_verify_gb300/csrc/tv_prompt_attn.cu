@@ -716,8 +716,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             first = last = empty = b.x;
             end = b.y;
           } else if (b.x < b.y) {
-            if (first >= last) last = b.y;
-            first = b.x;
+            if (first >= last) first = b.x, last = b.y;
+            else first = min(first, b.x);   // (rows before the sinks' end see fewer of them)
           }
         }
         constexpr int CH = D / 8;   // 16-byte pieces of a row, 32 / CH rows a step
