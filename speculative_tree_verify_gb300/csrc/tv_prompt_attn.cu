@@ -949,8 +949,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                                       : start + 127 > tmin || (start <= last - p.window && start + 127 >= p.sinks);
             const int at = start + 64 * hf;
             if (!masked && before <= tmin) window(std::true_type{}, false, 63, 0, true, -1, 0);
-            else if (sinks) window(std::false_type{}, masked, p.sinks - 1 - at, before, w > f, -1, 0);
-            else window(std::false_type{}, masked, masked ? t - at : 63, before, w > f, masked ? t - p.window - at : -1, p.sinks - at);
+            else   // (one copy of the code for both)
+              window(std::false_type{}, masked, sinks ? p.sinks - 1 - at : (masked ? t - at : 63), before, w > f,
+                     masked && !sinks ? t - p.window - at : -1, p.sinks - at);
           }
         } else {
           for (; w < k.nwin; ++w) {
