@@ -276,11 +276,11 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* r) {
 // WIN: what is not finite in V, of keys j0 .. j1 - 1 that row t sees, into its
 // result in dimensions d0 .. + n - 1 (row), added to what the products left.
 // Keys that the products had are added twice, which changes nothing.
-__device__ __noinline__ void put_back(const PrParams& p, const __nv_bfloat16* v, int j0, int j1, int t, uint16_t* row,
-                                      int n) {
+__device__ __noinline__ void put_back(const __nv_bfloat16* v, size_t stride, int window, int sinks, int j0, int j1, int t,
+                                      uint16_t* row, int n) {
   for (int j = j0; j < j1 && j <= t; ++j) {
-    if (j <= t - p.window && j >= p.sinks) continue;
-    const uint4* x = reinterpret_cast<const uint4*>(v + (size_t)j * p.kv_stride);
+    if (j <= t - window && j >= sinks) continue;
+    const uint4* x = reinterpret_cast<const uint4*>(v + (size_t)j * stride);
     for (int c = 0; c < n; c += 8) {
       const uint4 y = __ldg(x + c / 8);
       const uint32_t q[4] = {y.x, y.y, y.z, y.w};
@@ -835,30 +835,36 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // Of a masked window's pieces of 32 keys, those that every row of the
         // warp sees need no mask, and those that none sees are not read.
         int all_see = 63, any_see = 63;
-        if (!PLAIN && masked) {
+        if (!WIN && !PLAIN && masked) {
           all_see = __reduce_min_sync(0xffffffffu, live ? lim : 63);
           any_see = __reduce_max_sync(0xffffffffu, live ? lim : -1);
         }
-        int all_low = -1, any_low = -1;   // above all_low every row sees them again; up to any_low no row does
+        // WIN: a bit for each of a piece's keys that the row sees (bits 0 .. n of a word: upto(n))
+        uint32_t sees[2] = {~0u, ~0u};
         if (WIN && !PLAIN && masked) {
-          all_low = __reduce_max_sync(0xffffffffu, live ? low : -1);
-          any_low = __reduce_min_sync(0xffffffffu, live ? low : 63);
+          auto upto = [](int n) { return n < 0 ? 0u : (n >= 31 ? ~0u : (2u << n) - 1u); };
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            sees[c] = upto(lim - 32 * c) & (~upto(low - 32 * c) | upto(sink - 1 - 32 * c));
         }
         auto unseen = [&](int c) {   // by every row of the warp
-          return 32 * c > any_see || (WIN && 32 * c + 31 <= any_low && 32 * c >= sink);
+          if constexpr (WIN) return masked && !__any_sync(0xffffffffu, live && sees[c] != 0u);
+          else return 32 * c > any_see;
         };
         auto scores = [&](int c, uint32_t (&x)[32]) {   // half of its scores
           ld32(sS + 64 * hf + 32 * c, x);
           tmem_ld_wait();
-          if (!PLAIN && 32 * c + 31 > all_see) {
+          if (WIN && !PLAIN) {
+            const uint32_t see = c == 0 ? sees[0] : sees[1];
+            if (masked && !__all_sync(0xffffffffu, !live || see == ~0u)) {
+#pragma unroll
+              for (int u = 0; u < 32; ++u)
+                if (!(see >> u & 1u)) x[u] = 0xff800000u;
+            }
+          } else if (!PLAIN && 32 * c + 31 > all_see) {
 #pragma unroll
             for (int u = 0; u < 32; ++u)
               if (32 * c + u > lim) x[u] = 0xff800000u;
-          }
-          if (WIN && !PLAIN && 32 * c <= all_low) {
-#pragma unroll
-            for (int u = 0; u < 32; ++u)
-              if (32 * c + u <= low && 32 * c + u >= sink) x[u] = 0xff800000u;
           }
         };
         uint32_t pk[32];
@@ -888,7 +894,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           sum = (part[0] + part[1]) + (part[2] + part[3]);
           const bool fresh = !PLAIN && before > t;   // the row's first keys, if it sees any
-          const bool has = lim >= 0 && (!WIN || low < min(lim, 63) || sink > 0);   // it sees some of them
+          const bool has = WIN ? (sees[0] | sees[1]) != 0u : lim >= 0;   // it sees some of them
           const bool off = sum > kHigh || (first && fresh && live && has && sum < kLow);
           tc_fence_before();
           const bool any = pair_any(off, pair);
@@ -1012,7 +1018,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             const __nv_bfloat16* v = p.v + (size_t)k.row0 * p.kv_stride + (size_t)k.h * D + hf * (D / 2);
             if (ok && live)
               for (int w = 0; w < k.nlow; ++w)
-                if (scrub(k, w)) put_back(p, v, w_start(k, w), w_start(k, w) + 128, t, row, D / 2);
+                if (scrub(k, w)) put_back(v, p.kv_stride, p.window, p.sinks, w_start(k, w), w_start(k, w) + 128, t, row, D / 2);
           } else {
           auto sees = [&](unsigned long long x) { return (unsigned)(x >> 32) == ~tag && (int)(unsigned)x <= t; };
           __syncwarp();   // over what the other lane has stored
