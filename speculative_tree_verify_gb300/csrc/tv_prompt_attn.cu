@@ -374,6 +374,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     int row0, len, t0, h;   // first row and length of the sequence, first token, KV head
     int hi, nst, nwin, skip0;
     int lo, nlow;   // WIN: the pair's first key but for the sinks; windows from it on, the others hold sinks
+    int up, down;   // WIN: windows before up hold keys above the pair's first token, those from down on keys that the
+                    // lower end hides (or, sinks behind which a step is not full, are treated as if)
   };
   auto read_work = [&](int it, bool ok) {   // again and again until free_work
     Work w;
@@ -391,7 +393,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
     w.nlow = (w.hi - w.lo + 127) / 128;
     w.nwin = w.nlow;
-    if (WIN && w.lo > 0) w.nwin += (p.sinks + 127) / 128;   // (sinks < lo)
+    if constexpr (WIN) {
+      const bool apart = w.lo > 0;   // (sinks < lo then)
+      const int hidden = w.hi - p.window - w.lo;   // below 2 T
+      w.up = max(1, w.nlow - ((w.t0 + 1 - w.lo) >> 7));
+      w.down = hidden > 0 ? w.nlow - ((hidden + 127) >> 7) : w.nlow;
+      if (apart) w.nwin += (p.sinks + 127) / 128;
+      if (hidden <= 0 && (!apart || (p.sinks & 15) == 0)) w.down = w.nwin;
+    }
     w.skip0 = w.nst == 2 ? w.nlow - (w.t0 + p.T - w.lo + 127) / 128 : 0;   // tile 0 sees nothing of the first window (0 or 1)
     return w;
   };
@@ -422,12 +431,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   };
   // window w holds keys that a row may not see (so does the first, if only as a rule)
   auto scrub = [&](const Work& k, int w) {
-    if constexpr (WIN) {
-      const int2 b = below(k, w);
-      if (b.x < b.y) return true;
-      if (w >= k.nlow) return false;
-    }
-    return w == 0 || w_start(k, w) + 127 > k.t0;
+    if constexpr (WIN) return w < k.up || w >= k.down;
+    else return w == 0 || w_start(k, w) + 127 > k.t0;
   };
 
   if (warp >= kPrSoftWarps) {
@@ -628,9 +633,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         bool look = scrub(k, w);
         int seen = min(8, max(0, k.t0 + 1 - w_start(k, w)) >> 4);   // steps whose keys every row sees
         int low = 0;   // WIN: the first of them
-        if constexpr (WIN) {
-          const int2 b = below(k, w);
-          if (look && b.x < b.y) low = (b.y + 15) >> 4;
+        if (WIN && w >= k.down) {
+          low = (below(k, w).y + 15) >> 4;
           if (w >= k.nlow) seen = 8;
         }
 #pragma unroll
@@ -710,7 +714,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const int key0 = w_start(k, w);
         int first = max(0, k.t0 + 1 - key0), last = min(128, k.hi - key0);
         int empty = last, end = (last + 15) & ~15;
-        if constexpr (WIN) {   // and the rows that the lower end hides
+        if (WIN && w >= k.down) {   // and the rows that the lower end hides
           const int2 b = below(k, w);
           if (w >= k.nlow) {   // the sinks are seen, what is behind them in their last step is not
             first = last = empty = b.x;
@@ -842,7 +846,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // WIN: a bit for each of a piece's keys that the row sees (bits 0 .. n of a word: upto(n))
         uint32_t sees[2] = {~0u, ~0u};
         if (WIN && !PLAIN && masked) {
-          auto upto = [](int n) { return n < 0 ? 0u : (n >= 31 ? ~0u : (2u << n) - 1u); };
+          auto upto = [](int n) {
+            uint32_t r;   // (a shift by 32 or more leaves nothing)
+            asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(~0u), "r"(max(n + 1, 0)));
+            return ~r;
+          };
 #pragma unroll
           for (int c = 0; c < 2; ++c)
             sees[c] = upto(lim - 32 * c) & (~upto(low - 32 * c) | upto(sink - 1 - 32 * c));
