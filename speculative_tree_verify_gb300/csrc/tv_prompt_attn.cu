@@ -47,14 +47,17 @@
 // such key), and put into the rows that do see it at the end.
 //
 // Through a window (WIN: tv_attend_prompt_window) row t sees keys (t - W, t]
-// and the first K, the sinks:  of the pair's keys, those from lo, its first
-// token's lowest, come in windows of 128 counted from lo, then the sinks in
-// windows counted from 0, of 16-key steps that hold any.  So a pair costs
-// (W + 2T + 127) / 128 windows and the sinks' steps, whatever the length.  What
-// is masked is now at both ends; the lower end's V (keys up to W before the
-// pair's last token) is looked over as well, and a pair whose V held something
-// not finite reads its keys again from memory at the end, each row those that
-// it sees (put_back): which rows see a key is no longer told by one number.
+// and the first K, the sinks.  Of the pair's keys, those from its first token's
+// lowest come in windows of 128.  Where these leave room for the sinks, they are
+// counted from the pair's last key down, and the sinks are loaded into the last
+// one's lowest steps, below what any row sees (16k tokens, 40/8 heads, W = 1024, K =
+// 4: 281 us with a window of the sinks' own, 273 so, 256 without sinks); else the
+// sinks have windows of their own behind the others.  So a pair costs about (W +
+// 2T + 127) / 128 windows, whatever the length.  What is masked is now at both
+// ends; the lower end's V (keys up to W before the pair's last token) is looked
+// over as well, and a pair whose V held something not finite reads its keys again
+// from memory at the end, each row those that it sees (put_back): which rows see
+// a key is no longer told by one number.
 #include <cmath>
 #include <type_traits>
 
@@ -301,10 +304,18 @@ __device__ __noinline__ void put_back(const __nv_bfloat16* v, size_t stride, int
 // the place of one that has not started, so that the next queries, keys and
 // first products are under way while it writes its output; set-up is paid once
 // an SM.
+template <bool WIN>
+struct PrMaps {
+  CUtensorMap q, k, v;
+};
+template <>
+struct PrMaps<true> {
+  CUtensorMap q, k, v, k16, v16;   // boxes of 128 rows of K and V, and of 16
+};
+
 template <int D, bool WIN>
 __global__ void __launch_bounds__(kPrThreads, 1)
-    prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v, const PrParams p) {
+    prompt_attn_kernel(const __grid_constant__ PrMaps<WIN> maps, const PrParams p) {
   using L = PrSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -353,9 +364,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     mbar_init(clc_bar, 1);
     mbar_init(want, 1);
     fence_mbar_init();
-    prefetch_tmap(&map_q);
-    prefetch_tmap(&map_k);
-    prefetch_tmap(&map_v);
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+    if constexpr (WIN) {
+      prefetch_tmap(&maps.k16);
+      prefetch_tmap(&maps.v16);
+    }
   }
   for (int e = tid; e < 2 * 3 * D; e += kPrThreads) s_bad[e] = ~0ull;
   if (warp == kWarpMma) {
@@ -373,7 +388,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   struct Work {
     int row0, len, t0, h;   // first row and length of the sequence, first token, KV head
     int hi, nst, nwin, skip0;
-    int lo, nlow;   // WIN: the pair's first key but for the sinks; windows from it on, the others hold sinks
+    int lo, nlow;   // WIN: first key of the windows but for the sinks; windows from it on, the others hold sinks
+    int ss;         // WIN: 16-row steps of the last window that hold sinks instead, below every key that is seen
     int up, down;   // WIN: windows before up hold keys above the pair's first token, those from down on keys that the
                     // lower end hides (or, sinks behind which a step is not full, are treated as if)
   };
@@ -393,8 +409,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
     w.nlow = (w.hi - w.lo + 127) / 128;
     w.nwin = w.nlow;
+    w.ss = 0;
+    if (WIN && w.lo > 0 && p.sinks > 0 && ((p.sinks + 15) & ~15) <= 128 * w.nlow - (w.hi - w.lo)) {
+      w.ss = (p.sinks + 15) >> 4;
+      w.lo = w.hi - 128 * w.nlow;   // (may lie before the sequence)
+    }
     if constexpr (WIN) {
-      const bool apart = w.lo > 0;   // (sinks < lo then)
+      const bool apart = w.lo > 0 && w.ss == 0;   // (sinks < lo then)
       const int hidden = w.hi - p.window - w.lo;   // below 2 T
       w.up = max(1, w.nlow - ((w.t0 + 1 - w.lo) >> 7));
       w.down = hidden > 0 ? w.nlow - ((hidden + 127) >> 7) : w.nlow;
@@ -427,7 +448,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   auto below = [&](const Work& k, int w) {
     const int start = w_start(k, w);
     if (w >= k.nlow) return make_int2(min(128, p.sinks - start), 16 * steps(k, 0, w));
-    return make_int2(max(0, p.sinks - start), min(128, k.hi - p.window - start));
+    return make_int2(k.ss > 0 ? (w == k.nlow - 1 ? p.sinks : 0) : max(0, p.sinks - start), min(128, k.hi - p.window - start));
   };
   // window w holds keys that a row may not see (so does the first, if only as a rule)
   auto scrub = [&](const Work& k, int w) {
@@ -544,13 +565,20 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const Work k = read_work(it, ok);
       free_work(it);
       if (k.len == 0) break;
-      auto load_kv = [&](const CUtensorMap* map, uint64_t* full, uint64_t* free, int off, int w, int& issued) {
+      auto load_kv = [&](const CUtensorMap* map, const CUtensorMap* map16, uint64_t* full, uint64_t* free, int off, int w, int& issued) {
         const int i = kv + w;
         if (i >= 2) ok = ok && mbar_wait(&free[i & 1], (uint32_t)((i - 2) >> 1) & 1u);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&full[i & 1], L::TILE);
+        if (lane == 0) mbar_arrive_expect_tx(&full[i & 1], L::TILE);
+        if (WIN && k.ss > 0 && w == k.nlow - 1) {   // the sinks, and what is left of the window above them
+          __syncwarp();
+          const int b = lane / (D / 64), a = lane % (D / 64);
+          if (b < 8)
+            tma_load_3d(smem + off + (i & 1) * L::TILE + a * kAtomP + b * 2048, map16, &full[i & 1], k.h * D + a * 64, 0,
+                        k.row0 + 16 * b + (b < k.ss ? 0 : w_start(k, w)));
+          __syncwarp();
+        } else if (lane == 0) {
 #pragma unroll
           for (int a = 0; a < D / 64; ++a)
             tma_load_3d(smem + off + (i & 1) * L::TILE + a * kAtomP, map, &full[i & 1], k.h * D + a * 64, 0,
@@ -558,6 +586,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         ++issued;
       };
+      const CUtensorMap *k16 = nullptr, *v16 = nullptr;
+      if constexpr (WIN) k16 = &maps.k16, v16 = &maps.v16;
       auto load_q = [&](int s) {
         if (nq[s] > 0) ok = ok && mbar_wait(&q_free[s], (uint32_t)(nq[s] - 1) & 1u);
         ok = __all_sync(0xffffffffu, ok);
@@ -566,7 +596,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           mbar_arrive_expect_tx(&q_full[s], qbytes);
 #pragma unroll
           for (int a = 0; a < D / 64; ++a)
-            tma_load_3d(smem + L::OFF_Q + s * L::TILE + a * kAtomP, &map_q, &q_full[s], a * 64, k.h * p.G,
+            tma_load_3d(smem + L::OFF_Q + s * L::TILE + a * kAtomP, &maps.q, &q_full[s], a * 64, k.h * p.G,
                         k.row0 + k.t0 + s * p.T);
         }
         ++nq[s];
@@ -574,9 +604,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       for (int w = 0; w < k.nwin && ok; ++w) {
         // some three windows (5 us) before its end, time to find the next place
         if (w == max(0, k.nwin - 3) && lane == 0) mbar_arrive(want);
-        load_kv(&map_k, k_full, k_free, L::OFF_K, w, nk);
+        load_kv(&maps.k, k16, k_full, k_free, L::OFF_K, w, nk);
         if (w == 0 && ok) load_q(0);
-        if (ok) load_kv(&map_v, v_full, v_free, L::OFF_V, w, nv);
+        if (ok) load_kv(&maps.v, v16, v_full, v_free, L::OFF_V, w, nv);
         if (w == 0 && ok && k.nst == 2) load_q(1);
       }
       if (!ok) break;
@@ -960,12 +990,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             const bool sinks = w >= k.nlow;
             const int before = w == f ? 0x7fffffff : (sinks ? 0 : start + 128);
             const bool masked = sinks ? p.sinks - start < 128
-                                      : start + 127 > tmin || (start <= last - p.window && start + 127 >= p.sinks);
+                                      : start + 127 > tmin || (start <= last - p.window && (k.ss > 0 || start + 127 >= p.sinks));
             const int at = start + 64 * hf;
             if (!masked && before <= tmin) window(std::true_type{}, false, 63, 0, true, -1, 0);
             else   // (one copy of the code for both)
               window(std::false_type{}, masked, sinks ? p.sinks - 1 - at : (masked ? t - at : 63), before, w > f,
-                     masked && !sinks ? t - p.window - at : -1, p.sinks - at);
+                     masked && !sinks ? t - p.window - at : -1,
+                     k.ss > 0 ? (w == k.nlow - 1 ? p.sinks - 64 * hf : 0) : p.sinks - at);
           }
         } else {
           for (; w < k.nwin; ++w) {
@@ -1026,7 +1057,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             const __nv_bfloat16* v = p.v + (size_t)k.row0 * p.kv_stride + (size_t)k.h * D + hf * (D / 2);
             if (ok && live)
               for (int w = 0; w < k.nlow; ++w)
-                if (scrub(k, w)) put_back(v, p.kv_stride, p.window, p.sinks, w_start(k, w), w_start(k, w) + 128, t, row, D / 2);
+                if (scrub(k, w)) put_back(v, p.kv_stride, p.window, p.sinks, max(0, w_start(k, w)), w_start(k, w) + 128, t, row, D / 2);
           } else {
           auto sees = [&](unsigned long long x) { return (unsigned)(x >> 32) == ~tag && (int)(unsigned)x <= t; };
           __syncwarp();   // over what the other lane has stored
@@ -1061,11 +1092,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 template <int D, bool WIN>
 int launch_prompt(PrParams& p, const void* q, const void* k, const void* v, size_t q_stride, size_t kv_stride,
                   cudaStream_t st) {
-  CUtensorMap mq, mk, mv;
-  int rc = make_tmap_bf16_rows(&mq, q, D, p.Hq, p.rows, q_stride, 64, p.G, p.T);
-  if (rc || (rc = make_tmap_bf16_rows(&mk, k, p.Hkv * D, 1, p.rows, kv_stride, 64, 1, 128)) ||
-      (rc = make_tmap_bf16_rows(&mv, v, p.Hkv * D, 1, p.rows, kv_stride, 64, 1, 128)))
+  PrMaps<WIN> m;
+  int rc = make_tmap_bf16_rows(&m.q, q, D, p.Hq, p.rows, q_stride, 64, p.G, p.T);
+  if (rc || (rc = make_tmap_bf16_rows(&m.k, k, p.Hkv * D, 1, p.rows, kv_stride, 64, 1, 128)) ||
+      (rc = make_tmap_bf16_rows(&m.v, v, p.Hkv * D, 1, p.rows, kv_stride, 64, 1, 128)))
     return rc;
+  if constexpr (WIN)
+    if ((rc = make_tmap_bf16_rows(&m.k16, k, p.Hkv * D, 1, p.rows, kv_stride, 64, 1, 16)) ||
+        (rc = make_tmap_bf16_rows(&m.v16, v, p.Hkv * D, 1, p.rows, kv_stride, 64, 1, 16)))
+      return rc;
   static std::atomic<bool> attr[64];
   if (ensure_smem_limit(prompt_attn_kernel<D, WIN>, PrSmem<D>::BYTES, attr)) return TV_E_CUDA;
   // the roles' register split must not ask for more than the launch brings
@@ -1082,8 +1117,8 @@ int launch_prompt(PrParams& p, const void* q, const void* k, const void* v, size
   const int sms = num_sms();
   if (sms <= 0) return TV_E_CUDA;
   p.queued = pairs * p.Hkv > sms;
-  return launch_pdl(prompt_attn_kernel<D, WIN>, dim3((unsigned)(pairs * p.Hkv)), dim3(kPrThreads), PrSmem<D>::BYTES, st, mq,
-                    mk, mv, p);
+  return launch_pdl(prompt_attn_kernel<D, WIN>, dim3((unsigned)(pairs * p.Hkv)), dim3(kPrThreads), PrSmem<D>::BYTES, st, m,
+                    p);
 }
 
 int attend_prompt(bool win, int n_q_heads, int n_kv_heads, int head_dim, int window, int sinks, const tv_bf16* q,
