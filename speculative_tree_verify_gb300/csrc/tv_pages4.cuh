@@ -41,9 +41,12 @@ __device__ __forceinline__ uint32_t round4(const uint4& x, uint32_t& scale) {
   if (top >= 0x7f80u) s = __uint_as_float(0x7fc00000u);
   scale = __float_as_uint(s) >> 16;
   // x / s is a multiple of 2^-10 or so away from a half, or one: 2^-20 more
-  // takes halves away from zero and nothing else across.  The sum with
-  // 1.5 * 2^23 + 8 rounds to a whole number, the code its lowest bits.
-  const float r = (1.f / s) * (1.f + 0x1p-20f);
+  // (the reciprocal is right to 2^-23) takes halves away from zero and nothing
+  // else across.  The sum with 1.5 * 2^23 + 8 rounds to a whole number, the code
+  // its lowest bits.
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  r *= 1.f + 0x1p-20f;
   uint32_t w = 0u;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
