@@ -823,12 +823,14 @@ TV_API int tv_pages4_read(const tv_pool4 *pool, int layer, const tv_seqs *seqs, 
  * tv_attend_paged_window, of the values that the cache stands for.  k_new and
  * v_new are bf16 rows; they are stored in 4 bits, and the new token sees what
  * was stored.
- * Scores are fp32 (q . k of one group of 32 dimensions exactly as the tensor
- * core adds it, then scaled; q enters with 11 bits relative to its own
- * exponent down to 2^-28 of the row's largest value); weights relative to a row's
- * offset enter the product with V, scaled by its group's scale, as fp16
- * (11 bits, and 2^-39 of the largest scaled weight or so); sums are fp32; out is rounded
- * once.  |q| up to 2^100.
+ * Scores are fp32: q enters as fp16 relative to its row's largest value, exactly
+ * down to 2^-23 of that, and a group's sum takes its scale.  A weight times its
+ * group's scale enters the product with V as fp16 (11 bits, down to 2^-29 of the
+ * largest so far); sums are fp32, and out is rounded once.  |q| up to 2^100, scores up
+ * to 2^27, |v| up to 2^100, and below 2^-100 v counts for less than it is.  What
+ * the new token does not see is never used, whatever it holds; a group of V that
+ * stands for NaN is NaN in its 32 dimensions of the heads that see it, whatever it
+ * weighs.  The same inputs give the same bits.
  */
 TV_API int tv_attend_paged4_workspace_size(const tv_pool4 *pool, int n_q_heads, int n, size_t *bytes);
 TV_API int tv_attend_paged4(const tv_pool4 *pool, int layer, const tv_seqs *seqs, const int32_t *ids, int n,
@@ -865,8 +867,9 @@ TV_API int tv_attend_paged4(const tv_pool4 *pool, int layer, const tv_seqs *seqs
  *              row's heads; out may be x (with the same stride) and may not
  *              overlap it otherwise
  *   positions  device int32 [rows], any value
- * Angles are exact to 2^-31 of a turn at every position (fixed point), one
- * fp32 sine and cosine each; the result is rounded once.
+ * An angle's fraction of a turn is a 64-bit product, reduced without a rounding
+ * at any position; that fraction, its sine and cosine and the products are fp32,
+ * and the result is rounded once.
  * Host checks: TV_E_ARG, TV_E_UNSUPPORTED (head_dim not 64 or 128, rot_dim
  * above it, n_heads > 65536).
  */

@@ -4,29 +4,31 @@
 // n the codes less 8, s a scale of each token's 32 dimensions.
 //
 // What bounds it: 9/8 bytes a value of K and V together, so that instructions
-// come near to memory: a block of 16 tokens of one head (2.3 KB of K and V at D = 128) is
-// about 90 cycles of an SM's share of the bandwidth, and as many issue slots
-// on each of its four schedulers as there are.  Hence:
+// come near to memory: a block of 16 tokens of one head (2.3 KB of K and V at
+// D = 128) is some 95 cycles of an SM's share of the bandwidth, and 128 sequences of
+// 8k take 139 a block now (265 us; 4.6 TB/s), about 300 issue slots on four
+// schedulers, half of which go to the pipe of masks and conversions.  Hence:
 // - The cache lies as the tensor cores' operands do (tv_pool4): a lane loads its
 //   codes with 16-byte loads, no ldmatrix, no shuffle.
 // - Codes become fp16 operands without arithmetic: 4 bits masked out of 16 are the
 //   subnormal n' 2^-24 or 16 times that, n' = n + 8, and 8 bits (n' + 16 n") 2^-24 of
 //   neighbours.  Where dimensions are summed (K), q carries the 16th part; where
 //   they are rows (V), neighbours come apart at the end, which saves a mask.
+//   (e4m3 products, to which four bits are an operand as well, turn into
+//   conversions and fp16 products on this architecture: 549 us instead of 346.)
 // - Both products have the codes as the operand of 16 rows and 8 heads as columns
-//   (S^T = K Q^T, O^T += V^T P^T): up to 8 heads a KV head cost half of what 16 do.
-//   S^T begins at -8 sum q instead of zero, a group of 32 dimensions at a time, and
-//   each group's sum takes the token's scale; V's 8 goes by a product of the weights
-//   with a constant, which costs less than 32 packed subtractions did.
+//   (S^T = K Q^T, O^T += V^T P^T): up to 8 heads a KV head cost half of what 16 do
+//   (346 -> 292 us).  -8 sum q of a group of 32 dimensions is added to its sum, which
+//   then takes the token's scale; V's codes less 8 are one packed subtraction.
 // - A token's V scale goes into its weight, four weights of fp16 a token (one a
 //   group), so that V needs no product.  The weights are relative to the largest
 //   scale so far, as they are to the offset: 2^15 at most, 2^-24 at least.
 //
 // How the work is cut over CTAs is in tv_paged_runs.cuh.  In a CTA four warps look
 // up pages (32 boxes' entries at a time, the next 32 on their way) and copy whole
-// blocks into a ring of stages, each every fourth tile (one warp alone takes 1200
-// cycles a tile); the others compute, tile t by warps 2 (t mod teams) and the next, 32
-// tokens each.
+// blocks into a ring of stages, each every fourth tile (one warp alone issued one
+// in 1200 cycles: 549 -> 346 us); the others compute, tile t by warps
+// 2 (t mod teams) and the next, 32 tokens each (16 each: 292 us instead of 271).
 #include <cmath>
 #include <type_traits>
 
@@ -90,6 +92,11 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 // an 8 x 8 matrix of 16-bit values, a row to four lanes, transposed
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
@@ -514,10 +521,10 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
               const uint32_t w = vw[n][j], u1 = __byte_perm(w, 0u, 0x4341);
-              a[0][n] = w & 0x000f000fu;
-              a[1][n] = w & 0x00ff00ffu;
-              a[2][n] = u1 & 0x000f000fu;
-              a[3][n] = u1;
+              a[0][n] = sub_f16(w & 0x000f000fu, 0x00080008u);
+              a[1][n] = sub_f16(w & 0x00ff00ffu, 0x00880088u);
+              a[2][n] = sub_f16(u1 & 0x000f000fu, 0x00080008u);
+              a[3][n] = sub_f16(u1, 0x00880088u);
             }
 #pragma unroll
             for (int b = 0; b < HN; ++b) {
@@ -532,8 +539,6 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
               mma_f16(lo, a[0][0], a[1][0], a[0][1], a[1][1], pw[0], pw[1], lo[0], lo[1], lo[2], lo[3]);
               mma_f16(hi, a[2][0], a[3][0], a[2][1], a[3][1], pw[0], pw[1], hi[0], hi[1], hi[2], hi[3]);
               // less 8 (and 8 + 16 * 8) of every code
-              mma_f16(lo, 0x80088008u, 0x80888088u, 0x80088008u, 0x80888088u, pw[0], pw[1], lo[0], lo[1], lo[2], lo[3]);
-              mma_f16(hi, 0x80088008u, 0x80888088u, 0x80088008u, 0x80888088u, pw[0], pw[1], hi[0], hi[1], hi[2], hi[3]);
             }
           }
         }
