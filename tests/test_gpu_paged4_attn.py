@@ -384,3 +384,97 @@ def test_a_serving_run(gpu, kind, interleaved):
                 history[s][j] = np.concatenate([history[s][j], part(turned[i:i + 1], a, Hkv)])
             see = longctx.seen(len(history[s][0]) - 1, window, sinks)
             close4(got[i], bf16_to_f64(part(turned[i:i + 1], 0, Hq))[0], held(history[s][0])[see], held(history[s][1])[see], f"step {step}, sequence {s}")
+
+
+def test_the_longest_length(gpu):
+    """2^31 - 16 tokens: a table row that names one page over and over, but for its last place (its 16 tokens weigh less
+    than 2^-20).  A warp adds up 2^25 / (6 * 148) tiles of two products or fewer; sums that drop what lies below their last
+    place lose at most 2^-23 of themselves a product: 2^17 2^-23 = 2^-6 of sum w |v|, and half of that of the denominator."""
+    ps, D, n_pages = 16, 64, 2 ** 27 - 1
+    rng = np.random.default_rng(21)
+    raw = [np.zeros((1, 2, 1, 1, 9 * D), np.uint8) for _ in range(2)]
+    rows, held = longctx.Pages4(*raw, ps, D), []
+    for name in "kv":
+        codes, scales = longctx.quantise(bits(rng.standard_normal((2, ps, D)) / 8))
+        held.append(longctx.stands_for(codes, scales)[0])
+        for p in range(2):
+            for t in range(ps):
+                rows.put(name, 0, p, t, codes[p, t][None], scales[p, t][None])
+    q = bits(rng.standard_normal((1, 4, D)) / 2)
+    table = torch.zeros(1, n_pages, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    gk, gv, refs, lens = *(torch.from_numpy(x).cuda() for x in raw), i32([1, 1]), i32([n_pages * ps])
+    pool, seqs = abi.TvPool4(gk.data_ptr(), gv.data_ptr(), refs.data_ptr(), 1, 2, 1, ps, D), abi.TvSeqs(table.data_ptr(), lens.data_ptr(), 1, n_pages)
+    out, st, gq = torch.zeros(1, 4, D, dtype=torch.int16, device="cuda"), i32([0]), dev(q)
+    size = abi.tv_attend_paged4_workspace_size(pool, 4, 1)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert abi.tv_attend_paged4(pool, 0, seqs, i32([0]), 1, 4, ALL, 0, gq, 4 * D, None, None, 0, out, ws, size, st) == 0
+    assert int(st.item()) == 0
+    qf, (kf, vf) = bf16_to_f64(q[0]), held
+    w = np.exp(qf @ kf.T / np.sqrt(D))
+    w /= w.sum(1, keepdims=True)
+    o, mag = w @ vf, w @ np.abs(vf)
+    assert (np.abs(bf16_to_f64(host(out))[0] - o) <= (2.0 ** -6 + 2.0 ** -7 + 3 * 2.0 ** -8 + 2.0 ** -10) * mag + 2.0 ** -22).all()
+
+
+def test_pages_past_two_to_the_32_bytes(gpu):
+    """The last pages of a pool whose K alone is more than 2^32 bytes: written, read, and attended to."""
+    ps, D = 16, 64
+    n_pages = 2 ** 32 // (9 * D) + 5000
+    k, v = (torch.zeros(1, n_pages, 1, 1, 9 * D, dtype=torch.uint8, device="cuda") for _ in range(2))
+    rng = np.random.default_rng(22)
+    pages = [n_pages - 1, n_pages - 4000, 3]
+    kk, vv = (bits(rng.standard_normal((40, 1, D))) for _ in range(2))
+    q = bits(rng.standard_normal((1, 2, D)))
+    refs, table, lens, ids, st = torch.ones(n_pages, dtype=torch.int32, device="cuda"), i32([pages]), i32([40]), i32([0]), i32([0])
+    pool, seqs = abi.TvPool4(k.data_ptr(), v.data_ptr(), refs.data_ptr(), 1, n_pages, 1, ps, D), abi.TvSeqs(table.data_ptr(), lens.data_ptr(), 1, 3)
+    assert abi.tv_pages4_write(pool, 0, seqs, ids, i32([0]), i32([0, 39]), 1, 39, dev(kk), dev(vv), D, D, st) == 0
+    out = torch.zeros(1, 2, D, dtype=torch.int16, device="cuda")
+    size = abi.tv_attend_paged4_workspace_size(pool, 2, 1)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    qkv = dev(np.concatenate([q.reshape(-1), kk[-1].reshape(-1), vv[-1].reshape(-1)]))
+    assert abi.tv_attend_paged4(pool, 0, seqs, ids, 1, 2, ALL, 0, qkv, 128, qkv[128:], qkv[192:], 64, out, ws, size, st) == 0
+    back = [torch.zeros(40, D, dtype=torch.int16, device="cuda") for _ in range(2)]
+    assert abi.tv_pages4_read(pool, 0, seqs, ids, i32([0]), i32([0, 40]), 1, 40, *back, D, D, st) == 0
+    assert int(st.item()) == 0
+    held = [longctx.stands_for(*longctx.quantise(x)) for x in (kk, vv)]
+    for x, b in zip(held, back):
+        assert (bf16_to_f64(host(b)) == bf16_to_f64(longctx.bf16(x[:, 0]))).all()
+    close4(bf16_to_f64(host(out))[0], bf16_to_f64(q[0]), *held)
+
+
+def test_captured_first(gpu):
+    """A process whose first call of each kind is made while capturing."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from speculative_tree_verify_gb300 import abi
+from speculative_tree_verify_gb300.device import PagedCache, PagedCache4, rotate
+from speculative_tree_verify_gb300.synth import Dims
+d = Dims(hidden=64, n_q_heads=4, n_kv_heads=2, head_dim=128, vocab=64)
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+x, out = torch.randn(40, 8 * 128, device="cuda").bfloat16(), torch.zeros(40, 4, 128, device="cuda", dtype=torch.bfloat16)
+caches = [kind.alloc(d, 1, 9, 16, 2, 6) for kind in (PagedCache, PagedCache4)]
+lists = i32([0]), i32([40]), i32([0, 40]), i32(list(range(40)))
+rope = abi.tv_rope_init(128)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    s = torch.cuda.current_stream()
+    for c in caches:
+        assert rotate(rope, x, lists[3], 6, 128, c.status, stream=s) == 0
+        assert c.attend_prompt(x, lists[2], out, s, window=9, sinks=2) == 0
+        assert c.extend(lists[0], lists[1], s) == 0
+        assert c.write(0, lists[0], lists[0], lists[2], x, s) == 0
+        assert c.attend(0, lists[0], x, out, s, window=9, sinks=2) == 0
+        assert c.release(lists[0], lists[0], s) == 0
+g.replay()
+g.replay()
+torch.cuda.synchronize()
+assert [int(c.status.item()) for c in caches] == [0, 0]
+assert torch.isfinite(out.float()).all()
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]

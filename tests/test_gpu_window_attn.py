@@ -252,3 +252,43 @@ def test_the_same_bits_twice(gpu):
     c = WindowCase(300, 4, [3000, 17, 900], 40, 8, 128, 16, seed=9)
     a, b = run_tokens(c), run_tokens(c)
     assert all((x == y).all() for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_the_longest_length(gpu, four):
+    """2^31 - 16 tokens, of which a window and the sinks are seen; the entries of all pages between name none."""
+    ps, D, n_pages, window, sinks = 16, 64, 2 ** 27 - 1, 100, 20
+    rng = np.random.default_rng(14)
+    k, v = (bits(rng.standard_normal((12, ps, D))) for _ in range(2))
+    q = bits(rng.standard_normal((1, 4, D)))
+    table = torch.full((1, n_pages), 1 << 30, dtype=torch.int32, device="cuda")
+    L = n_pages * ps
+    # sinks and window are looked up in tiles of 64 tokens: pages 0 .. 3, and the last 8 (the window lies in 7 of them)
+    table[0, :4] = i32([0, 1, 2, 3])
+    table[0, -8:] = i32([4, 5, 6, 7, 8, 9, 10, 11])
+    refs, lens, ids, st = i32(np.ones(12)), i32([L]), i32([0]), i32([0])
+    out, gq = torch.zeros(1, 4, D, dtype=torch.int16, device="cuda"), dev(q)
+    seqs = abi.TvSeqs(table.data_ptr(), lens.data_ptr(), 1, n_pages)
+    if four:
+        raw = [np.zeros((1, 12, 1, 1, 9 * D), np.uint8) for _ in range(2)]
+        rows, held = longctx.Pages4(*raw, ps, D), []
+        for name, x in zip("kv", (k, v)):
+            codes, scales = longctx.quantise(x)
+            held.append(longctx.stands_for(codes, scales))
+            for p in range(12):
+                for t in range(ps):
+                    rows.put(name, 0, p, t, codes[p, t][None], scales[p, t][None])
+        gk, gv = (torch.from_numpy(x).cuda() for x in raw)
+        pool = abi.TvPool4(gk.data_ptr(), gv.data_ptr(), refs.data_ptr(), 1, 12, 1, ps, D)
+        size, call = abi.tv_attend_paged4_workspace_size(pool, 4, 1), abi.tv_attend_paged4
+    else:
+        held, gk, gv = [bf16_to_f64(k), bf16_to_f64(v)], dev(k), dev(v)
+        pool = abi.TvPool(gk.data_ptr(), gv.data_ptr(), refs.data_ptr(), 1, 12, 1, ps, D)
+        size, call = abi.tv_attend_paged_workspace_size(pool, 4, 1), abi.tv_attend_paged_window
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert call(pool, 0, seqs, ids, 1, 4, window, sinks, gq, 4 * D, None, None, 0, out, ws, size, st) == 0
+    assert int(st.item()) == 0
+    kk, vv = (np.concatenate([x.reshape(-1, 1, D)[:sinks], x.reshape(-1, 1, D)[-window:]]) for x in held)
+    o, off = attend(bf16_to_f64(q[0]), kk, vv, True)
+    # 4 bits: 2^-11 of sum w |v| more, which is at most |o| and the spread together
+    close(bf16_to_f64(host(out))[0], o, off + (2.0 ** -3 * (np.abs(o) + off) if four else 0))
