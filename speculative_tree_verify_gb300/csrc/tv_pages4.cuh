@@ -57,18 +57,19 @@ __device__ __forceinline__ uint32_t round4(const uint4& x, uint32_t& scale) {
   return s > 0.f ? w : 0x88888888u;
 }
 
-// the 8 values that a word of codes stands for
+// The 8 values that a word of codes stands for.  128 + a code is a bf16 value, less
+// 136 it is n, and n s is rounded once: two values an instruction.
 __device__ __forceinline__ uint4 value4(uint32_t w, float s) {
-  uint32_t q[4];
+  const __nv_bfloat162 off = __float2bfloat162_rn(136.f), scale = __float2bfloat162_rn(s);   // (s is a bf16 value)
+  uint32_t y[4];   // values u and u + 4
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    // 1.5 * 2^23 + code, less 1.5 * 2^23 + 8
-    const float a = __uint_as_float(0x4b400000u | (w >> (8 * u) & 15u)) - 12582920.f;
-    const float b = __uint_as_float(0x4b400000u | (w >> (8 * u + 4) & 15u)) - 12582920.f;
-    const __nv_bfloat162 y = __floats2bfloat162_rn(a * s, b * s);
-    q[u] = *reinterpret_cast<const uint32_t*>(&y);
+    const uint32_t x = (w >> (4 * u) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hmul2_rn(__hsub2_rn(*reinterpret_cast<const __nv_bfloat162*>(&x), off), scale);
+    y[u] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  return make_uint4(q[0], q[1], q[2], q[3]);
+  return make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410), __byte_perm(y[0], y[1], 0x7632),
+                    __byte_perm(y[2], y[3], 0x7632));
 }
 
 }  // namespace tv
