@@ -310,10 +310,10 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
       top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // the largest to 2^13 .. 2^14; below 2^-114 it stays smaller
-      const int e = max((int)(top >> 7), 13);   // 127 + exponent
+      // the largest to 2^13 .. 2^14; below 2^-113 it stays smaller, so that both factors are normal
+      const int e = max((int)(top >> 7), 14);   // 127 + exponent
       const float f = __uint_as_float((uint32_t)(267 - e) << 23);
-      const float worth = p.scale_log2 * 0x1p24f * __uint_as_float((uint32_t)max(e - 13, 1) << 23);
+      const float worth = p.scale_log2 * 0x1p24f * __uint_as_float((uint32_t)(e - 13) << 23);
       sc[b][0] = __shfl_sync(0xffffffffu, worth, 8 * t4);
       sc[b][1] = __shfl_sync(0xffffffffu, worth, 8 * t4 + 4);
 #pragma unroll

@@ -188,6 +188,16 @@ def test_queries_of_any_size(gpu, scale):
     Case4([700, 130, 3000], 8, 2, 128, 32, seed=3, scale=scale, edit=edit).check()
 
 
+@pytest.mark.parametrize("scale,kscale", [(2.0 ** -112, 2.0 ** 111), (2.0 ** -115, 2.0 ** 114), (2.0 ** -118, 2.0 ** 117), (2.0 ** -125, 2.0 ** 123)])
+def test_the_smallest_queries(gpu, scale, kscale):
+    """Down to values that are not normal, beside keys that make scores of them."""
+    def edit(c):
+        for pair in c.kv:
+            pair[0] = bits(bf16_to_f64(pair[0]) * kscale)
+    for heads in ((8, 2, 128), (12, 1, 64)):
+        Case4([1, 70, 700], *heads, 32, scale=scale, seed=41, edit=edit).check()
+
+
 @pytest.mark.parametrize("vscale", [2.0 ** -60, 1e-4, 1e4, 2.0 ** 90])
 def test_values_of_any_size(gpu, vscale):
     Case4([700, 65], 8, 2, 128, 32, seed=4, vscale=vscale).check()
