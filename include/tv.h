@@ -827,7 +827,7 @@ TV_API int tv_pages4_read(const tv_pool4 *pool, int layer, const tv_seqs *seqs, 
  * down to 2^-23 of that, and a group's sum takes its scale.  A weight times its
  * group's scale enters the product with V as fp16 (11 bits, down to 2^-29 of the
  * largest so far); sums are fp32, and out is rounded once.  |q| up to 2^100, scores up
- * to 2^27, |v| up to 2^100, and below 2^-100 v counts for less than it is.  What
+ * to 2^27, |v| up to 2^100, and below 2^-80 v counts for less than it is.  What
  * the new token does not see is never used, whatever it holds; a group of V that
  * stands for NaN is NaN in its 32 dimensions of the heads that see it, whatever it
  * weighs.  The same inputs give the same bits.

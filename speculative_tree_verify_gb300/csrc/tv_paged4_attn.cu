@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
     // Weights are 2^(score - off) and go up to 2^limit: off is the head's offset less
     // what lifts the weights to fp16's range beside the scales, limit = 15 - log2 vtop.
     float off[HN][2], l[HN][2];  // l: sums of this thread's tokens
-    float vtop = 0x1p-100f;      // power of two above the scales of V so far
-    float limit = 115.f;
+    float vtop = 0x1p-80f;       // power of two above the scales of V so far; at least so much that
+    float limit = 95.f;          // a sum of 2^30 weights, whose V may all be zero, stays below 2^128
 #pragma unroll
     for (int b = 0; b < HN; ++b) {
       off[b][0] = off[b][1] = 0.f, l[b][0] = l[b][1] = 0.f;

@@ -453,6 +453,37 @@ def test_pages_past_two_to_the_32_bytes(gpu):
     close4(bf16_to_f64(host(out))[0], bf16_to_f64(q[0]), *held)
 
 
+def test_many_tokens_without_values(gpu):
+    """Weights whose V is zero are summed as all others are, however many they are: 2^18 tokens of one
+    sequence a CTA, V zero (a scale of zero) but in the last 128 tokens, whose values are 7; scores 0 in the first
+    384 tokens, which is where each warp has its offset from, and 5.375 in all others.
+    Tolerance: a weight times a scale is fp16 (2^-11), scores 1e-3, sums of 2^18 / 96 fp32 terms a thread
+    2^-12 (each step 2^-24 of the sum), joins 2^-16, the result's rounding 2^-8."""
+    D, ps, tokens, n = 64, 128, 1 << 18, torch.cuda.get_device_properties(0).multi_processor_count
+    k = torch.full((1, tokens // ps, 1, ps // 16, 9 * D), 0x99, dtype=torch.uint8, device="cuda")   # codes: 1
+    v = torch.full_like(k, 0xFF)                                                                    # 7
+    ks, vs = (x[..., 8 * D:].view(torch.int16) for x in (k, v))
+    ks.fill_(0x3F2C)     # 0.671875
+    ks[:, :384 // ps] = 0
+    vs.zero_()
+    vs[:, -1] = 0x3F80   # 1
+    refs, status = i32(np.full(tokens // ps, n)), i32([0])
+    pages, lens, ids = i32(np.tile(np.arange(tokens // ps), (n, 1))), i32(np.full(n, tokens)), i32(np.arange(n))
+    pool = abi.TvPool4(k.data_ptr(), v.data_ptr(), refs.data_ptr(), 1, tokens // ps, 1, ps, D)
+    seqs = abi.TvSeqs(pages.data_ptr(), lens.data_ptr(), n, tokens // ps)
+    size = abi.tv_attend_paged4_workspace_size(pool, 2, n)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    q = torch.ones((n, 2, D), dtype=torch.bfloat16, device="cuda").view(torch.int16)
+    out = torch.empty_like(q)
+    assert abi.tv_attend_paged4(pool, 0, seqs, ids, n, 2, ALL, 0, q, 2 * D, None, None, 0, out, ws, size, status) == 0
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    w = np.exp(D * 0.671875 / 8)
+    o = 7 * 128 * w / (384 + (tokens - 384) * w)
+    err = np.abs(bf16_to_f64(host(out)) - o)
+    assert (err <= o * ((2.0 ** -11 + 2e-3 + 2.0 ** -12 + 2.0 ** -16) * (1 + 2.0 ** -7) + 2.0 ** -8 * (1 + 2.0 ** -7))).all(), err.max() / o
+
+
 def test_captured_first(gpu):
     """A process whose first call of each kind is made while capturing."""
     import subprocess
