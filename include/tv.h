@@ -855,8 +855,8 @@ TV_API int tv_attend_paged4(const tv_pool4 *pool, int layer, const tv_seqs *seqs
  *                   low_turns or fewer as LINEAR, high_turns or more as PLAIN,
  *                   linear in between
  * rot_dim: a multiple of 16 up to 128; theta and factor finite and positive;
- * 0 <= low_turns < high_turns and original_ctx >= 1 (BLEND); gain finite (1,
- * or what a stretched model multiplies its rotated values by).  A caller may
+ * 0 <= low_turns < high_turns and original_ctx >= 1 (BLEND); gain finite as a
+ * float (1, or what a stretched model multiplies its rotated values by).  A caller may
  * set freq itself, to any finite values.  TV_E_ARG otherwise.
  *
  * tv_rope_rows: head h of row t of x, at t * x_stride + h * head_dim, to the

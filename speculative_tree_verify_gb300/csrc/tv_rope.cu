@@ -120,7 +120,7 @@ int tv_rope_init(tv_rope* rope, int rot_dim, int interleaved, double theta, int 
   constexpr double kTwoPi = 6.283185307179586476925286766559;
   if (!rope || rot_dim < 16 || rot_dim > 2 * TV_ROPE_MAX_PAIRS || rot_dim % 16 != 0) return TV_E_ARG;
   if (interleaved != 0 && interleaved != 1) return TV_E_ARG;
-  if (!std::isfinite(theta) || theta <= 0.0 || !std::isfinite(gain)) return TV_E_ARG;
+  if (!std::isfinite(theta) || theta <= 0.0 || !std::isfinite((float)gain)) return TV_E_ARG;
   if (scaling < TV_ROPE_PLAIN || scaling > TV_ROPE_BLEND) return TV_E_ARG;
   if (scaling != TV_ROPE_PLAIN && (!std::isfinite(factor) || factor <= 0.0)) return TV_E_ARG;
   if (scaling == TV_ROPE_BLEND &&
@@ -151,7 +151,7 @@ int tv_rope_rows(const tv_rope* rope, const tv_bf16* x, size_t x_stride, tv_bf16
                  int head_dim, const int32_t* positions, int rows, int32_t* dev_status, void* stream) {
   if (!rope || !x || !out || !positions || !dev_status || n_heads < 1 || rows < 1) return TV_E_ARG;
   if (rope->rot_dim < 16 || rope->rot_dim > 2 * kPairs || rope->rot_dim % 16 != 0) return TV_E_ARG;
-  if ((rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite(rope->gain)) return TV_E_ARG;
+  if ((rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite((float)rope->gain)) return TV_E_ARG;
   if (!finite_all(rope->freq, rope->rot_dim / 2)) return TV_E_ARG;
   if ((head_dim != 64 && head_dim != 128) || rope->rot_dim > head_dim || n_heads > 65536) return TV_E_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(out) || x_stride % 8 != 0 || out_stride % 8 != 0) return TV_E_ARG;

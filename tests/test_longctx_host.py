@@ -123,6 +123,15 @@ def test_rope_host_checks():
     assert call(rope=bad) == E["TV_E_ARG"]
 
 
+def test_a_gain_no_float_holds():
+    rope = abi.tv_rope_init(64, gain=3e38)
+    for gain in (1e39, -1e300):
+        with pytest.raises(ValueError, match="ARG"):
+            abi.tv_rope_init(64, gain=gain)
+        rope.gain = gain
+        assert abi.tv_rope_rows(rope, FAKE, 512, FAKE, 512, 4, 128, FAKE, 3, FAKE) == E["TV_E_ARG"]
+
+
 def test_rope_tables():
     for args, kw in (((64, False, 10000.0), {}), ((128, True, 5e5), dict(scaling="linear", factor=4.0)), ((48, False, 1e4), dict(scaling="base", factor=8.0)),
                      ((128, False, 1e6), dict(scaling="blend", factor=8.0, original_ctx=8192, low_turns=1.0, high_turns=4.0)),
