@@ -52,12 +52,16 @@ constexpr int kLoadWarps = 3;
 static_assert(kStages % kLoadWarps == 0, "a stage always belongs to the same loading warp");
 constexpr int kPaThreads = kCompThreads + 32 * kLoadWarps;
 constexpr int kQueries = 8;                      // segments whose queries are loaded ahead, at most
-constexpr int kRedRows = 4;                      // rows joined at a time when a head block ends
+// rows joined at a time when a head block ends: as many as there is room for
+// (at D = 128 and up to 357 sequences 5 or 6, at D = 64 all 8; with four at a time
+// 128 sequences of 1 to 8191, 40/8 heads, a window of 2047, took 63.9 us, now 56.6)
+constexpr int kRedRows = 4, kMostRedRows = 8;
 // What a head block costs besides its tiles, in tiles (its queries, its join).
-// 48 sequences of 1 to 8191 tokens, 8/2 heads, with 0, 1, 2, 4 tiles: 19.4,
-// 16.4, 15.0, 16.3 us (D = 128; 1 and 2 of 64 values: 13.9, 12.6 us).  Through a
-// window few tiles are left to a head block (128 such sequences, 40/8 heads, a
-// window of 2047, with 1, 2, 3, 5, 8 tiles: 85, 72, 66, 64, 68 us).
+// 48 sequences of 1 to 8191 tokens, 8/2 heads, with 2, 3, 5, 6 tiles: 14.7, 14.6,
+// 13.7, 14.0 us; 128 of them, 40/8 heads: 82, 77, 74, 75 us.  It stays at 2 there: another
+// cut sums in another order, and results keep their last bits.  Through a window few
+// tiles are left to a head block (the 128, a window of 2047, with 2, 3, 4, 5, 6 tiles:
+// 62, 58, 58, 56, 57 us).
 constexpr int kSegCost = 2, kSegCostWin = 5;
 constexpr float kMoveLog2 = 8.f;
 
@@ -66,16 +70,25 @@ struct PaSmem {
   static constexpr int SLAB = kTile * 128;                   // 64 dimensions of a tile
   static constexpr int HALF = (D / 64) * SLAB;               // a tile's K (or V)
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int OFF_RED = kStages * STAGE;   // [8 warps][kRedRows][D] fp32; the marks of listed rows first
-  static constexpr int OFF_ML = OFF_RED + kCompWarps * kRedRows * D * 4;
+  static constexpr int OFF_ML = kStages * STAGE;
   static constexpr int Q_ROW = D * 2 + 16;          // rows 16 bytes apart in the banks: ldmatrix without conflicts
   // 2 kRows query rows: those of the next 2 to kQueries runs
   static constexpr int OFF_Q = OFF_ML + kCompWarps * kRows * 8;
   static constexpr int OFF_BAR = OFF_Q + 2 * kRows * Q_ROW;
   static constexpr int OFF_FIRST = OFF_BAR + 256;   // [n + 1]; up to kInfo sequences also their rows and lengths
-  static size_t bytes(int n) { return 1024 + OFF_FIRST + (size_t)(n + 1) * 4 + (n <= kInfo ? (size_t)n * 8 : 0); }
-  static_assert(kCompWarps * kRedRows * D * 4 >= kMaxSeqs / 8, "a mark for every table row");
-  static_assert(1024 + OFF_FIRST + (kMaxTokens + 1) * 4 <= 232448 - 64, "shared memory of one CTA");
+  static constexpr int RED_ROW = kCompWarps * D * 4;
+  static constexpr int MOST = 232448 - 64 - 1024;   // of a CTA, static arrays and alignment aside
+  // [8 warps][red_rows][D] fp32 at the end; the marks of listed rows first
+  __host__ __device__ static constexpr int off_red(int n) {
+    return (OFF_FIRST + (n + 1) * 4 + (n <= kInfo ? n * 8 : 0) + 15) & ~15;
+  }
+  __host__ __device__ static constexpr int red_rows(int n) {
+    const int fit = (MOST - off_red(n)) / RED_ROW;
+    return fit < kMostRedRows ? fit : kMostRedRows;
+  }
+  static size_t bytes(int n) { return 1024 + (size_t)off_red(n) + red_rows(n) * RED_ROW; }
+  static_assert(kRedRows * RED_ROW >= kMaxSeqs / 8, "a mark for every table row");
+  static_assert(red_rows(kMaxTokens) >= kRedRows && red_rows(kInfo) >= kRedRows, "shared memory of one CTA");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -183,9 +196,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   uint64_t* q_full = empty + kStages;    // [kQueries] a segment's queries landed
   uint64_t* q_free = q_full + kQueries;  // [kQueries] all eight warps have seen them, those that compute it are done with them
   uint32_t* s_first = reinterpret_cast<uint32_t*>(smem + L::OFF_FIRST);
-  float* s_red = reinterpret_cast<float*>(smem + L::OFF_RED);
+  const int red_rows = L::red_rows(p.n);
+  float* s_red = reinterpret_cast<float*>(smem + L::off_red(p.n));
   float2* s_ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
-  uint32_t* s_mark = reinterpret_cast<uint32_t*>(smem + L::OFF_RED);
+  uint32_t* s_mark = reinterpret_cast<uint32_t*>(s_red);
   __shared__ uint32_t s_part[kPaThreads / 32];
   __shared__ int s_bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -494,10 +508,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       if (lane == 0) mbar_arrive(&q_free[qs]);
       bool lost = false;   // an element is NaN
 #pragma unroll 1   // one copy of the code: most groups need one or two parts, and short sequences run it once a tile
-      for (int part = 0; part * kRedRows < nr; ++part) {   // rows 4 part .. + 3, of the lanes with g8 / 4 = part mod 2
-        const bool upper = part >> 1;
-        if ((g8 >> 2) == (part & 1)) {
-          const int row = g8 + (upper ? 8 : 0);
+      for (int row0 = 0; row0 < nr; row0 += red_rows) {   // rows row0 .. + red_rows - 1, a lane has one of them at most
+        const bool upper = g8 < row0;
+        const int row = g8 + (upper ? 8 : 0), mine = row - row0;
+        if (mine >= 0 && mine < red_rows) {
           float2 ml[NW];
           float M = -INFINITY, L = 0.f;
 #pragma unroll
@@ -512,24 +526,24 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           if (whole) f /= L;
           else if (warp == w0 && t4 == 0 && row < nr)
             *reinterpret_cast<float2*>(p.ws.ml + (slot * kRows + row) * 2) = make_float2(M, L);
-          // row r: groups of 8 values XOR r, no bank twice
-          float* dst = s_red + (warp * kRedRows + (g8 & 3)) * D + 2 * t4;
+          // row r: groups of 8 values XOR r, no bank twice in four rows
+          float* dst = s_red + (warp * red_rows + mine) * D + 2 * t4;
           float* at[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) at[k] = dst + ((8 * k) ^ ((g8 & 3) * 8));
+          for (int k = 0; k < 4; ++k) at[k] = dst + ((8 * k) ^ ((mine & 3) * 8));
 #pragma unroll
           for (int k = 0; k < 2 * KS; ++k)
             *reinterpret_cast<float2*>(at[k & 3] + 32 * (k >> 2)) =
                 make_float2((upper ? o[k][2] : o[k][0]) * f, (upper ? o[k][3] : o[k][1]) * f);
         }
         meet();
-        for (int e = me; e < kRedRows * (D / 2); e += 32 * NW) {
-          const int r = e / (D / 2), d = 2 * (e % (D / 2)), row = r + kRedRows * part;
-          if (row < nr) {
+        for (int e = me; e < min(red_rows, nr - row0) * (D / 2); e += 32 * NW) {
+          const int r = e / (D / 2), d = 2 * (e % (D / 2)), row = r + row0;
+          {
             float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-              const float2 v = *reinterpret_cast<const float2*>(s_red + ((w0 + w) * kRedRows + r) * D + (d ^ (r * 8)));
+              const float2 v = *reinterpret_cast<const float2*>(s_red + ((w0 + w) * red_rows + r) * D + (d ^ ((r & 3) * 8)));
               acc.x += v.x;
               acc.y += v.y;
             }
@@ -541,13 +555,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               *reinterpret_cast<float2*>(p.ws.o + (slot * kRows + row) * D + d) = acc;
           }
         }
-        if ((part + 1) * kRedRows < nr) meet();
+        if (row0 + red_rows < nr) meet();
       }
       const int bar = NW == kCompWarps ? 1 : 2 + quad;
       if (bar_any(lost, bar, 32 * NW))
         put_infinities<D, WIN>(p, g.i, g.s, g.len, g, (uint32_t)g.t0 * kTile,
                           !WIN && g.t1 == g.T ? g.len : (uint32_t)g.t1 * kTile, h, nr,
-                          reinterpret_cast<uint32_t*>(s_red + w0 * kRedRows * D), s_ml + w0 * kRows, NW, me, bar,
+                          reinterpret_cast<uint32_t*>(s_red + w0 * red_rows * D), s_ml + w0 * kRows, NW, me, bar,
                           whole ? p.out + ((size_t)g.i * p.Hq + h * p.G + r0) * D : nullptr, p.ws.o + slot * kRows * D);
     };
     if (g.T > 1) join(std::integral_constant<int, kCompWarps>{});
@@ -646,7 +660,7 @@ int launch_paged(const PaParams& p, int ctas, cudaStream_t st) {
   int rc = make_tmap_bf16(&mk, p.pool.k, D, rows, 64, R);
   if (rc || (rc = make_tmap_bf16(&mv, p.pool.v, D, rows, 64, R))) return rc;
   static std::atomic<bool> attr[64];
-  if (ensure_smem_limit(paged_attn_kernel<D, WIN>, PaSmem<D>::bytes(kMaxTokens), attr)) return TV_E_CUDA;
+  if (ensure_smem_limit(paged_attn_kernel<D, WIN>, 1024 + PaSmem<D>::MOST, attr)) return TV_E_CUDA;
   rc = launch_pdl(paged_attn_kernel<D, WIN>, dim3(ctas), dim3(kPaThreads), PaSmem<D>::bytes(p.n), st, mk, mv, p);
   return rc ? rc : launch_paged_merge(p, ctas, st);
 }
