@@ -490,15 +490,18 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
               for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
               y -= down;
               // the offset to 2^kMoveLog2 above the largest, or as it was
-              const float up = (fresh || y > limit ? y - (limit - kMoveLog2) : 0.f) + down, a = ex2f(-up);
+              const float up = (fresh || y > limit ? y - (limit - kMoveLog2) : 0.f) + down;
+              // 2^-up as a square: scales that grow from next to nothing take `up` beyond what
+              // one factor can hold, and the weights so far are still the sum's
+              const float a = ex2f(-0.5f * up);
               off[b][e] += up;
 #pragma unroll
               for (int s = 0; s < NS; ++s) x[s][b][0][e] -= up, x[s][b][1][e] -= up;
-              l[b][e] = fresh ? 0.f : l[b][e] * a;
+              l[b][e] = fresh ? 0.f : l[b][e] * a * a;
 #pragma unroll
               for (int j = 0; j < G; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[b][j][2 * i + e] = fresh ? 0.f : o[b][j][2 * i + e] * a;
+                for (int i = 0; i < 4; ++i) o[b][j][2 * i + e] = fresh ? 0.f : o[b][j][2 * i + e] * a * a;
             }
           fresh = false;
         }

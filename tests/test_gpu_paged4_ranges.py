@@ -1,0 +1,29 @@
+"""tv_attend_paged4 over the whole of its stated range, with test_gpu_paged4_attn.py's
+cases and tolerance."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import bf16_to_f64
+from test_gpu_paged4_attn import Case4, bits, close4, spreads
+
+pytestmark = pytest.mark.gpu
+
+# 8 (or 16) heads a KV head: six (or four) pairs of warps take a head block's tiles in turn, and a block of the grid has
+# whole head blocks of 15 tiles, so that what comes late in a sequence comes late in every warp
+LATE = [(8, 8, 64, 40), (8, 8, 128, 40), (32, 2, 64, 80)]
+
+
+@pytest.mark.parametrize("early,late", [(0.0, 2.0 ** 46), (0.0, 2.0 ** 60), (0.0, 2.0 ** 90), (2.0 ** -30, 2.0 ** 97)])
+@pytest.mark.parametrize("q_heads,kv_heads,dim,n", LATE)
+def test_values_that_come_late(gpu, q_heads, kv_heads, dim, n, early, late):
+    """Nothing (or next to it) in V of every warp's first tiles, then values of any size: the weights of the first tokens
+    count, whatever the scales grow by."""
+    def edit(c):
+        for pair in c.kv:
+            x = bf16_to_f64(pair[1])
+            pair[1] = bits(x * np.where(np.arange(len(x)) < 400, early, late)[:, None, None])
+    c = Case4([900] * n, q_heads, kv_heads, dim, 64, seed=30, edit=edit)
+    got, q = c.run(), bf16_to_f64(c.q)
+    for i in range(n):
+        close4(got[i], q[i], *c.rows_of(i), f"sequence {i}")
