@@ -744,6 +744,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const int key0 = w_start(k, w);
         int first = max(0, k.t0 + 1 - key0), last = min(128, k.hi - key0);
         int empty = last, end = (last + 15) & ~15;
+        int below0 = 0, below1 = 0;   // WIN: a second range of them
         if (WIN && w >= k.down) {   // and the rows that the lower end hides
           const int2 b = below(k, w);
           if (w >= k.nlow) {   // the sinks are seen, what is behind them in their last step is not
@@ -751,7 +752,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             end = b.y;
           } else if (b.x < b.y) {
             if (first >= last) first = b.x, last = b.y;
-            else first = min(first, b.x);   // (rows before the sinks' end see fewer of them)
+            else if (first <= b.y) first = min(first, b.x);
+            else below0 = b.x, below1 = b.y;   // what lies between is not touched: its steps do not wait for this look
           }
         }
         constexpr int CH = D / 8;   // 16-byte pieces of a row, 32 / CH rows a step
@@ -762,44 +764,49 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           *reinterpret_cast<uint4*>(piece + swz(row, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
         // eight rows a round: their swizzles repeat, so that a round's addresses are the last's and 1024
         constexpr int PER = CH / 4, BATCH = 2 * PER;
-        const uint8_t* at[PER];
-#pragma unroll
-        for (int u = 0; u < PER; ++u) at[u] = piece + swz(first + lane / CH + u * (32 / CH), c & 7);
-        for (int r0 = first + lane / CH; r0 < last; r0 += 16) {
-          uint4 y[BATCH];
-#pragma unroll
-          for (int u = 0; u < BATCH; ++u) {
-            const int row = r0 + u * (32 / CH);
-            y[u] = row < last ? *reinterpret_cast<const uint4*>(at[u % PER] + (u / PER) * 1024) : make_uint4(0u, 0u, 0u, 0u);
-          }
-#pragma unroll
-          for (int u = 0; u < PER; ++u) at[u] += 2048;
-          // 0 x, summed: NaN where an x is not finite
-          uint32_t any[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-          for (int u = 0; u < BATCH; ++u) {
-            any[0] = times_zero(y[u].x, any[0]);
-            any[1] = times_zero(y[u].y, any[1]);
-            any[2] = times_zero(y[u].z, any[2]);
-            any[3] = times_zero(y[u].w, any[3]);
-          }
-          if (((any[0] | any[1]) | (any[2] | any[3])) & 0x7fff7fffu) {
 #pragma unroll 1
-            for (int row = r0; row < last && row < r0 + 16; row += 32 / CH) {
-              uint16_t* x = reinterpret_cast<uint16_t*>(piece + swz(row, c & 7));
+        for (;;) {
+          const uint8_t* at[PER];
+#pragma unroll
+          for (int u = 0; u < PER; ++u) at[u] = piece + swz(first + lane / CH + u * (32 / CH), c & 7);
+          for (int r0 = first + lane / CH; r0 < last; r0 += 16) {
+            uint4 y[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+              const int row = r0 + u * (32 / CH);
+              y[u] = row < last ? *reinterpret_cast<const uint4*>(at[u % PER] + (u / PER) * 1024) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int u = 0; u < PER; ++u) at[u] += 2048;
+            // 0 x, summed: NaN where an x is not finite
+            uint32_t any[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+              any[0] = times_zero(y[u].x, any[0]);
+              any[1] = times_zero(y[u].y, any[1]);
+              any[2] = times_zero(y[u].z, any[2]);
+              any[3] = times_zero(y[u].w, any[3]);
+            }
+            if (((any[0] | any[1]) | (any[2] | any[3])) & 0x7fff7fffu) {
 #pragma unroll 1
-              for (int u = 0; u < 8; ++u) {
-                const uint32_t b = x[u];
-                if ((b & 0x7f80u) == 0x7f80u) {
-                  const int kind = (b & 0x7fu) ? 0 : (b & 0x8000u ? 2 : 1);   // NaN, +inf, -inf
-                  if (!WIN) atomicMin(&bad[kind * D + c * 8 + u], (unsigned long long)~tag << 32 | (unsigned)(key0 + row));
-                  x[u] = 0;
+              for (int row = r0; row < last && row < r0 + 16; row += 32 / CH) {
+                uint16_t* x = reinterpret_cast<uint16_t*>(piece + swz(row, c & 7));
+#pragma unroll 1
+                for (int u = 0; u < 8; ++u) {
+                  const uint32_t b = x[u];
+                  if ((b & 0x7f80u) == 0x7f80u) {
+                    const int kind = (b & 0x7fu) ? 0 : (b & 0x8000u ? 2 : 1);   // NaN, +inf, -inf
+                    if (!WIN) atomicMin(&bad[kind * D + c * 8 + u], (unsigned long long)~tag << 32 | (unsigned)(key0 + row));
+                    x[u] = 0;
+                  }
                 }
               }
+              *reinterpret_cast<volatile unsigned*>(&s_anybad[it & 1]) = tag;
+              wrote = true;
             }
-            *reinterpret_cast<volatile unsigned*>(&s_anybad[it & 1]) = tag;
-            wrote = true;
           }
+          if (!WIN || below0 >= below1) break;
+          first = below0, last = below1, below1 = 0;
         }
         if (wrote) fence_async_smem();
         __syncwarp();
