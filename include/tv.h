@@ -823,8 +823,8 @@ TV_API int tv_pages4_read(const tv_pool4 *pool, int layer, const tv_seqs *seqs, 
  * tv_attend_paged_window, of the values that the cache stands for.  k_new and
  * v_new are bf16 rows; they are stored in 4 bits, and the new token sees what
  * was stored.
- * Scores are fp32: q enters as fp16 relative to its row's largest value, exactly
- * down to 2^-23 of that, and a group's sum takes its scale.  A weight times its
+ * Scores are fp32: q enters as it is, products with the codes are summed down to
+ * 2^-18 of the row's largest |q|, and a group's sum takes its scale.  A weight times its
  * group's scale enters the product with V as fp16 (11 bits, down to 2^-29 of the
  * largest so far); sums are fp32, and out is rounded once.  |q| up to 2^100, scores up
  * to 2^27, |v| up to 2^100, and below 2^-80 v counts for less than it is.  What

@@ -11,10 +11,13 @@
 // conversions is taken.  Hence:
 // - The cache lies as the tensor cores' operands do (tv_pool4): a lane loads its
 //   codes with 16-byte loads, no ldmatrix, no shuffle.
-// - Codes become fp16 operands without arithmetic: 4 bits masked out of 16 are the
-//   subnormal n' 2^-24 or 16 times that, n' = n + 8, and 8 bits (n' + 16 n") 2^-24 of
-//   neighbours.  Where dimensions are summed (K), q carries the 16th part; where
-//   they are rows (V), neighbours come apart at the end, which saves a mask.
+// - Codes become operands without arithmetic: bits masked out of 16 are a whole number
+//   times the type's smallest subnormal.  K goes in as bf16, n' 2^-133 or 16 times that,
+//   n' = n + 8 (q, which is bf16 as it stands, carries the 16th part).  The tensor cores
+//   align products as if subnormals were the smallest normal value and keep 25 bits, so
+//   that of a code's products 2^-18 of the largest q of 16 dimensions is kept (fp16: 2^-15).
+//   V goes in as fp16, as do the weights: n' 2^-24, and 8 bits (n' + 16 n") 2^-24 of
+//   neighbours, which come apart at the end: that saves a mask.
 //   (e4m3 products, to which four bits are an operand as well, turn into
 //   conversions and fp16 products on this architecture: 549 us instead of 346.)
 // - Both products have the codes as the operand of 16 rows and 8 heads as columns
@@ -86,6 +89,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                                         uint32_t b1, float c0, float c1, float c2, float c3) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
@@ -291,7 +302,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
     }
     // Queries, as columns: head g8 (and g8 + 8), dimensions 32 j + 8 t4 .. + 7 of
     // group j, q0 .. q7, relative to the row's exponent: (q0, q4), (q1, q5) / 16,
-    // (q2, q6), (q3, q7) / 16, exact down to 2^-24 of the row's largest.
+    // (q2, q6), (q3, q7) / 16: exact.
     uint32_t q[HN][G][4];
     // of heads 2 t4 and 2 t4 + 1: -8 sum q of a group; what a product of q and codes is worth
     float bias[HN][G][2], sc[HN][2];
@@ -310,10 +321,10 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
       top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // the largest to 2^13 .. 2^14; below 2^-113 it stays smaller, so that both factors are normal
-      const int e = max((int)(top >> 7), 14);   // 127 + exponent
-      const float f = __uint_as_float((uint32_t)(267 - e) << 23);
-      const float worth = p.scale_log2 * 0x1p24f * __uint_as_float((uint32_t)(e - 13) << 23);
+      // the largest to 2^120 .. 2^121, by two factors that are normal
+      const int e = max((int)(top >> 7), 1), up = 247 - e;   // 127 + exponent
+      const float f = __uint_as_float((uint32_t)(127 + min(up, 127)) << 23), f2 = __uint_as_float((uint32_t)(127 + max(up - 127, 0)) << 23);
+      const float worth = p.scale_log2 * __uint_as_float((uint32_t)min(e + 13, 254) << 23);   // 2^(133 - up)
       sc[b][0] = __shfl_sync(0xffffffffu, worth, 8 * t4);
       sc[b][1] = __shfl_sync(0xffffffffu, worth, 8 * t4 + 4);
 #pragma unroll
@@ -321,18 +332,20 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
         float sum = 0.f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {   // dimensions u and u + 4: halves u % 2 of words u / 2 and u / 2 + 2
-          const float k = u & 1 ? f * 0.0625f : f;
+          const float k = u & 1 ? f2 * 0.0625f : f2;
           const uint32_t y = x[j][u >> 1], z = x[j][(u >> 1) + 2];
-          const __half2 v = __floats2half2_rn(__uint_as_float(u & 1 ? y & 0xffff0000u : y << 16) * k,
-                                              __uint_as_float(u & 1 ? z & 0xffff0000u : z << 16) * k);
-          const float2 r = __half22float2(v);
+          const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(u & 1 ? y & 0xffff0000u : y << 16) * f * k,
+                                                         __uint_as_float(u & 1 ? z & 0xffff0000u : z << 16) * f * k);
+          const float2 r = __bfloat1622float2(v);
           q[b][j][u] = *reinterpret_cast<const uint32_t*>(&v);
           sum += (r.x + r.y) * (u & 1 ? 16.f : 1.f);
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        bias[b][j][0] = __shfl_sync(0xffffffffu, sum, 8 * t4) * -0x1p-21f;   // -8 * 2^-24
-        bias[b][j][1] = __shfl_sync(0xffffffffu, sum, 8 * t4 + 4) * -0x1p-21f;
+        sum *= -0x1p-65f;   // -8 * 2^-133
+        sum *= 0x1p-65f;
+        bias[b][j][0] = __shfl_sync(0xffffffffu, sum, 8 * t4);
+        bias[b][j][1] = __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
       }
     }
     // O^T: o[8 heads][j][0 .. 3] rows 32 j + 4 g8, that and 16 times the next, heads 2 t4, 2 t4 + 1; [4 .. 7]: two rows more
@@ -413,10 +426,10 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
 #pragma unroll
             for (int b = 0; b < HN; ++b) {
               float c[4];
-              mma_f16(c, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, q[b][j][0], q[b][j][1],
-                      0.f, 0.f, 0.f, 0.f);
-              mma_f16(c, u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u, q[b][j][2], q[b][j][3], c[0],
-                      c[1], c[2], c[3]);
+              mma_bf16(c, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, q[b][j][0], q[b][j][1],
+                       0.f, 0.f, 0.f, 0.f);
+              mma_bf16(c, u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u, q[b][j][2], q[b][j][3], c[0],
+                       c[1], c[2], c[3]);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 float(&y)[2][2] = x[s][b];

@@ -27,3 +27,18 @@ def test_values_that_come_late(gpu, q_heads, kv_heads, dim, n, early, late):
     got, q = c.run(), bf16_to_f64(c.q)
     for i in range(n):
         close4(got[i], q[i], *c.rows_of(i), f"sequence {i}")
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(8, 2, 128), (8, 2, 64), (12, 1, 64), (24, 1, 128)])
+def test_small_queries_beside_large_ones(gpu, q_heads, kv_heads, dim):
+    """Whole numbers up to 3 beside 2^18, which meets zeros of K alone: the scores are what the small ones make of them,
+    and exact (products and their sums are whole numbers below 2^24 of a scale)."""
+    def edit(c):
+        q = np.random.default_rng(37).integers(-3, 4, c.q.shape).astype(np.float64)
+        q[..., 4::32], q[..., 6::32] = 2.0 ** 18, -2.0 ** 18
+        c.q[:] = bits(q)
+        for pair in c.kv:
+            k = bf16_to_f64(pair[0])
+            k[..., 4::32] = k[..., 6::32] = 0
+            pair[0] = bits(k)
+    Case4([700, 33], q_heads, kv_heads, dim, 32, seed=38, edit=edit).check()
