@@ -23,7 +23,8 @@
 // - Both products have the codes as the operand of 16 rows and 8 heads as columns
 //   (S^T = K Q^T, O^T += V^T P^T): up to 8 heads a KV head cost half of what 16 do
 //   (346 -> 292 us).  -8 sum q of a group of 32 dimensions is added to its sum, which
-//   then takes the token's scale; V's codes less 8 are one packed subtraction.
+//   then takes the token's scale; V's codes become n 2^-9, normal values, by one packed
+//   multiply-add (subtracted only, they lost what is 2^-15 of the heaviest of 16 tokens).
 // - A token's V scale goes into its weight, four weights of fp16 a token (one a
 //   group), so that V needs no product.  The weights are relative to the largest
 //   scale so far, as they are to the offset: 2^15 at most, 2^-24 at least.
@@ -105,9 +106,12 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
+// two whole numbers times 2^-24, less `off` of them, to whole numbers times 2^-9
+template <int OFF>
+__device__ __forceinline__ uint32_t lift_f16(uint32_t a) {
+  static_assert(OFF == 8 || OFF == 136, "");
   uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0x78007800u), "r"(OFF == 8 ? 0xa400a400u : 0xb440b440u));   // 2^15, -OFF 2^-9
   return r;
 }
 // an 8 x 8 matrix of 16-bit values, a row to four lanes, transposed
@@ -538,10 +542,10 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
               const uint32_t w = vw[n][j], u1 = __byte_perm(w, 0u, 0x4341);
-              a[0][n] = sub_f16(w & 0x000f000fu, 0x00080008u);
-              a[1][n] = sub_f16(w & 0x00ff00ffu, 0x00880088u);
-              a[2][n] = sub_f16(u1 & 0x000f000fu, 0x00080008u);
-              a[3][n] = sub_f16(u1, 0x00880088u);
+              a[0][n] = lift_f16<8>(w & 0x000f000fu);
+              a[1][n] = lift_f16<136>(w & 0x00ff00ffu);
+              a[2][n] = lift_f16<8>(u1 & 0x000f000fu);
+              a[3][n] = lift_f16<136>(u1);
             }
 #pragma unroll
             for (int b = 0; b < HN; ++b) {
@@ -589,11 +593,11 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
         float* dst = s_red + ((size_t)warp * L::HEADS + 8 * b + 2 * t4 + e) * D + ((g8 + 2 * t4) & 7) * 4;
         if (8 * b + 2 * t4 + e < nr)
 #pragma unroll
-          for (int j = 0; j < G; ++j) {   // what the codes' and the weights' factors leave: 2^17 vtop
+          for (int j = 0; j < G; ++j) {   // what the codes' and the weights' factors leave: 4 vtop
             const float(&r)[8] = o[b][j];
             *reinterpret_cast<float4*>(dst + 32 * j) =
-                make_float4(r[e] * 0x1p17f * vtop, (r[2 + e] - r[e]) * 0x1p13f * vtop, r[4 + e] * 0x1p17f * vtop,
-                            (r[6 + e] - r[4 + e]) * 0x1p13f * vtop);
+                make_float4(r[e] * 4.f * vtop, (r[2 + e] - r[e]) * 0.25f * vtop, r[4 + e] * 4.f * vtop,
+                            (r[6 + e] - r[4 + e]) * 0.25f * vtop);
           }
       }
     }

@@ -42,3 +42,22 @@ def test_small_queries_beside_large_ones(gpu, q_heads, kv_heads, dim):
             k[..., 4::32] = k[..., 6::32] = 0
             pair[0] = bits(k)
     Case4([700, 33], q_heads, kv_heads, dim, 32, seed=38, edit=edit).check()
+
+
+@pytest.mark.parametrize("less", [9, 12, 14, 16])
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(8, 2, 128), (8, 2, 64), (12, 1, 64), (24, 1, 128)])
+def test_light_tokens_beside_heavy_ones(gpu, q_heads, kv_heads, dim, less):
+    """15 of 16 tokens weigh 2^-less of the 16th, whose V is zero in the odd dimensions: there the others' V is the
+    result."""
+    def edit(c):
+        q = np.zeros(c.q.shape)
+        q[..., 0] = 8
+        c.q[:] = bits(q)
+        for pair in c.kv:
+            k, v = np.zeros(pair[0].shape), np.zeros(pair[0].shape)
+            light = np.arange(len(k)) % 16 != 5
+            k[light, :, 0] = -(less * np.log(2) - 0.1) * np.sqrt(dim) / 8
+            v[~light, :, 0::2], v[light, :, 1::2] = 7, 1
+            v[..., 30::32] = 7   # a scale of one
+            pair[0], pair[1] = bits(k), bits(v)
+    Case4([700, 40], q_heads, kv_heads, dim, 32, seed=39, edit=edit).check()
