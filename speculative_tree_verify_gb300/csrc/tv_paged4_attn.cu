@@ -57,6 +57,7 @@ constexpr int kQueries = 8;                      // runs whose queries are loade
 // heads, with 1, 3, 5, 8 tiles: 98, 85, 72, 64 us.
 constexpr int kSegCost = 8;
 constexpr float kMoveLog2 = 8.f;                 // offsets move when a score passes them by this
+constexpr float kFar = 1024.f;                   // a move by less rounds a score by 2^-14 at most
 
 // HN: blocks of 8 heads
 template <int D, int HN>
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
 
     bool fresh = true;           // no token so far
     int t = g.t0 + turn;
-    for (; t < g.t1; t += NT) {
+    for (bool again = false; t < g.t1;) {   // again: a tile for the second time
       uint8_t* sk = smem + st * L::STAGE + first / 16 * B::BYTES;
       uint8_t* sv = sk + L::HALF;
       if (ok && !mbar_wait(&full[st], st_par)) ok = false;
@@ -478,6 +479,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
             for (int j = 0; j < G; j += 2) top = __vimax3_u16x2(top, sb[s][n][j], sb[s][n][j + 1]);
         }
         if (__any_sync(0xffffffffu, fresh || most > limit || top != vt)) {
+          float far = 0.f;
           // scales that are NaN say nothing of the others
           top = 0u;
 #pragma unroll
@@ -508,12 +510,14 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
               y -= down;
               // the offset to 2^kMoveLog2 above the largest, or as it was
               const float up = (fresh || y > limit ? y - (limit - kMoveLog2) : 0.f) + down;
-              // 2^-up as a square: scales that grow from next to nothing take `up` beyond what
+              const float now = off[b][e] + up, move = now - off[b][e];   // (rounded, as the offset is)
+              // 2^-move as a square: scales that grow from next to nothing take it beyond what
               // one factor can hold, and the weights so far are still the sum's
-              const float a = ex2f(-0.5f * up);
-              off[b][e] += up;
+              const float a = ex2f(-0.5f * move);
+              far = fmaxf(far, fabsf(move));
+              off[b][e] = now;
 #pragma unroll
-              for (int s = 0; s < NS; ++s) x[s][b][0][e] -= up, x[s][b][1][e] -= up;
+              for (int s = 0; s < NS; ++s) x[s][b][0][e] -= move, x[s][b][1][e] -= move;
               l[b][e] = fresh ? 0.f : l[b][e] * a * a;
 #pragma unroll
               for (int j = 0; j < G; ++j)
@@ -521,6 +525,13 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
                 for (int i = 0; i < 4; ++i) o[b][j][2 * i + e] = fresh ? 0.f : o[b][j][2 * i + e] * a * a;
             }
           fresh = false;
+          // A score of kFar and more, less the offset from before a move by as much, has lost
+          // places that matter behind the move: then the tile once more, so that tokens of equal
+          // scores weigh the same wherever they are.
+          if (!again && __any_sync(0xffffffffu, far >= kFar)) {
+            again = true;
+            continue;
+          }
         }
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
@@ -568,6 +579,8 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
       if ((st += NT) >= kStages) st = team, st_par ^= 1u;
+      again = false;
+      t += NT;
     }
     turn = t - g.t1;
 
@@ -578,26 +591,25 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
     const int nw = g.T > 1 ? NW : 2, w0 = g.T > 1 ? 0 : 2 * team, me = tid - 32 * w0;
     // a CTA's first run may begin inside a head block, its last end inside one
     const size_t slot = (size_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0);
-    // the weights' lift, 2^7 / vtop, is the offset's again
+    // the weights' lift, 2^7 / vtop, is the offset's again; what the offset's rounding drops stays in the weights
     const float lift = limit - kMoveLog2, unlift = __uint_as_float(__float_as_uint(vtop) - (7u << 23));
 #pragma unroll
     for (int b = 0; b < HN; ++b) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        const float at = off[b][e] + lift, rest = ex2f(lift - (at - off[b][e]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
-        if (g8 == 0) s_ml[warp * kRows + 8 * b + 2 * t4 + e] = make_float2(fresh ? -INFINITY : off[b][e] + lift, l[b][e] * unlift);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {   // head 8 b + 2 t4 + e, dimensions 32 j + 4 g8 .. + 3: chunks turned by the head, no bank twice
+        if (g8 == 0) s_ml[warp * kRows + 8 * b + 2 * t4 + e] = make_float2(fresh ? -INFINITY : at, l[b][e] * unlift * rest);
+        // head 8 b + 2 t4 + e, dimensions 32 j + 4 g8 .. + 3: chunks turned by the head, no bank twice
         float* dst = s_red + ((size_t)warp * L::HEADS + 8 * b + 2 * t4 + e) * D + ((g8 + 2 * t4) & 7) * 4;
+        const float worth = 4.f * vtop * rest, part = 0.25f * vtop * rest;   // what the codes' and the weights' factors leave
         if (8 * b + 2 * t4 + e < nr)
 #pragma unroll
-          for (int j = 0; j < G; ++j) {   // what the codes' and the weights' factors leave: 4 vtop
+          for (int j = 0; j < G; ++j) {
             const float(&r)[8] = o[b][j];
             *reinterpret_cast<float4*>(dst + 32 * j) =
-                make_float4(r[e] * 4.f * vtop, (r[2 + e] - r[e]) * 0.25f * vtop, r[4 + e] * 4.f * vtop,
-                            (r[6 + e] - r[4 + e]) * 0.25f * vtop);
+                make_float4(r[e] * worth, (r[2 + e] - r[e]) * part, r[4 + e] * worth, (r[6 + e] - r[4 + e]) * part);
           }
       }
     }

@@ -61,3 +61,36 @@ def test_light_tokens_beside_heavy_ones(gpu, q_heads, kv_heads, dim, less):
             v[..., 30::32] = 7   # a scale of one
             pair[0], pair[1] = bits(k), bits(v)
     Case4([700, 40], q_heads, kv_heads, dim, 32, seed=39, edit=edit).check()
+
+
+@pytest.mark.parametrize("step", [2.0 ** -3, 2.0 ** 3, 2.0 ** 10])
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("q_heads,kv_heads,dim,n", LATE)
+def test_scores_of_any_size(gpu, q_heads, kv_heads, dim, n, first, step):
+    """Scores up to 2^27, exact in fp32: tokens of equal scores weigh the same wherever they are, and whichever warp and
+    block has them.
+
+    q is 8^i step in dimensions 0 .. 6 and K of these the digits of a whole number below 8^7, so that products and sums
+    are whole numbers below 2^24 times step.  V is 1 in a warp's first tiles and -1 behind them (or, where the scores rise
+    from next to nothing after 400 tokens, in the tile that they rise in and behind it): weights that depend on
+    the place do not cancel.  Tolerance: close4's, whose 1e-3 of a weight is for rounding scores of some hundreds; here
+    what is left of a score less an offset is exact, or at most 2^-24 of some hundreds."""
+    L, rise, turn = 900, 0 if first else 400, 400 if first else 784
+
+    def edit(c):
+        rng = np.random.default_rng(31)
+        q = np.zeros(c.q.shape)
+        q[..., :7] = 8.0 ** np.arange(7) * step
+        c.q[:] = bits(q)
+        for i, pair in enumerate(c.kv):
+            k = np.zeros((L, kv_heads, dim))
+            top = 2 ** 20 - 1234 * (i + 1) + rng.integers(-3, 1, (L, kv_heads)) * (1 if step > 1 else 8)
+            top[:rise] = rng.integers(0, 9, (rise, kv_heads))
+            k[..., :7] = top[..., None] // 8 ** np.arange(7) % 8
+            k[..., 7::32] = 7   # a scale of one
+            pair[0] = bits(k)
+            pair[1] = bits(np.broadcast_to(np.where(np.arange(L) < turn, 1.0, -1.0)[:, None, None], k.shape))
+    c = Case4([L] * n, q_heads, kv_heads, dim, 64, seed=32, edit=edit)
+    got, q = c.run(), bf16_to_f64(c.q)
+    for i in range(n):
+        close4(got[i], q[i], *c.rows_of(i), f"sequence {i}")
