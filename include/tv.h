@@ -823,10 +823,15 @@ TV_API int tv_pages4_read(const tv_pool4 *pool, int layer, const tv_seqs *seqs, 
  * tv_attend_paged_window, of the values that the cache stands for.  k_new and
  * v_new are bf16 rows; they are stored in 4 bits, and the new token sees what
  * was stored.
- * Scores are fp32: q enters as it is, products with the codes are summed down to
- * 2^-18 of the row's largest |q|, and a group's sum takes its scale.  A weight times its
- * group's scale enters the product with V as fp16 (11 bits, down to 2^-29 of the
- * largest so far); sums are fp32, and out is rounded once.  |q| up to 2^100, scores up
+ * Scores are fp32: q enters as it is, its products with a group's codes (0 .. 15) are
+ * summed down to 2^-18 of the row's largest |q|, and 8 q less, the sum takes the
+ * group's scale.  A weight times its
+ * group's scale enters the product with V as fp16, relative to the largest weight
+ * times the largest scale so far, of whichever token and group each is: 11 bits
+ * down to 2^-20 of that (less by up to 8 powers of two with scores from 2^23 on),
+ * below it a step of 2^-30.  So a token or a group of V that is 2^20 times as large as
+ * others takes digits from theirs, even where it weighs nothing.  Sums are
+ * fp32, and out is rounded once.  |q| up to 2^100, scores up
  * to 2^27, |v| up to 2^100, and below 2^-80 v counts for less than it is.  What
  * the new token does not see is never used, whatever it holds; a group of V that
  * stands for NaN is NaN in its 32 dimensions of the heads that see it, whatever it

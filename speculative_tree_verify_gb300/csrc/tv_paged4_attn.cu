@@ -27,7 +27,9 @@
 //   multiply-add (subtracted only, they lost what is 2^-15 of the heaviest of 16 tokens).
 // - A token's V scale goes into its weight, four weights of fp16 a token (one a
 //   group), so that V needs no product.  The weights are relative to the largest
-//   scale so far, as they are to the offset: 2^15 at most, 2^-24 at least.
+//   scale so far, as they are to the offset: 2^15 at most, and 2^7 for the largest
+//   weight times the largest scale where an offset is set, so that fp16 has its 11
+//   bits down to 2^-20 of that and a step of 2^-24, 2^-30 of it or less, below.
 //
 // How the work is cut over CTAs is in tv_paged_runs.cuh.  In a CTA four warps look
 // up pages (32 boxes' entries at a time, the next 32 on their way) and copy whole

@@ -94,3 +94,67 @@ def test_scores_of_any_size(gpu, q_heads, kv_heads, dim, n, first, step):
     got, q = c.run(), bf16_to_f64(c.q)
     for i in range(n):
         close4(got[i], q[i], *c.rows_of(i), f"sequence {i}")
+
+
+def close_loud(got, q, k, v, scale, quiet, what=""):
+    """Where values of very different size meet.  scale: the largest of V's scales that are seen, quiet: the dimensions
+    compared.  With weights w, their largest m, o and A as in close4, B = sum w |v|, C = sum w times the largest |v| of the
+    token's 32: a weight times a scale is fp16, 2^-11 of itself (B) or half of 2^-24, 2^-31 of m times `scale`, of codes up to
+    7; a run's few fp32 products lose 2^-23 of C each; scores, sums and the result's rounding as in close4."""
+    heads, tokens = len(q), len(k)
+    o, A, B, _ = spreads(q, k, v)
+    for h in range(heads):
+        g = h * k.shape[1] // heads
+        a = k[:, g] @ q[h] / np.sqrt(q.shape[1])
+        w = np.exp(a - a.max())
+        w /= w.sum()
+        C = (w @ np.abs(v[:, g]).reshape(tokens, -1, 32).max(-1)).repeat(32)
+        tol = (2.0 ** -11 * B[h] + (1e-3 + 2.0 ** -10) * A[h] + 2.0 ** -16 * np.abs(o[h]) + 2.0 ** -20 * C
+               + 7 * 2.0 ** -31 * tokens * w.max() * scale) * (1 + 2.0 ** -7) + 2.0 ** -8 * np.abs(o[h]) * (1 + 2.0 ** -7)
+        err = np.abs(got[h] - o[h])
+        assert (tol[quiet] < 0.5 * np.abs(o[h][quiet])).all(), "the bound says something"
+        assert (err[quiet] <= tol[quiet]).all(), f"{what}: head {h}, worst {np.max(err[quiet] / tol[quiet]):.3f} of the tolerance"
+
+
+HEADS = [(8, 2, 128), (8, 2, 64), (12, 1, 64)]
+
+
+@pytest.mark.parametrize("up", [10, 16, 20, 24])
+@pytest.mark.parametrize("q_heads,kv_heads,dim", HEADS)
+def test_a_loud_token_that_weighs_nothing(gpu, q_heads, kv_heads, dim, up):
+    """One token's V is 2^up times the others', its weight below 2^-90."""
+    at = [7, 450]
+
+    def edit(c):
+        rng = np.random.default_rng(33)
+        q = bf16_to_f64(c.q)
+        q[..., 0] = 8
+        c.q[:] = bits(q)
+        for i, pair in enumerate(c.kv):
+            k, v = bf16_to_f64(pair[0]), rng.uniform(0.5, 1, pair[1].shape)
+            k[..., 0], k[at[i]], v[at[i]] = 0, 0, v[at[i]] * 2.0 ** up
+            k[at[i], :, 0] = -12 * np.sqrt(dim)
+            pair[0], pair[1] = bits(k), bits(v)
+    c = Case4([60, 900], q_heads, kv_heads, dim, 16, seed=34, edit=edit)
+    got, q = c.run(), bf16_to_f64(c.q)
+    for i in range(2):
+        k, v = c.rows_of(i)
+        close_loud(got[i], q[i], k, v, bf16_to_f64(c.held[i][1][1]).max(), slice(None), f"sequence {i}")
+
+
+@pytest.mark.parametrize("up", [10, 16, 20, 24])
+@pytest.mark.parametrize("q_heads,kv_heads,dim", HEADS)
+def test_a_loud_group(gpu, q_heads, kv_heads, dim, up):
+    """Every token's V is 2^up times as large in its last 32 dimensions as in the others."""
+    def edit(c):
+        rng = np.random.default_rng(35)
+        for pair in c.kv:
+            v = rng.uniform(0.5, 1, pair[1].shape)
+            v[..., -32:] *= 2.0 ** up
+            pair[1] = bits(v)
+    c = Case4([60, 900], q_heads, kv_heads, dim, 16, seed=36, edit=edit)
+    got, q = c.run(), bf16_to_f64(c.q)
+    for i in range(2):
+        k, v = c.rows_of(i)
+        for part in (slice(0, -32), slice(-32, None)):
+            close_loud(got[i], q[i], k, v, bf16_to_f64(c.held[i][1][1]).max(), part, f"sequence {i}")
