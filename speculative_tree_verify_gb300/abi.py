@@ -207,6 +207,11 @@ def _p(x) -> Optional[int]:
     return x.data_ptr()
 
 
+def _i32(x) -> int:
+    """A count of rows: what no int32 holds is more than any sequence has, and ctypes would cut it to 32 bits."""
+    return max(-(1 << 31), min(int(x), (1 << 31) - 1))
+
+
 def _arr(ctype, items: Sequence):
     return (ctype * len(items))(*items)
 
@@ -437,7 +442,7 @@ def tv_attend_prompt_window(n_q_heads: int, n_kv_heads: int, head_dim: int, wind
                             q_stride: int, kv_stride: int, starts, n_seqs: int, rows: int, out, dev_status,
                             stream=None) -> int:
     """Strides in elements."""
-    return load().tv_attend_prompt_window(int(n_q_heads), int(n_kv_heads), int(head_dim), int(window), int(sinks),
+    return load().tv_attend_prompt_window(int(n_q_heads), int(n_kv_heads), int(head_dim), _i32(window), _i32(sinks),
                                           _p(q), _p(k), _p(v), int(q_stride), int(kv_stride), _p(starts), int(n_seqs),
                                           int(rows), _p(out), _p(dev_status), _stream(stream))
 
@@ -447,7 +452,7 @@ def tv_attend_paged_window(pool: TvPool, layer: int, seqs: TvSeqs, ids, n: int, 
                            workspace_bytes: int, dev_status, stream=None) -> int:
     """Strides in elements; k_new and v_new may be None."""
     return load().tv_attend_paged_window(ctypes.byref(pool), int(layer), ctypes.byref(seqs), _p(ids), int(n),
-                                         int(n_q_heads), int(window), int(sinks), _p(q), int(q_stride), _p(k_new),
+                                         int(n_q_heads), _i32(window), _i32(sinks), _p(q), int(q_stride), _p(k_new),
                                          _p(v_new), int(kv_stride), _p(out), _p(workspace), int(workspace_bytes),
                                          _p(dev_status), _stream(stream))
 
@@ -511,7 +516,7 @@ def tv_attend_paged4(pool: TvPool4, layer: int, seqs: TvSeqs, ids, n: int, n_q_h
                      stream=None) -> int:
     """Strides in elements; k_new and v_new may be None."""
     return load().tv_attend_paged4(ctypes.byref(pool), int(layer), ctypes.byref(seqs), _p(ids), int(n),
-                                   int(n_q_heads), int(window), int(sinks), _p(q), int(q_stride), _p(k_new), _p(v_new),
+                                   int(n_q_heads), _i32(window), _i32(sinks), _p(q), int(q_stride), _p(k_new), _p(v_new),
                                    int(kv_stride), _p(out), _p(workspace), int(workspace_bytes), _p(dev_status),
                                    _stream(stream))
 
@@ -520,6 +525,8 @@ def tv_rope_init(rot_dim: int, interleaved: bool = False, theta: float = 10000.0
                  factor: float = 1.0, original_ctx: int = 1, low_turns: float = 1.0, high_turns: float = 32.0,
                  gain: float = 1.0) -> TvRope:
     rope = TvRope()
+    if scaling == TV_ROPE_BLEND and int(original_ctx) >= 1 << 31:   # ctypes would cut it to 32 bits
+        raise ValueError("tv_rope_init: TV_E_ARG")
     rc = load().tv_rope_init(ctypes.byref(rope), int(rot_dim), 1 if interleaved else 0, float(theta), int(scaling),
                              float(factor), int(original_ctx), float(low_turns), float(high_turns), float(gain))
     if rc != TV_OK:
