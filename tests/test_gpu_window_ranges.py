@@ -6,7 +6,8 @@ import torch
 
 from oracle import bf16_to_f64, longctx
 from test_gpu_paged_attn import bits, close, host
-from test_gpu_window_attn import WindowPrompt
+from test_gpu_paged4_attn import Case4
+from test_gpu_window_attn import WindowCase, WindowPrompt, check_tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,32 @@ def test_infinities_between_hidden_keys(gpu, q_heads, kv_heads, dim, window, sin
         assert p.run() == 0
         torch.cuda.synchronize()
         assert (host(p.out) == first).all()
+
+
+def forget_hidden(c):
+    """Entries of pages that hold nothing but hidden tokens name no page."""
+    ps, gone = c.k.shape[3] if isinstance(c, WindowCase) else c.ps, 0
+    for i, x in enumerate(c.lens):
+        see = set(longctx.seen(x - 1, c.window, c.sinks)) if x else set()
+        for j in range(-(-x // ps)):
+            if not see & set(range(j * ps, (j + 1) * ps)):
+                c.pages[c.ids[i], j] = 1 << 30 if j % 2 else -7
+                gone += 1
+    assert gone
+
+
+@pytest.mark.parametrize("new", [True, False])
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("window,sinks", [(20, 0), (70, 4), (33, 17), (130, 65)])
+@pytest.mark.parametrize("ps", [16, 32, 64, 128])
+def test_hidden_pages_beside_visible_ones(gpu, ps, window, sinks, four, new):
+    """Entries between sinks and window may name anything, those in one tile of 64 tokens with a visible page among them."""
+    lens, heads = [700, 3, 129, 1283, 410, 64], (8, 2, 128) if ps < 64 else (12, 1, 64)
+    if four:
+        c = Case4(lens, *heads, ps, window, sinks, seed=ps, new=new)
+        forget_hidden(c)
+        c.check()
+    else:
+        c = WindowCase(window, sinks, lens, *heads, ps, seed=ps, new=new, lost=False)
+        forget_hidden(c)
+        check_tokens(c)
