@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
 
     bool fresh = true;           // no token so far
     int t = g.t0 + turn;
-    for (bool again = false; t < g.t1;) {   // again: a tile for the second time
+    uint32_t again = 0u;         // a tile for the second time: a bit for each head whose offset moved far, and one more
+    while (t < g.t1) {
       uint8_t* sk = smem + st * L::STAGE + first / 16 * B::BYTES;
       uint8_t* sv = sk + L::HALF;
       if (ok && !mbar_wait(&full[st], st_par)) ok = false;
@@ -480,8 +481,8 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
 #pragma unroll
             for (int j = 0; j < G; j += 2) top = __vimax3_u16x2(top, sb[s][n][j], sb[s][n][j + 1]);
         }
-        if (__any_sync(0xffffffffu, fresh || most > limit || top != vt)) {
-          float far = 0.f;
+        if (__any_sync(0xffffffffu, fresh || most > limit || top != vt || again != 0u)) {
+          uint32_t far = 0u;
           // scales that are NaN say nothing of the others
           top = 0u;
 #pragma unroll
@@ -511,12 +512,13 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
               for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
               y -= down;
               // the offset to 2^kMoveLog2 above the largest, or as it was
-              const float up = (fresh || y > limit ? y - (limit - kMoveLog2) : 0.f) + down;
+              const uint32_t head = 1u << (2 * b + e);
+              const float up = (fresh || y > limit || (again & head) != 0u ? y - (limit - kMoveLog2) : 0.f) + down;
               const float now = off[b][e] + up, move = now - off[b][e];   // (rounded, as the offset is)
               // 2^-move as a square: scales that grow from next to nothing take it beyond what
               // one factor can hold, and the weights so far are still the sum's
               const float a = ex2f(-0.5f * move);
-              far = fmaxf(far, fabsf(move));
+              if (fabsf(move) >= kFar) far |= head;
               off[b][e] = now;
 #pragma unroll
               for (int s = 0; s < NS; ++s) x[s][b][0][e] -= move, x[s][b][1][e] -= move;
@@ -529,9 +531,9 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
           fresh = false;
           // A score of kFar and more, less the offset from before a move by as much, has lost
           // places that matter behind the move: then the tile once more, so that tokens of equal
-          // scores weigh the same wherever they are.
-          if (!again && __any_sync(0xffffffffu, far >= kFar)) {
-            again = true;
+          // scores weigh the same wherever they are, and the offset by what is exact now.
+          if (again == 0u && __any_sync(0xffffffffu, far != 0u)) {
+            again = far | 0x100u;
             continue;
           }
         }
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(P4<D, HN>::THREADS, 1) paged4_attn_kernel(cons
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
       if ((st += NT) >= kStages) st = team, st_par ^= 1u;
-      again = false;
+      again = 0u;
       t += NT;
     }
     turn = t - g.t1;

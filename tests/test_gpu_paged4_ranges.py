@@ -158,3 +158,28 @@ def test_a_loud_group(gpu, q_heads, kv_heads, dim, up):
         k, v = c.rows_of(i)
         for part in (slice(0, -32), slice(-32, None)):
             close_loud(got[i], q[i], k, v, bf16_to_f64(c.held[i][1][1]).max(), part, f"sequence {i}")
+
+
+@pytest.mark.parametrize("early", [0, 400])
+@pytest.mark.parametrize("q_heads,kv_heads,dim,n", LATE)
+def test_the_largest_scores_keep_their_digits(gpu, q_heads, kv_heads, dim, n, early):
+    """One token in 16 has a score near 2^27, all others (after `early` tokens next to nothing) 2^7 less or lower still:
+    its V is the result, to a weight's 2^-11 and the result's rounding, however the offsets were rounded."""
+    def edit(c):
+        rng = np.random.default_rng(40)
+        q = np.zeros(c.q.shape)
+        q[..., :7] = 8.0 ** np.arange(7) * 2.0 ** 10
+        c.q[:] = bits(q)
+        for pair in c.kv:
+            k = np.zeros(pair[0].shape)
+            top = rng.integers(2 ** 19, 2 ** 20, (1, kv_heads)) - (np.arange(len(k)) % 16 != 5)[:, None]
+            top[:early] = rng.integers(0, 9, (early, kv_heads))
+            k[..., :7] = top[..., None] // 8 ** np.arange(7) % 8
+            k[..., 7::32] = 7   # a scale of one
+            pair[0] = bits(k)
+            pair[1] = bits(np.broadcast_to(rng.uniform(0.5, 1, (1, kv_heads, dim)), k.shape))
+    c = Case4([900] * n, q_heads, kv_heads, dim, 64, seed=41, edit=edit)
+    got = c.run()
+    for i in range(n):
+        v = c.rows_of(i)[1][-1].repeat(q_heads // kv_heads, 0)
+        assert (np.abs(got[i] - v) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16) * (1 + 2.0 ** -7) * np.abs(v) + 2.0 ** -22 * np.abs(v).max()).all(), i
