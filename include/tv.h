@@ -760,7 +760,12 @@ TV_API int tv_attend_paged(const tv_pool *pool, int layer, const tv_seqs *seqs, 
  * tv_attend_prompt_window: otherwise as tv_attend_prompt.
  * tv_attend_paged_window: otherwise as tv_attend_paged, of the new token: it
  * is row len - 1 of its sequence.  Pages that only hold rows between the sinks
- * and the window are not looked at; their table entries may name anything.
+ * and the window are not looked at; their table entries may name anything as far
+ * as this call goes (the page calls look at every entry of a sequence).
+ *
+ * Prompts and single tokens alone: tv_verify_tree and tv_verify_stack see every
+ * row of their contiguous cache, so that a layer that looks through a window can
+ * be prefilled and continued a token at a time, but not verified.
  */
 TV_API int tv_attend_prompt_window(int n_q_heads, int n_kv_heads, int head_dim, int window, int sinks,
                                    const tv_bf16 *q, const tv_bf16 *k, const tv_bf16 *v, size_t q_stride,
@@ -794,6 +799,9 @@ TV_API int tv_attend_paged_window(const tv_pool *pool, int layer, const tv_seqs 
  * over the same tv_seqs; a sequence table belongs to one pool.  tv_pages4_write
  * takes bf16 rows and rounds them as above; tv_pages4_read gives bf16(n s).
  * What a forked or moved page stands for does not change.
+ * A draft tree over a sequence in 4 bits is verified over a contiguous tv_kv of
+ * what it stands for (tv_pages4_read); what the verify committed is rounded as it
+ * is written back.
  */
 typedef struct tv_pool4 {
   uint8_t *k, *v;
@@ -873,8 +881,13 @@ TV_API int tv_attend_paged4(const tv_pool4 *pool, int layer, const tv_seqs *seqs
  *              overlap it otherwise
  *   positions  device int32 [rows], any value
  * An angle's fraction of a turn is a 64-bit product, reduced without a rounding
- * at any position; that fraction, its sine and cosine and the products are fp32,
- * and the result is rounded once.
+ * at any position (freq / 2 pi is a double: 2^-52 of position * freq may be lost);
+ * that fraction, its sine and cosine and the products are fp32, and the result is
+ * rounded once.
+ * tv_verify_tree and tv_verify_stack turn the rows of a draft tree themselves:
+ * whole heads, halves as pairs, plain frequencies of rope_theta.  A cache whose
+ * rows were turned in any other way (neighbours, part of a head, stretched, a
+ * gain) is not one that they can verify over.
  * Host checks: TV_E_ARG, TV_E_UNSUPPORTED (head_dim not 64 or 128, rot_dim
  * above it, n_heads > 65536).
  */

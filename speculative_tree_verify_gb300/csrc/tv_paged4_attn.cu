@@ -6,7 +6,7 @@
 // What bounds it: 9/8 bytes a value of K and V together, so that instructions
 // come near to memory: a block of 16 tokens of one head (2.3 KB of K and V at
 // D = 128) is some 100 cycles of an SM's share of the bandwidth, and 128 sequences of
-// 8k take 149 a block now (265 us; 4.6 TB/s): 370 instructions on four schedulers,
+// 8k take 152 a block now (270 us; 4.5 TB/s): 374 instructions on four schedulers,
 // everything counted (48 such sequences), and half of the time the pipe of masks and
 // conversions is taken.  Hence:
 // - The cache lies as the tensor cores' operands do (tv_pool4): a lane loads its

@@ -4,7 +4,9 @@
 // What bounds it: a value is 2 bytes on one side and 9/16 on the other, and
 // little is computed, so both kernels are streams over memory.  A warp takes a
 // pair of tokens (their V share words) and 2 U 16-byte pieces a lane, K and V
-// of U heads of 128 or 2 U of 64.
+// of U heads of 128 or 2 U of 64.  What V's 16-byte pieces, 64 bytes apart, take
+// besides: 32-byte sectors between SM and L2 are 1.5 times the pool's bytes in, 1.7
+// out (10610 rows; 27.0 us both ways, 60 % of the copy rate).
 #include "tv_kernels.cuh"
 #include "tv_pages.cuh"
 #include "tv_pages4.cuh"
@@ -12,7 +14,7 @@
 namespace tv {
 namespace {
 
-constexpr int kBlocksPerSm = 3;    // of 85 registers a thread (10610 rows in and out: 26.3 us; of 64, four: 27.2)
+constexpr int kBlocksPerSm = 3;    // of up to 85 registers a thread (10610 rows in and out, in turn: 26.3 us; of 64, four: 27.2)
 constexpr int kMany = 4;           // U where there are rows enough for every warp
 
 // One task: R packed rows (writing, U = 1: one row, else two) and U pieces of

@@ -51,9 +51,10 @@
 // lowest come in windows of 128.  Where these leave room for the sinks, they are
 // counted from the pair's last key down, and the sinks are loaded into the last
 // one's lowest steps, below what any row sees (16k tokens, 40/8 heads, W = 1024, K =
-// 4: 281 us with a window of the sinks' own, 273 so, 256 without sinks); else the
-// sinks have windows of their own behind the others.  So a pair costs about (W +
-// 2T + 127) / 128 windows, whatever the length.  What is masked is now at both
+// 4, in turn: 281 us with a window of the sinks' own, 273 so, 256 without sinks; the
+// present code by itself 279, 274 to 288 a call); else the sinks have windows of
+// their own behind the others.  So a pair costs about (W + 2T + 127) / 128 windows,
+// whatever the length.  What is masked is now at both
 // ends; the lower end's V (keys up to W before the pair's last token) is looked
 // over as well, and a pair whose V held something not finite reads its keys again
 // from memory at the end, each row those that it sees (put_back): which rows see
@@ -276,9 +277,9 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* r) {
                : "memory");
 }
 
-// WIN: what is not finite in V, of keys j0 .. j1 - 1 that row t sees, into its
-// result in dimensions d0 .. + n - 1 (row), added to what the products left.
-// Keys that the products had are added twice, which changes nothing.
+// WIN: what is not finite in V, of keys j0 .. j1 - 1 that row t sees, into n
+// dimensions of its result (row; v: the same dimensions of key 0), added to what
+// the products left.  Keys that the products had are added twice, which changes nothing.
 __device__ __noinline__ void put_back(const __nv_bfloat16* v, size_t stride, int window, int sinks, int j0, int j1, int t,
                                       uint16_t* row, int n) {
   for (int j = j0; j < j1 && j <= t; ++j) {
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
     if constexpr (WIN) {
       const bool apart = w.lo > 0 && w.ss == 0;   // (sinks < lo then)
-      const int hidden = w.hi - p.window - w.lo;   // below 2 T
+      const int hidden = w.hi - p.window - w.lo;   // below 2 T, or 2 T + 128 where the sinks share the last window
       w.up = max(1, w.nlow - ((w.t0 + 1 - w.lo) >> 7));
       w.down = hidden > 0 ? w.nlow - ((hidden + 127) >> 7) : w.nlow;
       if (apart) w.nwin += (p.sinks + 127) / 128;
