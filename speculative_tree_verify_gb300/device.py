@@ -255,10 +255,10 @@ class PagedCache:
         shape = (n_layers, n_pages, dims.n_kv_heads, page_size, dims.head_dim)
         return [torch.empty(shape, device=device, dtype=torch.bfloat16) for _ in range(2)]
 
-    # the library's struct and calls for this kind of pool
-    _pool, _ws_size, _attend_ws_size = abi.TvPool, staticmethod(abi.tv_pages_workspace_size), staticmethod(abi.tv_attend_paged_workspace_size)
-    _extend, _fork, _release = map(staticmethod, (abi.tv_pages_extend, abi.tv_pages_fork, abi.tv_pages_release))
-    _compact, _write, _read = map(staticmethod, (abi.tv_pages_compact, abi.tv_pages_write, abi.tv_pages_read))
+    # the library's struct and calls (of abi) for this kind of pool
+    _pool, _ws_size, _attend_ws_size = abi.TvPool, "tv_pages_workspace_size", "tv_attend_paged_workspace_size"
+    _extend, _fork, _release = "tv_pages_extend", "tv_pages_fork", "tv_pages_release"
+    _compact, _write, _read = "tv_pages_compact", "tv_pages_write", "tv_pages_read"
 
     @classmethod
     def alloc(cls, dims: Dims, n_layers: int, n_pages: int, page_size: int, max_seqs: int, max_pages: int,
@@ -270,7 +270,7 @@ class PagedCache:
         pool = cls._pool(k.data_ptr(), v.data_ptr(), refs.data_ptr(), n_layers, n_pages, dims.n_kv_heads, page_size,
                          dims.head_dim)
         seqs = abi.TvSeqs(pages.data_ptr(), lens.data_ptr(), max_seqs, max_pages)
-        bytes_ = cls._ws_size(pool, seqs), cls._attend_ws_size(pool, dims.n_q_heads, min(max_seqs, 2048))
+        bytes_ = getattr(abi, cls._ws_size)(pool, seqs), getattr(abi, cls._attend_ws_size)(pool, dims.n_q_heads, min(max_seqs, 2048))
         ws, attend_ws = (torch.empty(b, device=device, dtype=torch.uint8) for b in bytes_)
         return cls(dims, k, v, refs, pages, lens, torch.zeros(1, **i32), ws, attend_ws, pool, seqs)
 
@@ -310,44 +310,44 @@ class PagedCache:
 
     def extend(self, ids, add, stream=None) -> int:
         n = self._list(ids.numel(), ids=ids, add=add)
-        return self._extend(self.pool, self.seqs, ids, add, n, self.ws, self.ws.numel(), self.status, stream)
+        return getattr(abi, self._extend)(self.pool, self.seqs, ids, add, n, self.ws, self.ws.numel(), self.status, stream)
 
     def fork(self, src, dst, stream=None) -> int:
         n = self._list(src.numel(), src=src, dst=dst)
-        return self._fork(self.pool, self.seqs, src, dst, n, self.status, stream)
+        return getattr(abi, self._fork)(self.pool, self.seqs, src, dst, n, self.status, stream)
 
     def release(self, ids, keep, stream=None) -> int:
         n = self._list(ids.numel(), ids=ids, keep=keep)
-        return self._release(self.pool, self.seqs, ids, keep, n, self.status, stream)
+        return getattr(abi, self._release)(self.pool, self.seqs, ids, keep, n, self.status, stream)
 
     def compact(self, remap, n_used, stream=None) -> int:
         self._list(self.refs.numel(), remap=remap)
         self._list(1, n_used=n_used)
-        return self._compact(self.pool, self.seqs, remap, n_used, self.ws, self.ws.numel(), self.status, stream)
+        return getattr(abi, self._compact)(self.pool, self.seqs, remap, n_used, self.ws, self.ws.numel(), self.status, stream)
 
     def write(self, layer: int, ids, pos, starts, qkv: torch.Tensor, stream=None) -> int:
         """Rows of a projection into the pages of the sequences they belong to."""
         n = self._list(ids.numel(), ids=ids, pos=pos)
         self._list(n + 1, starts=starts)
         _, k, v = self._heads(qkv)
-        return self._write(self.pool, layer, self.seqs, ids, pos, starts, n, qkv.shape[0], k, v,
-                           qkv.stride(0), self.dims.head_dim, self.status, stream)
+        return getattr(abi, self._write)(self.pool, layer, self.seqs, ids, pos, starts, n, qkv.shape[0], k, v,
+                                         qkv.stride(0), self.dims.head_dim, self.status, stream)
 
     def read_into(self, layer: int, ids, pos, starts, rows: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> int:
         """Tokens of one or more sequences into contiguous caches [n_kv_heads][capacity][head_dim]."""
         n = self._list(ids.numel(), ids=ids, pos=pos)
         self._list(n + 1, starts=starts)
         self._caches(k, v, rows)
-        return self._read(self.pool, layer, self.seqs, ids, pos, starts, n, rows, k, v, k.stride(1),
-                          k.stride(0), self.status, stream)
+        return getattr(abi, self._read)(self.pool, layer, self.seqs, ids, pos, starts, n, rows, k, v, k.stride(1),
+                                        k.stride(0), self.status, stream)
 
     def write_from(self, layer: int, ids, pos, starts, rows: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> int:
         """The other way: rows of contiguous caches (a committed path) into pages."""
         n = self._list(ids.numel(), ids=ids, pos=pos)
         self._list(n + 1, starts=starts)
         self._caches(k, v, rows)
-        return self._write(self.pool, layer, self.seqs, ids, pos, starts, n, rows, k, v, k.stride(1),
-                           k.stride(0), self.status, stream)
+        return getattr(abi, self._write)(self.pool, layer, self.seqs, ids, pos, starts, n, rows, k, v, k.stride(1),
+                                         k.stride(0), self.status, stream)
 
     def attend_prompt(self, qkv: torch.Tensor, starts, out: torch.Tensor, stream=None, window: Optional[int] = None,
                       sinks: int = 0) -> int:
@@ -387,9 +387,9 @@ class PagedCache4(PagedCache):
         shape = (n_layers, n_pages, dims.n_kv_heads, page_size // 16, 9 * dims.head_dim)
         return [torch.empty(shape, device=device, dtype=torch.uint8) for _ in range(2)]
 
-    _pool, _ws_size, _attend_ws_size = abi.TvPool4, staticmethod(abi.tv_pages4_workspace_size), staticmethod(abi.tv_attend_paged4_workspace_size)
-    _extend, _fork, _release = map(staticmethod, (abi.tv_pages4_extend, abi.tv_pages4_fork, abi.tv_pages4_release))
-    _compact, _write, _read = map(staticmethod, (abi.tv_pages4_compact, abi.tv_pages4_write, abi.tv_pages4_read))
+    _pool, _ws_size, _attend_ws_size = abi.TvPool4, "tv_pages4_workspace_size", "tv_attend_paged4_workspace_size"
+    _extend, _fork, _release = "tv_pages4_extend", "tv_pages4_fork", "tv_pages4_release"
+    _compact, _write, _read = "tv_pages4_compact", "tv_pages4_write", "tv_pages4_read"
 
     def attend(self, layer: int, ids, qkv: torch.Tensor, out: torch.Tensor, stream=None, window: Optional[int] = None,
                sinks: int = 0) -> int:

@@ -16,13 +16,23 @@ def lib():
 
 
 @pytest.mark.parametrize("kind,prefix,attend", [(PagedCache, "tv_pages_", "tv_attend_paged_"), (PagedCache4, "tv_pages4_", "tv_attend_paged4_")])
-def test_the_calls_of_a_kind(kind, prefix, attend):
-    """They are the class's: a call looks nothing up by its name."""
+def test_the_calls_of_a_kind(kind, prefix, attend, monkeypatch):
+    """Their names are the class's: no call puts one together."""
     for name in ("extend", "fork", "release", "compact", "write", "read"):
-        assert getattr(kind, "_" + name) is getattr(abi, prefix + name)
-    assert kind._ws_size is getattr(abi, prefix + "workspace_size") and kind._attend_ws_size is getattr(abi, attend + "workspace_size")
+        assert getattr(kind, "_" + name) == prefix + name
+    assert (kind._ws_size, kind._attend_ws_size) == (prefix + "workspace_size", attend + "workspace_size")
     c = kind.alloc(Dims(hidden=64, n_q_heads=4, n_kv_heads=2, head_dim=64, vocab=64), 1, 4, 16, 2, 3, device="cpu")
-    assert type(c.pool) is kind._pool and c.ws.numel() == kind._ws_size(c.pool, c.seqs)
+    assert type(c.pool) is kind._pool and c.ws.numel() == getattr(abi, kind._ws_size)(c.pool, c.seqs)
+    got = []
+    for name in ("extend", "fork", "release", "compact", "write", "read"):
+        for x in ("tv_pages_", "tv_pages4_"):
+            monkeypatch.setattr(abi, x + name, lambda *a, name=x + name: got.append(name) or 0)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)
+    rows, caches = torch.zeros(3, 8 * 64, dtype=torch.bfloat16), torch.zeros(2, 5, 64, dtype=torch.bfloat16)
+    c.extend(i32(0), i32(3)), c.fork(i32(0), i32(1)), c.release(i32(0), i32(0)), c.compact(i32(0, 0, 0, 0), i32(0))
+    c.write(0, i32(0), i32(0), i32(0, 3), rows), c.read_into(0, i32(0), i32(0), i32(0, 3), 3, caches, caches)
+    c.write_from(0, i32(0), i32(0), i32(0, 3), 3, caches, caches)
+    assert got == [prefix + x for x in ("extend", "fork", "release", "compact", "write", "read", "write")]
 
 
 @pytest.mark.parametrize("name", ["tv_attend_prompt_window", "tv_attend_paged_window", "tv_attend_paged4"])
