@@ -183,3 +183,19 @@ def test_the_largest_scores_keep_their_digits(gpu, q_heads, kv_heads, dim, n, ea
     for i in range(n):
         v = c.rows_of(i)[1][-1].repeat(q_heads // kv_heads, 0)
         assert (np.abs(got[i] - v) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16) * (1 + 2.0 ** -7) * np.abs(v) + 2.0 ** -22 * np.abs(v).max()).all(), i
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(8, 2, 128), (12, 1, 64)])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+def test_a_query_that_is_not_finite(gpu, q_heads, kv_heads, dim, value):
+    """Its head is NaN (all of K counts towards it), and no other one is touched."""
+    def edit(c):
+        c.q[:, 3, 5] = bits(np.array([value]))[0] if np.isinf(value) else 0x7FC0
+    c = Case4([900, 40], q_heads, kv_heads, dim, 16, seed=42, edit=edit)
+    got, q = c.run(), bf16_to_f64(c.q)
+    assert np.isnan(got[:, 3]).all()
+    for i in range(2):
+        bad = np.zeros(got[i].shape, bool)
+        bad[3] = True
+        with np.errstate(invalid="ignore"):
+            close4(got[i], np.where(np.isfinite(q[i]), q[i], 0), *c.rows_of(i), but=bad)
